@@ -26,6 +26,12 @@ the graph-transformer attention (score scale * q_i . key_j, value val_j):
     out, lse = transformer_forward(g, q, key, val)     # scale defaults to 1/sqrt(D)
     dq, dkey, dval = transformer_backward(g, q, key, val, lse, dout)
 
+the same with a learned relative position bias (bias [buckets, H], pos [N] int32):
+
+    rel = RelPos(g, pos, 32, 128)                      # once per position vector
+    out, lse = transformer_rel_forward(g, rel, q, key, val, bias)
+    dq, dkey, dval, dbias = transformer_rel_backward(g, rel, q, key, val, bias, lse, dout)
+
 and the max / min neighbourhood reduction with its winners:
 
     out, arg = reduce_forward(g, x, "max")         # arg [N, F] int32, -1 if no in-edges
@@ -33,6 +39,7 @@ and the max / min neighbourhood reduction with its winners:
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 
 import torch
@@ -44,7 +51,8 @@ __all__ = ["Graph", "gat_forward", "gat_backward", "GATAggregate", "GnnError", "
            "check_device_error", "default_tiling", "gcn_forward", "gcn_backward",
            "GCNAggregate", "reduce_forward", "reduce_backward", "ReduceAggregate",
            "gatv2_forward", "gatv2_backward", "GATv2Aggregate", "transformer_forward",
-           "transformer_backward", "TransformerAggregate"]
+           "transformer_backward", "TransformerAggregate", "RelPos", "transformer_rel_forward",
+           "transformer_rel_backward", "TransformerRelAggregate"]
 
 
 def _ptr(t):
@@ -452,6 +460,160 @@ class TransformerAggregate(torch.autograd.Function):
         q, key, val, lse = ctx.saved_tensors
         dq, dk, dv = transformer_backward(ctx.g, q, key, val, lse, dout.contiguous(), ctx.scale)
         return None, dq, dk, dv, None
+
+
+@contextlib.contextmanager
+def _launch_on(device, stream):
+    """The launch's device current and its stream torch's own, so that what the
+    call allocates belongs to the stream that uses it."""
+    if stream is None and torch.cuda.current_device() == device.index:
+        yield torch.cuda.current_stream(device).cuda_stream
+        return
+    with torch.cuda.device(device):
+        if stream is None:
+            yield torch.cuda.current_stream(device).cuda_stream
+        else:
+            with torch.cuda.stream(stream):
+                yield stream.cuda_stream
+
+
+class RelPos:
+    """Buckets of the relative positions of a graph's edges.
+
+    pos [N] int32: the nodes' positions.  An edge j -> i falls into the bucket
+    of pos[j] - pos[i].  The default rule gives small distances a bucket each
+    and lets the others grow by equal ratios up to max_distance; bidirectional
+    gives half of the buckets to sources after the destination, otherwise these
+    all share bucket 0 with distance 0.  bounds: the lower bounds of one side's
+    buckets (ascending whole numbers from 0) instead of that rule.  At most
+    128 buckets.  Prepare it once per position vector; pos is not kept.
+    """
+
+    def __init__(self, g: Graph, pos: torch.Tensor, num_buckets: int = 32,
+                 max_distance: int = 128, bidirectional: bool = True, bounds=None, stream=None):
+        lib = _native.load()
+        _check_tensor(g, pos, "pos", (g.n,), torch.int32)
+        if bounds is None:
+            if bidirectional and num_buckets % 2:
+                raise ValueError("a bidirectional rule needs an even number of buckets")
+            side = num_buckets // 2 if bidirectional else num_buckets
+            table = (ctypes.c_int32 * max(side, 1))()
+            _native.check(lib.gnn_rel_log_bounds(side, int(max_distance), table),
+                          "gnn_rel_log_bounds")
+        else:
+            table = (ctypes.c_int32 * len(bounds))(*bounds)
+        self.graph = g
+        self.bounds = list(table)
+        self.bidirectional = bool(bidirectional)
+        handle = ctypes.c_void_p()
+        n = lib.gnn_rel_buffer_bytes(g.handle)
+        with _launch_on(g.device, stream) as s:
+            self.buffer = torch.empty(n, dtype=torch.uint8, device=g.device)
+            rc = lib.gnn_rel_prepare(g.handle, _ptr(pos), table, len(table),
+                                     int(self.bidirectional), _ptr(self.buffer), n, s,
+                                     ctypes.byref(handle))
+        _native.check(rc, "gnn_rel_prepare")
+        self.handle = handle
+        self._lib = lib
+        self.buckets = lib.gnn_rel_buckets(handle)
+
+    def __del__(self):
+        h = getattr(self, "handle", None)
+        if h is not None and h.value:
+            self._lib.gnn_rel_destroy(h)
+            self.handle = None
+
+    def arrays(self):
+        """The buckets of the edges, uint8 [E], in CSR and in CSC order (views)."""
+        ptrs = (ctypes.c_void_p * 2)()
+        _native.check(self._lib.gnn_rel_arrays(self.handle, ptrs, 2), "gnn_rel_arrays")
+        at = [p - self.buffer.data_ptr() for p in ptrs]
+        return tuple(self.buffer[o:o + self.graph.e] for o in at)
+
+
+def _rel_inputs(g: Graph, rel: RelPos, bias, H: int):
+    if not isinstance(rel, RelPos):
+        raise TypeError(f"rel must be a RelPos, got {type(rel).__name__}")
+    if rel.graph is not g:
+        raise ValueError("rel was prepared for another graph")
+    _check_tensor(g, bias, "bias", (rel.buckets, H), floating=True)
+    return bias.to(torch.float32)
+
+
+def _rel_ws(g, rel, H, D, dtype, ws):
+    if _check_ws(g, ws) is not None:
+        return ws
+    n = g._lib.transformer_rel_workspace_bytes(g.handle, rel.handle, H, D, _dtype_code(dtype))
+    if n == 0:
+        raise GnnError(_native.ERR_UNSUPPORTED, f"(H={H}, D={D}, {dtype})")
+    return torch.empty(n, dtype=torch.uint8, device=g.device)
+
+
+def transformer_rel_forward(g: Graph, rel: RelPos, q: torch.Tensor, key: torch.Tensor,
+                            val: torch.Tensor, bias: torch.Tensor, scale: float | None = None,
+                            out=None, lse=None, ws=None, stream=None):
+    """transformer_forward with bias [buckets, H] added to the scores by the
+    bucket of each edge: out [N,H,D] (q's dtype) and lse [N,H] float32.  An
+    entry of -inf masks its bucket."""
+    N, H, D = _gt_inputs(g, q, key, val)
+    scale = D ** -0.5 if scale is None else float(scale)
+    with _launch_on(g.device, stream) as s:
+        bias = _rel_inputs(g, rel, bias, H)
+        out = _given(g, out, "out", q.shape, q.dtype, lambda: torch.empty_like(q))
+        lse = _given(g, lse, "lse", (N, H), torch.float32,
+                     lambda: torch.empty((N, H), dtype=torch.float32, device=q.device))
+        ws = _rel_ws(g, rel, H, D, q.dtype, ws)
+        rc = g._lib.transformer_rel_forward(g.handle, rel.handle, H, D, _dtype_code(q.dtype),
+                                            _ptr(q), _ptr(key), _ptr(val), scale, _ptr(bias),
+                                            _ptr(out), _ptr(lse), _ptr(ws), ws.numel(), s)
+    _native.check(rc, "transformer_rel_forward")
+    return out, lse
+
+
+def transformer_rel_backward(g: Graph, rel: RelPos, q: torch.Tensor, key: torch.Tensor,
+                             val: torch.Tensor, bias: torch.Tensor, lse: torch.Tensor,
+                             dout: torch.Tensor, scale: float | None = None, dq=None, dkey=None,
+                             dval=None, dbias=None, ws=None, stream=None):
+    """dq, dkey, dval [N,H,D] (q's dtype) and dbias [buckets,H] float32."""
+    N, H, D = _gt_inputs(g, q, key, val)
+    _check_features(g, dout, "dout")
+    if dout.shape != q.shape or dout.dtype != q.dtype:
+        raise ValueError("dout must match q")
+    scale = D ** -0.5 if scale is None else float(scale)
+    _check_tensor(g, lse, "lse", (N, H), torch.float32)
+    with _launch_on(g.device, stream) as s:
+        bias = _rel_inputs(g, rel, bias, H)
+        dq = _given(g, dq, "dq", q.shape, q.dtype, lambda: torch.empty_like(q))
+        dkey = _given(g, dkey, "dkey", q.shape, q.dtype, lambda: torch.empty_like(q))
+        dval = _given(g, dval, "dval", q.shape, q.dtype, lambda: torch.empty_like(q))
+        dbias = _given(g, dbias, "dbias", bias.shape, torch.float32,
+                       lambda: torch.empty_like(bias))
+        ws = _rel_ws(g, rel, H, D, q.dtype, ws)
+        rc = g._lib.transformer_rel_backward(g.handle, rel.handle, H, D, _dtype_code(q.dtype),
+                                             _ptr(q), _ptr(key), _ptr(val), scale, _ptr(bias),
+                                             _ptr(lse), _ptr(dout), _ptr(dq), _ptr(dkey),
+                                             _ptr(dval), _ptr(dbias), _ptr(ws), ws.numel(), s)
+    _native.check(rc, "transformer_rel_backward")
+    return dq, dkey, dval, dbias
+
+
+class TransformerRelAggregate(torch.autograd.Function):
+    """out = TransformerRelAggregate.apply(graph, rel, q, key, val, bias, scale)."""
+
+    @staticmethod
+    def forward(ctx, g, rel, q, key, val, bias, scale):
+        q, key, val, bias = (t.contiguous() for t in (q, key, val, bias))
+        out, lse = transformer_rel_forward(g, rel, q, key, val, bias, scale)
+        ctx.g, ctx.rel, ctx.scale = g, rel, scale
+        ctx.save_for_backward(q, key, val, bias, lse)
+        return out
+
+    @staticmethod
+    def backward(ctx, dout):
+        q, key, val, bias, lse = ctx.saved_tensors
+        dq, dk, dv, db = transformer_rel_backward(ctx.g, ctx.rel, q, key, val, bias, lse,
+                                                  dout.contiguous(), ctx.scale)
+        return None, None, dq, dk, dv, db.to(bias.dtype), None
 
 
 def _reduce_ws(g, F, dt, ws, device):

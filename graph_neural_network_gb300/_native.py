@@ -56,6 +56,17 @@ SIGNATURES = [
                                        _P]),
     ("transformer_agg_backward", _I32, [_P, _I32, _I32, _I32, _P, _P, _P, _F, _P, _P, _P, _P,
                                         _P, _P, _SZ, _P]),
+    ("gnn_rel_log_bounds", _I32, [_I32, _I32, _P]),
+    ("gnn_rel_buffer_bytes", _SZ, [_P]),
+    ("gnn_rel_prepare", _I32, [_P, _P, _P, _I32, _I32, _P, _SZ, _P, _P]),
+    ("gnn_rel_destroy", _I32, [_P]),
+    ("gnn_rel_arrays", _I32, [_P, _P, _I32]),
+    ("gnn_rel_buckets", _I32, [_P]),
+    ("transformer_rel_workspace_bytes", _SZ, [_P, _P, _I32, _I32, _I32]),
+    ("transformer_rel_forward", _I32, [_P, _P, _I32, _I32, _I32, _P, _P, _P, _F, _P, _P, _P, _P,
+                                       _SZ, _P]),
+    ("transformer_rel_backward", _I32, [_P, _P, _I32, _I32, _I32, _P, _P, _P, _F, _P, _P, _P, _P,
+                                        _P, _P, _P, _P, _SZ, _P]),
     ("reduce_agg_workspace_bytes", _SZ, [_P, _I32, _I32]),
     ("reduce_agg_forward", _I32, [_P, _I32, _I32, _I32, _P, _P, _P, _P, _SZ, _P]),
     ("reduce_agg_backward", _I32, [_P, _I32, _I32, _P, _P, _P, _P, _SZ, _P]),

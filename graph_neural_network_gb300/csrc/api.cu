@@ -407,6 +407,19 @@ gnn_status gatv2_shape(const gnn_graph* g, int H, int D, gnn_dtype dt, Shape* s)
   return s->nv == 1 ? GNN_OK : GNN_ERR_UNSUPPORTED;
 }
 
+// The current device is the graph's (a launch on another device's stream, or on
+// memory of another device, would fail after the call has returned).
+bool device_ok(const gnn_graph* g) {
+  int dev = -1;
+  return cudaGetDevice(&dev) == cudaSuccess && dev == g->device;
+}
+
+gnn_status rel_shape(const gnn_graph* g, const gnn_rel* rel, int H, int D, gnn_dtype dt,
+                     Shape* s) {
+  if (!g || !rel || rel->g != g || rel->n != g->n || rel->e != g->e) return GNN_ERR_INVALID_ARG;
+  return gatv2_shape(g, H, D, dt, s);
+}
+
 }  // namespace
 
 extern "C" {
@@ -498,6 +511,122 @@ gnn_status transformer_agg_backward(const gnn_graph* g, int H, int D, gnn_dtype 
   return from_cuda(gnn::launch_transformer_backward(g, s, dtype, q, key, val, scale, lse, dout,
                                                     dq, dkey, dval, static_cast<char*>(ws),
                                                     static_cast<cudaStream_t>(stream)));
+}
+
+gnn_status gnn_rel_log_bounds(int n_bounds, int max_distance, int32_t* bounds) {
+  if (!bounds || n_bounds < 2 || n_bounds > gnn::kMaxBuckets || max_distance <= n_bounds / 2)
+    return GNN_ERR_INVALID_ARG;
+  gnn::rel_log_bounds(n_bounds, max_distance, bounds);
+  return GNN_OK;
+}
+
+size_t gnn_rel_buffer_bytes(const gnn_graph* g) {
+  return g ? 2 * gnn::align_up(size_t(g->e) + 1, 256) : 0;
+}
+
+gnn_status gnn_rel_prepare(const gnn_graph* g, const int32_t* pos_d, const int32_t* bounds,
+                           int n_bounds, int two_sided, void* buffer_d, size_t buffer_bytes,
+                           void* stream, gnn_rel** out) {
+  if (!out) return GNN_ERR_INVALID_ARG;
+  *out = nullptr;
+  if (!g || !bounds || n_bounds < 1 || (two_sided != 0 && two_sided != 1) ||
+      n_bounds > gnn::kMaxBuckets / (two_sided ? 2 : 1))
+    return GNN_ERR_INVALID_ARG;
+  if (bounds[0] != 0) return GNN_ERR_INVALID_ARG;
+  for (int b = 1; b < n_bounds; ++b)
+    if (bounds[b] < bounds[b - 1]) return GNN_ERR_INVALID_ARG;
+  if ((g->n > 0 && !pos_d) || !aligned(pos_d, 4) || !buffer_d || !aligned(buffer_d, 256))
+    return GNN_ERR_INVALID_ARG;
+  if (buffer_bytes < gnn_rel_buffer_bytes(g)) return GNN_ERR_WORKSPACE_TOO_SMALL;
+  if (!device_ok(g)) return GNN_ERR_INVALID_ARG;
+  gnn_rel* r = new (std::nothrow) gnn_rel;
+  if (!r) return GNN_ERR_INVALID_ARG;
+  uint8_t* csr = static_cast<uint8_t*>(buffer_d);
+  uint8_t* csc = csr + gnn::align_up(size_t(g->e) + 1, 256);
+  r->g = g;
+  r->n = g->n;
+  r->e = g->e;
+  r->csr = csr;
+  r->csc = csc;
+  r->buckets = n_bounds * (two_sided ? 2 : 1);
+  if (gnn::launch_rel_buckets(g, pos_d, bounds, n_bounds, two_sided, csr, csc,
+                              static_cast<cudaStream_t>(stream)) != cudaSuccess) {
+    delete r;
+    return GNN_ERR_CUDA;
+  }
+  *out = r;
+  return GNN_OK;
+}
+
+gnn_status gnn_rel_destroy(gnn_rel* r) {
+  delete r;
+  return GNN_OK;
+}
+
+gnn_status gnn_rel_arrays(const gnn_rel* r, const void** p, int n) {
+  if (!r || !p || n < 2) return GNN_ERR_INVALID_ARG;
+  p[0] = r->csr;
+  p[1] = r->csc;
+  for (int k = 2; k < n; ++k) p[k] = nullptr;
+  return GNN_OK;
+}
+
+int gnn_rel_buckets(const gnn_rel* r) { return r ? r->buckets : 0; }
+
+size_t transformer_rel_workspace_bytes(const gnn_graph* g, const gnn_rel* rel, int H, int D,
+                                       gnn_dtype dtype) {
+  Shape s;
+  if (rel_shape(g, rel, H, D, dtype, &s) != GNN_OK) return 0;
+  return gnn::transformer_ws_bytes(g, s, rel->buckets);
+}
+
+gnn_status transformer_rel_forward(const gnn_graph* g, const gnn_rel* rel, int H, int D,
+                                   gnn_dtype dtype, const void* q, const void* key,
+                                   const void* val, float scale, const float* bias, void* out,
+                                   float* lse, void* ws, size_t ws_bytes, void* stream) {
+  Shape s;
+  gnn_status r = rel_shape(g, rel, H, D, dtype, &s);
+  if (r != GNN_OK) return r;
+  if (g->n == 0) return GNN_OK;
+  if (!q || !key || !val || !bias || !out || !lse) return GNN_ERR_INVALID_ARG;
+  if (!aligned(q, 16) || !aligned(key, 16) || !aligned(val, 16) || !aligned(out, 16) ||
+      !aligned(bias, 4) || !aligned(lse, 4))
+    return GNN_ERR_INVALID_ARG;
+  if (ws_bytes < gnn::transformer_ws_bytes(g, s, rel->buckets))
+    return GNN_ERR_WORKSPACE_TOO_SMALL;
+  if (!ws || !aligned(ws, 256) || !device_ok(g)) return GNN_ERR_INVALID_ARG;
+  return from_cuda(gnn::launch_transformer_rel_forward(
+      g, rel, s, dtype, q, key, val, scale, bias, out, lse, static_cast<char*>(ws),
+      static_cast<cudaStream_t>(stream)));
+}
+
+gnn_status transformer_rel_backward(const gnn_graph* g, const gnn_rel* rel, int H, int D,
+                                    gnn_dtype dtype, const void* q, const void* key,
+                                    const void* val, float scale, const float* bias,
+                                    const float* lse, const void* dout, void* dq, void* dkey,
+                                    void* dval, float* dbias, void* ws, size_t ws_bytes,
+                                    void* stream) {
+  Shape s;
+  gnn_status r = rel_shape(g, rel, H, D, dtype, &s);
+  if (r != GNN_OK) return r;
+  if (!dbias || !aligned(dbias, 4)) return GNN_ERR_INVALID_ARG;
+  if (g->n == 0) {
+    if (!device_ok(g)) return GNN_ERR_INVALID_ARG;
+    return from_cuda(cudaMemsetAsync(dbias, 0, size_t(rel->buckets) * H * sizeof(float),
+                                     static_cast<cudaStream_t>(stream)));
+  }
+  if (!q || !key || !val || !bias || !lse || !dout || !dq || !dkey || !dval)
+    return GNN_ERR_INVALID_ARG;
+  if (!aligned(q, 16) || !aligned(key, 16) || !aligned(val, 16) || !aligned(dout, 16) ||
+      !aligned(dq, 16) || !aligned(dkey, 16) || !aligned(dval, 16) || !aligned(lse, 4) ||
+      !aligned(bias, 4))
+    return GNN_ERR_INVALID_ARG;
+  if (ws_bytes < gnn::transformer_ws_bytes(g, s, rel->buckets))
+    return GNN_ERR_WORKSPACE_TOO_SMALL;
+  if (!ws || !aligned(ws, 256) || !device_ok(g)) return GNN_ERR_INVALID_ARG;
+  return from_cuda(gnn::launch_transformer_rel_backward(
+      g, rel, s, dtype, q, key, val, scale, bias, lse, dout, dq, dkey, dval, dbias,
+      static_cast<char*>(ws), static_cast<cudaStream_t>(stream)));
 }
 
 size_t reduce_agg_workspace_bytes(const gnn_graph* g, int F, gnn_dtype dtype) {

@@ -45,7 +45,19 @@ struct gnn_graph {
   int sm_count = 0;
 };
 
+// Buckets of a graph's relative node positions (in the caller's buffer).
+struct gnn_rel {
+  const gnn_graph* g = nullptr;
+  int64_t n = 0, e = 0;     // sizes of *g at prepare
+  const uint8_t* csr = nullptr;  // bucket of each edge in CSR order
+  const uint8_t* csc = nullptr;  // ... and in CSC order
+  int buckets = 0;
+};
+
 namespace gnn {
+
+// Buckets of one gnn_rel, both sides together.
+constexpr int kMaxBuckets = 128;
 
 // Per-call shape of the feature rows.
 struct Shape {
@@ -149,7 +161,7 @@ cudaError_t launch_gatv2_backward(const gnn_graph* g, const Shape& s, gnn_dtype 
                                   float* datt, char* ws, cudaStream_t st);
 
 // Graph-transformer attention (transformer.cu), rows of at most 512 bytes.
-size_t transformer_ws_bytes(const gnn_graph* g, const Shape& s);
+size_t transformer_ws_bytes(const gnn_graph* g, const Shape& s, int buckets = 0);
 cudaError_t launch_transformer_forward(const gnn_graph* g, const Shape& s, gnn_dtype dt,
                                        const void* q, const void* key, const void* val,
                                        float scale, void* out, float* lse, char* ws,
@@ -159,6 +171,24 @@ cudaError_t launch_transformer_backward(const gnn_graph* g, const Shape& s, gnn_
                                         float scale, const float* lse, const void* dout,
                                         void* dq, void* dkey, void* dval, char* ws,
                                         cudaStream_t st);
+
+// The same with a learned relative position bias [buckets][H].
+cudaError_t launch_transformer_rel_forward(const gnn_graph* g, const gnn_rel* rel, const Shape& s,
+                                           gnn_dtype dt, const void* q, const void* key,
+                                           const void* val, float scale, const float* bias,
+                                           void* out, float* lse, char* ws, cudaStream_t st);
+cudaError_t launch_transformer_rel_backward(const gnn_graph* g, const gnn_rel* rel,
+                                            const Shape& s, gnn_dtype dt, const void* q,
+                                            const void* key, const void* val, float scale,
+                                            const float* bias, const float* lse,
+                                            const void* dout, void* dq, void* dkey, void* dval,
+                                            float* dbias, char* ws, cudaStream_t st);
+
+// Buckets of relative node positions (relpos.cu).
+void rel_log_bounds(int n, int max_distance, int32_t* bounds);
+cudaError_t launch_rel_buckets(const gnn_graph* g, const int32_t* pos, const int32_t* bounds,
+                               int nb, int two_sided, uint8_t* csr, uint8_t* csc,
+                               cudaStream_t st);
 
 // Bounded-wait self-test (diag.cu).
 cudaError_t launch_wait_selftest(const gnn_graph* g, int polls, cudaStream_t st);

@@ -342,6 +342,76 @@ gnn_status transformer_agg_backward(const gnn_graph* g, int H, int D, gnn_dtype 
                                     const float* lse, const void* dout, void* dq, void* dkey,
                                     void* dval, void* ws, size_t ws_bytes, void* stream);
 
+/* ---- Relative position buckets and the transformer's learned bias -----------
+ *
+ * Nodes that lie along a sequence (tokens, residues, time steps) carry an int32
+ * position pos[N].  A learned bias by relative position adds one number per
+ * (bucket, head) to the attention score:
+ *     e_ij = scale * q_i[k] . key_j[k] + bias[b(pos[j] - pos[i])][k]
+ * with everything else as for transformer_agg_* (positions enter nowhere
+ * else).  The bucket of a difference d: the largest b with bounds[b] <= dist,
+ * dist = |d| for a two-sided rule and max(-d, 0) for a one-sided one; a
+ * two-sided rule then adds n_bounds when d > 0 (the source lies after the
+ * destination).  bounds are whole numbers, ascending (equal neighbours leave a
+ * bucket empty), bounds[0] = 0.  There are n_bounds buckets, or 2 * n_bounds
+ * with two sides, at most 128.
+ * An entry of -infinity masks its bucket for that head: those edges get weight
+ * and gradient 0 whatever their rows hold; a (node, head) with no other edge
+ * gets out = 0 and lse = -infinity.  Any other bias enters as it is. */
+
+/* Host only: bounds of the logarithmic rule.  Distances below m = n_bounds / 2
+ * have a bucket each; bucket m + k starts at the smallest whole t with
+ * floor((n_bounds - m) * log(t / m) / log(max_distance / m)) = k, decided in
+ * whole numbers.  2 <= n_bounds <= 128, max_distance > n_bounds / 2. */
+gnn_status gnn_rel_log_bounds(int n_bounds, int max_distance, int32_t* bounds);
+
+typedef struct gnn_rel gnn_rel; /* opaque; immutable after prepare */
+
+/* Bytes of caller-owned device memory a gnn_rel of g keeps: a byte per edge
+ * and direction. */
+size_t gnn_rel_buffer_bytes(const gnn_graph* g);
+
+/* The bucket of every edge of g, in both directions, from pos_d [n_nodes]
+ * (device; read during the call's kernels only).  bounds [n_bounds]: host.
+ * buffer_d: device, 256-byte aligned, holds the buckets for the lifetime of
+ * *out.  Asynchronous on `stream`, no synchronisation.  g must outlive *out;
+ * the calls below take it with the same g only. */
+gnn_status gnn_rel_prepare(const gnn_graph* g, const int32_t* pos_d, const int32_t* bounds,
+                           int n_bounds, int two_sided, void* buffer_d, size_t buffer_bytes,
+                           void* stream, gnn_rel** out);
+
+/* Frees the host-side handle only. */
+gnn_status gnn_rel_destroy(gnn_rel* r);
+
+/* ptrs[2] receives the bucket bytes [E] in CSR and in CSC order (device). */
+gnn_status gnn_rel_arrays(const gnn_rel* r, const void** ptrs, int n);
+
+/* Buckets of r, both sides together. */
+int gnn_rel_buckets(const gnn_rel* r);
+
+/* Forward and backward pass with the bias.  bias, dbias: float [buckets][H].
+ * The other arguments, shapes and errors are those of transformer_agg_*; the
+ * workspace is transformer_rel_workspace_bytes (0 for an unsupported shape).
+ * The backward writes every element of dq, dkey, dval and dbias,
+ *     dbias[b][k] = sum over the edges of bucket b of
+ *                   alpha_ij[k] (dout_i[k] . val_j[k] - Delta_i[k]);
+ * all four are bitwise reproducible.  The graph's device must be current (else
+ * GNN_ERR_INVALID_ARG). */
+size_t transformer_rel_workspace_bytes(const gnn_graph* g, const gnn_rel* rel, int H, int D,
+                                       gnn_dtype dtype);
+
+gnn_status transformer_rel_forward(const gnn_graph* g, const gnn_rel* rel, int H, int D,
+                                   gnn_dtype dtype, const void* q, const void* key,
+                                   const void* val, float scale, const float* bias, void* out,
+                                   float* lse, void* ws, size_t ws_bytes, void* stream);
+
+gnn_status transformer_rel_backward(const gnn_graph* g, const gnn_rel* rel, int H, int D,
+                                    gnn_dtype dtype, const void* q, const void* key,
+                                    const void* val, float scale, const float* bias,
+                                    const float* lse, const void* dout, void* dq, void* dkey,
+                                    void* dval, float* dbias, void* ws, size_t ws_bytes,
+                                    void* stream);
+
 /* ---- Max / min neighbourhood reduction -----------------------------------
  *
  * out[i][f] = max (or min) over the in-neighbours j of i of x[j][f], and
