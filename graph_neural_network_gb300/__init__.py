@@ -32,6 +32,11 @@ the same with a learned relative position bias (bias [buckets, H], pos [N] int32
     out, lse = transformer_rel_forward(g, rel, q, key, val, bias)
     dq, dkey, dval, dbias = transformer_rel_backward(g, rel, q, key, val, bias, lse, dout)
 
+the norms, gate and residual scale between two blocks of a layer:
+
+    y, z = norm_residual_forward(x, o, gate, w_post, scale=scale, w_pre=w_pre)
+    grads = norm_residual_backward(y, o, dy, dz, gate, w_post, scale=scale, w_pre=w_pre)
+
 and the max / min neighbourhood reduction with its winners:
 
     out, arg = reduce_forward(g, x, "max")         # arg [N, F] int32, -1 if no in-edges
@@ -52,7 +57,8 @@ __all__ = ["Graph", "gat_forward", "gat_backward", "GATAggregate", "GnnError", "
            "GCNAggregate", "reduce_forward", "reduce_backward", "ReduceAggregate",
            "gatv2_forward", "gatv2_backward", "GATv2Aggregate", "transformer_forward",
            "transformer_backward", "TransformerAggregate", "RelPos", "transformer_rel_forward",
-           "transformer_rel_backward", "TransformerRelAggregate"]
+           "transformer_rel_backward", "TransformerRelAggregate", "norm_residual_forward",
+           "norm_residual_backward", "NormResidual"]
 
 
 def _ptr(t):
@@ -614,6 +620,154 @@ class TransformerRelAggregate(torch.autograd.Function):
         dq, dk, dv, db = transformer_rel_backward(ctx.g, ctx.rel, q, key, val, bias, lse,
                                                   dout.contiguous(), ctx.scale)
         return None, None, dq, dk, dv, db.to(bias.dtype), None
+
+
+_NORM_PARAMS = ("w_post", "b_post", "scale", "w_pre", "b_pre")
+
+
+def _plain_tensor(t, name, shape, dtype, device):
+    """Raise unless t is a contiguous tensor of that shape, dtype and device."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor, got {type(t).__name__}")
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if t.device != device or not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous and on {device}")
+    return t
+
+
+def _norm_desc(o, gate, params, kind, eps):
+    """The call's gnn_norm_residual, the float32 parameters it points to (to be
+    kept until the launch) and the norm before the next block."""
+    if not isinstance(o, torch.Tensor) or o.dim() < 2:
+        raise ValueError("o must be a tensor [N, ...]")
+    _dtype_code(o.dtype)
+    if not o.is_cuda or not o.is_contiguous():
+        raise ValueError("o must be a contiguous CUDA tensor")
+    post, pre = (kind, kind) if isinstance(kind, str) else kind
+    if post not in _native.ROWNORMS or pre not in _native.ROWNORMS:
+        raise ValueError(f"kind must be one of {sorted(_native.ROWNORMS)}, or a pair of them "
+                         "(after the block, before the next)")
+    n = o.shape[0]
+    F = 1
+    for d in o.shape[1:]:
+        F *= d
+    d = _native.NormResidual(n=n, F=F, post=_native.ROWNORMS[post], pre=_native.ROWNORMS[pre],
+                             eps=eps)
+    if gate is not None:
+        wide = isinstance(gate, torch.Tensor) and gate.shape == o.shape
+        _plain_tensor(gate, "gate", o.shape if wide else (n, 1), o.dtype, o.device)
+        d.gate_width = F if wide else 1
+    kept = {}
+    for k, t in zip(_NORM_PARAMS, params):
+        if t is None:
+            continue
+        if not isinstance(t, torch.Tensor) or not t.is_floating_point():
+            raise TypeError(f"{k} must be a floating-point tensor")
+        kept[k] = _plain_tensor(t.to(torch.float32), k, (F,), torch.float32, o.device)
+        setattr(d, k, t.data_ptr() if kept[k] is t else kept[k].data_ptr())
+    return d, kept, pre
+
+
+def norm_residual_forward(x: torch.Tensor, o: torch.Tensor, gate=None, w_post=None, b_post=None,
+                          scale=None, w_pre=None, b_pre=None, kind="rms", eps: float = 1e-6,
+                          y=None, z=None, stream=None):
+    """y = x + scale * sigmoid(gate) * (norm(o) w_post + b_post) and
+    z = norm(y) w_pre + b_pre, for x, o [N, ...] (a node's features flattened).
+
+    kind: "rms", "layer" or "none" for both norms, or a pair (after the block,
+    before the next).  gate: None, [N, 1] or o's shape (before its sigmoid).
+    Parameters have one entry per feature; None leaves a factor or a sum out.
+    z is None where the second norm is "none"."""
+    d, kept, pre = _norm_desc(o, gate, (w_post, b_post, scale, w_pre, b_pre), kind, eps)
+    _plain_tensor(x, "x", o.shape, o.dtype, o.device)
+    with _launch_on(o.device, stream) as s:
+        y = torch.empty_like(o) if y is None else _plain_tensor(y, "y", o.shape, o.dtype, o.device)
+        if pre != "none":
+            z = torch.empty_like(o) if z is None else _plain_tensor(z, "z", o.shape, o.dtype,
+                                                                    o.device)
+        elif z is not None:
+            raise ValueError("there is no z without a norm before the next block")
+        rc = _native.load().gnn_norm_residual_forward(
+            ctypes.byref(d), _dtype_code(o.dtype), _ptr(x), _ptr(o), _ptr(gate), _ptr(y), _ptr(z),
+            s)
+    _native.check(rc, "gnn_norm_residual_forward")
+    return y, z
+
+
+def norm_residual_backward(y, o: torch.Tensor, dy: torch.Tensor, dz=None, gate=None, w_post=None,
+                           b_post=None, scale=None, w_pre=None, b_pre=None, kind="rms",
+                           eps: float = 1e-6, ws=None, stream=None, grads=None):
+    """The gradients of norm_residual_forward, as a dict: dx, do, dgate (o's
+    dtype; dgate None without a gate) and dw_post, db_post, dscale, dw_pre,
+    db_pre (float32; None where the parameter is).  y is the forward's y, dy the
+    gradient that reaches it past the second norm and dz that of z; y and dz are
+    None where that norm is "none".  grads: outputs to write, by those names."""
+    d, kept, pre = _norm_desc(o, gate, (w_post, b_post, scale, w_pre, b_pre), kind, eps)
+    like = (o.shape, o.dtype, o.device)
+    _plain_tensor(dy, "dy", *like)
+    for name, t in (("y", y), ("dz", dz)):
+        if pre != "none":
+            _plain_tensor(t, name, *like)
+        elif t is not None:
+            raise ValueError(f"there is no {name} without a norm before the next block")
+    given = dict(grads or {})
+    with _launch_on(o.device, stream) as s:
+        def out(name, like_):
+            t = given.pop(name, None)
+            if like_ is None:
+                if t is not None:
+                    raise ValueError(f"there is no {name} in this call")
+                return None
+            return torch.empty_like(like_) if t is None else _plain_tensor(
+                t, name, like_.shape, like_.dtype, o.device)
+
+        got = {"dx": out("dx", o), "do": out("do", o), "dgate": out("dgate", gate)}
+        for k in _NORM_PARAMS:
+            got["d" + k] = out("d" + k, kept.get(k))
+        if given:
+            raise ValueError(f"unknown gradients {sorted(given)}")
+        lib = _native.load()
+        dt = _dtype_code(o.dtype)
+        need = lib.gnn_norm_residual_workspace_bytes(ctypes.byref(d), dt)
+        if ws is None:
+            ws = torch.empty(need, dtype=torch.uint8, device=o.device)
+        elif not isinstance(ws, torch.Tensor) or ws.dtype != torch.uint8 or ws.dim() != 1 or \
+                ws.device != o.device or not ws.is_contiguous():
+            raise ValueError(f"ws must be a one-dimensional uint8 tensor on {o.device}")
+        gr = _native.NormGrads(*(None if t is None else t.data_ptr() for t in got.values()))
+        rc = lib.gnn_norm_residual_backward(
+            ctypes.byref(d), dt, _ptr(y), _ptr(o), _ptr(gate), _ptr(dy), _ptr(dz),
+            ctypes.byref(gr), _ptr(ws), ws.numel(), s)
+    _native.check(rc, "gnn_norm_residual_backward")
+    return got
+
+
+class NormResidual(torch.autograd.Function):
+    """y, z = NormResidual.apply(x, o, gate, w_post, b_post, scale, w_pre, b_pre,
+    kind, eps)."""
+
+    @staticmethod
+    def forward(ctx, x, o, gate, w_post, b_post, scale, w_pre, b_pre, kind, eps):
+        x, o, gate = (None if t is None else t.contiguous() for t in (x, o, gate))
+        params = [None if t is None else t.contiguous()
+                  for t in (w_post, b_post, scale, w_pre, b_pre)]
+        y, z = norm_residual_forward(x, o, gate, *params, kind=kind, eps=eps)
+        ctx.kind, ctx.eps = kind, eps
+        ctx.save_for_backward(None if z is None else y, o, gate, *params)
+        return y, z
+
+    @staticmethod
+    def backward(ctx, dy, dz):
+        y, o, gate, *params = ctx.saved_tensors
+        dz = None if y is None else dz.contiguous()
+        g = norm_residual_backward(y, o, dy.contiguous(), dz, gate, *params, kind=ctx.kind,
+                                   eps=ctx.eps)
+        return (g["dx"], g["do"], g["dgate"],
+                *(None if t is None else g["d" + k].to(t.dtype)
+                  for k, t in zip(_NORM_PARAMS, params)), None, None)
 
 
 def _reduce_ws(g, F, dt, ws, device):

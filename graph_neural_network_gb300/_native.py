@@ -20,6 +20,7 @@ ERR_WORKSPACE_TOO_SMALL, ERR_CUDA, ERR_DEVICE_ASSERT, ERR_TIMEOUT = 4, 5, 6, 7
 F32, BF16 = 0, 1
 NORMS = {"sum": 0, "mean": 1, "sym": 2}  # gnn_norm
 REDUCE_OPS = {"max": 0, "min": 1}        # gnn_reduce_op
+ROWNORMS = {"none": 0, "rms": 1, "layer": 2}  # gnn_rownorm
 
 # (name, restype, argtypes) of every exported symbol, in header order
 _P, _I64, _I32, _SZ, _F = (ctypes.c_void_p, ctypes.c_int64, ctypes.c_int32, ctypes.c_size_t,
@@ -67,6 +68,9 @@ SIGNATURES = [
                                        _SZ, _P]),
     ("transformer_rel_backward", _I32, [_P, _P, _I32, _I32, _I32, _P, _P, _P, _F, _P, _P, _P, _P,
                                         _P, _P, _P, _P, _SZ, _P]),
+    ("gnn_norm_residual_forward", _I32, [_P, _I32, _P, _P, _P, _P, _P, _P]),
+    ("gnn_norm_residual_workspace_bytes", _SZ, [_P, _I32]),
+    ("gnn_norm_residual_backward", _I32, [_P, _I32, _P, _P, _P, _P, _P, _P, _P, _SZ, _P]),
     ("reduce_agg_workspace_bytes", _SZ, [_P, _I32, _I32]),
     ("reduce_agg_forward", _I32, [_P, _I32, _I32, _I32, _P, _P, _P, _P, _SZ, _P]),
     ("reduce_agg_backward", _I32, [_P, _I32, _I32, _P, _P, _P, _P, _SZ, _P]),
@@ -81,6 +85,16 @@ SIGNATURES = [
 class Tiling(ctypes.Structure):
     _fields_ = [("light_max_deg", ctypes.c_int32), ("cta_max_deg", ctypes.c_int32),
                 ("hub_chunk", ctypes.c_int32)]
+
+
+class NormResidual(ctypes.Structure):  # gnn_norm_residual, its parameters in line
+    _fields_ = [("n", _I64), ("F", _I32), ("post", _I32), ("pre", _I32), ("gate_width", _I32),
+                ("eps", _F)] + [(k, _P) for k in ("w_post", "b_post", "scale", "w_pre", "b_pre")]
+
+
+class NormGrads(ctypes.Structure):
+    _fields_ = [(k, _P) for k in ("dx", "dout", "dgate", "dw_post", "db_post", "dscale", "dw_pre",
+                                  "db_pre")]
 
 
 class GnnError(RuntimeError):

@@ -414,6 +414,33 @@ bool device_ok(const gnn_graph* g) {
   return cudaGetDevice(&dev) == cudaSuccess && dev == g->device;
 }
 
+gnn_status norm_residual_check(const gnn_norm_residual* d, gnn_dtype dt) {
+  if (!d || (dt != GNN_F32 && dt != GNN_BF16) || d->n < 0 || d->n >= (int64_t(1) << 31) ||
+      d->F < 1)
+    return GNN_ERR_INVALID_ARG;
+  const auto known = [](gnn_rownorm k) {
+    return k == GNN_ROWNORM_NONE || k == GNN_ROWNORM_RMS || k == GNN_ROWNORM_LAYER;
+  };
+  const gnn_norm_params& p = d->params;
+  if (!known(d->post) || !known(d->pre) || !(d->eps > 0.f) || d->eps > 3.0e38f ||
+      (d->gate_width != 0 && d->gate_width != 1 && d->gate_width != d->F))
+    return GNN_ERR_INVALID_ARG;
+  if ((d->post == GNN_ROWNORM_NONE && (p.w_post || p.b_post)) ||
+      (d->pre == GNN_ROWNORM_NONE && (p.w_pre || p.b_pre)))
+    return GNN_ERR_INVALID_ARG;
+  if (!aligned(p.w_post, 4) || !aligned(p.b_post, 4) || !aligned(p.scale, 4) ||
+      !aligned(p.w_pre, 4) || !aligned(p.b_pre, 4))
+    return GNN_ERR_INVALID_ARG;
+  const int64_t bytes = int64_t(d->F) * (dt == GNN_F32 ? 4 : 2);
+  return bytes % 16 || bytes > 2048 ? GNN_ERR_UNSUPPORTED : GNN_OK;
+}
+
+// A gate or its gradient: null exactly where there is no gate, aligned.
+bool gate_ok(const gnn_norm_residual* d, gnn_dtype dt, const void* gate) {
+  if (d->gate_width == 0) return !gate;
+  return gate && aligned(gate, d->gate_width == 1 ? (dt == GNN_F32 ? 4 : 2) : 16);
+}
+
 gnn_status rel_shape(const gnn_graph* g, const gnn_rel* rel, int H, int D, gnn_dtype dt,
                      Shape* s) {
   if (!g || !rel || rel->g != g || rel->n != g->n || rel->e != g->e) return GNN_ERR_INVALID_ARG;
@@ -627,6 +654,57 @@ gnn_status transformer_rel_backward(const gnn_graph* g, const gnn_rel* rel, int 
   return from_cuda(gnn::launch_transformer_rel_backward(
       g, rel, s, dtype, q, key, val, scale, bias, lse, dout, dq, dkey, dval, dbias,
       static_cast<char*>(ws), static_cast<cudaStream_t>(stream)));
+}
+
+gnn_status gnn_norm_residual_forward(const gnn_norm_residual* d, gnn_dtype dtype, const void* x,
+                                     const void* o, const void* gate, void* y, void* z,
+                                     void* stream) {
+  const gnn_status r = norm_residual_check(d, dtype);
+  if (r != GNN_OK) return r;
+  if ((d->pre == GNN_ROWNORM_NONE) != !z && d->n > 0) return GNN_ERR_INVALID_ARG;
+  if (d->n == 0) return GNN_OK;
+  if (!x || !o || !y || !gate_ok(d, dtype, gate)) return GNN_ERR_INVALID_ARG;
+  if (!aligned(x, 16) || !aligned(o, 16) || !aligned(y, 16) || !aligned(z, 16))
+    return GNN_ERR_INVALID_ARG;
+  int dev = 0, sms = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess ||
+      cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
+    return GNN_ERR_CUDA;
+  return from_cuda(gnn::launch_norm_residual_forward(*d, dtype, x, o, gate, y, z, sms,
+                                                     static_cast<cudaStream_t>(stream)));
+}
+
+size_t gnn_norm_residual_workspace_bytes(const gnn_norm_residual* d, gnn_dtype dtype) {
+  if (norm_residual_check(d, dtype) != GNN_OK) return 0;
+  return gnn::norm_residual_ws_bytes(d->n, d->F, dtype);
+}
+
+gnn_status gnn_norm_residual_backward(const gnn_norm_residual* d, gnn_dtype dtype, const void* y,
+                                      const void* o, const void* gate, const void* dy,
+                                      const void* dz, const gnn_norm_grads* grads, void* ws,
+                                      size_t ws_bytes, void* stream) {
+  const gnn_status r = norm_residual_check(d, dtype);
+  if (r != GNN_OK) return r;
+  if (!grads) return GNN_ERR_INVALID_ARG;
+  const gnn_norm_grads& g = *grads;
+  if (d->n > 0) {
+    const bool pre = d->pre != GNN_ROWNORM_NONE;
+    if (!o || !dy || !g.dx || !g.dout || pre != (y != nullptr) || pre != (dz != nullptr) ||
+        !gate_ok(d, dtype, gate) || !gate_ok(d, dtype, g.dgate))
+      return GNN_ERR_INVALID_ARG;
+    if (!aligned(y, 16) || !aligned(o, 16) || !aligned(dy, 16) || !aligned(dz, 16) ||
+        !aligned(g.dx, 16) || !aligned(g.dout, 16))
+      return GNN_ERR_INVALID_ARG;
+  }
+  if (!aligned(g.dw_post, 4) || !aligned(g.db_post, 4) || !aligned(g.dscale, 4) ||
+      !aligned(g.dw_pre, 4) || !aligned(g.db_pre, 4))
+    return GNN_ERR_INVALID_ARG;
+  if (ws_bytes < gnn::norm_residual_ws_bytes(d->n, d->F, dtype))
+    return GNN_ERR_WORKSPACE_TOO_SMALL;
+  if (!ws || !aligned(ws, 256)) return GNN_ERR_INVALID_ARG;
+  return from_cuda(gnn::launch_norm_residual_backward(*d, dtype, y, o, gate, dy, dz, g,
+                                                      static_cast<char*>(ws),
+                                                      static_cast<cudaStream_t>(stream)));
 }
 
 size_t reduce_agg_workspace_bytes(const gnn_graph* g, int F, gnn_dtype dtype) {

@@ -190,6 +190,17 @@ cudaError_t launch_rel_buckets(const gnn_graph* g, const int32_t* pos, const int
                                int nb, int two_sided, uint8_t* csr, uint8_t* csc,
                                cudaStream_t st);
 
+// Norms before and after a block with its gate and residual scale
+// (norm_residual.cu).
+size_t norm_residual_ws_bytes(int64_t n, int F, gnn_dtype dt);
+cudaError_t launch_norm_residual_forward(const gnn_norm_residual& d, gnn_dtype dt, const void* x,
+                                         const void* o, const void* gate, void* y, void* z,
+                                         int sm_count, cudaStream_t st);
+cudaError_t launch_norm_residual_backward(const gnn_norm_residual& d, gnn_dtype dt, const void* y,
+                                          const void* o, const void* gate, const void* dy,
+                                          const void* dz, const gnn_norm_grads& grads, char* ws,
+                                          cudaStream_t st);
+
 // Bounded-wait self-test (diag.cu).
 cudaError_t launch_wait_selftest(const gnn_graph* g, int polls, cudaStream_t st);
 

@@ -412,6 +412,62 @@ gnn_status transformer_rel_backward(const gnn_graph* g, const gnn_rel* rel, int 
                                     void* dval, float* dbias, void* ws, size_t ws_bytes,
                                     void* stream);
 
+/* ---- Norms before and after a block, gate and residual scale ----------------
+ *
+ * The per-node half of a transformer layer, between one block (an aggregation
+ * with its output projection) and the next.  Per node, with the residual stream
+ * x, the block's output o and the gate's pre-activation g:
+ *     n = norm(o) * w_post + b_post
+ *     y = x + scale * sigmoid(g) * n
+ *     z = norm(y) * w_pre + b_pre
+ * norm: GNN_ROWNORM_RMS v / sqrt(mean(v^2) + eps), GNN_ROWNORM_LAYER
+ * (v - mean) / sqrt(mean((v - mean)^2) + eps), GNN_ROWNORM_NONE v itself.
+ * post = NONE leaves the block's output as it is (w_post and b_post must be
+ * null); pre = NONE computes no z (z, dz, w_pre and b_pre must be null, and the
+ * backward takes no y).  A null weight or scale counts as 1, a null bias as 0.
+ * gate_width 0: no gate (g null); 1: g [n], one per node; F: g [n][F].
+ * n rows of F elements; F * sizeof(dtype) a multiple of 16, at most 2048
+ * bytes.  x, o, y, z, g and their gradients: dtype, 16-byte aligned (g of
+ * width 1: by its element); parameters and their gradients float [F].
+ * Arithmetic in float32, each output rounded once.  No output may overlap an
+ * input.  Asynchronous on `stream`; results are bitwise reproducible. */
+typedef enum { GNN_ROWNORM_NONE = 0, GNN_ROWNORM_RMS = 1, GNN_ROWNORM_LAYER = 2 } gnn_rownorm;
+
+typedef struct {
+  const float *w_post, *b_post, *scale, *w_pre, *b_pre; /* [F] each, or null */
+} gnn_norm_params;
+
+typedef struct {
+  int64_t n;
+  int32_t F;
+  gnn_rownorm post, pre;
+  int32_t gate_width; /* 0, 1 or F */
+  float eps;          /* > 0 */
+  gnn_norm_params params;
+} gnn_norm_residual;
+
+/* Gradients: dx = the gradient of x (all that reaches y), dout of o, dgate of g
+ * (null without a gate); of the parameters, null where not wanted. */
+typedef struct {
+  void *dx, *dout, *dgate;
+  float *dw_post, *db_post, *dscale, *dw_pre, *db_pre;
+} gnn_norm_grads;
+
+gnn_status gnn_norm_residual_forward(const gnn_norm_residual* d, gnn_dtype dtype, const void* x,
+                                     const void* o, const void* gate, void* y, void* z,
+                                     void* stream);
+
+/* Workspace of the backward pass (host only; 0 for an unsupported shape). */
+size_t gnn_norm_residual_workspace_bytes(const gnn_norm_residual* d, gnn_dtype dtype);
+
+/* dy: the gradient that reaches y past the next norm, dz that of z.  y is the
+ * forward's y; the rows' statistics are computed again.  Writes every element
+ * of the gradients given. */
+gnn_status gnn_norm_residual_backward(const gnn_norm_residual* d, gnn_dtype dtype, const void* y,
+                                      const void* o, const void* gate, const void* dy,
+                                      const void* dz, const gnn_norm_grads* grads, void* ws,
+                                      size_t ws_bytes, void* stream);
+
 /* ---- Max / min neighbourhood reduction -----------------------------------
  *
  * out[i][f] = max (or min) over the in-neighbours j of i of x[j][f], and

@@ -151,3 +151,114 @@ def log_bounds(n, max_distance):
                 lo = mid + 1
         out.append(lo)
     return out
+
+
+# ---------------------------------------------------------------------------
+# norms, gate and residual scale
+# ---------------------------------------------------------------------------
+#
+# Bounds.  A sum over a row (at most 1024 elements: eight in a thread, then a
+# tree) makes at most 20 roundings: relative to its magnitude sum, G = 32 u with
+# the products and the division.  A layer mean is then off by e = G max|x|, a
+# normed value by E = e rstd + |hat| (G + e rstd) (rms: e = 0).  The sigmoid is
+# off by 2^-21 + 2 u |g| relative (exponential 2^-22, its argument g log2(e) with
+# a rounded constant and product, sum and quotient).  The rest is the product rule, each operation adding u; parameter sums add R u
+# for the R rows that a thread adds in sequence.
+
+G = 32 * U
+SIG = 2.0 ** -21
+
+
+def _norm(x, kind, eps):
+    """hat, rstd, and the bounds of hat (absolute) and rstd (relative)."""
+    if kind == "none":
+        return x, np.ones((len(x), 1)), np.zeros_like(x), 0.0
+    mean = x.mean(-1, keepdims=True) if kind == "layer" else 0.0
+    e = G * np.abs(x).max(-1, keepdims=True) if kind == "layer" else 0.0
+    rstd = 1 / np.sqrt(((x - mean) ** 2).mean(-1, keepdims=True) + eps)
+    hat = (x - mean) * rstd
+    rho = G + e * rstd
+    return hat, rstd, e * rstd + np.abs(hat) * rho, rho
+
+
+def _params(p, F):
+    one, nil = np.ones(F), np.zeros(F)
+    return [np.asarray(p.get(k), np.float64) if p.get(k) is not None else d for k, d in
+            (("w_post", one), ("b_post", nil), ("scale", one), ("w_pre", one), ("b_pre", nil))]
+
+
+def _sig(gate, like):
+    if gate is None:
+        return np.ones_like(like), 0.0
+    return (np.broadcast_to(1 / (1 + np.exp(-gate)), like.shape),
+            np.broadcast_to(SIG + 2 * U * np.abs(gate), like.shape))
+
+
+def norm_residual(x, o, gate, p, kinds, eps):
+    """y, z and their bounds (without the rounding of the result)."""
+    wp, bp, sc, wn, bn = _params(p, x.shape[1])
+    oh, _, Eo, _ = _norm(o, kinds[0], eps)
+    sig, serr = _sig(gate, x)
+    n = oh * wp + bp
+    dn = np.abs(wp) * Eo + 3 * U * (np.abs(oh * wp) + np.abs(bp))
+    y = x + sc * sig * n
+    by = np.abs(sc * sig) * dn + (serr + 4 * U) * np.abs(sc * sig * n) + U * np.abs(y)
+    if kinds[1] == "none":
+        return y, by, None, None
+    yh, rstd, Ey, _ = _norm(y, kinds[1], eps)
+    # an error d of y moves the normed row by rstd (d - mean d) and by its length
+    move = rstd * (by + by.mean(-1, keepdims=True)) + np.abs(yh) * rstd * np.sqrt(
+        (by ** 2).mean(-1, keepdims=True))
+    z = yh * wn + bn
+    bz = np.abs(wn) * (Ey + move) + 3 * U * (np.abs(yh * wn) + np.abs(bn))
+    return y, by, z, bz
+
+
+def _norm_back(g, dg, hat, E, rstd, rho, kind):
+    if kind == "none":
+        return g, dg
+    m = lambda a: a.mean(-1, keepdims=True)  # noqa: E731
+    c0, b0 = m(g * hat), m(dg * np.abs(hat) + np.abs(g) * E) + G * m(np.abs(g * hat))
+    c1, b1 = (m(g), m(dg) + G * m(np.abs(g))) if kind == "layer" else (0.0, 0.0)
+    d = rstd * (g - c1 - hat * c0)
+    return d, np.abs(d) * rho + rstd * (dg + b1 + np.abs(c0) * E + np.abs(hat) * b0 + 4 * U * (
+        np.abs(g) + np.abs(c1) + np.abs(hat * c0)))
+
+
+def norm_residual_grads(y, o, gate, dy, dz, p, kinds, eps):
+    """{name: (value, bound)} of the gradients, from y as given."""
+    n_rows, F = o.shape
+    wp, bp, sc, wn, _ = _params(p, F)
+    oh, ro, Eo, rho_o = _norm(o, kinds[0], eps)
+    got = {}
+    R = 32 + n_rows / 600
+    def total(a, da): return a.sum(0), da.sum(0) + R * U * np.abs(a).sum(0)  # noqa: E704
+    if kinds[1] == "none":
+        dx, bx = dy, np.zeros_like(dy)
+    else:
+        yh, ry, Ey, rho_y = _norm(y, kinds[1], eps)
+        t, bt = _norm_back(dz * wn, U * np.abs(dz * wn), yh, Ey, ry, rho_y, kinds[1])
+        dx = dy + t
+        bx = bt + U * np.abs(dx)
+        got["dw_pre"] = total(dz * yh, np.abs(dz) * Ey + U * np.abs(dz * yh))
+        got["db_pre"] = total(dz, 0 * dz)
+    got["dx"] = dx, bx
+    sig, serr = _sig(gate, o)
+    n = oh * wp + bp
+    bn = np.abs(wp) * Eo + 3 * U * (np.abs(oh * wp) + np.abs(bp))
+    u = dx * sc * sig
+    bu = bx * np.abs(sc * sig) + (serr + 3 * U) * np.abs(u)
+    got["dscale"] = total(dx * sig * n, np.abs(sig) * (bx * np.abs(n) + np.abs(dx) * bn) +
+                          (serr + 3 * U) * np.abs(dx * sig * n))
+    got["dw_post"] = total(u * oh, bu * np.abs(oh) + np.abs(u) * Eo + U * np.abs(u * oh))
+    got["db_post"] = total(u, bu)
+    if gate is not None:
+        dg = u * n * (1 - sig)
+        bg = (bu * np.abs(n) + np.abs(u) * bn) * (1 - sig) + np.abs(u * n) * (
+            serr * sig + 2 * U) + 4 * U * np.abs(dg)
+        if gate.shape[1] == 1 and F != 1:
+            dg, bg = dg.sum(-1, keepdims=True), (bg + G * np.abs(dg)).sum(-1, keepdims=True)
+        got["dgate"] = dg, bg
+    got["do"] = _norm_back(u * wp, bu * np.abs(wp) + U * np.abs(u * wp), oh, Eo, ro, rho_o,
+                           kinds[0])
+    return got
