@@ -32,6 +32,11 @@ the same with a learned relative position bias (bias [buckets, H], pos [N] int32
     out, lse = transformer_rel_forward(g, rel, q, key, val, bias)
     dq, dkey, dval, dbias = transformer_rel_backward(g, rel, q, key, val, bias, lse, dout)
 
+the attention's backward pass from 8-bit checkpoints of q, key and val:
+
+    q8, key8, val8 = pack8(q, key, val)                # int8 values, a scale per head vector
+    dq, dkey, dval = transformer_backward8(g, q8, key8, val8, dout)   # rel=, bias= too
+
 the norms, gate and residual scale between two blocks of a layer:
 
     y, z = norm_residual_forward(x, o, gate, w_post, scale=scale, w_pre=w_pre)
@@ -46,6 +51,7 @@ from __future__ import annotations
 
 import contextlib
 import ctypes
+from typing import NamedTuple
 
 import torch
 
@@ -58,7 +64,8 @@ __all__ = ["Graph", "gat_forward", "gat_backward", "GATAggregate", "GnnError", "
            "gatv2_forward", "gatv2_backward", "GATv2Aggregate", "transformer_forward",
            "transformer_backward", "TransformerAggregate", "RelPos", "transformer_rel_forward",
            "transformer_rel_backward", "TransformerRelAggregate", "norm_residual_forward",
-           "norm_residual_backward", "NormResidual"]
+           "norm_residual_backward", "NormResidual", "Packed8", "pack8", "unpack8",
+           "transformer_backward8", "TransformerCheckpoint8"]
 
 
 def _ptr(t):
@@ -620,6 +627,135 @@ class TransformerRelAggregate(torch.autograd.Function):
         dq, dk, dv, db = transformer_rel_backward(ctx.g, ctx.rel, q, key, val, bias, lse,
                                                   dout.contiguous(), ctx.scale)
         return None, None, dq, dk, dv, db.to(bias.dtype), None
+
+
+class Packed8(NamedTuple):
+    """An activation [N, H, D] in 8 bits: int8 values of that shape and a
+    float32 scale [N, H], standing for values * scale[..., None]."""
+
+    values: torch.Tensor
+    scale: torch.Tensor
+
+
+def pack8(*xs: torch.Tensor, out=None, stream=None):
+    """8-bit checkpoints of up to 8 tensors [N, H, D] of one shape and dtype, in
+    one launch: a Packed8 for each.  Every head vector has its own scale, the
+    largest magnitude over 127; values are rounded to nearest, ties to even.
+    out: the Packed8s to write."""
+    if not 1 <= len(xs) <= 8:
+        raise ValueError("pack8 takes 1 to 8 tensors")
+    x = xs[0]
+    if not isinstance(x, torch.Tensor) or x.dim() != 3 or not x.is_cuda:
+        raise ValueError("pack8 takes CUDA tensors [N, H, D]")
+    dt = _dtype_code(x.dtype)
+    for k, t in enumerate(xs):
+        _plain_tensor(t, f"tensor {k}", x.shape, x.dtype, x.device)
+    N, H, D = x.shape
+    with _launch_on(x.device, stream) as s:
+        if out is None:
+            out = tuple(Packed8(torch.empty(x.shape, dtype=torch.int8, device=x.device),
+                                torch.empty((N, H), dtype=torch.float32, device=x.device))
+                        for _ in xs)
+        else:
+            out = tuple(out)
+            if len(out) != len(xs):
+                raise ValueError("out must have a Packed8 for every tensor")
+            for p in out:
+                _packed(p, "out", x.shape, x.device)
+        rows = ctypes.c_void_p * len(xs)
+        rc = _native.load().gnn_pack8(len(xs), N, H, D, dt, rows(*(t.data_ptr() for t in xs)),
+                                      rows(*(p.values.data_ptr() for p in out)),
+                                      rows(*(p.scale.data_ptr() for p in out)), s)
+    _native.check(rc, "gnn_pack8")
+    return out
+
+
+def _packed(p, name, shape, device) -> _native.Packed8:
+    if not isinstance(p, Packed8):
+        raise TypeError(f"{name} must be a Packed8, got {type(p).__name__}")
+    _plain_tensor(p.values, f"{name}.values", shape, torch.int8, device)
+    _plain_tensor(p.scale, f"{name}.scale", shape[:2], torch.float32, device)
+    return _native.Packed8(p.values.data_ptr(), p.scale.data_ptr())
+
+
+def unpack8(p: Packed8, dtype: torch.dtype = torch.float32, out=None, stream=None):
+    """values * scale, rounded to dtype (float32 or bfloat16)."""
+    if not isinstance(p, Packed8) or not isinstance(p.values, torch.Tensor) or \
+            p.values.dim() != 3 or not p.values.is_cuda:
+        raise ValueError("unpack8 takes a Packed8 of CUDA tensors")
+    dt = _dtype_code(dtype)
+    shape, device = p.values.shape, p.values.device
+    c = _packed(p, "p", shape, device)
+    with _launch_on(device, stream) as s:
+        out = torch.empty(shape, dtype=dtype, device=device) if out is None else \
+            _plain_tensor(out, "out", shape, dtype, device)
+        rc = _native.load().gnn_unpack8(*shape, dt, ctypes.byref(c), _ptr(out), s)
+    _native.check(rc, "gnn_unpack8")
+    return out
+
+
+def transformer_backward8(g: Graph, q: Packed8, key: Packed8, val: Packed8, dout: torch.Tensor,
+                          scale: float | None = None, rel: RelPos | None = None, bias=None,
+                          dq=None, dkey=None, dval=None, dbias=None, ws=None, stream=None):
+    """The gradients of the graph-transformer attention from 8-bit checkpoints
+    of q, key and val, taken at the values that these stand for (its softmax is
+    computed there too; no lse is needed): dq, dkey, dval (dout's dtype) and,
+    with rel and bias, dbias [buckets,H] float32."""
+    _check_features(g, dout, "dout")
+    N, H, D = dout.shape
+    c = [_packed(p, name, dout.shape, g.device) for name, p in
+         (("q", q), ("key", key), ("val", val))]
+    if (rel is None) != (bias is None):
+        raise ValueError("rel and bias go together")
+    scale = D ** -0.5 if scale is None else float(scale)
+    dt = _dtype_code(dout.dtype)
+    with _launch_on(g.device, stream) as s:
+        if rel is not None:
+            bias = _rel_inputs(g, rel, bias, H)
+            dbias = _given(g, dbias, "dbias", bias.shape, torch.float32,
+                           lambda: torch.empty_like(bias))
+        elif dbias is not None:
+            raise ValueError("there is no dbias without a bias")
+        dq, dkey, dval = (_given(g, t, name, dout.shape, dout.dtype,
+                                 lambda: torch.empty_like(dout))
+                          for name, t in (("dq", dq), ("dkey", dkey), ("dval", dval)))
+        handle = None if rel is None else rel.handle
+        if _check_ws(g, ws) is None:
+            n = g._lib.transformer_packed8_workspace_bytes(g.handle, handle, H, D, dt)
+            if n == 0:
+                raise GnnError(_native.ERR_UNSUPPORTED, f"(H={H}, D={D}, {dout.dtype})")
+            ws = torch.empty(n, dtype=torch.uint8, device=g.device)
+        rc = g._lib.transformer_packed8_backward(
+            g.handle, handle, H, D, dt, *(ctypes.byref(x) for x in c), scale, _ptr(bias),
+            _ptr(dout), _ptr(dq), _ptr(dkey), _ptr(dval), _ptr(dbias), _ptr(ws), ws.numel(), s)
+    _native.check(rc, "transformer_packed8_backward")
+    return (dq, dkey, dval) if rel is None else (dq, dkey, dval, dbias)
+
+
+class TransformerCheckpoint8(torch.autograd.Function):
+    """out = TransformerCheckpoint8.apply(graph, rel, q, key, val, bias, scale):
+    the graph-transformer attention (rel and bias None, or both given) that
+    keeps only 8-bit checkpoints of q, key and val for its backward pass."""
+
+    @staticmethod
+    def forward(ctx, g, rel, q, key, val, bias, scale):
+        q, key, val = q.contiguous(), key.contiguous(), val.contiguous()
+        if rel is None:
+            out, _ = transformer_forward(g, q, key, val, scale)
+        else:
+            bias = bias.contiguous()
+            out, _ = transformer_rel_forward(g, rel, q, key, val, bias, scale)
+        packed = pack8(q, key, val)
+        ctx.g, ctx.rel, ctx.scale = g, rel, scale
+        ctx.save_for_backward(*(t for p in packed for t in p), bias)
+        return out
+
+    @staticmethod
+    def backward(ctx, dout):
+        *flat, bias = ctx.saved_tensors
+        c = [Packed8(*flat[k:k + 2]) for k in (0, 2, 4)]
+        d = transformer_backward8(ctx.g, *c, dout.contiguous(), ctx.scale, ctx.rel, bias)
+        return None, None, *d[:3], None if ctx.rel is None else d[3].to(bias.dtype), None
 
 
 _NORM_PARAMS = ("w_post", "b_post", "scale", "w_pre", "b_pre")

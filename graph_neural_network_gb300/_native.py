@@ -68,6 +68,11 @@ SIGNATURES = [
                                        _SZ, _P]),
     ("transformer_rel_backward", _I32, [_P, _P, _I32, _I32, _I32, _P, _P, _P, _F, _P, _P, _P, _P,
                                         _P, _P, _P, _P, _SZ, _P]),
+    ("gnn_pack8", _I32, [_I32, _I64, _I32, _I32, _I32, _P, _P, _P, _P]),
+    ("gnn_unpack8", _I32, [_I64, _I32, _I32, _I32, _P, _P, _P]),
+    ("transformer_packed8_workspace_bytes", _SZ, [_P, _P, _I32, _I32, _I32]),
+    ("transformer_packed8_backward", _I32, [_P, _P, _I32, _I32, _I32, _P, _P, _P, _F, _P, _P, _P,
+                                            _P, _P, _P, _P, _SZ, _P]),
     ("gnn_norm_residual_forward", _I32, [_P, _I32, _P, _P, _P, _P, _P, _P]),
     ("gnn_norm_residual_workspace_bytes", _SZ, [_P, _I32]),
     ("gnn_norm_residual_backward", _I32, [_P, _I32, _P, _P, _P, _P, _P, _P, _P, _SZ, _P]),
@@ -85,6 +90,10 @@ SIGNATURES = [
 class Tiling(ctypes.Structure):
     _fields_ = [("light_max_deg", ctypes.c_int32), ("cta_max_deg", ctypes.c_int32),
                 ("hub_chunk", ctypes.c_int32)]
+
+
+class Packed8(ctypes.Structure):
+    _fields_ = [("values", _P), ("scale", _P)]
 
 
 class NormResidual(ctypes.Structure):  # gnn_norm_residual, its parameters in line

@@ -414,6 +414,22 @@ bool device_ok(const gnn_graph* g) {
   return cudaGetDevice(&dev) == cudaSuccess && dev == g->device;
 }
 
+bool current_sms(int* sms) {
+  int dev = 0;
+  return cudaGetDevice(&dev) == cudaSuccess &&
+         cudaDeviceGetAttribute(sms, cudaDevAttrMultiProcessorCount, dev) == cudaSuccess;
+}
+
+gnn_status pack8_shape(int64_t n, int H, int D, gnn_dtype dt, Shape* s) {
+  if (n < 0 || n >= (int64_t(1) << 31) || (dt != GNN_F32 && dt != GNN_BF16) || H < 1 || D < 1)
+    return GNN_ERR_INVALID_ARG;
+  return gnn::make_shape(H, D, dt, s) ? GNN_OK : GNN_ERR_UNSUPPORTED;
+}
+
+bool packed_ok(const gnn_packed8* p) {
+  return p && p->values && p->scale && aligned(p->values, 16) && aligned(p->scale, 4);
+}
+
 gnn_status norm_residual_check(const gnn_norm_residual* d, gnn_dtype dt) {
   if (!d || (dt != GNN_F32 && dt != GNN_BF16) || d->n < 0 || d->n >= (int64_t(1) << 31) ||
       d->F < 1)
@@ -666,10 +682,8 @@ gnn_status gnn_norm_residual_forward(const gnn_norm_residual* d, gnn_dtype dtype
   if (!x || !o || !y || !gate_ok(d, dtype, gate)) return GNN_ERR_INVALID_ARG;
   if (!aligned(x, 16) || !aligned(o, 16) || !aligned(y, 16) || !aligned(z, 16))
     return GNN_ERR_INVALID_ARG;
-  int dev = 0, sms = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess ||
-      cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
-    return GNN_ERR_CUDA;
+  int sms = 0;
+  if (!current_sms(&sms)) return GNN_ERR_CUDA;
   return from_cuda(gnn::launch_norm_residual_forward(*d, dtype, x, o, gate, y, z, sms,
                                                      static_cast<cudaStream_t>(stream)));
 }
@@ -705,6 +719,77 @@ gnn_status gnn_norm_residual_backward(const gnn_norm_residual* d, gnn_dtype dtyp
   return from_cuda(gnn::launch_norm_residual_backward(*d, dtype, y, o, gate, dy, dz, g,
                                                       static_cast<char*>(ws),
                                                       static_cast<cudaStream_t>(stream)));
+}
+
+gnn_status gnn_pack8(int count, int64_t n, int H, int D, gnn_dtype dtype, const void* const* x,
+                     int8_t* const* values, float* const* scale, void* stream) {
+  Shape s;
+  const gnn_status r = pack8_shape(n, H, D, dtype, &s);
+  if (r != GNN_OK) return r;
+  if (count < 1 || count > gnn::kPack8Max || !x || !values || !scale) return GNN_ERR_INVALID_ARG;
+  if (n == 0) return GNN_OK;
+  for (int k = 0; k < count; ++k)
+    if (!x[k] || !values[k] || !scale[k] || !aligned(x[k], 16) || !aligned(values[k], 16) ||
+        !aligned(scale[k], 4))
+      return GNN_ERR_INVALID_ARG;
+  int sms = 0;
+  if (!current_sms(&sms)) return GNN_ERR_CUDA;
+  return from_cuda(gnn::launch_pack8(count, n * s.rv, s.hv_log2, dtype, x, values, scale, sms,
+                                     static_cast<cudaStream_t>(stream)));
+}
+
+gnn_status gnn_unpack8(int64_t n, int H, int D, gnn_dtype dtype, const gnn_packed8* p, void* x,
+                       void* stream) {
+  // what either type packs reads back as either type
+  Shape s;
+  if (dtype != GNN_F32 && dtype != GNN_BF16) return GNN_ERR_INVALID_ARG;
+  gnn_status r = pack8_shape(n, H, D, GNN_F32, &s);
+  if (r == GNN_ERR_UNSUPPORTED) r = pack8_shape(n, H, D, GNN_BF16, &s);
+  if (r != GNN_OK) return r;
+  if (n == 0) return GNN_OK;
+  if (!packed_ok(p) || !x || !aligned(x, 16)) return GNN_ERR_INVALID_ARG;
+  int sms = 0;
+  if (!current_sms(&sms)) return GNN_ERR_CUDA;
+  return from_cuda(gnn::launch_unpack8(p->values, p->scale, n, H, D, dtype, x, sms,
+                                       static_cast<cudaStream_t>(stream)));
+}
+
+size_t transformer_packed8_workspace_bytes(const gnn_graph* g, const gnn_rel* rel, int H, int D,
+                                           gnn_dtype dtype) {
+  Shape s;
+  if ((rel ? rel_shape(g, rel, H, D, dtype, &s) : gatv2_shape(g, H, D, dtype, &s)) != GNN_OK)
+    return 0;
+  return gnn::transformer8_ws_bytes(g, s, rel ? rel->buckets : 0);
+}
+
+gnn_status transformer_packed8_backward(const gnn_graph* g, const gnn_rel* rel, int H, int D,
+                                        gnn_dtype dtype, const gnn_packed8* q,
+                                        const gnn_packed8* key, const gnn_packed8* val,
+                                        float scale, const float* bias, const void* dout,
+                                        void* dq, void* dkey, void* dval, float* dbias, void* ws,
+                                        size_t ws_bytes, void* stream) {
+  Shape s;
+  const gnn_status r =
+      rel ? rel_shape(g, rel, H, D, dtype, &s) : gatv2_shape(g, H, D, dtype, &s);
+  if (r != GNN_OK) return r;
+  if ((rel != nullptr) != (dbias != nullptr) || !aligned(dbias, 4)) return GNN_ERR_INVALID_ARG;
+  if (!device_ok(g)) return GNN_ERR_INVALID_ARG;
+  if (g->n == 0)
+    return rel ? from_cuda(cudaMemsetAsync(dbias, 0, size_t(rel->buckets) * H * sizeof(float),
+                                           static_cast<cudaStream_t>(stream)))
+               : GNN_OK;
+  if (!packed_ok(q) || !packed_ok(key) || !packed_ok(val) || !dout || !dq || !dkey || !dval ||
+      (rel != nullptr) != (bias != nullptr))
+    return GNN_ERR_INVALID_ARG;
+  if (!aligned(dout, 16) || !aligned(dq, 16) || !aligned(dkey, 16) || !aligned(dval, 16) ||
+      !aligned(bias, 4))
+    return GNN_ERR_INVALID_ARG;
+  if (ws_bytes < gnn::transformer8_ws_bytes(g, s, rel ? rel->buckets : 0))
+    return GNN_ERR_WORKSPACE_TOO_SMALL;
+  if (!ws || !aligned(ws, 256)) return GNN_ERR_INVALID_ARG;
+  return from_cuda(gnn::launch_transformer8_backward(
+      g, rel, s, dtype, *q, *key, *val, scale, bias, dout, dq, dkey, dval, dbias,
+      static_cast<char*>(ws), static_cast<cudaStream_t>(stream)));
 }
 
 size_t reduce_agg_workspace_bytes(const gnn_graph* g, int F, gnn_dtype dtype) {

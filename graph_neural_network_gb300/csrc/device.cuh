@@ -502,6 +502,18 @@ __device__ __forceinline__ void own_row(const void* x, int64_t node, const Shape
             r);
 }
 
+// The four signed bytes of w as floats, exactly: a byte with its sign bit
+// flipped, placed below the exponent of 2^23, is the float 2^23 + 128 + value.
+__device__ __forceinline__ void widen8(uint32_t w, float* x) {
+  w ^= 0x80808080u;
+  x[0] = __uint_as_float(__byte_perm(w, 0x4b000000u, 0x7440));
+  x[1] = __uint_as_float(__byte_perm(w, 0x4b000000u, 0x7441));
+  x[2] = __uint_as_float(__byte_perm(w, 0x4b000000u, 0x7442));
+  x[3] = __uint_as_float(__byte_perm(w, 0x4b000000u, 0x7443));
+  add2(x[0], x[1], x[0], x[1], -8388736.f, -8388736.f);
+  add2(x[2], x[3], x[2], x[3], -8388736.f, -8388736.f);
+}
+
 // ---- mbarrier + bulk copy (shared::cta) --------------------------------------
 
 __device__ __forceinline__ uint32_t smem_u32(const void* p) {

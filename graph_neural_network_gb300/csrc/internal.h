@@ -184,6 +184,25 @@ cudaError_t launch_transformer_rel_backward(const gnn_graph* g, const gnn_rel* r
                                             const void* dout, void* dq, void* dkey, void* dval,
                                             float* dbias, char* ws, cudaStream_t st);
 
+// dbias[x] = the sum of part[blocks][entries] over the blocks, in a fixed order.
+cudaError_t launch_dbias_sum(const double* part, int blocks, int entries, float* dbias,
+                             cudaStream_t st);
+
+// 8-bit activation checkpoints (pack8.cu) and the attention's backward pass
+// from them (transformer8.cu).  vecs: 16-byte vectors of a tensor, a head 2^hv_log2.
+constexpr int kPack8Max = 8;  // tensors of one call
+cudaError_t launch_pack8(int count, int64_t vecs, int hv_log2, gnn_dtype dt, const void* const* x,
+                         int8_t* const* x8, float* const* s, int sm_count, cudaStream_t st);
+cudaError_t launch_unpack8(const int8_t* x8, const float* s, int64_t n, int H, int D,
+                           gnn_dtype dt, void* x, int sm_count, cudaStream_t st);
+size_t transformer8_ws_bytes(const gnn_graph* g, const Shape& s, int buckets);
+cudaError_t launch_transformer8_backward(const gnn_graph* g, const gnn_rel* rel, const Shape& s,
+                                         gnn_dtype dt, const gnn_packed8& q,
+                                         const gnn_packed8& key, const gnn_packed8& val,
+                                         float scale, const float* bias, const void* dout,
+                                         void* dq, void* dkey, void* dval, float* dbias, char* ws,
+                                         cudaStream_t st);
+
 // Buckets of relative node positions (relpos.cu).
 void rel_log_bounds(int n, int max_distance, int32_t* bounds);
 cudaError_t launch_rel_buckets(const gnn_graph* g, const int32_t* pos, const int32_t* bounds,

@@ -1,0 +1,76 @@
+// The learned relative position bias inside an attention kernel: its table in
+// shared memory, the buckets of a batch of edges, and the bias gradient's tables.
+#pragma once
+
+#include "device.cuh"
+
+namespace gnn {
+
+// The bias table [buckets][H] in base-2 score units.  Ends with a barrier.
+__device__ __forceinline__ float* stage_bias(const float* bias, int entries, unsigned char* to) {
+  float* t = reinterpret_cast<float*>(to);
+  for (int x = threadIdx.x; x < entries; x += kThreads) t[x] = bias[x] * kLog2e;
+  __syncthreads();
+  return t;
+}
+
+// Buckets of the edges batch_ids() takes (0 past the end).
+template <int U>
+__device__ __forceinline__ void batch_buckets(const uint8_t* rb, int beg, int end, int g, int G,
+                                              int (&b)[U]) {
+#pragma unroll
+  for (int u = 0; u < U; ++u) {
+    const int e = beg + u * G + g;
+    b[u] = e < end ? int(__ldg(rb + e)) : 0;
+  }
+}
+
+// This lane's bias of each edge of the batch; edges that -infinity masks for
+// its head become absent.
+template <int U>
+__device__ __forceinline__ void edge_bias(const float* sb, const Shape& s, const Lane<1>& L,
+                                          const int (&b)[U], int (&j)[U], float (&bs)[U]) {
+#pragma unroll
+  for (int u = 0; u < U; ++u) {
+    bs[u] = sb[b[u] * s.H + L.k[0]];
+    if (bs[u] == -INFINITY) j[u] = -1;
+  }
+}
+
+// Gradient tables: per warp [buckets][32 / hv] floats, the column a lane's head
+// group, so that the lanes leading a head add without atomics or conflicts.
+__host__ __device__ inline size_t grad_tables_bytes(const Shape& s, int buckets) {
+  return size_t(kWarps) * buckets * 4 << (5 - s.hv_log2);
+}
+
+// Clears the block's tables (a barrier must follow) and returns this lane's column.
+__device__ __forceinline__ float* clear_grad_tables(float* tables, const Shape& s,
+                                                    const Lane<1>& L, int buckets) {
+  const int cols_log2 = 5 - s.hv_log2;
+  for (int x = threadIdx.x; x < kWarps * buckets << cols_log2; x += kThreads) tables[x] = 0.f;
+  return tables + (((threadIdx.x >> 5) * buckets) << cols_log2) + (L.lane >> s.hv_log2);
+}
+
+__device__ __forceinline__ void add_grad(float* column, const Shape& s, int bucket, float de) {
+  column[bucket << (5 - s.hv_log2)] += de;
+}
+
+// This block's share [buckets][H] of the bias gradient, its tables added in
+// float64 in a fixed order.  Called by every thread of the block.
+__device__ __forceinline__ void fold_grad_tables(const float* tables, const Shape& s,
+                                                 const Lane<1>& L, int buckets, double* part) {
+  const int H = s.H;
+  const int cols_log2 = 5 - s.hv_log2;             // columns of a table
+  const int heads_log2 = s.lpr_log2 - s.hv_log2;   // columns of a sub-group
+  __syncthreads();
+  for (int x = threadIdx.x; x < buckets * H; x += kThreads) {
+    const int b = x / H, k = x - b * H;
+    double sum = 0.0;
+    for (int w = 0; w < kWarps; ++w)
+      for (int g = 0; g < L.G; ++g)
+        sum += double(tables[((w * buckets + b) << cols_log2) + (g << heads_log2) + k]);
+    part[int64_t(blockIdx.x) * buckets * H + x] = sum;
+  }
+}
+
+}  // namespace gnn

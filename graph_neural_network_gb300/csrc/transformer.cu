@@ -35,7 +35,7 @@
 // dbias_sum adds the blocks.  These sums cross nodes, so with kRel pass 2 deals
 // its work to warps by index instead of by counter: the result then depends on
 // the grid alone, not on timing.
-#include "device.cuh"
+#include "relbias.cuh"
 
 namespace gnn {
 namespace {
@@ -88,36 +88,6 @@ struct GtArgs {
   int* ctr;
   int32_t* err;
 };
-
-// kRel: the bias table in base-2 score units.  Ends with a barrier.
-__device__ __forceinline__ float* stage_bias(const GtArgs& A, unsigned char* smem) {
-  float* t = reinterpret_cast<float*>(smem + A.rel_off);
-  for (int x = threadIdx.x; x < A.buckets * A.s.H; x += kThreads) t[x] = A.bias[x] * kLog2e;
-  __syncthreads();
-  return t;
-}
-
-// kRel: buckets of the edges batch_ids() takes (0 past the end).
-template <int U>
-__device__ __forceinline__ void batch_buckets(const uint8_t* rb, int beg, int end, int g, int G,
-                                              int (&b)[U]) {
-#pragma unroll
-  for (int u = 0; u < U; ++u) {
-    const int e = beg + u * G + g;
-    b[u] = e < end ? int(__ldg(rb + e)) : 0;
-  }
-}
-
-// kRel: this lane's bias of each edge of the batch; masked edges become absent.
-template <int U>
-__device__ __forceinline__ void edge_bias(const GtArgs& A, const Lane<1>& L, const float* sb,
-                                          const int (&b)[U], int (&j)[U], float (&bs)[U]) {
-#pragma unroll
-  for (int u = 0; u < U; ++u) {
-    bs[u] = sb[b[u] * A.s.H + L.k[0]];
-    if (bs[u] == -INFINITY) j[u] = -1;
-  }
-}
 
 template <typename T>
 __device__ __forceinline__ uint4 gather(const void* x, int node, const Shape& s,
@@ -175,7 +145,7 @@ __device__ __forceinline__ void fwd_edges(const GtArgs& A, const Lane<1>& L, con
 #pragma unroll
     for (int u = 0; u < U; ++u) j[u] = jn[u];
     float bs[U];
-    if (kRel) edge_bias<U>(A, L, sb, bn, j, bs);
+    if (kRel) edge_bias<U>(sb, A.s, L, bn, j, bs);
     uint4 rk[U], rv[U];
 #pragma unroll
     for (int u = 0; u < U; ++u) {
@@ -251,7 +221,7 @@ __global__ void __launch_bounds__(kThreads, 3) gt_fwd_main(const GtArgs A) {
   const int H = A.s.H;
   extern __shared__ __align__(16) unsigned char smem[];
   __shared__ int s_item;
-  const float* sb = kRel ? stage_bias(A, smem) : nullptr;
+  const float* sb = kRel ? stage_bias(A.bias, A.buckets * A.s.H, smem + A.rel_off) : nullptr;
   float qs[V];
 
   if (D.n_items > 0) {
@@ -419,7 +389,7 @@ __device__ __forceinline__ void dst_edges(const GtArgs& A, const Lane<1>& L, con
 #pragma unroll
     for (int u = 0; u < U; ++u) j[u] = jn[u];
     float bs[U];
-    if (kRel) edge_bias<U>(A, L, sb, bn, j, bs);
+    if (kRel) edge_bias<U>(sb, A.s, L, bn, j, bs);
     uint4 rk[U], rv[U];
 #pragma unroll
     for (int u = 0; u < U; ++u) {
@@ -478,7 +448,7 @@ __global__ void __launch_bounds__(kThreads, 3) gt_dst_main(const GtArgs A) {
   const int H = A.s.H;
   extern __shared__ __align__(16) unsigned char smem[];
   __shared__ int s_item;
-  const float* sb = kRel ? stage_bias(A, smem) : nullptr;
+  const float* sb = kRel ? stage_bias(A.bias, A.buckets * A.s.H, smem + A.rel_off) : nullptr;
   float qs[V], gi[V];
 
   if (D.n_items > 0) {
@@ -679,7 +649,7 @@ __device__ __forceinline__ void src_edges(const GtArgs& A, const Lane<1>& L, con
     if (kRel) {
 #pragma unroll
       for (int u = 0; u < U; ++u) b[u] = bn[u];
-      edge_bias<U>(A, L, sb, bn, i, bs);
+      edge_bias<U>(sb, A.s, L, bn, i, bs);
     }
     uint4 rq[U], rg[U];
     float2 st[U];
@@ -709,7 +679,7 @@ __device__ __forceinline__ void src_edges(const GtArgs& A, const Lane<1>& L, con
       if (kRel) red[u] += bs[u];
       const float al = i[u] >= 0 ? ex2(red[u] - st[u].x) : 0.f;
       float de = kRel && i[u] < 0 ? 0.f : al * (red[U + u] - st[u].y);
-      if (kRel && i[u] >= 0 && L.head_leader(A.s, 0)) hist[b[u] << (5 - A.s.hv_log2)] += de;
+      if (kRel && i[u] >= 0 && L.head_leader(A.s, 0)) add_grad(hist, A.s, b[u], de);
       de *= A.scale;
       float x[V], y[V];
       unpack_alt<T>(rq[u], x);
@@ -730,25 +700,7 @@ __device__ __forceinline__ void src_write(const GtArgs& A, const Lane<1>& L, int
   st16(reinterpret_cast<char*>(A.dval) + off, pack<T>(dv));
 }
 
-// kRel: this block's share of the bias gradient, its warps' tables added in
-// float64 in a fixed order.  Called by every thread of the block.
-__device__ __forceinline__ void dbias_block(const GtArgs& A, const Lane<1>& L,
-                                            const float* tables) {
-  const int H = A.s.H;
-  const int cols_log2 = 5 - A.s.hv_log2;                      // columns of a table
-  const int heads_log2 = A.s.lpr_log2 - A.s.hv_log2;          // columns of a sub-group
-  __syncthreads();
-  for (int x = threadIdx.x; x < A.buckets * H; x += kThreads) {
-    const int b = x / H, k = x - b * H;
-    double sum = 0.0;
-    for (int w = 0; w < kWarps; ++w)
-      for (int g = 0; g < L.G; ++g)
-        sum += double(tables[((w * A.buckets + b) << cols_log2) + (g << heads_log2) + k]);
-    A.db_part[int64_t(blockIdx.x) * A.buckets * H + x] = sum;
-  }
-}
-
-// kRel: dbias[x] = sum over the blocks of pass 2, one warp per entry.
+// dbias[x] = sum over the blocks of pass 2, one warp per entry.
 __global__ void __launch_bounds__(kThreads) dbias_sum(const double* part, int blocks, int entries,
                                                       float* dbias) {
   const int x = blockIdx.x * kWarps + (threadIdx.x >> 5);
@@ -771,17 +723,13 @@ __global__ void __launch_bounds__(kThreads, 3) gt_src_main(const GtArgs A) {
   extern __shared__ __align__(16) unsigned char smem[];
   __shared__ int s_item;
   float ks[V], vj[V], dk[V], dv[V];
-  // kRel: the bias table, then per warp a gradient table [buckets][32 / hv]
-  // whose column is the lane's head group
   const float* sb = nullptr;
-  float* tables = nullptr;
+  float* tables = nullptr;   // kRel: the bias table, then the gradient tables
   float* hist = nullptr;
-  const int cols_log2 = 5 - A.s.hv_log2;
   if (kRel) {
     tables = reinterpret_cast<float*>(smem + A.rel_off) + A.buckets * A.s.H;
-    for (int x = threadIdx.x; x < kWarps * A.buckets << cols_log2; x += kThreads) tables[x] = 0.f;
-    sb = stage_bias(A, smem);
-    hist = tables + ((wid * A.buckets) << cols_log2) + (L.lane >> A.s.hv_log2);
+    hist = clear_grad_tables(tables, A.s, L, A.buckets);
+    sb = stage_bias(A.bias, A.buckets * A.s.H, smem + A.rel_off);
   }
 
   if (D.n_items > 0) {
@@ -889,7 +837,7 @@ __global__ void __launch_bounds__(kThreads, 3) gt_src_main(const GtArgs A) {
         if (j >= 0) src_write<T>(A, L, j, dk, dv);
       }
     }
-    if (kRel) dbias_block(A, L, tables);
+    if (kRel) fold_grad_tables(tables, A.s, L, A.buckets, A.db_part);
     return;
   }
 
@@ -938,7 +886,7 @@ __global__ void __launch_bounds__(kThreads, 3) gt_src_main(const GtArgs A) {
       for (int u = 0; u < kU; ++u) in[u] = in2[u];
     }
   }
-  if (kRel) dbias_block(A, L, tables);
+  if (kRel) fold_grad_tables(tables, A.s, L, A.buckets, A.db_part);
 }
 
 template <typename T>
@@ -1031,7 +979,7 @@ cudaError_t bwd_t(GtArgs A, float* dbias, int sm_count, cudaStream_t st) {
   }
   size_t smem2 = size_t(A.csc.col_off) + size_t(kWarps) * 2 * row_f * 4;
   A.rel_off = int(smem2);
-  if (kRel) smem2 += table + (size_t(kWarps) * A.buckets * 4 << (5 - A.s.hv_log2));
+  if (kRel) smem2 += table + grad_tables_bytes(A.s, A.buckets);
   int blocks = 0;
   if ((e = persistent_launch<T>(
            A.s.lpr < 32 ? gt_src_main<T, true, kRel> : gt_src_main<T, false, kRel>, A, A.csc,
@@ -1041,13 +989,7 @@ cudaError_t bwd_t(GtArgs A, float* dbias, int sm_count, cudaStream_t st) {
     gt_src_merge<T><<<unsigned((A.csc.n_hubs + kWarps - 1) / kWarps), kThreads, 0, st>>>(A);
     if ((e = cudaGetLastError()) != cudaSuccess) return e;
   }
-  if (kRel) {
-    const int entries = A.buckets * A.s.H;
-    dbias_sum<<<unsigned((entries + kWarps - 1) / kWarps), kThreads, 0, st>>>(A.db_part, blocks,
-                                                                             entries, dbias);
-    if ((e = cudaGetLastError()) != cudaSuccess) return e;
-  }
-  return cudaSuccess;
+  return kRel ? launch_dbias_sum(A.db_part, blocks, A.buckets * A.s.H, dbias, st) : cudaSuccess;
 }
 
 GtDir gt_dir(const Dir& d) {
@@ -1123,6 +1065,13 @@ GtArgs gt_args(const gnn_graph* g, const Shape& s, const void* q, const void* ke
 }
 
 }  // namespace
+
+cudaError_t launch_dbias_sum(const double* part, int blocks, int entries, float* dbias,
+                             cudaStream_t st) {
+  dbias_sum<<<unsigned((entries + kWarps - 1) / kWarps), kThreads, 0, st>>>(part, blocks, entries,
+                                                                           dbias);
+  return cudaGetLastError();
+}
 
 size_t transformer_ws_bytes(const gnn_graph* g, const Shape& s, int buckets) {
   return gt_layout(g, s, buckets).total;

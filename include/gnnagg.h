@@ -412,6 +412,48 @@ gnn_status transformer_rel_backward(const gnn_graph* g, const gnn_rel* rel, int 
                                     void* dval, float* dbias, void* ws, size_t ws_bytes,
                                     void* stream);
 
+/* ---- 8-bit activation checkpoints -------------------------------------------
+ *
+ * What a backward pass needs of an activation, in a byte per element: each head
+ * vector x[n][k] becomes integers and one float scale,
+ *     scale = max(max |x| / 127, 2^-126),  values = x / scale rounded to the
+ *     nearest integer (ties to even; the exact quotient decides),
+ * standing for values * scale, at most half a scale from x.  A head vector with
+ * an infinity or NaN gets scale NaN and values 0, so it reads back as NaN.
+ * values: int8 [n][H][D], 16-byte aligned; scale: float [n][H].  Shapes: D *
+ * sizeof(dtype) a multiple of 16 bytes and a power of two of them up to 32, H *
+ * D * sizeof(dtype) <= 2048 bytes.  Asynchronous on `stream`. */
+typedef struct {
+  const int8_t* values;
+  const float* scale;
+} gnn_packed8;
+
+/* Packs `count` (1 to 8) tensors x[t] of the same shape and dtype in one
+ * launch; the arrays of pointers are host memory, read during the call. */
+gnn_status gnn_pack8(int count, int64_t n, int H, int D, gnn_dtype dtype, const void* const* x,
+                     int8_t* const* values, float* const* scale, void* stream);
+
+/* x = values * scale, rounded to dtype (either, whichever was packed). */
+gnn_status gnn_unpack8(int64_t n, int H, int D, gnn_dtype dtype, const gnn_packed8* p, void* x,
+                       void* stream);
+
+/* Backward pass of the graph-transformer attention from the checkpoints of q,
+ * key and val: the exact gradient at the values that they stand for.  The
+ * softmax is computed anew there (the forward call's lse belongs to the
+ * unrounded activations), so the forward's q, key, val and lse need not be
+ * kept.  rel null: no bias (bias and dbias null); otherwise as for
+ * transformer_rel_backward.  dout, dq, dkey, dval: dtype [n][H][D].  Shapes and
+ * errors as for transformer_agg_backward.  Bitwise reproducible. */
+size_t transformer_packed8_workspace_bytes(const gnn_graph* g, const gnn_rel* rel, int H, int D,
+                                           gnn_dtype dtype);
+
+gnn_status transformer_packed8_backward(const gnn_graph* g, const gnn_rel* rel, int H, int D,
+                                        gnn_dtype dtype, const gnn_packed8* q,
+                                        const gnn_packed8* key, const gnn_packed8* val,
+                                        float scale, const float* bias, const void* dout,
+                                        void* dq, void* dkey, void* dval, float* dbias, void* ws,
+                                        size_t ws_bytes, void* stream);
+
 /* ---- Norms before and after a block, gate and residual scale ----------------
  *
  * The per-node half of a transformer layer, between one block (an aggregation

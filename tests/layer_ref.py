@@ -16,6 +16,11 @@ those with weights) add their own relative error to sums of magnitudes.  Every
 attention bound is therefore C * mag with mag the sum of the terms' magnitudes,
 |da| taken as sum_c |dout_c val_c| and |Delta| as its weighted mean, and
     C = 3 |w| + (deg + 2 D + 16) u.
+The hardware's exponential flushes results below 2^-126 to zero: a weight may
+also be off by 2^-126 itself, whatever it multiplies.  A sum of terms alpha t is
+then off by another 2^-126 sum |t|; in de = alpha (da - Delta) the factor is |da|
++ |Delta|, and Delta, a sum over the row, is off by 2^-126 sum |da| at alpha <= 1.
+*_one holds these sums, counted twice (2^-125) for products of two such errors.
 """
 from __future__ import annotations
 
@@ -40,11 +45,11 @@ def attention(rp, ci, q, k, v, scale, bias=None, bucket=None, dout=None):
     t = lambda a: torch.from_numpy(np.asarray(a, np.float64))  # noqa: E731
     q, k, v = t(q), t(k), t(v)
     g = None if dout is None else t(dout)
-    r = {x: [] for x in ("out", "lse", "out_mag")}
+    r = {x: [] for x in ("out", "lse", "out_mag", "out_one")}
     if g is not None:
-        r.update({x: [] for x in ("dq", "dkey", "dval", "dq_mag", "dkey_mag", "dval_mag")})
+        r.update({x + y: [] for x in ("dq", "dkey", "dval") for y in ("", "_mag", "_one")})
         if bias is not None:
-            r.update(dbias=[], dbias_mag=[])
+            r.update(dbias=[], dbias_mag=[], dbias_one=[])
     S, lse_top = 0.0, 0.0
     for h in range(H):
         i, j, b = dst, src, None
@@ -69,6 +74,7 @@ def attention(rp, ci, q, k, v, scale, bias=None, bucket=None, dout=None):
                                          dtype=torch.float64).index_add(0, idx, x)
         r["out"].append(add(i, a[:, None] * vh[j]))
         r["out_mag"].append(add(i, a[:, None] * vh[j].abs()))
+        r["out_one"].append(add(i, vh[j].abs()))
         r["lse"].append(lse)
         if len(e):
             S = max(S, float(mag_e.max()))
@@ -79,7 +85,11 @@ def attention(rp, ci, q, k, v, scale, bias=None, bucket=None, dout=None):
         da, da_m = (gi * vh[j]).sum(-1), (gi * vh[j]).abs().sum(-1)
         delta, delta_m = add(i, a * da), add(i, a * da_m)
         de, de_m = a * (da - delta[i]), a * (da_m + delta_m[i])
+        de_1 = da_m + delta_m[i] + add(i, da_m)[i]
         sc = abs(scale)
+        r["dq_one"].append(sc * add(i, de_1[:, None] * kh[j].abs()))
+        r["dkey_one"].append(sc * add(j, de_1[:, None] * qh[i].abs()))
+        r["dval_one"].append(add(j, gi.abs()))
         r["dq"].append(scale * add(i, de[:, None] * kh[j]))
         r["dq_mag"].append(sc * add(i, de_m[:, None] * kh[j].abs()))
         r["dkey"].append(scale * add(j, de[:, None] * qh[i]))
@@ -90,6 +100,7 @@ def attention(rp, ci, q, k, v, scale, bias=None, bucket=None, dout=None):
             nb = len(bh)
             r["dbias"].append(torch.zeros(nb, dtype=torch.float64).index_add(0, b, de))
             r["dbias_mag"].append(torch.zeros(nb, dtype=torch.float64).index_add(0, b, de_m))
+            r["dbias_one"].append(torch.zeros(nb, dtype=torch.float64).index_add(0, b, de_1))
     out = {x: torch.stack(y, 1).numpy() for x, y in r.items()}
     deg = max(int(np.diff(rp).max(initial=0)),
               int(np.bincount(np.asarray(ci, np.int64), minlength=1).max(initial=0)))
@@ -121,8 +132,8 @@ def hold_attention(got, ref, dtype, what, names):
             hold(got[x], ref[x], ref["lse_bound"], f"{what} lse")
             continue
         half = 0.0 if x == "dbias" else HALF[dtype]
-        hold(got[x], ref[x], ref["C"] * ref[x + "_mag"] + half * np.abs(ref[x]) + 1e-37,
-             f"{what} {x}")
+        hold(got[x], ref[x], ref["C"] * ref[x + "_mag"] + half * np.abs(ref[x]) +
+             2.0 ** -125 * ref[x + "_one"] + 1e-37, f"{what} {x}")
 
 
 def bucket_of(d, bounds, two_sided):
