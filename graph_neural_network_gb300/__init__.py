@@ -42,6 +42,10 @@ the norms, gate and residual scale between two blocks of a layer:
     y, z = norm_residual_forward(x, o, gate, w_post, scale=scale, w_pre=w_pre)
     grads = norm_residual_backward(y, o, dy, dz, gate, w_post, scale=scale, w_pre=w_pre)
 
+``transformer_layer`` runs a layer between its projections with autograd: the
+attention (bias and 8-bit checkpoints if asked for), the output projection that
+the caller gives, and the norms, gate and residual.
+
 and the max / min neighbourhood reduction with its winners:
 
     out, arg = reduce_forward(g, x, "max")         # arg [N, F] int32, -1 if no in-edges
@@ -65,7 +69,7 @@ __all__ = ["Graph", "gat_forward", "gat_backward", "GATAggregate", "GnnError", "
            "transformer_backward", "TransformerAggregate", "RelPos", "transformer_rel_forward",
            "transformer_rel_backward", "TransformerRelAggregate", "norm_residual_forward",
            "norm_residual_backward", "NormResidual", "Packed8", "pack8", "unpack8",
-           "transformer_backward8", "TransformerCheckpoint8"]
+           "transformer_backward8", "TransformerCheckpoint8", "transformer_layer"]
 
 
 def _ptr(t):
@@ -904,6 +908,31 @@ class NormResidual(torch.autograd.Function):
         return (g["dx"], g["do"], g["dgate"],
                 *(None if t is None else g["d" + k].to(t.dtype)
                   for k, t in zip(_NORM_PARAMS, params)), None, None)
+
+
+def transformer_layer(g: Graph, x: torch.Tensor, q: torch.Tensor, key: torch.Tensor,
+                      val: torch.Tensor, rel: RelPos | None = None, bias=None, gate=None,
+                      w_post=None, b_post=None, res_scale=None, w_pre=None, b_pre=None,
+                      project=None, scale: float | None = None, kind="rms", eps: float = 1e-6,
+                      checkpoint8: bool = False):
+    """One graph-transformer layer between its input projections and the next
+    layer's, with autograd: attention of q, key, val [N,H,D] over g (with rel and
+    bias, if given), `project` (the output projection, a function of the
+    attention's [N,H,D] returning x's shape; None where H*D is x's width), then
+    norm, gate, residual scale and sum with x, and the norm before the next
+    layer.  Returns (y, z) as norm_residual_forward does.  checkpoint8: the
+    attention keeps 8-bit checkpoints of q, key and val for its backward pass
+    instead of the tensors."""
+    if (rel is None) != (bias is None):
+        raise ValueError("rel and bias go together")
+    if checkpoint8:
+        out = TransformerCheckpoint8.apply(g, rel, q, key, val, bias, scale)
+    elif rel is not None:
+        out = TransformerRelAggregate.apply(g, rel, q, key, val, bias, scale)
+    else:
+        out = TransformerAggregate.apply(g, q, key, val, scale)
+    o = out.reshape(x.shape) if project is None else project(out)
+    return NormResidual.apply(x, o, gate, w_post, b_post, res_scale, w_pre, b_pre, kind, eps)
 
 
 def _reduce_ws(g, F, dt, ws, device):
