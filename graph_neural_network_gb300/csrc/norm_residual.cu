@@ -12,7 +12,11 @@
 //   u = dx scale sigmoid(g):  dgate = u n (1 - sigmoid(g)),
 //   do = rstd_o (u w_post - [mean(u w_post)] - o^ mean(u w_post o^))
 //   dw_post = sum u o^, db_post = sum u, dscale = sum dx sigmoid(g) n,
-//   dw_pre = sum dz y^, db_pre = sum dz  over the rows
+//   dw_pre = sum dz y^, db_pre = sum dz  over the rows.
+// A channel's parameters leave the sums over rows: with a = sum dx sigmoid(g) o^ and
+// b = sum dx sigmoid(g), dw_post = scale a, db_post = scale b and dscale = w_post a +
+// b_post b.  So the kernels carry four sums per channel, and the rows need only
+// scale w_post, scale b_post and w_pre
 // (the bracketed terms for layer only).  Means, variances and all sums are
 // float32 (parameter sums: float32 per thread over its own rows, float64 over
 // threads and blocks); a layer variance is the mean of squared differences from
@@ -44,16 +48,12 @@ struct NrArgs {
   const void *x, *o, *gate, *dy, *dz;   // x holds y in the backward pass
   gnn_norm_params p;
   void *y, *z, *dx, *dout, *dgate;
-  double* part;       // [blocks][5][F]
+  double* part;       // [blocks][kSums][F]
   int blocks;
 };
 
-enum { kDwPost, kDbPost, kDscale, kDwPre, kDbPre, kParams };
-
-template <typename T>
-__device__ __forceinline__ float load1(const void* p, int64_t at) {
-  return float(reinterpret_cast<const T*>(p)[at]);
-}
+// Sums over the rows, per channel: a and b above, dw_pre, db_pre.
+enum { kSumA, kSumB, kSumW, kSumC, kSums };
 
 __device__ __forceinline__ float sigmoid(float g) {
   // 1 / (1 + 2^(-g log2 e)); the exponential overflows to infinity and the
@@ -103,35 +103,43 @@ struct Place {
   }
 };
 
-template <typename T>
-__device__ __forceinline__ void load_vec(const void* p, int64_t at, bool ok,
-                                         float (&x)[VecOf<T>::n]) {
-  unpack<T>(ok ? ld16(reinterpret_cast<const char*>(p) + 16 * at) : make_uint4(0, 0, 0, 0), x);
+__device__ __forceinline__ uint4 load_raw(const void* p, int64_t at, bool ok) {
+  return ok ? ld16(reinterpret_cast<const char*>(p) + 16 * at) : make_uint4(0, 0, 0, 0);
 }
 
-template <typename T>
-__device__ __forceinline__ void load_param(const float* p, const Place& P, float none,
-                                           float (&w)[VecOf<T>::n]) {
-  constexpr int V = VecOf<T>::n;
+// w[c] = a[c] * b[c] of the thread's channels; a null factor counts as `none`.
+template <int V>
+__device__ __forceinline__ void load_product(const float* a, float none_a, const float* b,
+                                             const Place& P, float (&w)[V]) {
 #pragma unroll
-  for (int c = 0; c < V; ++c) w[c] = p && P.in ? __ldg(p + P.vec * V + c) : none;
+  for (int c = 0; c < V; ++c) {
+    const int f = P.vec * V + c;
+    w[c] = P.in ? (a ? __ldg(a + f) : none_a) * (b ? __ldg(b + f) : 1.f) : 0.f;
+  }
+}
+
+// The gate of a row as loaded: this thread's vector of it (width F) or the row's
+// value as a float's bits (width 1).
+template <typename T>
+__device__ __forceinline__ uint4 load_gate(const NrArgs& A, const Place& P, int64_t row, bool ok) {
+  if (A.gate_width == 1)
+    return make_uint4(ok ? __float_as_uint(float(reinterpret_cast<const T*>(A.gate)[row])) : 0u, 0,
+                      0, 0);
+  return load_raw(A.gate, row * A.rv + P.vec, ok && A.gate_width > 1);
 }
 
 template <typename T>
-__device__ __forceinline__ void load_gate(const NrArgs& A, const Place& P, int64_t row, bool ok,
+__device__ __forceinline__ void open_gate(const NrArgs& A, const uint4& raw,
                                           float (&s)[VecOf<T>::n]) {
   constexpr int V = VecOf<T>::n;
-  if (A.gate_width == 0) {
-#pragma unroll
-    for (int c = 0; c < V; ++c) s[c] = 1.f;
-  } else if (A.gate_width == 1) {
-    const float t = ok ? sigmoid(load1<T>(A.gate, row)) : 1.f;
-#pragma unroll
-    for (int c = 0; c < V; ++c) s[c] = t;
-  } else {
-    load_vec<T>(A.gate, row * A.rv + P.vec, ok, s);
+  if (A.gate_width > 1) {
+    unpack<T>(raw, s);
 #pragma unroll
     for (int c = 0; c < V; ++c) s[c] = sigmoid(s[c]);
+  } else {
+    const float t = A.gate_width == 1 ? sigmoid(__uint_as_float(raw.x)) : 1.f;
+#pragma unroll
+    for (int c = 0; c < V; ++c) s[c] = t;
   }
 }
 
@@ -163,37 +171,54 @@ __device__ __forceinline__ float norm_row(const NrArgs& A, const Place& P, int k
   return rstd;
 }
 
+// Blocks per SM the kernels are compiled for.  Each thread loads the next row's
+// vectors before it works on the present one's, so that loads are always in
+// flight; the registers of a bfloat16 vector (eight channels of parameters and,
+// backward, of sums) leave room for three blocks forward and two backward.
+template <typename T>
+struct NrBlocks {
+  static constexpr int fwd = sizeof(T) == 4 ? 4 : 3;
+  static constexpr int bwd = sizeof(T) == 4 ? 3 : 2;
+};
+
 template <typename T, int WPR>
-__global__ void __launch_bounds__(kThreads) nr_fwd(const NrArgs A) {
+__global__ void __launch_bounds__(kThreads, NrBlocks<T>::fwd) nr_fwd(const NrArgs A) {
   constexpr int V = VecOf<T>::n;
   __shared__ float buf[2 * kWarps * 4];
   int turn = 0;
   const Place P(A);
-  float wp[V], bp[V], sc[V], wn[V], bn[V];
-  load_param<T>(A.p.w_post, P, 1.f, wp);
-  load_param<T>(A.p.b_post, P, 0.f, bp);
-  load_param<T>(A.p.scale, P, 1.f, sc);
-  load_param<T>(A.p.w_pre, P, 1.f, wn);
-  load_param<T>(A.p.b_pre, P, 0.f, bn);
+  float wp[V], bp[V], wn[V], bn[V];
+  load_product<V>(A.p.w_post, 1.f, A.p.scale, P, wp);
+  load_product<V>(A.p.b_post, 0.f, A.p.scale, P, bp);
+  load_product<V>(A.p.w_pre, 1.f, nullptr, P, wn);
+  load_product<V>(A.p.b_pre, 0.f, nullptr, P, bn);
   // every thread of the block makes the same number of turns (barriers)
-  for (int64_t r0 = int64_t(blockIdx.x) * (kThreads >> A.tpr_log2); r0 < A.n; r0 += P.stride) {
-    const int64_t row = r0 + (threadIdx.x >> A.tpr_log2);
-    const bool ok = P.in && row < A.n;
-    const int64_t at = row * A.rv + P.vec;
+  int64_t r0 = int64_t(blockIdx.x) * (kThreads >> A.tpr_log2);
+  int64_t row = r0 + (threadIdx.x >> A.tpr_log2);
+  bool ok = P.in && row < A.n;
+  uint4 ro = load_raw(A.o, row * A.rv + P.vec, ok), rx = load_raw(A.x, row * A.rv + P.vec, ok);
+  uint4 rg = load_gate<T>(A, P, row, ok);
+  for (; r0 < A.n; r0 += P.stride) {
     float o[V], y[V], s[V];
-    load_vec<T>(A.o, at, ok, o);
-    load_vec<T>(A.x, at, ok, y);
-    load_gate<T>(A, P, row, ok, s);
+    unpack<T>(ro, o);
+    unpack<T>(rx, y);
+    open_gate<T>(A, rg, s);
+    const int64_t at = row * A.rv + P.vec;
+    const bool now = ok;
+    row += P.stride;
+    ok = P.in && row < A.n;
+    ro = load_raw(A.o, row * A.rv + P.vec, ok);
+    rx = load_raw(A.x, row * A.rv + P.vec, ok);
+    rg = load_gate<T>(A, P, row, ok);
     norm_row<T, WPR>(A, P, A.post, buf, turn, o);
 #pragma unroll
-    for (int c = 0; c < V; ++c) y[c] = fmaf(sc[c] * s[c], fmaf(o[c], wp[c], bp[c]), y[c]);
-    if (!ok) zero<V>(y);
-    if (ok) st16(reinterpret_cast<char*>(A.y) + 16 * at, pack<T>(y));
+    for (int c = 0; c < V; ++c) y[c] = fmaf(s[c], fmaf(o[c], wp[c], bp[c]), y[c]);
+    if (now) st16(reinterpret_cast<char*>(A.y) + 16 * at, pack<T>(y));
     if (A.pre != GNN_ROWNORM_NONE) {
       norm_row<T, WPR>(A, P, A.pre, buf, turn, y);
 #pragma unroll
       for (int c = 0; c < V; ++c) y[c] = fmaf(y[c], wn[c], bn[c]);
-      if (ok) st16(reinterpret_cast<char*>(A.z) + 16 * at, pack<T>(y));
+      if (now) st16(reinterpret_cast<char*>(A.z) + 16 * at, pack<T>(y));
     }
   }
 }
@@ -216,106 +241,128 @@ __device__ __forceinline__ void norm_grad(const NrArgs& A, const Place& P, int k
 }
 
 template <typename T, int WPR>
-__global__ void __launch_bounds__(kThreads) nr_bwd(const NrArgs A) {
+__global__ void __launch_bounds__(kThreads, NrBlocks<T>::bwd) nr_bwd(const NrArgs A) {
   constexpr int V = VecOf<T>::n;
   __shared__ float buf[2 * kWarps * 4];
-  extern __shared__ float sums[];  // [groups of the block][F], one parameter at a time
+  extern __shared__ float sums[];  // [row slots of the block][F], one sum at a time
   int turn = 0;
   const Place P(A);
-  float wp[V], bp[V], sc[V], wn[V];
-  load_param<T>(A.p.w_post, P, 1.f, wp);
-  load_param<T>(A.p.b_post, P, 0.f, bp);
-  load_param<T>(A.p.scale, P, 1.f, sc);
-  load_param<T>(A.p.w_pre, P, 1.f, wn);
-  float acc[kParams][V];
+  const bool pre = A.pre != GNN_ROWNORM_NONE;
+  float wp[V], bp[V], wn[V];
+  load_product<V>(A.p.w_post, 1.f, A.p.scale, P, wp);
+  load_product<V>(A.p.b_post, 0.f, A.p.scale, P, bp);
+  load_product<V>(A.p.w_pre, 1.f, nullptr, P, wn);
+  float acc[kSums][V];
 #pragma unroll
-  for (int k = 0; k < kParams; ++k) zero<V>(acc[k]);
-  for (int64_t r0 = int64_t(blockIdx.x) * (kThreads >> A.tpr_log2); r0 < A.n; r0 += P.stride) {
-    const int64_t row = r0 + (threadIdx.x >> A.tpr_log2);
-    const bool ok = P.in && row < A.n;
+  for (int k = 0; k < kSums; ++k) zero<V>(acc[k]);
+  int64_t r0 = int64_t(blockIdx.x) * (kThreads >> A.tpr_log2);
+  int64_t row = r0 + (threadIdx.x >> A.tpr_log2);
+  uint4 ro, rd, rg, ry, rz;
+  bool ok;
+  const auto load = [&] {
+    ok = P.in && row < A.n;
     const int64_t at = row * A.rv + P.vec;
+    ry = load_raw(A.x, at, ok && pre);
+    rz = load_raw(A.dz, at, ok && pre);
+    rd = load_raw(A.dy, at, ok);
+    ro = load_raw(A.o, at, ok);
+    rg = load_gate<T>(A, P, row, ok);
+  };
+  load();
+  for (; r0 < A.n; r0 += P.stride) {
     float o[V], y[V], s[V], d[V], g[V];
-    load_vec<T>(A.o, at, ok, o);
-    load_vec<T>(A.dy, at, ok, d);
-    load_gate<T>(A, P, row, ok, s);
-    float none = 0.f;
-    if (A.pre != GNN_ROWNORM_NONE) {
-      load_vec<T>(A.x, at, ok, y);
-      load_vec<T>(A.dz, at, ok, g);
+    unpack<T>(ry, y);
+    unpack<T>(rz, g);
+    unpack<T>(rd, d);
+    unpack<T>(ro, o);
+    open_gate<T>(A, rg, s);
+    const int64_t this_row = row, at = row * A.rv + P.vec;
+    const bool now = ok;
+    row += P.stride;
+    load();
+    if (pre) {
       const float rstd = norm_row<T, WPR>(A, P, A.pre, buf, turn, y);
 #pragma unroll
       for (int c = 0; c < V; ++c) {
-        acc[kDwPre][c] = fmaf(g[c], y[c], acc[kDwPre][c]);
-        acc[kDbPre][c] += g[c];
+        acc[kSumW][c] = fmaf(g[c], y[c], acc[kSumW][c]);
+        acc[kSumC][c] += g[c];
         g[c] *= wn[c];
       }
+      float none = 0.f;
       norm_grad<T, WPR>(A, P, A.pre, rstd, y, buf, turn, g, none);
 #pragma unroll
       for (int c = 0; c < V; ++c) d[c] += g[c];
     }
-    if (!ok) zero<V>(d);
-    if (ok) st16(reinterpret_cast<char*>(A.dx) + 16 * at, pack<T>(d));
+    if (now) st16(reinterpret_cast<char*>(A.dx) + 16 * at, pack<T>(d));
     const float rstd = norm_row<T, WPR>(A, P, A.post, buf, turn, o);
-    float dg[V];
+    // d becomes dx sigmoid(g), s the gate's gradient; a thread without a vector
+    // or a row adds nothing to the sums
 #pragma unroll
     for (int c = 0; c < V; ++c) {
       const float n = fmaf(o[c], wp[c], bp[c]);
-      const float ds = d[c] * s[c];
-      const float u = ds * sc[c];
-      acc[kDscale][c] = fmaf(ds, n, acc[kDscale][c]);
-      acc[kDwPost][c] = fmaf(u, o[c], acc[kDwPost][c]);
-      acc[kDbPost][c] += u;
-      dg[c] = u * n * (1.f - s[c]);
-      g[c] = u * wp[c];
+      d[c] = now ? d[c] * s[c] : 0.f;
+      s[c] = d[c] * n * (1.f - s[c]);
+      acc[kSumA][c] = fmaf(d[c], o[c], acc[kSumA][c]);
+      acc[kSumB][c] += d[c];
+      g[c] = d[c] * wp[c];
     }
-    float all = total<V>(dg);
+    float all = total<V>(s);
     norm_grad<T, WPR>(A, P, A.post, rstd, o, buf, turn, g, all);
-    if (ok) {
+    if (now) {
       st16(reinterpret_cast<char*>(A.dout) + 16 * at, pack<T>(g));
       if (A.gate_width == 1) {
-        if (P.vec == 0) reinterpret_cast<T*>(A.dgate)[row] = T(all);
+        if (P.vec == 0) reinterpret_cast<T*>(A.dgate)[this_row] = T(all);
       } else if (A.gate_width > 1) {
-        st16(reinterpret_cast<char*>(A.dgate) + 16 * at, pack<T>(dg));
+        st16(reinterpret_cast<char*>(A.dgate) + 16 * at, pack<T>(s));
       }
     }
   }
-  // the block's parameter sums, its row slots added in order in float64
+  // the block's sums, its row slots added in order in float64
   const int slots = kThreads >> A.tpr_log2;
 #pragma unroll
-  for (int k = 0; k < kParams; ++k) {
+  for (int k = 0; k < kSums; ++k) {
     __syncthreads();
     if (P.in)
 #pragma unroll
-      for (int c = 0; c < V; ++c) sums[(threadIdx.x >> A.tpr_log2) * A.F + P.vec * V + c] = acc[k][c];
+      for (int c = 0; c < V; ++c)
+        sums[(threadIdx.x >> A.tpr_log2) * A.F + P.vec * V + c] = acc[k][c];
     __syncthreads();
     for (int f = threadIdx.x; f < A.F; f += kThreads) {
       double t = 0.0;
       for (int x = 0; x < slots; ++x) t += double(sums[x * A.F + f]);
-      A.part[(int64_t(blockIdx.x) * kParams + k) * A.F + f] = t;
+      A.part[(int64_t(blockIdx.x) * kSums + k) * A.F + f] = t;
     }
   }
 }
 
-// Parameter gradients: column f of parameter k summed over the blocks, 32
-// columns and 32 slices of blocks at a time, in a fixed order.
+// Parameter gradients from the blocks' sums: 32 channels a block, the four sums
+// of each in 32 slices of blocks, in a fixed order.
 __global__ void __launch_bounds__(1024) nr_sum(const double* part, int blocks, int F,
-                                               float* dw_post, float* db_post, float* dscale,
-                                               float* dw_pre, float* db_pre) {
-  __shared__ double t[32][33];
-  float* out[kParams] = {dw_post, db_post, dscale, dw_pre, db_pre};
-  const int col = blockIdx.x * 32 + (threadIdx.x & 31), slice = threadIdx.x >> 5;
-  const int cols = kParams * F;
-  double s = 0.0;
-  if (col < cols)
-    for (int b = slice; b < blocks; b += 32) s += part[int64_t(b) * cols + col];
-  t[slice][threadIdx.x & 31] = s;
+                                               const gnn_norm_params p, const gnn_norm_grads d) {
+  __shared__ double t[kSums][32][33];
+  const int lane = threadIdx.x & 31, slice = threadIdx.x >> 5;
+  const int f = blockIdx.x * 32 + lane;
+  double s[kSums] = {0.0, 0.0, 0.0, 0.0};
+  if (f < F)
+    for (int b = slice; b < blocks; b += 32)
+#pragma unroll
+      for (int k = 0; k < kSums; ++k) s[k] += part[(int64_t(b) * kSums + k) * F + f];
+#pragma unroll
+  for (int k = 0; k < kSums; ++k) t[k][slice][lane] = s[k];
   __syncthreads();
-  if (slice == 0 && col < cols) {
-    double a = 0.0;
-    for (int x = 0; x < 32; ++x) a += t[x][threadIdx.x];
-    float* o = out[col / F];
-    if (o) o[col % F] = float(a);
-  }
+  if (slice >= kSums) return;
+  double a = 0.0;
+  for (int x = 0; x < 32; ++x) a += t[slice][x][lane];
+  t[slice][0][lane] = a;
+  asm volatile("bar.sync 1, 128;" ::: "memory");  // the four warps that are left
+  if (slice != 0 || f >= F) return;
+  const double sc = p.scale ? p.scale[f] : 1.0, w = p.w_post ? p.w_post[f] : 1.0,
+               c = p.b_post ? p.b_post[f] : 0.0, va = t[kSumA][0][lane], vb = t[kSumB][0][lane];
+  if (d.dw_post) d.dw_post[f] = float(sc * va);
+  if (d.db_post) d.db_post[f] = float(sc * vb);
+  if (d.dscale) d.dscale[f] = float(w * va + c * vb);
+  if (d.dw_pre) d.dw_pre[f] = float(t[kSumW][0][lane]);
+  if (d.db_pre) d.db_pre[f] = float(t[kSumC][0][lane]);
 }
 
 int tpr_log2(int rv) {
@@ -324,13 +371,13 @@ int tpr_log2(int rv) {
   return l;
 }
 
-// Blocks of the backward pass: at most four on each of 152 SMs, at least 16
-// rows a slot before its sums are folded.
-constexpr int kBwdBlocks = 4 * 152;
-int bwd_blocks(int64_t n, int rv) {
+// Blocks of the backward pass: what fits on 152 SMs, at least 16 rows a slot
+// before its sums are folded.
+int bwd_blocks(int64_t n, int rv, gnn_dtype dt) {
+  const int cap = 152 * (dt == GNN_F32 ? NrBlocks<float>::bwd : NrBlocks<__nv_bfloat16>::bwd);
   const int64_t slots = kThreads >> tpr_log2(rv);
   const int64_t want = (n + slots * 16 - 1) / (slots * 16);
-  return want < 1 ? 1 : want < kBwdBlocks ? int(want) : kBwdBlocks;
+  return want < 1 ? 1 : want < cap ? int(want) : cap;
 }
 
 NrArgs nr_args(const gnn_norm_residual& d, gnn_dtype dt) {
@@ -367,8 +414,7 @@ cudaError_t bwd_t(const NrArgs& A, const gnn_norm_grads& d, cudaStream_t st) {
   kernel<<<unsigned(A.blocks), kThreads, smem, st>>>(A);
   cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return e;
-  nr_sum<<<unsigned((kParams * A.F + 31) / 32), 1024, 0, st>>>(
-      A.part, A.blocks, A.F, d.dw_post, d.db_post, d.dscale, d.dw_pre, d.db_pre);
+  nr_sum<<<unsigned((A.F + 31) / 32), 1024, 0, st>>>(A.part, A.blocks, A.F, A.p, d);
   return cudaGetLastError();
 }
 
@@ -376,7 +422,7 @@ cudaError_t bwd_t(const NrArgs& A, const gnn_norm_grads& d, cudaStream_t st) {
 
 size_t norm_residual_ws_bytes(int64_t n, int F, gnn_dtype dt) {
   const int rv = F * (dt == GNN_F32 ? 4 : 2) / 16;
-  return align_up(size_t(bwd_blocks(n, rv)) * kParams * F * 8, 256);
+  return align_up(size_t(bwd_blocks(n, rv, dt)) * kSums * F * 8, 256);
 }
 
 cudaError_t launch_norm_residual_forward(const gnn_norm_residual& d, gnn_dtype dt, const void* x,
@@ -405,7 +451,7 @@ cudaError_t launch_norm_residual_backward(const gnn_norm_residual& d, gnn_dtype 
   A.dout = grads.dout;
   A.dgate = grads.dgate;
   A.part = reinterpret_cast<double*>(ws);
-  A.blocks = bwd_blocks(d.n, A.rv);
+  A.blocks = bwd_blocks(d.n, A.rv, dt);
   return dt == GNN_F32 ? bwd_t<float>(A, grads, st) : bwd_t<__nv_bfloat16>(A, grads, st);
 }
 
