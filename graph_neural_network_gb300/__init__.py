@@ -53,8 +53,9 @@ and the max / min neighbourhood reduction with its winners:
 """
 from __future__ import annotations
 
-import contextlib
 import ctypes
+import functools
+import math
 from typing import NamedTuple
 
 import torch
@@ -479,19 +480,55 @@ class TransformerAggregate(torch.autograd.Function):
         return None, dq, dk, dv, None
 
 
-@contextlib.contextmanager
-def _launch_on(device, stream):
-    """The launch's device current and its stream torch's own, so that what the
-    call allocates belongs to the stream that uses it."""
-    if stream is None and torch.cuda.current_device() == device.index:
-        yield torch.cuda.current_stream(device).cuda_stream
-        return
-    with torch.cuda.device(device):
+def _on_stream(fn):
+    """Lets a call take stream=: it then runs with that stream as torch's own, so
+    that what it allocates belongs to the stream that uses it."""
+    @functools.wraps(fn)
+    def call(*args, stream=None, **kw):
         if stream is None:
-            yield torch.cuda.current_stream(device).cuda_stream
-        else:
-            with torch.cuda.stream(stream):
-                yield stream.cuda_stream
+            return fn(*args, **kw)
+        device = next((a.device for a in args if hasattr(a, "device")), stream.device)
+        if stream.device != device:
+            raise ValueError(f"stream is on {stream.device}, the arguments on {device}")
+        with torch.cuda.stream(stream):
+            return fn(*args, **kw)
+    return call
+
+
+def _launch(fn, what: str, device, *args):
+    """fn(*args, the device's current stream), with the device current."""
+    index = device.index
+    if torch.cuda.current_device() == index:
+        rc = fn(*args, torch._C._cuda_getCurrentRawStream(index))
+    else:
+        with torch.cuda.device(device):
+            rc = fn(*args, torch._C._cuda_getCurrentRawStream(index))
+    if rc != _native.OK:
+        raise GnnError(rc, what)
+
+
+def _at(t):
+    return None if t is None else t.data_ptr()
+
+
+def _plain_tensor(t, name, shape, dtype, device):
+    """Raise unless t is a contiguous tensor of that shape, dtype and device."""
+    if isinstance(t, torch.Tensor) and t.shape == shape and t.dtype == dtype and \
+            t.device == device and t.is_contiguous():
+        return t
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor, got {type(t).__name__}")
+    if t.shape != shape:
+        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    raise ValueError(f"{name} must be contiguous and on {device}")
+
+
+def _output(t, name, shape, dtype, device):
+    """A caller-supplied output (checked) or a new one."""
+    return torch.empty(shape, dtype=dtype, device=device) if t is None else \
+        _plain_tensor(t, name, shape, dtype, device)
 
 
 class RelPos:
@@ -506,8 +543,9 @@ class RelPos:
     128 buckets.  Prepare it once per position vector; pos is not kept.
     """
 
+    @_on_stream
     def __init__(self, g: Graph, pos: torch.Tensor, num_buckets: int = 32,
-                 max_distance: int = 128, bidirectional: bool = True, bounds=None, stream=None):
+                 max_distance: int = 128, bidirectional: bool = True, bounds=None):
         lib = _native.load()
         _check_tensor(g, pos, "pos", (g.n,), torch.int32)
         if bounds is None:
@@ -524,14 +562,17 @@ class RelPos:
         self.bidirectional = bool(bidirectional)
         handle = ctypes.c_void_p()
         n = lib.gnn_rel_buffer_bytes(g.handle)
-        with _launch_on(g.device, stream) as s:
-            self.buffer = torch.empty(n, dtype=torch.uint8, device=g.device)
-            rc = lib.gnn_rel_prepare(g.handle, _ptr(pos), table, len(table),
-                                     int(self.bidirectional), _ptr(self.buffer), n, s,
-                                     ctypes.byref(handle))
-        _native.check(rc, "gnn_rel_prepare")
+        self.buffer = torch.empty(n, dtype=torch.uint8, device=g.device)
+
+        def prepare(s):
+            return lib.gnn_rel_prepare(g.handle, _at(pos), table, len(table),
+                                       int(self.bidirectional), _at(self.buffer), n, s,
+                                       ctypes.byref(handle))
+
+        _launch(prepare, "gnn_rel_prepare", g.device)
         self.handle = handle
         self._lib = lib
+        self._ws = {}  # workspace bytes by (H, D, dtype)
         self.buckets = lib.gnn_rel_buckets(handle)
 
     def __del__(self):
@@ -548,69 +589,72 @@ class RelPos:
         return tuple(self.buffer[o:o + self.graph.e] for o in at)
 
 
-def _rel_inputs(g: Graph, rel: RelPos, bias, H: int):
+def _rel_bias(g: Graph, rel: RelPos, bias, H: int):
     if not isinstance(rel, RelPos):
         raise TypeError(f"rel must be a RelPos, got {type(rel).__name__}")
     if rel.graph is not g:
         raise ValueError("rel was prepared for another graph")
     _check_tensor(g, bias, "bias", (rel.buckets, H), floating=True)
-    return bias.to(torch.float32)
+    return bias if bias.dtype == torch.float32 else bias.to(torch.float32)
+
+
+def _rel_qkv(g: Graph, q, key, val):
+    _check_features(g, q, "q")
+    _plain_tensor(key, "key", q.shape, q.dtype, g.device)
+    _plain_tensor(val, "val", q.shape, q.dtype, g.device)
+    return q.shape
 
 
 def _rel_ws(g, rel, H, D, dtype, ws):
     if _check_ws(g, ws) is not None:
         return ws
-    n = g._lib.transformer_rel_workspace_bytes(g.handle, rel.handle, H, D, _dtype_code(dtype))
-    if n == 0:
-        raise GnnError(_native.ERR_UNSUPPORTED, f"(H={H}, D={D}, {dtype})")
+    n = rel._ws.get((H, D, dtype))
+    if n is None:
+        n = g._lib.transformer_rel_workspace_bytes(g.handle, rel.handle, H, D, _dtype_code(dtype))
+        if n == 0:
+            raise GnnError(_native.ERR_UNSUPPORTED, f"(H={H}, D={D}, {dtype})")
+        rel._ws[H, D, dtype] = n
     return torch.empty(n, dtype=torch.uint8, device=g.device)
 
 
+@_on_stream
 def transformer_rel_forward(g: Graph, rel: RelPos, q: torch.Tensor, key: torch.Tensor,
                             val: torch.Tensor, bias: torch.Tensor, scale: float | None = None,
-                            out=None, lse=None, ws=None, stream=None):
+                            out=None, lse=None, ws=None):
     """transformer_forward with bias [buckets, H] added to the scores by the
     bucket of each edge: out [N,H,D] (q's dtype) and lse [N,H] float32.  An
     entry of -inf masks its bucket."""
-    N, H, D = _gt_inputs(g, q, key, val)
-    scale = D ** -0.5 if scale is None else float(scale)
-    with _launch_on(g.device, stream) as s:
-        bias = _rel_inputs(g, rel, bias, H)
-        out = _given(g, out, "out", q.shape, q.dtype, lambda: torch.empty_like(q))
-        lse = _given(g, lse, "lse", (N, H), torch.float32,
-                     lambda: torch.empty((N, H), dtype=torch.float32, device=q.device))
-        ws = _rel_ws(g, rel, H, D, q.dtype, ws)
-        rc = g._lib.transformer_rel_forward(g.handle, rel.handle, H, D, _dtype_code(q.dtype),
-                                            _ptr(q), _ptr(key), _ptr(val), scale, _ptr(bias),
-                                            _ptr(out), _ptr(lse), _ptr(ws), ws.numel(), s)
-    _native.check(rc, "transformer_rel_forward")
+    N, H, D = _rel_qkv(g, q, key, val)
+    bias = _rel_bias(g, rel, bias, H)
+    out = _output(out, "out", q.shape, q.dtype, g.device)
+    lse = _output(lse, "lse", (N, H), torch.float32, g.device)
+    ws = _rel_ws(g, rel, H, D, q.dtype, ws)
+    _launch(g._lib.transformer_rel_forward, "transformer_rel_forward", g.device, g.handle,
+            rel.handle, H, D, _dtype_code(q.dtype), _at(q), _at(key), _at(val),
+            D ** -0.5 if scale is None else float(scale), _at(bias), _at(out), _at(lse), _at(ws),
+            ws.numel())
     return out, lse
 
 
+@_on_stream
 def transformer_rel_backward(g: Graph, rel: RelPos, q: torch.Tensor, key: torch.Tensor,
                              val: torch.Tensor, bias: torch.Tensor, lse: torch.Tensor,
                              dout: torch.Tensor, scale: float | None = None, dq=None, dkey=None,
-                             dval=None, dbias=None, ws=None, stream=None):
+                             dval=None, dbias=None, ws=None):
     """dq, dkey, dval [N,H,D] (q's dtype) and dbias [buckets,H] float32."""
-    N, H, D = _gt_inputs(g, q, key, val)
-    _check_features(g, dout, "dout")
-    if dout.shape != q.shape or dout.dtype != q.dtype:
-        raise ValueError("dout must match q")
-    scale = D ** -0.5 if scale is None else float(scale)
-    _check_tensor(g, lse, "lse", (N, H), torch.float32)
-    with _launch_on(g.device, stream) as s:
-        bias = _rel_inputs(g, rel, bias, H)
-        dq = _given(g, dq, "dq", q.shape, q.dtype, lambda: torch.empty_like(q))
-        dkey = _given(g, dkey, "dkey", q.shape, q.dtype, lambda: torch.empty_like(q))
-        dval = _given(g, dval, "dval", q.shape, q.dtype, lambda: torch.empty_like(q))
-        dbias = _given(g, dbias, "dbias", bias.shape, torch.float32,
-                       lambda: torch.empty_like(bias))
-        ws = _rel_ws(g, rel, H, D, q.dtype, ws)
-        rc = g._lib.transformer_rel_backward(g.handle, rel.handle, H, D, _dtype_code(q.dtype),
-                                             _ptr(q), _ptr(key), _ptr(val), scale, _ptr(bias),
-                                             _ptr(lse), _ptr(dout), _ptr(dq), _ptr(dkey),
-                                             _ptr(dval), _ptr(dbias), _ptr(ws), ws.numel(), s)
-    _native.check(rc, "transformer_rel_backward")
+    N, H, D = shape = _rel_qkv(g, q, key, val)
+    _plain_tensor(dout, "dout", shape, q.dtype, g.device)
+    _plain_tensor(lse, "lse", (N, H), torch.float32, g.device)
+    bias = _rel_bias(g, rel, bias, H)
+    dq = _output(dq, "dq", shape, q.dtype, g.device)
+    dkey = _output(dkey, "dkey", shape, q.dtype, g.device)
+    dval = _output(dval, "dval", shape, q.dtype, g.device)
+    dbias = _output(dbias, "dbias", bias.shape, torch.float32, g.device)
+    ws = _rel_ws(g, rel, H, D, q.dtype, ws)
+    _launch(g._lib.transformer_rel_backward, "transformer_rel_backward", g.device, g.handle,
+            rel.handle, H, D, _dtype_code(q.dtype), _at(q), _at(key), _at(val),
+            D ** -0.5 if scale is None else float(scale), _at(bias), _at(lse), _at(dout), _at(dq),
+            _at(dkey), _at(dval), _at(dbias), _at(ws), ws.numel())
     return dq, dkey, dval, dbias
 
 
@@ -640,8 +684,13 @@ class Packed8(NamedTuple):
     values: torch.Tensor
     scale: torch.Tensor
 
+    @property
+    def device(self):
+        return self.values.device
 
-def pack8(*xs: torch.Tensor, out=None, stream=None):
+
+@_on_stream
+def pack8(*xs: torch.Tensor, out=None):
     """8-bit checkpoints of up to 8 tensors [N, H, D] of one shape and dtype, in
     one launch: a Packed8 for each.  Every head vector has its own scale, the
     largest magnitude over 127; values are rounded to nearest, ties to even.
@@ -651,26 +700,24 @@ def pack8(*xs: torch.Tensor, out=None, stream=None):
     x = xs[0]
     if not isinstance(x, torch.Tensor) or x.dim() != 3 or not x.is_cuda:
         raise ValueError("pack8 takes CUDA tensors [N, H, D]")
+    shape, device = x.shape, x.device
     dt = _dtype_code(x.dtype)
-    for k, t in enumerate(xs):
-        _plain_tensor(t, f"tensor {k}", x.shape, x.dtype, x.device)
-    N, H, D = x.shape
-    with _launch_on(x.device, stream) as s:
-        if out is None:
-            out = tuple(Packed8(torch.empty(x.shape, dtype=torch.int8, device=x.device),
-                                torch.empty((N, H), dtype=torch.float32, device=x.device))
-                        for _ in xs)
-        else:
-            out = tuple(out)
-            if len(out) != len(xs):
-                raise ValueError("out must have a Packed8 for every tensor")
-            for p in out:
-                _packed(p, "out", x.shape, x.device)
-        rows = ctypes.c_void_p * len(xs)
-        rc = _native.load().gnn_pack8(len(xs), N, H, D, dt, rows(*(t.data_ptr() for t in xs)),
-                                      rows(*(p.values.data_ptr() for p in out)),
-                                      rows(*(p.scale.data_ptr() for p in out)), s)
-    _native.check(rc, "gnn_pack8")
+    for t in xs:
+        _plain_tensor(t, "every tensor", shape, x.dtype, device)
+    N, H, D = shape
+    if out is None:
+        out = tuple(Packed8(torch.empty(shape, dtype=torch.int8, device=device),
+                            torch.empty((N, H), dtype=torch.float32, device=device)) for _ in xs)
+    else:
+        out = tuple(out)
+        if len(out) != len(xs):
+            raise ValueError("out must have a Packed8 for every tensor")
+        for p in out:
+            _packed(p, "out", shape, device)
+    rows = _native.PTRS[len(xs)]
+    _launch(_native.load().gnn_pack8, "gnn_pack8", device, len(xs), N, H, D, dt,
+            rows(*[t.data_ptr() for t in xs]), rows(*[p.values.data_ptr() for p in out]),
+            rows(*[p.scale.data_ptr() for p in out]))
     return out
 
 
@@ -682,7 +729,8 @@ def _packed(p, name, shape, device) -> _native.Packed8:
     return _native.Packed8(p.values.data_ptr(), p.scale.data_ptr())
 
 
-def unpack8(p: Packed8, dtype: torch.dtype = torch.float32, out=None, stream=None):
+@_on_stream
+def unpack8(p: Packed8, dtype: torch.dtype = torch.float32, out=None):
     """values * scale, rounded to dtype (float32 or bfloat16)."""
     if not isinstance(p, Packed8) or not isinstance(p.values, torch.Tensor) or \
             p.values.dim() != 3 or not p.values.is_cuda:
@@ -690,49 +738,46 @@ def unpack8(p: Packed8, dtype: torch.dtype = torch.float32, out=None, stream=Non
     dt = _dtype_code(dtype)
     shape, device = p.values.shape, p.values.device
     c = _packed(p, "p", shape, device)
-    with _launch_on(device, stream) as s:
-        out = torch.empty(shape, dtype=dtype, device=device) if out is None else \
-            _plain_tensor(out, "out", shape, dtype, device)
-        rc = _native.load().gnn_unpack8(*shape, dt, ctypes.byref(c), _ptr(out), s)
-    _native.check(rc, "gnn_unpack8")
+    out = _output(out, "out", shape, dtype, device)
+    _launch(_native.load().gnn_unpack8, "gnn_unpack8", device, *shape, dt, ctypes.byref(c),
+            _at(out))
     return out
 
 
+@_on_stream
 def transformer_backward8(g: Graph, q: Packed8, key: Packed8, val: Packed8, dout: torch.Tensor,
                           scale: float | None = None, rel: RelPos | None = None, bias=None,
-                          dq=None, dkey=None, dval=None, dbias=None, ws=None, stream=None):
+                          dq=None, dkey=None, dval=None, dbias=None, ws=None):
     """The gradients of the graph-transformer attention from 8-bit checkpoints
     of q, key and val, taken at the values that these stand for (its softmax is
     computed there too; no lse is needed): dq, dkey, dval (dout's dtype) and,
     with rel and bias, dbias [buckets,H] float32."""
     _check_features(g, dout, "dout")
-    N, H, D = dout.shape
-    c = [_packed(p, name, dout.shape, g.device) for name, p in
-         (("q", q), ("key", key), ("val", val))]
+    shape, device, dtype = dout.shape, g.device, dout.dtype
+    N, H, D = shape
+    cq, ck, cv = (_packed(q, "q", shape, device), _packed(key, "key", shape, device),
+                  _packed(val, "val", shape, device))
     if (rel is None) != (bias is None):
         raise ValueError("rel and bias go together")
-    scale = D ** -0.5 if scale is None else float(scale)
-    dt = _dtype_code(dout.dtype)
-    with _launch_on(g.device, stream) as s:
-        if rel is not None:
-            bias = _rel_inputs(g, rel, bias, H)
-            dbias = _given(g, dbias, "dbias", bias.shape, torch.float32,
-                           lambda: torch.empty_like(bias))
-        elif dbias is not None:
-            raise ValueError("there is no dbias without a bias")
-        dq, dkey, dval = (_given(g, t, name, dout.shape, dout.dtype,
-                                 lambda: torch.empty_like(dout))
-                          for name, t in (("dq", dq), ("dkey", dkey), ("dval", dval)))
-        handle = None if rel is None else rel.handle
-        if _check_ws(g, ws) is None:
-            n = g._lib.transformer_packed8_workspace_bytes(g.handle, handle, H, D, dt)
-            if n == 0:
-                raise GnnError(_native.ERR_UNSUPPORTED, f"(H={H}, D={D}, {dout.dtype})")
-            ws = torch.empty(n, dtype=torch.uint8, device=g.device)
-        rc = g._lib.transformer_packed8_backward(
-            g.handle, handle, H, D, dt, *(ctypes.byref(x) for x in c), scale, _ptr(bias),
-            _ptr(dout), _ptr(dq), _ptr(dkey), _ptr(dval), _ptr(dbias), _ptr(ws), ws.numel(), s)
-    _native.check(rc, "transformer_packed8_backward")
+    if rel is not None:
+        bias = _rel_bias(g, rel, bias, H)
+        dbias = _output(dbias, "dbias", bias.shape, torch.float32, device)
+    elif dbias is not None:
+        raise ValueError("there is no dbias without a bias")
+    dq = _output(dq, "dq", shape, dtype, device)
+    dkey = _output(dkey, "dkey", shape, dtype, device)
+    dval = _output(dval, "dval", shape, dtype, device)
+    handle = None if rel is None else rel.handle
+    dt = _dtype_code(dtype)
+    if _check_ws(g, ws) is None:
+        n = g._lib.transformer_packed8_workspace_bytes(g.handle, handle, H, D, dt)
+        if n == 0:
+            raise GnnError(_native.ERR_UNSUPPORTED, f"(H={H}, D={D}, {dtype})")
+        ws = torch.empty(n, dtype=torch.uint8, device=device)
+    _launch(g._lib.transformer_packed8_backward, "transformer_packed8_backward", device, g.handle,
+            handle, H, D, dt, ctypes.byref(cq), ctypes.byref(ck), ctypes.byref(cv),
+            D ** -0.5 if scale is None else float(scale), _at(bias), _at(dout), _at(dq), _at(dkey),
+            _at(dval), _at(dbias), _at(ws), ws.numel())
     return (dq, dkey, dval) if rel is None else (dq, dkey, dval, dbias)
 
 
@@ -763,57 +808,45 @@ class TransformerCheckpoint8(torch.autograd.Function):
 
 
 _NORM_PARAMS = ("w_post", "b_post", "scale", "w_pre", "b_pre")
-
-
-def _plain_tensor(t, name, shape, dtype, device):
-    """Raise unless t is a contiguous tensor of that shape, dtype and device."""
-    if not isinstance(t, torch.Tensor):
-        raise TypeError(f"{name} must be a torch.Tensor, got {type(t).__name__}")
-    if tuple(t.shape) != tuple(shape):
-        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
-    if t.dtype != dtype:
-        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
-    if t.device != device or not t.is_contiguous():
-        raise ValueError(f"{name} must be contiguous and on {device}")
-    return t
+_NORM_GRADS = ("dx", "do", "dgate") + tuple("d" + k for k in _NORM_PARAMS)
 
 
 def _norm_desc(o, gate, params, kind, eps):
     """The call's gnn_norm_residual, the float32 parameters it points to (to be
-    kept until the launch) and the norm before the next block."""
+    kept until the launch) and whether there is a norm before the next block."""
     if not isinstance(o, torch.Tensor) or o.dim() < 2:
         raise ValueError("o must be a tensor [N, ...]")
-    _dtype_code(o.dtype)
+    shape, dtype, device = o.shape, o.dtype, o.device
+    _dtype_code(dtype)
     if not o.is_cuda or not o.is_contiguous():
         raise ValueError("o must be a contiguous CUDA tensor")
     post, pre = (kind, kind) if isinstance(kind, str) else kind
-    if post not in _native.ROWNORMS or pre not in _native.ROWNORMS:
+    post, pre = _native.ROWNORMS.get(post), _native.ROWNORMS.get(pre)
+    if post is None or pre is None:
         raise ValueError(f"kind must be one of {sorted(_native.ROWNORMS)}, or a pair of them "
                          "(after the block, before the next)")
-    n = o.shape[0]
-    F = 1
-    for d in o.shape[1:]:
-        F *= d
-    d = _native.NormResidual(n=n, F=F, post=_native.ROWNORMS[post], pre=_native.ROWNORMS[pre],
-                             eps=eps)
+    n = shape[0]
+    F = math.prod(shape[1:])
+    width = 0
     if gate is not None:
-        wide = isinstance(gate, torch.Tensor) and gate.shape == o.shape
-        _plain_tensor(gate, "gate", o.shape if wide else (n, 1), o.dtype, o.device)
-        d.gate_width = F if wide else 1
-    kept = {}
+        width = F if isinstance(gate, torch.Tensor) and gate.shape == shape else 1
+        _plain_tensor(gate, "gate", shape if width == F else (n, 1), dtype, device)
+    kept = []
     for k, t in zip(_NORM_PARAMS, params):
-        if t is None:
-            continue
-        if not isinstance(t, torch.Tensor) or not t.is_floating_point():
-            raise TypeError(f"{k} must be a floating-point tensor")
-        kept[k] = _plain_tensor(t.to(torch.float32), k, (F,), torch.float32, o.device)
-        setattr(d, k, t.data_ptr() if kept[k] is t else kept[k].data_ptr())
-    return d, kept, pre
+        if t is not None:
+            if not isinstance(t, torch.Tensor) or not t.is_floating_point():
+                raise TypeError(f"{k} must be a floating-point tensor")
+            if t.dtype != torch.float32:
+                t = t.to(torch.float32)
+            _plain_tensor(t, k, (F,), torch.float32, device)
+        kept.append(t)
+    return (_native.NormResidual(n, F, post, pre, width, eps, *map(_at, kept)), kept, pre != 0)
 
 
+@_on_stream
 def norm_residual_forward(x: torch.Tensor, o: torch.Tensor, gate=None, w_post=None, b_post=None,
                           scale=None, w_pre=None, b_pre=None, kind="rms", eps: float = 1e-6,
-                          y=None, z=None, stream=None):
+                          y=None, z=None):
     """y = x + scale * sigmoid(gate) * (norm(o) w_post + b_post) and
     z = norm(y) w_pre + b_pre, for x, o [N, ...] (a node's features flattened).
 
@@ -822,66 +855,58 @@ def norm_residual_forward(x: torch.Tensor, o: torch.Tensor, gate=None, w_post=No
     Parameters have one entry per feature; None leaves a factor or a sum out.
     z is None where the second norm is "none"."""
     d, kept, pre = _norm_desc(o, gate, (w_post, b_post, scale, w_pre, b_pre), kind, eps)
-    _plain_tensor(x, "x", o.shape, o.dtype, o.device)
-    with _launch_on(o.device, stream) as s:
-        y = torch.empty_like(o) if y is None else _plain_tensor(y, "y", o.shape, o.dtype, o.device)
-        if pre != "none":
-            z = torch.empty_like(o) if z is None else _plain_tensor(z, "z", o.shape, o.dtype,
-                                                                    o.device)
-        elif z is not None:
-            raise ValueError("there is no z without a norm before the next block")
-        rc = _native.load().gnn_norm_residual_forward(
-            ctypes.byref(d), _dtype_code(o.dtype), _ptr(x), _ptr(o), _ptr(gate), _ptr(y), _ptr(z),
-            s)
-    _native.check(rc, "gnn_norm_residual_forward")
+    like = (o.shape, o.dtype, o.device)
+    _plain_tensor(x, "x", *like)
+    if z is not None and not pre:
+        raise ValueError("there is no z without a norm before the next block")
+    y = _output(y, "y", *like)
+    if pre:
+        z = _output(z, "z", *like)
+    _launch(_native.load().gnn_norm_residual_forward, "gnn_norm_residual_forward", o.device,
+            ctypes.byref(d), _dtype_code(o.dtype), _at(x), _at(o), _at(gate), _at(y), _at(z))
     return y, z
 
 
+@_on_stream
 def norm_residual_backward(y, o: torch.Tensor, dy: torch.Tensor, dz=None, gate=None, w_post=None,
                            b_post=None, scale=None, w_pre=None, b_pre=None, kind="rms",
-                           eps: float = 1e-6, ws=None, stream=None, grads=None):
+                           eps: float = 1e-6, ws=None, grads=None):
     """The gradients of norm_residual_forward, as a dict: dx, do, dgate (o's
     dtype; dgate None without a gate) and dw_post, db_post, dscale, dw_pre,
     db_pre (float32; None where the parameter is).  y is the forward's y, dy the
     gradient that reaches it past the second norm and dz that of z; y and dz are
     None where that norm is "none".  grads: outputs to write, by those names."""
     d, kept, pre = _norm_desc(o, gate, (w_post, b_post, scale, w_pre, b_pre), kind, eps)
-    like = (o.shape, o.dtype, o.device)
+    device = o.device
+    like = (o.shape, o.dtype, device)
     _plain_tensor(dy, "dy", *like)
     for name, t in (("y", y), ("dz", dz)):
-        if pre != "none":
+        if pre:
             _plain_tensor(t, name, *like)
         elif t is not None:
             raise ValueError(f"there is no {name} without a norm before the next block")
-    given = dict(grads or {})
-    with _launch_on(o.device, stream) as s:
-        def out(name, like_):
-            t = given.pop(name, None)
-            if like_ is None:
-                if t is not None:
-                    raise ValueError(f"there is no {name} in this call")
-                return None
-            return torch.empty_like(like_) if t is None else _plain_tensor(
-                t, name, like_.shape, like_.dtype, o.device)
-
-        got = {"dx": out("dx", o), "do": out("do", o), "dgate": out("dgate", gate)}
-        for k in _NORM_PARAMS:
-            got["d" + k] = out("d" + k, kept.get(k))
-        if given:
-            raise ValueError(f"unknown gradients {sorted(given)}")
-        lib = _native.load()
-        dt = _dtype_code(o.dtype)
-        need = lib.gnn_norm_residual_workspace_bytes(ctypes.byref(d), dt)
-        if ws is None:
-            ws = torch.empty(need, dtype=torch.uint8, device=o.device)
-        elif not isinstance(ws, torch.Tensor) or ws.dtype != torch.uint8 or ws.dim() != 1 or \
-                ws.device != o.device or not ws.is_contiguous():
-            raise ValueError(f"ws must be a one-dimensional uint8 tensor on {o.device}")
-        gr = _native.NormGrads(*(None if t is None else t.data_ptr() for t in got.values()))
-        rc = lib.gnn_norm_residual_backward(
-            ctypes.byref(d), dt, _ptr(y), _ptr(o), _ptr(gate), _ptr(dy), _ptr(dz),
-            ctypes.byref(gr), _ptr(ws), ws.numel(), s)
-    _native.check(rc, "gnn_norm_residual_backward")
+    got = {}
+    for name, t in zip(_NORM_GRADS, (o, o, gate, *kept)):
+        given = None if grads is None else grads.get(name)
+        if t is not None:
+            got[name] = _output(given, name, t.shape, t.dtype, device)
+        elif given is None:
+            got[name] = None
+        else:
+            raise ValueError(f"there is no {name} in this call")
+    if grads is not None and not grads.keys() <= got.keys():
+        raise ValueError(f"unknown gradients {sorted(grads.keys() - got.keys())}")
+    lib = _native.load()
+    dt = _dtype_code(o.dtype)
+    if ws is None:
+        ws = torch.empty(lib.gnn_norm_residual_workspace_bytes(ctypes.byref(d), dt),
+                         dtype=torch.uint8, device=device)
+    elif not isinstance(ws, torch.Tensor) or ws.dtype != torch.uint8 or ws.dim() != 1 or \
+            ws.device != device or not ws.is_contiguous():
+        raise ValueError(f"ws must be a one-dimensional uint8 tensor on {device}")
+    c = _native.NormGrads(*map(_at, got.values()))
+    _launch(lib.gnn_norm_residual_backward, "gnn_norm_residual_backward", device, ctypes.byref(d),
+            dt, _at(y), _at(o), _at(gate), _at(dy), _at(dz), ctypes.byref(c), _at(ws), ws.numel())
     return got
 
 

@@ -92,6 +92,9 @@ class Tiling(ctypes.Structure):
                 ("hub_chunk", ctypes.c_int32)]
 
 
+PTRS = [_P * n for n in range(9)]  # arrays of pointers, by length
+
+
 class Packed8(ctypes.Structure):
     _fields_ = [("values", _P), ("scale", _P)]
 

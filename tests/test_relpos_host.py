@@ -73,13 +73,13 @@ def test_binding_checks_positions_and_rel(lib):
         with pytest.raises(err):
             gnn.RelPos(g, pos)
     with pytest.raises(TypeError):
-        gnn._rel_inputs(g, "rel", torch.zeros(32, 2), 2)
+        gnn._rel_bias(g, "rel", torch.zeros(32, 2), 2)
     rel = object.__new__(gnn.RelPos)
     rel.graph, rel.buckets = g, 32
     for bias, err in ((torch.zeros(32, 3), ValueError), (torch.zeros(31, 2), ValueError),
                       (torch.zeros(32, 2, dtype=torch.int32), TypeError),
                       (torch.zeros(32, 2), ValueError)):                  # a host tensor
         with pytest.raises(err):
-            gnn._rel_inputs(g, rel, bias, 2)
+            gnn._rel_bias(g, rel, bias, 2)
     with pytest.raises(ValueError):
-        gnn._rel_inputs(_FakeGraph(), rel, torch.zeros(32, 2), 2)         # another graph
+        gnn._rel_bias(_FakeGraph(), rel, torch.zeros(32, 2), 2)         # another graph
