@@ -57,8 +57,34 @@ enum { kSumA, kSumB, kSumW, kSumC, kSums };
 
 __device__ __forceinline__ float sigmoid(float g) {
   // 1 / (1 + 2^(-g log2 e)); the exponential overflows to infinity and the
-  // quotient to 0 where the sigmoid is below the smallest float
-  return __fdividef(1.f, 1.f + ex2(-g * kLog2e));
+  // reciprocal to 0 where the sigmoid is below the smallest float
+  float r;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.f + ex2(-kLog2e * g)));
+  return r;
+}
+
+// Element-wise arithmetic on a thread's vector, two floats an instruction.
+// d = a * b + c
+template <int V>
+__device__ __forceinline__ void vfma(float (&d)[V], const float (&a)[V], const float (&b)[V],
+                                     const float (&c)[V]) {
+#pragma unroll
+  for (int k = 0; k < V; k += 2) {
+    float x = c[k], y = c[k + 1];
+    fma2(x, y, a[k], a[k + 1], b[k], b[k + 1]);
+    d[k] = x;
+    d[k + 1] = y;
+  }
+}
+template <int V>
+__device__ __forceinline__ void vmul(float (&d)[V], const float (&a)[V], const float (&b)[V]) {
+#pragma unroll
+  for (int k = 0; k < V; k += 2) mul2v(d[k], d[k + 1], a[k], a[k + 1], b[k], b[k + 1]);
+}
+template <int V>
+__device__ __forceinline__ void vadd(float (&d)[V], const float (&a)[V]) {
+#pragma unroll
+  for (int k = 0; k < V; k += 2) add2(d[k], d[k + 1], d[k], d[k + 1], a[k], a[k + 1]);
 }
 
 // Sums of each element of v over the threads of a row, on every thread of it.
@@ -145,19 +171,20 @@ __device__ __forceinline__ void open_gate(const NrArgs& A, const uint4& raw,
 
 template <int V>
 __device__ __forceinline__ float total(const float (&x)[V]) {
-  float s = 0.f;
+  float a = x[0], b = x[1];
 #pragma unroll
-  for (int c = 0; c < V; ++c) s += x[c];
-  return s;
+  for (int c = 2; c < V; c += 2) add2(a, b, a, b, x[c], x[c + 1]);
+  return a + b;
 }
 
-// x becomes (x - mean) * rstd (rows of `kind`), rstd returned.
-template <typename T, int WPR>
+// x becomes (x - mean) * rstd (rows of `kind`), rstd returned.  kLayer: a kind of
+// the call is the layer norm.
+template <typename T, int WPR, bool kLayer>
 __device__ __forceinline__ float norm_row(const NrArgs& A, const Place& P, int kind, float* buf,
                                           int& turn, float (&x)[VecOf<T>::n]) {
   constexpr int V = VecOf<T>::n;
   if (kind == GNN_ROWNORM_NONE) return 1.f;
-  if (kind == GNN_ROWNORM_LAYER) {
+  if (kLayer && kind == GNN_ROWNORM_LAYER) {
     float m[1] = {total<V>(x)};
     row_sums<WPR, 1>(m, A.tpr_log2, buf, turn);
     const float mean = m[0] * A.inv_f;
@@ -181,7 +208,7 @@ struct NrBlocks {
   static constexpr int bwd = sizeof(T) == 4 ? 3 : 2;
 };
 
-template <typename T, int WPR>
+template <typename T, int WPR, bool kLayer>
 __global__ void __launch_bounds__(kThreads, NrBlocks<T>::fwd) nr_fwd(const NrArgs A) {
   constexpr int V = VecOf<T>::n;
   __shared__ float buf[2 * kWarps * 4];
@@ -210,37 +237,49 @@ __global__ void __launch_bounds__(kThreads, NrBlocks<T>::fwd) nr_fwd(const NrArg
     ro = load_raw(A.o, row * A.rv + P.vec, ok);
     rx = load_raw(A.x, row * A.rv + P.vec, ok);
     rg = load_gate<T>(A, P, row, ok);
-    norm_row<T, WPR>(A, P, A.post, buf, turn, o);
-#pragma unroll
-    for (int c = 0; c < V; ++c) y[c] = fmaf(s[c], fmaf(o[c], wp[c], bp[c]), y[c]);
+    norm_row<T, WPR, kLayer>(A, P, A.post, buf, turn, o);
+    vfma<V>(o, o, wp, bp);
+    vfma<V>(y, s, o, y);
     if (now) st16(reinterpret_cast<char*>(A.y) + 16 * at, pack<T>(y));
     if (A.pre != GNN_ROWNORM_NONE) {
-      norm_row<T, WPR>(A, P, A.pre, buf, turn, y);
-#pragma unroll
-      for (int c = 0; c < V; ++c) y[c] = fmaf(y[c], wn[c], bn[c]);
+      norm_row<T, WPR, kLayer>(A, P, A.pre, buf, turn, y);
+      vfma<V>(y, y, wn, bn);
       if (now) st16(reinterpret_cast<char*>(A.z) + 16 * at, pack<T>(y));
     }
   }
 }
 
 // g becomes rstd (g - [mean(g)] - hat mean(g hat)): the gradient of the norm.
-// extra: one more value summed over the row along with them.
-template <typename T, int WPR>
-__device__ __forceinline__ void norm_grad(const NrArgs& A, const Place& P, int kind, float rstd,
+// kExtra: `extra` is summed over the row along with them.
+template <typename T, int WPR, bool kLayer, bool kExtra>
+__device__ __forceinline__ void norm_grad(const NrArgs& A, int kind, float rstd,
                                           const float (&hat)[VecOf<T>::n], float* buf, int& turn,
                                           float (&g)[VecOf<T>::n], float& extra) {
   constexpr int V = VecOf<T>::n;
-  float c[3] = {dot<V>(g, hat), total<V>(g), extra};
-  if (!P.in) c[0] = c[1] = c[2] = 0.f;
-  row_sums<WPR, 3>(c, A.tpr_log2, buf, turn);
-  extra = c[2];
+  if (!kExtra && kind == GNN_ROWNORM_NONE) return;
+  constexpr int N = 1 + kLayer + kExtra;
+  float c[N];
+  c[0] = dot<V>(g, hat);
+  if (kLayer) c[1] = total<V>(g);
+  if (kExtra) c[N - 1] = extra;
+  row_sums<WPR, N>(c, A.tpr_log2, buf, turn);
+  if (kExtra) extra = c[N - 1];
   if (kind == GNN_ROWNORM_NONE) return;
-  const float a = c[0] * A.inv_f, b = kind == GNN_ROWNORM_LAYER ? c[1] * A.inv_f : 0.f;
+  // rstd g + (-rstd mean(g hat)) hat + (-rstd mean(g))
+  const float a = -rstd * A.inv_f * c[0];
+  const float b = kLayer && kind == GNN_ROWNORM_LAYER ? -rstd * A.inv_f * c[1] : 0.f;
 #pragma unroll
-  for (int k = 0; k < V; ++k) g[k] = rstd * (g[k] - b - hat[k] * a);
+  for (int k = 0; k < V; k += 2) {
+    float x = b, y = b;
+    fma2(x, y, hat[k], hat[k + 1], a, a);
+    fma2(x, y, g[k], g[k + 1], rstd, rstd);
+    g[k] = x;
+    g[k + 1] = y;
+  }
 }
 
-template <typename T, int WPR>
+// kRow: the gate is one number per row.
+template <typename T, int WPR, bool kLayer, bool kRow>
 __global__ void __launch_bounds__(kThreads, NrBlocks<T>::bwd) nr_bwd(const NrArgs A) {
   constexpr int V = VecOf<T>::n;
   __shared__ float buf[2 * kWarps * 4];
@@ -281,39 +320,39 @@ __global__ void __launch_bounds__(kThreads, NrBlocks<T>::bwd) nr_bwd(const NrArg
     row += P.stride;
     load();
     if (pre) {
-      const float rstd = norm_row<T, WPR>(A, P, A.pre, buf, turn, y);
-#pragma unroll
-      for (int c = 0; c < V; ++c) {
-        acc[kSumW][c] = fmaf(g[c], y[c], acc[kSumW][c]);
-        acc[kSumC][c] += g[c];
-        g[c] *= wn[c];
-      }
+      const float rstd = norm_row<T, WPR, kLayer>(A, P, A.pre, buf, turn, y);
+      vfma<V>(acc[kSumW], g, y, acc[kSumW]);
+      vadd<V>(acc[kSumC], g);
+      vmul<V>(g, g, wn);
       float none = 0.f;
-      norm_grad<T, WPR>(A, P, A.pre, rstd, y, buf, turn, g, none);
-#pragma unroll
-      for (int c = 0; c < V; ++c) d[c] += g[c];
+      norm_grad<T, WPR, kLayer, false>(A, A.pre, rstd, y, buf, turn, g, none);
+      vadd<V>(d, g);
     }
     if (now) st16(reinterpret_cast<char*>(A.dx) + 16 * at, pack<T>(d));
-    const float rstd = norm_row<T, WPR>(A, P, A.post, buf, turn, o);
-    // d becomes dx sigmoid(g), s the gate's gradient; a thread without a vector
-    // or a row adds nothing to the sums
+    const float rstd = norm_row<T, WPR, kLayer>(A, P, A.post, buf, turn, o);
+    // d becomes dx sigmoid(g) (0 on a thread without a vector or a row: it adds
+    // nothing to the sums), y the gate's gradient d n (1 - sigmoid(g)), g = d wp
+    if (!now) zero<V>(s);
+    vmul<V>(d, d, s);
+    vfma<V>(acc[kSumA], d, o, acc[kSumA]);
+    vadd<V>(acc[kSumB], d);
+    vmul<V>(g, d, wp);
+    float all = 0.f;
+    if (A.gate_width > 0) {
+      vfma<V>(y, o, wp, bp);
+      vmul<V>(y, y, d);
 #pragma unroll
-    for (int c = 0; c < V; ++c) {
-      const float n = fmaf(o[c], wp[c], bp[c]);
-      d[c] = now ? d[c] * s[c] : 0.f;
-      s[c] = d[c] * n * (1.f - s[c]);
-      acc[kSumA][c] = fmaf(d[c], o[c], acc[kSumA][c]);
-      acc[kSumB][c] += d[c];
-      g[c] = d[c] * wp[c];
+      for (int c = 0; c < V; ++c) s[c] = 1.f - s[c];
+      vmul<V>(y, y, s);
+      if (kRow) all = total<V>(y);
     }
-    float all = total<V>(s);
-    norm_grad<T, WPR>(A, P, A.post, rstd, o, buf, turn, g, all);
+    norm_grad<T, WPR, kLayer, kRow>(A, A.post, rstd, o, buf, turn, g, all);
     if (now) {
       st16(reinterpret_cast<char*>(A.dout) + 16 * at, pack<T>(g));
-      if (A.gate_width == 1) {
+      if (kRow) {
         if (P.vec == 0) reinterpret_cast<T*>(A.dgate)[this_row] = T(all);
-      } else if (A.gate_width > 1) {
-        st16(reinterpret_cast<char*>(A.dgate) + 16 * at, pack<T>(s));
+      } else if (A.gate_width > 0) {
+        st16(reinterpret_cast<char*>(A.dgate) + 16 * at, pack<T>(y));
       }
     }
   }
@@ -335,34 +374,40 @@ __global__ void __launch_bounds__(kThreads, NrBlocks<T>::bwd) nr_bwd(const NrArg
   }
 }
 
-// Parameter gradients from the blocks' sums: 32 channels a block, the four sums
-// of each in 32 slices of blocks, in a fixed order.
-__global__ void __launch_bounds__(1024) nr_sum(const double* part, int blocks, int F,
-                                               const gnn_norm_params p, const gnn_norm_grads d) {
-  __shared__ double t[kSums][32][33];
-  const int lane = threadIdx.x & 31, slice = threadIdx.x >> 5;
-  const int f = blockIdx.x * 32 + lane;
-  double s[kSums] = {0.0, 0.0, 0.0, 0.0};
-  if (f < F)
-    for (int b = slice; b < blocks; b += 32)
+// Parameter gradients from the blocks' sums: 16 channels a block, the four sums of
+// each in 16 slices of blocks, in a fixed order.
+constexpr int kSlices = 16;
+__global__ void __launch_bounds__(kSlices * kSums * 16)
+    nr_sum(const double* part, int blocks, int F, const gnn_norm_params p,
+           const gnn_norm_grads d) {
+  __shared__ double t[kSlices][kSums][17];
+  const int lane = threadIdx.x & 15, k = (threadIdx.x >> 4) & 3, slice = threadIdx.x >> 6;
+  const int f = blockIdx.x * 16 + lane;
+  double s[4] = {0.0, 0.0, 0.0, 0.0};  // four loads in flight
+  if (f < F) {
+    const double* at = part + k * F + f;
+    const int64_t step = int64_t(kSums) * F;
+    int b = slice;
+    for (; b + 3 * kSlices < blocks; b += 4 * kSlices)
 #pragma unroll
-      for (int k = 0; k < kSums; ++k) s[k] += part[(int64_t(b) * kSums + k) * F + f];
-#pragma unroll
-  for (int k = 0; k < kSums; ++k) t[k][slice][lane] = s[k];
+      for (int u = 0; u < 4; ++u) s[u] += at[(b + u * kSlices) * step];
+    for (; b < blocks; b += kSlices) s[0] += at[b * step];
+  }
+  t[slice][k][lane] = (s[0] + s[1]) + (s[2] + s[3]);
   __syncthreads();
-  if (slice >= kSums) return;
+  if (slice != 0) return;
   double a = 0.0;
-  for (int x = 0; x < 32; ++x) a += t[slice][x][lane];
-  t[slice][0][lane] = a;
-  asm volatile("bar.sync 1, 128;" ::: "memory");  // the four warps that are left
-  if (slice != 0 || f >= F) return;
+  for (int x = 0; x < kSlices; ++x) a += t[x][k][lane];
+  t[0][k][lane] = a;
+  asm volatile("bar.sync 1, 64;" ::: "memory");  // the two warps that are left
+  if (k != 0 || f >= F) return;
   const double sc = p.scale ? p.scale[f] : 1.0, w = p.w_post ? p.w_post[f] : 1.0,
-               c = p.b_post ? p.b_post[f] : 0.0, va = t[kSumA][0][lane], vb = t[kSumB][0][lane];
+               c = p.b_post ? p.b_post[f] : 0.0, va = t[0][kSumA][lane], vb = t[0][kSumB][lane];
   if (d.dw_post) d.dw_post[f] = float(sc * va);
   if (d.db_post) d.db_post[f] = float(sc * vb);
   if (d.dscale) d.dscale[f] = float(w * va + c * vb);
-  if (d.dw_pre) d.dw_pre[f] = float(t[kSumW][0][lane]);
-  if (d.db_pre) d.db_pre[f] = float(t[kSumC][0][lane]);
+  if (d.dw_pre) d.dw_pre[f] = float(t[0][kSumW][lane]);
+  if (d.db_pre) d.db_pre[f] = float(t[0][kSumC][lane]);
 }
 
 int tpr_log2(int rv) {
@@ -395,10 +440,13 @@ NrArgs nr_args(const gnn_norm_residual& d, gnn_dtype dt) {
   return A;
 }
 
-template <typename T>
-cudaError_t fwd_t(const NrArgs& A, int sm_count, cudaStream_t st) {
-  const int wpr = A.tpr_log2 <= 5 ? 1 : 1 << (A.tpr_log2 - 5);
-  auto kernel = wpr == 1 ? nr_fwd<T, 1> : wpr == 2 ? nr_fwd<T, 2> : nr_fwd<T, 4>;
+bool any_layer(const NrArgs& A) {
+  return A.post == GNN_ROWNORM_LAYER || A.pre == GNN_ROWNORM_LAYER;
+}
+
+template <typename T, int WPR>
+cudaError_t fwd_w(const NrArgs& A, int sm_count, cudaStream_t st) {
+  auto kernel = any_layer(A) ? nr_fwd<T, WPR, true> : nr_fwd<T, WPR, false>;
   const int64_t slots = kThreads >> A.tpr_log2;
   const int64_t want = (A.n + slots - 1) / slots;
   const int64_t cap = persistent_blocks(kernel, 0, sm_count);
@@ -406,16 +454,33 @@ cudaError_t fwd_t(const NrArgs& A, int sm_count, cudaStream_t st) {
   return cudaGetLastError();
 }
 
-template <typename T>
-cudaError_t bwd_t(const NrArgs& A, const gnn_norm_grads& d, cudaStream_t st) {
-  const int wpr = A.tpr_log2 <= 5 ? 1 : 1 << (A.tpr_log2 - 5);
-  auto kernel = wpr == 1 ? nr_bwd<T, 1> : wpr == 2 ? nr_bwd<T, 2> : nr_bwd<T, 4>;
+template <typename T, int WPR>
+cudaError_t bwd_w(const NrArgs& A, const gnn_norm_grads& d, cudaStream_t st) {
+  const bool row = A.gate_width == 1;
+  auto kernel = any_layer(A) ? (row ? nr_bwd<T, WPR, true, true> : nr_bwd<T, WPR, true, false>)
+                             : (row ? nr_bwd<T, WPR, false, true> : nr_bwd<T, WPR, false, false>);
   const size_t smem = size_t(kThreads >> A.tpr_log2) * A.F * 4;
   kernel<<<unsigned(A.blocks), kThreads, smem, st>>>(A);
   cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return e;
-  nr_sum<<<unsigned((A.F + 31) / 32), 1024, 0, st>>>(A.part, A.blocks, A.F, A.p, d);
+  nr_sum<<<unsigned((A.F + 15) / 16), kSlices * kSums * 16, 0, st>>>(A.part, A.blocks, A.F, A.p,
+                                                                     d);
   return cudaGetLastError();
+}
+
+// Warps per row from the threads per row: 1 (a part or all of one), 2 or 4.
+template <typename T>
+cudaError_t fwd_t(const NrArgs& A, int sm_count, cudaStream_t st) {
+  return A.tpr_log2 <= 5   ? fwd_w<T, 1>(A, sm_count, st)
+         : A.tpr_log2 == 6 ? fwd_w<T, 2>(A, sm_count, st)
+                           : fwd_w<T, 4>(A, sm_count, st);
+}
+
+template <typename T>
+cudaError_t bwd_t(const NrArgs& A, const gnn_norm_grads& d, cudaStream_t st) {
+  return A.tpr_log2 <= 5   ? bwd_w<T, 1>(A, d, st)
+         : A.tpr_log2 == 6 ? bwd_w<T, 2>(A, d, st)
+                           : bwd_w<T, 4>(A, d, st);
 }
 
 }  // namespace
