@@ -54,6 +54,7 @@ struct NrArgs {
 
 // Sums over the rows, per channel: a and b above, dw_pre, db_pre.
 enum { kSumA, kSumB, kSumW, kSumC, kSums };
+static_assert(kSums == 4, "nr_sum takes them in two pairs");
 
 __device__ __forceinline__ float sigmoid(float g) {
   // 1 / (1 + 2^(-g log2 e)); the exponential overflows to infinity and the
@@ -205,8 +206,8 @@ __device__ __forceinline__ float norm_row(const NrArgs& A, const Place& P, int k
 template <typename T>
 struct NrBlocks {
   static constexpr int fwd = sizeof(T) == 4 ? 4 : 3;
-  static constexpr int bwd = sizeof(T) == 4 ? 3 : 2;
 };
+constexpr int kBwdPerSm = 2;
 
 template <typename T, int WPR, bool kLayer>
 __global__ void __launch_bounds__(kThreads, NrBlocks<T>::fwd) nr_fwd(const NrArgs A) {
@@ -280,7 +281,7 @@ __device__ __forceinline__ void norm_grad(const NrArgs& A, int kind, float rstd,
 
 // kRow: the gate is one number per row.
 template <typename T, int WPR, bool kLayer, bool kRow>
-__global__ void __launch_bounds__(kThreads, NrBlocks<T>::bwd) nr_bwd(const NrArgs A) {
+__global__ void __launch_bounds__(kThreads, kBwdPerSm) nr_bwd(const NrArgs A) {
   constexpr int V = VecOf<T>::n;
   __shared__ float buf[2 * kWarps * 4];
   extern __shared__ float sums[];  // [row slots of the block][F], one sum at a time
@@ -374,16 +375,17 @@ __global__ void __launch_bounds__(kThreads, NrBlocks<T>::bwd) nr_bwd(const NrArg
   }
 }
 
-// Parameter gradients from the blocks' sums: 16 channels a block, the four sums of
-// each in 16 slices of blocks, in a fixed order.
-constexpr int kSlices = 16;
-__global__ void __launch_bounds__(kSlices * kSums * 16)
+// Parameter gradients from the blocks' sums, in a fixed order: a block takes 16
+// channels and two of their four sums (a and b, blockIdx.y 0, or dw_pre and
+// db_pre), in 32 slices of blocks with four loads in flight.
+constexpr int kSlices = 32;
+__global__ void __launch_bounds__(kSlices * 32)
     nr_sum(const double* part, int blocks, int F, const gnn_norm_params p,
            const gnn_norm_grads d) {
-  __shared__ double t[kSlices][kSums][17];
-  const int lane = threadIdx.x & 15, k = (threadIdx.x >> 4) & 3, slice = threadIdx.x >> 6;
-  const int f = blockIdx.x * 16 + lane;
-  double s[4] = {0.0, 0.0, 0.0, 0.0};  // four loads in flight
+  __shared__ double t[kSlices][33];
+  const int lane = threadIdx.x & 31, slice = threadIdx.x >> 5;
+  const int f = blockIdx.x * 16 + (lane & 15), k = 2 * blockIdx.y + (lane >> 4);
+  double s[4] = {0.0, 0.0, 0.0, 0.0};
   if (f < F) {
     const double* at = part + k * F + f;
     const int64_t step = int64_t(kSums) * F;
@@ -393,21 +395,24 @@ __global__ void __launch_bounds__(kSlices * kSums * 16)
       for (int u = 0; u < 4; ++u) s[u] += at[(b + u * kSlices) * step];
     for (; b < blocks; b += kSlices) s[0] += at[b * step];
   }
-  t[slice][k][lane] = (s[0] + s[1]) + (s[2] + s[3]);
+  t[slice][lane] = (s[0] + s[1]) + (s[2] + s[3]);
   __syncthreads();
   if (slice != 0) return;
-  double a = 0.0;
-  for (int x = 0; x < kSlices; ++x) a += t[x][k][lane];
-  t[0][k][lane] = a;
-  asm volatile("bar.sync 1, 64;" ::: "memory");  // the two warps that are left
-  if (k != 0 || f >= F) return;
-  const double sc = p.scale ? p.scale[f] : 1.0, w = p.w_post ? p.w_post[f] : 1.0,
-               c = p.b_post ? p.b_post[f] : 0.0, va = t[0][kSumA][lane], vb = t[0][kSumB][lane];
-  if (d.dw_post) d.dw_post[f] = float(sc * va);
-  if (d.db_post) d.db_post[f] = float(sc * vb);
-  if (d.dscale) d.dscale[f] = float(w * va + c * vb);
-  if (d.dw_pre) d.dw_pre[f] = float(t[0][kSumW][lane]);
-  if (d.db_pre) d.db_pre[f] = float(t[0][kSumC][lane]);
+  double first = 0.0;
+#pragma unroll
+  for (int x = 0; x < kSlices; ++x) first += t[x][lane];
+  const double second = __shfl_down_sync(kFull, first, 16);
+  if (lane >= 16 || f >= F) return;
+  if (blockIdx.y == 0) {
+    const double sc = p.scale ? p.scale[f] : 1.0, w = p.w_post ? p.w_post[f] : 1.0,
+                 c = p.b_post ? p.b_post[f] : 0.0;
+    if (d.dw_post) d.dw_post[f] = float(sc * first);
+    if (d.db_post) d.db_post[f] = float(sc * second);
+    if (d.dscale) d.dscale[f] = float(w * first + c * second);
+  } else {
+    if (d.dw_pre) d.dw_pre[f] = float(first);
+    if (d.db_pre) d.db_pre[f] = float(second);
+  }
 }
 
 int tpr_log2(int rv) {
@@ -418,8 +423,8 @@ int tpr_log2(int rv) {
 
 // Blocks of the backward pass: what fits on 152 SMs, at least 16 rows a slot
 // before its sums are folded.
-int bwd_blocks(int64_t n, int rv, gnn_dtype dt) {
-  const int cap = 152 * (dt == GNN_F32 ? NrBlocks<float>::bwd : NrBlocks<__nv_bfloat16>::bwd);
+int bwd_blocks(int64_t n, int rv) {
+  const int cap = 152 * kBwdPerSm;
   const int64_t slots = kThreads >> tpr_log2(rv);
   const int64_t want = (n + slots * 16 - 1) / (slots * 16);
   return want < 1 ? 1 : want < cap ? int(want) : cap;
@@ -463,8 +468,8 @@ cudaError_t bwd_w(const NrArgs& A, const gnn_norm_grads& d, cudaStream_t st) {
   kernel<<<unsigned(A.blocks), kThreads, smem, st>>>(A);
   cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return e;
-  nr_sum<<<unsigned((A.F + 15) / 16), kSlices * kSums * 16, 0, st>>>(A.part, A.blocks, A.F, A.p,
-                                                                     d);
+  nr_sum<<<dim3(unsigned((A.F + 15) / 16), 2), kSlices * 32, 0, st>>>(A.part, A.blocks, A.F, A.p,
+                                                                      d);
   return cudaGetLastError();
 }
 
@@ -487,7 +492,7 @@ cudaError_t bwd_t(const NrArgs& A, const gnn_norm_grads& d, cudaStream_t st) {
 
 size_t norm_residual_ws_bytes(int64_t n, int F, gnn_dtype dt) {
   const int rv = F * (dt == GNN_F32 ? 4 : 2) / 16;
-  return align_up(size_t(bwd_blocks(n, rv, dt)) * kSums * F * 8, 256);
+  return align_up(size_t(bwd_blocks(n, rv)) * kSums * F * 8, 256);
 }
 
 cudaError_t launch_norm_residual_forward(const gnn_norm_residual& d, gnn_dtype dt, const void* x,
@@ -516,7 +521,7 @@ cudaError_t launch_norm_residual_backward(const gnn_norm_residual& d, gnn_dtype 
   A.dout = grads.dout;
   A.dgate = grads.dgate;
   A.part = reinterpret_cast<double*>(ws);
-  A.blocks = bwd_blocks(d.n, A.rv, dt);
+  A.blocks = bwd_blocks(d.n, A.rv);
   return dt == GNN_F32 ? bwd_t<float>(A, grads, st) : bwd_t<__nv_bfloat16>(A, grads, st);
 }
 
