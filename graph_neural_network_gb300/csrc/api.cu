@@ -620,7 +620,7 @@ size_t transformer_rel_workspace_bytes(const gnn_graph* g, const gnn_rel* rel, i
                                        gnn_dtype dtype) {
   Shape s;
   if (rel_shape(g, rel, H, D, dtype, &s) != GNN_OK) return 0;
-  return gnn::transformer_ws_bytes(g, s, rel->buckets);
+  return gnn::transformer_rel_ws_bytes(g, s, rel->buckets);
 }
 
 gnn_status transformer_rel_forward(const gnn_graph* g, const gnn_rel* rel, int H, int D,
@@ -635,7 +635,7 @@ gnn_status transformer_rel_forward(const gnn_graph* g, const gnn_rel* rel, int H
   if (!aligned(q, 16) || !aligned(key, 16) || !aligned(val, 16) || !aligned(out, 16) ||
       !aligned(bias, 4) || !aligned(lse, 4))
     return GNN_ERR_INVALID_ARG;
-  if (ws_bytes < gnn::transformer_ws_bytes(g, s, rel->buckets))
+  if (ws_bytes < gnn::transformer_rel_ws_bytes(g, s, rel->buckets))
     return GNN_ERR_WORKSPACE_TOO_SMALL;
   if (!ws || !aligned(ws, 256) || !device_ok(g)) return GNN_ERR_INVALID_ARG;
   return from_cuda(gnn::launch_transformer_rel_forward(
@@ -664,7 +664,7 @@ gnn_status transformer_rel_backward(const gnn_graph* g, const gnn_rel* rel, int 
       !aligned(dq, 16) || !aligned(dkey, 16) || !aligned(dval, 16) || !aligned(lse, 4) ||
       !aligned(bias, 4))
     return GNN_ERR_INVALID_ARG;
-  if (ws_bytes < gnn::transformer_ws_bytes(g, s, rel->buckets))
+  if (ws_bytes < gnn::transformer_rel_ws_bytes(g, s, rel->buckets))
     return GNN_ERR_WORKSPACE_TOO_SMALL;
   if (!ws || !aligned(ws, 256) || !device_ok(g)) return GNN_ERR_INVALID_ARG;
   return from_cuda(gnn::launch_transformer_rel_backward(

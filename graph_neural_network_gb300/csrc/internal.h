@@ -161,7 +161,7 @@ cudaError_t launch_gatv2_backward(const gnn_graph* g, const Shape& s, gnn_dtype 
                                   float* datt, char* ws, cudaStream_t st);
 
 // Graph-transformer attention (transformer.cu), rows of at most 512 bytes.
-size_t transformer_ws_bytes(const gnn_graph* g, const Shape& s, int buckets = 0);
+size_t transformer_ws_bytes(const gnn_graph* g, const Shape& s);
 cudaError_t launch_transformer_forward(const gnn_graph* g, const Shape& s, gnn_dtype dt,
                                        const void* q, const void* key, const void* val,
                                        float scale, void* out, float* lse, char* ws,
@@ -172,7 +172,9 @@ cudaError_t launch_transformer_backward(const gnn_graph* g, const Shape& s, gnn_
                                         void* dq, void* dkey, void* dval, char* ws,
                                         cudaStream_t st);
 
-// The same with a learned relative position bias [buckets][H].
+// The same with a learned relative position bias [buckets][H]
+// (transformer_rel.cu).
+size_t transformer_rel_ws_bytes(const gnn_graph* g, const Shape& s, int buckets);
 cudaError_t launch_transformer_rel_forward(const gnn_graph* g, const gnn_rel* rel, const Shape& s,
                                            gnn_dtype dt, const void* q, const void* key,
                                            const void* val, float scale, const float* bias,

@@ -21,21 +21,7 @@
 // No reduction crosses nodes, so work is pulled dynamically and results are
 // still reproducible bit for bit.  Rows up to 512 bytes; degree-aware tiling
 // and hub merges as in the other attention kernels.
-//
-// kRel adds a learned relative position bias, e_ij += bias[b_ij][k], with the
-// bucket b_ij of the edge read from the prepared bucket bytes (relpos.cu) of
-// the direction being walked, next to the edge's node id.  The table sits in
-// shared memory.  An entry of -infinity masks its edges for that head: the
-// lane treats them as absent, so it neither gathers their rows (which may hold
-// anything) nor adds them to a sum.  The bias gradient
-// dbias[b][k] = sum of de_ij / scale over the edges of bucket b comes out of
-// pass 2, where de is known per edge: each lane that leads a head adds into a
-// column of its own of its warp's table in shared memory (no atomics, no
-// bank conflicts), the block adds its tables in a fixed order in float64 and
-// dbias_sum adds the blocks.  These sums cross nodes, so with kRel pass 2 deals
-// its work to warps by index instead of by counter: the result then depends on
-// the grid alone, not on timing.
-#include "relbias.cuh"
+#include "device.cuh"
 
 namespace gnn {
 namespace {
@@ -75,12 +61,6 @@ struct GtArgs {
   void* dq;
   void* dkey;
   void* dval;
-  const uint8_t* rb_csr;  // kRel: bucket of each edge, in CSR and in CSC order
-  const uint8_t* rb_csc;
-  const float* bias;  // kRel: [buckets][H]
-  int buckets;
-  int rel_off;        // kRel: byte offset of the tables in dynamic shared memory
-  double* db_part;    // kRel: [pass 2 blocks][buckets][H]
   float2* stats;      // [N][H] {lse (base 2), Delta}
   float* d_delta;     // [CSR hub chunks][H]
   float* d_vec;       // [CSR hub chunks][2][row_f]  (P, Q)
@@ -130,32 +110,26 @@ struct GtOnline {
   }
 };
 
-template <typename T, bool kFixed, bool kRel>
+template <typename T, bool kFixed>
 __device__ __forceinline__ void fwd_edges(const GtArgs& A, const Lane<1>& L, const int32_t* cols,
                                           int colbase, int beg, int end, int sg, int SG,
-                                          int step, int trips, int (&jn)[kU], const float* sb,
+                                          int step, int trips, int (&jn)[kU],
                                           const float (&qs)[VecOf<T>::n], GtOnline<T>& st) {
   constexpr int V = VecOf<T>::n;
   constexpr int U = kU;
-  int bn[U];
-  if (kRel) batch_buckets<U>(A.rb_csr, beg, end, sg, SG, bn);
   int base = beg;
   for (int t = 0; kFixed ? t < trips : base < end; ++t, base += step) {
     int j[U];
 #pragma unroll
     for (int u = 0; u < U; ++u) j[u] = jn[u];
-    float bs[U];
-    if (kRel) edge_bias<U>(sb, A.s, L, bn, j, bs);
     uint4 rk[U], rv[U];
 #pragma unroll
     for (int u = 0; u < U; ++u) {
       rk[u] = gather<T>(A.key, j[u], A.s, L);
       rv[u] = gather<T>(A.val, j[u], A.s, L);
     }
-    if (kFixed ? t + 1 < trips : base + step < end) {
+    if (kFixed ? t + 1 < trips : base + step < end)
       batch_ids<U>(cols, colbase, base + step, end, sg, SG, jn);
-      if (kRel) batch_buckets<U>(A.rb_csr, base + step, end, sg, SG, bn);
-    }
     float sc[U];
 #pragma unroll
     for (int u = 0; u < U; ++u) {
@@ -167,7 +141,6 @@ __device__ __forceinline__ void fwd_edges(const GtArgs& A, const Lane<1>& L, con
     float bm = -INFINITY;
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-      if (kRel) sc[u] += bs[u];
       sc[u] = j[u] >= 0 ? sc[u] : -INFINITY;
       bm = fmaxf(bm, sc[u]);
     }
@@ -211,7 +184,7 @@ __device__ __forceinline__ void query(const GtArgs& A, const Lane<1>& L, int64_t
   scale<VecOf<T>::n>(qs, A.scale2);
 }
 
-template <typename T, bool kRel>
+template <typename T>
 __global__ void __launch_bounds__(kThreads, 3) gt_fwd_main(const GtArgs A) {
   constexpr int V = VecOf<T>::n;
   const GtDir& D = A.csr;
@@ -221,7 +194,6 @@ __global__ void __launch_bounds__(kThreads, 3) gt_fwd_main(const GtArgs A) {
   const int H = A.s.H;
   extern __shared__ __align__(16) unsigned char smem[];
   __shared__ int s_item;
-  const float* sb = kRel ? stage_bias(A.bias, A.buckets * A.s.H, smem + A.rel_off) : nullptr;
   float qs[V];
 
   if (D.n_items > 0) {
@@ -247,8 +219,7 @@ __global__ void __launch_bounds__(kThreads, 3) gt_fwd_main(const GtArgs A) {
       query<T>(A, L, it.x, qs);
       GtOnline<T> st;
       st.init();
-      fwd_edges<T, false, kRel>(A, L, cols, colbase, wb, we, L.g, L.G, kWarps * kU * L.G, 0, jn,
-                                sb, qs, st);
+      fwd_edges<T, false>(A, L, cols, colbase, wb, we, L.g, L.G, kWarps * kU * L.G, 0, jn, qs, st);
       st.merge_subgroups(A.s);
       if (L.g == 0 && L.ok[0]) {
 #pragma unroll
@@ -312,7 +283,7 @@ __global__ void __launch_bounds__(kThreads, 3) gt_fwd_main(const GtArgs A) {
       query<T>(A, L, i, qs);
       GtOnline<T> st;
       st.init();
-      fwd_edges<T, false, kRel>(A, L, D.idx, 0, beg, end, L.g, L.G, kU * L.G, 0, jn, sb, qs, st);
+      fwd_edges<T, false>(A, L, D.idx, 0, beg, end, L.g, L.G, kU * L.G, 0, jn, qs, st);
       st.merge_subgroups(A.s);
       if (L.g == 0) fwd_write<T>(A, L, i, st);
       i = i2;
@@ -372,34 +343,28 @@ struct GtDst {
   }
 };
 
-template <typename T, bool kFixed, bool kRel>
+template <typename T, bool kFixed>
 __device__ __forceinline__ void dst_edges(const GtArgs& A, const Lane<1>& L, const int32_t* cols,
                                           int colbase, int beg, int end, int sg, int SG,
-                                          int step, int trips, int (&jn)[kU], const float* sb,
+                                          int step, int trips, int (&jn)[kU],
                                           const float (&qs)[VecOf<T>::n],
                                           const float (&gi)[VecOf<T>::n], float lse2,
                                           GtDst<T>& sm) {
   constexpr int V = VecOf<T>::n;
   constexpr int U = kU;
-  int bn[U];
-  if (kRel) batch_buckets<U>(A.rb_csr, beg, end, sg, SG, bn);
   int base = beg;
   for (int t = 0; kFixed ? t < trips : base < end; ++t, base += step) {
     int j[U];
 #pragma unroll
     for (int u = 0; u < U; ++u) j[u] = jn[u];
-    float bs[U];
-    if (kRel) edge_bias<U>(sb, A.s, L, bn, j, bs);
     uint4 rk[U], rv[U];
 #pragma unroll
     for (int u = 0; u < U; ++u) {
       rk[u] = gather<T>(A.key, j[u], A.s, L);
       rv[u] = gather<T>(A.val, j[u], A.s, L);
     }
-    if (kFixed ? t + 1 < trips : base + step < end) {
+    if (kFixed ? t + 1 < trips : base + step < end)
       batch_ids<U>(cols, colbase, base + step, end, sg, SG, jn);
-      if (kRel) batch_buckets<U>(A.rb_csr, base + step, end, sg, SG, bn);
-    }
     float red[2 * U];
 #pragma unroll
     for (int u = 0; u < U; ++u) {
@@ -412,10 +377,8 @@ __device__ __forceinline__ void dst_edges(const GtArgs& A, const Lane<1>& L, con
     head_sums<2 * U>(red, A.s.hv_log2);
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-      if (kRel) red[u] += bs[u];
       const float al = j[u] >= 0 ? ex2(red[u] - lse2) : 0.f;
-      // with kRel an absent edge may face an own row that holds anything
-      const float ad = kRel && j[u] < 0 ? 0.f : al * red[U + u];
+      const float ad = al * red[U + u];
       sm.delta += ad;
       float x[V];
       unpack_alt<T>(rk[u], x);
@@ -438,7 +401,7 @@ __device__ __forceinline__ void dst_finish(const GtArgs& A, const Lane<1>& L, in
 }
 
 // kSub: light nodes take one sub-group each (rows narrower than a warp).
-template <typename T, bool kSub, bool kRel>
+template <typename T, bool kSub>
 __global__ void __launch_bounds__(kThreads, 3) gt_dst_main(const GtArgs A) {
   constexpr int V = VecOf<T>::n;
   const GtDir& D = A.csr;
@@ -448,7 +411,6 @@ __global__ void __launch_bounds__(kThreads, 3) gt_dst_main(const GtArgs A) {
   const int H = A.s.H;
   extern __shared__ __align__(16) unsigned char smem[];
   __shared__ int s_item;
-  const float* sb = kRel ? stage_bias(A.bias, A.buckets * A.s.H, smem + A.rel_off) : nullptr;
   float qs[V], gi[V];
 
   if (D.n_items > 0) {
@@ -474,8 +436,7 @@ __global__ void __launch_bounds__(kThreads, 3) gt_dst_main(const GtArgs A) {
       const float lse2 = L.ok[0] ? A.lse_in[int64_t(it.x) * H + L.k[0]] * kLog2e : 0.f;
       GtDst<T> sm;
       sm.init();
-      dst_edges<T, false, kRel>(A, L, cols, colbase, wb, we, L.g, L.G, kWarps * kU * L.G, 0, jn,
-                                sb, qs, gi, lse2, sm);
+      dst_edges<T, false>(A, L, cols, colbase, wb, we, L.g, L.G, kWarps * kU * L.G, 0, jn, qs, gi, lse2, sm);
       sm.subgroup_total(A.s);
       float* mine = wbuf + wid * (H + 2 * row_f);
       if (L.g == 0 && L.ok[0]) {
@@ -550,8 +511,7 @@ __global__ void __launch_bounds__(kThreads, 3) gt_dst_main(const GtArgs A) {
         const float lse2 = L.ok[0] ? A.lse_in[int64_t(ii) * H + L.k[0]] * kLog2e : 0.f;
         GtDst<T> sm;
         sm.init();
-        dst_edges<T, true, kRel>(A, L, D.idx, 0, beg, end, 0, 1, kU, trips, jn, sb, qs, gi, lse2,
-                                 sm);
+        dst_edges<T, true>(A, L, D.idx, 0, beg, end, 0, 1, kU, trips, jn, qs, gi, lse2, sm);
         if (i >= 0) dst_finish<T>(A, L, i, sm, lse2);
       }
     }
@@ -586,8 +546,7 @@ __global__ void __launch_bounds__(kThreads, 3) gt_dst_main(const GtArgs A) {
       const float lse2 = L.ok[0] ? A.lse_in[int64_t(i) * H + L.k[0]] * kLog2e : 0.f;
       GtDst<T> sm;
       sm.init();
-      dst_edges<T, false, kRel>(A, L, D.idx, 0, beg, end, L.g, L.G, kU * L.G, 0, jn, sb, qs, gi,
-                                lse2, sm);
+      dst_edges<T, false>(A, L, D.idx, 0, beg, end, L.g, L.G, kU * L.G, 0, jn, qs, gi, lse2, sm);
       sm.subgroup_total(A.s);
       if (L.g == 0) dst_finish<T>(A, L, i, sm, lse2);
       i = i2;
@@ -627,30 +586,21 @@ __global__ void __launch_bounds__(kThreads) gt_dst_merge(const GtArgs A) {
 // backward pass 2: source side
 // ---------------------------------------------------------------------------
 
-template <typename T, bool kFixed, bool kRel>
+template <typename T, bool kFixed>
 __device__ __forceinline__ void src_edges(const GtArgs& A, const Lane<1>& L, const int32_t* cols,
                                           int colbase, int beg, int end, int sg, int SG,
-                                          int step, int trips, int (&in)[kU], const float* sb,
-                                          float* hist,
+                                          int step, int trips, int (&in)[kU],
                                           const float (&ks)[VecOf<T>::n],
                                           const float (&vj)[VecOf<T>::n],
                                           float (&dk)[VecOf<T>::n], float (&dv)[VecOf<T>::n]) {
   constexpr int V = VecOf<T>::n;
   constexpr int U = kU;
   const int H = A.s.H;
-  int bn[U];
-  if (kRel) batch_buckets<U>(A.rb_csc, beg, end, sg, SG, bn);
   int base = beg;
   for (int t = 0; kFixed ? t < trips : base < end; ++t, base += step) {
-    int i[U], b[U];
+    int i[U];
 #pragma unroll
     for (int u = 0; u < U; ++u) i[u] = in[u];
-    float bs[U];
-    if (kRel) {
-#pragma unroll
-      for (int u = 0; u < U; ++u) b[u] = bn[u];
-      edge_bias<U>(sb, A.s, L, bn, i, bs);
-    }
     uint4 rq[U], rg[U];
     float2 st[U];
 #pragma unroll
@@ -660,10 +610,8 @@ __device__ __forceinline__ void src_edges(const GtArgs& A, const Lane<1>& L, con
       st[u] = (i[u] >= 0 && L.ok[0]) ? __ldg(A.stats + int64_t(i[u]) * H + L.k[0])
                                      : make_float2(0.f, 0.f);
     }
-    if (kFixed ? t + 1 < trips : base + step < end) {
+    if (kFixed ? t + 1 < trips : base + step < end)
       batch_ids<U>(cols, colbase, base + step, end, sg, SG, in);
-      if (kRel) batch_buckets<U>(A.rb_csc, base + step, end, sg, SG, bn);
-    }
     float red[2 * U];
 #pragma unroll
     for (int u = 0; u < U; ++u) {
@@ -676,11 +624,8 @@ __device__ __forceinline__ void src_edges(const GtArgs& A, const Lane<1>& L, con
     head_sums<2 * U>(red, A.s.hv_log2);
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-      if (kRel) red[u] += bs[u];
       const float al = i[u] >= 0 ? ex2(red[u] - st[u].x) : 0.f;
-      float de = kRel && i[u] < 0 ? 0.f : al * (red[U + u] - st[u].y);
-      if (kRel && i[u] >= 0 && L.head_leader(A.s, 0)) add_grad(hist, A.s, b[u], de);
-      de *= A.scale;
+      const float de = al * (red[U + u] - st[u].y) * A.scale;
       float x[V], y[V];
       unpack_alt<T>(rq[u], x);
       unpack_alt<T>(rg[u], y);
@@ -700,20 +645,8 @@ __device__ __forceinline__ void src_write(const GtArgs& A, const Lane<1>& L, int
   st16(reinterpret_cast<char*>(A.dval) + off, pack<T>(dv));
 }
 
-// dbias[x] = sum over the blocks of pass 2, one warp per entry.
-__global__ void __launch_bounds__(kThreads) dbias_sum(const double* part, int blocks, int entries,
-                                                      float* dbias) {
-  const int x = blockIdx.x * kWarps + (threadIdx.x >> 5);
-  if (x >= entries) return;
-  double sum = 0.0;
-  for (int b = threadIdx.x & 31; b < blocks; b += 32) sum += part[int64_t(b) * entries + x];
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(kFull, sum, o);
-  if ((threadIdx.x & 31) == 0) dbias[x] = float(sum);
-}
-
 // kSub: light nodes take one sub-group each (rows narrower than a warp).
-template <typename T, bool kSub, bool kRel>
+template <typename T, bool kSub>
 __global__ void __launch_bounds__(kThreads, 3) gt_src_main(const GtArgs A) {
   constexpr int V = VecOf<T>::n;
   const GtDir& D = A.csc;
@@ -723,14 +656,6 @@ __global__ void __launch_bounds__(kThreads, 3) gt_src_main(const GtArgs A) {
   extern __shared__ __align__(16) unsigned char smem[];
   __shared__ int s_item;
   float ks[V], vj[V], dk[V], dv[V];
-  const float* sb = nullptr;
-  float* tables = nullptr;   // kRel: the bias table, then the gradient tables
-  float* hist = nullptr;
-  if (kRel) {
-    tables = reinterpret_cast<float*>(smem + A.rel_off) + A.buckets * A.s.H;
-    hist = clear_grad_tables(tables, A.s, L, A.buckets);
-    sb = stage_bias(A.bias, A.buckets * A.s.H, smem + A.rel_off);
-  }
 
   if (D.n_items > 0) {
     uint64_t* bar = reinterpret_cast<uint64_t*>(smem);
@@ -738,10 +663,10 @@ __global__ void __launch_bounds__(kThreads, 3) gt_src_main(const GtArgs A) {
     float* wbuf = reinterpret_cast<float*>(smem + D.col_off);  // [kWarps][2 row_f]
     uint32_t parity = 0;
     if (threadIdx.x == 0) mbar_init(bar, 1);
-    for (int turn = 0;; ++turn) {
-      if (!kRel && threadIdx.x == 0) s_item = atomicAdd(A.ctr + 2, 1);
+    for (;;) {
+      if (threadIdx.x == 0) s_item = atomicAdd(A.ctr + 2, 1);
       __syncthreads();
-      const int64_t it_i = kRel ? blockIdx.x + int64_t(turn) * gridDim.x : s_item;
+      const int it_i = s_item;
       if (it_i >= D.n_items) break;
       const int4 it = D.items[it_i];
       if (!stage_edges(cols, D.idx, it.y, it.z, bar, parity, A.err)) return;
@@ -755,8 +680,7 @@ __global__ void __launch_bounds__(kThreads, 3) gt_src_main(const GtArgs A) {
       own_row<T>(A.val, it.x, A.s, L, vj);
       zero<V>(dk);
       zero<V>(dv);
-      src_edges<T, false, kRel>(A, L, cols, colbase, wb, we, L.g, L.G, kWarps * kU * L.G, 0, in,
-                                sb, hist, ks, vj, dk, dv);
+      src_edges<T, false>(A, L, cols, colbase, wb, we, L.g, L.G, kWarps * kU * L.G, 0, in, ks, vj, dk, dv);
       subgroup_sums<V>(dk, A.s);
       subgroup_sums<V>(dv, A.s);
       if (L.g == 0 && L.ok[0])
@@ -798,15 +722,10 @@ __global__ void __launch_bounds__(kThreads, 3) gt_src_main(const GtArgs A) {
     // two otherwise
     const int R = L.G >= 32 ? 1 : (L.G == 2 ? 4 : 2);
     const int npull = R * L.G;
-    for (int64_t turn = 0;; ++turn) {
-      int64_t t0 = 0;
-      if (kRel) {
-        t0 = (turn * gridDim.x * kWarps + int64_t(wid) * gridDim.x + blockIdx.x) * npull;
-      } else {
-        int t = 0;
-        if (L.lane == 0) t = atomicAdd(A.ctr + 3, npull);
-        t0 = __shfl_sync(kFull, t, 0);
-      }
+    for (;;) {
+      int t0 = 0;
+      if (L.lane == 0) t0 = atomicAdd(A.ctr + 3, npull);
+      t0 = __shfl_sync(kFull, t0, 0);
       if (t0 >= D.n_light) break;
       int my_n = -1, my_b = 0, my_e = 0;
       if (L.lane < npull && t0 + L.lane < D.n_light) {
@@ -832,25 +751,18 @@ __global__ void __launch_bounds__(kThreads, 3) gt_src_main(const GtArgs A) {
         own_row<T>(A.val, jj, A.s, L, vj);
         zero<V>(dk);
         zero<V>(dv);
-        src_edges<T, true, kRel>(A, L, D.idx, 0, beg, end, 0, 1, kU, trips, in, sb, hist, ks, vj,
-                                 dk, dv);
+        src_edges<T, true>(A, L, D.idx, 0, beg, end, 0, 1, kU, trips, in, ks, vj, dk, dv);
         if (j >= 0) src_write<T>(A, L, j, dk, dv);
       }
     }
-    if (kRel) fold_grad_tables(tables, A.s, L, A.buckets, A.db_part);
     return;
   }
 
   // ---- light nodes, rows of a whole warp: one warp each -----------------
-  for (int64_t turn = 0;; ++turn) {
-    int64_t t0 = 0;
-    if (kRel) {
-      t0 = (turn * gridDim.x * kWarps + int64_t(wid) * gridDim.x + blockIdx.x) * kGrab;
-    } else {
-      int t = 0;
-      if (L.lane == 0) t = atomicAdd(A.ctr + 3, kGrab);
-      t0 = __shfl_sync(kFull, t, 0);
-    }
+  for (;;) {
+    int t0 = 0;
+    if (L.lane == 0) t0 = atomicAdd(A.ctr + 3, kGrab);
+    t0 = __shfl_sync(kFull, t0, 0);
     if (t0 >= D.n_light) break;
     int my_j = -1, my_b = 0, my_e = 0;
     if (L.lane < kGrab && t0 + L.lane < D.n_light) {
@@ -874,8 +786,7 @@ __global__ void __launch_bounds__(kThreads, 3) gt_src_main(const GtArgs A) {
       own_row<T>(A.val, j, A.s, L, vj);
       zero<V>(dk);
       zero<V>(dv);
-      src_edges<T, false, kRel>(A, L, D.idx, 0, beg, end, L.g, L.G, kU * L.G, 0, in, sb, hist, ks,
-                                vj, dk, dv);
+      src_edges<T, false>(A, L, D.idx, 0, beg, end, L.g, L.G, kU * L.G, 0, in, ks, vj, dk, dv);
       subgroup_sums<V>(dk, A.s);
       subgroup_sums<V>(dv, A.s);
       if (L.g == 0) src_write<T>(A, L, j, dk, dv);
@@ -886,7 +797,6 @@ __global__ void __launch_bounds__(kThreads, 3) gt_src_main(const GtArgs A) {
       for (int u = 0; u < kU; ++u) in[u] = in2[u];
     }
   }
-  if (kRel) fold_grad_tables(tables, A.s, L, A.buckets, A.db_part);
 }
 
 template <typename T>
@@ -919,39 +829,26 @@ cudaError_t set_smem(K kernel, size_t bytes) {
   return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, int(bytes));
 }
 
-// max_blocks: a further bound on the grid (0 = none); *blocks (optional) receives it.
 template <typename T, typename K>
 cudaError_t persistent_launch(K kernel, const GtArgs& A, const GtDir& D, size_t smem,
-                              int sm_count, cudaStream_t st, int max_blocks = 0,
-                              int* blocks = nullptr) {
-  if (blocks) *blocks = 0;
+                              int sm_count, cudaStream_t st) {
   if (D.n_items + D.n_light == 0) return cudaSuccess;
   cudaError_t e;
   if ((e = set_smem(kernel, smem)) != cudaSuccess) return e;
   const int64_t work = D.n_items + (D.n_light + kWarps * kGrab - 1) / (kWarps * kGrab);
-  int64_t cap = persistent_blocks(kernel, smem, sm_count);
-  if (max_blocks > 0 && cap > max_blocks) cap = max_blocks;
-  if (work < cap) cap = work;
-  if (blocks) *blocks = int(cap);
-  kernel<<<unsigned(cap), kThreads, smem, st>>>(A);
+  const int64_t cap = persistent_blocks(kernel, smem, sm_count);
+  kernel<<<unsigned(work < cap ? work : cap), kThreads, smem, st>>>(A);
   return cudaGetLastError();
 }
 
-// Blocks of pass 2 with kRel (each writes a share of the bias gradient): the
-// three per SM that its registers allow.
-int rel_blocks(int sm_count) { return 3 * (sm_count > 0 ? sm_count : 1); }
-
-template <typename T, bool kRel>
-cudaError_t fwd_t(GtArgs A, int sm_count, cudaStream_t st) {
+template <typename T>
+cudaError_t fwd_t(const GtArgs& A, int sm_count, cudaStream_t st) {
   constexpr int V = VecOf<T>::n;
   const int row_f = A.s.rv * V;
   cudaError_t e;
   if ((e = cudaMemsetAsync(A.ctr, 0, kCounters * sizeof(int), st)) != cudaSuccess) return e;
-  size_t smem = size_t(A.csr.col_off) + size_t(kWarps) * (2 * A.s.H + row_f) * 4;
-  A.rel_off = int(smem);
-  if (kRel) smem += size_t(A.buckets) * A.s.H * 4;
-  if ((e = persistent_launch<T>(gt_fwd_main<T, kRel>, A, A.csr, smem, sm_count, st)) !=
-      cudaSuccess)
+  const size_t smem = size_t(A.csr.col_off) + size_t(kWarps) * (2 * A.s.H + row_f) * 4;
+  if ((e = persistent_launch<T>(gt_fwd_main<T>, A, A.csr, smem, sm_count, st)) != cudaSuccess)
     return e;
   if (A.csr.n_hubs > 0) {
     gt_fwd_merge<T><<<unsigned((A.csr.n_hubs + kWarps - 1) / kWarps), kThreads, 0, st>>>(A);
@@ -960,36 +857,29 @@ cudaError_t fwd_t(GtArgs A, int sm_count, cudaStream_t st) {
   return cudaSuccess;
 }
 
-template <typename T, bool kRel>
-cudaError_t bwd_t(GtArgs A, float* dbias, int sm_count, cudaStream_t st) {
+template <typename T>
+cudaError_t bwd_t(const GtArgs& A, int sm_count, cudaStream_t st) {
   constexpr int V = VecOf<T>::n;
   const int row_f = A.s.rv * V;
   cudaError_t e;
   if ((e = cudaMemsetAsync(A.ctr, 0, kCounters * sizeof(int), st)) != cudaSuccess) return e;
-  const size_t table = kRel ? size_t(A.buckets) * A.s.H * 4 : 0;
   const size_t smem1 = size_t(A.csr.col_off) + size_t(kWarps) * (A.s.H + 2 * row_f) * 4;
-  A.rel_off = int(smem1);
-  if ((e = persistent_launch<T>(
-           A.s.lpr < 32 ? gt_dst_main<T, true, kRel> : gt_dst_main<T, false, kRel>, A, A.csr,
-           smem1 + table, sm_count, st)) != cudaSuccess)
+  if ((e = persistent_launch<T>(A.s.lpr < 32 ? gt_dst_main<T, true> : gt_dst_main<T, false>, A, A.csr,
+                                    smem1, sm_count, st)) != cudaSuccess)
     return e;
   if (A.csr.n_hubs > 0) {
     gt_dst_merge<T><<<unsigned((A.csr.n_hubs + kWarps - 1) / kWarps), kThreads, 0, st>>>(A);
     if ((e = cudaGetLastError()) != cudaSuccess) return e;
   }
-  size_t smem2 = size_t(A.csc.col_off) + size_t(kWarps) * 2 * row_f * 4;
-  A.rel_off = int(smem2);
-  if (kRel) smem2 += table + grad_tables_bytes(A.s, A.buckets);
-  int blocks = 0;
-  if ((e = persistent_launch<T>(
-           A.s.lpr < 32 ? gt_src_main<T, true, kRel> : gt_src_main<T, false, kRel>, A, A.csc,
-           smem2, sm_count, st, kRel ? rel_blocks(sm_count) : 0, &blocks)) != cudaSuccess)
+  const size_t smem2 = size_t(A.csc.col_off) + size_t(kWarps) * 2 * row_f * 4;
+  if ((e = persistent_launch<T>(A.s.lpr < 32 ? gt_src_main<T, true> : gt_src_main<T, false>, A, A.csc,
+                                    smem2, sm_count, st)) != cudaSuccess)
     return e;
   if (A.csc.n_hubs > 0) {
     gt_src_merge<T><<<unsigned((A.csc.n_hubs + kWarps - 1) / kWarps), kThreads, 0, st>>>(A);
     if ((e = cudaGetLastError()) != cudaSuccess) return e;
   }
-  return kRel ? launch_dbias_sum(A.db_part, blocks, A.buckets * A.s.H, dbias, st) : cudaSuccess;
+  return cudaSuccess;
 }
 
 GtDir gt_dir(const Dir& d) {
@@ -1007,11 +897,10 @@ GtDir gt_dir(const Dir& d) {
 }
 
 struct GtLayout {
-  size_t ctr, f_acc, f_ml, stats, d_delta, d_vec, s_vec, db_part, total;
+  size_t ctr, f_acc, f_ml, stats, d_delta, d_vec, s_vec, total;
 };
 
-// buckets: 0 without a relative position bias
-GtLayout gt_layout(const gnn_graph* g, const Shape& s, int buckets) {
+GtLayout gt_layout(const gnn_graph* g, const Shape& s) {
   const size_t row_f = size_t(s.rv) * 16 / s.esize;
   const size_t cc = size_t(g->csr.n_hub_chunks), sc = size_t(g->csc.n_hub_chunks);
   GtLayout L{};
@@ -1028,15 +917,13 @@ GtLayout gt_layout(const gnn_graph* g, const Shape& s, int buckets) {
   L.d_delta = take(cc * s.H * 4);
   L.d_vec = take(cc * 2 * row_f * 4);
   L.s_vec = take(sc * 2 * row_f * 4);
-  if (buckets > 0) L.db_part = take(size_t(rel_blocks(g->sm_count)) * buckets * s.H * 8);
   L.total = off;
   return L;
 }
 
 GtArgs gt_args(const gnn_graph* g, const Shape& s, const void* q, const void* key,
-               const void* val, float scale, char* ws, const gnn_rel* rel = nullptr,
-               const float* bias = nullptr) {
-  const GtLayout W = gt_layout(g, s, rel ? rel->buckets : 0);
+               const void* val, float scale, char* ws) {
+  const GtLayout W = gt_layout(g, s);
   GtArgs A{};
   A.s = s;
   A.csr = gt_dir(g->csr);
@@ -1054,28 +941,12 @@ GtArgs gt_args(const gnn_graph* g, const Shape& s, const void* q, const void* ke
   A.d_vec = reinterpret_cast<float*>(ws + W.d_vec);
   A.s_vec = reinterpret_cast<float*>(ws + W.s_vec);
   A.err = g->err;
-  if (rel) {
-    A.rb_csr = rel->csr;
-    A.rb_csc = rel->csc;
-    A.bias = bias;
-    A.buckets = rel->buckets;
-    A.db_part = reinterpret_cast<double*>(ws + W.db_part);
-  }
   return A;
 }
 
 }  // namespace
 
-cudaError_t launch_dbias_sum(const double* part, int blocks, int entries, float* dbias,
-                             cudaStream_t st) {
-  dbias_sum<<<unsigned((entries + kWarps - 1) / kWarps), kThreads, 0, st>>>(part, blocks, entries,
-                                                                           dbias);
-  return cudaGetLastError();
-}
-
-size_t transformer_ws_bytes(const gnn_graph* g, const Shape& s, int buckets) {
-  return gt_layout(g, s, buckets).total;
-}
+size_t transformer_ws_bytes(const gnn_graph* g, const Shape& s) { return gt_layout(g, s).total; }
 
 cudaError_t launch_transformer_forward(const gnn_graph* g, const Shape& s, gnn_dtype dt,
                                        const void* q, const void* key, const void* val,
@@ -1084,8 +955,8 @@ cudaError_t launch_transformer_forward(const gnn_graph* g, const Shape& s, gnn_d
   GtArgs A = gt_args(g, s, q, key, val, scale, ws);
   A.out = out;
   A.lse = lse;
-  return dt == GNN_F32 ? fwd_t<float, false>(A, g->sm_count, st)
-                       : fwd_t<__nv_bfloat16, false>(A, g->sm_count, st);
+  return dt == GNN_F32 ? fwd_t<float>(A, g->sm_count, st)
+                       : fwd_t<__nv_bfloat16>(A, g->sm_count, st);
 }
 
 cudaError_t launch_transformer_backward(const gnn_graph* g, const Shape& s, gnn_dtype dt,
@@ -1099,35 +970,8 @@ cudaError_t launch_transformer_backward(const gnn_graph* g, const Shape& s, gnn_
   A.dq = dq;
   A.dkey = dkey;
   A.dval = dval;
-  return dt == GNN_F32 ? bwd_t<float, false>(A, nullptr, g->sm_count, st)
-                       : bwd_t<__nv_bfloat16, false>(A, nullptr, g->sm_count, st);
-}
-
-cudaError_t launch_transformer_rel_forward(const gnn_graph* g, const gnn_rel* rel, const Shape& s,
-                                           gnn_dtype dt, const void* q, const void* key,
-                                           const void* val, float scale, const float* bias,
-                                           void* out, float* lse, char* ws, cudaStream_t st) {
-  GtArgs A = gt_args(g, s, q, key, val, scale, ws, rel, bias);
-  A.out = out;
-  A.lse = lse;
-  return dt == GNN_F32 ? fwd_t<float, true>(A, g->sm_count, st)
-                       : fwd_t<__nv_bfloat16, true>(A, g->sm_count, st);
-}
-
-cudaError_t launch_transformer_rel_backward(const gnn_graph* g, const gnn_rel* rel,
-                                            const Shape& s, gnn_dtype dt, const void* q,
-                                            const void* key, const void* val, float scale,
-                                            const float* bias, const float* lse,
-                                            const void* dout, void* dq, void* dkey, void* dval,
-                                            float* dbias, char* ws, cudaStream_t st) {
-  GtArgs A = gt_args(g, s, q, key, val, scale, ws, rel, bias);
-  A.lse_in = lse;
-  A.dout = dout;
-  A.dq = dq;
-  A.dkey = dkey;
-  A.dval = dval;
-  return dt == GNN_F32 ? bwd_t<float, true>(A, dbias, g->sm_count, st)
-                       : bwd_t<__nv_bfloat16, true>(A, dbias, g->sm_count, st);
+  return dt == GNN_F32 ? bwd_t<float>(A, g->sm_count, st)
+                       : bwd_t<__nv_bfloat16>(A, g->sm_count, st);
 }
 
 }  // namespace gnn

@@ -1,0 +1,497 @@
+// Graph-transformer attention with a learned relative position bias, forward and
+// backward.  As transformer.cu, with
+//   e_ij = scale * q_i[k] . key_j[k] + bias[b_ij][k],
+// the bucket b_ij read next to the edge's node id from the prepared bucket bytes
+// (relpos.cu) of the direction being walked, and the bias table in shared
+// memory.  An entry of -infinity masks its edges for that head: the lane treats
+// them as absent, so it neither gathers their rows (which may hold anything) nor
+// adds them to a sum.
+//
+// Forward: one pass over the CSR with an online softmax whose reference moves
+// only when a score passes it.  Backward pass 1 (CSR): Delta, P = sum alpha da
+// key_j, Q = sum alpha key_j, dq_i = scale (P - Delta Q), record {lse, Delta}.  Pass
+// 2 (CSC): dkey, dval, and dbias[b][k] = sum of de_ij over the edges of bucket
+// b, de_ij = alpha_ij (da_ij - Delta_i) being known per edge there: each lane that
+// leads a head adds into a column of its own of its warp's table in shared
+// memory (no atomics, no bank conflicts), the block adds its tables in a fixed
+// order in float64, and dbias_sum adds the blocks.
+//
+// Bound: gathers, 2 rows an edge and pass.  A lane holds 32 bytes of a row (16 where
+// a head has no more), so that what an edge costs whatever its width (ids,
+// bucket, bias, score, exponential, addresses) is shared by more elements; both
+// dot products of bfloat16 rows multiply the packed halves.  The work is cut as
+// edgewalk.cuh says.
+#include "edgewalk.cuh"
+#include "lanevec.cuh"
+
+namespace gnn {
+namespace {
+
+struct RelArgs {
+  Shape s;                 // in kE-element vectors
+  Walk walk;
+  WalkDir dir;
+  const void *q, *key, *val;
+  float scale, scale2;     // natural units, base 2
+  const float* bias;       // [buckets][H]
+  int buckets;
+  void* out;
+  float* lse;
+  const float* lse_in;
+  const void* dout;
+  void *dq, *dkey, *dval;
+  float2* stats;           // [N][H] {lse (base 2), Delta}
+  double* db_part;         // [pass 2 blocks][buckets][H]
+};
+
+// Edges in flight per lane: 64 bytes of each of the two gathered rows.
+template <typename T, int kE>
+struct RelUnroll {
+  static constexpr int value = 64 / (kE * int(sizeof(T)));
+};
+
+// ---- forward -----------------------------------------------------------------
+
+template <typename T, int kE_>
+struct RelFwd {
+  static constexpr int kE = kE_;
+  static constexpr int U = RelUnroll<T, kE>::value;
+  static constexpr bool kBuckets = true;
+  const RelArgs& A;
+  const Lane<1>& L;
+  const float* sb;
+  HeldT<T, kE> q;
+  float m, l, acc[kE];  // m in base 2
+
+  __device__ __forceinline__ RelFwd(const RelArgs& a, const Lane<1>& lane) : A(a), L(lane) {}
+  static __host__ __device__ int floats(const Shape& s) { return s.rv * kE + 2 * s.H; }
+
+  __device__ __forceinline__ void clear() {
+    m = -INFINITY;
+    l = 0.f;
+    zero<kE>(acc);
+  }
+  __device__ __forceinline__ void begin(int i, bool ok) {
+    q.set(ldT<T, kE>(A.q, i, A.s, L, ok && L.ok[0]));
+    clear();
+  }
+  template <class F>
+  __device__ __forceinline__ void batch(int (&j)[U], const int (&b)[U], const F& sent) {
+    float bs[U];
+    edge_bias<U>(sb, A.s, L, b, j, bs);
+    RawT<T, kE> rk[U], rv[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const bool ok = j[u] >= 0 && L.ok[0];
+      rk[u] = ldT<T, kE>(A.key, j[u], A.s, L, ok);
+      rv[u] = ldT<T, kE>(A.val, j[u], A.s, L, ok);
+    }
+    sent();
+    float sc[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u) sc[u] = q.dot_with(rk[u]);
+    head_sums<U>(sc, A.s.hv_log2);
+    float top = m;
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      sc[u] = j[u] >= 0 ? fmaf(sc[u], A.scale2, bs[u]) : -INFINITY;
+      top = fmaxf(top, sc[u]);
+    }
+    if (top > m) {
+      const float s0 = ex2(m - top);
+      l *= s0;
+      scale<kE>(acc, s0);
+      m = top;
+    }
+    const float mr = m == -INFINITY ? 0.f : m;
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const float p = ex2(sc[u] - mr);
+      l += p;
+      float x[kE];
+      widenT<T, kE>(rv[u], x);
+      axpy<kE>(acc, p, x);
+    }
+  }
+  __device__ __forceinline__ void put(float* to) const {
+#pragma unroll
+    for (int c = 0; c < kE; ++c) to[L.q[0] * kE + c] = acc[c];
+    if (L.head_leader(A.s, 0)) {
+      to[A.s.rv * kE + 2 * L.k[0]] = m;
+      to[A.s.rv * kE + 2 * L.k[0] + 1] = l;
+    }
+  }
+  __device__ __forceinline__ void take(const float* from) {
+    const float mb = part_load(from + A.s.rv * kE + 2 * L.k[0]);
+    const float lb = part_load(from + A.s.rv * kE + 2 * L.k[0] + 1);
+    float x[kE];
+#pragma unroll
+    for (int c = 0; c < kE; ++c) x[c] = part_load(from + L.q[0] * kE + c);
+    const float M = fmaxf(m, mb), Mr = M == -INFINITY ? 0.f : M;
+    const float sa = ex2(m - Mr), sx = ex2(mb - Mr);
+    l = l * sa + lb * sx;
+    scale<kE>(acc, sa);
+    axpy<kE>(acc, sx, x);
+    m = M;
+  }
+  __device__ __forceinline__ void finish(int i) {
+    const bool any = l != 0.f;  // a NaN stays one
+    scale<kE>(acc, any ? __frcp_rn(l) : 0.f);
+    storeT<T, kE>(A.out, i, A.s, L, acc);
+    if (L.head_leader(A.s, 0))
+      A.lse[int64_t(i) * A.s.H + L.k[0]] = any ? (m + __log2f(l)) * kLn2 : -INFINITY;
+  }
+};
+
+// ---- backward pass 1: destination side ---------------------------------------
+
+template <typename T, int kE_>
+struct RelDst {
+  static constexpr int kE = kE_;
+  static constexpr int U = RelUnroll<T, kE>::value;
+  static constexpr bool kBuckets = true;
+  const RelArgs& A;
+  const Lane<1>& L;
+  const float* sb;
+  HeldT<T, kE> q, g;
+  float lse2, delta, P[kE], Q[kE];
+
+  __device__ __forceinline__ RelDst(const RelArgs& a, const Lane<1>& lane) : A(a), L(lane) {}
+  static __host__ __device__ int floats(const Shape& s) { return 2 * s.rv * kE + s.H; }
+
+  __device__ __forceinline__ void clear() {
+    delta = 0.f;
+    zero<kE>(P);
+    zero<kE>(Q);
+  }
+  __device__ __forceinline__ void begin(int i, bool ok) {
+    q.set(ldT<T, kE>(A.q, i, A.s, L, ok && L.ok[0]));
+    g.set(ldT<T, kE>(A.dout, i, A.s, L, ok && L.ok[0]));
+    lse2 = ok && L.ok[0] ? __ldg(A.lse_in + int64_t(i) * A.s.H + L.k[0]) * kLog2e : 0.f;
+    clear();
+  }
+  template <class F>
+  __device__ __forceinline__ void batch(int (&j)[U], const int (&b)[U], const F& sent) {
+    float bs[U];
+    edge_bias<U>(sb, A.s, L, b, j, bs);
+    RawT<T, kE> rk[U], rv[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const bool ok = j[u] >= 0 && L.ok[0];
+      rk[u] = ldT<T, kE>(A.key, j[u], A.s, L, ok);
+      rv[u] = ldT<T, kE>(A.val, j[u], A.s, L, ok);
+    }
+    sent();
+    float red[2 * U];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      red[u] = q.dot_with(rk[u]);
+      red[U + u] = g.dot_with(rv[u]);
+    }
+    head_sums<2 * U>(red, A.s.hv_log2);
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      // an absent edge may face an own row that holds anything
+      const float al = j[u] >= 0 ? ex2(fmaf(red[u], A.scale2, bs[u]) - lse2) : 0.f;
+      const float ad = j[u] >= 0 ? al * red[U + u] : 0.f;
+      delta += ad;
+      float x[kE];
+      widenT<T, kE>(rk[u], x);
+      axpy<kE>(P, ad, x);
+      axpy<kE>(Q, al, x);
+    }
+  }
+  __device__ __forceinline__ void put(float* to) const {
+    const int row = A.s.rv * kE, at = L.q[0] * kE;
+#pragma unroll
+    for (int c = 0; c < kE; ++c) {
+      to[at + c] = P[c];
+      to[row + at + c] = Q[c];
+    }
+    if (L.head_leader(A.s, 0)) to[2 * row + L.k[0]] = delta;
+  }
+  __device__ __forceinline__ void take(const float* from) {
+    const int row = A.s.rv * kE, at = L.q[0] * kE;
+#pragma unroll
+    for (int c = 0; c < kE; ++c) {
+      P[c] += part_load(from + at + c);
+      Q[c] += part_load(from + row + at + c);
+    }
+    delta += part_load(from + 2 * row + L.k[0]);
+  }
+  __device__ __forceinline__ void finish(int i) {
+#pragma unroll
+    for (int c = 0; c < kE; ++c) P[c] = A.scale * fmaf(-delta, Q[c], P[c]);
+    storeT<T, kE>(A.dq, i, A.s, L, P);
+    if (L.head_leader(A.s, 0))
+      A.stats[int64_t(i) * A.s.H + L.k[0]] = make_float2(lse2, delta);
+  }
+};
+
+// ---- backward pass 2: source side --------------------------------------------
+
+template <typename T, int kE_>
+struct RelSrc {
+  static constexpr int kE = kE_;
+  static constexpr int U = RelUnroll<T, kE>::value;
+  static constexpr bool kBuckets = true;
+  const RelArgs& A;
+  const Lane<1>& L;
+  const float* sb;
+  float* hist;  // this lane's column of its warp's gradient table
+  HeldT<T, kE> k, v;
+  float dk[kE], dv[kE];
+
+  __device__ __forceinline__ RelSrc(const RelArgs& a, const Lane<1>& lane) : A(a), L(lane) {}
+  static __host__ __device__ int floats(const Shape& s) { return 2 * s.rv * kE; }
+
+  __device__ __forceinline__ void clear() {
+    zero<kE>(dk);
+    zero<kE>(dv);
+  }
+  __device__ __forceinline__ void begin(int j, bool ok) {
+    k.set(ldT<T, kE>(A.key, j, A.s, L, ok && L.ok[0]));
+    v.set(ldT<T, kE>(A.val, j, A.s, L, ok && L.ok[0]));
+    clear();
+  }
+  template <class F>
+  __device__ __forceinline__ void batch(int (&i)[U], const int (&b)[U], const F& sent) {
+    float bs[U];
+    edge_bias<U>(sb, A.s, L, b, i, bs);
+    RawT<T, kE> rq[U], rg[U];
+    float2 st[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const bool ok = i[u] >= 0 && L.ok[0];
+      rq[u] = ldT<T, kE>(A.q, i[u], A.s, L, ok);
+      rg[u] = ldT<T, kE>(A.dout, i[u], A.s, L, ok);
+      st[u] = ok ? __ldg(A.stats + int64_t(i[u]) * A.s.H + L.k[0]) : make_float2(0.f, 0.f);
+    }
+    sent();
+    float red[2 * U];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      red[u] = k.dot_with(rq[u]);
+      red[U + u] = v.dot_with(rg[u]);
+    }
+    head_sums<2 * U>(red, A.s.hv_log2);
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const float al = i[u] >= 0 ? ex2(fmaf(red[u], A.scale2, bs[u]) - st[u].x) : 0.f;
+      const float de = i[u] >= 0 ? al * (red[U + u] - st[u].y) : 0.f;
+      if (i[u] >= 0 && L.head_leader(A.s, 0)) add_grad(hist, A.s, b[u], de);
+      float x[kE];
+      widenT<T, kE>(rq[u], x);
+      axpy<kE>(dk, de, x);
+      widenT<T, kE>(rg[u], x);
+      axpy<kE>(dv, al, x);
+    }
+  }
+  __device__ __forceinline__ void put(float* to) const {
+    const int row = A.s.rv * kE, at = L.q[0] * kE;
+#pragma unroll
+    for (int c = 0; c < kE; ++c) {
+      to[at + c] = dk[c];
+      to[row + at + c] = dv[c];
+    }
+  }
+  __device__ __forceinline__ void take(const float* from) {
+    const int row = A.s.rv * kE, at = L.q[0] * kE;
+#pragma unroll
+    for (int c = 0; c < kE; ++c) {
+      dk[c] += part_load(from + at + c);
+      dv[c] += part_load(from + row + at + c);
+    }
+  }
+  __device__ __forceinline__ void finish(int j) {
+    scale<kE>(dk, A.scale);
+    storeT<T, kE>(A.dkey, j, A.s, L, dk);
+    storeT<T, kE>(A.dval, j, A.s, L, dv);
+  }
+};
+
+// ---- kernels -----------------------------------------------------------------
+
+constexpr int kFwdPerSm = 3, kBwdPerSm = 2;  // resident blocks
+
+template <typename T, int kE>
+__global__ void __launch_bounds__(kThreads, kFwdPerSm) rel_fwd(const __grid_constant__ RelArgs A) {
+  extern __shared__ __align__(16) unsigned char smem[];
+  const Lane<1> L(A.s);
+  RelFwd<T, kE> p(A, L);
+  p.sb = stage_bias(A.bias, A.buckets * A.s.H, smem);
+  walk(p, A.walk, A.dir, A.s, L);
+}
+
+template <typename T, int kE>
+__global__ void __launch_bounds__(kThreads, kBwdPerSm) rel_dst(const __grid_constant__ RelArgs A) {
+  extern __shared__ __align__(16) unsigned char smem[];
+  const Lane<1> L(A.s);
+  RelDst<T, kE> p(A, L);
+  p.sb = stage_bias(A.bias, A.buckets * A.s.H, smem);
+  walk(p, A.walk, A.dir, A.s, L);
+}
+
+template <typename T, int kE>
+__global__ void __launch_bounds__(kThreads, kBwdPerSm) rel_src(const __grid_constant__ RelArgs A) {
+  extern __shared__ __align__(16) unsigned char smem[];
+  const Lane<1> L(A.s);
+  RelSrc<T, kE> p(A, L);
+  float* tables = reinterpret_cast<float*>(smem) + A.buckets * A.s.H;
+  p.hist = clear_grad_tables(tables, A.s, L, A.buckets);
+  p.sb = stage_bias(A.bias, A.buckets * A.s.H, smem);
+  walk(p, A.walk, A.dir, A.s, L);
+  fold_grad_tables(tables, A.s, L, A.buckets, A.db_part);
+}
+
+// dbias[x] = sum over the blocks of pass 2, one warp per entry.
+__global__ void __launch_bounds__(kThreads) dbias_sum(const double* part, int blocks, int entries,
+                                                      float* dbias) {
+  const int x = blockIdx.x * kWarps + (threadIdx.x >> 5);
+  if (x >= entries) return;
+  double sum = 0.0;
+  for (int b = threadIdx.x & 31; b < blocks; b += 32) sum += part[int64_t(b) * entries + x];
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(kFull, sum, o);
+  if ((threadIdx.x & 31) == 0) dbias[x] = float(sum);
+}
+
+// ---- host side ---------------------------------------------------------------
+
+// Elements of a lane vector: 32 bytes where a head has as many.
+int lane_elems(const Shape& s) {
+  const int most = 32 / s.esize;
+  return s.D >= most ? most : s.D;
+}
+
+struct RelLayout {
+  size_t arrived, part, stats, db_part, total;
+  WalkPlan fwd, bwd;  // the same for both directions: n and e are
+};
+
+RelLayout rel_layout(const gnn_graph* g, const Shape& s, int buckets) {
+  const Shape w = lane_shape(s, lane_elems(s));
+  const size_t row = size_t(s.H) * s.D;
+  RelLayout L{};
+  L.fwd = walk_plan(g->n, g->e, w, kFwdPerSm, g->sm_count);
+  L.bwd = walk_plan(g->n, g->e, w, kBwdPerSm, g->sm_count);
+  const size_t workers = size_t(L.fwd.workers > L.bwd.workers ? L.fwd.workers : L.bwd.workers);
+  size_t off = 0;
+  auto take = [&](size_t bytes) {
+    const size_t r = off;
+    off += align_up(bytes > 0 ? bytes : 1, 256);
+    return r;
+  };
+  L.arrived = take(workers * 2 * sizeof(int));
+  const size_t fwd = size_t(L.fwd.workers) * 2 * (row + 2 * s.H) * 4;
+  const size_t bwd = size_t(L.bwd.workers) * 2 * (2 * row + s.H) * 4;
+  L.part = take(fwd > bwd ? fwd : bwd);
+  L.stats = take(size_t(g->n) * s.H * 8);
+  L.db_part = take(size_t(L.bwd.blocks) * buckets * s.H * 8);
+  L.total = off;
+  return L;
+}
+
+template <typename K>
+cudaError_t launch(K kernel, const RelArgs& A, int blocks, size_t smem, cudaStream_t st) {
+  cudaError_t e;
+  if (smem > 48 * 1024 &&
+      (e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, int(smem))) !=
+          cudaSuccess)
+    return e;
+  kernel<<<unsigned(blocks), kThreads, smem, st>>>(A);
+  return cudaGetLastError();
+}
+
+template <typename T, int kE>
+cudaError_t fwd_t(const RelArgs& A, const WalkPlan& p, cudaStream_t st) {
+  const cudaError_t e = cudaMemsetAsync(A.walk.arrived, 0, size_t(p.workers) * sizeof(int), st);
+  if (e != cudaSuccess) return e;
+  return launch(rel_fwd<T, kE>, A, p.blocks, size_t(A.buckets) * A.s.H * 4, st);
+}
+
+template <typename T, int kE>
+cudaError_t bwd_t(RelArgs A, const gnn_graph* g, const gnn_rel* rel, const WalkPlan& p,
+                  float* dbias, cudaStream_t st) {
+  // the counters of both passes
+  cudaError_t e = cudaMemsetAsync(A.walk.arrived, 0, size_t(p.workers) * 2 * sizeof(int), st);
+  if (e != cudaSuccess) return e;
+  const size_t table = size_t(A.buckets) * A.s.H * 4;
+  if ((e = launch(rel_dst<T, kE>, A, p.blocks, table, st)) != cudaSuccess) return e;
+  A.dir = WalkDir{g->csc.ptr, g->csc.idx, rel->csc};
+  A.walk.arrived += p.workers;
+  if ((e = launch(rel_src<T, kE>, A, p.blocks, table + grad_tables_bytes(A.s, A.buckets), st)) !=
+      cudaSuccess)
+    return e;
+  return launch_dbias_sum(A.db_part, p.blocks, A.buckets * A.s.H, dbias, st);
+}
+
+RelArgs rel_args(const gnn_graph* g, const gnn_rel* rel, const Shape& s, const void* q,
+                 const void* key, const void* val, float scale, const float* bias,
+                 const RelLayout& W, const WalkPlan& p, char* ws) {
+  RelArgs A{};
+  A.s = lane_shape(s, lane_elems(s));
+  A.walk = make_walk(p, g->n, reinterpret_cast<int*>(ws + W.arrived),
+                     reinterpret_cast<float*>(ws + W.part));
+  A.dir = WalkDir{g->csr.ptr, g->csr.idx, rel->csr};
+  A.q = q;
+  A.key = key;
+  A.val = val;
+  A.scale = scale;
+  A.scale2 = scale * kLog2e;
+  A.bias = bias;
+  A.buckets = rel->buckets;
+  A.stats = reinterpret_cast<float2*>(ws + W.stats);
+  A.db_part = reinterpret_cast<double*>(ws + W.db_part);
+  return A;
+}
+
+}  // namespace
+
+cudaError_t launch_dbias_sum(const double* part, int blocks, int entries, float* dbias,
+                             cudaStream_t st) {
+  dbias_sum<<<unsigned((entries + kWarps - 1) / kWarps), kThreads, 0, st>>>(part, blocks, entries,
+                                                                           dbias);
+  return cudaGetLastError();
+}
+
+size_t transformer_rel_ws_bytes(const gnn_graph* g, const Shape& s, int buckets) {
+  return rel_layout(g, s, buckets).total;
+}
+
+cudaError_t launch_transformer_rel_forward(const gnn_graph* g, const gnn_rel* rel, const Shape& s,
+                                           gnn_dtype dt, const void* q, const void* key,
+                                           const void* val, float scale, const float* bias,
+                                           void* out, float* lse, char* ws, cudaStream_t st) {
+  const RelLayout W = rel_layout(g, s, rel->buckets);
+  RelArgs A = rel_args(g, rel, s, q, key, val, scale, bias, W, W.fwd, ws);
+  A.out = out;
+  A.lse = lse;
+  const int e = lane_elems(s);
+  if (dt == GNN_F32)
+    return e == 8 ? fwd_t<float, 8>(A, W.fwd, st) : fwd_t<float, 4>(A, W.fwd, st);
+  return e == 16 ? fwd_t<__nv_bfloat16, 16>(A, W.fwd, st) : fwd_t<__nv_bfloat16, 8>(A, W.fwd, st);
+}
+
+cudaError_t launch_transformer_rel_backward(const gnn_graph* g, const gnn_rel* rel,
+                                            const Shape& s, gnn_dtype dt, const void* q,
+                                            const void* key, const void* val, float scale,
+                                            const float* bias, const float* lse,
+                                            const void* dout, void* dq, void* dkey, void* dval,
+                                            float* dbias, char* ws, cudaStream_t st) {
+  const RelLayout W = rel_layout(g, s, rel->buckets);
+  RelArgs A = rel_args(g, rel, s, q, key, val, scale, bias, W, W.bwd, ws);
+  A.lse_in = lse;
+  A.dout = dout;
+  A.dq = dq;
+  A.dkey = dkey;
+  A.dval = dval;
+  const int e = lane_elems(s);
+  if (dt == GNN_F32)
+    return e == 8 ? bwd_t<float, 8>(A, g, rel, W.bwd, dbias, st)
+                  : bwd_t<float, 4>(A, g, rel, W.bwd, dbias, st);
+  return e == 16 ? bwd_t<__nv_bfloat16, 16>(A, g, rel, W.bwd, dbias, st)
+                 : bwd_t<__nv_bfloat16, 8>(A, g, rel, W.bwd, dbias, st);
+}
+
+}  // namespace gnn
