@@ -27,7 +27,7 @@ namespace gnn {
 
 constexpr int kNodeCost = 4;   // of a node, in edges: its own rows, its result
 constexpr int kMinSeg = 16;    // units of a worker on small graphs
-constexpr int kWaves = 2;      // segments per resident sub-group on large ones
+constexpr int kWaves = 1;      // segments per resident sub-group on large ones
 
 struct WalkDir {
   const int32_t* ptr;
@@ -59,10 +59,11 @@ __device__ __forceinline__ int nodes_below(const int32_t* ptr, int n, int64_t d)
 __device__ __forceinline__ float part_load(const float* p) { return __ldcg(p); }
 
 // P holds a node's own rows and its partial state:
-//   begin(i, ok)     loads the rows of node i (if ok) and clears the state
+//   begin(i)         loads the rows of node i and clears the state
 //   clear()          clears the state
-//   batch(j, b, f)   adds the edges to j[u] >= 0 with buckets b[u]; calls f()
-//                    once its gathers are on their way
+//   batch(j, b, cnt, f)  adds the edges to j[u] with buckets b[u], u < cnt (the
+//                    others name some node, whose rows may be loaded but enter
+//                    nowhere); calls f() once its gathers are on their way
 //   finish(i)        writes node i's results from the state; the rows of begin(i)
 //                    are still there unless the node has no edges
 //   put(p), take(p)  stores the state, adds a stored one; P::floats(s) of them
@@ -114,13 +115,13 @@ __device__ __forceinline__ void walk(P& p, const Walk& W, const WalkDir& D, cons
   };
 
   int lim = i < i1 ? row_end : e1;  // edges of node i in this segment end here
-  p.begin(i, live);
+  p.begin(i);  // (node 0 where there is no segment)
   int jn[U], bn[U];
   const auto ids = [&](int from) {
 #pragma unroll
     for (int u = 0; u < U; ++u) {
       const bool ok = live && from + u < e1;
-      jn[u] = ok ? __ldg(D.idx + from + u) : -1;
+      jn[u] = ok ? __ldg(D.idx + from + u) : 0;
       bn[u] = with_buckets && ok ? int(__ldg(D.buckets + from + u)) : 0;
     }
   };
@@ -130,11 +131,11 @@ __device__ __forceinline__ void walk(P& p, const Walk& W, const WalkDir& D, cons
     int j[U], b[U];
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-      j[u] = u < cnt ? jn[u] : -1;
+      j[u] = jn[u];
       b[u] = bn[u];
     }
     e += cnt;
-    p.batch(j, b, [&] { ids(e); });
+    p.batch(j, b, cnt, [&] { ids(e); });
     if (live && e == lim) {
       for (;;) {
         if (i == i1) {  // the segment ends inside node i
@@ -156,7 +157,7 @@ __device__ __forceinline__ void walk(P& p, const Walk& W, const WalkDir& D, cons
         ahead = __ldg(D.ptr + (i + 2 < W.n ? i + 2 : W.n));
         lim = i < i1 ? row_end : e1;
         if (lim > e) {
-          p.begin(i, true);
+          p.begin(i);
           break;
         }
         p.clear();  // a node without edges: straight to its result

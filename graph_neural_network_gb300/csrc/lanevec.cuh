@@ -12,14 +12,26 @@ struct RawT {
   uint4 v[kE * int(sizeof(T)) / 16];
 };
 
+// This lane's part of the rows of a tensor: kBytes at a fixed place of every row.
+// (A lane beyond the row's vectors reads the first one, for nothing.)
+template <int kBytes>
+struct LaneRows {
+  const char* base;
+  uint32_t stride;
+  __device__ __forceinline__ LaneRows(const void* p, const Shape& s, const Lane<1>& L)
+      : base(static_cast<const char*>(p) + (L.ok[0] ? L.q[0] * kBytes : 0)),
+        stride(uint32_t(s.rv) * kBytes) {}
+  __device__ __forceinline__ const char* at(int node) const {
+    return base + uint64_t(uint32_t(node)) * stride;
+  }
+};
+
 template <typename T, int kE>
-__device__ __forceinline__ RawT<T, kE> ldT(const void* p, int64_t node, const Shape& s,
-                                           const Lane<1>& L, bool ok) {
+__device__ __forceinline__ RawT<T, kE> ldT(const LaneRows<kE * int(sizeof(T))>& rows, int node) {
   RawT<T, kE> r;
-  constexpr int n = kE * int(sizeof(T)) / 16;
-  const char* at = reinterpret_cast<const char*>(p) + (node * s.rv + L.q[0]) * (kE * sizeof(T));
+  const char* at = rows.at(node);
 #pragma unroll
-  for (int k = 0; k < n; ++k) r.v[k] = ok ? ld16(at + 16 * k) : make_uint4(0, 0, 0, 0);
+  for (int k = 0; k < kE * int(sizeof(T)) / 16; ++k) r.v[k] = ld16(at + 16 * k);
   return r;
 }
 
@@ -40,33 +52,56 @@ __device__ __forceinline__ void storeT(void* p, int64_t node, const Shape& s, co
     st16(at + 16 * k, pack<T>(*reinterpret_cast<const float(*)[V]>(x + V * k)));
 }
 
-// Dot product with a vector held for many edges: bfloat16 stays packed on both
-// sides (every product is exact in float32), float32 is widened already.
+// Dot product of two lane vectors: bfloat16 stays packed on both sides (every
+// product is exact in float32), float32 as it is.
+template <int kE>
+__device__ __forceinline__ float dotT(const RawT<float, kE>& a, const RawT<float, kE>& b) {
+  float x[kE], y[kE];
+  widenT<float, kE>(a, x);
+  widenT<float, kE>(b, y);
+  return dot<kE>(x, y);
+}
+template <int kE>
+__device__ __forceinline__ float dotT(const RawT<__nv_bfloat16, kE>& p,
+                                      const RawT<__nv_bfloat16, kE>& q) {
+  const uint32_t* a = reinterpret_cast<const uint32_t*>(&p);
+  const uint32_t* b = reinterpret_cast<const uint32_t*>(&q);
+  float d0 = 0.f, d1 = 0.f;
+#pragma unroll
+  for (int w = 0; w < kE / 2; ++w)
+    asm("{\n .reg .b16 al, ah, bl, bh;\n mov.b32 {al, ah}, %2;\n mov.b32 {bl, bh}, %3;\n"
+        " fma.rn.f32.bf16 %0, al, bl, %0;\n fma.rn.f32.bf16 %1, ah, bh, %1;\n}"
+        : "+f"(d0), "+f"(d1)
+        : "r"(a[w]), "r"(b[w]));
+  return d0 + d1;
+}
+
+// A lane vector kept in shared memory between its uses, in 16-byte parts of its
+// own (512 bytes apart, one lane's next to the other's): a few registers less.
 template <typename T, int kE>
 struct HeldT {
-  float x[kE];
-  __device__ __forceinline__ void set(const RawT<T, kE>& r) { widenT<T, kE>(r, x); }
-  __device__ __forceinline__ float dot_with(const RawT<T, kE>& r) const {
-    float y[kE];
-    widenT<T, kE>(r, y);
-    return dot<kE>(y, x);
+  static constexpr int kParts = kE * int(sizeof(T)) / 16;
+  static constexpr int kBytes = 512 * kParts;  // of a warp
+  uint32_t at;
+  __device__ __forceinline__ void place(const unsigned char* warp, int lane) {
+    at = uint32_t(__cvta_generic_to_shared(warp)) + 16 * lane;
   }
-};
-template <int kE>
-struct HeldT<__nv_bfloat16, kE> {
-  RawT<__nv_bfloat16, kE> x;
-  __device__ __forceinline__ void set(const RawT<__nv_bfloat16, kE>& r) { x = r; }
-  __device__ __forceinline__ float dot_with(const RawT<__nv_bfloat16, kE>& r) const {
-    const uint32_t* a = reinterpret_cast<const uint32_t*>(&x);
-    const uint32_t* b = reinterpret_cast<const uint32_t*>(&r);
-    float d0 = 0.f, d1 = 0.f;
+  __device__ __forceinline__ void set(const RawT<T, kE>& r) {
 #pragma unroll
-    for (int w = 0; w < kE / 2; ++w)
-      asm("{\n .reg .b16 al, ah, bl, bh;\n mov.b32 {al, ah}, %2;\n mov.b32 {bl, bh}, %3;\n"
-          " fma.rn.f32.bf16 %0, al, bl, %0;\n fma.rn.f32.bf16 %1, ah, bh, %1;\n}"
-          : "+f"(d0), "+f"(d1)
-          : "r"(a[w]), "r"(b[w]));
-    return d0 + d1;
+    for (int k = 0; k < kParts; ++k)
+      asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(at + 512 * k), "r"(r.v[k].x),
+                   "r"(r.v[k].y), "r"(r.v[k].z), "r"(r.v[k].w)
+                   : "memory");
+  }
+  __device__ __forceinline__ RawT<T, kE> get() const {
+    RawT<T, kE> r;
+#pragma unroll
+    for (int k = 0; k < kParts; ++k)
+      asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+                   : "=r"(r.v[k].x), "=r"(r.v[k].y), "=r"(r.v[k].z), "=r"(r.v[k].w)
+                   : "r"(at + 512 * k)
+                   : "memory");
+    return r;
   }
 };
 

@@ -14,29 +14,6 @@ __device__ __forceinline__ float* stage_bias(const float* bias, int entries, uns
   return t;
 }
 
-// Buckets of the edges batch_ids() takes (0 past the end).
-template <int U>
-__device__ __forceinline__ void batch_buckets(const uint8_t* rb, int beg, int end, int g, int G,
-                                              int (&b)[U]) {
-#pragma unroll
-  for (int u = 0; u < U; ++u) {
-    const int e = beg + u * G + g;
-    b[u] = e < end ? int(__ldg(rb + e)) : 0;
-  }
-}
-
-// This lane's bias of each edge of the batch; edges that -infinity masks for
-// its head become absent.
-template <int U>
-__device__ __forceinline__ void edge_bias(const float* sb, const Shape& s, const Lane<1>& L,
-                                          const int (&b)[U], int (&j)[U], float (&bs)[U]) {
-#pragma unroll
-  for (int u = 0; u < U; ++u) {
-    bs[u] = sb[b[u] * s.H + L.k[0]];
-    if (bs[u] == -INFINITY) j[u] = -1;
-  }
-}
-
 // Gradient tables: per warp [buckets][32 / hv] floats, the column a lane's head
 // group, so that the lanes leading a head add without atomics or conflicts.
 __host__ __device__ inline size_t grad_tables_bytes(const Shape& s, int buckets) {

@@ -55,24 +55,29 @@ struct Raw8 {
 };
 
 template <int kE>
-__device__ __forceinline__ Raw8<kE> ld8(const int8_t* p, int64_t node, const Shape& s,
-                                        const Lane<1>& L, bool ok) {
+__device__ __forceinline__ Raw8<kE> ld8(const LaneRows<kE>& rows, int node) {
   Raw8<kE> r;
-  const int8_t* at = p + (node * s.rv + L.q[0]) * kE;
+  const char* at = rows.at(node);
   if constexpr (kE == 16) {
-    const uint4 t = ok ? ld16(at) : make_uint4(0, 0, 0, 0);
+    const uint4 t = ld16(at);
     r.w[0] = t.x;
     r.w[1] = t.y;
     r.w[2] = t.z;
     r.w[3] = t.w;
   } else if constexpr (kE == 8) {
-    const uint2 t = ok ? __ldg(reinterpret_cast<const uint2*>(at)) : make_uint2(0, 0);
+    const uint2 t = __ldg(reinterpret_cast<const uint2*>(at));
     r.w[0] = t.x;
     r.w[1] = t.y;
   } else {
-    r.w[0] = ok ? __ldg(reinterpret_cast<const uint32_t*>(at)) : 0u;
+    r.w[0] = __ldg(reinterpret_cast<const uint32_t*>(at));
   }
   return r;
+}
+
+// The number of head k (base points to it) of a node in a [N][H] array.
+template <typename X>
+__device__ __forceinline__ X of_head(const X* base, int node, const Shape& s) {
+  return __ldg(base + uint64_t(uint32_t(node)) * uint32_t(s.H));
 }
 
 template <int kE>
@@ -106,7 +111,8 @@ struct DstPass {
   static constexpr bool kBuckets = kRel;
   const T8Args& A;
   const Lane<1>& L;
-  const float* sb;
+  const LaneRows<kE> r0, r1;  // the gathered rows
+  const float* sb;            // the bias table
   // the node
   Raw8<kE> q8;
   float qsc;        // qs_i
@@ -114,7 +120,8 @@ struct DstPass {
   // its sums; m is in base 2
   float m, l, d, P[kE], Q[kE];
 
-  __device__ __forceinline__ DstPass(const T8Args& a, const Lane<1>& lane) : A(a), L(lane) {}
+  __device__ __forceinline__ DstPass(const T8Args& a, const Lane<1>& lane)
+      : A(a), L(lane), r0(a.k8, a.s, lane), r1(a.v8, a.s, lane) {}
   // floats of a partial state: P, Q, then m, l, d per head
   static __host__ __device__ int floats(const Shape& s) { return 2 * s.rv * kE + 3 * s.H; }
 
@@ -124,11 +131,10 @@ struct DstPass {
     zero<kE>(P);
     zero<kE>(Q);
   }
-  __device__ __forceinline__ void begin(int i, bool ok) {
-    ok = ok && L.ok[0];
-    q8 = ld8<kE>(A.q8, i, A.s, L, ok);
-    qsc = ok ? __ldg(A.qs + int64_t(i) * A.s.H + L.k[0]) : 0.f;
-    widenT<T, kE>(ldT<T, kE>(A.dout, i, A.s, L, ok), g);
+  __device__ __forceinline__ void begin(int i) {
+    q8 = ld8<kE>(LaneRows<kE>(A.q8, A.s, L), i);
+    qsc = of_head(A.qs + L.k[0], i, A.s);
+    widenT<T, kE>(ldT<T, kE>(LaneRows<kE * int(sizeof(T))>(A.dout, A.s, L), i), g);
     clear();
   }
   __device__ __forceinline__ void rescale(float mn) {
@@ -141,22 +147,26 @@ struct DstPass {
   }
 
   template <class F>
-  __device__ __forceinline__ void batch(int (&j)[U], const int (&b)[U], const F& sent) {
-    const int H = A.s.H;
-    const float qk = qsc * A.scale2;
-    float bs[U];
-    if (kRel) edge_bias<U>(sb, A.s, L, b, j, bs);
+  __device__ __forceinline__ void batch(const int (&j)[U], const int (&b)[U], int cnt,
+                                        const F& sent) {
     Raw8<kE> rk[U], rv[U];
     float ks[U], vs[U];
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-      const bool ok = j[u] >= 0 && L.ok[0];
-      rk[u] = ld8<kE>(A.k8, j[u], A.s, L, ok);
-      rv[u] = ld8<kE>(A.v8, j[u], A.s, L, ok);
-      ks[u] = ok ? __ldg(A.ks + int64_t(j[u]) * H + L.k[0]) : 0.f;
-      vs[u] = ok ? __ldg(A.vs + int64_t(j[u]) * H + L.k[0]) : 0.f;
+      rk[u] = ld8<kE>(r0, j[u]);
+      rv[u] = ld8<kE>(r1, j[u]);
+      ks[u] = of_head(A.ks + L.k[0], j[u], A.s);
+      vs[u] = of_head(A.vs + L.k[0], j[u], A.s);
     }
     sent();
+    float bs[U];
+    bool ok[U];  // there, and not masked for the lane's head
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      bs[u] = kRel ? sb[b[u] * A.s.H] : 0.f;
+      ok[u] = u < cnt && (!kRel || bs[u] != -INFINITY);
+    }
+    const float qk = qsc * A.scale2;
     float red[2 * U];
 #pragma unroll
     for (int u = 0; u < U; ++u) {
@@ -170,16 +180,16 @@ struct DstPass {
 #pragma unroll
     for (int u = 0; u < U; ++u) {
       red[u] = kRel ? fmaf(red[u], qk * ks[u], bs[u]) : red[u] * (qk * ks[u]);
-      if (j[u] < 0) red[u] = -INFINITY;
+      if (!ok[u]) red[u] = -INFINITY;
       top = fmaxf(top, red[u]);
     }
     if (top > m) rescale(top);
     const float mr = m == -INFINITY ? 0.f : m;
 #pragma unroll
     for (int u = 0; u < U; ++u) {
+      if (!ok[u]) continue;
       const float p = ex2(red[u] - mr);
-      // an absent edge may face an own row that holds anything
-      const float pd = j[u] < 0 ? 0.f : p * (red[U + u] * vs[u]);
+      const float pd = p * (red[U + u] * vs[u]);
       l += p;
       d += pd;
       float x[kE];
@@ -252,46 +262,52 @@ struct SrcPass {
   static constexpr bool kBuckets = kRel;
   const T8Args& A;
   const Lane<1>& L;
-  const float* sb;
+  const LaneRows<kE> r0;      // the gathered rows
+  const LaneRows<kE * int(sizeof(T))> r1;
+  const float* sb;            // the bias table
   float* hist;      // this lane's column of its warp's gradient table
   Raw8<kE> k8;
   float ksc, vsc;
   float v[kE];      // v8_j as floats
   float dk[kE], dv[kE];
 
-  __device__ __forceinline__ SrcPass(const T8Args& a, const Lane<1>& lane) : A(a), L(lane) {}
+  __device__ __forceinline__ SrcPass(const T8Args& a, const Lane<1>& lane)
+      : A(a), L(lane), r0(a.q8, a.s, lane), r1(a.dout, a.s, lane) {}
   static __host__ __device__ int floats(const Shape& s) { return 2 * s.rv * kE; }
 
   __device__ __forceinline__ void clear() {
     zero<kE>(dk);
     zero<kE>(dv);
   }
-  __device__ __forceinline__ void begin(int j, bool ok) {
-    ok = ok && L.ok[0];
-    k8 = ld8<kE>(A.k8, j, A.s, L, ok);
-    widen<kE>(ld8<kE>(A.v8, j, A.s, L, ok), v);
-    ksc = ok ? __ldg(A.ks + int64_t(j) * A.s.H + L.k[0]) : 0.f;
-    vsc = ok ? __ldg(A.vs + int64_t(j) * A.s.H + L.k[0]) : 0.f;
+  __device__ __forceinline__ void begin(int j) {
+    k8 = ld8<kE>(LaneRows<kE>(A.k8, A.s, L), j);
+    widen<kE>(ld8<kE>(LaneRows<kE>(A.v8, A.s, L), j), v);
+    ksc = of_head(A.ks + L.k[0], j, A.s);
+    vsc = of_head(A.vs + L.k[0], j, A.s);
     clear();
   }
 
   template <class F>
-  __device__ __forceinline__ void batch(int (&i)[U], const int (&b)[U], const F& sent) {
-    const int H = A.s.H;
-    const float kq = ksc * A.scale2;
-    float bs[U];
-    if (kRel) edge_bias<U>(sb, A.s, L, b, i, bs);
+  __device__ __forceinline__ void batch(const int (&i)[U], const int (&b)[U], int cnt,
+                                        const F& sent) {
     Raw8<kE> rq[U];
     RawT<T, kE> rg[U];
     float4 st[U];
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-      const bool ok = i[u] >= 0 && L.ok[0];
-      rq[u] = ld8<kE>(A.q8, i[u], A.s, L, ok);
-      rg[u] = ldT<T, kE>(A.dout, i[u], A.s, L, ok);
-      st[u] = ok ? ld16f(A.stats + int64_t(i[u]) * H + L.k[0]) : make_float4(0.f, 0.f, 0.f, 0.f);
+      rq[u] = ld8<kE>(r0, i[u]);
+      rg[u] = ldT<T, kE>(r1, i[u]);
+      st[u] = of_head(A.stats + L.k[0], i[u], A.s);
     }
     sent();
+    float bs[U];
+    bool ok[U];  // there, and not masked for the lane's head
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      bs[u] = kRel ? sb[b[u] * A.s.H] : 0.f;
+      ok[u] = u < cnt && (!kRel || bs[u] != -INFINITY);
+    }
+    const float kq = ksc * A.scale2;
     float red[2 * U];
 #pragma unroll
     for (int u = 0; u < U; ++u) {
@@ -304,9 +320,10 @@ struct SrcPass {
 #pragma unroll
     for (int u = 0; u < U; ++u) {
       const float e = kRel ? fmaf(red[u], kq * st[u].z, bs[u]) : red[u] * (kq * st[u].z);
-      const float al = i[u] >= 0 ? ex2(e - st[u].x) : 0.f;
-      const float de = i[u] >= 0 ? al * fmaf(red[U + u], vsc, -st[u].y) : 0.f;
-      if (kRel && i[u] >= 0 && L.head_leader(A.s, 0)) add_grad(hist, A.s, b[u], de);
+      if (!ok[u]) continue;
+      const float al = ex2(e - st[u].x);
+      const float de = al * fmaf(red[U + u], vsc, -st[u].y);
+      if (kRel && L.head_leader(A.s, 0)) add_grad(hist, A.s, b[u], de);
       float x[kE];
       widen<kE>(rq[u], x);
       axpy<kE>(dk, de * A.scale * st[u].z, x);
@@ -343,7 +360,7 @@ __global__ void __launch_bounds__(kThreads, kPerSm) t8_dst(const __grid_constant
   extern __shared__ __align__(16) unsigned char smem[];
   const Lane<1> L(A.s);
   DstPass<T, kE, kRel> p(A, L);
-  p.sb = kRel ? stage_bias(A.bias, A.buckets * A.s.H, smem) : nullptr;
+  p.sb = kRel ? stage_bias(A.bias, A.buckets * A.s.H, smem) + L.k[0] : nullptr;
   walk(p, A.walk, A.dir, A.s, L);
 }
 
@@ -358,7 +375,7 @@ __global__ void __launch_bounds__(kThreads, kPerSm) t8_src(const __grid_constant
   if (kRel) {
     tables = reinterpret_cast<float*>(smem) + A.buckets * A.s.H;
     p.hist = clear_grad_tables(tables, A.s, L, A.buckets);
-    p.sb = stage_bias(A.bias, A.buckets * A.s.H, smem);
+    p.sb = stage_bias(A.bias, A.buckets * A.s.H, smem) + L.k[0];
   }
   walk(p, A.walk, A.dir, A.s, L);
   if (kRel) fold_grad_tables(tables, A.s, L, A.buckets, A.db_part);

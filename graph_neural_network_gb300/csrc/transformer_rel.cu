@@ -3,9 +3,8 @@
 //   e_ij = scale * q_i[k] . key_j[k] + bias[b_ij][k],
 // the bucket b_ij read next to the edge's node id from the prepared bucket bytes
 // (relpos.cu) of the direction being walked, and the bias table in shared
-// memory.  An entry of -infinity masks its edges for that head: the lane treats
-// them as absent, so it neither gathers their rows (which may hold anything) nor
-// adds them to a sum.
+// memory.  An entry of -infinity masks its edges for that head: the lanes of the head
+// skip them like absent ones, so what their rows hold enters no sum.
 //
 // Forward: one pass over the CSR with an online softmax whose reference moves
 // only when a score passes it.  Backward pass 1 (CSR): Delta, P = sum alpha da
@@ -56,14 +55,17 @@ template <typename T, int kE_>
 struct RelFwd {
   static constexpr int kE = kE_;
   static constexpr int U = RelUnroll<T, kE>::value;
+  using Rows = LaneRows<kE * int(sizeof(T))>;
   static constexpr bool kBuckets = true;
   const RelArgs& A;
   const Lane<1>& L;
-  const float* sb;
+  const Rows r0, r1;  // the gathered rows
+  const float* sb;    // the bias table
   HeldT<T, kE> q;
   float m, l, acc[kE];  // m in base 2
 
-  __device__ __forceinline__ RelFwd(const RelArgs& a, const Lane<1>& lane) : A(a), L(lane) {}
+  __device__ __forceinline__ RelFwd(const RelArgs& a, const Lane<1>& lane)
+      : A(a), L(lane), r0(a.key, a.s, lane), r1(a.val, a.s, lane) {}
   static __host__ __device__ int floats(const Shape& s) { return s.rv * kE + 2 * s.H; }
 
   __device__ __forceinline__ void clear() {
@@ -71,30 +73,36 @@ struct RelFwd {
     l = 0.f;
     zero<kE>(acc);
   }
-  __device__ __forceinline__ void begin(int i, bool ok) {
-    q.set(ldT<T, kE>(A.q, i, A.s, L, ok && L.ok[0]));
+  __device__ __forceinline__ void begin(int i) {
+    q.set(ldT<T, kE>(Rows(A.q, A.s, L), i));
     clear();
   }
   template <class F>
-  __device__ __forceinline__ void batch(int (&j)[U], const int (&b)[U], const F& sent) {
-    float bs[U];
-    edge_bias<U>(sb, A.s, L, b, j, bs);
+  __device__ __forceinline__ void batch(const int (&j)[U], const int (&b)[U], int cnt,
+                                        const F& sent) {
     RawT<T, kE> rk[U], rv[U];
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-      const bool ok = j[u] >= 0 && L.ok[0];
-      rk[u] = ldT<T, kE>(A.key, j[u], A.s, L, ok);
-      rv[u] = ldT<T, kE>(A.val, j[u], A.s, L, ok);
+      rk[u] = ldT<T, kE>(r0, j[u]);
+      rv[u] = ldT<T, kE>(r1, j[u]);
     }
     sent();
-    float sc[U];
+    float bs[U];
+    bool ok[U];  // there, and not masked for the lane's head
 #pragma unroll
-    for (int u = 0; u < U; ++u) sc[u] = q.dot_with(rk[u]);
+    for (int u = 0; u < U; ++u) {
+      bs[u] = sb[b[u] * A.s.H];
+      ok[u] = u < cnt && bs[u] != -INFINITY;
+    }
+    float sc[U];
+    const RawT<T, kE> own = q.get();
+#pragma unroll
+    for (int u = 0; u < U; ++u) sc[u] = dotT<kE>(own, rk[u]);
     head_sums<U>(sc, A.s.hv_log2);
     float top = m;
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-      sc[u] = j[u] >= 0 ? fmaf(sc[u], A.scale2, bs[u]) : -INFINITY;
+      sc[u] = ok[u] ? fmaf(sc[u], A.scale2, bs[u]) : -INFINITY;
       top = fmaxf(top, sc[u]);
     }
     if (top > m) {
@@ -106,6 +114,7 @@ struct RelFwd {
     const float mr = m == -INFINITY ? 0.f : m;
 #pragma unroll
     for (int u = 0; u < U; ++u) {
+      if (!ok[u]) continue;
       const float p = ex2(sc[u] - mr);
       l += p;
       float x[kE];
@@ -149,14 +158,17 @@ template <typename T, int kE_>
 struct RelDst {
   static constexpr int kE = kE_;
   static constexpr int U = RelUnroll<T, kE>::value;
+  using Rows = LaneRows<kE * int(sizeof(T))>;
   static constexpr bool kBuckets = true;
   const RelArgs& A;
   const Lane<1>& L;
-  const float* sb;
+  const Rows r0, r1;  // the gathered rows
+  const float* sb;    // the bias table
   HeldT<T, kE> q, g;
   float lse2, delta, P[kE], Q[kE];
 
-  __device__ __forceinline__ RelDst(const RelArgs& a, const Lane<1>& lane) : A(a), L(lane) {}
+  __device__ __forceinline__ RelDst(const RelArgs& a, const Lane<1>& lane)
+      : A(a), L(lane), r0(a.key, a.s, lane), r1(a.val, a.s, lane) {}
   static __host__ __device__ int floats(const Shape& s) { return 2 * s.rv * kE + s.H; }
 
   __device__ __forceinline__ void clear() {
@@ -164,36 +176,46 @@ struct RelDst {
     zero<kE>(P);
     zero<kE>(Q);
   }
-  __device__ __forceinline__ void begin(int i, bool ok) {
-    q.set(ldT<T, kE>(A.q, i, A.s, L, ok && L.ok[0]));
-    g.set(ldT<T, kE>(A.dout, i, A.s, L, ok && L.ok[0]));
-    lse2 = ok && L.ok[0] ? __ldg(A.lse_in + int64_t(i) * A.s.H + L.k[0]) * kLog2e : 0.f;
+  __device__ __forceinline__ void begin(int i) {
+    q.set(ldT<T, kE>(Rows(A.q, A.s, L), i));
+    g.set(ldT<T, kE>(Rows(A.dout, A.s, L), i));
+    lse2 = __ldg(A.lse_in + int64_t(i) * A.s.H + L.k[0]) * kLog2e;
     clear();
   }
   template <class F>
-  __device__ __forceinline__ void batch(int (&j)[U], const int (&b)[U], const F& sent) {
-    float bs[U];
-    edge_bias<U>(sb, A.s, L, b, j, bs);
+  __device__ __forceinline__ void batch(const int (&j)[U], const int (&b)[U], int cnt,
+                                        const F& sent) {
     RawT<T, kE> rk[U], rv[U];
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-      const bool ok = j[u] >= 0 && L.ok[0];
-      rk[u] = ldT<T, kE>(A.key, j[u], A.s, L, ok);
-      rv[u] = ldT<T, kE>(A.val, j[u], A.s, L, ok);
+      rk[u] = ldT<T, kE>(r0, j[u]);
+      rv[u] = ldT<T, kE>(r1, j[u]);
     }
     sent();
-    float red[2 * U];
+    float bs[U];
+    bool ok[U];  // there, and not masked for the lane's head
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-      red[u] = q.dot_with(rk[u]);
-      red[U + u] = g.dot_with(rv[u]);
+      bs[u] = sb[b[u] * A.s.H];
+      ok[u] = u < cnt && bs[u] != -INFINITY;
+    }
+    float red[2 * U];
+    {
+      const RawT<T, kE> own = g.get();
+#pragma unroll
+      for (int u = 0; u < U; ++u) red[U + u] = dotT<kE>(own, rv[u]);
+    }
+    {
+      const RawT<T, kE> own = q.get();
+#pragma unroll
+      for (int u = 0; u < U; ++u) red[u] = dotT<kE>(own, rk[u]);
     }
     head_sums<2 * U>(red, A.s.hv_log2);
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-      // an absent edge may face an own row that holds anything
-      const float al = j[u] >= 0 ? ex2(fmaf(red[u], A.scale2, bs[u]) - lse2) : 0.f;
-      const float ad = j[u] >= 0 ? al * red[U + u] : 0.f;
+      if (!ok[u]) continue;
+      const float al = ex2(fmaf(red[u], A.scale2, bs[u]) - lse2);
+      const float ad = al * red[U + u];
       delta += ad;
       float x[kE];
       widenT<T, kE>(rk[u], x);
@@ -234,52 +256,66 @@ template <typename T, int kE_>
 struct RelSrc {
   static constexpr int kE = kE_;
   static constexpr int U = RelUnroll<T, kE>::value;
+  using Rows = LaneRows<kE * int(sizeof(T))>;
   static constexpr bool kBuckets = true;
   const RelArgs& A;
   const Lane<1>& L;
-  const float* sb;
+  const Rows r0, r1;  // the gathered rows
+  const float* sb;    // the bias table
   float* hist;  // this lane's column of its warp's gradient table
   HeldT<T, kE> k, v;
   float dk[kE], dv[kE];
 
-  __device__ __forceinline__ RelSrc(const RelArgs& a, const Lane<1>& lane) : A(a), L(lane) {}
+  __device__ __forceinline__ RelSrc(const RelArgs& a, const Lane<1>& lane)
+      : A(a), L(lane), r0(a.q, a.s, lane), r1(a.dout, a.s, lane) {}
   static __host__ __device__ int floats(const Shape& s) { return 2 * s.rv * kE; }
 
   __device__ __forceinline__ void clear() {
     zero<kE>(dk);
     zero<kE>(dv);
   }
-  __device__ __forceinline__ void begin(int j, bool ok) {
-    k.set(ldT<T, kE>(A.key, j, A.s, L, ok && L.ok[0]));
-    v.set(ldT<T, kE>(A.val, j, A.s, L, ok && L.ok[0]));
+  __device__ __forceinline__ void begin(int j) {
+    k.set(ldT<T, kE>(Rows(A.key, A.s, L), j));
+    v.set(ldT<T, kE>(Rows(A.val, A.s, L), j));
     clear();
   }
   template <class F>
-  __device__ __forceinline__ void batch(int (&i)[U], const int (&b)[U], const F& sent) {
-    float bs[U];
-    edge_bias<U>(sb, A.s, L, b, i, bs);
+  __device__ __forceinline__ void batch(const int (&i)[U], const int (&b)[U], int cnt,
+                                        const F& sent) {
     RawT<T, kE> rq[U], rg[U];
     float2 st[U];
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-      const bool ok = i[u] >= 0 && L.ok[0];
-      rq[u] = ldT<T, kE>(A.q, i[u], A.s, L, ok);
-      rg[u] = ldT<T, kE>(A.dout, i[u], A.s, L, ok);
-      st[u] = ok ? __ldg(A.stats + int64_t(i[u]) * A.s.H + L.k[0]) : make_float2(0.f, 0.f);
+      rq[u] = ldT<T, kE>(r0, i[u]);
+      rg[u] = ldT<T, kE>(r1, i[u]);
+      st[u] = __ldg(A.stats + L.k[0] + uint64_t(uint32_t(i[u])) * uint32_t(A.s.H));
     }
     sent();
-    float red[2 * U];
+    float bs[U];
+    bool ok[U];  // there, and not masked for the lane's head
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-      red[u] = k.dot_with(rq[u]);
-      red[U + u] = v.dot_with(rg[u]);
+      bs[u] = sb[b[u] * A.s.H];
+      ok[u] = u < cnt && bs[u] != -INFINITY;
+    }
+    float red[2 * U];
+    {
+      const RawT<T, kE> own = k.get();
+#pragma unroll
+      for (int u = 0; u < U; ++u) red[u] = dotT<kE>(own, rq[u]);
+    }
+    {
+      const RawT<T, kE> own = v.get();
+#pragma unroll
+      for (int u = 0; u < U; ++u) red[U + u] = dotT<kE>(own, rg[u]);
     }
     head_sums<2 * U>(red, A.s.hv_log2);
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-      const float al = i[u] >= 0 ? ex2(fmaf(red[u], A.scale2, bs[u]) - st[u].x) : 0.f;
-      const float de = i[u] >= 0 ? al * (red[U + u] - st[u].y) : 0.f;
-      if (i[u] >= 0 && L.head_leader(A.s, 0)) add_grad(hist, A.s, b[u], de);
+      if (!ok[u]) continue;
+      const float al = ex2(fmaf(red[u], A.scale2, bs[u]) - st[u].x);
+      const float de = al * (red[U + u] - st[u].y);
+      if (L.head_leader(A.s, 0)) add_grad(hist, A.s, b[u], de);
       float x[kE];
       widenT<T, kE>(rq[u], x);
       axpy<kE>(dk, de, x);
@@ -318,8 +354,10 @@ template <typename T, int kE>
 __global__ void __launch_bounds__(kThreads, kFwdPerSm) rel_fwd(const __grid_constant__ RelArgs A) {
   extern __shared__ __align__(16) unsigned char smem[];
   const Lane<1> L(A.s);
+  __shared__ __align__(16) unsigned char held[kWarps * HeldT<T, kE>::kBytes];
   RelFwd<T, kE> p(A, L);
-  p.sb = stage_bias(A.bias, A.buckets * A.s.H, smem);
+  p.q.place(held + (threadIdx.x >> 5) * HeldT<T, kE>::kBytes, L.lane);
+  p.sb = stage_bias(A.bias, A.buckets * A.s.H, smem) + L.k[0];
   walk(p, A.walk, A.dir, A.s, L);
 }
 
@@ -327,8 +365,11 @@ template <typename T, int kE>
 __global__ void __launch_bounds__(kThreads, kBwdPerSm) rel_dst(const __grid_constant__ RelArgs A) {
   extern __shared__ __align__(16) unsigned char smem[];
   const Lane<1> L(A.s);
+  __shared__ __align__(16) unsigned char held[2 * kWarps * HeldT<T, kE>::kBytes];
   RelDst<T, kE> p(A, L);
-  p.sb = stage_bias(A.bias, A.buckets * A.s.H, smem);
+  p.q.place(held + (threadIdx.x >> 5) * HeldT<T, kE>::kBytes, L.lane);
+  p.g.place(held + (kWarps + (threadIdx.x >> 5)) * HeldT<T, kE>::kBytes, L.lane);
+  p.sb = stage_bias(A.bias, A.buckets * A.s.H, smem) + L.k[0];
   walk(p, A.walk, A.dir, A.s, L);
 }
 
@@ -336,10 +377,13 @@ template <typename T, int kE>
 __global__ void __launch_bounds__(kThreads, kBwdPerSm) rel_src(const __grid_constant__ RelArgs A) {
   extern __shared__ __align__(16) unsigned char smem[];
   const Lane<1> L(A.s);
+  __shared__ __align__(16) unsigned char held[2 * kWarps * HeldT<T, kE>::kBytes];
   RelSrc<T, kE> p(A, L);
+  p.k.place(held + (threadIdx.x >> 5) * HeldT<T, kE>::kBytes, L.lane);
+  p.v.place(held + (kWarps + (threadIdx.x >> 5)) * HeldT<T, kE>::kBytes, L.lane);
   float* tables = reinterpret_cast<float*>(smem) + A.buckets * A.s.H;
   p.hist = clear_grad_tables(tables, A.s, L, A.buckets);
-  p.sb = stage_bias(A.bias, A.buckets * A.s.H, smem);
+  p.sb = stage_bias(A.bias, A.buckets * A.s.H, smem) + L.k[0];
   walk(p, A.walk, A.dir, A.s, L);
   fold_grad_tables(tables, A.s, L, A.buckets, A.db_part);
 }
@@ -395,7 +439,8 @@ RelLayout rel_layout(const gnn_graph* g, const Shape& s, int buckets) {
 template <typename K>
 cudaError_t launch(K kernel, const RelArgs& A, int blocks, size_t smem, cudaStream_t st) {
   cudaError_t e;
-  if (smem > 48 * 1024 &&
+  // (the default limit, 48 KB, counts the kernels' static 16 KB too)
+  if (smem > 32 * 1024 &&
       (e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, int(smem))) !=
           cudaSuccess)
     return e;
