@@ -63,7 +63,8 @@ __device__ __forceinline__ float part_load(const float* p) { return __ldcg(p); }
 //   clear()          clears the state
 //   batch(j, b, cnt, f)  adds the edges to j[u] with buckets b[u], u < cnt (the
 //                    others name some node, whose rows may be loaded but enter
-//                    nowhere); calls f() once its gathers are on their way
+//                    nowhere); calls f(), which overwrites j and b, once its
+//                    gathers are on their way
 //   finish(i)        writes node i's results from the state; the rows of begin(i)
 //                    are still there unless the node has no edges
 //   put(p), take(p)  stores the state, adds a stored one; P::floats(s) of them
@@ -71,7 +72,6 @@ template <class P>
 __device__ __forceinline__ void walk(P& p, const Walk& W, const WalkDir& D, const Shape& s,
                                      const Lane<1>& L) {
   constexpr int U = P::U;
-  const bool with_buckets = P::kBuckets;
   const int64_t worker = (int64_t(blockIdx.x) * kWarps + (threadIdx.x >> 5)) * L.G + L.g;
   const int64_t d0 = worker * W.seg < W.total ? worker * W.seg : W.total;
   const int64_t d1 = d0 + W.seg < W.total ? d0 + W.seg : W.total;
@@ -116,26 +116,28 @@ __device__ __forceinline__ void walk(P& p, const Walk& W, const WalkDir& D, cons
 
   int lim = i < i1 ? row_end : e1;  // edges of node i in this segment end here
   p.begin(i);  // (node 0 where there is no segment)
+  // Node ids (and buckets) of the next batch: the segment's next U edges, also
+  // where they belong to the next node.
   int jn[U], bn[U];
-  const auto ids = [&](int from) {
+  const int32_t* ip = D.idx + e;
+  const uint8_t* bp = P::kBuckets ? D.buckets + e : nullptr;
+  int left = live ? e1 - e : 0;
+  const auto ids = [&] {
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-      const bool ok = live && from + u < e1;
-      jn[u] = ok ? __ldg(D.idx + from + u) : 0;
-      bn[u] = with_buckets && ok ? int(__ldg(D.buckets + from + u)) : 0;
+      jn[u] = u < left ? __ldg(ip + u) : 0;
+      if (P::kBuckets) bn[u] = u < left ? int(__ldg(bp + u)) : 0;
     }
   };
-  ids(e);
+  ids();
   while (__any_sync(kFull, live)) {
-    const int cnt = live ? (lim - e < U ? lim - e : U) : 0;
-    int j[U], b[U];
-#pragma unroll
-    for (int u = 0; u < U; ++u) {
-      j[u] = jn[u];
-      b[u] = bn[u];
-    }
+    const int rest = lim - e;
+    const int cnt = live ? (rest < U ? rest : U) : 0;
     e += cnt;
-    p.batch(j, b, cnt, [&] { ids(e); });
+    ip += cnt;
+    if (P::kBuckets) bp += cnt;
+    left -= cnt;
+    p.batch(jn, bn, cnt, ids);
     if (live && e == lim) {
       for (;;) {
         if (i == i1) {  // the segment ends inside node i

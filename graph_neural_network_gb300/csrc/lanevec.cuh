@@ -15,21 +15,30 @@ struct RawT {
 // This lane's part of the rows of a tensor: kBytes at a fixed place of every row.
 // (A lane beyond the row's vectors reads the first one, for nothing.)
 template <int kBytes>
+struct LanePlace {
+  uint32_t off, stride;
+  __device__ __forceinline__ LanePlace(const Shape& s, const Lane<1>& L)
+      : off(L.ok[0] ? uint32_t(L.q[0]) * kBytes : 0u), stride(uint32_t(s.rv) * kBytes) {}
+  // the same place of another tensor's row
+  __device__ __forceinline__ const char* of(const void* p, int node) const {
+    return static_cast<const char*>(p) + (uint64_t(uint32_t(node)) * stride + off);
+  }
+};
+// ... of one tensor that is gathered.
+template <int kBytes>
 struct LaneRows {
   const char* base;
   uint32_t stride;
-  __device__ __forceinline__ LaneRows(const void* p, const Shape& s, const Lane<1>& L)
-      : base(static_cast<const char*>(p) + (L.ok[0] ? L.q[0] * kBytes : 0)),
-        stride(uint32_t(s.rv) * kBytes) {}
+  __device__ __forceinline__ LaneRows(const void* p, const LanePlace<kBytes>& at)
+      : base(static_cast<const char*>(p) + at.off), stride(at.stride) {}
   __device__ __forceinline__ const char* at(int node) const {
     return base + uint64_t(uint32_t(node)) * stride;
   }
 };
 
 template <typename T, int kE>
-__device__ __forceinline__ RawT<T, kE> ldT(const LaneRows<kE * int(sizeof(T))>& rows, int node) {
+__device__ __forceinline__ RawT<T, kE> ldT(const char* at) {
   RawT<T, kE> r;
-  const char* at = rows.at(node);
 #pragma unroll
   for (int k = 0; k < kE * int(sizeof(T)) / 16; ++k) r.v[k] = ld16(at + 16 * k);
   return r;
@@ -43,10 +52,8 @@ __device__ __forceinline__ void widenT(const RawT<T, kE>& r, float (&x)[kE]) {
 }
 
 template <typename T, int kE>
-__device__ __forceinline__ void storeT(void* p, int64_t node, const Shape& s, const Lane<1>& L,
-                                       const float (&x)[kE]) {
+__device__ __forceinline__ void storeT(char* at, const float (&x)[kE]) {
   constexpr int V = VecOf<T>::n;
-  char* at = reinterpret_cast<char*>(p) + (node * s.rv + L.q[0]) * (kE * sizeof(T));
 #pragma unroll
   for (int k = 0; k < kE / V; ++k)
     st16(at + 16 * k, pack<T>(*reinterpret_cast<const float(*)[V]>(x + V * k)));
@@ -76,8 +83,10 @@ __device__ __forceinline__ float dotT(const RawT<__nv_bfloat16, kE>& p,
   return d0 + d1;
 }
 
-// A lane vector kept in shared memory between its uses, in 16-byte parts of its
-// own (512 bytes apart, one lane's next to the other's): a few registers less.
+// A lane vector of a node's own row kept in shared memory, in 16-byte parts of the
+// lane's own (512 bytes apart, one lane's next to the other's): copied there
+// asynchronously, so that the change of nodes waits for nothing, and no
+// registers between its uses.
 template <typename T, int kE>
 struct HeldT {
   static constexpr int kParts = kE * int(sizeof(T)) / 16;
@@ -86,13 +95,14 @@ struct HeldT {
   __device__ __forceinline__ void place(const unsigned char* warp, int lane) {
     at = uint32_t(__cvta_generic_to_shared(warp)) + 16 * lane;
   }
-  __device__ __forceinline__ void set(const RawT<T, kE>& r) {
+  __device__ __forceinline__ void fetch(const char* from) {
 #pragma unroll
     for (int k = 0; k < kParts; ++k)
-      asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(at + 512 * k), "r"(r.v[k].x),
-                   "r"(r.v[k].y), "r"(r.v[k].z), "r"(r.v[k].w)
+      asm volatile("cp.async.ca.shared.global [%0], [%1], 16;" ::"r"(at + 512 * k),
+                   "l"(from + 16 * k)
                    : "memory");
   }
+  // after held_ready()
   __device__ __forceinline__ RawT<T, kE> get() const {
     RawT<T, kE> r;
 #pragma unroll
@@ -104,6 +114,9 @@ struct HeldT {
     return r;
   }
 };
+
+// Waits for this lane's copies.
+__device__ __forceinline__ void held_ready() { asm volatile("cp.async.wait_all;" ::: "memory"); }
 
 // The geometry of rows of s in vectors of e elements (a power of two dividing D).
 inline Shape lane_shape(const Shape& s, int e) {

@@ -55,9 +55,8 @@ struct Raw8 {
 };
 
 template <int kE>
-__device__ __forceinline__ Raw8<kE> ld8(const LaneRows<kE>& rows, int node) {
+__device__ __forceinline__ Raw8<kE> ld8(const char* at) {
   Raw8<kE> r;
-  const char* at = rows.at(node);
   if constexpr (kE == 16) {
     const uint4 t = ld16(at);
     r.w[0] = t.x;
@@ -95,8 +94,13 @@ __device__ __forceinline__ void widen(const Raw8<kE>& r, float (&x)[kE]) {
 }
 
 // Edges in flight per lane.
+//
+// Edges in flight per lane: pass 1 gathers 32 bytes of an edge and keeps four in
+// flight (857 us instead of 1,028 with two on the 300k-node graph); pass 2 gathers
+// three to five times as much, and four spill.
+constexpr int kDstEdges = 4;
 template <int kE>
-struct Unroll8 {
+struct SrcEdges {
   static constexpr int value = kE == 16 ? 2 : 4;
 };
 
@@ -107,21 +111,23 @@ struct Unroll8 {
 template <typename T, int kE_, bool kRel>
 struct DstPass {
   static constexpr int kE = kE_;
-  static constexpr int U = Unroll8<kE>::value;
+  static constexpr int U = kDstEdges;
   static constexpr bool kBuckets = kRel;
   const T8Args& A;
   const Lane<1>& L;
+  const LanePlace<kE> place;                      // in rows of bytes
+  const LanePlace<kE * int(sizeof(T))> rows;      // in rows of T
   const LaneRows<kE> r0, r1;  // the gathered rows
   const float* sb;            // the bias table
   // the node
   Raw8<kE> q8;
   float qsc;        // qs_i
-  float g[kE];      // dout_i
+  HeldT<T, kE> g;   // dout_i
   // its sums; m is in base 2
   float m, l, d, P[kE], Q[kE];
 
   __device__ __forceinline__ DstPass(const T8Args& a, const Lane<1>& lane)
-      : A(a), L(lane), r0(a.k8, a.s, lane), r1(a.v8, a.s, lane) {}
+      : A(a), L(lane), place(a.s, lane), rows(a.s, lane), r0(a.k8, place), r1(a.v8, place) {}
   // floats of a partial state: P, Q, then m, l, d per head
   static __host__ __device__ int floats(const Shape& s) { return 2 * s.rv * kE + 3 * s.H; }
 
@@ -132,9 +138,9 @@ struct DstPass {
     zero<kE>(Q);
   }
   __device__ __forceinline__ void begin(int i) {
-    q8 = ld8<kE>(LaneRows<kE>(A.q8, A.s, L), i);
+    q8 = ld8<kE>(place.of(A.q8, i));
     qsc = of_head(A.qs + L.k[0], i, A.s);
-    widenT<T, kE>(ldT<T, kE>(LaneRows<kE * int(sizeof(T))>(A.dout, A.s, L), i), g);
+    g.fetch(rows.of(A.dout, i));
     clear();
   }
   __device__ __forceinline__ void rescale(float mn) {
@@ -153,12 +159,11 @@ struct DstPass {
     float ks[U], vs[U];
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-      rk[u] = ld8<kE>(r0, j[u]);
-      rv[u] = ld8<kE>(r1, j[u]);
+      rk[u] = ld8<kE>(r0.at(j[u]));
+      rv[u] = ld8<kE>(r1.at(j[u]));
       ks[u] = of_head(A.ks + L.k[0], j[u], A.s);
       vs[u] = of_head(A.vs + L.k[0], j[u], A.s);
     }
-    sent();
     float bs[U];
     bool ok[U];  // there, and not masked for the lane's head
 #pragma unroll
@@ -166,14 +171,20 @@ struct DstPass {
       bs[u] = kRel ? sb[b[u] * A.s.H] : 0.f;
       ok[u] = u < cnt && (!kRel || bs[u] != -INFINITY);
     }
+    sent();
     const float qk = qsc * A.scale2;
     float red[2 * U];
+    {
+      float own[kE];
+      held_ready();
+      widenT<T, kE>(g.get(), own);
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
-      float x[kE];
-      red[u] = dot8<kE>(rk[u], q8);
-      widen<kE>(rv[u], x);
-      red[U + u] = dot<kE>(x, g);
+      for (int u = 0; u < U; ++u) {
+        float x[kE];
+        red[u] = dot8<kE>(rk[u], q8);
+        widen<kE>(rv[u], x);
+        red[U + u] = dot<kE>(x, own);
+      }
     }
     head_sums<2 * U>(red, A.s.hv_log2);
     float top = m;
@@ -244,7 +255,7 @@ struct DstPass {
     const float f = A.scale * inv;
 #pragma unroll
     for (int c = 0; c < kE; ++c) P[c] = f * fmaf(-delta, Q[c], P[c]);
-    storeT<T, kE>(A.dq, i, A.s, L, P);
+    storeT<T, kE>(const_cast<char*>(rows.of(A.dq, i)), P);
     if (L.head_leader(A.s, 0))
       A.stats[int64_t(i) * A.s.H + L.k[0]] =
           make_float4(any ? m + __log2f(l) : 0.f, delta, qsc, 0.f);
@@ -258,21 +269,25 @@ struct DstPass {
 template <typename T, int kE_, bool kRel>
 struct SrcPass {
   static constexpr int kE = kE_;
-  static constexpr int U = Unroll8<kE>::value;
+  static constexpr int U = SrcEdges<kE>::value;
   static constexpr bool kBuckets = kRel;
   const T8Args& A;
   const Lane<1>& L;
+  const LanePlace<kE> place;                      // in rows of bytes
+  const LanePlace<kE * int(sizeof(T))> rows;      // in rows of T
   const LaneRows<kE> r0;      // the gathered rows
   const LaneRows<kE * int(sizeof(T))> r1;
   const float* sb;            // the bias table
   float* hist;      // this lane's column of its warp's gradient table
   Raw8<kE> k8;
   float ksc, vsc;
+  Raw8<kE> v8;
+  bool fresh;       // v8 not widened yet (begin waits for no load)
   float v[kE];      // v8_j as floats
   float dk[kE], dv[kE];
 
   __device__ __forceinline__ SrcPass(const T8Args& a, const Lane<1>& lane)
-      : A(a), L(lane), r0(a.q8, a.s, lane), r1(a.dout, a.s, lane) {}
+      : A(a), L(lane), place(a.s, lane), rows(a.s, lane), r0(a.q8, place), r1(a.dout, rows) {}
   static __host__ __device__ int floats(const Shape& s) { return 2 * s.rv * kE; }
 
   __device__ __forceinline__ void clear() {
@@ -280,8 +295,9 @@ struct SrcPass {
     zero<kE>(dv);
   }
   __device__ __forceinline__ void begin(int j) {
-    k8 = ld8<kE>(LaneRows<kE>(A.k8, A.s, L), j);
-    widen<kE>(ld8<kE>(LaneRows<kE>(A.v8, A.s, L), j), v);
+    k8 = ld8<kE>(place.of(A.k8, j));
+    v8 = ld8<kE>(place.of(A.v8, j));
+    fresh = true;
     ksc = of_head(A.ks + L.k[0], j, A.s);
     vsc = of_head(A.vs + L.k[0], j, A.s);
     clear();
@@ -295,19 +311,23 @@ struct SrcPass {
     float4 st[U];
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-      rq[u] = ld8<kE>(r0, i[u]);
-      rg[u] = ldT<T, kE>(r1, i[u]);
+      rq[u] = ld8<kE>(r0.at(i[u]));
+      rg[u] = ldT<T, kE>(r1.at(i[u]));
       st[u] = of_head(A.stats + L.k[0], i[u], A.s);
     }
-    sent();
     float bs[U];
+    int bk[U];
     bool ok[U];  // there, and not masked for the lane's head
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-      bs[u] = kRel ? sb[b[u] * A.s.H] : 0.f;
+      bk[u] = kRel ? b[u] : 0;
+      bs[u] = kRel ? sb[bk[u] * A.s.H] : 0.f;
       ok[u] = u < cnt && (!kRel || bs[u] != -INFINITY);
     }
+    sent();
     const float kq = ksc * A.scale2;
+    if (fresh) widen<kE>(v8, v);
+    fresh = false;
     float red[2 * U];
 #pragma unroll
     for (int u = 0; u < U; ++u) {
@@ -323,7 +343,7 @@ struct SrcPass {
       if (!ok[u]) continue;
       const float al = ex2(e - st[u].x);
       const float de = al * fmaf(red[U + u], vsc, -st[u].y);
-      if (kRel && L.head_leader(A.s, 0)) add_grad(hist, A.s, b[u], de);
+      if (kRel && L.head_leader(A.s, 0)) add_grad(hist, A.s, bk[u], de);
       float x[kE];
       widen<kE>(rq[u], x);
       axpy<kE>(dk, de * A.scale * st[u].z, x);
@@ -348,8 +368,8 @@ struct SrcPass {
     }
   }
   __device__ __forceinline__ void finish(int j) {
-    storeT<T, kE>(A.dkey, j, A.s, L, dk);
-    storeT<T, kE>(A.dval, j, A.s, L, dv);
+    storeT<T, kE>(const_cast<char*>(rows.of(A.dkey, j)), dk);
+    storeT<T, kE>(const_cast<char*>(rows.of(A.dval, j)), dv);
   }
 };
 
@@ -359,7 +379,9 @@ template <typename T, int kE, bool kRel>
 __global__ void __launch_bounds__(kThreads, kPerSm) t8_dst(const __grid_constant__ T8Args A) {
   extern __shared__ __align__(16) unsigned char smem[];
   const Lane<1> L(A.s);
+  __shared__ __align__(16) unsigned char held[kWarps * HeldT<T, kE>::kBytes];
   DstPass<T, kE, kRel> p(A, L);
+  p.g.place(held + (threadIdx.x >> 5) * HeldT<T, kE>::kBytes, L.lane);
   p.sb = kRel ? stage_bias(A.bias, A.buckets * A.s.H, smem) + L.k[0] : nullptr;
   walk(p, A.walk, A.dir, A.s, L);
 }
@@ -384,7 +406,8 @@ __global__ void __launch_bounds__(kThreads, kPerSm) t8_src(const __grid_constant
 template <typename K>
 cudaError_t launch(K kernel, const T8Args& A, int blocks, size_t smem, cudaStream_t st) {
   cudaError_t e;
-  if (smem > 48 * 1024 &&
+  // (the default limit, 48 KB, counts the kernels' static 16 KB too)
+  if (smem > 32 * 1024 &&
       (e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, int(smem))) !=
           cudaSuccess)
     return e;

@@ -43,29 +43,31 @@ struct RelArgs {
   double* db_part;         // [pass 2 blocks][buckets][H]
 };
 
-// Edges in flight per lane: 64 bytes of each of the two gathered rows.
-template <typename T, int kE>
-struct RelUnroll {
-  static constexpr int value = 64 / (kE * int(sizeof(T)));
+// Edges in flight per lane, for lane vectors of 32 bytes (twice as many of 16).
+template <int kBytes, int kEdges>
+struct RelEdges {
+  static constexpr int value = kEdges * (32 / kBytes);
 };
+constexpr int kFwdEdges = 4, kDstEdges = 3, kSrcEdges = 2;
 
 // ---- forward -----------------------------------------------------------------
 
 template <typename T, int kE_>
 struct RelFwd {
   static constexpr int kE = kE_;
-  static constexpr int U = RelUnroll<T, kE>::value;
-  using Rows = LaneRows<kE * int(sizeof(T))>;
+  static constexpr int U = RelEdges<kE * int(sizeof(T)), kFwdEdges>::value;
+  static constexpr int kRow = kE * int(sizeof(T));
   static constexpr bool kBuckets = true;
   const RelArgs& A;
   const Lane<1>& L;
-  const Rows r0, r1;  // the gathered rows
+  const LanePlace<kRow> place;
+  const LaneRows<kRow> r0, r1;  // the gathered rows
   const float* sb;    // the bias table
   HeldT<T, kE> q;
   float m, l, acc[kE];  // m in base 2
 
   __device__ __forceinline__ RelFwd(const RelArgs& a, const Lane<1>& lane)
-      : A(a), L(lane), r0(a.key, a.s, lane), r1(a.val, a.s, lane) {}
+      : A(a), L(lane), place(a.s, lane), r0(a.key, place), r1(a.val, place) {}
   static __host__ __device__ int floats(const Shape& s) { return s.rv * kE + 2 * s.H; }
 
   __device__ __forceinline__ void clear() {
@@ -74,7 +76,7 @@ struct RelFwd {
     zero<kE>(acc);
   }
   __device__ __forceinline__ void begin(int i) {
-    q.set(ldT<T, kE>(Rows(A.q, A.s, L), i));
+    q.fetch(place.of(A.q, i));
     clear();
   }
   template <class F>
@@ -83,10 +85,9 @@ struct RelFwd {
     RawT<T, kE> rk[U], rv[U];
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-      rk[u] = ldT<T, kE>(r0, j[u]);
-      rv[u] = ldT<T, kE>(r1, j[u]);
+      rk[u] = ldT<T, kE>(r0.at(j[u]));
+      rv[u] = ldT<T, kE>(r1.at(j[u]));
     }
-    sent();
     float bs[U];
     bool ok[U];  // there, and not masked for the lane's head
 #pragma unroll
@@ -94,6 +95,8 @@ struct RelFwd {
       bs[u] = sb[b[u] * A.s.H];
       ok[u] = u < cnt && bs[u] != -INFINITY;
     }
+    sent();
+    held_ready();
     float sc[U];
     const RawT<T, kE> own = q.get();
 #pragma unroll
@@ -146,7 +149,7 @@ struct RelFwd {
   __device__ __forceinline__ void finish(int i) {
     const bool any = l != 0.f;  // a NaN stays one
     scale<kE>(acc, any ? __frcp_rn(l) : 0.f);
-    storeT<T, kE>(A.out, i, A.s, L, acc);
+    storeT<T, kE>(const_cast<char*>(place.of(A.out, i)), acc);
     if (L.head_leader(A.s, 0))
       A.lse[int64_t(i) * A.s.H + L.k[0]] = any ? (m + __log2f(l)) * kLn2 : -INFINITY;
   }
@@ -157,18 +160,19 @@ struct RelFwd {
 template <typename T, int kE_>
 struct RelDst {
   static constexpr int kE = kE_;
-  static constexpr int U = RelUnroll<T, kE>::value;
-  using Rows = LaneRows<kE * int(sizeof(T))>;
+  static constexpr int U = RelEdges<kE * int(sizeof(T)), kDstEdges>::value;
+  static constexpr int kRow = kE * int(sizeof(T));
   static constexpr bool kBuckets = true;
   const RelArgs& A;
   const Lane<1>& L;
-  const Rows r0, r1;  // the gathered rows
+  const LanePlace<kRow> place;
+  const LaneRows<kRow> r0, r1;  // the gathered rows
   const float* sb;    // the bias table
   HeldT<T, kE> q, g;
   float lse2, delta, P[kE], Q[kE];
 
   __device__ __forceinline__ RelDst(const RelArgs& a, const Lane<1>& lane)
-      : A(a), L(lane), r0(a.key, a.s, lane), r1(a.val, a.s, lane) {}
+      : A(a), L(lane), place(a.s, lane), r0(a.key, place), r1(a.val, place) {}
   static __host__ __device__ int floats(const Shape& s) { return 2 * s.rv * kE + s.H; }
 
   __device__ __forceinline__ void clear() {
@@ -177,8 +181,8 @@ struct RelDst {
     zero<kE>(Q);
   }
   __device__ __forceinline__ void begin(int i) {
-    q.set(ldT<T, kE>(Rows(A.q, A.s, L), i));
-    g.set(ldT<T, kE>(Rows(A.dout, A.s, L), i));
+    q.fetch(place.of(A.q, i));
+    g.fetch(place.of(A.dout, i));
     lse2 = __ldg(A.lse_in + int64_t(i) * A.s.H + L.k[0]) * kLog2e;
     clear();
   }
@@ -188,10 +192,9 @@ struct RelDst {
     RawT<T, kE> rk[U], rv[U];
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-      rk[u] = ldT<T, kE>(r0, j[u]);
-      rv[u] = ldT<T, kE>(r1, j[u]);
+      rk[u] = ldT<T, kE>(r0.at(j[u]));
+      rv[u] = ldT<T, kE>(r1.at(j[u]));
     }
-    sent();
     float bs[U];
     bool ok[U];  // there, and not masked for the lane's head
 #pragma unroll
@@ -199,6 +202,8 @@ struct RelDst {
       bs[u] = sb[b[u] * A.s.H];
       ok[u] = u < cnt && bs[u] != -INFINITY;
     }
+    sent();
+    held_ready();
     float red[2 * U];
     {
       const RawT<T, kE> own = g.get();
@@ -244,7 +249,7 @@ struct RelDst {
   __device__ __forceinline__ void finish(int i) {
 #pragma unroll
     for (int c = 0; c < kE; ++c) P[c] = A.scale * fmaf(-delta, Q[c], P[c]);
-    storeT<T, kE>(A.dq, i, A.s, L, P);
+    storeT<T, kE>(const_cast<char*>(place.of(A.dq, i)), P);
     if (L.head_leader(A.s, 0))
       A.stats[int64_t(i) * A.s.H + L.k[0]] = make_float2(lse2, delta);
   }
@@ -255,19 +260,20 @@ struct RelDst {
 template <typename T, int kE_>
 struct RelSrc {
   static constexpr int kE = kE_;
-  static constexpr int U = RelUnroll<T, kE>::value;
-  using Rows = LaneRows<kE * int(sizeof(T))>;
+  static constexpr int U = RelEdges<kE * int(sizeof(T)), kSrcEdges>::value;
+  static constexpr int kRow = kE * int(sizeof(T));
   static constexpr bool kBuckets = true;
   const RelArgs& A;
   const Lane<1>& L;
-  const Rows r0, r1;  // the gathered rows
+  const LanePlace<kRow> place;
+  const LaneRows<kRow> r0, r1;  // the gathered rows
   const float* sb;    // the bias table
   float* hist;  // this lane's column of its warp's gradient table
   HeldT<T, kE> k, v;
   float dk[kE], dv[kE];
 
   __device__ __forceinline__ RelSrc(const RelArgs& a, const Lane<1>& lane)
-      : A(a), L(lane), r0(a.q, a.s, lane), r1(a.dout, a.s, lane) {}
+      : A(a), L(lane), place(a.s, lane), r0(a.q, place), r1(a.dout, place) {}
   static __host__ __device__ int floats(const Shape& s) { return 2 * s.rv * kE; }
 
   __device__ __forceinline__ void clear() {
@@ -275,8 +281,8 @@ struct RelSrc {
     zero<kE>(dv);
   }
   __device__ __forceinline__ void begin(int j) {
-    k.set(ldT<T, kE>(Rows(A.key, A.s, L), j));
-    v.set(ldT<T, kE>(Rows(A.val, A.s, L), j));
+    k.fetch(place.of(A.key, j));
+    v.fetch(place.of(A.val, j));
     clear();
   }
   template <class F>
@@ -286,18 +292,21 @@ struct RelSrc {
     float2 st[U];
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-      rq[u] = ldT<T, kE>(r0, i[u]);
-      rg[u] = ldT<T, kE>(r1, i[u]);
+      rq[u] = ldT<T, kE>(r0.at(i[u]));
+      rg[u] = ldT<T, kE>(r1.at(i[u]));
       st[u] = __ldg(A.stats + L.k[0] + uint64_t(uint32_t(i[u])) * uint32_t(A.s.H));
     }
-    sent();
     float bs[U];
+    int bk[U];
     bool ok[U];  // there, and not masked for the lane's head
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-      bs[u] = sb[b[u] * A.s.H];
+      bk[u] = b[u];
+      bs[u] = sb[bk[u] * A.s.H];
       ok[u] = u < cnt && bs[u] != -INFINITY;
     }
+    sent();
+    held_ready();
     float red[2 * U];
     {
       const RawT<T, kE> own = k.get();
@@ -315,7 +324,7 @@ struct RelSrc {
       if (!ok[u]) continue;
       const float al = ex2(fmaf(red[u], A.scale2, bs[u]) - st[u].x);
       const float de = al * (red[U + u] - st[u].y);
-      if (L.head_leader(A.s, 0)) add_grad(hist, A.s, b[u], de);
+      if (L.head_leader(A.s, 0)) add_grad(hist, A.s, bk[u], de);
       float x[kE];
       widenT<T, kE>(rq[u], x);
       axpy<kE>(dk, de, x);
@@ -341,14 +350,14 @@ struct RelSrc {
   }
   __device__ __forceinline__ void finish(int j) {
     scale<kE>(dk, A.scale);
-    storeT<T, kE>(A.dkey, j, A.s, L, dk);
-    storeT<T, kE>(A.dval, j, A.s, L, dv);
+    storeT<T, kE>(const_cast<char*>(place.of(A.dkey, j)), dk);
+    storeT<T, kE>(const_cast<char*>(place.of(A.dval, j)), dv);
   }
 };
 
 // ---- kernels -----------------------------------------------------------------
 
-constexpr int kFwdPerSm = 3, kBwdPerSm = 2;  // resident blocks
+constexpr int kFwdPerSm = 2, kBwdPerSm = 2;  // resident blocks
 
 template <typename T, int kE>
 __global__ void __launch_bounds__(kThreads, kFwdPerSm) rel_fwd(const __grid_constant__ RelArgs A) {
