@@ -102,7 +102,15 @@ struct HeldT {
                    "l"(from + 16 * k)
                    : "memory");
   }
-  // after held_ready()
+  // float32: values computed by this lane
+  __device__ __forceinline__ void put(const float (&x)[kE]) {
+#pragma unroll
+    for (int k = 0; k < kParts; ++k)
+      asm volatile("st.shared.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(at + 512 * k), "f"(x[4 * k]),
+                   "f"(x[4 * k + 1]), "f"(x[4 * k + 2]), "f"(x[4 * k + 3])
+                   : "memory");
+  }
+  // after held_ready() or put()
   __device__ __forceinline__ RawT<T, kE> get() const {
     RawT<T, kE> r;
 #pragma unroll

@@ -282,8 +282,8 @@ struct SrcPass {
   Raw8<kE> k8;
   float ksc, vsc;
   Raw8<kE> v8;
-  bool fresh;       // v8 not widened yet (begin waits for no load)
-  float v[kE];      // v8_j as floats
+  bool fresh;              // v8 not widened yet (begin waits for no load)
+  HeldT<float, kE> v;      // v8_j as floats
   float dk[kE], dv[kE];
 
   __device__ __forceinline__ SrcPass(const T8Args& a, const Lane<1>& lane)
@@ -326,15 +326,21 @@ struct SrcPass {
     }
     sent();
     const float kq = ksc * A.scale2;
-    if (fresh) widen<kE>(v8, v);
-    fresh = false;
+    if (fresh) {
+      float x[kE];
+      widen<kE>(v8, x);
+      v.put(x);
+      fresh = false;
+    }
+    float own[kE];
+    widenT<float, kE>(v.get(), own);
     float red[2 * U];
 #pragma unroll
     for (int u = 0; u < U; ++u) {
       float x[kE];
       red[u] = dot8<kE>(rq[u], k8);
       widenT<T, kE>(rg[u], x);
-      red[U + u] = dot<kE>(x, v);
+      red[U + u] = dot<kE>(x, own);
     }
     head_sums<2 * U>(red, A.s.hv_log2);
 #pragma unroll
@@ -390,7 +396,9 @@ template <typename T, int kE, bool kRel>
 __global__ void __launch_bounds__(kThreads, kPerSm) t8_src(const __grid_constant__ T8Args A) {
   extern __shared__ __align__(16) unsigned char smem[];
   const Lane<1> L(A.s);
+  __shared__ __align__(16) unsigned char held[kWarps * HeldT<float, kE>::kBytes];
   SrcPass<T, kE, kRel> p(A, L);
+  p.v.place(held + (threadIdx.x >> 5) * HeldT<float, kE>::kBytes, L.lane);
   float* tables = nullptr;
   p.sb = nullptr;
   p.hist = nullptr;
