@@ -36,11 +36,22 @@ struct LaneRows {
   }
 };
 
+// (Vectors of 32 bytes or more: one load per 32, from 32-byte boundaries.)
 template <typename T, int kE>
 __device__ __forceinline__ RawT<T, kE> ldT(const char* at) {
   RawT<T, kE> r;
+  constexpr int n = kE * int(sizeof(T)) / 16;
+  if constexpr (n % 2 == 0) {
 #pragma unroll
-  for (int k = 0; k < kE * int(sizeof(T)) / 16; ++k) r.v[k] = ld16(at + 16 * k);
+    for (int k = 0; k < n; k += 2) {
+      const RawV<32> t = ldv<32>(at + 16 * k);
+      r.v[k] = t.a;
+      r.v[k + 1] = t.b;
+    }
+  } else {
+#pragma unroll
+    for (int k = 0; k < n; ++k) r.v[k] = ld16(at + 16 * k);
+  }
   return r;
 }
 
@@ -125,6 +136,20 @@ struct HeldT {
 
 // Waits for this lane's copies.
 __device__ __forceinline__ void held_ready() { asm volatile("cp.async.wait_all;" ::: "memory"); }
+
+// P = f (P - d Q)
+template <int kE>
+__device__ __forceinline__ void minus_scaled(float (&P)[kE], const float (&Q)[kE], float d, float f) {
+  scale<kE>(P, f);
+  axpy<kE>(P, -f * d, Q);
+}
+
+// 1 / x to within an ulp of float32 (x a sum of weights: from 2^-126 to 2^31).
+__device__ __forceinline__ float reciprocal(float x) {
+  float r;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
 
 // The geometry of rows of s in vectors of e elements (a power of two dividing D).
 inline Shape lane_shape(const Shape& s, int e) {

@@ -250,11 +250,9 @@ struct DstPass {
   }
   __device__ __forceinline__ void finish(int i) {
     const bool any = l != 0.f;  // a NaN stays one
-    const float inv = any ? __frcp_rn(l) : 0.f;
+    const float inv = any ? reciprocal(l) : 0.f;
     const float delta = d * inv;
-    const float f = A.scale * inv;
-#pragma unroll
-    for (int c = 0; c < kE; ++c) P[c] = f * fmaf(-delta, Q[c], P[c]);
+    minus_scaled<kE>(P, Q, delta, A.scale * inv);
     storeT<T, kE>(const_cast<char*>(rows.of(A.dq, i)), P);
     if (L.head_leader(A.s, 0))
       A.stats[int64_t(i) * A.s.H + L.k[0]] =
@@ -445,17 +443,21 @@ cudaError_t bwd8_rel(const T8Args& A, const gnn_graph* g, const gnn_rel* rel, co
              : bwd8_t<T, kE, false>(A, g, rel, p, dbias, st);
 }
 
-// Elements of a lane vector: 16 where a head has as many.
-int lane_elems(int D) { return D >= 16 ? 16 : D; }
+// Elements of a lane vector: 16 where a head has as many and dout's rows can be read
+// 32 bytes at a time, else those of 16 bytes of dout.
+int lane_elems(const Shape& s, bool aligned) {
+  if (!aligned) return 16 / s.esize;
+  return s.D >= 16 ? 16 : s.D;
+}
 
 struct T8Layout {
   size_t arrived, part, stats, db_part, total;
   WalkPlan plan;  // the same for both directions: n and e are
 };
 
-T8Layout t8_layout(const gnn_graph* g, const Shape& s, int buckets) {
+T8Layout t8_layout(const gnn_graph* g, const Shape& s, int buckets, int elems) {
   T8Layout L{};
-  L.plan = walk_plan(g->n, g->e, lane_shape(s, lane_elems(s.D)), kPerSm, g->sm_count);
+  L.plan = walk_plan(g->n, g->e, lane_shape(s, elems), kPerSm, g->sm_count);
   size_t off = 0;
   auto take = [&](size_t bytes) {
     const size_t r = off;
@@ -473,7 +475,9 @@ T8Layout t8_layout(const gnn_graph* g, const Shape& s, int buckets) {
 }  // namespace
 
 size_t transformer8_ws_bytes(const gnn_graph* g, const Shape& s, int buckets) {
-  return t8_layout(g, s, buckets).total;
+  const size_t a = t8_layout(g, s, buckets, lane_elems(s, true)).total;
+  const size_t b = t8_layout(g, s, buckets, lane_elems(s, false)).total;
+  return a > b ? a : b;
 }
 
 cudaError_t launch_transformer8_backward(const gnn_graph* g, const gnn_rel* rel, const Shape& s,
@@ -482,9 +486,10 @@ cudaError_t launch_transformer8_backward(const gnn_graph* g, const gnn_rel* rel,
                                          float scale, const float* bias, const void* dout,
                                          void* dq, void* dkey, void* dval, float* dbias, char* ws,
                                          cudaStream_t st) {
-  const T8Layout W = t8_layout(g, s, rel ? rel->buckets : 0);
+  const int e = lane_elems(s, aligned32(dout));
+  const T8Layout W = t8_layout(g, s, rel ? rel->buckets : 0, e);
   T8Args A{};
-  A.s = lane_shape(s, lane_elems(s.D));
+  A.s = lane_shape(s, e);
   A.walk = make_walk(W.plan, g->n, reinterpret_cast<int*>(ws + W.arrived),
                      reinterpret_cast<float*>(ws + W.part));
   A.dir = WalkDir{g->csr.ptr, g->csr.idx, rel ? rel->csr : nullptr};
@@ -504,7 +509,6 @@ cudaError_t launch_transformer8_backward(const gnn_graph* g, const gnn_rel* rel,
   A.bias = bias;
   A.buckets = rel ? rel->buckets : 0;
   A.db_part = reinterpret_cast<double*>(ws + W.db_part);
-  const int e = lane_elems(s.D);
   if (dt == GNN_F32)
     return e == 16  ? bwd8_rel<float, 16>(A, g, rel, W.plan, dbias, st)
            : e == 8 ? bwd8_rel<float, 8>(A, g, rel, W.plan, dbias, st)

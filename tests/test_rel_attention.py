@@ -256,3 +256,39 @@ def test_refusals():
     wide_row = torch.zeros(6, 1, 256, device="cuda")
     with pytest.raises(gnn.GnnError):
         gnn.transformer_rel_forward(g, rel, wide_row, wide_row, wide_row, b[:, :1].contiguous())
+
+
+@pytest.mark.parametrize("H,D,dtype", [(4, 32, "f32"), (4, 64, "bf16"), (2, 8, "f32")])
+def test_rows_on_odd_16_byte_boundaries(H, D, dtype):
+    """Tensors that start 16 bytes past a 32-byte boundary give the same within
+    the bounds (both are held to them), and the workspace serves either."""
+    import graph_neural_network_gb300 as gnn
+    rp, ci = testgraphs.with_in_degrees([0, 5, 70, 300], n_nodes=500, seed=5)
+    g, rel, got, feats, bias = check(rp, ci, H, D, dtype, (8, 64, 16), what="aligned")
+    n = len(rp) - 1
+
+    def moved(x):
+        t = to_device(x, dtype)
+        pad = 16 // t.element_size()
+        room = torch.empty(t.numel() + pad, dtype=t.dtype, device="cuda")
+        v = room[pad:].view(t.shape)
+        v.copy_(t)
+        assert v.data_ptr() % 32 == 16
+        return v
+
+    q, k, v, dout = (moved(x) for x in feats)
+    b = torch.from_numpy(bias).cuda()
+    out, lse = gnn.transformer_rel_forward(g, rel, q, k, v, b)
+    gr = gnn.transformer_rel_backward(g, rel, q, k, v, b, lse, dout)
+    bucket = rel.arrays()[0].cpu().numpy()
+    ref = layer_ref.attention(rp, ci, *(wide(x) for x in feats[:3]), D ** -0.5, bias, bucket,
+                              wide(feats[3]))
+    layer_ref.hold_attention({x: to_f64(t) for x, t in zip(NAMES, (out, lse) + gr)}, ref, dtype,
+                             "odd", NAMES)
+    packed = gnn.pack8(q, k, v)
+    at = [p.values.cpu().numpy() * p.scale.cpu().numpy().astype(np.float64)[..., None]
+          for p in packed]
+    g8 = gnn.transformer_backward8(g, *packed, dout, rel=rel, bias=b)
+    ref = layer_ref.attention(rp, ci, *at, D ** -0.5, bias, bucket, wide(feats[3]))
+    names = ("dq", "dkey", "dval", "dbias")
+    layer_ref.hold_attention({x: to_f64(t) for x, t in zip(names, g8)}, ref, dtype, "odd 8", names)
