@@ -25,7 +25,7 @@
 
 namespace gnn {
 
-constexpr int kNodeCost = 4;   // of a node, in edges: its own rows, its result
+constexpr int kNodeCost = 3;   // of a node, in edges: its own rows, its result
 constexpr int kMinSeg = 16;    // units of a worker on small graphs
 constexpr int kWaves = 1;      // segments per resident sub-group on large ones
 
