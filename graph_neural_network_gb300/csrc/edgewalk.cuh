@@ -5,14 +5,18 @@
 // (edges first, then the node's own cost) that is a line of E + kNodeCost n units,
 // and worker w takes units [w seg, (w + 1) seg) of it: a path through row
 // pointers and edges cut at equal steps (Merrill and Garland, "Merge-based
-// parallel sparse matrix-vector multiplication", SC 2016).  A worker is a
-// sub-group of a warp, as wide as a feature row.  It finds its two ends by
-// bisection, finishes the nodes that lie whole inside, and leaves partial states
-// of the node that it begins in the middle (its head) and of the one that it
+// parallel sparse matrix-vector multiplication", SC 2016).  A cut that falls into a
+// node of at most `split` units moves to the node's end; only longer nodes are cut.
+// A worker is a sub-group of a warp, as wide as a feature row.  It finds its two ends
+// by bisection, finishes the nodes that lie whole inside, and leaves partial states
+// of the long node that it begins in the middle (its head) and of the one that it
 // leaves unfinished (its tail) in the workspace.  Whoever brings the last piece of
 // a node (a counter per node, no waiting) adds its pieces in worker order and
 // finishes it, so results do not depend on timing, and sums across nodes
-// that a block keeps (the bias gradient) depend on the grid alone.
+// that a block keeps (the bias gradient) depend on the grid alone.  (Cutting every
+// node costs two pieces a worker, each with a fence and a counter: 153 instead of
+// 110 us for pass 1 of 100k nodes of 17 edges from checkpoints, 20 instead of 9 us
+// for a forward pass over 512 nodes.)
 //
 // Why: on the power-law graphs more than half of the edges belong to nodes that
 // the degree buckets give to whole blocks, each with a staged edge list and three
@@ -26,7 +30,7 @@
 namespace gnn {
 
 constexpr int kNodeCost = 3;   // of a node, in edges: its own rows, its result
-constexpr int kMinSeg = 16;    // units of a worker on small graphs
+constexpr int kMinSeg = 32;    // units of a worker on small graphs
 constexpr int kWaves = 1;      // segments per resident sub-group on large ones
 
 struct WalkDir {
@@ -38,27 +42,74 @@ struct WalkDir {
 struct Walk {
   int n;
   int64_t total, seg;      // units, and units of a worker
+  int split;               // units of the longest node that is not cut
+  bool cuts;               // there are longer ones (else the counters are not used)
   int* arrived;            // [workers] pieces of the node whose first piece is the worker's
   float* part;             // [workers][head, tail][state floats]
 };
 
-// Nodes whose units all lie below d.
-__device__ __forceinline__ int nodes_below(const int32_t* ptr, int n, int64_t d) {
-  int lo = 0, hi = n;
-  while (lo < hi) {
-    const int mid = lo + (hi - lo) / 2;
-    if (int64_t(__ldg(ptr + mid + 1)) + int64_t(kNodeCost) * (mid + 1) <= d)
-      lo = mid + 1;
-    else
-      hi = mid;
+// a, b = how many nodes start at or below units d0 and d1: two bisections side by
+// side, three probes a step, so that n nodes take log4(n) dependent loads.
+__device__ __forceinline__ void nodes_from(const int32_t* ptr, int n, int64_t d0, int64_t d1,
+                                           int& a, int& b) {
+  int lo[2] = {0, 0}, hi[2] = {n, n};
+  const int64_t d[2] = {d0, d1};
+  while (lo[0] < hi[0] || lo[1] < hi[1]) {
+    bool in[2][3];
+    int m[2][3];
+#pragma unroll
+    for (int k = 0; k < 2; ++k)
+#pragma unroll
+      for (int x = 0; x < 3; ++x) {
+        m[k][x] = lo[k] + int((int64_t(hi[k] - lo[k]) * (x + 1)) >> 2);
+        const int at = m[k][x] < n ? m[k][x] : n - 1;
+        in[k][x] = int64_t(__ldg(ptr + at)) + int64_t(kNodeCost) * at <= d[k];
+      }
+#pragma unroll
+    for (int k = 0; k < 2; ++k)
+      if (lo[k] < hi[k]) {
+        if (!in[k][0]) {
+          hi[k] = m[k][0];
+        } else if (!in[k][1]) {
+          lo[k] = m[k][0] + 1;
+          hi[k] = m[k][1];
+        } else if (!in[k][2]) {
+          lo[k] = m[k][1] + 1;
+          hi[k] = m[k][2];
+        } else {
+          lo[k] = m[k][2] + 1;
+        }
+      }
   }
-  return lo;
+  a = lo[0];
+  b = lo[1];
 }
 
 // Partial states pass between workers through L2.
 __device__ __forceinline__ float part_load(const float* p) { return __ldcg(p); }
+template <int kE>
+__device__ __forceinline__ void part_row(const float* p, float (&x)[kE]) {
+#pragma unroll
+  for (int c = 0; c < kE; ++c) x[c] = __ldcg(p + c);
+}
+template <int kE>
+__device__ __forceinline__ void add_row(float (&a)[kE], const float (&x)[kE]) {
+#pragma unroll
+  for (int c = 0; c < kE; c += 2) add2(a[c], a[c + 1], a[c], a[c + 1], x[c], x[c + 1]);
+}
+// a += the N rows at p, p + step, ... in that order.
+template <int kE, int N>
+__device__ __forceinline__ void take_rows(float (&a)[kE], const float* p, int step) {
+  float x[N][kE];
+#pragma unroll
+  for (int n = 0; n < N; ++n) part_row<kE>(p + n * step, x[n]);
+#pragma unroll
+  for (int n = 0; n < N; ++n) add_row<kE>(a, x[n]);
+}
 
-// P holds a node's own rows and its partial state:
+// Called by every thread of a block that has written its tables to shared memory
+// (the walk begins with the barrier that ends those writes).  P holds a node's own
+// rows and its partial state:
 //   begin(i)         loads the rows of node i and clears the state
 //   clear()          clears the state
 //   batch(j, b, cnt, f)  adds the edges to j[u] with buckets b[u], u < cnt (the
@@ -67,7 +118,8 @@ __device__ __forceinline__ float part_load(const float* p) { return __ldcg(p); }
 //                    gathers are on their way
 //   finish(i)        writes node i's results from the state; the rows of begin(i)
 //                    are still there unless the node has no edges
-//   put(p), take(p)  stores the state, adds a stored one; P::floats(s) of them
+//   put(p)           stores the state, P::floats(s) numbers
+//   take<N>(p, d)    adds the N stored states at p, p + d, ... in that order
 template <class P>
 __device__ __forceinline__ void walk(P& p, const Walk& W, const WalkDir& D, const Shape& s,
                                      const Lane<1>& L) {
@@ -80,17 +132,36 @@ __device__ __forceinline__ void walk(P& p, const Walk& W, const WalkDir& D, cons
   int i = 0, e = 0, i1 = 0, e1 = 0, row_end = 0, ahead = 0;
   bool cont = false;  // node i has edges before this segment
   if (live) {
-    i = nodes_below(D.ptr, W.n, d0);
-    i1 = nodes_below(D.ptr, W.n, d1);
+    int c0, c1;
+    nodes_from(D.ptr, W.n, d0, d1, c0, c1);
+    // the cut at unit d of the line, node k being the last that starts there or
+    // before: (node, edge) from which the work goes on
+    const auto cut = [&](int64_t d, int k, int& node, int& edge) {
+      const int from = __ldg(D.ptr + k), to = __ldg(D.ptr + k + 1);
+      const int64_t in = d - (int64_t(from) + int64_t(kNodeCost) * k);  // units into the node
+      if (to - from + kNodeCost > W.split) {
+        node = k;
+        edge = in < to - from ? from + int(in) : to;
+      } else {
+        node = in > 0 ? k + 1 : k;
+        edge = in > 0 ? to : from;
+      }
+    };
+    cut(d0, c0 - 1, i, e);
+    if (d1 < W.total) {
+      cut(d1, c1 - 1, i1, e1);
+    } else {
+      i1 = W.n;
+      e1 = __ldg(D.ptr + W.n);
+    }
+    live = i < i1 || e < e1;
+    cont = live && i < W.n && e > __ldg(D.ptr + i);
+  }
+  if (live) {
     row_end = __ldg(D.ptr + i + 1);
-    const int64_t at = d0 - int64_t(kNodeCost) * i;
-    e = int(at < row_end ? at : row_end);
-    const int end1 = __ldg(D.ptr + (i1 < W.n ? i1 + 1 : W.n));
-    const int64_t at1 = d1 - int64_t(kNodeCost) * i1;
-    e1 = int(at1 < end1 ? at1 : end1);
-    cont = e > __ldg(D.ptr + i);
     ahead = __ldg(D.ptr + (i + 2 < W.n ? i + 2 : W.n));
   }
+  __syncthreads();  // the block's tables are staged
   const int nf = P::floats(s);
 
   // Hands over a piece of node i; the last to arrive finishes the node.
@@ -107,8 +178,12 @@ __device__ __forceinline__ void walk(P& p, const Walk& W, const WalkDir& D, cons
       __threadfence();
       p.clear();
       if (L.ok[0]) {
-        for (int64_t w = first; w < last; ++w) p.take(W.part + (2 * w + 1) * nf);
-        p.take(W.part + 2 * last * nf);
+        // tails first .. last - 1, then the head of the last: four loads at a time
+        const float* from = W.part + (2 * first + 1) * nf;
+        int more = int(last - first);
+        for (; more >= 4; more -= 4, from += 8 * nf) p.template take<4>(from, 2 * nf);
+        for (; more > 0; --more, from += 2 * nf) p.template take<1>(from, 0);
+        p.template take<1>(W.part + 2 * last * nf, 0);
         p.finish(i);
       }
     }
@@ -190,8 +265,14 @@ inline WalkPlan walk_plan(int64_t n, int64_t e, const Shape& s, int per_sm, int 
   return p;
 }
 
-inline Walk make_walk(const WalkPlan& p, int64_t n, int* arrived, float* part) {
+// max_deg: of the direction walked.
+inline Walk make_walk(const WalkPlan& p, int64_t n, int max_deg, int* arrived, float* part) {
   Walk w{};
+  // at most an eighth of a segment more or less; on small graphs, where the
+  // latency of a few nodes is all there is, two segments
+  w.split = int(p.seg / 8 > 2 * kMinSeg ? (p.seg / 8 < (1 << 30) ? p.seg / 8 : (1 << 30))
+                                        : 2 * kMinSeg);
+  w.cuts = max_deg > w.split - kNodeCost;
   w.n = int(n);
   w.total = p.total;
   w.seg = p.seg;

@@ -210,19 +210,6 @@ struct DstPass {
     }
   }
 
-  // adds another partial state of the same node
-  __device__ __forceinline__ void add(float mb, float lb, float db, const float (&Pb)[kE],
-                                      const float (&Qb)[kE]) {
-    const float M = fmaxf(m, mb), Mr = M == -INFINITY ? 0.f : M;
-    const float sa = ex2(m - Mr), sb_ = ex2(mb - Mr);
-    l = l * sa + lb * sb_;
-    d = d * sa + db * sb_;
-    scale<kE>(P, sa);
-    axpy<kE>(P, sb_, Pb);
-    scale<kE>(Q, sa);
-    axpy<kE>(Q, sb_, Qb);
-    m = M;
-  }
   __device__ __forceinline__ void put(float* to) const {
     const int row = A.s.rv * kE, at = L.q[0] * kE;
 #pragma unroll
@@ -237,16 +224,33 @@ struct DstPass {
       h[2] = d;
     }
   }
-  __device__ __forceinline__ void take(const float* from) {
+  template <int N>
+  __device__ __forceinline__ void take(const float* from, int step) {
     const int row = A.s.rv * kE, at = L.q[0] * kE;
-    float Pb[kE], Qb[kE];
+    float h[N][3], top = m;
 #pragma unroll
-    for (int c = 0; c < kE; ++c) {
-      Pb[c] = part_load(from + at + c);
-      Qb[c] = part_load(from + row + at + c);
+    for (int n = 0; n < N; ++n)
+#pragma unroll
+      for (int x = 0; x < 3; ++x) h[n][x] = part_load(from + n * step + 2 * row + 3 * L.k[0] + x);
+#pragma unroll
+    for (int n = 0; n < N; ++n) top = fmaxf(top, h[n][0]);
+    if (top > m) rescale(top);
+    const float mr = m == -INFINITY ? 0.f : m;
+#pragma unroll
+    for (int n = 0; n < N; ++n) {
+      h[n][0] = ex2(h[n][0] - mr);
+      l = fmaf(h[n][1], h[n][0], l);
+      d = fmaf(h[n][2], h[n][0], d);
     }
-    const float* h = from + 2 * row + 3 * L.k[0];
-    add(part_load(h), part_load(h + 1), part_load(h + 2), Pb, Qb);
+    float x[N][kE];
+#pragma unroll
+    for (int n = 0; n < N; ++n) part_row<kE>(from + n * step + at, x[n]);
+#pragma unroll
+    for (int n = 0; n < N; ++n) axpy<kE>(P, h[n][0], x[n]);
+#pragma unroll
+    for (int n = 0; n < N; ++n) part_row<kE>(from + n * step + row + at, x[n]);
+#pragma unroll
+    for (int n = 0; n < N; ++n) axpy<kE>(Q, h[n][0], x[n]);
   }
   __device__ __forceinline__ void finish(int i) {
     const bool any = l != 0.f;  // a NaN stays one
@@ -363,13 +367,11 @@ struct SrcPass {
       to[row + at + c] = dv[c];
     }
   }
-  __device__ __forceinline__ void take(const float* from) {
+  template <int N>
+  __device__ __forceinline__ void take(const float* from, int step) {
     const int row = A.s.rv * kE, at = L.q[0] * kE;
-#pragma unroll
-    for (int c = 0; c < kE; ++c) {
-      dk[c] += part_load(from + at + c);
-      dv[c] += part_load(from + row + at + c);
-    }
+    take_rows<kE, N>(dk, from + at, step);
+    take_rows<kE, N>(dv, from + row + at, step);
   }
   __device__ __forceinline__ void finish(int j) {
     storeT<T, kE>(const_cast<char*>(rows.of(A.dkey, j)), dk);
@@ -424,13 +426,17 @@ cudaError_t launch(K kernel, const T8Args& A, int blocks, size_t smem, cudaStrea
 template <typename T, int kE, bool kRel>
 cudaError_t bwd8_t(T8Args A, const gnn_graph* g, const gnn_rel* rel, const WalkPlan& p,
                    float* dbias, cudaStream_t st) {
+  const Walk src = make_walk(p, g->n, g->csc.max_deg, A.walk.arrived + p.workers, A.walk.part);
+  cudaError_t e;
   // the counters of both passes
-  cudaError_t e = cudaMemsetAsync(A.walk.arrived, 0, size_t(p.workers) * 2 * sizeof(int), st);
-  if (e != cudaSuccess) return e;
+  if ((A.walk.cuts || src.cuts) &&
+      (e = cudaMemsetAsync(A.walk.arrived, 0, size_t(p.workers) * 2 * sizeof(int), st)) !=
+          cudaSuccess)
+    return e;
   const size_t table = kRel ? size_t(A.buckets) * A.s.H * 4 : 0;
   if ((e = launch(t8_dst<T, kE, kRel>, A, p.blocks, table, st)) != cudaSuccess) return e;
   A.dir = WalkDir{g->csc.ptr, g->csc.idx, rel ? rel->csc : nullptr};
-  A.walk.arrived += p.workers;
+  A.walk = src;
   const size_t grads = kRel ? grad_tables_bytes(A.s, A.buckets) : 0;
   if ((e = launch(t8_src<T, kE, kRel>, A, p.blocks, table + grads, st)) != cudaSuccess) return e;
   return kRel ? launch_dbias_sum(A.db_part, p.blocks, A.buckets * A.s.H, dbias, st) : cudaSuccess;
@@ -490,7 +496,7 @@ cudaError_t launch_transformer8_backward(const gnn_graph* g, const gnn_rel* rel,
   const T8Layout W = t8_layout(g, s, rel ? rel->buckets : 0, e);
   T8Args A{};
   A.s = lane_shape(s, e);
-  A.walk = make_walk(W.plan, g->n, reinterpret_cast<int*>(ws + W.arrived),
+  A.walk = make_walk(W.plan, g->n, g->csr.max_deg, reinterpret_cast<int*>(ws + W.arrived),
                      reinterpret_cast<float*>(ws + W.part));
   A.dir = WalkDir{g->csr.ptr, g->csr.idx, rel ? rel->csr : nullptr};
   A.q8 = q.values;

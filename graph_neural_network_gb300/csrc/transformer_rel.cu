@@ -133,18 +133,25 @@ struct RelFwd {
       to[A.s.rv * kE + 2 * L.k[0] + 1] = l;
     }
   }
-  __device__ __forceinline__ void take(const float* from) {
-    const float mb = part_load(from + A.s.rv * kE + 2 * L.k[0]);
-    const float lb = part_load(from + A.s.rv * kE + 2 * L.k[0] + 1);
-    float x[kE];
+  template <int N>
+  __device__ __forceinline__ void take(const float* from, int step) {
+    float mb[N], lb[N], x[N][kE];
 #pragma unroll
-    for (int c = 0; c < kE; ++c) x[c] = part_load(from + L.q[0] * kE + c);
-    const float M = fmaxf(m, mb), Mr = M == -INFINITY ? 0.f : M;
-    const float sa = ex2(m - Mr), sx = ex2(mb - Mr);
-    l = l * sa + lb * sx;
-    scale<kE>(acc, sa);
-    axpy<kE>(acc, sx, x);
-    m = M;
+    for (int n = 0; n < N; ++n) {
+      const float* f = from + n * step;
+      mb[n] = part_load(f + A.s.rv * kE + 2 * L.k[0]);
+      lb[n] = part_load(f + A.s.rv * kE + 2 * L.k[0] + 1);
+      part_row<kE>(f + L.q[0] * kE, x[n]);
+    }
+#pragma unroll
+    for (int n = 0; n < N; ++n) {
+      const float M = fmaxf(m, mb[n]), Mr = M == -INFINITY ? 0.f : M;
+      const float sa = ex2(m - Mr), sx = ex2(mb[n] - Mr);
+      l = l * sa + lb[n] * sx;
+      scale<kE>(acc, sa);
+      axpy<kE>(acc, sx, x[n]);
+      m = M;
+    }
   }
   __device__ __forceinline__ void finish(int i) {
     const bool any = l != 0.f;  // a NaN stays one
@@ -237,14 +244,24 @@ struct RelDst {
     }
     if (L.head_leader(A.s, 0)) to[2 * row + L.k[0]] = delta;
   }
-  __device__ __forceinline__ void take(const float* from) {
+  template <int N>
+  __device__ __forceinline__ void take(const float* from, int step) {
     const int row = A.s.rv * kE, at = L.q[0] * kE;
+    float d[N], x[N][kE];
 #pragma unroll
-    for (int c = 0; c < kE; ++c) {
-      P[c] += part_load(from + at + c);
-      Q[c] += part_load(from + row + at + c);
+    for (int n = 0; n < N; ++n) {
+      d[n] = part_load(from + n * step + 2 * row + L.k[0]);
+      part_row<kE>(from + n * step + at, x[n]);
     }
-    delta += part_load(from + 2 * row + L.k[0]);
+#pragma unroll
+    for (int n = 0; n < N; ++n) {
+      delta += d[n];
+      add_row<kE>(P, x[n]);
+    }
+#pragma unroll
+    for (int n = 0; n < N; ++n) part_row<kE>(from + n * step + row + at, x[n]);
+#pragma unroll
+    for (int n = 0; n < N; ++n) add_row<kE>(Q, x[n]);
   }
   __device__ __forceinline__ void finish(int i) {
     minus_scaled<kE>(P, Q, delta, A.scale);
@@ -339,13 +356,11 @@ struct RelSrc {
       to[row + at + c] = dv[c];
     }
   }
-  __device__ __forceinline__ void take(const float* from) {
+  template <int N>
+  __device__ __forceinline__ void take(const float* from, int step) {
     const int row = A.s.rv * kE, at = L.q[0] * kE;
-#pragma unroll
-    for (int c = 0; c < kE; ++c) {
-      dk[c] += part_load(from + at + c);
-      dv[c] += part_load(from + row + at + c);
-    }
+    take_rows<kE, N>(dk, from + at, step);
+    take_rows<kE, N>(dv, from + row + at, step);
   }
   __device__ __forceinline__ void finish(int j) {
     scale<kE>(dk, A.scale);
@@ -460,21 +475,27 @@ cudaError_t launch(K kernel, const RelArgs& A, int blocks, size_t smem, cudaStre
 
 template <typename T, int kE>
 cudaError_t fwd_t(const RelArgs& A, const WalkPlan& p, cudaStream_t st) {
-  const cudaError_t e = cudaMemsetAsync(A.walk.arrived, 0, size_t(p.workers) * sizeof(int), st);
-  if (e != cudaSuccess) return e;
+  cudaError_t e;
+  if (A.walk.cuts && (e = cudaMemsetAsync(A.walk.arrived, 0, size_t(p.workers) * sizeof(int),
+                                            st)) != cudaSuccess)
+    return e;
   return launch(rel_fwd<T, kE>, A, p.blocks, size_t(A.buckets) * A.s.H * 4, st);
 }
 
 template <typename T, int kE>
 cudaError_t bwd_t(RelArgs A, const gnn_graph* g, const gnn_rel* rel, const WalkPlan& p,
                   float* dbias, cudaStream_t st) {
+  const Walk src = make_walk(p, g->n, g->csc.max_deg, A.walk.arrived + p.workers, A.walk.part);
+  cudaError_t e;
   // the counters of both passes
-  cudaError_t e = cudaMemsetAsync(A.walk.arrived, 0, size_t(p.workers) * 2 * sizeof(int), st);
-  if (e != cudaSuccess) return e;
+  if ((A.walk.cuts || src.cuts) &&
+      (e = cudaMemsetAsync(A.walk.arrived, 0, size_t(p.workers) * 2 * sizeof(int), st)) !=
+          cudaSuccess)
+    return e;
   const size_t table = size_t(A.buckets) * A.s.H * 4;
   if ((e = launch(rel_dst<T, kE>, A, p.blocks, table, st)) != cudaSuccess) return e;
   A.dir = WalkDir{g->csc.ptr, g->csc.idx, rel->csc};
-  A.walk.arrived += p.workers;
+  A.walk = src;
   if ((e = launch(rel_src<T, kE>, A, p.blocks, table + grad_tables_bytes(A.s, A.buckets), st)) !=
       cudaSuccess)
     return e;
@@ -486,7 +507,7 @@ RelArgs rel_args(const gnn_graph* g, const gnn_rel* rel, const Shape& s, const v
                  const RelLayout& W, const WalkPlan& p, int elems, char* ws) {
   RelArgs A{};
   A.s = lane_shape(s, elems);
-  A.walk = make_walk(p, g->n, reinterpret_cast<int*>(ws + W.arrived),
+  A.walk = make_walk(p, g->n, g->csr.max_deg, reinterpret_cast<int*>(ws + W.arrived),
                      reinterpret_cast<float*>(ws + W.part));
   A.dir = WalkDir{g->csr.ptr, g->csr.idx, rel->csr};
   A.q = q;
