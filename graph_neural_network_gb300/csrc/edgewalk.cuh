@@ -22,7 +22,15 @@
 // the degree buckets give to whole blocks, each with a staged edge list and three
 // barriers around about a hundred edges a warp, and the reproducible bias
 // gradient needs a fixed assignment, which those items balance badly.  300k
-// nodes, 6M edges, H4 D64 bf16, degree buckets -> this walk: WALKTIMES.
+// nodes, 6M edges, H4 D64 bf16: forward 0.85 ms by degree buckets, 0.52 by this walk
+// (with 32-byte lane vectors), pass 1 1.02 and 0.67 ms, pass 2 1.97 and 0.85 ms.
+//
+// Bound: per SM 16 warps wait about 1,700 cycles a batch for gathered rows and issue for
+// about half of the time; gathers alone would run at twice the rate (nodes of 300
+// edges, everything in L2: 333 us forward, 458 pass 1, 572 pass 2).  What did not help:
+// a ring of asynchronous copies to shared memory (no waits left, but a third more
+// instructions: 982 to 1,106 us a kernel), prefetches to L2, more warps with fewer
+// registers (spills), more and smaller segments (1.02 to 1.1 times the time).
 #pragma once
 
 #include "relbias.cuh"
@@ -31,7 +39,6 @@ namespace gnn {
 
 constexpr int kNodeCost = 3;   // of a node, in edges: its own rows, its result
 constexpr int kMinSeg = 32;    // units of a worker on small graphs
-constexpr int kWaves = 1;      // segments per resident sub-group on large ones
 
 struct WalkDir {
   const int32_t* ptr;
@@ -139,7 +146,7 @@ __device__ __forceinline__ void walk(P& p, const Walk& W, const WalkDir& D, cons
     const auto cut = [&](int64_t d, int k, int& node, int& edge) {
       const int from = __ldg(D.ptr + k), to = __ldg(D.ptr + k + 1);
       const int64_t in = d - (int64_t(from) + int64_t(kNodeCost) * k);  // units into the node
-      if (to - from + kNodeCost > W.split) {
+      if (to - from > W.split - kNodeCost) {
         node = k;
         edge = in < to - from ? from + int(in) : to;
       } else {
@@ -257,7 +264,7 @@ inline WalkPlan walk_plan(int64_t n, int64_t e, const Shape& s, int per_sm, int 
   WalkPlan p{};
   p.total = e + int64_t(kNodeCost) * n;
   const int64_t per_block = int64_t(kWarps) * (32 >> s.lpr_log2);
-  const int64_t most = int64_t(kWaves) * per_sm * (sm_count > 0 ? sm_count : 1) * per_block;
+  const int64_t most = int64_t(per_sm) * (sm_count > 0 ? sm_count : 1) * per_block;
   p.seg = (p.total + most - 1) / most;
   if (p.seg < kMinSeg) p.seg = kMinSeg;
   p.blocks = int((p.total + p.seg * per_block - 1) / (p.seg * per_block));
@@ -268,9 +275,9 @@ inline WalkPlan walk_plan(int64_t n, int64_t e, const Shape& s, int per_sm, int 
 // max_deg: of the direction walked.
 inline Walk make_walk(const WalkPlan& p, int64_t n, int max_deg, int* arrived, float* part) {
   Walk w{};
-  // at most an eighth of a segment more or less; on small graphs, where the
+  // at most a sixteenth of a segment more or less; on small graphs, where the
   // latency of a few nodes is all there is, two segments
-  w.split = int(p.seg / 8 > 2 * kMinSeg ? (p.seg / 8 < (1 << 30) ? p.seg / 8 : (1 << 30))
+  w.split = int(p.seg / 16 > 2 * kMinSeg ? (p.seg / 16 < (1 << 30) ? p.seg / 16 : (1 << 30))
                                         : 2 * kMinSeg);
   w.cuts = max_deg > w.split - kNodeCost;
   w.n = int(n);

@@ -15,7 +15,7 @@
 // for any graph in use here) and a byte written.  A block takes 4 * kThreads
 // consecutive edges: one thread finds the rows that they span by bisection,
 // every thread bisects within that span for the first of its four edges and
-// walks on from there.  19.8M edges (1M nodes): see the measurements table.
+// walks on from there.  6M edges over 300k nodes: RELTIME.
 #include <math.h>
 #include <string.h>
 

@@ -19,10 +19,15 @@
 // dot instruction: whole numbers below 2^23, exact in float32 as well, scaled
 // once.  The other products need a gathered byte as a float (widen8).
 //
-// Bound: gathers.  Per edge pass 1 reads 2 F bytes and two scales per head, pass 2
-// F (1 + s) bytes and a record per head; half to three quarters of what the
-// 16-bit pass gathers.  A lane holds kE = 16 (or 8, 4 for narrow heads) elements:
-// per-edge work that does not depend on them is then shared by more.
+// Bound: instruction issue and the latency of gathers together (issue 50 to 60 % of
+// cycles).  Per edge pass 1 gathers 2 F bytes and two scales per head, pass 2 F (1 + s)
+// bytes and a record per head: half to three quarters of what the passes over
+// 16-bit rows gather, while widening bytes costs more than widening bfloat16.  A lane
+// holds 16 elements (8 or 4 of narrow heads), so that what an edge costs whatever its
+// width is shared by more.  300k nodes, 6M edges, H4 D64 bf16 with the bias: 0.81 and
+// 0.91 ms, against 0.67 and 0.85 from the rows themselves; 100k nodes, 1.7M edges, H4
+// D32 f32 without: 0.11 and 0.17 ms.  What the checkpoints save is memory: a byte
+// instead of two or four per element of q, key and val, and lse.
 //
 // Masks, buckets and the bias gradient as in transformer_rel.cu; the work is cut as
 // edgewalk.cuh says.
@@ -93,11 +98,9 @@ __device__ __forceinline__ void widen(const Raw8<kE>& r, float (&x)[kE]) {
   for (int k = 0; k < kE / 4; ++k) widen8(r.w[k], x + 4 * k);
 }
 
-// Edges in flight per lane.
-//
 // Edges in flight per lane: pass 1 gathers 32 bytes of an edge and keeps four in
 // flight (857 us instead of 1,028 with two on the 300k-node graph); pass 2 gathers
-// three to five times as much, and four spill.
+// three to five times as much, and three spill (1,577 us instead of 957).
 constexpr int kDstEdges = 4;
 template <int kE>
 struct SrcEdges {

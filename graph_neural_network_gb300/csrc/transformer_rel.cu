@@ -15,11 +15,11 @@
 // memory (no atomics, no bank conflicts), the block adds its tables in a fixed
 // order in float64, and dbias_sum adds the blocks.
 //
-// Bound: gathers, 2 rows an edge and pass.  A lane holds 32 bytes of a row (16 where
-// a head has no more), so that what an edge costs whatever its width (ids,
-// bucket, bias, score, exponential, addresses) is shared by more elements; both
-// dot products of bfloat16 rows multiply the packed halves.  The work is cut as
-// edgewalk.cuh says.
+// Bound: latency of the gathers, 2 rows an edge and pass (edgewalk.cuh, which also
+// says how the work is cut and what it measured).  A lane holds 32 bytes of a row
+// (16 where a head has no more), so that what an edge costs whatever its width
+// (ids, bucket, bias, score, exponential, addresses) is shared by more elements;
+// both dot products of bfloat16 rows multiply the packed halves.
 #include "edgewalk.cuh"
 #include "lanevec.cuh"
 
@@ -43,7 +43,10 @@ struct RelArgs {
   double* db_part;         // [pass 2 blocks][buckets][H]
 };
 
-// Edges in flight per lane, for lane vectors of 32 bytes (twice as many of 16).
+// Edges in flight per lane, for lane vectors of 32 bytes (twice as many of 16): as
+// many as the registers of 16 warps an SM hold beside the accumulators.  300k-node
+// graph: forward 595 us with four and 2 blocks, 672 with two and 3; pass 1 752 with
+// three, 817 with two; pass 2 920 with two, 929 with three.
 template <int kBytes, int kEdges>
 struct RelEdges {
   static constexpr int value = kEdges * (32 / kBytes);
@@ -371,10 +374,10 @@ struct RelSrc {
 
 // ---- kernels -----------------------------------------------------------------
 
-constexpr int kFwdPerSm = 2, kBwdPerSm = 2;  // resident blocks
+constexpr int kPerSm = 2;  // resident blocks
 
 template <typename T, int kE>
-__global__ void __launch_bounds__(kThreads, kFwdPerSm) rel_fwd(const __grid_constant__ RelArgs A) {
+__global__ void __launch_bounds__(kThreads, kPerSm) rel_fwd(const __grid_constant__ RelArgs A) {
   extern __shared__ __align__(16) unsigned char smem[];
   const Lane<1> L(A.s);
   __shared__ __align__(16) unsigned char held[kWarps * HeldT<T, kE>::kBytes];
@@ -385,7 +388,7 @@ __global__ void __launch_bounds__(kThreads, kFwdPerSm) rel_fwd(const __grid_cons
 }
 
 template <typename T, int kE>
-__global__ void __launch_bounds__(kThreads, kBwdPerSm) rel_dst(const __grid_constant__ RelArgs A) {
+__global__ void __launch_bounds__(kThreads, kPerSm) rel_dst(const __grid_constant__ RelArgs A) {
   extern __shared__ __align__(16) unsigned char smem[];
   const Lane<1> L(A.s);
   __shared__ __align__(16) unsigned char held[2 * kWarps * HeldT<T, kE>::kBytes];
@@ -397,7 +400,7 @@ __global__ void __launch_bounds__(kThreads, kBwdPerSm) rel_dst(const __grid_cons
 }
 
 template <typename T, int kE>
-__global__ void __launch_bounds__(kThreads, kBwdPerSm) rel_src(const __grid_constant__ RelArgs A) {
+__global__ void __launch_bounds__(kThreads, kPerSm) rel_src(const __grid_constant__ RelArgs A) {
   extern __shared__ __align__(16) unsigned char smem[];
   const Lane<1> L(A.s);
   __shared__ __align__(16) unsigned char held[2 * kWarps * HeldT<T, kE>::kBytes];
@@ -435,28 +438,25 @@ int lane_elems(const Shape& s, bool aligned) {
 
 struct RelLayout {
   size_t arrived, part, stats, db_part, total;
-  WalkPlan fwd, bwd;  // the same for both directions: n and e are
+  WalkPlan plan;  // the same for both directions: n and e are
 };
 
 RelLayout rel_layout(const gnn_graph* g, const Shape& s, int buckets, bool aligned) {
-  const Shape w = lane_shape(s, lane_elems(s, aligned));
   const size_t row = size_t(s.H) * s.D;
   RelLayout L{};
-  L.fwd = walk_plan(g->n, g->e, w, kFwdPerSm, g->sm_count);
-  L.bwd = walk_plan(g->n, g->e, w, kBwdPerSm, g->sm_count);
-  const size_t workers = size_t(L.fwd.workers > L.bwd.workers ? L.fwd.workers : L.bwd.workers);
+  L.plan = walk_plan(g->n, g->e, lane_shape(s, lane_elems(s, aligned)), kPerSm, g->sm_count);
   size_t off = 0;
   auto take = [&](size_t bytes) {
     const size_t r = off;
     off += align_up(bytes > 0 ? bytes : 1, 256);
     return r;
   };
-  L.arrived = take(workers * 2 * sizeof(int));
-  const size_t fwd = size_t(L.fwd.workers) * 2 * (row + 2 * s.H) * 4;
-  const size_t bwd = size_t(L.bwd.workers) * 2 * (2 * row + s.H) * 4;
-  L.part = take(fwd > bwd ? fwd : bwd);
+  L.arrived = take(size_t(L.plan.workers) * 2 * sizeof(int));
+  // at least every pass's state: two rows and a number per head in pass 1
+  const size_t state = 2 * row + 2 * s.H;
+  L.part = take(size_t(L.plan.workers) * 2 * state * 4);
   L.stats = take(size_t(g->n) * s.H * 8);
-  L.db_part = take(size_t(L.bwd.blocks) * buckets * s.H * 8);
+  L.db_part = take(size_t(L.plan.blocks) * buckets * s.H * 8);
   L.total = off;
   return L;
 }
@@ -544,12 +544,12 @@ cudaError_t launch_transformer_rel_forward(const gnn_graph* g, const gnn_rel* re
   const bool aligned = aligned32(key) && aligned32(val);
   const int e = lane_elems(s, aligned);
   const RelLayout W = rel_layout(g, s, rel->buckets, aligned);
-  RelArgs A = rel_args(g, rel, s, q, key, val, scale, bias, W, W.fwd, e, ws);
+  RelArgs A = rel_args(g, rel, s, q, key, val, scale, bias, W, W.plan, e, ws);
   A.out = out;
   A.lse = lse;
   if (dt == GNN_F32)
-    return e == 8 ? fwd_t<float, 8>(A, W.fwd, st) : fwd_t<float, 4>(A, W.fwd, st);
-  return e == 16 ? fwd_t<__nv_bfloat16, 16>(A, W.fwd, st) : fwd_t<__nv_bfloat16, 8>(A, W.fwd, st);
+    return e == 8 ? fwd_t<float, 8>(A, W.plan, st) : fwd_t<float, 4>(A, W.plan, st);
+  return e == 16 ? fwd_t<__nv_bfloat16, 16>(A, W.plan, st) : fwd_t<__nv_bfloat16, 8>(A, W.plan, st);
 }
 
 cudaError_t launch_transformer_rel_backward(const gnn_graph* g, const gnn_rel* rel,
@@ -561,17 +561,17 @@ cudaError_t launch_transformer_rel_backward(const gnn_graph* g, const gnn_rel* r
   const bool aligned = aligned32(q) && aligned32(key) && aligned32(val) && aligned32(dout);
   const int e = lane_elems(s, aligned);
   const RelLayout W = rel_layout(g, s, rel->buckets, aligned);
-  RelArgs A = rel_args(g, rel, s, q, key, val, scale, bias, W, W.bwd, e, ws);
+  RelArgs A = rel_args(g, rel, s, q, key, val, scale, bias, W, W.plan, e, ws);
   A.lse_in = lse;
   A.dout = dout;
   A.dq = dq;
   A.dkey = dkey;
   A.dval = dval;
   if (dt == GNN_F32)
-    return e == 8 ? bwd_t<float, 8>(A, g, rel, W.bwd, dbias, st)
-                  : bwd_t<float, 4>(A, g, rel, W.bwd, dbias, st);
-  return e == 16 ? bwd_t<__nv_bfloat16, 16>(A, g, rel, W.bwd, dbias, st)
-                 : bwd_t<__nv_bfloat16, 8>(A, g, rel, W.bwd, dbias, st);
+    return e == 8 ? bwd_t<float, 8>(A, g, rel, W.plan, dbias, st)
+                  : bwd_t<float, 4>(A, g, rel, W.plan, dbias, st);
+  return e == 16 ? bwd_t<__nv_bfloat16, 16>(A, g, rel, W.plan, dbias, st)
+                 : bwd_t<__nv_bfloat16, 8>(A, g, rel, W.plan, dbias, st);
 }
 
 }  // namespace gnn
