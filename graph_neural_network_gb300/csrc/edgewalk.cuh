@@ -197,7 +197,7 @@ __device__ __forceinline__ void walk(P& p, const Walk& W, const WalkDir& D, cons
   };
 
   int lim = i < i1 ? row_end : e1;  // edges of node i in this segment end here
-  p.begin(i);  // (node 0 where there is no segment)
+  p.begin(live ? i : 0);  // without a segment i may be past the last node
   // Node ids (and buckets) of the next batch: the segment's next U edges, also
   // where they belong to the next node.
   int jn[U], bn[U];
