@@ -551,11 +551,15 @@ class RelPos:
         if bounds is None:
             if bidirectional and num_buckets % 2:
                 raise ValueError("a bidirectional rule needs an even number of buckets")
+            if not 0 < max_distance < 2 ** 31:
+                raise ValueError("max_distance must be a positive 32-bit number")
             side = num_buckets // 2 if bidirectional else num_buckets
             table = (ctypes.c_int32 * max(side, 1))()
             _native.check(lib.gnn_rel_log_bounds(side, int(max_distance), table),
                           "gnn_rel_log_bounds")
         else:
+            if not all(0 <= b < 2 ** 31 for b in bounds):
+                raise ValueError("bounds must be whole numbers of 32 bits, not negative")
             table = (ctypes.c_int32 * len(bounds))(*bounds)
         self.graph = g
         self.bounds = list(table)
@@ -788,6 +792,8 @@ class TransformerCheckpoint8(torch.autograd.Function):
 
     @staticmethod
     def forward(ctx, g, rel, q, key, val, bias, scale):
+        if (rel is None) != (bias is None):
+            raise ValueError("rel and bias go together")
         q, key, val = q.contiguous(), key.contiguous(), val.contiguous()
         if rel is None:
             out, _ = transformer_forward(g, q, key, val, scale)
@@ -947,7 +953,9 @@ def transformer_layer(g: Graph, x: torch.Tensor, q: torch.Tensor, key: torch.Ten
     norm, gate, residual scale and sum with x, and the norm before the next
     layer.  Returns (y, z) as norm_residual_forward does.  checkpoint8: the
     attention keeps 8-bit checkpoints of q, key and val for its backward pass
-    instead of the tensors."""
+    instead of the tensors.  To capture a training step into a CUDA graph, let no
+    eager autograd graph of the same leaves be alive (torch would order the
+    captured gradients behind the eager stream)."""
     if (rel is None) != (bias is None):
         raise ValueError("rel and bias go together")
     if checkpoint8:

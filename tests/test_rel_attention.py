@@ -292,3 +292,21 @@ def test_rows_on_odd_16_byte_boundaries(H, D, dtype):
     ref = layer_ref.attention(rp, ci, *at, D ** -0.5, bias, bucket, wide(feats[3]))
     names = ("dq", "dkey", "dval", "dbias")
     layer_ref.hold_attention({x: to_f64(t) for x, t in zip(names, g8)}, ref, dtype, "odd 8", names)
+
+
+@pytest.mark.parametrize("make", [testgraphs.star_in, testgraphs.star_out], ids=["in", "out"])
+def test_one_node_with_every_edge(make):
+    """A node whose edges run through all workers, as destination and as source."""
+    rp, ci = make(30_000)
+    check(rp, ci, 2, 16, "f32", what="star")
+    check(rp, ci, 4, 64, "bf16", what="star")
+
+
+def test_positions_and_bounds_outside_32_bits_are_refused():
+    import graph_neural_network_gb300 as gnn
+    g = device_graph(dict(row_ptr=np.zeros(7, np.int32), col=np.zeros(0, np.int32)))
+    pos = torch.arange(6, dtype=torch.int32, device="cuda")
+    for kw in (dict(bounds=[0, 2 ** 32 + 5]), dict(bounds=[0, -1]), dict(max_distance=2 ** 32 + 64),
+               dict(max_distance=0)):
+        with pytest.raises(ValueError):
+            gnn.RelPos(g, pos, **kw)

@@ -158,3 +158,94 @@ def test_no_gate_no_bias_no_projection():
     assert all(torch.isfinite(t.grad).all() for t in (q, k, v))
     with pytest.raises(ValueError):
         gnn.transformer_layer(g, x, q, k, v, rel=rel)
+
+
+def test_offsets_past_32_bits():
+    """A ring of 8.5M nodes with 512-byte rows: every row has one edge, so the
+    attention copies its source's value and the gradients are known; rows beyond
+    the first 4 GB go through every operator."""
+    import graph_neural_network_gb300 as gnn
+    n, D = 8_500_001, 128
+    if torch.cuda.mem_get_info()[0] < 64 << 30:
+        pytest.skip("needs 64 GB of free device memory")
+    rp = torch.arange(n + 1, dtype=torch.int32, device="cuda")
+    ci = torch.roll(torch.arange(n, dtype=torch.int32, device="cuda"), -1)
+    g = gnn.Graph(rp, ci)
+    rel = gnn.RelPos(g, torch.arange(n, dtype=torch.int32, device="cuda") % 1000)
+    gen = torch.Generator(device="cuda").manual_seed(1)
+    x = torch.randn(n, 1, D, generator=gen, device="cuda")
+    bias = torch.ones(32, 1, device="cuda")
+    out, lse = gnn.transformer_rel_forward(g, rel, x, x, x, bias)
+    assert torch.equal(out, torch.roll(x, -1, 0))
+    dq, dk, dv, db = gnn.transformer_rel_backward(g, rel, x, x, x, bias, lse, x)
+    # one weight a row: exp(e - lse) with both rounded, e below 32: 2^-17 covers it
+    top = float(x.abs().max())
+    assert float((dv - torch.roll(x, 1, 0)).abs().max()) <= 2.0 ** -17 * top
+    del dq, dk, dv, out
+    (p,) = gnn.pack8(x)
+    tail = slice(n - 1000, n)
+    (q,) = gnn.pack8(x[tail].contiguous())
+    assert torch.equal(p.values[tail], q.values) and torch.equal(p.scale[tail], q.scale)
+    dq, dk, dv = gnn.transformer_backward8(g, p, p, p, x)
+    assert float((dv - torch.roll(x, 1, 0)).abs().max()) <= 2.0 ** -17 * top
+    del dq, dk, dv
+    rows = x.view(n, D)
+    y, z = gnn.norm_residual_forward(rows, rows, rows)
+    ty, tz = gnn.norm_residual_forward(*(rows[tail].contiguous(),) * 3)
+    assert torch.equal(y[tail], ty) and torch.equal(z[tail], tz)
+    del z
+    gr = gnn.norm_residual_backward(y, rows, rows, rows, rows)
+    tr = gnn.norm_residual_backward(ty, *(rows[tail].contiguous(),) * 4)
+    for k in ("dx", "do", "dgate"):
+        assert torch.equal(gr[k][tail], tr[k]), k
+
+
+def test_two_streams_at_once():
+    """Calls that overlap on two streams, each with a workspace of its own."""
+    import graph_neural_network_gb300 as gnn
+    rp, ci = workload.chung_lu(50_000, 2.1, 20.0, 10_000.0, 3)
+    g = device_graph(dict(row_ptr=rp, col=ci))
+    n = len(rp) - 1
+    rel = gnn.RelPos(g, torch.arange(n, dtype=torch.int32, device="cuda"))
+    gen = torch.Generator(device="cuda").manual_seed(1)
+    sets = [[torch.randn(n, 4, 32, generator=gen, device="cuda") for _ in range(4)]
+            for _ in range(2)]
+    bias = torch.randn(32, 4, generator=gen, device="cuda")
+
+    def step(a, **kw):
+        q, k, v, d = a
+        out, lse = gnn.transformer_rel_forward(g, rel, q, k, v, bias, **kw)
+        r = gnn.transformer_rel_backward(g, rel, q, k, v, bias, lse, d, **kw)
+        p = gnn.pack8(q, k, v, **kw)
+        return (out, lse) + r + tuple(gnn.transformer_backward8(g, *p, d, rel=rel, bias=bias, **kw))
+
+    alone = [step(a) for a in sets]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    for _ in range(3):
+        both = [step(a, stream=s) for a, s in zip(sets, streams)]
+        torch.cuda.synchronize()
+        for x, y in zip(alone, both):
+            assert all(torch.equal(a, b) for a, b in zip(x, y))
+
+
+def test_rel_and_bias_go_together_in_autograd():
+    import graph_neural_network_gb300 as gnn
+    g, rel, x, par, graph, dy, dz = setup()
+    q = x.view(N, H, D)
+    with pytest.raises(ValueError):
+        gnn.TransformerCheckpoint8.apply(g, None, q, q, q, par[0]["bias"], None)
+    with pytest.raises(ValueError):
+        gnn.TransformerCheckpoint8.apply(g, rel, q, q, q, None, None)
+
+
+def test_autograd_without_the_second_norm():
+    import graph_neural_network_gb300 as gnn
+    g, rel, x, par, graph, dy, dz = setup()
+    a, o, w = (t.clone().requires_grad_(True) for t in (x, dz, par[0]["w_post"]))
+    y, z = gnn.NormResidual.apply(a, o, None, w, None, None, None, None, ("rms", "none"), 1e-6)
+    assert z is None
+    got = torch.autograd.grad(y, (a, o, w), dy)
+    want = gnn.norm_residual_backward(None, dz, dy, w_post=par[0]["w_post"], kind=("rms", "none"))
+    for t, k in zip(got, ("dx", "do", "dw_post")):
+        assert torch.equal(t, want[k]), k
