@@ -531,6 +531,11 @@ def _output(t, name, shape, dtype, device):
         _plain_tensor(t, name, shape, dtype, device)
 
 
+def _like(t, name, x):
+    """_output of x's shape, dtype and device (x contiguous)."""
+    return torch.empty_like(x) if t is None else _plain_tensor(t, name, x.shape, x.dtype, x.device)
+
+
 class RelPos:
     """Buckets of the relative positions of a graph's edges.
 
@@ -630,7 +635,7 @@ def transformer_rel_forward(g: Graph, rel: RelPos, q: torch.Tensor, key: torch.T
     entry of -inf masks its bucket."""
     N, H, D = _rel_qkv(g, q, key, val)
     bias = _rel_bias(g, rel, bias, H)
-    out = _output(out, "out", q.shape, q.dtype, g.device)
+    out = _like(out, "out", q)
     lse = _output(lse, "lse", (N, H), torch.float32, g.device)
     ws = _rel_ws(g, rel, H, D, q.dtype, ws)
     _launch(g._lib.transformer_rel_forward, "transformer_rel_forward", g.device, g.handle,
@@ -650,10 +655,10 @@ def transformer_rel_backward(g: Graph, rel: RelPos, q: torch.Tensor, key: torch.
     _plain_tensor(dout, "dout", shape, q.dtype, g.device)
     _plain_tensor(lse, "lse", (N, H), torch.float32, g.device)
     bias = _rel_bias(g, rel, bias, H)
-    dq = _output(dq, "dq", shape, q.dtype, g.device)
-    dkey = _output(dkey, "dkey", shape, q.dtype, g.device)
-    dval = _output(dval, "dval", shape, q.dtype, g.device)
-    dbias = _output(dbias, "dbias", bias.shape, torch.float32, g.device)
+    dq = _like(dq, "dq", q)
+    dkey = _like(dkey, "dkey", q)
+    dval = _like(dval, "dval", q)
+    dbias = _like(dbias, "dbias", bias)
     ws = _rel_ws(g, rel, H, D, q.dtype, ws)
     _launch(g._lib.transformer_rel_backward, "transformer_rel_backward", g.device, g.handle,
             rel.handle, H, D, _dtype_code(q.dtype), _at(q), _at(key), _at(val),
@@ -765,12 +770,12 @@ def transformer_backward8(g: Graph, q: Packed8, key: Packed8, val: Packed8, dout
         raise ValueError("rel and bias go together")
     if rel is not None:
         bias = _rel_bias(g, rel, bias, H)
-        dbias = _output(dbias, "dbias", bias.shape, torch.float32, device)
+        dbias = _like(dbias, "dbias", bias)
     elif dbias is not None:
         raise ValueError("there is no dbias without a bias")
-    dq = _output(dq, "dq", shape, dtype, device)
-    dkey = _output(dkey, "dkey", shape, dtype, device)
-    dval = _output(dval, "dval", shape, dtype, device)
+    dq = _like(dq, "dq", dout)
+    dkey = _like(dkey, "dkey", dout)
+    dval = _like(dval, "dval", dout)
     handle = None if rel is None else rel.handle
     dt = _dtype_code(dtype)
     if _check_ws(g, ws) is None:
@@ -837,16 +842,20 @@ def _norm_desc(o, gate, params, kind, eps):
     if gate is not None:
         width = F if isinstance(gate, torch.Tensor) and gate.shape == shape else 1
         _plain_tensor(gate, "gate", shape if width == F else (n, 1), dtype, device)
-    kept = []
+    kept, at, line = [], [], (F,)
     for k, t in zip(_NORM_PARAMS, params):
-        if t is not None:
+        if t is None:
+            at.append(None)
+        else:
             if not isinstance(t, torch.Tensor) or not t.is_floating_point():
                 raise TypeError(f"{k} must be a floating-point tensor")
-            if t.dtype != torch.float32:
+            if t.dtype is not torch.float32:
                 t = t.to(torch.float32)
-            _plain_tensor(t, k, (F,), torch.float32, device)
+            if t.shape != line or t.device != device or not t.is_contiguous():
+                _plain_tensor(t, k, line, torch.float32, device)
+            at.append(t.data_ptr())
         kept.append(t)
-    return (_native.NormResidual(n, F, post, pre, width, eps, *map(_at, kept)), kept, pre != 0)
+    return _native.NormResidual(n, F, post, pre, width, eps, *at), kept, pre != 0
 
 
 @_on_stream
@@ -861,13 +870,12 @@ def norm_residual_forward(x: torch.Tensor, o: torch.Tensor, gate=None, w_post=No
     Parameters have one entry per feature; None leaves a factor or a sum out.
     z is None where the second norm is "none"."""
     d, kept, pre = _norm_desc(o, gate, (w_post, b_post, scale, w_pre, b_pre), kind, eps)
-    like = (o.shape, o.dtype, o.device)
-    _plain_tensor(x, "x", *like)
+    _plain_tensor(x, "x", o.shape, o.dtype, o.device)
     if z is not None and not pre:
         raise ValueError("there is no z without a norm before the next block")
-    y = _output(y, "y", *like)
+    y = _like(y, "y", o)
     if pre:
-        z = _output(z, "z", *like)
+        z = _like(z, "z", o)
     _launch(_native.load().gnn_norm_residual_forward, "gnn_norm_residual_forward", o.device,
             ctypes.byref(d), _dtype_code(o.dtype), _at(x), _at(o), _at(gate), _at(y), _at(z))
     return y, z
@@ -895,7 +903,7 @@ def norm_residual_backward(y, o: torch.Tensor, dy: torch.Tensor, dz=None, gate=N
     for name, t in zip(_NORM_GRADS, (o, o, gate, *kept)):
         given = None if grads is None else grads.get(name)
         if t is not None:
-            got[name] = _output(given, name, t.shape, t.dtype, device)
+            got[name] = _like(given, name, t)
         elif given is None:
             got[name] = None
         else:

@@ -454,7 +454,7 @@ cudaError_t fwd_w(const NrArgs& A, int sm_count, cudaStream_t st) {
   auto kernel = any_layer(A) ? nr_fwd<T, WPR, true> : nr_fwd<T, WPR, false>;
   const int64_t slots = kThreads >> A.tpr_log2;
   const int64_t want = (A.n + slots - 1) / slots;
-  const int64_t cap = persistent_blocks(kernel, 0, sm_count);
+  const int64_t cap = int64_t(sm_count) * NrBlocks<T>::fwd;  // what the launch bounds allow
   kernel<<<unsigned(want < cap ? want : cap), kThreads, 0, st>>>(A);
   return cudaGetLastError();
 }
