@@ -178,6 +178,13 @@ __device__ __forceinline__ float total(const float (&x)[V]) {
   return a + b;
 }
 
+// x += s over a thread's vector.
+template <int V>
+__device__ __forceinline__ void shift(float (&x)[V], float s) {
+#pragma unroll
+  for (int c = 0; c < V; c += 2) add2(x[c], x[c + 1], x[c], x[c + 1], s, s);
+}
+
 // x becomes (x - mean) * rstd (rows of `kind`), rstd returned.  kLayer: a kind of
 // the call is the layer norm.
 template <typename T, int WPR, bool kLayer>
@@ -188,9 +195,7 @@ __device__ __forceinline__ float norm_row(const NrArgs& A, const Place& P, int k
   if (kLayer && kind == GNN_ROWNORM_LAYER) {
     float m[1] = {total<V>(x)};
     row_sums<WPR, 1>(m, A.tpr_log2, buf, turn);
-    const float mean = m[0] * A.inv_f;
-#pragma unroll
-    for (int c = 0; c < V; ++c) x[c] = P.in ? x[c] - mean : 0.f;
+    shift<V>(x, P.in ? -m[0] * A.inv_f : 0.f);
   }
   float q[1] = {dot<V>(x, x)};
   row_sums<WPR, 1>(q, A.tpr_log2, buf, turn);
@@ -248,6 +253,28 @@ __global__ void __launch_bounds__(kThreads, NrBlocks<T>::fwd) nr_fwd(const NrArg
       if (now) st16(reinterpret_cast<char*>(A.z) + 16 * at, pack<T>(y));
     }
   }
+}
+
+// Both rows of the backward pass at once: a and b become their normed rows (kinds ka,
+// kb), ra and rb their rstd (1 without a norm).  Half the chain of row sums of two
+// calls of norm_row: the pass waits for shuffles as much as for memory.
+template <typename T, int WPR, bool kLayer>
+__device__ __forceinline__ void norm_rows(const NrArgs& A, const Place& P, int ka, int kb,
+                                          float* buf, int& turn, float (&a)[VecOf<T>::n],
+                                          float (&b)[VecOf<T>::n], float& ra, float& rb) {
+  constexpr int V = VecOf<T>::n;
+  if (kLayer) {
+    float m[2] = {total<V>(a), total<V>(b)};
+    row_sums<WPR, 2>(m, A.tpr_log2, buf, turn);
+    shift<V>(a, P.in && ka == GNN_ROWNORM_LAYER ? -m[0] * A.inv_f : 0.f);
+    shift<V>(b, P.in && kb == GNN_ROWNORM_LAYER ? -m[1] * A.inv_f : 0.f);
+  }
+  float q[2] = {dot<V>(a, a), dot<V>(b, b)};
+  row_sums<WPR, 2>(q, A.tpr_log2, buf, turn);
+  ra = ka == GNN_ROWNORM_NONE ? 1.f : rsqrtf(fmaf(q[0], A.inv_f, A.eps));
+  rb = kb == GNN_ROWNORM_NONE ? 1.f : rsqrtf(fmaf(q[1], A.inv_f, A.eps));
+  scale<V>(a, ra);
+  scale<V>(b, rb);
 }
 
 // g becomes rstd (g - [mean(g)] - hat mean(g hat)): the gradient of the norm.
@@ -320,17 +347,17 @@ __global__ void __launch_bounds__(kThreads, kBwdPerSm) nr_bwd(const NrArgs A) {
     const bool now = ok;
     row += P.stride;
     load();
+    float rstd_y, rstd_o;
+    norm_rows<T, WPR, kLayer>(A, P, A.pre, A.post, buf, turn, y, o, rstd_y, rstd_o);
     if (pre) {
-      const float rstd = norm_row<T, WPR, kLayer>(A, P, A.pre, buf, turn, y);
       vfma<V>(acc[kSumW], g, y, acc[kSumW]);
       vadd<V>(acc[kSumC], g);
       vmul<V>(g, g, wn);
       float none = 0.f;
-      norm_grad<T, WPR, kLayer, false>(A, A.pre, rstd, y, buf, turn, g, none);
+      norm_grad<T, WPR, kLayer, false>(A, A.pre, rstd_y, y, buf, turn, g, none);
       vadd<V>(d, g);
     }
     if (now) st16(reinterpret_cast<char*>(A.dx) + 16 * at, pack<T>(d));
-    const float rstd = norm_row<T, WPR, kLayer>(A, P, A.post, buf, turn, o);
     // d becomes dx sigmoid(g) (0 on a thread without a vector or a row: it adds
     // nothing to the sums), y the gate's gradient d n (1 - sigmoid(g)), g = d wp
     if (!now) zero<V>(s);
@@ -347,7 +374,7 @@ __global__ void __launch_bounds__(kThreads, kBwdPerSm) nr_bwd(const NrArgs A) {
       vmul<V>(y, y, s);
       if (kRow) all = total<V>(y);
     }
-    norm_grad<T, WPR, kLayer, kRow>(A, A.post, rstd, o, buf, turn, g, all);
+    norm_grad<T, WPR, kLayer, kRow>(A, A.post, rstd_o, o, buf, turn, g, all);
     if (now) {
       st16(reinterpret_cast<char*>(A.dout) + 16 * at, pack<T>(g));
       if (kRow) {
