@@ -590,6 +590,17 @@ class RelPos:
             self._lib.gnn_rel_destroy(h)
             self.handle = None
 
+    def workspace(self, H: int, D: int, dtype: torch.dtype) -> torch.Tensor:
+        """A workspace that serves transformer_rel_forward, transformer_rel_backward
+        and transformer_backward8 with this plan (one call at a time)."""
+        dt = _dtype_code(dtype)
+        n = max(f(self.graph.handle, self.handle, H, D, dt) for f in (
+            self._lib.transformer_rel_workspace_bytes,
+            self._lib.transformer_packed8_workspace_bytes))
+        if n == 0:
+            raise GnnError(_native.ERR_UNSUPPORTED, f"(H={H}, D={D}, {dtype})")
+        return torch.empty(n, dtype=torch.uint8, device=self.graph.device)
+
     def arrays(self):
         """The buckets of the edges, uint8 [E], in CSR and in CSC order (views)."""
         ptrs = (ctypes.c_void_p * 2)()

@@ -249,3 +249,38 @@ def test_autograd_without_the_second_norm():
     want = gnn.norm_residual_backward(None, dz, dy, w_post=par[0]["w_post"], kind=("rms", "none"))
     for t, k in zip(got, ("dx", "do", "dw_post")):
         assert torch.equal(t, want[k]), k
+
+
+def test_nothing_is_allocated_with_outputs_and_workspaces_given():
+    import graph_neural_network_gb300 as gnn
+    g, rel, x, par, graph, dy, dz = setup()
+    q, k, v, d = (t.view(N, H, D) for t in (x, dy, dz, x))
+    b, w = par[0]["bias"], par[0]["w_post"]
+    ws = rel.workspace(H, D, torch.float32)
+    out, lse = gnn.transformer_rel_forward(g, rel, q, k, v, b, ws=ws)
+    dq, dk, dv, db = gnn.transformer_rel_backward(g, rel, q, k, v, b, lse, d, ws=ws)
+    packed = gnn.pack8(q, k, v)
+    back = gnn.unpack8(packed[0])
+    y, z = gnn.norm_residual_forward(x, dy, dz, w, w_pre=w)
+    grads = gnn.norm_residual_backward(y, dy, dy, dz, dz, w, w_pre=w)
+    nws = torch.empty(1 << 22, dtype=torch.uint8, device="cuda")
+    want = [t.clone() for t in (out, lse, dq, dk, dv, db, back, y, z)]
+    torch.cuda.synchronize()
+    before = torch.cuda.memory_stats()["allocation.all.allocated"]
+    gnn.transformer_rel_forward(g, rel, q, k, v, b, out=out, lse=lse, ws=ws)
+    gnn.transformer_rel_backward(g, rel, q, k, v, b, lse, d, dq=dq, dkey=dk, dval=dv, dbias=db,
+                                 ws=ws)
+    gnn.pack8(q, k, v, out=packed)
+    gnn.unpack8(packed[0], out=back)
+    gnn.norm_residual_forward(x, dy, dz, w, w_pre=w, y=y, z=z)
+    gnn.norm_residual_backward(y, dy, dy, dz, dz, w, w_pre=w, grads=grads, ws=nws)
+    assert torch.cuda.memory_stats()["allocation.all.allocated"] == before
+    for a, c in zip(want, (out, lse, dq, dk, dv, db, back, y, z)):
+        assert torch.equal(a, c)
+    # the comparisons above allocate their own results
+    before = torch.cuda.memory_stats()["allocation.all.allocated"]
+    gnn.transformer_backward8(g, *packed, d, rel=rel, bias=b, dq=dq, dkey=dk, dval=dv, dbias=db,
+                              ws=ws)
+    assert torch.cuda.memory_stats()["allocation.all.allocated"] == before
+    with pytest.raises(gnn.GnnError):
+        rel.workspace(1, 256, torch.float32)
