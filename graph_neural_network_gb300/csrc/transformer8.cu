@@ -271,7 +271,8 @@ struct DstPass {
 // pass 2: source side
 // ---------------------------------------------------------------------------
 
-template <typename T, int kE_, bool kRel>
+// kPair: the form of the bias gradient's tables.
+template <typename T, int kE_, bool kRel, bool kPair>
 struct SrcPass {
   static constexpr int kE = kE_;
   static constexpr int U = SrcEdges<kE>::value;
@@ -354,7 +355,7 @@ struct SrcPass {
       if (!ok[u]) continue;
       const float al = ex2(e - st[u].x);
       const float de = al * fmaf(red[U + u], vsc, -st[u].y);
-      if (kRel && L.head_leader(A.s, 0)) add_grad(hist, A.s, bk[u], de);
+      if (kRel) add_grad<kPair>(hist, A.s, L.head_leader(A.s, 0), bk[u], de);
       float x[kE];
       widen<kE>(rq[u], x);
       axpy<kE>(dk, de * A.scale * st[u].z, x);
@@ -395,23 +396,24 @@ __global__ void __launch_bounds__(kThreads, kPerSm) t8_dst(const __grid_constant
   walk(p, A.walk, A.dir, A.s, L);
 }
 
-template <typename T, int kE, bool kRel>
+template <typename T, int kE, bool kRel, bool kPair>
 __global__ void __launch_bounds__(kThreads, kPerSm) t8_src(const __grid_constant__ T8Args A) {
   extern __shared__ __align__(16) unsigned char smem[];
   const Lane<1> L(A.s);
   __shared__ __align__(16) unsigned char held[kWarps * HeldT<float, kE>::kBytes];
-  SrcPass<T, kE, kRel> p(A, L);
+  SrcPass<T, kE, kRel, kPair> p(A, L);
   p.v.place(held + (threadIdx.x >> 5) * HeldT<float, kE>::kBytes, L.lane);
   float* tables = nullptr;
   p.sb = nullptr;
   p.hist = nullptr;
   if (kRel) {
-    tables = reinterpret_cast<float*>(smem) + A.buckets * A.s.H;
+    tables = reinterpret_cast<float*>(smem);
     p.hist = clear_grad_tables(tables, A.s, L, A.buckets);
-    p.sb = stage_bias(A.bias, A.buckets * A.s.H, smem) + L.k[0];
+    p.sb = stage_bias(A.bias, A.buckets * A.s.H, smem + grad_tables_bytes(A.s, A.buckets)) +
+           L.k[0];
   }
   walk(p, A.walk, A.dir, A.s, L);
-  if (kRel) fold_grad_tables(tables, A.s, L, A.buckets, A.db_part);
+  if (kRel) fold_grad_tables<kPair>(tables, A.s, L, A.buckets, A.db_part);
 }
 
 template <typename K>
@@ -441,7 +443,9 @@ cudaError_t bwd8_t(T8Args A, const gnn_graph* g, const gnn_rel* rel, const WalkP
   A.dir = WalkDir{g->csc.ptr, g->csc.idx, rel ? rel->csc : nullptr};
   A.walk = src;
   const size_t grads = kRel ? grad_tables_bytes(A.s, A.buckets) : 0;
-  if ((e = launch(t8_src<T, kE, kRel>, A, p.blocks, table + grads, st)) != cudaSuccess) return e;
+  const auto src_pass = kRel && grad_pairs(A.s, A.buckets) ? t8_src<T, kE, kRel, kRel>
+                                                           : t8_src<T, kE, kRel, false>;
+  if ((e = launch(src_pass, A, p.blocks, table + grads, st)) != cudaSuccess) return e;
   return kRel ? launch_dbias_sum(A.db_part, p.blocks, A.buckets * A.s.H, dbias, st) : cudaSuccess;
 }
 

@@ -276,7 +276,7 @@ struct RelDst {
 
 // ---- backward pass 2: source side --------------------------------------------
 
-template <typename T, int kE_>
+template <typename T, int kE_, bool kPair>
 struct RelSrc {
   static constexpr int kE = kE_;
   static constexpr int U = RelEdges<kE * int(sizeof(T)), kSrcEdges>::value;
@@ -343,7 +343,7 @@ struct RelSrc {
       if (!ok[u]) continue;
       const float al = ex2(fmaf(red[u], A.scale2, bs[u]) - st[u].x);
       const float de = al * (red[U + u] - st[u].y);
-      if (L.head_leader(A.s, 0)) add_grad(hist, A.s, bk[u], de);
+      add_grad<kPair>(hist, A.s, L.head_leader(A.s, 0), bk[u], de);
       float x[kE];
       widenT<T, kE>(rq[u], x);
       axpy<kE>(dk, de, x);
@@ -399,19 +399,20 @@ __global__ void __launch_bounds__(kThreads, kPerSm) rel_dst(const __grid_constan
   walk(p, A.walk, A.dir, A.s, L);
 }
 
-template <typename T, int kE>
+template <typename T, int kE, bool kPair>
 __global__ void __launch_bounds__(kThreads, kPerSm) rel_src(const __grid_constant__ RelArgs A) {
   extern __shared__ __align__(16) unsigned char smem[];
   const Lane<1> L(A.s);
   __shared__ __align__(16) unsigned char held[2 * kWarps * HeldT<T, kE>::kBytes];
-  RelSrc<T, kE> p(A, L);
+  RelSrc<T, kE, kPair> p(A, L);
   p.k.place(held + (threadIdx.x >> 5) * HeldT<T, kE>::kBytes, L.lane);
   p.v.place(held + (kWarps + (threadIdx.x >> 5)) * HeldT<T, kE>::kBytes, L.lane);
-  float* tables = reinterpret_cast<float*>(smem) + A.buckets * A.s.H;
+  float* tables = reinterpret_cast<float*>(smem);
   p.hist = clear_grad_tables(tables, A.s, L, A.buckets);
-  p.sb = stage_bias(A.bias, A.buckets * A.s.H, smem) + L.k[0];
+  p.sb = stage_bias(A.bias, A.buckets * A.s.H, smem + grad_tables_bytes(A.s, A.buckets)) +
+         L.k[0];
   walk(p, A.walk, A.dir, A.s, L);
-  fold_grad_tables(tables, A.s, L, A.buckets, A.db_part);
+  fold_grad_tables<kPair>(tables, A.s, L, A.buckets, A.db_part);
 }
 
 // dbias[x] = sum over the blocks of pass 2, one warp per entry.
@@ -496,7 +497,9 @@ cudaError_t bwd_t(RelArgs A, const gnn_graph* g, const gnn_rel* rel, const WalkP
   if ((e = launch(rel_dst<T, kE>, A, p.blocks, table, st)) != cudaSuccess) return e;
   A.dir = WalkDir{g->csc.ptr, g->csc.idx, rel->csc};
   A.walk = src;
-  if ((e = launch(rel_src<T, kE>, A, p.blocks, table + grad_tables_bytes(A.s, A.buckets), st)) !=
+  const auto src_pass =
+      grad_pairs(A.s, A.buckets) ? rel_src<T, kE, true> : rel_src<T, kE, false>;
+  if ((e = launch(src_pass, A, p.blocks, table + grad_tables_bytes(A.s, A.buckets), st)) !=
       cudaSuccess)
     return e;
   return launch_dbias_sum(A.db_part, p.blocks, A.buckets * A.s.H, dbias, st);

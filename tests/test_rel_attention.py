@@ -310,3 +310,38 @@ def test_positions_and_bounds_outside_32_bits_are_refused():
                dict(max_distance=0)):
         with pytest.raises(ValueError):
             gnn.RelPos(g, pos, **kw)
+
+
+def test_bias_gradient_is_no_worse_than_its_terms():
+    """Six million edges, most into 2 x 4 sums: the error stays that of the terms, however
+    long the columns that add them.  A term de = alpha (da - Delta) carries the
+    rounding of a dot product of 64 products in each factor, of the exponential
+    and of two subtractions, all of random sign: under ten half steps in the root
+    of the mean square, which N independent terms keep as sqrt(sum de^2)."""
+    import graph_neural_network_gb300 as gnn
+    n, deg, H, D = 300_000, 20, 4, 64
+    gen = torch.Generator("cuda").manual_seed(5)
+    rp = torch.arange(0, n * deg + 1, deg, dtype=torch.int32, device="cuda")
+    ci = torch.randint(n, (n * deg,), generator=gen, device="cuda", dtype=torch.int32)
+    pos = torch.randint(1 << 16, (n,), generator=gen, device="cuda", dtype=torch.int32)
+    g = gnn.Graph(rp, ci)
+    rel = gnn.RelPos(g, pos, 32, 128)          # nearly every edge in the two last buckets
+    q, k, v, d = (torch.randn(n, H, D, generator=gen, device="cuda").bfloat16() for _ in range(4))
+    b = torch.randn(32, H, generator=gen, device="cuda")
+    _, lse = gnn.transformer_rel_forward(g, rel, q, k, v, b)
+    got = gnn.transformer_rel_backward(g, rel, q, k, v, b, lse, d)[3].double()
+    bucket = rel.arrays()[0].long().view(n, deg)
+    want, square = (torch.zeros(32, H, dtype=torch.float64, device="cuda") for _ in range(2))
+    step = 25_000
+    for r in range(0, n, step):
+        at, j = bucket[r:r + step], ci.view(n, deg)[r:r + step].long()
+        for h in range(H):
+            own = lambda t: t[r:r + step, None, h].double()  # noqa: E731
+            e = (own(q) * k[:, h].double()[j]).sum(-1) * D ** -0.5 + b[:, h].double()[at]
+            al = torch.softmax(e, 1)
+            da = (own(d) * v[:, h].double()[j]).sum(-1)
+            de = al * (da - (al * da).sum(1, keepdim=True))
+            want[:, h].index_add_(0, at.reshape(-1), de.reshape(-1))
+            square[:, h].index_add_(0, at.reshape(-1), (de * de).reshape(-1))
+    error = (got - want).norm() / square.sum().sqrt()
+    assert error <= 10 * 2.0 ** -24, float(error)
