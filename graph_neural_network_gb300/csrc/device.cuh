@@ -614,4 +614,36 @@ __host__ int persistent_blocks(K kernel, size_t smem, int sm_count) {
   return per_sm * (sm_count > 0 ? sm_count : 1);
 }
 
+// A kernel launched by launch_after may start while the kernel before it in the
+// stream still runs, once every block of that one has called let_next_start or
+// ended.  grid_wait waits until that kernel is complete and its writes are seen; it
+// returns at once in a kernel launched otherwise.
+__device__ __forceinline__ void let_next_start() {
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+}
+__device__ __forceinline__ void grid_wait() {
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+}
+
+// kernel<<<grid, threads, smem, st>>>(args...), started early as above, for a kernel
+// that follows another of the same call: before grid_wait it may read what was
+// complete when that one began, through loads that grid_wait orders (no __ldg of what
+// that one writes).  Its start and its set-up then hide under the end of that
+// kernel: 5 us of a backward call.
+template <typename... Params, typename... Args>
+inline cudaError_t launch_after(void (*kernel)(Params...), dim3 grid, int threads, size_t smem,
+                                cudaStream_t st, const Args&... args) {
+  cudaLaunchAttribute early{};
+  early.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  early.val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(unsigned(threads));
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = st;
+  cfg.attrs = &early;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, Params(args)...);
+}
+
 }  // namespace gnn

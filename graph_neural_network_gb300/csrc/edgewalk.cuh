@@ -169,6 +169,7 @@ __device__ __forceinline__ void walk(P& p, const Walk& W, const WalkDir& D, cons
     ahead = __ldg(D.ptr + (i + 2 < W.n ? i + 2 : W.n));
   }
   __syncthreads();  // the block's tables are staged
+  grid_wait();      // and the pass before, whose results batch() may read, is complete
   const int nf = P::floats(s);
 
   // Hands over a piece of node i; the last to arrive finishes the node.

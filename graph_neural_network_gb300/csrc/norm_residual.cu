@@ -384,6 +384,7 @@ __global__ void __launch_bounds__(kThreads, kBwdPerSm) nr_bwd(const NrArgs A) {
       }
     }
   }
+  let_next_start();
   // the block's sums, its row slots added in order in float64
   const int slots = kThreads >> A.tpr_log2;
 #pragma unroll
@@ -404,25 +405,29 @@ __global__ void __launch_bounds__(kThreads, kBwdPerSm) nr_bwd(const NrArgs A) {
 
 // Parameter gradients from the blocks' sums, in a fixed order: a block takes 16
 // channels and two of their four sums (a and b, blockIdx.y 0, or dw_pre and
-// db_pre), in 32 slices of blocks with four loads in flight.
-constexpr int kSlices = 32;
+// db_pre), in 32 slices of blocks, every load of a slice in flight at once.
+constexpr int kSlices = 32, kLoads = 10;  // 320 blocks at once
 __global__ void __launch_bounds__(kSlices * 32)
     nr_sum(const double* part, int blocks, int F, const gnn_norm_params p,
            const gnn_norm_grads d) {
   __shared__ double t[kSlices][33];
   const int lane = threadIdx.x & 31, slice = threadIdx.x >> 5;
   const int f = blockIdx.x * 16 + (lane & 15), k = 2 * blockIdx.y + (lane >> 4);
-  double s[4] = {0.0, 0.0, 0.0, 0.0};
+  double s = 0.0;
+  grid_wait();
   if (f < F) {
     const double* at = part + k * F + f;
     const int64_t step = int64_t(kSums) * F;
-    int b = slice;
-    for (; b + 3 * kSlices < blocks; b += 4 * kSlices)
+    for (int b = slice; b < blocks; b += kLoads * kSlices) {
+      double v[kLoads];
 #pragma unroll
-      for (int u = 0; u < 4; ++u) s[u] += at[(b + u * kSlices) * step];
-    for (; b < blocks; b += kSlices) s[0] += at[b * step];
+      for (int u = 0; u < kLoads; ++u)
+        v[u] = b + u * kSlices < blocks ? at[(b + u * kSlices) * step] : 0.0;
+#pragma unroll
+      for (int u = 0; u < kLoads; ++u) s += v[u];
+    }
   }
-  t[slice][lane] = (s[0] + s[1]) + (s[2] + s[3]);
+  t[slice][lane] = s;
   __syncthreads();
   if (slice != 0) return;
   double first = 0.0;
@@ -495,9 +500,8 @@ cudaError_t bwd_w(const NrArgs& A, const gnn_norm_grads& d, cudaStream_t st) {
   kernel<<<unsigned(A.blocks), kThreads, smem, st>>>(A);
   cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return e;
-  nr_sum<<<dim3(unsigned((A.F + 15) / 16), 2), kSlices * 32, 0, st>>>(A.part, A.blocks, A.F, A.p,
-                                                                      d);
-  return cudaGetLastError();
+  return launch_after(nr_sum, dim3(unsigned((A.F + 15) / 16), 2), kSlices * 32, 0, st, A.part,
+                      A.blocks, A.F, A.p, d);
 }
 
 // Warps per row from the threads per row: 1 (a part or all of one), 2 or 4.

@@ -319,7 +319,8 @@ struct SrcPass {
     for (int u = 0; u < U; ++u) {
       rq[u] = ld8<kE>(r0.at(i[u]));
       rg[u] = ldT<T, kE>(r1.at(i[u]));
-      st[u] = of_head(A.stats + L.k[0], i[u], A.s);
+      // (no __ldg: pass 1 may still be writing when this kernel starts)
+      st[u] = A.stats[L.k[0] + uint64_t(uint32_t(i[u])) * uint32_t(A.s.H)];
     }
     float bs[U];
     int bk[U];
@@ -387,6 +388,7 @@ constexpr int kPerSm = 2;  // resident blocks
 
 template <typename T, int kE, bool kRel>
 __global__ void __launch_bounds__(kThreads, kPerSm) t8_dst(const __grid_constant__ T8Args A) {
+  let_next_start();
   extern __shared__ __align__(16) unsigned char smem[];
   const Lane<1> L(A.s);
   __shared__ __align__(16) unsigned char held[kWarps * HeldT<T, kE>::kBytes];
@@ -413,17 +415,21 @@ __global__ void __launch_bounds__(kThreads, kPerSm) t8_src(const __grid_constant
            L.k[0];
   }
   walk(p, A.walk, A.dir, A.s, L);
-  if (kRel) fold_grad_tables<kPair>(tables, A.s, L, A.buckets, A.db_part);
+  if (!kRel) return;
+  let_next_start();
+  fold_grad_tables<kPair>(tables, A.s, L, A.buckets, A.db_part);
 }
 
-template <typename K>
-cudaError_t launch(K kernel, const T8Args& A, int blocks, size_t smem, cudaStream_t st) {
+// after: launched behind the first pass of the same call (launch_after).
+cudaError_t launch(void (*kernel)(T8Args), const T8Args& A, int blocks, size_t smem,
+                   cudaStream_t st, bool after = false) {
   cudaError_t e;
   // (the default limit, 48 KB, counts the kernels' static 16 KB too)
   if (smem > 32 * 1024 &&
       (e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, int(smem))) !=
           cudaSuccess)
     return e;
+  if (after) return launch_after(kernel, dim3(unsigned(blocks)), kThreads, smem, st, A);
   kernel<<<unsigned(blocks), kThreads, smem, st>>>(A);
   return cudaGetLastError();
 }
@@ -445,7 +451,7 @@ cudaError_t bwd8_t(T8Args A, const gnn_graph* g, const gnn_rel* rel, const WalkP
   const size_t grads = kRel ? grad_tables_bytes(A.s, A.buckets) : 0;
   const auto src_pass = kRel && grad_pairs(A.s, A.buckets) ? t8_src<T, kE, kRel, kRel>
                                                            : t8_src<T, kE, kRel, false>;
-  if ((e = launch(src_pass, A, p.blocks, table + grads, st)) != cudaSuccess) return e;
+  if ((e = launch(src_pass, A, p.blocks, table + grads, st, true)) != cudaSuccess) return e;
   return kRel ? launch_dbias_sum(A.db_part, p.blocks, A.buckets * A.s.H, dbias, st) : cudaSuccess;
 }
 

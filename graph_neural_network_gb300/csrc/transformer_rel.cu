@@ -313,7 +313,8 @@ struct RelSrc {
     for (int u = 0; u < U; ++u) {
       rq[u] = ldT<T, kE>(r0.at(i[u]));
       rg[u] = ldT<T, kE>(r1.at(i[u]));
-      st[u] = __ldg(A.stats + L.k[0] + uint64_t(uint32_t(i[u])) * uint32_t(A.s.H));
+      // (no __ldg: pass 1 may still be writing when this kernel starts)
+      st[u] = A.stats[L.k[0] + uint64_t(uint32_t(i[u])) * uint32_t(A.s.H)];
     }
     float bs[U];
     int bk[U];
@@ -389,6 +390,7 @@ __global__ void __launch_bounds__(kThreads, kPerSm) rel_fwd(const __grid_constan
 
 template <typename T, int kE>
 __global__ void __launch_bounds__(kThreads, kPerSm) rel_dst(const __grid_constant__ RelArgs A) {
+  let_next_start();
   extern __shared__ __align__(16) unsigned char smem[];
   const Lane<1> L(A.s);
   __shared__ __align__(16) unsigned char held[2 * kWarps * HeldT<T, kE>::kBytes];
@@ -412,6 +414,7 @@ __global__ void __launch_bounds__(kThreads, kPerSm) rel_src(const __grid_constan
   p.sb = stage_bias(A.bias, A.buckets * A.s.H, smem + grad_tables_bytes(A.s, A.buckets)) +
          L.k[0];
   walk(p, A.walk, A.dir, A.s, L);
+  let_next_start();
   fold_grad_tables<kPair>(tables, A.s, L, A.buckets, A.db_part);
 }
 
@@ -420,6 +423,7 @@ __global__ void __launch_bounds__(kThreads) dbias_sum(const double* part, int bl
                                                       float* dbias) {
   const int x = blockIdx.x * kWarps + (threadIdx.x >> 5);
   if (x >= entries) return;
+  grid_wait();
   double sum = 0.0;
   for (int b = threadIdx.x & 31; b < blocks; b += 32) sum += part[int64_t(b) * entries + x];
 #pragma unroll
@@ -462,14 +466,16 @@ RelLayout rel_layout(const gnn_graph* g, const Shape& s, int buckets, bool align
   return L;
 }
 
-template <typename K>
-cudaError_t launch(K kernel, const RelArgs& A, int blocks, size_t smem, cudaStream_t st) {
+// after: launched behind the first pass of the same call (launch_after).
+cudaError_t launch(void (*kernel)(RelArgs), const RelArgs& A, int blocks, size_t smem,
+                   cudaStream_t st, bool after = false) {
   cudaError_t e;
   // (the default limit, 48 KB, counts the kernels' static 16 KB too)
   if (smem > 32 * 1024 &&
       (e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, int(smem))) !=
           cudaSuccess)
     return e;
+  if (after) return launch_after(kernel, dim3(unsigned(blocks)), kThreads, smem, st, A);
   kernel<<<unsigned(blocks), kThreads, smem, st>>>(A);
   return cudaGetLastError();
 }
@@ -499,7 +505,7 @@ cudaError_t bwd_t(RelArgs A, const gnn_graph* g, const gnn_rel* rel, const WalkP
   A.walk = src;
   const auto src_pass =
       grad_pairs(A.s, A.buckets) ? rel_src<T, kE, true> : rel_src<T, kE, false>;
-  if ((e = launch(src_pass, A, p.blocks, table + grad_tables_bytes(A.s, A.buckets), st)) !=
+  if ((e = launch(src_pass, A, p.blocks, table + grad_tables_bytes(A.s, A.buckets), st, true)) !=
       cudaSuccess)
     return e;
   return launch_dbias_sum(A.db_part, p.blocks, A.buckets * A.s.H, dbias, st);
@@ -529,9 +535,8 @@ RelArgs rel_args(const gnn_graph* g, const gnn_rel* rel, const Shape& s, const v
 
 cudaError_t launch_dbias_sum(const double* part, int blocks, int entries, float* dbias,
                              cudaStream_t st) {
-  dbias_sum<<<unsigned((entries + kWarps - 1) / kWarps), kThreads, 0, st>>>(part, blocks, entries,
-                                                                           dbias);
-  return cudaGetLastError();
+  return launch_after(dbias_sum, dim3(unsigned((entries + kWarps - 1) / kWarps)), kThreads, 0, st,
+                      part, blocks, entries, dbias);
 }
 
 size_t transformer_rel_ws_bytes(const gnn_graph* g, const Shape& s, int buckets) {
