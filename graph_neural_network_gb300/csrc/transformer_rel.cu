@@ -44,21 +44,24 @@ struct RelArgs {
 };
 
 // Edges in flight per lane, for lane vectors of 32 bytes (twice as many of 16): as
-// many as the registers of 16 warps an SM hold beside the accumulators.  300k-node
-// graph: forward 595 us with four and 2 blocks, 672 with two and 3; pass 1 752 with
-// three, 817 with two; pass 2 920 with two, 929 with three.
-template <int kBytes, int kEdges>
+// many as the registers of 16 warps an SM hold beside the accumulators, of which
+// float32 lanes have half as many.  300k-node bfloat16 graph: forward 595 us with
+// four and 2 blocks, 672 with two and 3; pass 1 752 with three, 817 with two; pass 2
+// 920 with two, 929 with three.  100k-node float32 graph, training step: 499 us with
+// three in pass 2, 524 with two.
+template <typename T, int kE, int kBf16, int kF32>
 struct RelEdges {
-  static constexpr int value = kEdges * (32 / kBytes);
+  static constexpr int value =
+      (sizeof(T) == 4 ? kF32 : kBf16) * (32 / (kE * int(sizeof(T))));
 };
-constexpr int kFwdEdges = 4, kDstEdges = 3, kSrcEdges = 2;
+constexpr int kFwdEdges = 4, kDstEdges = 3, kDstEdgesF32 = 3, kSrcEdges = 2, kSrcEdgesF32 = 3;
 
 // ---- forward -----------------------------------------------------------------
 
 template <typename T, int kE_>
 struct RelFwd {
   static constexpr int kE = kE_;
-  static constexpr int U = RelEdges<kE * int(sizeof(T)), kFwdEdges>::value;
+  static constexpr int U = RelEdges<T, kE, kFwdEdges, kFwdEdges>::value;
   static constexpr int kRow = kE * int(sizeof(T));
   static constexpr bool kBuckets = true;
   const RelArgs& A;
@@ -170,7 +173,7 @@ struct RelFwd {
 template <typename T, int kE_>
 struct RelDst {
   static constexpr int kE = kE_;
-  static constexpr int U = RelEdges<kE * int(sizeof(T)), kDstEdges>::value;
+  static constexpr int U = RelEdges<T, kE, kDstEdges, kDstEdgesF32>::value;
   static constexpr int kRow = kE * int(sizeof(T));
   static constexpr bool kBuckets = true;
   const RelArgs& A;
@@ -279,7 +282,7 @@ struct RelDst {
 template <typename T, int kE_, bool kPair>
 struct RelSrc {
   static constexpr int kE = kE_;
-  static constexpr int U = RelEdges<kE * int(sizeof(T)), kSrcEdges>::value;
+  static constexpr int U = RelEdges<T, kE, kSrcEdges, kSrcEdgesF32>::value;
   static constexpr int kRow = kE * int(sizeof(T));
   static constexpr bool kBuckets = true;
   const RelArgs& A;
