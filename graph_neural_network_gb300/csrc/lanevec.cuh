@@ -113,13 +113,16 @@ struct HeldT {
                    "l"(from + 16 * k)
                    : "memory");
   }
-  // float32: values computed by this lane
+  // values computed by this lane
   __device__ __forceinline__ void put(const float (&x)[kE]) {
+    constexpr int V = VecOf<T>::n;
 #pragma unroll
-    for (int k = 0; k < kParts; ++k)
-      asm volatile("st.shared.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(at + 512 * k), "f"(x[4 * k]),
-                   "f"(x[4 * k + 1]), "f"(x[4 * k + 2]), "f"(x[4 * k + 3])
+    for (int k = 0; k < kParts; ++k) {
+      const uint4 v = pack<T>(*reinterpret_cast<const float(*)[V]>(x + V * k));
+      asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(at + 512 * k), "r"(v.x),
+                   "r"(v.y), "r"(v.z), "r"(v.w)
                    : "memory");
+    }
   }
   // after held_ready() or put()
   __device__ __forceinline__ RawT<T, kE> get() const {

@@ -289,7 +289,9 @@ struct SrcPass {
   float ksc, vsc;
   Raw8<kE> v8;
   bool fresh;              // v8 not widened yet (begin waits for no load)
-  HeldT<float, kE> v;      // v8_j as floats
+  // v8_j, exact in bfloat16 too, where both halves of the product stay packed (300k-node
+  // graph: 1,699 us a call, 1,730 with floats)
+  HeldT<T, kE> v;
   float dk[kE], dv[kE];
 
   __device__ __forceinline__ SrcPass(const T8Args& a, const Lane<1>& lane)
@@ -339,15 +341,12 @@ struct SrcPass {
       v.put(x);
       fresh = false;
     }
-    float own[kE];
-    widenT<float, kE>(v.get(), own);
+    const RawT<T, kE> own = v.get();
     float red[2 * U];
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-      float x[kE];
       red[u] = dot8<kE>(rq[u], k8);
-      widenT<T, kE>(rg[u], x);
-      red[U + u] = dot<kE>(x, own);
+      red[U + u] = dotT<kE>(own, rg[u]);
     }
     head_sums<2 * U>(red, A.s.hv_log2);
 #pragma unroll
@@ -402,9 +401,9 @@ template <typename T, int kE, bool kRel, bool kPair>
 __global__ void __launch_bounds__(kThreads, kPerSm) t8_src(const __grid_constant__ T8Args A) {
   extern __shared__ __align__(16) unsigned char smem[];
   const Lane<1> L(A.s);
-  __shared__ __align__(16) unsigned char held[kWarps * HeldT<float, kE>::kBytes];
+  __shared__ __align__(16) unsigned char held[kWarps * HeldT<T, kE>::kBytes];
   SrcPass<T, kE, kRel, kPair> p(A, L);
-  p.v.place(held + (threadIdx.x >> 5) * HeldT<float, kE>::kBytes, L.lane);
+  p.v.place(held + (threadIdx.x >> 5) * HeldT<T, kE>::kBytes, L.lane);
   float* tables = nullptr;
   p.sb = nullptr;
   p.hist = nullptr;
