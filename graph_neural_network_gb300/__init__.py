@@ -498,7 +498,7 @@ def _on_stream(fn):
 def _launch(fn, what: str, device, *args):
     """fn(*args, the device's current stream), with the device current."""
     index = device.index
-    if torch.cuda.current_device() == index:
+    if torch._C._cuda_getDevice() == index:
         rc = fn(*args, torch._C._cuda_getCurrentRawStream(index))
     else:
         with torch.cuda.device(device):
@@ -726,8 +726,9 @@ def pack8(*xs: torch.Tensor, out=None):
         _plain_tensor(t, "every tensor", shape, x.dtype, device)
     N, H, D = shape
     if out is None:
-        out = tuple(Packed8(torch.empty(shape, dtype=torch.int8, device=device),
-                            torch.empty((N, H), dtype=torch.float32, device=device)) for _ in xs)
+        line = (N, H)
+        out = tuple([Packed8(torch.empty(shape, dtype=torch.int8, device=device),
+                             torch.empty(line, dtype=torch.float32, device=device)) for _ in xs])
     else:
         out = tuple(out)
         if len(out) != len(xs):
@@ -736,8 +737,8 @@ def pack8(*xs: torch.Tensor, out=None):
             _packed(p, "out", shape, device)
     rows = _native.PTRS[len(xs)]
     _launch(_native.load().gnn_pack8, "gnn_pack8", device, len(xs), N, H, D, dt,
-            rows(*[t.data_ptr() for t in xs]), rows(*[p.values.data_ptr() for p in out]),
-            rows(*[p.scale.data_ptr() for p in out]))
+            rows(*[t.data_ptr() for t in xs]), rows(*[p[0].data_ptr() for p in out]),
+            rows(*[p[1].data_ptr() for p in out]))
     return out
 
 

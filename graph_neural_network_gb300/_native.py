@@ -123,6 +123,8 @@ def load(path: str = LIB_PATH) -> ctypes.CDLL:
     """Load the library (once).  Raises when it is missing: build it with
     ``graph_neural_network_gb300.build.build()``."""
     global _lib
+    if _lib is not None:  # set once, complete
+        return _lib
     with _lock:
         if _lib is not None:
             return _lib
