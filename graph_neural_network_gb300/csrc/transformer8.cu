@@ -99,8 +99,9 @@ __device__ __forceinline__ void widen(const Raw8<kE>& r, float (&x)[kE]) {
 }
 
 // Edges in flight per lane: pass 1 gathers 32 bytes of an edge and keeps four in
-// flight (857 us instead of 1,028 with two on the 300k-node graph); pass 2 gathers
-// three to five times as much, and three spill (1,577 us instead of 957).
+// flight (300k-node graph, both passes: 1,700 us; with three 1,746, with five
+// 1,743); pass 2 gathers three to five times as much and keeps two (with three
+// 1,735 us; 100k nodes in float32 272 us, with three 320).
 constexpr int kDstEdges = 4;
 template <int kE>
 struct SrcEdges {

@@ -45,10 +45,10 @@ struct RelArgs {
 
 // Edges in flight per lane, for lane vectors of 32 bytes (twice as many of 16): as
 // many as the registers of 16 warps an SM hold beside the accumulators, of which
-// float32 lanes have half as many.  300k-node bfloat16 graph: forward 595 us with
-// four and 2 blocks, 672 with two and 3; pass 1 752 with three, 817 with two; pass 2
-// 920 with two, 929 with three.  100k-node float32 graph, training step: 499 us with
-// three in pass 2, 524 with two.
+// float32 lanes have half as many.  Training step on the 300k-node bfloat16 graph:
+// 2,044 us; forward with three edges 2,083, with five 2,060; pass 1 with two 2,162,
+// with four 2,216; pass 2 with three 2,088.  On the 100k-node float32 graph: 499 us;
+// pass 2 with two 524, with four 642; pass 1 with two 562, with five 518.
 template <typename T, int kE, int kBf16, int kF32>
 struct RelEdges {
   static constexpr int value =
