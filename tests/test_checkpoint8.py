@@ -328,3 +328,25 @@ def test_refusals_of_the_binding():
         gnn.pack8(x, x.bfloat16())
     with pytest.raises(TypeError):
         gnn.unpack8(p, torch.float16)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("H, D, dtype", [(32, 4, "f32"), (8, 16, "bf16"), (1, 8, "bf16"),
+                                         (4, 64, "bf16")])
+def test_most_buckets(H, D, dtype):
+    """Tables of the bias gradient of every size, the widest one included."""
+    import graph_neural_network_gb300 as gnn
+    rp, ci = testgraphs.with_in_degrees([0, 5, 70, 300], n_nodes=500, seed=H + D)
+    n = len(rp) - 1
+    g = device_graph(dict(row_ptr=rp, col=ci), (8, 64, 16))
+    q, k, v, dout = features(n, H, D, dtype, 23)
+    packed = gnn.pack8(*(to_device(x, dtype) for x in (q, k, v)))
+    at = [p.values.cpu().numpy() * p.scale.cpu().numpy().astype(np.float64)[..., None]
+          for p in packed]
+    pos = positions(n, 23, 900)
+    rel = gnn.RelPos(g, torch.from_numpy(pos).cuda(), 128, 1000)
+    bucket = edge_buckets(rp, ci, pos, rel.bounds, True)
+    bias = workload.normal_f32(23, 7, (128, H), 1.0)
+    got = backward(g, packed, dout, dtype, rel, bias)
+    ref = layer_ref.attention(rp, ci, *at, D ** -0.5, bias, bucket, wide(dout))
+    layer_ref.hold_attention({x: to_f64(t) for x, t in got.items()}, ref, dtype, "128", list(got))
