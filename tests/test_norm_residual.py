@@ -280,3 +280,22 @@ def test_refusals_of_the_binding():
         gnn.norm_residual_backward(x, x, x, x, grads={"dnothing": x})
     with pytest.raises(TypeError):
         gnn.norm_residual_backward(x, x, x, None)
+
+
+@pytest.mark.gpu
+def test_parameter_sums_over_many_rows():
+    """400k rows, some 660 of them a thread.  The terms of db_pre are dz itself, so its
+    error is that of the additions alone.  An addition into a partial sum of k
+    random terms is off by u / sqrt(3) of it at most on average, so m of them in a row
+    by u sqrt(m / 6) of their sum: 3.3 u for 64, 1.3 u for the 11 parts after them,
+    3.6 u together (one chain of 660: 10.5 u, and the partial sums of a thread lie
+    anywhere in their binades, which takes a third off each)."""
+    import graph_neural_network_gb300 as gnn
+    n, F = 400_000, 512
+    gen = torch.Generator("cuda").manual_seed(3)
+    o, y, dy, dz = (torch.randn(n, F, generator=gen, device="cuda") for _ in range(4))
+    w = torch.ones(F, device="cuda")
+    got = gnn.norm_residual_backward(y, o, dy, dz, None, w, w_pre=w, b_pre=w)["db_pre"].double()
+    want = torch.stack([t.double().sum(0) for t in dz.split(50_000)]).sum(0)
+    error = (got - want).norm() / want.norm()
+    assert error <= 4 * 2.0 ** -24, float(error)
