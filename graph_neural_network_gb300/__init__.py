@@ -643,7 +643,8 @@ def transformer_rel_forward(g: Graph, rel: RelPos, q: torch.Tensor, key: torch.T
                             out=None, lse=None, ws=None):
     """transformer_forward with bias [buckets, H] added to the scores by the
     bucket of each edge: out [N,H,D] (q's dtype) and lse [N,H] float32.  An
-    entry of -inf masks its bucket."""
+    entry of -inf masks its bucket; finite entries may have any size (a row
+    whose edges all carry the same one has the weights that it has without)."""
     N, H, D = _rel_qkv(g, q, key, val)
     bias = _rel_bias(g, rel, bias, H)
     out = _like(out, "out", q)

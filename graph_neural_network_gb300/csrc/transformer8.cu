@@ -8,7 +8,7 @@
 // one), so no statistic is kept from the forward either.
 //
 //   pass 1, destination side (CSR), one streaming pass with an online softmax
-//     over e_ij = scale q^_i . k^_j (+ bias): with p = exp(e - m) it carries
+//     over e_ij = scale q^_i . k^_j (+ bias): with p = exp(e - m) (SoftRef) it carries
 //     l = sum p, D = sum p da, P = sum p da k^_j, Q = sum p k^_j (da = dout_i . v^_j)
 //     and ends with Delta_i = D / l, lse_i = m + log l,
 //     dq_i = scale (P - Delta_i Q) / l.  Record {lse, Delta, qs} to the workspace.
@@ -29,7 +29,7 @@
 // D32 f32 without: 0.11 and 0.17 ms.  What the checkpoints save is memory: a byte
 // instead of two or four per element of q, key and val, and lse.
 //
-// Masks, buckets and the bias gradient as in transformer_rel.cu; the work is cut as
+// Masks, biases of any size and the bias gradient as in transformer_rel.cu; the work is cut as
 // edgewalk.cuh says.
 #include "edgewalk.cuh"
 #include "lanevec.cuh"
@@ -46,7 +46,9 @@ struct T8Args {
   float scale, scale2;     // natural units, base 2
   const void* dout;
   void *dq, *dkey, *dval;
-  float4* stats;           // [N][H] {lse (base 2), Delta, qs, -}
+  // [N][H] {lse (base 2), Delta, qs, 0}, or {log2 of the sum, Delta, qs, the reference's
+  // bias} (Bias::kAny)
+  float4* stats;
   const float* bias;
   int buckets;
   double* db_part;         // [pass 2 blocks][buckets][H]
@@ -102,20 +104,23 @@ __device__ __forceinline__ void widen(const Raw8<kE>& r, float (&x)[kE]) {
 // flight (300k-node graph, both passes: 1,700 us; with three 1,746, with five
 // 1,743); pass 2 gathers three to five times as much and keeps two (with three
 // 1,735 us; 100k nodes in float32 272 us, with three 320).
-constexpr int kDstEdges = 4;
-template <int kE>
-struct SrcEdges {
-  static constexpr int value = kE == 16 ? 2 : 4;
+// Half as many beside large biases, where that costs the ordinary form nothing
+// (transformer_rel.cu).
+template <int kE, Bias kBias>
+struct Edges {
+  static constexpr bool any = kBias == Bias::kAny;
+  static constexpr int dst = any ? 2 : 4, src = kE < 16 ? 4 : any ? 1 : 2;
 };
 
 // ---------------------------------------------------------------------------
 // pass 1: destination side
 // ---------------------------------------------------------------------------
 
-template <typename T, int kE_, bool kRel>
+template <typename T, int kE_, Bias kBias>
 struct DstPass {
   static constexpr int kE = kE_;
-  static constexpr int U = kDstEdges;
+  static constexpr bool kRel = kBias != Bias::kNone;
+  static constexpr int U = Edges<kE, kBias>::dst;
   static constexpr bool kBuckets = kRel;
   const T8Args& A;
   const Lane<1>& L;
@@ -127,16 +132,18 @@ struct DstPass {
   Raw8<kE> q8;
   float qsc;        // qs_i
   HeldT<T, kE> g;   // dout_i
-  // its sums; m is in base 2
-  float m, l, d, P[kE], Q[kE];
+  // its sums
+  SoftRef<kBias> ref;
+  float l, d, P[kE], Q[kE];
 
   __device__ __forceinline__ DstPass(const T8Args& a, const Lane<1>& lane)
       : A(a), L(lane), place(a.s, lane), rows(a.s, lane), r0(a.k8, place), r1(a.v8, place) {}
-  // floats of a partial state: P, Q, then m, l, d per head
-  static __host__ __device__ int floats(const Shape& s) { return 2 * s.rv * kE + 3 * s.H; }
+  // floats of a partial state: P, Q, then l, d and the reference per head
+  static constexpr int kHead = 2 + SoftRef<kBias>::kFloats;
+  static __host__ __device__ int floats(const Shape& s) { return 2 * s.rv * kE + kHead * s.H; }
 
   __device__ __forceinline__ void clear() {
-    m = -INFINITY;
+    ref.clear();
     l = d = 0.f;
     zero<kE>(P);
     zero<kE>(Q);
@@ -147,13 +154,11 @@ struct DstPass {
     g.fetch(rows.of(A.dout, i));
     clear();
   }
-  __device__ __forceinline__ void rescale(float mn) {
-    const float s0 = ex2(m - mn);
-    l *= s0;
-    d *= s0;
-    scale<kE>(P, s0);
-    scale<kE>(Q, s0);
-    m = mn;
+  __device__ __forceinline__ void rescale(float r) {
+    l *= r;
+    d *= r;
+    scale<kE>(P, r);
+    scale<kE>(Q, r);
   }
 
   template <class F>
@@ -191,19 +196,11 @@ struct DstPass {
       }
     }
     head_sums<2 * U>(red, A.s.hv_log2);
-    float top = m;
-#pragma unroll
-    for (int u = 0; u < U; ++u) {
-      red[u] = kRel ? fmaf(red[u], qk * ks[u], bs[u]) : red[u] * (qk * ks[u]);
-      if (!ok[u]) red[u] = -INFINITY;
-      top = fmaxf(top, red[u]);
-    }
-    if (top > m) rescale(top);
-    const float mr = m == -INFINITY ? 0.f : m;
+    ref.template weigh<U>(red, qk, ks, bs, ok, l, [&](float r) { rescale(r); });
 #pragma unroll
     for (int u = 0; u < U; ++u) {
       if (!ok[u]) continue;
-      const float p = ex2(red[u] - mr);
+      const float p = ex2(red[u]);
       const float pd = p * (red[U + u] * vs[u]);
       l += p;
       d += pd;
@@ -222,39 +219,39 @@ struct DstPass {
       to[row + at + c] = Q[c];
     }
     if (L.head_leader(A.s, 0)) {
-      float* h = to + 2 * row + 3 * L.k[0];
-      h[0] = m;
-      h[1] = l;
-      h[2] = d;
+      float* h = to + 2 * row + kHead * L.k[0];
+      h[0] = l;
+      h[1] = d;
+      ref.put(h + 2);
     }
   }
   template <int N>
   __device__ __forceinline__ void take(const float* from, int step) {
     const int row = A.s.rv * kE, at = L.q[0] * kE;
-    float h[N][3], top = m;
-#pragma unroll
-    for (int n = 0; n < N; ++n)
-#pragma unroll
-      for (int x = 0; x < 3; ++x) h[n][x] = part_load(from + n * step + 2 * row + 3 * L.k[0] + x);
-#pragma unroll
-    for (int n = 0; n < N; ++n) top = fmaxf(top, h[n][0]);
-    if (top > m) rescale(top);
-    const float mr = m == -INFINITY ? 0.f : m;
+    float lb[N], db[N], ref_b[SoftRef<kBias>::kFloats][N], r[N];
 #pragma unroll
     for (int n = 0; n < N; ++n) {
-      h[n][0] = ex2(h[n][0] - mr);
-      l = fmaf(h[n][1], h[n][0], l);
-      d = fmaf(h[n][2], h[n][0], d);
+      const float* h = from + n * step + 2 * row + kHead * L.k[0];
+      lb[n] = part_load(h);
+      db[n] = part_load(h + 1);
+#pragma unroll
+      for (int c = 0; c < SoftRef<kBias>::kFloats; ++c) ref_b[c][n] = part_load(h + 2 + c);
+    }
+    ref.template join<N>(l, lb, ref_b, [&](float by) { rescale(by); }, r);
+#pragma unroll
+    for (int n = 0; n < N; ++n) {
+      l = fmaf(lb[n], r[n], l);
+      d = fmaf(db[n], r[n], d);
     }
     float x[N][kE];
 #pragma unroll
     for (int n = 0; n < N; ++n) part_row<kE>(from + n * step + at, x[n]);
 #pragma unroll
-    for (int n = 0; n < N; ++n) axpy<kE>(P, h[n][0], x[n]);
+    for (int n = 0; n < N; ++n) axpy<kE>(P, r[n], x[n]);
 #pragma unroll
     for (int n = 0; n < N; ++n) part_row<kE>(from + n * step + row + at, x[n]);
 #pragma unroll
-    for (int n = 0; n < N; ++n) axpy<kE>(Q, h[n][0], x[n]);
+    for (int n = 0; n < N; ++n) axpy<kE>(Q, r[n], x[n]);
   }
   __device__ __forceinline__ void finish(int i) {
     const bool any = l != 0.f;  // a NaN stays one
@@ -262,9 +259,15 @@ struct DstPass {
     const float delta = d * inv;
     minus_scaled<kE>(P, Q, delta, A.scale * inv);
     storeT<T, kE>(const_cast<char*>(rows.of(A.dq, i)), P);
-    if (L.head_leader(A.s, 0))
-      A.stats[int64_t(i) * A.s.H + L.k[0]] =
-          make_float4(any ? m + __log2f(l) : 0.f, delta, qsc, 0.f);
+    if (!L.head_leader(A.s, 0)) return;
+    float4 r = make_float4(0.f, delta, qsc, 0.f);
+    if constexpr (kBias == Bias::kAny) {  // (a row without weights: pass 2 gives it none)
+      r.x = any ? ref.d + __log2f(l) : 0.f;
+      r.w = any ? ref.b : INFINITY;
+    } else if (any) {
+      r.x = ref.m + __log2f(l);
+    }
+    A.stats[int64_t(i) * A.s.H + L.k[0]] = r;
   }
 };
 
@@ -273,10 +276,11 @@ struct DstPass {
 // ---------------------------------------------------------------------------
 
 // kPair: the form of the bias gradient's tables.
-template <typename T, int kE_, bool kRel, bool kPair>
+template <typename T, int kE_, Bias kBias, bool kPair>
 struct SrcPass {
   static constexpr int kE = kE_;
-  static constexpr int U = SrcEdges<kE>::value;
+  static constexpr bool kRel = kBias != Bias::kNone;
+  static constexpr int U = Edges<kE, kBias>::src;
   static constexpr bool kBuckets = kRel;
   const T8Args& A;
   const Lane<1>& L;
@@ -352,9 +356,13 @@ struct SrcPass {
     head_sums<2 * U>(red, A.s.hv_log2);
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-      const float e = kRel ? fmaf(red[u], kq * st[u].z, bs[u]) : red[u] * (kq * st[u].z);
+      float e;
+      if (kBias == Bias::kAny)
+        e = fmaf(bs[u] - st[u].w, kLog2e, fmaf(red[u], beside(st[u].w, kq * st[u].z), -st[u].x));
+      else
+        e = (kRel ? fmaf(red[u], kq * st[u].z, bs[u]) : red[u] * (kq * st[u].z)) - st[u].x;
       if (!ok[u]) continue;
-      const float al = ex2(e - st[u].x);
+      const float al = ex2(e);
       const float de = al * fmaf(red[U + u], vsc, -st[u].y);
       if (kRel) add_grad<kPair>(hist, A.s, L.head_leader(A.s, 0), bk[u], de);
       float x[kE];
@@ -392,10 +400,20 @@ __global__ void __launch_bounds__(kThreads, kPerSm) t8_dst(const __grid_constant
   extern __shared__ __align__(16) unsigned char smem[];
   const Lane<1> L(A.s);
   __shared__ __align__(16) unsigned char held[kWarps * HeldT<T, kE>::kBytes];
-  DstPass<T, kE, kRel> p(A, L);
-  p.g.place(held + (threadIdx.x >> 5) * HeldT<T, kE>::kBytes, L.lane);
-  p.sb = kRel ? stage_bias(A.bias, A.buckets * A.s.H, smem) + L.k[0] : nullptr;
-  walk(p, A.walk, A.dir, A.s, L);
+  const auto pass = [&](auto p, float* table) {
+    p.g.place(held + (threadIdx.x >> 5) * HeldT<T, kE>::kBytes, L.lane);
+    p.sb = table + L.k[0];
+    walk(p, A.walk, A.dir, A.s, L);
+  };
+  if constexpr (kRel) {
+    float* table = reinterpret_cast<float*>(smem);
+    if (stage_bias(A.bias, A.buckets * A.s.H, table))
+      pass(DstPass<T, kE, Bias::kAny>(A, L), table);
+    else
+      pass(DstPass<T, kE, Bias::kOrdinary>(A, L), table);
+  } else {
+    pass(DstPass<T, kE, Bias::kNone>(A, L), nullptr);
+  }
 }
 
 template <typename T, int kE, bool kRel, bool kPair>
@@ -403,21 +421,25 @@ __global__ void __launch_bounds__(kThreads, kPerSm) t8_src(const __grid_constant
   extern __shared__ __align__(16) unsigned char smem[];
   const Lane<1> L(A.s);
   __shared__ __align__(16) unsigned char held[kWarps * HeldT<T, kE>::kBytes];
-  SrcPass<T, kE, kRel, kPair> p(A, L);
-  p.v.place(held + (threadIdx.x >> 5) * HeldT<T, kE>::kBytes, L.lane);
-  float* tables = nullptr;
-  p.sb = nullptr;
-  p.hist = nullptr;
-  if (kRel) {
-    tables = reinterpret_cast<float*>(smem);
-    p.hist = clear_grad_tables(tables, A.s, L, A.buckets);
-    p.sb = stage_bias(A.bias, A.buckets * A.s.H, smem + grad_tables_bytes(A.s, A.buckets)) +
-           L.k[0];
+  const auto pass = [&](auto p, float* table, float* column) {
+    p.v.place(held + (threadIdx.x >> 5) * HeldT<T, kE>::kBytes, L.lane);
+    p.sb = table + L.k[0];
+    p.hist = column;
+    walk(p, A.walk, A.dir, A.s, L);
+  };
+  if constexpr (kRel) {
+    float* tables = reinterpret_cast<float*>(smem);
+    float* column = clear_grad_tables(tables, A.s, L, A.buckets);
+    float* table = reinterpret_cast<float*>(smem + grad_tables_bytes(A.s, A.buckets));
+    if (stage_bias(A.bias, A.buckets * A.s.H, table))
+      pass(SrcPass<T, kE, Bias::kAny, kPair>(A, L), table, column);
+    else
+      pass(SrcPass<T, kE, Bias::kOrdinary, kPair>(A, L), table, column);
+    let_next_start();
+    fold_grad_tables<kPair>(tables, A.s, L, A.buckets, A.db_part);
+  } else {
+    pass(SrcPass<T, kE, Bias::kNone, kPair>(A, L), nullptr, nullptr);
   }
-  walk(p, A.walk, A.dir, A.s, L);
-  if (!kRel) return;
-  let_next_start();
-  fold_grad_tables<kPair>(tables, A.s, L, A.buckets, A.db_part);
 }
 
 // after: launched behind the first pass of the same call (launch_after).
@@ -484,7 +506,7 @@ T8Layout t8_layout(const gnn_graph* g, const Shape& s, int buckets, int elems) {
     return r;
   };
   L.arrived = take(size_t(L.plan.workers) * 2 * sizeof(int));
-  L.part = take(size_t(L.plan.workers) * 2 * (2 * size_t(s.H) * s.D + 3 * s.H) * 4);
+  L.part = take(size_t(L.plan.workers) * 2 * (2 * size_t(s.H) * s.D + 4 * s.H) * 4);
   L.stats = take(size_t(g->n) * s.H * 16);
   L.db_part = take(size_t(L.plan.blocks) * buckets * s.H * 8);
   L.total = off;

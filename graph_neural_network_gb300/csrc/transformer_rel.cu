@@ -4,12 +4,14 @@
 // the bucket b_ij read next to the edge's node id from the prepared bucket bytes
 // (relpos.cu) of the direction being walked, and the bias table in shared
 // memory.  An entry of -infinity masks its edges for that head: the lanes of the head
-// skip them like absent ones, so what their rows hold enters no sum.
+// skip them like absent ones, so what their rows hold enters no sum.  Tables with large
+// finite entries take another form of the scores (Bias), within the same kernels.
 //
 // Forward: one pass over the CSR with an online softmax whose reference moves
 // only when a score passes it.  Backward pass 1 (CSR): Delta, P = sum alpha da
-// key_j, Q = sum alpha key_j, dq_i = scale (P - Delta Q), record {lse, Delta}.  Pass
-// 2 (CSC): dkey, dval, and dbias[b][k] = sum of de_ij over the edges of bucket
+// key_j, Q = sum alpha key_j, dq_i = scale (P - Delta Q), record {lse, Delta}.  (Beside
+// large biases lse, one number, has lost what the weights need: there the pass is an online
+// softmax of its own and records the sum and the reference apart.)  Pass 2 (CSC): dkey, dval, and dbias[b][k] = sum of de_ij over the edges of bucket
 // b, de_ij = alpha_ij (da_ij - Delta_i) being known per edge there: each lane that
 // leads a head adds into a column of its own of its warp's table in shared
 // memory (no atomics, no bank conflicts), the block adds its tables in a fixed
@@ -20,6 +22,8 @@
 // (16 where a head has no more), so that what an edge costs whatever its width
 // (ids, bucket, bias, score, exponential, addresses) is shared by more elements;
 // both dot products of bfloat16 rows multiply the packed halves.
+#include <type_traits>
+
 #include "edgewalk.cuh"
 #include "lanevec.cuh"
 
@@ -39,7 +43,9 @@ struct RelArgs {
   const float* lse_in;
   const void* dout;
   void *dq, *dkey, *dval;
-  float2* stats;           // [N][H] {lse (base 2), Delta}
+  // [N][H] {lse (base 2), Delta}, or {log2 of the sum, Delta, the reference's bias,
+  // factor of the dot products} (Bias::kAny)
+  void* stats;
   double* db_part;         // [pass 2 blocks][buckets][H]
 };
 
@@ -49,19 +55,24 @@ struct RelArgs {
 // 2,044 us; forward with three edges 2,083, with five 2,060; pass 1 with two 2,162,
 // with four 2,216; pass 2 with three 2,088.  On the 100k-node float32 graph: 499 us;
 // pass 2 with two 524, with four 642; pass 1 with two 562, with five 518.
-template <typename T, int kE, int kBf16, int kF32>
+// Beside large biases, whose form needs more registers, as many or fewer: with more the
+// compiler also schedules the ordinary form of the same kernel worse (forward 593 instead
+// of 514 us; pass 2 with 16-byte vectors, 200k nodes H8 D4 float32, 235 instead of 221).
+template <typename T, int kE, Bias kBias, int kBf16, int kF32, bool kHalve = true>
 struct RelEdges {
-  static constexpr int value =
-      (sizeof(T) == 4 ? kF32 : kBf16) * (32 / (kE * int(sizeof(T))));
+  static constexpr int full = 32 / (kE * int(sizeof(T)));  // 1: vectors of 32 bytes
+  static constexpr int all = (sizeof(T) == 4 ? kF32 : kBf16) * full;
+  static constexpr int any = full == 2 ? 2 : kHalve ? (all + 1) / 2 : all;
+  static constexpr int value = kBias == Bias::kAny ? any : all;
 };
 constexpr int kFwdEdges = 4, kDstEdges = 3, kDstEdgesF32 = 3, kSrcEdges = 2, kSrcEdgesF32 = 3;
 
 // ---- forward -----------------------------------------------------------------
 
-template <typename T, int kE_>
+template <typename T, int kE_, Bias kBias>
 struct RelFwd {
   static constexpr int kE = kE_;
-  static constexpr int U = RelEdges<T, kE, kFwdEdges, kFwdEdges>::value;
+  static constexpr int U = RelEdges<T, kE, kBias, kFwdEdges, kFwdEdges>::value;
   static constexpr int kRow = kE * int(sizeof(T));
   static constexpr bool kBuckets = true;
   const RelArgs& A;
@@ -70,16 +81,22 @@ struct RelFwd {
   const LaneRows<kRow> r0, r1;  // the gathered rows
   const float* sb;    // the bias table
   HeldT<T, kE> q;
-  float m, l, acc[kE];  // m in base 2
+  SoftRef<kBias> ref;
+  float l, acc[kE];
 
   __device__ __forceinline__ RelFwd(const RelArgs& a, const Lane<1>& lane)
       : A(a), L(lane), place(a.s, lane), r0(a.key, place), r1(a.val, place) {}
-  static __host__ __device__ int floats(const Shape& s) { return s.rv * kE + 2 * s.H; }
+  static constexpr int kHead = 1 + SoftRef<kBias>::kFloats;  // l, the reference
+  static __host__ __device__ int floats(const Shape& s) { return s.rv * kE + kHead * s.H; }
 
   __device__ __forceinline__ void clear() {
-    m = -INFINITY;
+    ref.clear();
     l = 0.f;
     zero<kE>(acc);
+  }
+  __device__ __forceinline__ void rescale(float by) {
+    l *= by;
+    scale<kE>(acc, by);
   }
   __device__ __forceinline__ void begin(int i) {
     q.fetch(place.of(A.q, i));
@@ -108,23 +125,14 @@ struct RelFwd {
 #pragma unroll
     for (int u = 0; u < U; ++u) sc[u] = dotT<kE>(own, rk[u]);
     head_sums<U>(sc, A.s.hv_log2);
-    float top = m;
+    float one[U];
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
-      sc[u] = ok[u] ? fmaf(sc[u], A.scale2, bs[u]) : -INFINITY;
-      top = fmaxf(top, sc[u]);
-    }
-    if (top > m) {
-      const float s0 = ex2(m - top);
-      l *= s0;
-      scale<kE>(acc, s0);
-      m = top;
-    }
-    const float mr = m == -INFINITY ? 0.f : m;
+    for (int u = 0; u < U; ++u) one[u] = 1.f;
+    ref.template weigh<U>(sc, A.scale2, one, bs, ok, l, [&](float by) { rescale(by); });
 #pragma unroll
     for (int u = 0; u < U; ++u) {
       if (!ok[u]) continue;
-      const float p = ex2(sc[u] - mr);
+      const float p = ex2(sc[u]);
       l += p;
       float x[kE];
       widenT<T, kE>(rv[u], x);
@@ -135,28 +143,28 @@ struct RelFwd {
 #pragma unroll
     for (int c = 0; c < kE; ++c) to[L.q[0] * kE + c] = acc[c];
     if (L.head_leader(A.s, 0)) {
-      to[A.s.rv * kE + 2 * L.k[0]] = m;
-      to[A.s.rv * kE + 2 * L.k[0] + 1] = l;
+      float* h = to + A.s.rv * kE + kHead * L.k[0];
+      h[0] = l;
+      ref.put(h + 1);
     }
   }
   template <int N>
   __device__ __forceinline__ void take(const float* from, int step) {
-    float mb[N], lb[N], x[N][kE];
+    float lb[N], ref_b[SoftRef<kBias>::kFloats][N], r[N], x[N][kE];
 #pragma unroll
     for (int n = 0; n < N; ++n) {
-      const float* f = from + n * step;
-      mb[n] = part_load(f + A.s.rv * kE + 2 * L.k[0]);
-      lb[n] = part_load(f + A.s.rv * kE + 2 * L.k[0] + 1);
-      part_row<kE>(f + L.q[0] * kE, x[n]);
+      const float* h = from + n * step + A.s.rv * kE + kHead * L.k[0];
+      lb[n] = part_load(h);
+#pragma unroll
+      for (int c = 0; c < SoftRef<kBias>::kFloats; ++c) ref_b[c][n] = part_load(h + 1 + c);
     }
+    ref.template join<N>(l, lb, ref_b, [&](float by) { rescale(by); }, r);
+#pragma unroll
+    for (int n = 0; n < N; ++n) part_row<kE>(from + n * step + L.q[0] * kE, x[n]);
 #pragma unroll
     for (int n = 0; n < N; ++n) {
-      const float M = fmaxf(m, mb[n]), Mr = M == -INFINITY ? 0.f : M;
-      const float sa = ex2(m - Mr), sx = ex2(mb[n] - Mr);
-      l = l * sa + lb[n] * sx;
-      scale<kE>(acc, sa);
-      axpy<kE>(acc, sx, x[n]);
-      m = M;
+      l = fmaf(lb[n], r[n], l);
+      axpy<kE>(acc, r[n], x[n]);
     }
   }
   __device__ __forceinline__ void finish(int i) {
@@ -164,16 +172,16 @@ struct RelFwd {
     scale<kE>(acc, any ? reciprocal(l) : 0.f);
     storeT<T, kE>(const_cast<char*>(place.of(A.out, i)), acc);
     if (L.head_leader(A.s, 0))
-      A.lse[int64_t(i) * A.s.H + L.k[0]] = any ? (m + __log2f(l)) * kLn2 : -INFINITY;
+      A.lse[int64_t(i) * A.s.H + L.k[0]] = any ? ref.lse(l) : -INFINITY;
   }
 };
 
 // ---- backward pass 1: destination side ---------------------------------------
 
-template <typename T, int kE_>
+template <typename T, int kE_, Bias kBias>
 struct RelDst {
   static constexpr int kE = kE_;
-  static constexpr int U = RelEdges<T, kE, kDstEdges, kDstEdgesF32>::value;
+  static constexpr int U = RelEdges<T, kE, kBias, kDstEdges, kDstEdgesF32>::value;
   static constexpr int kRow = kE * int(sizeof(T));
   static constexpr bool kBuckets = true;
   const RelArgs& A;
@@ -182,21 +190,33 @@ struct RelDst {
   const LaneRows<kRow> r0, r1;  // the gathered rows
   const float* sb;    // the bias table
   HeldT<T, kE> q, g;
-  float lse2, delta, P[kE], Q[kE];
+  static constexpr bool kAny = kBias == Bias::kAny;
+  float lse2;          // ordinary biases: weights are relative to it
+  SoftRef<kBias> ref;  // any: weights to be divided by their sum l
+  float l;
+  float delta, P[kE], Q[kE];
 
   __device__ __forceinline__ RelDst(const RelArgs& a, const Lane<1>& lane)
       : A(a), L(lane), place(a.s, lane), r0(a.key, place), r1(a.val, place) {}
-  static __host__ __device__ int floats(const Shape& s) { return 2 * s.rv * kE + s.H; }
+  static constexpr int kHead = kAny ? 4 : 1;  // Delta, l, the reference
+  static __host__ __device__ int floats(const Shape& s) { return 2 * s.rv * kE + kHead * s.H; }
 
   __device__ __forceinline__ void clear() {
-    delta = 0.f;
+    ref.clear();
+    l = delta = 0.f;
     zero<kE>(P);
     zero<kE>(Q);
+  }
+  __device__ __forceinline__ void rescale(float by) {
+    l *= by;
+    delta *= by;
+    scale<kE>(P, by);
+    scale<kE>(Q, by);
   }
   __device__ __forceinline__ void begin(int i) {
     q.fetch(place.of(A.q, i));
     g.fetch(place.of(A.dout, i));
-    lse2 = __ldg(A.lse_in + int64_t(i) * A.s.H + L.k[0]) * kLog2e;
+    if (!kAny) lse2 = __ldg(A.lse_in + int64_t(i) * A.s.H + L.k[0]) * kLog2e;
     clear();
   }
   template <class F>
@@ -229,11 +249,21 @@ struct RelDst {
       for (int u = 0; u < U; ++u) red[u] = dotT<kE>(own, rk[u]);
     }
     head_sums<2 * U>(red, A.s.hv_log2);
+    if (kAny) {
+      float one[U];
+#pragma unroll
+      for (int u = 0; u < U; ++u) one[u] = 1.f;
+      ref.template weigh<U>(red, A.scale2, one, bs, ok, l, [&](float by) { rescale(by); });
+    } else {
+#pragma unroll
+      for (int u = 0; u < U; ++u) red[u] = fmaf(red[u], A.scale2, bs[u]) - lse2;
+    }
 #pragma unroll
     for (int u = 0; u < U; ++u) {
       if (!ok[u]) continue;
-      const float al = ex2(fmaf(red[u], A.scale2, bs[u]) - lse2);
+      const float al = ex2(red[u]);
       const float ad = al * red[U + u];
+      if (kAny) l += al;
       delta += ad;
       float x[kE];
       widenT<T, kE>(rk[u], x);
@@ -248,41 +278,69 @@ struct RelDst {
       to[at + c] = P[c];
       to[row + at + c] = Q[c];
     }
-    if (L.head_leader(A.s, 0)) to[2 * row + L.k[0]] = delta;
+    if (L.head_leader(A.s, 0)) {
+      float* h = to + 2 * row + kHead * L.k[0];
+      h[0] = delta;
+      if (kAny) {
+        h[1] = l;
+        ref.put(h + 2);
+      }
+    }
   }
   template <int N>
   __device__ __forceinline__ void take(const float* from, int step) {
     const int row = A.s.rv * kE, at = L.q[0] * kE;
-    float d[N], x[N][kE];
+    float db[N], lb[N], ref_b[SoftRef<kBias>::kFloats][N], r[N], x[N][kE];
 #pragma unroll
     for (int n = 0; n < N; ++n) {
-      d[n] = part_load(from + n * step + 2 * row + L.k[0]);
-      part_row<kE>(from + n * step + at, x[n]);
+      const float* h = from + n * step + 2 * row + kHead * L.k[0];
+      db[n] = part_load(h);
+      r[n] = 1.f;
+      if (!kAny) continue;
+      lb[n] = part_load(h + 1);
+#pragma unroll
+      for (int c = 0; c < SoftRef<kBias>::kFloats; ++c) ref_b[c][n] = part_load(h + 2 + c);
+    }
+    if (kAny) {
+      ref.template join<N>(l, lb, ref_b, [&](float by) { rescale(by); }, r);
+#pragma unroll
+      for (int n = 0; n < N; ++n) l = fmaf(lb[n], r[n], l);
     }
 #pragma unroll
+    for (int n = 0; n < N; ++n) part_row<kE>(from + n * step + at, x[n]);
+#pragma unroll
     for (int n = 0; n < N; ++n) {
-      delta += d[n];
-      add_row<kE>(P, x[n]);
+      delta = fmaf(db[n], r[n], delta);
+      axpy<kE>(P, r[n], x[n]);
     }
 #pragma unroll
     for (int n = 0; n < N; ++n) part_row<kE>(from + n * step + row + at, x[n]);
 #pragma unroll
-    for (int n = 0; n < N; ++n) add_row<kE>(Q, x[n]);
+    for (int n = 0; n < N; ++n) axpy<kE>(Q, r[n], x[n]);
   }
   __device__ __forceinline__ void finish(int i) {
-    minus_scaled<kE>(P, Q, delta, A.scale);
+    const bool any = l != 0.f;  // a NaN stays one
+    const float inv = !kAny ? 1.f : any ? reciprocal(l) : 0.f;
+    if (kAny) delta *= inv;
+    minus_scaled<kE>(P, Q, delta, A.scale * inv);
     storeT<T, kE>(const_cast<char*>(place.of(A.dq, i)), P);
-    if (L.head_leader(A.s, 0))
-      A.stats[int64_t(i) * A.s.H + L.k[0]] = make_float2(lse2, delta);
+    if (!L.head_leader(A.s, 0)) return;
+    const int64_t to = int64_t(i) * A.s.H + L.k[0];
+    if constexpr (kAny)  // (a row without weights: no edge gets one in pass 2 either)
+      static_cast<float4*>(A.stats)[to] =
+          make_float4(any ? ref.d + __log2f(l) : 0.f, delta, any ? ref.b : INFINITY,
+                      beside(ref.b, A.scale2));
+    else
+      static_cast<float2*>(A.stats)[to] = make_float2(lse2, delta);
   }
 };
 
 // ---- backward pass 2: source side --------------------------------------------
 
-template <typename T, int kE_, bool kPair>
+template <typename T, int kE_, bool kPair, Bias kBias>
 struct RelSrc {
   static constexpr int kE = kE_;
-  static constexpr int U = RelEdges<T, kE, kSrcEdges, kSrcEdgesF32>::value;
+  static constexpr int U = RelEdges<T, kE, kBias, kSrcEdges, kSrcEdgesF32, false>::value;
   static constexpr int kRow = kE * int(sizeof(T));
   static constexpr bool kBuckets = true;
   const RelArgs& A;
@@ -311,13 +369,15 @@ struct RelSrc {
   __device__ __forceinline__ void batch(const int (&i)[U], const int (&b)[U], int cnt,
                                         const F& sent) {
     RawT<T, kE> rq[U], rg[U];
-    float2 st[U];
+    using Stats = std::conditional_t<kBias == Bias::kAny, float4, float2>;
+    Stats st[U];
 #pragma unroll
     for (int u = 0; u < U; ++u) {
       rq[u] = ldT<T, kE>(r0.at(i[u]));
       rg[u] = ldT<T, kE>(r1.at(i[u]));
       // (no __ldg: pass 1 may still be writing when this kernel starts)
-      st[u] = A.stats[L.k[0] + uint64_t(uint32_t(i[u])) * uint32_t(A.s.H)];
+      st[u] = static_cast<const Stats*>(
+          A.stats)[L.k[0] + uint64_t(uint32_t(i[u])) * uint32_t(A.s.H)];
     }
     float bs[U];
     int bk[U];
@@ -345,7 +405,12 @@ struct RelSrc {
 #pragma unroll
     for (int u = 0; u < U; ++u) {
       if (!ok[u]) continue;
-      const float al = ex2(fmaf(red[u], A.scale2, bs[u]) - st[u].x);
+      float t;
+      if constexpr (kBias == Bias::kAny)
+        t = fmaf(bs[u] - st[u].z, kLog2e, fmaf(red[u], st[u].w, -st[u].x));
+      else
+        t = fmaf(red[u], A.scale2, bs[u]) - st[u].x;
+      const float al = ex2(t);
       const float de = al * (red[U + u] - st[u].y);
       add_grad<kPair>(hist, A.s, L.head_leader(A.s, 0), bk[u], de);
       float x[kE];
@@ -385,10 +450,17 @@ __global__ void __launch_bounds__(kThreads, kPerSm) rel_fwd(const __grid_constan
   extern __shared__ __align__(16) unsigned char smem[];
   const Lane<1> L(A.s);
   __shared__ __align__(16) unsigned char held[kWarps * HeldT<T, kE>::kBytes];
-  RelFwd<T, kE> p(A, L);
-  p.q.place(held + (threadIdx.x >> 5) * HeldT<T, kE>::kBytes, L.lane);
-  p.sb = stage_bias(A.bias, A.buckets * A.s.H, smem) + L.k[0];
-  walk(p, A.walk, A.dir, A.s, L);
+  float* table = reinterpret_cast<float*>(smem);
+  const bool any = stage_bias(A.bias, A.buckets * A.s.H, table);
+  const auto pass = [&](auto p) {
+    p.q.place(held + (threadIdx.x >> 5) * HeldT<T, kE>::kBytes, L.lane);
+    p.sb = table + L.k[0];
+    walk(p, A.walk, A.dir, A.s, L);
+  };
+  if (any)
+    pass(RelFwd<T, kE, Bias::kAny>(A, L));
+  else
+    pass(RelFwd<T, kE, Bias::kOrdinary>(A, L));
 }
 
 template <typename T, int kE>
@@ -397,11 +469,18 @@ __global__ void __launch_bounds__(kThreads, kPerSm) rel_dst(const __grid_constan
   extern __shared__ __align__(16) unsigned char smem[];
   const Lane<1> L(A.s);
   __shared__ __align__(16) unsigned char held[2 * kWarps * HeldT<T, kE>::kBytes];
-  RelDst<T, kE> p(A, L);
-  p.q.place(held + (threadIdx.x >> 5) * HeldT<T, kE>::kBytes, L.lane);
-  p.g.place(held + (kWarps + (threadIdx.x >> 5)) * HeldT<T, kE>::kBytes, L.lane);
-  p.sb = stage_bias(A.bias, A.buckets * A.s.H, smem) + L.k[0];
-  walk(p, A.walk, A.dir, A.s, L);
+  float* table = reinterpret_cast<float*>(smem);
+  const bool any = stage_bias(A.bias, A.buckets * A.s.H, table);
+  const auto pass = [&](auto p) {
+    p.q.place(held + (threadIdx.x >> 5) * HeldT<T, kE>::kBytes, L.lane);
+    p.g.place(held + (kWarps + (threadIdx.x >> 5)) * HeldT<T, kE>::kBytes, L.lane);
+    p.sb = table + L.k[0];
+    walk(p, A.walk, A.dir, A.s, L);
+  };
+  if (any)
+    pass(RelDst<T, kE, Bias::kAny>(A, L));
+  else
+    pass(RelDst<T, kE, Bias::kOrdinary>(A, L));
 }
 
 template <typename T, int kE, bool kPair>
@@ -409,14 +488,21 @@ __global__ void __launch_bounds__(kThreads, kPerSm) rel_src(const __grid_constan
   extern __shared__ __align__(16) unsigned char smem[];
   const Lane<1> L(A.s);
   __shared__ __align__(16) unsigned char held[2 * kWarps * HeldT<T, kE>::kBytes];
-  RelSrc<T, kE, kPair> p(A, L);
-  p.k.place(held + (threadIdx.x >> 5) * HeldT<T, kE>::kBytes, L.lane);
-  p.v.place(held + (kWarps + (threadIdx.x >> 5)) * HeldT<T, kE>::kBytes, L.lane);
   float* tables = reinterpret_cast<float*>(smem);
-  p.hist = clear_grad_tables(tables, A.s, L, A.buckets);
-  p.sb = stage_bias(A.bias, A.buckets * A.s.H, smem + grad_tables_bytes(A.s, A.buckets)) +
-         L.k[0];
-  walk(p, A.walk, A.dir, A.s, L);
+  float* column = clear_grad_tables(tables, A.s, L, A.buckets);
+  float* table = reinterpret_cast<float*>(smem + grad_tables_bytes(A.s, A.buckets));
+  const bool any = stage_bias(A.bias, A.buckets * A.s.H, table);
+  const auto pass = [&](auto p) {
+    p.k.place(held + (threadIdx.x >> 5) * HeldT<T, kE>::kBytes, L.lane);
+    p.v.place(held + (kWarps + (threadIdx.x >> 5)) * HeldT<T, kE>::kBytes, L.lane);
+    p.hist = column;
+    p.sb = table + L.k[0];
+    walk(p, A.walk, A.dir, A.s, L);
+  };
+  if (any)
+    pass(RelSrc<T, kE, kPair, Bias::kAny>(A, L));
+  else
+    pass(RelSrc<T, kE, kPair, Bias::kOrdinary>(A, L));
   let_next_start();
   fold_grad_tables<kPair>(tables, A.s, L, A.buckets, A.db_part);
 }
@@ -460,10 +546,10 @@ RelLayout rel_layout(const gnn_graph* g, const Shape& s, int buckets, bool align
     return r;
   };
   L.arrived = take(size_t(L.plan.workers) * 2 * sizeof(int));
-  // at least every pass's state: two rows and a number per head in pass 1
-  const size_t state = 2 * row + 2 * s.H;
+  // at least every pass's state: two rows and four numbers per head in pass 1
+  const size_t state = 2 * row + 4 * s.H;
   L.part = take(size_t(L.plan.workers) * 2 * state * 4);
-  L.stats = take(size_t(g->n) * s.H * 8);
+  L.stats = take(size_t(g->n) * s.H * 16);
   L.db_part = take(size_t(L.plan.blocks) * buckets * s.H * 8);
   L.total = off;
   return L;
@@ -529,7 +615,7 @@ RelArgs rel_args(const gnn_graph* g, const gnn_rel* rel, const Shape& s, const v
   A.scale2 = scale * kLog2e;
   A.bias = bias;
   A.buckets = rel->buckets;
-  A.stats = reinterpret_cast<float2*>(ws + W.stats);
+  A.stats = ws + W.stats;
   A.db_part = reinterpret_cast<double*>(ws + W.db_part);
   return A;
 }

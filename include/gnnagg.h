@@ -357,7 +357,11 @@ gnn_status transformer_agg_backward(const gnn_graph* g, int H, int D, gnn_dtype 
  * with two sides, at most 128.
  * An entry of -infinity masks its bucket for that head: those edges get weight
  * and gradient 0 whatever their rows hold; a (node, head) with no other edge
- * gets out = 0 and lse = -infinity.  Any other bias enters as it is. */
+ * gets out = 0 and lse = -infinity.  Any finite bias enters as it is, whatever its
+ * size: weights depend on the differences of a row's scores, and these keep float32
+ * accuracy beside a bias of 1e9 as beside 0.  At 2^60 and above the dot product beside a
+ * bias counts for nothing, as in their sum in 64 bits: a row whose edges all carry the
+ * type's lowest value has equal weights. */
 
 /* Host only: bounds of the logarithmic rule.  Distances below m = n_bounds / 2
  * have a bucket each; bucket m + k starts at the smallest whole t with
