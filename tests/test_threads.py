@@ -1,0 +1,108 @@
+"""Calls of several host threads at once, each on a stream of its own.  Their kernels are the
+same functions with tables of different sizes in shared memory; the size that one thread's
+call needs must not limit another's."""
+import os
+import subprocess
+import sys
+import threading
+
+import pytest
+import torch
+
+from workload import testgraphs
+from gpu_util import device_graph
+
+pytestmark = pytest.mark.gpu
+
+# Waits 1 ms after a function's limit of shared memory (attribute 8) is set, so that another
+# thread's call falls between that and the launch.
+SLOW = r"""
+#define _GNU_SOURCE
+#include <dlfcn.h>
+#include <unistd.h>
+int cudaFuncSetAttribute(const void* f, int attr, int value) {
+  static int (*real)(const void*, int, int);
+  if (!real) {
+    void* h = dlopen("libcudart.so.13", RTLD_LAZY | RTLD_NOLOAD);
+    real = (int (*)(const void*, int, int))dlsym(h, "cudaFuncSetAttribute");
+  }
+  const int r = real(f, attr, value);
+  if (attr == 8) usleep(1000);
+  return r;
+}
+"""
+
+
+def backward_calls(checkpoints):
+    """Backward calls of 128, 40 and 64 buckets (147, 46 and 74 KB of shared memory in the
+    same kernel), with everything that they write given."""
+    import graph_neural_network_gb300 as gnn
+    rp, ci = testgraphs.with_in_degrees([5] * 60, n_nodes=64, seed=1)
+    g = device_graph(dict(row_ptr=rp, col=ci))
+    pos = torch.arange(64, dtype=torch.int32, device="cuda")
+    gen = torch.Generator("cuda").manual_seed(1)
+    q, k, v, d = (torch.randn(64, 1, 8, generator=gen, device="cuda").bfloat16()
+                  for _ in range(4))
+    packed = gnn.pack8(q, k, v)
+
+    def call(buckets):
+        rel = gnn.RelPos(g, pos, buckets, 200)
+        bias = torch.linspace(-1, 1, buckets, device="cuda")[:, None].contiguous()
+        ws = rel.workspace(1, 8, torch.bfloat16)
+        got = dict(dq=torch.empty_like(q), dkey=torch.empty_like(q), dval=torch.empty_like(q),
+                   dbias=torch.empty_like(bias))
+        _, lse = gnn.transformer_rel_forward(g, rel, q, k, v, bias)
+        if checkpoints:
+            return lambda **kw: gnn.transformer_backward8(g, *packed, d, rel=rel, bias=bias, ws=ws,
+                                                          **got, **kw)
+        return lambda **kw: gnn.transformer_rel_backward(g, rel, q, k, v, bias, lse, d, ws=ws,
+                                                         **got, **kw)
+
+    return [call(b) for b in (128, 40, 64)]
+
+
+def run_at_once(checkpoints, turns):
+    calls = backward_calls(checkpoints)
+    want = [[t.clone() for t in c()] for c in calls]
+    torch.cuda.synchronize()
+    failed = []
+
+    def work(c):
+        stream = torch.cuda.Stream()
+        try:
+            for turn in range(turns):
+                c(stream=stream)
+                if turn % 100 == 0:
+                    stream.synchronize()
+        except Exception as e:  # noqa: BLE001
+            failed.append(e)
+        stream.synchronize()
+
+    threads = [threading.Thread(target=work, args=(c,)) for c in calls]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not failed, failed
+    for c, w in zip(calls, want):
+        assert all(torch.equal(a, b) for a, b in zip(c(), w))
+
+
+@pytest.mark.parametrize("checkpoints", [False, True], ids=["rows", "checkpoints"])
+def test_backward_passes_with_different_bucket_counts(checkpoints):
+    run_at_once(checkpoints, 1000)
+
+
+def test_a_call_between_another_ones_limit_and_launch(tmp_path):
+    """The same in a child process in which setting the limit takes a millisecond."""
+    src, lib = tmp_path / "slow.c", tmp_path / "slow.so"
+    src.write_text(SLOW)
+    subprocess.run(["gcc", "-shared", "-fPIC", "-o", str(lib), str(src), "-ldl"], check=True)
+    here = os.path.dirname(os.path.abspath(__file__))
+    code = ("import test_threads as t\n"
+            "t.run_at_once(False, 60)\nt.run_at_once(True, 60)\nprint('both ran')\n")
+    env = dict(os.environ, LD_PRELOAD=str(lib), PYTHONPATH=os.pathsep.join(
+        [here, os.path.dirname(here), os.environ.get("PYTHONPATH", "")]))
+    r = subprocess.run([sys.executable, "-c", code], env=env, cwd=os.path.dirname(here),
+                       capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0 and "both ran" in r.stdout, r.stderr[-2000:]
