@@ -7,6 +7,8 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include <mutex>
+
 #include "internal.h"
 
 namespace gnn {
@@ -612,6 +614,20 @@ __host__ int persistent_blocks(K kernel, size_t smem, int sm_count) {
       per_sm < 1)
     per_sm = 1;
   return per_sm * (sm_count > 0 ? sm_count : 1);
+}
+
+// Lets `kernel` be launched with `bytes` of dynamic shared memory (up to `always` it can be
+// without this).  The limit belongs to the function, so it is only ever raised: set to a call's
+// own size, another thread's call could lower it between this one's setting and its launch.
+template <typename K>
+inline cudaError_t allow_smem(K kernel, size_t bytes, size_t always = 48 * 1024) {
+  if (bytes <= always) return cudaSuccess;
+  static std::mutex one;  // of all kernels of this signature
+  const std::lock_guard<std::mutex> lock(one);
+  cudaFuncAttributes now;
+  const cudaError_t e = cudaFuncGetAttributes(&now, kernel);
+  if (e != cudaSuccess || size_t(now.maxDynamicSharedSizeBytes) >= bytes) return e;
+  return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, int(bytes));
 }
 
 // A kernel launched by launch_after may start while the kernel before it in the

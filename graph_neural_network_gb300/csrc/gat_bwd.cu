@@ -778,12 +778,6 @@ __global__ void __launch_bounds__(kThreads) da_final(const double* part, int blo
   }
 }
 
-template <typename K>
-cudaError_t set_smem(K kernel, size_t bytes) {
-  if (bytes <= 48 * 1024) return cudaSuccess;
-  return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, int(bytes));
-}
-
 // Launch a kernel template instantiated for the 16-byte lane geometry M.s.
 template <typename T, template <typename, int> class K>
 cudaError_t launch16(const BwdArgs& M, unsigned grid, size_t smem, cudaStream_t st) {
@@ -814,7 +808,7 @@ struct SrcMerge {
 template <typename T, int NV>
 struct DaPartial {
   static cudaError_t launch(const BwdArgs& M, unsigned grid, size_t smem, cudaStream_t st) {
-    cudaError_t e = set_smem(da_partial<T, NV>, smem);
+    cudaError_t e = allow_smem(da_partial<T, NV>, smem);
     if (e != cudaSuccess) return e;
     da_partial<T, NV><<<grid, kThreads, smem, st>>>(M);
     return cudaSuccess;
@@ -850,7 +844,7 @@ cudaError_t launch_t(const BwdArgs& A, const Shape& s16, gnn_dtype dt, int sm_co
     const size_t smem = size_t(A.csr.col_off) + size_t(kWarps) * H * 3 * 4;
     if (work > 0) {
       auto kernel = sub ? bwd_dst_main<T, NV, VB, NV == 1> : bwd_dst_main<T, NV, VB, false>;
-      if ((e = set_smem(kernel, smem)) != cudaSuccess) return e;
+      if ((e = allow_smem(kernel, smem)) != cudaSuccess) return e;
       const int64_t cap = persistent_blocks(kernel, smem, sm_count);
       const int64_t blocks = work < cap ? work : cap;
       kernel<<<unsigned(blocks), kThreads, smem, st>>>(A);
@@ -869,7 +863,7 @@ cudaError_t launch_t(const BwdArgs& A, const Shape& s16, gnn_dtype dt, int sm_co
     const size_t smem = size_t(A.csc.col_off) + size_t(kWarps) * (H + row_f) * 4;
     if (work > 0) {
       auto kernel = sub ? bwd_src_main<T, NV, VB, NV == 1> : bwd_src_main<T, NV, VB, false>;
-      if ((e = set_smem(kernel, smem)) != cudaSuccess) return e;
+      if ((e = allow_smem(kernel, smem)) != cudaSuccess) return e;
       const int64_t cap = persistent_blocks(kernel, smem, sm_count);
       const int64_t blocks = work < cap ? work : cap;
       kernel<<<unsigned(blocks), kThreads, smem, st>>>(A);
@@ -888,7 +882,7 @@ cudaError_t launch_t(const BwdArgs& A, const Shape& s16, gnn_dtype dt, int sm_co
     const size_t smem = size_t(kWarps) * (32 / s16.lpr) * 2 * row_f * 4;
     void (*dk)(const BwdArgs) =
         M.s.nv == 1 ? da_partial<T, 1> : (M.s.nv == 2 ? da_partial<T, 2> : da_partial<T, 4>);
-    if ((e = set_smem(dk, smem)) != cudaSuccess) return e;
+    if ((e = allow_smem(dk, smem)) != cudaSuccess) return e;
     BwdArgs Md = M;
     const int64_t resident = persistent_blocks(dk, smem, sm_count);
     if (resident < Md.da_blocks) Md.da_blocks = int(resident);

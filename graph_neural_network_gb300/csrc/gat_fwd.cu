@@ -472,10 +472,7 @@ cudaError_t launch_t(const FwdArgs& A, const Shape& s16, gnn_dtype dt, const flo
     // rows that do not fill the warp give each light node a sub-group (NV = 1)
     auto kernel = (NV == 1 && A.s.lpr < 32) ? fwd_main<T, NV, VB, NV == 1>
                                              : fwd_main<T, NV, VB, false>;
-    if (smem > 48 * 1024 &&
-        (e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                  int(smem))) != cudaSuccess)
-      return e;
+    if ((e = allow_smem(kernel, smem)) != cudaSuccess) return e;
     const int64_t work = A.n_items + (A.n_light + kWarps * kGrab - 1) / (kWarps * kGrab);
     const int64_t cap = persistent_blocks(kernel, smem, sm_count);
     const int64_t blocks = work < cap ? work : cap;

@@ -978,12 +978,6 @@ __global__ void __launch_bounds__(kThreads) v2_datt_final(const double* part, in
   if (lane == 0) datt[t] = float(s);
 }
 
-template <typename K>
-cudaError_t set_smem(K kernel, size_t bytes) {
-  if (bytes <= 48 * 1024) return cudaSuccess;
-  return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, int(bytes));
-}
-
 template <typename T>
 cudaError_t fwd_t(const V2Args& A, int sm_count, cudaStream_t st) {
   constexpr int V = VecOf<T>::n;
@@ -994,7 +988,7 @@ cudaError_t fwd_t(const V2Args& A, int sm_count, cudaStream_t st) {
   if (D.n_items + D.n_light > 0) {
     const size_t smem = size_t(D.col_off) + size_t(kWarps) * (2 * A.s.H + row_f) * 4;
     auto kernel = A.s.lpr < 32 ? v2_fwd_main<T, true> : v2_fwd_main<T, false>;
-    if ((e = set_smem(kernel, smem)) != cudaSuccess) return e;
+    if ((e = allow_smem(kernel, smem)) != cudaSuccess) return e;
     const int64_t work = D.n_items + (D.n_light + kWarps * kGrab - 1) / (kWarps * kGrab);
     const int64_t cap = persistent_blocks(kernel, smem, sm_count);
     kernel<<<unsigned(work < cap ? work : cap), kThreads, smem, st>>>(A);
@@ -1023,7 +1017,7 @@ cudaError_t bwd_t(V2Args A, int sm_count, cudaStream_t st) {
     const size_t smem =
         size_t(D.col_off) + size_t(kWarps) * (A.s.H + 2 * row_f + nsub * row_f) * 4;
     auto kernel = sub ? v2_dst_main<T, true> : v2_dst_main<T, false>;
-    if ((e = set_smem(kernel, smem)) != cudaSuccess) return e;
+    if ((e = allow_smem(kernel, smem)) != cudaSuccess) return e;
     int64_t blocks = persistent_blocks(kernel, smem, sm_count);
     if (blocks > cap) blocks = cap;
     A.da_main_rows = int(blocks);
@@ -1041,7 +1035,7 @@ cudaError_t bwd_t(V2Args A, int sm_count, cudaStream_t st) {
     const V2Dir& D = A.csc;
     const size_t smem = size_t(D.col_off) + size_t(kWarps) * (1 + nsub) * row_f * 4;
     auto kernel = sub ? v2_src_main<T, true> : v2_src_main<T, false>;
-    if ((e = set_smem(kernel, smem)) != cudaSuccess) return e;
+    if ((e = allow_smem(kernel, smem)) != cudaSuccess) return e;
     int64_t blocks = persistent_blocks(kernel, smem, sm_count);
     if (blocks > cap) blocks = cap;
     kernel<<<unsigned(blocks), kThreads, smem, st>>>(A);

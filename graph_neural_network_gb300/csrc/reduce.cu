@@ -403,10 +403,7 @@ cudaError_t launch_fwd_t(const RedArgs& A, bool asc, int sm_count, cudaStream_t 
     } else {
       kernel = mn ? red_fwd_main<T, NV, false, true, false> : red_fwd_main<T, NV, false, false, false>;
     }
-    if (smem > 48 * 1024 &&
-        (e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                  int(smem))) != cudaSuccess)
-      return e;
+    if ((e = allow_smem(kernel, smem)) != cudaSuccess) return e;
     const int64_t work = A.n_items + (A.n_light + kWarps * kGrab - 1) / (kWarps * kGrab);
     const int64_t cap = persistent_blocks(kernel, smem, sm_count);
     const int64_t blocks = work < cap ? work : cap;

@@ -194,13 +194,6 @@ __host__ __device__ inline size_t grad_tables_bytes(const Shape& s, int buckets)
   return grad_columns(s, buckets) * (grad_pairs(s, buckets) ? 8 : 4);
 }
 
-// The most dynamic shared memory that a pass with a bias takes: gradient tables of sums
-// alone and the bias table, of the most buckets and heads of 16 bytes.  The limit of a
-// function is set to this and not to a call's own size: it belongs to the function, and
-// another thread's call could lower it between this one's setting and its launch.
-constexpr size_t kMostBiasBytes = (size_t(kWarps) * kMaxBuckets * 32 + kMaxBuckets * 32) * 4;
-static_assert(kPairBytes + kMaxBuckets * 32 * 4 <= kMostBiasBytes, "pairs take less");
-
 // Clears the block's tables (a barrier must follow) and returns this lane's column.
 __device__ __forceinline__ float* clear_grad_tables(float* tables, const Shape& s,
                                                     const Lane<1>& L, int buckets) {

@@ -355,10 +355,7 @@ cudaError_t launch_main(const SpmmArgs& A, int sm_count, cudaStream_t st) {
   }
   const size_t smem = size_t(A.col_off) + size_t(kWarps) * A.s.rv * V * 4;
   cudaError_t e;
-  if (smem > 48 * 1024 &&
-      (e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                int(smem))) != cudaSuccess)
-    return e;
+  if ((e = allow_smem(kernel, smem)) != cudaSuccess) return e;
   const int64_t work = A.n_items + (A.n_light + kWarps * kGrab - 1) / (kWarps * kGrab);
   const int64_t cap = persistent_blocks(kernel, smem, sm_count);
   const int64_t blocks = work < cap ? work : cap;

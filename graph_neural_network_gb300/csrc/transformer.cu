@@ -823,18 +823,12 @@ __global__ void __launch_bounds__(kThreads) gt_src_merge(const GtArgs A) {
   src_write<T>(A, L, hb.x, dk, dv);
 }
 
-template <typename K>
-cudaError_t set_smem(K kernel, size_t bytes) {
-  if (bytes <= 48 * 1024) return cudaSuccess;
-  return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, int(bytes));
-}
-
 template <typename T, typename K>
 cudaError_t persistent_launch(K kernel, const GtArgs& A, const GtDir& D, size_t smem,
                               int sm_count, cudaStream_t st) {
   if (D.n_items + D.n_light == 0) return cudaSuccess;
   cudaError_t e;
-  if ((e = set_smem(kernel, smem)) != cudaSuccess) return e;
+  if ((e = allow_smem(kernel, smem)) != cudaSuccess) return e;
   const int64_t work = D.n_items + (D.n_light + kWarps * kGrab - 1) / (kWarps * kGrab);
   const int64_t cap = persistent_blocks(kernel, smem, sm_count);
   kernel<<<unsigned(work < cap ? work : cap), kThreads, smem, st>>>(A);

@@ -560,10 +560,7 @@ cudaError_t launch(void (*kernel)(RelArgs), const RelArgs& A, int blocks, size_t
                    cudaStream_t st, bool after = false) {
   cudaError_t e;
   // (the default limit, 48 KB, counts the kernels' static 16 KB too)
-  if (smem > 32 * 1024 &&
-      (e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                int(kMostBiasBytes))) != cudaSuccess)
-    return e;
+  if ((e = allow_smem(kernel, smem, 32 * 1024)) != cudaSuccess) return e;
   if (after) return launch_after(kernel, dim3(unsigned(blocks)), kThreads, smem, st, A);
   kernel<<<unsigned(blocks), kThreads, smem, st>>>(A);
   return cudaGetLastError();

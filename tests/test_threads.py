@@ -20,13 +20,15 @@ SLOW = r"""
 #define _GNU_SOURCE
 #include <dlfcn.h>
 #include <unistd.h>
+static int refusing;
+void refuse(int on) { refusing = on; }
 int cudaFuncSetAttribute(const void* f, int attr, int value) {
   static int (*real)(const void*, int, int);
   if (!real) {
     void* h = dlopen("libcudart.so.13", RTLD_LAZY | RTLD_NOLOAD);
     real = (int (*)(const void*, int, int))dlsym(h, "cudaFuncSetAttribute");
   }
-  const int r = real(f, attr, value);
+  const int r = real(f, attr, attr == 8 && refusing ? 1 << 30 : value);
   if (attr == 8) usleep(1000);
   return r;
 }
@@ -61,8 +63,34 @@ def backward_calls(checkpoints):
     return [call(b) for b in (128, 40, 64)]
 
 
-def run_at_once(checkpoints, turns):
-    calls = backward_calls(checkpoints)
+def aggregation_calls(name):
+    """Forward calls over nodes of 13,000, 14,500 and 16,000 edges that each go to one block
+    with its edge list (52 to 64 KB of shared memory in the same kernel)."""
+    import graph_neural_network_gb300 as gnn
+
+    def call(deg):
+        rp = torch.tensor([0] + [deg] * 64, dtype=torch.int32, device="cuda")
+        ci = torch.arange(deg, dtype=torch.int32, device="cuda") % 64
+        g = gnn.Graph(rp, ci, gnn.Tiling(64, 16384, 2048))
+        x = torch.linspace(-1, 1, 64 * 32, device="cuda").view(64, 1, 32).contiguous()
+        out, lse = torch.empty_like(x), torch.empty(64, 1, device="cuda")
+        a = torch.linspace(-1, 1, 32, device="cuda")[None]
+        arg = torch.empty(64, 32, dtype=torch.int32, device="cuda")
+        ws = torch.empty(1 << 24, dtype=torch.uint8, device="cuda")
+        return {
+            "gat": lambda **kw: gnn.gat_forward(g, x, a, a, out=out, lse=lse, ws=ws, **kw),
+            "gatv2": lambda **kw: gnn.gatv2_forward(g, x, x, a, out=out, lse=lse, ws=ws, **kw),
+            "transformer": lambda **kw: gnn.transformer_forward(g, x, x, x, out=out, lse=lse,
+                                                                ws=ws, **kw),
+            "gcn": lambda **kw: (gnn.gcn_forward(g, x[:, 0], "sum", out=out[:, 0], ws=ws, **kw),),
+            "max": lambda **kw: gnn.reduce_forward(g, x[:, 0], "max", out=out[:, 0], arg=arg,
+                                                   ws=ws, **kw),
+        }[name]
+
+    return [call(d) for d in (16_000, 13_000, 14_500)]
+
+
+def run_at_once(calls, turns):
     want = [[t.clone() for t in c()] for c in calls]
     torch.cuda.synchronize()
     failed = []
@@ -90,19 +118,29 @@ def run_at_once(checkpoints, turns):
 
 @pytest.mark.parametrize("checkpoints", [False, True], ids=["rows", "checkpoints"])
 def test_backward_passes_with_different_bucket_counts(checkpoints):
-    run_at_once(checkpoints, 1000)
+    run_at_once(backward_calls(checkpoints), 1000)
 
 
-def test_a_call_between_another_ones_limit_and_launch(tmp_path):
-    """The same in a child process in which setting the limit takes a millisecond."""
+def child(tmp_path, code):
+    """Runs code in a process where setting a limit takes a millisecond."""
     src, lib = tmp_path / "slow.c", tmp_path / "slow.so"
     src.write_text(SLOW)
     subprocess.run(["gcc", "-shared", "-fPIC", "-o", str(lib), str(src), "-ldl"], check=True)
     here = os.path.dirname(os.path.abspath(__file__))
-    code = ("import test_threads as t\n"
-            "t.run_at_once(False, 60)\nt.run_at_once(True, 60)\nprint('both ran')\n")
     env = dict(os.environ, LD_PRELOAD=str(lib), PYTHONPATH=os.pathsep.join(
         [here, os.path.dirname(here), os.environ.get("PYTHONPATH", "")]))
-    r = subprocess.run([sys.executable, "-c", code], env=env, cwd=os.path.dirname(here),
-                       capture_output=True, text=True, timeout=300)
-    assert r.returncode == 0 and "both ran" in r.stdout, r.stderr[-2000:]
+    r = subprocess.run([sys.executable, "-c", f"SHIM = {str(lib)!r}\n{code}\nprint('done')\n"],
+                       env=env, cwd=os.path.dirname(here), capture_output=True, text=True,
+                       timeout=300)
+    assert r.returncode == 0 and "done" in r.stdout, r.stderr[-2000:]
+
+
+@pytest.mark.parametrize("checkpoints", [False, True], ids=["rows", "checkpoints"])
+def test_a_call_between_another_ones_limit_and_launch(tmp_path, checkpoints):
+    child(tmp_path, "import test_threads as t\n"
+                    f"t.run_at_once(t.backward_calls({checkpoints}), 60)")
+
+
+@pytest.mark.parametrize("name", ["gat", "gatv2", "transformer", "gcn", "max"])
+def test_the_same_in_the_aggregations(tmp_path, name):
+    child(tmp_path, f"import test_threads as t\nt.run_at_once(t.aggregation_calls({name!r}), 60)")
