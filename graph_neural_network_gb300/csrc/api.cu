@@ -127,7 +127,14 @@ gnn_status check_call(const gnn_graph* g, int H, int D, gnn_dtype dt, Shape* s) 
   return GNN_OK;
 }
 
-gnn_status from_cuda(cudaError_t e) { return e == cudaSuccess ? GNN_OK : GNN_ERR_CUDA; }
+// The status of a call's launches.  A refused one (cudaLaunchKernelEx, an attribute) also
+// stays as the thread's last error, which the next call's cudaGetLastError would take for
+// its own: it is taken here.
+gnn_status from_cuda(cudaError_t e) {
+  if (e == cudaSuccess) return GNN_OK;
+  (void)cudaGetLastError();
+  return GNN_ERR_CUDA;
+}
 
 }  // namespace
 

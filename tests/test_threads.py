@@ -144,3 +144,27 @@ def test_a_call_between_another_ones_limit_and_launch(tmp_path, checkpoints):
 @pytest.mark.parametrize("name", ["gat", "gatv2", "transformer", "gcn", "max"])
 def test_the_same_in_the_aggregations(tmp_path, name):
     child(tmp_path, f"import test_threads as t\nt.run_at_once(t.aggregation_calls({name!r}), 60)")
+
+
+def test_a_refused_launch_leaves_no_error_behind(tmp_path):
+    """A call whose kernel cannot be launched raises; the next call, whose kernels can, does
+    not find that error.  (The host refuses a limit far above the device's.)"""
+    child(tmp_path, """
+import ctypes
+import pytest
+import torch
+import graph_neural_network_gb300 as gnn
+import test_threads as t
+big = t.backward_calls(False)[0]
+shim = ctypes.CDLL(SHIM)
+x = torch.ones(8, 16, device="cuda")
+want = gnn.norm_residual_forward(x, x)[0]
+# (a fresh kernel: the limit of the first one is set already)
+shim.refuse(1)
+with pytest.raises(gnn.GnnError):
+    t.backward_calls(True)[0]()
+shim.refuse(0)
+assert torch.equal(gnn.norm_residual_forward(x, x)[0], want)
+big()
+torch.cuda.synchronize()
+""")
