@@ -56,12 +56,17 @@ struct NrArgs {
 enum { kSumA, kSumB, kSumW, kSumC, kSums };
 static_assert(kSums == 4, "nr_sum takes them in two pairs");
 
-__device__ __forceinline__ float sigmoid(float g) {
-  // 1 / (1 + 2^(-g log2 e)); the exponential overflows to infinity and the
-  // reciprocal to 0 where the sigmoid is below the smallest float
+// A gate's e = 2^(-g log2 e), from which s = sigmoid(g) = 1 / (1 + e) and 1 - s = e s, both
+// accurate relative to themselves (a difference from 1 has lost 1 - s at g = 17).  e
+// overflows to infinity and s to 0 where the sigmoid is below the smallest float.
+__device__ __forceinline__ float gate_e(float g) { return ex2(-kLog2e * g); }
+__device__ __forceinline__ float sigmoid_of(float e) {
   float r;
-  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.f + ex2(-kLog2e * g)));
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.f + e));
   return r;
+}
+__device__ __forceinline__ float complement_of(float e, float s) {
+  return e == INFINITY ? 1.f : e * s;
 }
 
 // Element-wise arithmetic on a thread's vector, two floats an instruction.
@@ -155,19 +160,27 @@ __device__ __forceinline__ uint4 load_gate(const NrArgs& A, const Place& P, int6
   return load_raw(A.gate, row * A.rv + P.vec, ok && A.gate_width > 1);
 }
 
+// The gates' e (0 without a gate).
 template <typename T>
 __device__ __forceinline__ void open_gate(const NrArgs& A, const uint4& raw,
-                                          float (&s)[VecOf<T>::n]) {
+                                          float (&e)[VecOf<T>::n]) {
   constexpr int V = VecOf<T>::n;
   if (A.gate_width > 1) {
-    unpack<T>(raw, s);
+    unpack<T>(raw, e);
 #pragma unroll
-    for (int c = 0; c < V; ++c) s[c] = sigmoid(s[c]);
+    for (int c = 0; c < V; ++c) e[c] = gate_e(e[c]);
   } else {
-    const float t = A.gate_width == 1 ? sigmoid(__uint_as_float(raw.x)) : 1.f;
+    const float t = A.gate_width == 1 ? gate_e(__uint_as_float(raw.x)) : 0.f;
 #pragma unroll
-    for (int c = 0; c < V; ++c) s[c] = t;
+    for (int c = 0; c < V; ++c) e[c] = t;
   }
+}
+
+// e becomes the gates' sigmoids.
+template <int V>
+__device__ __forceinline__ void sigmoids(float (&e)[V]) {
+#pragma unroll
+  for (int c = 0; c < V; ++c) e[c] = sigmoid_of(e[c]);
 }
 
 template <int V>
@@ -244,6 +257,7 @@ __global__ void __launch_bounds__(kThreads, NrBlocks<T>::fwd) nr_fwd(const NrArg
     unpack<T>(ro, o);
     unpack<T>(rx, y);
     open_gate<T>(A, rg, s);
+    sigmoids<V>(s);
     const int64_t at = row * A.rv + P.vec;
     const bool now = ok;
     row += P.stride;
@@ -373,12 +387,12 @@ __global__ void __launch_bounds__(kThreads, kBwdPerSm) nr_bwd(const NrArgs A) {
   };
   load();
   for (; r0 < A.n; r0 += P.stride) {
-    float o[V], y[V], s[V], d[V], g[V];
+    float o[V], y[V], e[V], d[V], g[V];
     unpack<T>(ry, y);
     unpack<T>(rz, g);
     unpack<T>(rd, d);
     unpack<T>(ro, o);
-    open_gate<T>(A, rg, s);
+    open_gate<T>(A, rg, e);
     const int64_t this_row = row, at = row * A.rv + P.vec;
     const bool now = ok;
     row += P.stride;
@@ -396,7 +410,9 @@ __global__ void __launch_bounds__(kThreads, kBwdPerSm) nr_bwd(const NrArgs A) {
     if (now) st16(reinterpret_cast<char*>(A.dx) + 16 * at, pack<T>(d));
     // d becomes dx sigmoid(g) (0 on a thread without a vector or a row: it adds
     // nothing to the sums), y the gate's gradient d n (1 - sigmoid(g)), g = d wp
-    if (!now) zero<V>(s);
+    float s[V];
+#pragma unroll
+    for (int c = 0; c < V; ++c) s[c] = now ? sigmoid_of(e[c]) : 0.f;
     vmul<V>(d, d, s);
     vfma<V>(acc[kSumA], d, o, acc[kSumA]);
     vadd<V>(acc[kSumB], d);
@@ -406,7 +422,7 @@ __global__ void __launch_bounds__(kThreads, kBwdPerSm) nr_bwd(const NrArgs A) {
       vfma<V>(y, o, wp, bp);
       vmul<V>(y, y, d);
 #pragma unroll
-      for (int c = 0; c < V; ++c) s[c] = 1.f - s[c];
+      for (int c = 0; c < V; ++c) s[c] = complement_of(e[c], s[c]);
       vmul<V>(y, y, s);
       if (kRow) all = total<V>(y);
     }
