@@ -50,6 +50,9 @@ and the max / min neighbourhood reduction with its winners:
 
     out, arg = reduce_forward(g, x, "max")         # arg [N, F] int32, -1 if no in-edges
     dx = reduce_backward(g, arg, dout)
+
+The autograd Functions' backward passes are kernels without derivatives of their own: a
+second derivative through them raises an error.
 """
 from __future__ import annotations
 
@@ -59,6 +62,7 @@ import math
 from typing import NamedTuple
 
 import torch
+from torch.autograd.function import once_differentiable
 
 from . import _native
 from ._native import GnnError, Tiling
@@ -331,6 +335,7 @@ class GCNAggregate(torch.autograd.Function):
         return gcn_forward(g, x.contiguous(), norm)
 
     @staticmethod
+    @once_differentiable
     def backward(ctx, dout):
         return None, gcn_backward(ctx.g, dout.contiguous(), ctx.norm), None
 
@@ -401,6 +406,7 @@ class GATv2Aggregate(torch.autograd.Function):
         return out
 
     @staticmethod
+    @once_differentiable
     def backward(ctx, dout):
         xl, xr, att, lse = ctx.saved_tensors
         dxl, dxr, datt = gatv2_backward(ctx.g, xl, xr, att, ctx.slope, lse, dout.contiguous())
@@ -474,6 +480,7 @@ class TransformerAggregate(torch.autograd.Function):
         return out
 
     @staticmethod
+    @once_differentiable
     def backward(ctx, dout):
         q, key, val, lse = ctx.saved_tensors
         dq, dk, dv = transformer_backward(ctx.g, q, key, val, lse, dout.contiguous(), ctx.scale)
@@ -691,6 +698,7 @@ class TransformerRelAggregate(torch.autograd.Function):
         return out
 
     @staticmethod
+    @once_differentiable
     def backward(ctx, dout):
         q, key, val, bias, lse = ctx.saved_tensors
         dq, dk, dv, db = transformer_rel_backward(ctx.g, ctx.rel, q, key, val, bias, lse,
@@ -824,6 +832,7 @@ class TransformerCheckpoint8(torch.autograd.Function):
         return out
 
     @staticmethod
+    @once_differentiable
     def backward(ctx, dout):
         *flat, bias = ctx.saved_tensors
         c = [Packed8(*flat[k:k + 2]) for k in (0, 2, 4)]
@@ -952,6 +961,7 @@ class NormResidual(torch.autograd.Function):
         return y, z
 
     @staticmethod
+    @once_differentiable
     def backward(ctx, dy, dz):
         y, o, gate, *params = ctx.saved_tensors
         dz = None if y is None else dz.contiguous()
@@ -1046,6 +1056,7 @@ class ReduceAggregate(torch.autograd.Function):
         return out
 
     @staticmethod
+    @once_differentiable
     def backward(ctx, dout):
         (arg,) = ctx.saved_tensors
         return None, reduce_backward(ctx.g, arg, dout.contiguous()), None
@@ -1074,6 +1085,7 @@ class GATAggregate(torch.autograd.Function):
         return out
 
     @staticmethod
+    @once_differentiable
     def backward(ctx, dout):
         h, a_src, a_dst, lse = ctx.saved_tensors
         dh, da_s, da_d = gat_backward(ctx.g, h, a_src, a_dst, ctx.slope, lse, dout.contiguous(),
