@@ -56,9 +56,11 @@ struct NrArgs {
 enum { kSumA, kSumB, kSumW, kSumC, kSums };
 static_assert(kSums == 4, "nr_sum takes them in two pairs");
 
-// A gate's e = 2^(-g log2 e), from which s = sigmoid(g) = 1 / (1 + e) and 1 - s = e s, both
-// accurate relative to themselves (a difference from 1 has lost 1 - s at g = 17).  e
-// overflows to infinity and s to 0 where the sigmoid is below the smallest float.
+// A gate's e = 2^(-g log2 e), from which s = sigmoid(g) = 1 / (1 + e) and 1 - s, both
+// accurate relative to themselves: 1 - s = e s where the gate is open (the difference has
+// lost it at g = 17), the difference where s is at most two thirds (it has fewer
+// roundings).  e overflows to infinity and s to 0 where the sigmoid is below the smallest
+// float.
 __device__ __forceinline__ float gate_e(float g) { return ex2(-kLog2e * g); }
 __device__ __forceinline__ float sigmoid_of(float e) {
   float r;
@@ -66,7 +68,7 @@ __device__ __forceinline__ float sigmoid_of(float e) {
   return r;
 }
 __device__ __forceinline__ float complement_of(float e, float s) {
-  return e == INFINITY ? 1.f : e * s;
+  return e < 0.5f ? e * s : 1.f - s;
 }
 
 // Element-wise arithmetic on a thread's vector, two floats an instruction.
