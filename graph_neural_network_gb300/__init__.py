@@ -622,6 +622,9 @@ def _rel_bias(g: Graph, rel: RelPos, bias, H: int):
     if rel.graph is not g:
         raise ValueError("rel was prepared for another graph")
     _check_tensor(g, bias, "bias", (rel.buckets, H), floating=True)
+    if bias.dtype == torch.float64:  # finite entries stay finite: an infinity masks
+        top = torch.finfo(torch.float32).max
+        bias = torch.where(bias.isinf(), bias, bias.clamp(-top, top))
     return bias if bias.dtype == torch.float32 else bias.to(torch.float32)
 
 

@@ -204,6 +204,31 @@ def test_scores_of_minus_infinity_and_masked_rows():
     assert not dval[3].any() and torch.isfinite(dval).all()
 
 
+@pytest.mark.gpu
+def test_a_float64_table_keeps_its_finite_entries_finite():
+    """float64's lowest value is not representable in float32; it stays a bias, and only
+    -infinity masks."""
+    import graph_neural_network_gb300 as gnn
+    rp, ci = graph(3)
+    n = len(rp) - 1
+    g = device_graph(dict(row_ptr=rp, col=ci))
+    rel = gnn.RelPos(g, torch.from_numpy(positions(n, 3, 300)).cuda())
+    q, k, v, dout = (to_device(x, "f32") for x in features(n, 2, 16, "f32", 3))
+    for low, high in ((-np.inf, F32), (-F32, 0.5), (-F32, F32)):
+        b32 = torch.full((32, 2), low, device="cuda")
+        b32[8:, 1] = high
+        b64 = b32.double()
+        b64[b32 == -F32] = torch.finfo(torch.float64).min
+        b64[b32 == F32] = torch.finfo(torch.float64).max
+        want = gnn.transformer_rel_forward(g, rel, q, k, v, b32)
+        got = gnn.transformer_rel_forward(g, rel, q, k, v, b64)
+        assert all(torch.equal(a, b) for a, b in zip(got, want))
+        want = gnn.transformer_rel_backward(g, rel, q, k, v, b32, got[1], dout)
+        got = gnn.transformer_rel_backward(g, rel, q, k, v, b64, got[1], dout)
+        assert all(torch.equal(a, b) for a, b in zip(got, want))
+        assert torch.isfinite(got[0]).all()
+
+
 def test_the_reference_agrees_with_the_plain_one():
     """At ordinary biases it is the reference of the other tests."""
     rp, ci = graph(3)
