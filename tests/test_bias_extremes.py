@@ -155,6 +155,68 @@ def test_beside_ordinary_ones(value, H, D, dtype):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("H, D, dtype, buckets", [
+    (1, 4, "f32", 32), (32, 4, "f32", 128), (3, 8, "f32", 40), (4, 32, "f32", 64),
+    (1, 128, "f32", 32), (1, 8, "bf16", 128), (32, 8, "bf16", 128), (5, 16, "bf16", 32),
+    (1, 256, "bf16", 32)])
+def test_shapes(H, D, dtype, buckets):
+    """Every lane width and form of the gradient tables, with a mask value in one bucket of
+    each side and one head."""
+    rp, ci = graph(H + D)
+    n = len(rp) - 1
+    bias = workload.normal_f32(3, 7, (buckets, H), 1.0)
+    bias[1], bias[buckets // 2 + 1] = -1e9, -F32
+    bias[2, H - 1] = 1e5
+    check_both(rp, ci, H, D, dtype, bias, positions(n, 3, 300), f"{H} {D}",
+               rel_args=(buckets, 400))
+
+
+@pytest.mark.gpu
+def test_reproducible_captured_and_masked():
+    """A power-law graph with every kind of bias: the same bits again, on another stream and
+    from a CUDA graph, and with NaN and infinities in the rows that only masked edges reach."""
+    import graph_neural_network_gb300 as gnn
+    rp, ci = workload.chung_lu(20_000, 2.1, 15.0, 6_000.0, 29)
+    n = len(rp) - 1
+    ci = np.where(ci == 17, 18, ci).astype(np.int32)
+    dst = np.repeat(np.arange(n), np.diff(rp))
+    ci[::50] = np.where(dst[::50] != 17, 17, ci[::50])      # node 17: a source far after all
+    pos = np.random.default_rng(1).integers(0, 100, n).astype(np.int32)
+    pos[17] = 10_000
+    g = device_graph(dict(row_ptr=rp, col=ci))
+    rel = gnn.RelPos(g, torch.from_numpy(pos).cuda(), 32, 128)
+    b = torch.from_numpy(workload.normal_f32(3, 7, (32, 2), 1.0)).cuda()
+    b[2], b[20], b[5, 1], b[31] = -1e9, 1e4, -F32, -float("inf")
+    q, k, v, dout = (to_device(x, "f32") for x in features(n, 2, 16, "f32", 9))
+
+    def step(k, v, packed, **kw):
+        out, lse = gnn.transformer_rel_forward(g, rel, q, k, v, b, **kw)
+        return ((out, lse) + gnn.transformer_rel_backward(g, rel, q, k, v, b, lse, dout, **kw)
+                + gnn.transformer_backward8(g, *packed, dout, rel=rel, bias=b, **kw))
+
+    packed = gnn.pack8(q, k, v)
+    first = step(k, v, packed)
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    runs = [step(k, v, packed), step(k, v, packed, stream=side)]
+    torch.cuda.synchronize()
+    cg = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(cg):
+        runs.append(step(k, v, packed))
+    cg.replay()
+    cg.replay()
+    bad_k, bad_v = k.clone(), v.clone()
+    bad_k[17], bad_v[17, :, ::2], bad_v[17, :, 1::2] = float("nan"), -float("inf"), float("nan")
+    runs.append(step(bad_k, bad_v, gnn.pack8(q, bad_k, bad_v)))
+    torch.cuda.synchronize()
+    own = np.flatnonzero(dst == 17)                          # its own row reads only others' keys
+    assert len(own) and (b[rel.arrays()[0][torch.from_numpy(own).cuda()].long()] > -1e38).any()
+    for r in runs:
+        for a, c in zip(first, r):
+            assert torch.isfinite(a).logical_or(torch.isneginf(a)).all() and torch.equal(a, c)
+
+
+@pytest.mark.gpu
 @pytest.mark.parametrize("order", [1, -1], ids=["last", "first"])
 @pytest.mark.parametrize("value", [-F32, -1e9, -1e4, 2.4e38], ids=lambda v: f"{v:.3g}")
 def test_a_long_row_that_changes_over(value, order):
