@@ -181,7 +181,8 @@ struct SoftRef<Bias::kAny> {
 // graph of 6M edges, against 2e-7 to 3e-7).  So an entry is a float2, the sum and
 // what its additions left over (Kahan), as long as two blocks stay on an SM: 839 us
 // instead of 831 in pass 2 of that graph, 920 instead of 904 from checkpoints.
-// Wider tables, of many buckets and heads as narrow as a lane, hold sums alone.
+// Wider tables, of many buckets and heads as narrow as a lane, hold sums alone (6M edges:
+// 6e-7 of the gradient for H8 D16 bf16 with 128 buckets, 1.5e-6 for H32 D8 with 64).
 constexpr size_t kPairBytes = 72 * 1024;  // and up to 32 KB of biases and own rows a block
 
 __host__ __device__ inline size_t grad_columns(const Shape& s, int buckets) {
