@@ -517,8 +517,8 @@ int tpr_log2(int rv) {
   return l;
 }
 
-// Blocks of the backward pass: what fits on 152 SMs, at least 16 rows a slot
-// before its sums are folded.
+// Blocks of the backward pass: what fits on a GB300's 152 SMs, at least 16 rows a slot
+// before its sums are folded.  (A constant, as the workspace query asks no device.)
 int bwd_blocks(int64_t n, int rv) {
   const int cap = 152 * kBwdPerSm;
   const int64_t slots = kThreads >> tpr_log2(rv);

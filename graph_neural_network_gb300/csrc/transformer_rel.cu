@@ -51,10 +51,11 @@ struct RelArgs {
 
 // Edges in flight per lane, for lane vectors of 32 bytes (twice as many of 16): as
 // many as the registers of 16 warps an SM hold beside the accumulators, of which
-// float32 lanes have half as many.  Training step on the 300k-node bfloat16 graph:
-// 2,044 us; forward with three edges 2,083, with five 2,060; pass 1 with two 2,162,
-// with four 2,216; pass 2 with three 2,088.  On the 100k-node float32 graph: 499 us;
-// pass 2 with two 524, with four 642; pass 1 with two 562, with five 518.
+// float32 lanes have half as many.  Training step on the 300k-node bfloat16 graph when
+// these were compared (2,026 us now): 2,044 us; forward with three edges 2,083, with five
+// 2,060; pass 1 with two 2,162, with four 2,216; pass 2 with three 2,088.  On the 100k-node
+// float32 graph: 499 us; pass 2 with two 524, with four 642; pass 1 with two 562, with
+// five 518.
 // Beside large biases, whose form needs more registers, as many or fewer: with more the
 // compiler also schedules the ordinary form of the same kernel worse (forward 593 instead
 // of 514 us; pass 2 with 16-byte vectors, 200k nodes H8 D4 float32, 235 instead of 221).
