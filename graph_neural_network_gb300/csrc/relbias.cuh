@@ -11,7 +11,7 @@ namespace gnn {
 enum class Bias {
   kNone,     // dot products alone
   kOrdinary, // every finite entry within +-kOrdinaryBias: dot + bias in one float
-  kAny       // a pair of both (PairRef)
+  kAny       // a pair of both (SoftRef<Bias::kAny>)
 };
 constexpr float kOrdinaryBias = 16.f;
 

@@ -402,15 +402,15 @@ __global__ void __launch_bounds__(kThreads, kPerSm) t8_dst(const __grid_constant
   __shared__ __align__(16) unsigned char held[kWarps * HeldT<T, kE>::kBytes];
   const auto pass = [&](auto p, float* table) {
     p.g.place(held + (threadIdx.x >> 5) * HeldT<T, kE>::kBytes, L.lane);
-    p.sb = table + L.k[0];
+    p.sb = table;
     walk(p, A.walk, A.dir, A.s, L);
   };
   if constexpr (kRel) {
     float* table = reinterpret_cast<float*>(smem);
     if (stage_bias(A.bias, A.buckets * A.s.H, table))
-      pass(DstPass<T, kE, Bias::kAny>(A, L), table);
+      pass(DstPass<T, kE, Bias::kAny>(A, L), table + L.k[0]);
     else
-      pass(DstPass<T, kE, Bias::kOrdinary>(A, L), table);
+      pass(DstPass<T, kE, Bias::kOrdinary>(A, L), table + L.k[0]);
   } else {
     pass(DstPass<T, kE, Bias::kNone>(A, L), nullptr);
   }
@@ -423,7 +423,7 @@ __global__ void __launch_bounds__(kThreads, kPerSm) t8_src(const __grid_constant
   __shared__ __align__(16) unsigned char held[kWarps * HeldT<T, kE>::kBytes];
   const auto pass = [&](auto p, float* table, float* column) {
     p.v.place(held + (threadIdx.x >> 5) * HeldT<T, kE>::kBytes, L.lane);
-    p.sb = table + L.k[0];
+    p.sb = table;
     p.hist = column;
     walk(p, A.walk, A.dir, A.s, L);
   };
@@ -432,9 +432,9 @@ __global__ void __launch_bounds__(kThreads, kPerSm) t8_src(const __grid_constant
     float* column = clear_grad_tables(tables, A.s, L, A.buckets);
     float* table = reinterpret_cast<float*>(smem + grad_tables_bytes(A.s, A.buckets));
     if (stage_bias(A.bias, A.buckets * A.s.H, table))
-      pass(SrcPass<T, kE, Bias::kAny, kPair>(A, L), table, column);
+      pass(SrcPass<T, kE, Bias::kAny, kPair>(A, L), table + L.k[0], column);
     else
-      pass(SrcPass<T, kE, Bias::kOrdinary, kPair>(A, L), table, column);
+      pass(SrcPass<T, kE, Bias::kOrdinary, kPair>(A, L), table + L.k[0], column);
     let_next_start();
     fold_grad_tables<kPair>(tables, A.s, L, A.buckets, A.db_part);
   } else {

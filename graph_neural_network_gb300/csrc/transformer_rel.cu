@@ -11,11 +11,11 @@
 // only when a score passes it.  Backward pass 1 (CSR): Delta, P = sum alpha da
 // key_j, Q = sum alpha key_j, dq_i = scale (P - Delta Q), record {lse, Delta}.  (Beside
 // large biases lse, one number, has lost what the weights need: there the pass is an online
-// softmax of its own and records the sum and the reference apart.)  Pass 2 (CSC): dkey, dval, and dbias[b][k] = sum of de_ij over the edges of bucket
-// b, de_ij = alpha_ij (da_ij - Delta_i) being known per edge there: each lane that
-// leads a head adds into a column of its own of its warp's table in shared
-// memory (no atomics, no bank conflicts), the block adds its tables in a fixed
-// order in float64, and dbias_sum adds the blocks.
+// softmax of its own and records the sum and the reference apart.)  Pass 2 (CSC): dkey,
+// dval, and dbias[b][k] = sum of de_ij over the edges of bucket b, de_ij = alpha_ij
+// (da_ij - Delta_i) being known per edge there: each lane that leads a head adds into a
+// column of its own of its warp's table in shared memory (no atomics, no bank conflicts),
+// the block adds its tables in a fixed order in float64, and dbias_sum adds the blocks.
 //
 // Bound: latency of the gathers, 2 rows an edge and pass (edgewalk.cuh, which also
 // says how the work is cut and what it measured).  A lane holds 32 bytes of a row

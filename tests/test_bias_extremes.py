@@ -86,7 +86,8 @@ def reference(rp, ci, q, k, v, dout, scale, bias, bucket):
         for name, idx, row, m, nd in (("dq", I, kh[J], I, deg), ("dkey", J, qh[I], J, odeg)):
             r[name] = (scale * add(idx, de[:, None] * row), sc * add(
                 idx, (de_e + (nd[m] + 6) * U * de_m)[:, None] * np.abs(row)))
-        r["dval"] = (add(J, A * gh[I]), add(J, (W + (odeg[J] + 4)[:, None] * U) * A * np.abs(gh[I])))
+        r["dval"] = (add(J, A * gh[I]),
+                     add(J, (W + (odeg[J] + 4)[:, None] * U) * A * np.abs(gh[I])))
         nb = len(bias)
         count = np.bincount(bucket[keep], minlength=nb)[bucket[keep]]
         db, db_e = np.zeros(nb), np.zeros(nb)

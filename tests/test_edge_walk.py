@@ -239,7 +239,7 @@ def test_cuts_at_long_segments(reverse):
     at = rng.choice(n, 600, replace=False)
     near, seg = rng.integers(-2, 3, 500), 0
     degs[at[500:]] = rng.integers(600, 5000, 100)
-    for _ in range(4):                                       # (the degrees move the segment a little)
+    for _ in range(4):                                       # (degrees move the segment)
         seg = -(-(int(degs.sum()) + 3 * n) // workers)
         degs[at[:500]] = seg // 16 - 3 + near                # 0: the longest whole node
     assert seg == -(-(int(degs.sum()) + 3 * n) // workers) and seg > 1040
