@@ -1,0 +1,480 @@
+"""Operators round the projections of a graph-transformer layer: rotary positions of
+queries and keys, the sum with the residual and its root-mean-square norm in 8 bits, and
+the order of tokens by expert with the rows' way there and back.
+
+``listed()`` and ``draw()`` give cases, ``prepare()`` their inputs, ``run()``
+one pass: the framework's kernels where ``own`` is set, plain torch operations
+otherwise.  ``exact()`` is the definition in 64 bits.
+"""
+import math
+
+import torch
+
+own = False
+
+DEV = "cuda"
+DTYPES = {"f32": torch.float32, "bf16": torch.bfloat16}
+EPS = 1e-6
+TOP = {"int8": 127.0, "e4m3": 448.0}
+
+
+# ---------------------------------------------------------------------------
+# cases
+# ---------------------------------------------------------------------------
+
+def listed():
+    def rope(name, op, n, Hq, Hk, D, rot, dtype, layout, scaling, reach, fused):
+        return dict(name=name, op=op, n=n, Hq=Hq, Hk=Hk, D=D, rot=rot, dtype=dtype, layout=layout,
+                    scaling=scaling, factor=1.0 if scaling == "none" else 8.0, reach=reach,
+                    fused=fused)
+
+    def norm(name, op, n, F, dtype, fmt="int8", group=0, weight=True):
+        return dict(name=name, op=op, n=n, F=F, dtype=dtype, fmt=fmt, group=group or F,
+                    weight=weight)
+
+    def expert(name, op, n, F, E, K, dtype, align, drop):
+        return dict(name=name, op=op, n=n, F=F, E=E, K=K, dtype=dtype, align=align, drop=drop)
+
+    return [
+        # one small molecule- or sentence-sized batch: latency counts
+        rope("rope fwd 512 f32", "rope_fwd", 512, 1, 1, 16, 16, "f32", "half", "none", 512, False),
+        # single tokens of 64 requests, far out in long contexts, fewer key heads than query heads
+        rope("rope fwd 64 bf16", "rope_fwd", 64, 32, 8, 128, 128, "bf16", "half", "yarn", 1_000_000,
+             False),
+        # a large batch, q and key read out of one fused projection, half of each head rotated
+        rope("rope fwd 300k bf16", "rope_fwd", 300_000, 4, 4, 64, 32, "bf16", "interleaved", "ntk",
+             100_000, True),
+        # the gradients of a million nodes' narrow heads
+        rope("rope bwd 1m bf16", "rope_bwd", 1_000_003, 8, 8, 16, 16, "bf16", "half", "linear",
+             30_000, False),
+        # single tokens of 64 requests, wide rows, before an 8-bit projection
+        norm("norm8 fwd 64 bf16", "norm8_fwd", 64, 4096, "bf16", "e4m3"),
+        # a graph's float32 rows, a scale for each head of 32
+        norm("norm8 fwd 100k f32", "norm8_fwd", 100_003, 128, "f32", "int8", 32),
+        # a training batch of wide rows with a scale for each block of 128
+        norm("norm8 fwd 64k bf16", "norm8_fwd", 65_536, 4096, "bf16", "int8", 128),
+        # its gradients, rows of no round width
+        norm("norm8 bwd 30k bf16", "norm8_bwd", 30_001, 4104, "bf16"),
+        # single tokens of 64 requests and many experts
+        expert("experts fwd 64 bf16", "experts_fwd", 64, 2048, 64, 8, "bf16", 1, 0.0),
+        # narrow rows of a large graph, segments padded for tiled products, a tenth of the
+        # choices dropped
+        expert("experts fwd 200k f32", "experts_fwd", 200_003, 64, 16, 2, "f32", 128, 0.1),
+        # the gradients of a middling batch in float32
+        expert("experts bwd 20k f32", "experts_bwd", 20_011, 512, 8, 2, "f32", 1, 0.0),
+        # the gradients of a training batch
+        expert("experts bwd 64k bf16", "experts_bwd", 65_536, 2048, 64, 4, "bf16", 128, 0.0),
+    ]
+
+
+def _log_int(rng, lo, hi):
+    return int(round(math.exp(rng.uniform(math.log(lo), math.log(max(lo, hi))))))
+
+
+def draw(rng):
+    op = rng.choice(["rope_fwd", "rope_bwd", "norm8_fwd", "norm8_bwd", "experts_fwd",
+                     "experts_bwd"])
+    dtype = rng.choice(["f32", "bf16"])
+    step = 4 if dtype == "f32" else 8
+    if op.startswith("rope"):
+        D = rng.choice([16, 32, 64, 80, 96, 128, 256])
+        rot = rng.choice([D, D, D // 2, 2 * rng.randint(1, D // 2)])
+        Hk = rng.randint(1, max(1, 512 // D))
+        fused = rng.random() < 0.4
+        Hq = Hk if fused else Hk * rng.randint(1, 4)
+        scaling = rng.choice(["none", "linear", "ntk", "yarn"])
+        if rot < 4:
+            scaling = "none"
+        return dict(op=op, n=_log_int(rng, 1, min(1_000_000, 64_000_000 // ((Hq + Hk) * D))), Hq=Hq,
+                    Hk=Hk, D=D, rot=rot, dtype=dtype, layout=rng.choice(["half", "interleaved"]),
+                    scaling=scaling, factor=1.0 if scaling == "none" else rng.uniform(1.5, 40.0),
+                    reach=_log_int(rng, 16, 2 ** 31 - 1), fused=fused)
+    if op.startswith("norm8"):
+        # rows of up to 16 KB: of any width with one scale, or of whole groups
+        top = 16384 // (16 // step)
+        if rng.random() < 0.5:
+            group = F = step * _log_int(rng, 1, top // step)
+        else:
+            group = step * rng.choice([1, 2, 4, 8, 16, 32])
+            F = group * _log_int(rng, 1, top // group)
+        return dict(op=op, n=_log_int(rng, 1, min(1_000_000, 200_000_000 // F)), F=F, dtype=dtype,
+                    fmt=rng.choice(["int8", "e4m3"]), group=group, weight=rng.random() < 0.8)
+    E = _log_int(rng, 1, 256)
+    K = rng.randint(1, min(E, 8))
+    F = step * _log_int(rng, 1, 4096 // step)
+    return dict(op=op, n=_log_int(rng, 1, min(300_000, 200_000_000 // (F * K))), F=F, E=E, K=K,
+                dtype=dtype, align=rng.choice([1, 16, 128]),
+                drop=rng.choice([0.0, 0.0, 0.1, 0.9]))
+
+
+def _rows(case):
+    """Rows of the tokens in the experts' order: every pair, and the padding at most."""
+    pairs = case["n"] * case["K"]
+    return (pairs + min(case["E"], pairs) * (case["align"] - 1)) // case["align"] * case["align"]
+
+
+# ---------------------------------------------------------------------------
+# inputs
+# ---------------------------------------------------------------------------
+
+LENGTH = 4096  # of the sequences that the frequencies were trained on
+
+
+def _frequencies(case):
+    """Radians a position of each rotated pair, and the factor on the rotated vectors."""
+    rot, factor, base = case["rot"], case["factor"], 10000.0
+    if case["scaling"] == "ntk":
+        base *= factor ** (rot / (rot - 2))
+    f = [base ** (-2 * i / rot) for i in range(rot // 2)]
+    if case["scaling"] == "linear":
+        f = [x / factor for x in f]
+    if case["scaling"] != "yarn":
+        return f, 1.0
+    # pairs that turn less than once in LENGTH positions are slowed by the factor, those that
+    # turn more than 32 times are kept, in between a line by the pair's index
+    def index(turns):
+        return rot * math.log(LENGTH / (turns * 2 * math.pi)) / (2 * math.log(base))
+
+    low = max(math.floor(index(32.0)), 0)
+    high = min(math.ceil(index(1.0)), rot // 2 - 1)
+    high = high if high > low else low + 0.001
+    slow = [min(max((i - low) / (high - low), 0.0), 1.0) for i in range(rot // 2)]
+    return [x / factor * s + x * (1 - s) for x, s in zip(f, slow)], 0.1 * math.log(factor) + 1.0
+
+
+def _order(ids, E, align):
+    """The experts' order of the pairs of ids [n, K]: each pair's row (-1 where dropped), the
+    experts' numbers of pairs and the first rows of their segments."""
+    flat = ids.reshape(-1)
+    key = torch.where((flat >= 0) & (flat < E), flat, E)
+    _, pairs = torch.sort(key, stable=True)
+    counts = torch.bincount(key, minlength=E + 1)
+    starts = torch.cumsum(counts, 0) - counts  # in the order without padding
+    padded = (counts[:E] + align - 1) // align * align
+    offsets = torch.zeros(E + 1, dtype=torch.int64, device=DEV)
+    offsets[1:] = torch.cumsum(padded, 0)
+    rank = torch.empty_like(pairs)
+    rank[pairs] = torch.arange(pairs.numel(), device=DEV)
+    slots = torch.where(key < E, offsets[key] + rank - starts[key], -1)
+    return slots.reshape(ids.shape).int(), counts[:E].int(), offsets.int()
+
+
+def prepare(case, seed):
+    gen = torch.Generator(device=DEV)
+    gen.manual_seed(seed)
+    dt = DTYPES[case["dtype"]]
+    n, op = case["n"], case["op"]
+
+    def normal(*shape, std=1.0, dtype=dt):
+        return (torch.randn(*shape, generator=gen, device=DEV) * std).to(dtype)
+
+    st = {"case": case, "dt": dt}
+    if op.startswith("rope"):
+        Hq, Hk, D = case["Hq"], case["Hk"], case["D"]
+        if case["fused"]:  # of a projection [n, (q, key, val), H, D]
+            qkv = normal(n, 3, Hq, D)
+            st["q"], st["key"] = qkv[:, 0], qkv[:, 1]
+        else:
+            st["q"], st["key"] = normal(n, Hq, D), normal(n, Hk, D)
+        st["pos"] = torch.randint(0, case["reach"], (n,), generator=gen, device=DEV).int()
+        freqs, st["amplitude"] = _frequencies(case)
+        st["freqs"] = torch.tensor(freqs, dtype=torch.float64, device=DEV)
+        if own:
+            import graph_neural_network_gb300 as gnn
+            st["rope"] = gnn.Rope(case["rot"], case["layout"], scaling=None
+                                  if case["scaling"] == "none" else case["scaling"],
+                                  factor=case["factor"], length=LENGTH)
+        return st
+    F = case["F"]
+    if op.startswith("norm8"):
+        st["w"] = 1 + normal(F, std=0.1, dtype=torch.float32) if case["weight"] else None
+        if op == "norm8_fwd":
+            st["x"], st["o"] = normal(n, F, std=2.0), normal(n, F)
+        else:
+            st["y"], st["dy"], st["dz"] = normal(n, F, std=2.0), normal(n, F), normal(n, F)
+        return st
+    # a router's choices: some experts are liked better than others
+    E, K = case["E"], case["K"]
+    liked = torch.randn(E, generator=gen, device=DEV)
+    logits, ids = torch.topk(torch.randn(n, E, generator=gen, device=DEV) + liked, K, dim=1)
+    st["weights"] = torch.softmax(logits, 1)
+    if case["drop"]:
+        ids = torch.where(torch.rand(n, K, generator=gen, device=DEV) < case["drop"], -1, ids)
+    st["ids"] = ids.contiguous()
+    m = _rows(case)
+    st["ys"] = normal(m, F)  # what the experts made of their rows
+    if op == "experts_fwd":
+        st["x"], st["residual"] = normal(n, F), normal(n, F)
+        return st
+    st["dy"], st["dxs"] = normal(n, F), normal(m, F)
+    st["slots"] = _order(st["ids"], E, case["align"])[0]
+    if own:
+        import graph_neural_network_gb300 as gnn
+        st["plan"] = gnn.Experts(st["ids"], E, align=case["align"])
+    return st
+
+
+# ---------------------------------------------------------------------------
+# one pass
+# ---------------------------------------------------------------------------
+
+def run(st):
+    if own:
+        return _own(st)
+    return {"rope_fwd": _plain_rope, "rope_bwd": _plain_rope, "norm8_fwd": _plain_norm8_fwd,
+            "norm8_bwd": _plain_norm8_bwd, "experts_fwd": _plain_experts_fwd,
+            "experts_bwd": _plain_experts_bwd}[st["case"]["op"]](st)
+
+
+def _own(st):
+    import graph_neural_network_gb300 as gnn
+    case, op = st["case"], st["case"]["op"]
+    if op == "rope_fwd":
+        return gnn.rope_forward(st["rope"], st["pos"], st["q"], st["key"])
+    if op == "rope_bwd":
+        return gnn.rope_backward(st["rope"], st["pos"], st["q"], st["key"])
+    if op == "norm8_fwd":
+        # the values are read back, as for a weight's gradient
+        y, z8 = gnn.add_norm8_forward(st["x"], st["o"], st["w"], fmt=case["fmt"],
+                                      group=case["group"], eps=EPS)
+        return y, gnn.unpack8(z8, st["dt"]), z8.scale
+    if op == "norm8_bwd":
+        dx, dw = gnn.add_norm8_backward(st["y"], st["dy"], st["dz"], st["w"], eps=EPS)
+        return {"dx": dx, "dw": dw}
+    if op == "experts_fwd":
+        plan = gnn.Experts(st["ids"], case["E"], align=case["align"])
+        xs = gnn.expert_dispatch_forward(plan, st["x"])
+        y = gnn.expert_combine_forward(plan, st["ys"], st["weights"], st["residual"])
+        return plan.slots, plan.counts, plan.offsets, xs, y
+    dys, dweights = gnn.expert_combine_backward(st["plan"], st["dy"], st["ys"], st["weights"])
+    return dys, dweights, gnn.expert_dispatch_backward(st["plan"], st["dxs"])
+
+
+def _pairs_of(case, x):
+    """The two halves of the rotated part's pairs."""
+    r = case["rot"]
+    if case["layout"] == "half":
+        return x[..., :r // 2], x[..., r // 2:r]
+    return x[..., 0:r:2], x[..., 1:r:2]
+
+
+def _plain_rope(st):
+    case = st["case"]
+    # far positions turn many times: their angles in 64 bits
+    angle = st["pos"].double()[:, None] * st["freqs"]
+    cos = (torch.cos(angle) * st["amplitude"]).float()[:, None]
+    sin = (torch.sin(angle) * st["amplitude"]).float()[:, None]
+    if case["op"] == "rope_bwd":
+        sin = -sin
+
+    def turn(x):
+        x = x.float()
+        a, b = _pairs_of(case, x)
+        u, v = a * cos - b * sin, a * sin + b * cos
+        first = (torch.cat([u, v], -1) if case["layout"] == "half" else
+                 torch.stack([u, v], -1).flatten(-2))
+        return torch.cat([first, x[..., case["rot"]:]], -1).to(st["dt"])
+
+    return turn(st["q"]), turn(st["key"])
+
+
+def _to_eight(fmt, q):
+    """q (64 bits) rounded to the nearest value of eight bits, ties to even."""
+    if fmt == "int8":
+        return torch.round(q)
+    _, e = torch.frexp(q)
+    step = torch.ldexp(torch.ones_like(q), (e - 1).clamp(min=-6) - 3)
+    return (torch.round(q / step) * step).clamp(-448.0, 448.0)
+
+
+def _plain_norm8_fwd(st):
+    case = st["case"]
+    n, F, group, top = case["n"], case["F"], case["group"], TOP[case["fmt"]]
+    y = st["x"].float() + st["o"].float()
+    t = y if st["w"] is None else y * st["w"]
+    rstd = torch.rsqrt((y * y).mean(-1, keepdim=True) + EPS)
+    t = t.reshape(n, F // group, group)
+    # in 64 bits: a quotient next to a border would round the other way
+    s = (t.abs().amax(-1).double() / top).float().clamp(min=2.0 ** -126)
+    z8 = _to_eight(case["fmt"], t.double() / s.double()[..., None]).float()
+    scale = s * rstd
+    return y.to(st["dt"]), (z8 * scale[..., None]).to(st["dt"]), scale
+
+
+def _plain_norm8_bwd(st):
+    y, dz = st["y"].float(), st["dz"].float()
+    rstd = torch.rsqrt((y * y).mean(-1, keepdim=True) + EPS)
+    hat = y * rstd
+    g = dz if st["w"] is None else dz * st["w"]
+    dx = st["dy"].float() + rstd * (g - hat * (g * hat).mean(-1, keepdim=True))
+    if st["w"] is None:
+        return {"dx": dx.to(st["dt"]), "dw": None}
+    # over all rows, in 64 bits
+    return {"dx": dx.to(st["dt"]), "dw": (dz * hat).sum(0, dtype=torch.float64).float()}
+
+
+def _to_rows(slots, x, m):
+    """x [n, K, F] laid into the rows of slots [n, K], the others zero."""
+    rows = torch.zeros(m + 1, x.shape[-1], dtype=x.dtype, device=DEV)
+    at = torch.where(slots >= 0, slots, m).reshape(-1).long()  # the last row takes the dropped
+    return rows.index_copy_(0, at, x.reshape(-1, x.shape[-1]))[:m]
+
+
+def _from_rows(slots, rows):
+    """The rows of slots [n, K] in 32 bits, zero where dropped."""
+    got = rows[slots.clamp(min=0).long()].float()
+    return torch.where((slots >= 0)[..., None], got, 0.0)
+
+
+def _plain_experts_fwd(st):
+    case = st["case"]
+    slots, counts, offsets = _order(st["ids"], case["E"], case["align"])
+    xs = _to_rows(slots, st["x"][:, None].expand(-1, case["K"], -1), _rows(case))
+    got = _from_rows(slots, st["ys"])
+    y = st["residual"].float() + (got * st["weights"][..., None]).sum(1)
+    return slots, counts, offsets, xs, y.to(st["dt"])
+
+
+def _plain_experts_bwd(st):
+    case, slots = st["case"], st["slots"]
+    dy = st["dy"].float()[:, None]
+    dys = _to_rows(slots, (dy * st["weights"][..., None]).to(st["dt"]), _rows(case))
+    dweights = (dy * _from_rows(slots, st["ys"])).sum(-1)
+    dx = _from_rows(slots, st["dxs"]).sum(1).to(st["dt"])
+    return dys, dweights, dx
+
+
+# ---------------------------------------------------------------------------
+# work and the definition in 64 bits
+# ---------------------------------------------------------------------------
+
+def work(case):
+    s = 4 if case["dtype"] == "f32" else 2
+    n, op = case["n"], case["op"]
+    if op.startswith("rope"):
+        heads = case["Hq"] + case["Hk"]
+        return {"bytes": 2 * n * heads * case["D"] * s + 4 * n, "flops": 3 * n * heads * case["rot"]}
+    F = case["F"]
+    if op == "norm8_fwd":
+        # x, o; y, the values and scales; these read back, and z
+        return {"bytes": n * F * (4 * s + 2) + 8 * n * (F // case["group"]) + 4 * F,
+                "flops": 10 * n * F}
+    if op == "norm8_bwd":  # y, dy, dz, w; dx, dw
+        return {"bytes": 4 * n * F * s + 8 * F, "flops": 14 * n * F}
+    m, kept = _rows(case), n * case["K"] * (1 - case["drop"])
+    small = 4 * n * case["K"]
+    if op == "experts_fwd":
+        # ids, x, ys, weights, the residual; rows, slots, xs and y
+        return {"bytes": F * s * (3 * n + m + kept) + 4 * small, "flops": 2 * kept * F}
+    # dy, ys, weights, slots, dxs; dys, dweights, dx
+    return {"bytes": F * s * (2 * n + m + 2 * kept) + 3 * small, "flops": 4 * kept * F}
+
+
+def exact(case, seed):
+    st = prepare(case, seed)
+    op = case["op"]
+    if op.startswith("rope"):
+        return _exact_rope(st)
+    if op.startswith("norm8"):
+        return _exact_norm8(st)
+    return _exact_experts(st)
+
+
+def _exact_rope(st):
+    """A pair is a complex number, and a position a power of its frequency's phase."""
+    case = st["case"]
+    phase = torch.polar(torch.full_like(st["freqs"], st["amplitude"]).expand(case["n"], -1),
+                        torch.outer(st["pos"].double(), st["freqs"])).unsqueeze(1)
+    if case["op"] == "rope_bwd":
+        phase = phase.conj()
+    out = []
+    for x in (st["q"], st["key"]):
+        x = x.double().clone()
+        a, b = _pairs_of(case, x)
+        z = torch.complex(a.contiguous(), b.contiguous()) * phase
+        a.copy_(z.real)
+        b.copy_(z.imag)
+        out.append(x)
+    return tuple(out)
+
+
+def _exact_norm8(st):
+    case = st["case"]
+    F, group, top = case["F"], case["group"], TOP[case["fmt"]]
+    parts, dw = [], 0
+    size = max(1, (1 << 26) // F)
+    for r in range(0, case["n"], size):
+        at = slice(r, r + size)
+        if case["op"] == "norm8_bwd":
+            y = st["y"][at].double().requires_grad_()
+            leaves = [y]
+            z = y / (y.pow(2).sum(-1, keepdim=True) / F + EPS).sqrt()
+            if st["w"] is not None:
+                w = st["w"].double().requires_grad_()
+                leaves.append(w)
+                z = z * w
+            got = torch.autograd.grad(z, leaves, st["dz"][at].double())
+            parts.append((got[0] + st["dy"][at].double(),))
+            dw = dw + got[1] if st["w"] is not None else None
+            continue
+        y = st["x"][at].double().add(st["o"][at])
+        rstd = 1 / (y.pow(2).sum(-1, keepdim=True) / F + EPS).sqrt()
+        # what is laid into eight bits are the sum and its product with the weight as float32,
+        # over a float32 scale: these roundings belong to the definition
+        t = y.float().double()
+        t = t if st["w"] is None else (t * st["w"].double()).float().double()
+        t = t.unflatten(-1, (-1, group))
+        scale = (torch.linalg.vector_norm(t, float("inf"), -1) / top).float().double()
+        scale = scale.clamp(min=2.0 ** -126)
+        q = t / scale.unsqueeze(-1)
+        if case["fmt"] == "int8":
+            down = torch.floor(q)
+            up = (q - down > 0.5) | ((q - down == 0.5) & (down % 2 != 0))
+            v = down + up
+        else:  # the nearest of all values of the type, the one of the even pattern of two
+            code = torch.arange(127, device=DEV)
+            table = code.to(torch.uint8).view(torch.float8_e4m3fn).double()
+            lo = torch.searchsorted(table, q.abs().contiguous(), right=True).clamp(max=126) - 1
+            below, above = q.abs() - table[lo], table[lo + 1] - q.abs()
+            lo = lo + ((above < below) | ((above == below) & (lo % 2 != 0)))
+            v = torch.copysign(table[lo], q)
+        scale = scale * rstd
+        parts.append((y, v * scale.unsqueeze(-1), scale))
+    whole = [torch.cat(p) for p in zip(*parts)]
+    return {"dx": whole[0], "dw": dw} if case["op"] == "norm8_bwd" else tuple(whole)
+
+
+def _exact_experts(st):
+    """Expert by expert: its pairs in the order of their numbers."""
+    case, ids = st["case"], st["ids"]
+    n, K, E, F = case["n"], case["K"], case["E"], case["F"]
+    m = _rows(case)
+    w = st["weights"].double()
+    slots = torch.full((n * K,), -1, dtype=torch.int64, device=DEV)
+    counts, offsets = [], [0]
+    for e in range(E):
+        mine = torch.nonzero(ids.reshape(-1) == e).squeeze(1)
+        slots[mine] = offsets[-1] + torch.arange(len(mine), device=DEV)
+        counts.append(len(mine))
+        offsets.append(offsets[-1] + -(-len(mine) // case["align"]) * case["align"])
+    kept = torch.nonzero(slots >= 0).squeeze(1)
+    row, token = slots[kept], kept // K
+    if case["op"] == "experts_fwd":
+        xs = torch.zeros(m, F, dtype=torch.float64, device=DEV)
+        xs[row] = st["x"][token].double()
+        y = st["residual"].double()
+        for k in range(K):
+            of = token[kept % K == k]
+            y[of] += w[of, k, None] * st["ys"][row[kept % K == k]].double()
+        return (slots.reshape(n, K), torch.tensor(counts, device=DEV),
+                torch.tensor(offsets, device=DEV), xs, y)
+    dys = torch.zeros(m, F, dtype=torch.float64, device=DEV)
+    dw = torch.zeros(n, K, dtype=torch.float64, device=DEV)
+    dx = torch.zeros(n, F, dtype=torch.float64, device=DEV)
+    for k in range(K):
+        of, at = token[kept % K == k], row[kept % K == k]
+        dy = st["dy"][of].double()
+        dys[at] = w[of, k, None] * dy
+        dw[of, k] = torch.einsum("tf,tf->t", dy, st["ys"][at].double())
+        dx[of] += st["dxs"][at].double()
+    return dys, dw, dx
