@@ -42,6 +42,12 @@ the norms, gate and residual scale between two blocks of a layer:
     y, z = norm_residual_forward(x, o, gate, w_post, scale=scale, w_pre=w_pre)
     grads = norm_residual_backward(y, o, dy, dz, gate, w_post, scale=scale, w_pre=w_pre)
 
+rotary positions of q and key (views of a fused projection [N, 3, H, D] as they are):
+
+    rope = Rope(D, "half", scaling="yarn", factor=8, length=4096)     # once
+    q, key = rope_forward(rope, pos, q, key)           # pos [N] int32
+    dq, dkey = rope_backward(rope, pos, dq, dkey)
+
 ``transformer_layer`` runs a layer between its projections with autograd: the
 attention (bias and 8-bit checkpoints if asked for), the output projection that
 the caller gives, and the norms, gate and residual.
@@ -74,7 +80,8 @@ __all__ = ["Graph", "gat_forward", "gat_backward", "GATAggregate", "GnnError", "
            "transformer_backward", "TransformerAggregate", "RelPos", "transformer_rel_forward",
            "transformer_rel_backward", "TransformerRelAggregate", "norm_residual_forward",
            "norm_residual_backward", "NormResidual", "Packed8", "pack8", "unpack8",
-           "transformer_backward8", "TransformerCheckpoint8", "transformer_layer"]
+           "transformer_backward8", "TransformerCheckpoint8", "transformer_layer", "Rope",
+           "rope_forward", "rope_backward", "RotaryPositions"]
 
 
 def _ptr(t):
@@ -975,11 +982,134 @@ class NormResidual(torch.autograd.Function):
                   for k, t in zip(_NORM_PARAMS, params)), None, None)
 
 
+class Rope:
+    """Frequencies of rotary positions: the first dim elements of a head vector are dim/2
+    pairs, of elements i and i + dim/2 (layout "half") or 2 i and 2 i + 1
+    ("interleaved"), and pair i turns by freqs[i] radians a position.
+
+    freqs are base^(-2 i / dim), or for contexts `factor` times as long: all divided
+    by factor (scaling "linear"), of the base raised by factor^(dim / (dim - 2))
+    ("ntk"), or divided for the pairs that turn less than slow times in `length`
+    positions, kept for those that turn more than fast times, with a line by the
+    pair's index between ("yarn").  amplitude multiplies the rotated elements; its
+    default is 0.1 ln(factor) + 1 for "yarn" and 1 otherwise.  freqs: dim/2 numbers
+    instead of a rule.  Host data only: it serves every device and stream."""
+
+    def __init__(self, dim: int, layout: str = "half", base: float = 10000.0,
+                 scaling: str | None = None, factor: float = 1.0, length: float | None = None,
+                 fast: float = 32.0, slow: float = 1.0, freqs=None,
+                 amplitude: float | None = None):
+        lib = _native.load()
+        if layout not in _native.ROPE_LAYOUTS:
+            raise ValueError(f"layout must be one of {sorted(_native.ROPE_LAYOUTS)}")
+        if scaling not in _native.ROPE_SCALINGS:
+            raise ValueError("scaling must be None, 'linear', 'ntk' or 'yarn'")
+        if not isinstance(dim, int) or not 2 <= dim <= _native.ROPE_MAX_DIM or dim % 2:
+            raise ValueError(f"dim must be even, 2 to {_native.ROPE_MAX_DIM}")
+        table = (ctypes.c_double * (dim // 2))()
+        rule = ctypes.c_float(1.0)
+        if freqs is not None:
+            if scaling is not None:
+                raise ValueError("freqs stand instead of a rule: scaling must be None")
+            freqs = [float(f) for f in freqs]
+            if len(freqs) != dim // 2:
+                raise ValueError(f"freqs must be {dim // 2} numbers")
+            table[:] = freqs
+        else:
+            if scaling is None and factor != 1.0:
+                raise ValueError("a factor needs a scaling")
+            if scaling == "yarn" and length is None:
+                raise ValueError("scaling 'yarn' needs the length that factor stretches")
+            _native.check(lib.gnn_rope_frequencies(
+                dim, base, _native.ROPE_SCALINGS[scaling], factor,
+                0.0 if length is None else length, fast, slow, table, ctypes.byref(rule)),
+                "gnn_rope_frequencies")
+        self.dim, self.layout = dim, layout
+        self.freqs = list(table)
+        self.amplitude = rule.value if amplitude is None else float(amplitude)
+        self._c = _native.Rope()
+        _native.check(lib.gnn_rope_prepare(dim, _native.ROPE_LAYOUTS[layout], table,
+                                           self.amplitude, ctypes.byref(self._c)),
+                      "gnn_rope_prepare")
+        self._lib = lib
+
+
+def _rope_call(rope, inverse, pos, xs, out, what):
+    if not isinstance(rope, Rope):
+        raise TypeError(f"rope must be a Rope, got {type(rope).__name__}")
+    if not 1 <= len(xs) <= 8:
+        raise ValueError("1 to 8 tensors are rotated in a call")
+    x = xs[0]
+    if not isinstance(x, torch.Tensor) or x.dim() != 3 or not x.is_cuda:
+        raise ValueError("rotary positions take CUDA tensors [N, H, D]")
+    n, _, D = x.shape
+    dtype, device = x.dtype, x.device
+    dt = _dtype_code(dtype)
+    if D < rope.dim:
+        raise ValueError(f"heads of {D} elements are narrower than the rope's {rope.dim}")
+    _plain_tensor(pos, "pos", (n,), torch.int32, device)
+    if out is None:
+        out = [None] * len(xs)
+    elif len(out) != len(xs):
+        raise ValueError("out must have a tensor for every tensor")
+    got, rows = [], []
+    for x, y in zip(xs, out):
+        y = torch.empty(x.shape, dtype=dtype, device=device) if y is None else y
+        for name, t in (("every tensor", x), ("out", y)):
+            if not isinstance(t, torch.Tensor) or t.dim() != 3 or t.shape[0] != n or \
+                    t.shape[2] != D or t.shape[1] != x.shape[1]:
+                raise ValueError(f"{name} must be [{n}, H, {D}]")
+            if t.dtype != dtype or t.device != device:
+                raise TypeError(f"{name} must be {dtype} on {device}")
+            if t.stride(2) != 1 and D > 1:
+                raise ValueError(f"{name} must have contiguous rows of D elements")
+        if x.shape[1] < 1:
+            raise ValueError("every tensor must have a head")
+        got.append(y)
+        rows.append(_native.RopeRows(x.data_ptr(), y.data_ptr(), x.stride(0), x.stride(1),
+                                     y.stride(0), y.stride(1), x.shape[1]))
+    _launch(rope._lib.gnn_rope_apply, what, device, ctypes.byref(rope._c), inverse, n, D,
+            _at(pos), len(rows), _native.ROPE_ROWS[len(rows)](*rows), dt)
+    return tuple(got)
+
+
+@_on_stream
+def rope_forward(rope: Rope, pos: torch.Tensor, *xs: torch.Tensor, out=None):
+    """The tensors xs [N, H, D] (any H each) with their pairs turned by the nodes'
+    positions pos [N] int32, in one launch, as a tuple.  Elements past rope.dim pass
+    as they are.  xs may be views with any node and head strides (q and key of a
+    fused projection); rows of D elements are contiguous.  out: the tensors to write,
+    xs themselves for a rotation in place."""
+    return _rope_call(rope, 0, pos, xs, out, "gnn_rope_apply")
+
+
+@_on_stream
+def rope_backward(rope: Rope, pos: torch.Tensor, *dys: torch.Tensor, out=None):
+    """The gradients of rope_forward's xs from those of its results."""
+    return _rope_call(rope, 1, pos, dys, out, "gnn_rope_apply")
+
+
+class RotaryPositions(torch.autograd.Function):
+    """q, key = RotaryPositions.apply(rope, pos, q, key): any number of tensors up to 8."""
+
+    @staticmethod
+    def forward(ctx, rope, pos, *xs):
+        ctx.rope = rope
+        ctx.save_for_backward(pos)
+        return rope_forward(rope, pos, *xs)
+
+    @staticmethod
+    @once_differentiable
+    def backward(ctx, *dys):
+        (pos,) = ctx.saved_tensors
+        return None, None, *rope_backward(ctx.rope, pos, *(d.contiguous() for d in dys))
+
+
 def transformer_layer(g: Graph, x: torch.Tensor, q: torch.Tensor, key: torch.Tensor,
                       val: torch.Tensor, rel: RelPos | None = None, bias=None, gate=None,
                       w_post=None, b_post=None, res_scale=None, w_pre=None, b_pre=None,
                       project=None, scale: float | None = None, kind="rms", eps: float = 1e-6,
-                      checkpoint8: bool = False):
+                      checkpoint8: bool = False, rope: Rope | None = None, pos=None):
     """One graph-transformer layer between its input projections and the next
     layer's, with autograd: attention of q, key, val [N,H,D] over g (with rel and
     bias, if given), `project` (the output projection, a function of the
@@ -987,11 +1117,16 @@ def transformer_layer(g: Graph, x: torch.Tensor, q: torch.Tensor, key: torch.Ten
     norm, gate, residual scale and sum with x, and the norm before the next
     layer.  Returns (y, z) as norm_residual_forward does.  checkpoint8: the
     attention keeps 8-bit checkpoints of q, key and val for its backward pass
-    instead of the tensors.  To capture a training step into a CUDA graph, let no
+    instead of the tensors.  rope and pos [N] int32: rotary positions of q and key
+    before the attention.  To capture a training step into a CUDA graph, let no
     eager autograd graph of the same leaves be alive (torch would order the
     captured gradients behind the eager stream)."""
     if (rel is None) != (bias is None):
         raise ValueError("rel and bias go together")
+    if (rope is None) != (pos is None):
+        raise ValueError("rope and pos go together")
+    if rope is not None:
+        q, key = RotaryPositions.apply(rope, pos, q, key)
     if checkpoint8:
         out = TransformerCheckpoint8.apply(g, rel, q, key, val, bias, scale)
     elif rel is not None:

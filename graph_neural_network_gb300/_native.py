@@ -20,11 +20,14 @@ ERR_WORKSPACE_TOO_SMALL, ERR_CUDA, ERR_DEVICE_ASSERT, ERR_TIMEOUT = 4, 5, 6, 7
 F32, BF16 = 0, 1
 NORMS = {"sum": 0, "mean": 1, "sym": 2}  # gnn_norm
 REDUCE_OPS = {"max": 0, "min": 1}        # gnn_reduce_op
+ROPE_LAYOUTS = {"half": 0, "interleaved": 1}  # gnn_rope_layout
+ROPE_SCALINGS = {None: 0, "linear": 1, "ntk": 2, "yarn": 3}  # gnn_rope_scaling
 ROWNORMS = {"none": 0, "rms": 1, "layer": 2}  # gnn_rownorm
 
 # (name, restype, argtypes) of every exported symbol, in header order
 _P, _I64, _I32, _SZ, _F = (ctypes.c_void_p, ctypes.c_int64, ctypes.c_int32, ctypes.c_size_t,
                            ctypes.c_float)
+_D = ctypes.c_double
 SIGNATURES = [
     ("gnn_default_tiling", None, [_P]),
     ("gnn_graph_buffer_bytes", _SZ, [_I64, _I64, _P]),
@@ -76,6 +79,9 @@ SIGNATURES = [
     ("gnn_norm_residual_forward", _I32, [_P, _I32, _P, _P, _P, _P, _P, _P]),
     ("gnn_norm_residual_workspace_bytes", _SZ, [_P, _I32]),
     ("gnn_norm_residual_backward", _I32, [_P, _I32, _P, _P, _P, _P, _P, _P, _P, _SZ, _P]),
+    ("gnn_rope_frequencies", _I32, [_I32, _D, _I32, _D, _D, _D, _D, _P, _P]),
+    ("gnn_rope_prepare", _I32, [_I32, _I32, _P, _F, _P]),
+    ("gnn_rope_apply", _I32, [_P, _I32, _I64, _I32, _P, _I32, _P, _I32, _P]),
     ("reduce_agg_workspace_bytes", _SZ, [_P, _I32, _I32]),
     ("reduce_agg_forward", _I32, [_P, _I32, _I32, _I32, _P, _P, _P, _P, _SZ, _P]),
     ("reduce_agg_backward", _I32, [_P, _I32, _I32, _P, _P, _P, _P, _SZ, _P]),
@@ -107,6 +113,22 @@ class NormResidual(ctypes.Structure):  # gnn_norm_residual, its parameters in li
 class NormGrads(ctypes.Structure):
     _fields_ = [(k, _P) for k in ("dx", "dout", "dgate", "dw_post", "db_post", "dscale", "dw_pre",
                                   "db_pre")]
+
+
+ROPE_MAX_DIM = 256  # GNN_ROPE_MAX_DIM
+
+
+class Rope(ctypes.Structure):  # gnn_rope
+    _fields_ = [("dim", _I32), ("layout", _I32), ("amplitude", _F),
+                ("turns", ctypes.c_uint64 * (ROPE_MAX_DIM // 2))]
+
+
+class RopeRows(ctypes.Structure):  # gnn_rope_rows
+    _fields_ = [("x", _P), ("y", _P), ("x_node", _I64), ("x_head", _I64), ("y_node", _I64),
+                ("y_head", _I64), ("H", _I32)]
+
+
+ROPE_ROWS = [RopeRows * n for n in range(9)]  # arrays of them, by length
 
 
 class GnnError(RuntimeError):

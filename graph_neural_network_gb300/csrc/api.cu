@@ -1,6 +1,7 @@
 // C-ABI entry points: argument checks, workspace layout, dispatch.
 #include <new>
 
+#include "api_util.h"
 #include "internal.h"
 
 namespace gnn {
@@ -86,12 +87,13 @@ WsLayout ws_layout(const gnn_graph* g, const Shape& s) {
 
 }  // namespace gnn
 
+using gnn::aligned;
+using gnn::current_sms;
+using gnn::from_cuda;
 using gnn::Shape;
 using gnn::WsLayout;
 
 namespace {
-
-bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
 
 bool tiling_ok(const gnn_tiling& t) {
   return t.light_max_deg >= GNN_LIGHT_AUTO && t.cta_max_deg >= 0 &&
@@ -125,15 +127,6 @@ gnn_status check_call(const gnn_graph* g, int H, int D, gnn_dtype dt, Shape* s) 
   if (H < 1 || D < 1) return GNN_ERR_INVALID_ARG;
   if (!gnn::make_shape(H, D, dt, s)) return GNN_ERR_UNSUPPORTED;
   return GNN_OK;
-}
-
-// The status of a call's launches.  A refused one (cudaLaunchKernelEx, an attribute) also
-// stays as the thread's last error, which the next call's cudaGetLastError would take for
-// its own: it is taken here.
-gnn_status from_cuda(cudaError_t e) {
-  if (e == cudaSuccess) return GNN_OK;
-  (void)cudaGetLastError();
-  return GNN_ERR_CUDA;
 }
 
 }  // namespace
@@ -419,12 +412,6 @@ gnn_status gatv2_shape(const gnn_graph* g, int H, int D, gnn_dtype dt, Shape* s)
 bool device_ok(const gnn_graph* g) {
   int dev = -1;
   return cudaGetDevice(&dev) == cudaSuccess && dev == g->device;
-}
-
-bool current_sms(int* sms) {
-  int dev = 0;
-  return cudaGetDevice(&dev) == cudaSuccess &&
-         cudaDeviceGetAttribute(sms, cudaDevAttrMultiProcessorCount, dev) == cudaSuccess;
 }
 
 gnn_status pack8_shape(int64_t n, int H, int D, gnn_dtype dt, Shape* s) {

@@ -1,0 +1,144 @@
+// C-ABI entry points of the operators round a layer's projections (rotary
+// positions): argument checks, then the launchers.
+#include <math.h>
+
+#include "api_util.h"
+#include "internal.h"
+
+using gnn::aligned;
+using gnn::current_sms;
+using gnn::from_cuda;
+
+namespace {
+
+bool dtype_ok(gnn_dtype dt) { return dt == GNN_F32 || dt == GNN_BF16; }
+
+bool rope_dim_ok(int dim) { return dim >= 2 && dim <= GNN_ROPE_MAX_DIM && dim % 2 == 0; }
+
+// Rows of D elements at these strides lie apart: heads inside nodes, or nodes
+// inside heads.  (A single node's or head's stride is of no account.)
+bool rows_apart(int64_t n, int64_t H, int64_t D, int64_t node, int64_t head) {
+  if (n == 1 && H == 1) return true;
+  if (n == 1) return head >= D;
+  if (H == 1) return node >= D;
+  // (in this order no product overflows: strides are compared with spans divided out)
+  const auto inside = [](int64_t inner, int64_t outer, int64_t count, int64_t width) {
+    return inner >= width && outer >= width && (outer - width) / inner >= count - 1;
+  };
+  return inside(head, node, H, D) || inside(node, head, n, D);
+}
+
+// |index| * |stride| * bytes stays within 62 bits for every row of the tensor.
+bool span_ok(int64_t count, int64_t stride) {
+  const int64_t a = stride < 0 ? -(stride + 1) : stride;
+  return count <= 1 || a <= (int64_t(1) << 58) / count;
+}
+
+}  // namespace
+
+extern "C" {
+
+gnn_status gnn_rope_frequencies(int dim, double base, gnn_rope_scaling scaling, double factor,
+                                double length, double fast, double slow, double* freqs,
+                                float* amplitude) {
+  if (!freqs || !amplitude || !rope_dim_ok(dim) || !(base > 1.0) || !isfinite(base))
+    return GNN_ERR_INVALID_ARG;
+  if (scaling != GNN_ROPE_PLAIN && (!(factor >= 1.0) || !isfinite(factor)))
+    return GNN_ERR_INVALID_ARG;
+  const int half = dim / 2;
+  *amplitude = 1.f;
+  switch (scaling) {
+    case GNN_ROPE_PLAIN:
+    case GNN_ROPE_LINEAR:
+    case GNN_ROPE_NTK:
+      if (scaling == GNN_ROPE_NTK) {
+        if (dim < 4) return GNN_ERR_INVALID_ARG;
+        base *= pow(factor, double(dim) / (dim - 2));
+        if (!isfinite(base)) return GNN_ERR_INVALID_ARG;
+      }
+      for (int i = 0; i < half; ++i) {
+        freqs[i] = pow(base, -2.0 * i / dim);
+        if (scaling == GNN_ROPE_LINEAR) freqs[i] /= factor;
+      }
+      return GNN_OK;
+    case GNN_ROPE_YARN: {
+      if (!(length > 0.0) || !isfinite(length) || !(slow > 0.0) || !(fast > slow) ||
+          !isfinite(fast))
+        return GNN_ERR_INVALID_ARG;
+      // the index whose pair turns `turns` times in `length` positions
+      const auto index = [&](double turns) {
+        return dim * log(length / (turns * 2.0 * M_PI)) / (2.0 * log(base));
+      };
+      double low = fmax(floor(index(fast)), 0.0);
+      double high = fmin(ceil(index(slow)), half - 1.0);
+      if (!(high > low)) high = low + 0.001;
+      for (int i = 0; i < half; ++i) {
+        const double f = pow(base, -2.0 * i / dim);
+        const double s = fmin(fmax((i - low) / (high - low), 0.0), 1.0);
+        freqs[i] = f / factor * s + f * (1.0 - s);
+      }
+      *amplitude = float(0.1 * log(factor) + 1.0);
+      return GNN_OK;
+    }
+  }
+  return GNN_ERR_INVALID_ARG;
+}
+
+gnn_status gnn_rope_prepare(int dim, gnn_rope_layout layout, const double* freqs, float amplitude,
+                            gnn_rope* out) {
+  if (!out || !freqs || !rope_dim_ok(dim) || !isfinite(amplitude) ||
+      (layout != GNN_ROPE_HALF && layout != GNN_ROPE_INTERLEAVED))
+    return GNN_ERR_INVALID_ARG;
+  for (int i = 0; i < dim / 2; ++i)
+    if (!(fabs(freqs[i]) <= 1073741824.0)) return GNN_ERR_INVALID_ARG;
+  *out = gnn_rope{};
+  out->dim = dim;
+  out->layout = layout;
+  out->amplitude = amplitude;
+  for (int i = 0; i < dim / 2; ++i) {
+    // the fraction of a turn in [0, 1), then its first 64 bits
+    long double t = (long double)(freqs[i]) / (2.0L * 3.14159265358979323846264338327950288L);
+    t -= floorl(t);
+    const long double w = floorl(ldexpl(t, 64));
+    out->turns[i] = w >= 18446744073709551616.0L ? ~uint64_t(0) : uint64_t(w);
+  }
+  return GNN_OK;
+}
+
+gnn_status gnn_rope_apply(const gnn_rope* rope, int inverse, int64_t n, int D, const int32_t* pos,
+                          int count, const gnn_rope_rows* t, gnn_dtype dtype, void* stream) {
+  if (!rope || !rope_dim_ok(rope->dim) || !isfinite(rope->amplitude) ||
+      (rope->layout != GNN_ROPE_HALF && rope->layout != GNN_ROPE_INTERLEAVED) ||
+      (inverse != 0 && inverse != 1) || !dtype_ok(dtype) || n < 0 ||
+      n >= (int64_t(1) << 31) || D < rope->dim || D > 65536 || !t || count < 1 ||
+      count > gnn::kRopeMax)
+    return GNN_ERR_INVALID_ARG;
+  const int s = dtype == GNN_F32 ? 4 : 2;
+  // the widest access that pointers, strides and both halves of the pairs allow
+  uint64_t all = uint64_t(D) * s | uint64_t(rope->dim) * s / 2 | 16;
+  for (int k = 0; k < count; ++k) {
+    const gnn_rope_rows& r = t[k];
+    if (r.H < 1 || r.H > 65536) return GNN_ERR_INVALID_ARG;
+    if (n == 0) continue;
+    if (!r.x || !r.y || !aligned(r.x, s) || !aligned(r.y, s)) return GNN_ERR_INVALID_ARG;
+    if (!span_ok(n, r.x_node) || !span_ok(r.H, r.x_head) || !span_ok(n, r.y_node) ||
+        !span_ok(r.H, r.y_head) || !rows_apart(n, r.H, D, r.y_node, r.y_head))
+      return GNN_ERR_INVALID_ARG;
+    if (r.x == r.y && ((n > 1 && r.x_node != r.y_node) || (r.H > 1 && r.x_head != r.y_head)))
+      return GNN_ERR_INVALID_ARG;
+    for (int j = 0; j < k; ++j)
+      if (t[j].y == r.y) return GNN_ERR_INVALID_ARG;
+    all |= reinterpret_cast<uintptr_t>(r.x) | reinterpret_cast<uintptr_t>(r.y);
+    if (n > 1) all |= uint64_t(r.x_node) * s | uint64_t(r.y_node) * s;
+    if (r.H > 1) all |= uint64_t(r.x_head) * s | uint64_t(r.y_head) * s;
+  }
+  if (n == 0) return GNN_OK;
+  if (!pos || !aligned(pos, 4)) return GNN_ERR_INVALID_ARG;
+  int sms = 0;
+  if (!current_sms(&sms)) return GNN_ERR_CUDA;
+  const int width = int(all & (~all + 1));  // the lowest bit set: at most 16
+  return from_cuda(gnn::launch_rope(*rope, inverse, n, D, pos, count, t, dtype, width, sms,
+                                    static_cast<cudaStream_t>(stream)));
+}
+
+}  // extern "C"

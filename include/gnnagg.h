@@ -514,6 +514,70 @@ gnn_status gnn_norm_residual_backward(const gnn_norm_residual* d, gnn_dtype dtyp
                                       const void* dz, const gnn_norm_grads* grads, void* ws,
                                       size_t ws_bytes, void* stream);
 
+/* ---- Rotary positions --------------------------------------------------------
+ *
+ * Nodes that lie along a sequence can carry their positions in q and key
+ * themselves: the first `dim` elements of a head vector are dim / 2 pairs (a, b),
+ * and pair i of a node at position p turns by the angle t = p * freqs[i],
+ *     a' = m (a cos t - b sin t),  b' = m (a sin t + b cos t),
+ * with m the amplitude, so that q_i . key_j depends on pos[i] - pos[j] only.
+ * Pair i: elements i and i + dim / 2 (GNN_ROPE_HALF), or 2 i and 2 i + 1
+ * (GNN_ROPE_INTERLEAVED).  Elements from dim on pass as they are.  The inverse
+ * (the gradient) turns by -t, with the same m.
+ * An angle is held as a fraction of a turn in 64 whole bits, where p times the
+ * frequency wraps round exactly: it is accurate at any 32-bit position, negative
+ * ones too.  Products are float32, each output is rounded once. */
+typedef enum { GNN_ROPE_HALF = 0, GNN_ROPE_INTERLEAVED = 1 } gnn_rope_layout;
+
+#define GNN_ROPE_MAX_DIM 256
+
+typedef struct {
+  int32_t dim, layout;
+  float amplitude;
+  uint64_t turns[GNN_ROPE_MAX_DIM / 2]; /* of one position, in 2^-64 of a turn */
+} gnn_rope; /* host memory, read during the calls */
+
+/* Frequencies of the usual rules (radians a position) and the amplitude of the
+ * rule.  Host only.  Plain: base^(-2 i / dim).  For contexts `factor` times as
+ * long (factor >= 1): LINEAR divides them all by factor; NTK raises base to
+ * base * factor^(dim / (dim - 2)) (dim >= 4); YARN divides pairs that turn less
+ * than `slow` times in `length` positions, keeps those that turn more than
+ * `fast` times and joins the two by a line over the pairs' indices, with an
+ * amplitude of 0.1 ln(factor) + 1 (length > 0, 0 < slow < fast).  dim: even, 2 to
+ * GNN_ROPE_MAX_DIM; base > 1. */
+typedef enum {
+  GNN_ROPE_PLAIN = 0,
+  GNN_ROPE_LINEAR = 1,
+  GNN_ROPE_NTK = 2,
+  GNN_ROPE_YARN = 3
+} gnn_rope_scaling;
+
+gnn_status gnn_rope_frequencies(int dim, double base, gnn_rope_scaling scaling, double factor,
+                                double length, double fast, double slow, double* freqs,
+                                float* amplitude);
+
+/* *out for freqs[dim / 2] (finite, at most 2^30 in magnitude) and an amplitude.
+ * Host only. */
+gnn_status gnn_rope_prepare(int dim, gnn_rope_layout layout, const double* freqs, float amplitude,
+                            gnn_rope* out);
+
+/* One tensor [n][H][D] of a call: rows of D contiguous elements, node and head
+ * strides in elements (x's any, y's such that no two rows overlap). */
+typedef struct {
+  const void* x;
+  void* y;
+  int64_t x_node, x_head, y_node, y_head;
+  int32_t H;
+} gnn_rope_rows;
+
+/* Rotates `count` (1 to 8) tensors of one D >= dim and dtype in one launch (t:
+ * host memory).  y may be x itself with the same strides; no output may overlap
+ * an input or another output otherwise.  Any alignment to the element; vectors of
+ * 16 bytes are used where pointers, strides, D and dim allow them.  D at most 65536.
+ * Asynchronous on `stream`; bitwise reproducible. */
+gnn_status gnn_rope_apply(const gnn_rope* rope, int inverse, int64_t n, int D, const int32_t* pos,
+                          int count, const gnn_rope_rows* t, gnn_dtype dtype, void* stream);
+
 /* ---- Max / min neighbourhood reduction -----------------------------------
  *
  * out[i][f] = max (or min) over the in-neighbours j of i of x[j][f], and
