@@ -225,7 +225,7 @@ cudaError_t launch_norm_residual_backward(const gnn_norm_residual& d, gnn_dtype 
 // Rotary positions (rope.cu): count tensors, `width` bytes an access (16, 8, 4 or 2).
 constexpr int kRopeMax = 8;  // tensors of one call
 cudaError_t launch_rope(const gnn_rope& rope, int inverse, int64_t n, int D, const int32_t* pos,
-                        int count, const gnn_rope_rows* t, gnn_dtype dt, int width, int sm_count,
+                        int count, const gnn_rope_rows* t, gnn_dtype dt, int width,
                         cudaStream_t st);
 
 // Bounded-wait self-test (diag.cu).

@@ -8,33 +8,34 @@
 // conversion's to float32, 2^-25 of half a turn at most, at position 2^31 as at 1:
 // a float32 product would have lost the angle at 2^20.
 //
-// Bound: HBM, 2 s bytes an element (and 4 a node).  A node's angles serve all its
-// heads and tensors, so a thread keeps the sines and cosines of its pairs (of two
-// accesses of `width` bytes) and walks heads with them, two vectors a head, four
-// heads in flight.  The threads of a node stand beside each other over the pairs
-// and then over heads, far enough that their accesses are whole lines, and
-// over more heads where there are too few nodes for the GPU.
+// Bound: HBM, 2 s bytes an element (and 4 a node).  A block takes a few nodes whole
+// and computes their sines and cosines once, together, into shared memory: one or
+// two sincospif a thread, where a thread for itself would need one for each pair it
+// turns.  A thread then turns a slot (two accesses of `width` bytes, the partners of
+// their pairs) of one head in each tensor, or of several heads, its loads issued
+// before the block computes.  Slots of a node, then its heads, stand side by side
+// over the threads, so that accesses are whole lines.
 #include "device.cuh"
 
 namespace gnn {
 namespace {
 
 struct RopeArgs {
-  int64_t items;         // nodes * per
-  uint64_t div_per;      // ceil(2^64 / per): item * div_per / 2^64 is the node (items * per < 2^62)
-  uint32_t per, slots;   // threads of a node, and of one of its heads
+  int64_t n;
+  int nodes_log2;        // nodes of a block
+  uint32_t slots, per;   // threads of a head, and of a node; slots > kThreads go round
+  uint32_t div_per, div_slots;  // ceil(2^16 / x): t * div >> 16 is t / x, t and x at most 2^8
+  int lanes, heads;      // heads of a node side by side; the most of a tensor
   int turned;            // slots of the rotated part; the others copy
   int half, dim, D;      // elements
-  int lanes;             // heads of a node side by side
   int count;
-  int interleaved;
   float amplitude, sine; // sine: the amplitude with the direction's sign
   const int32_t* pos;
   gnn_rope_rows t[kRopeMax];
   uint64_t turns[GNN_ROPE_MAX_DIM / 2];
 };
 
-// kB bytes of memory (not the read-only path: y may be x).
+// kB bytes of memory, as words or a half of one (not the read-only path: y may be x).
 template <int kB>
 struct Access;
 template <>
@@ -46,170 +47,220 @@ struct Access<4> { using type = uint32_t; };
 template <>
 struct Access<2> { using type = uint16_t; };
 
-__device__ __forceinline__ float widen(float x) { return x; }
-__device__ __forceinline__ float widen(__nv_bfloat16 x) { return __bfloat162float(x); }
-
 template <typename T, int kB>
 struct RopeVec {
   static constexpr int n = kB / int(sizeof(T));
   union {
     typename Access<kB>::type raw;
-    T e[n];
+    uint32_t w[(kB + 3) / 4];
   };
   __device__ __forceinline__ RopeVec() {}
   __device__ __forceinline__ void get(float (&x)[n]) const {
+    if constexpr (sizeof(T) == 4) {
 #pragma unroll
-    for (int c = 0; c < n; ++c) x[c] = widen(e[c]);
+      for (int c = 0; c < n; ++c) x[c] = __uint_as_float(w[c]);
+    } else if constexpr (n == 1) {
+      x[0] = __uint_as_float(uint32_t(raw) << 16);
+    } else {
+#pragma unroll
+      for (int c = 0; c < n; c += 2) {
+        x[c] = __uint_as_float(w[c / 2] << 16);
+        x[c + 1] = __uint_as_float(w[c / 2] & 0xffff0000u);
+      }
+    }
   }
   __device__ __forceinline__ void set(const float (&x)[n]) {
+    if constexpr (sizeof(T) == 4) {
 #pragma unroll
-    for (int c = 0; c < n; ++c) e[c] = T(x[c]);
+      for (int c = 0; c < n; ++c) w[c] = __float_as_uint(x[c]);
+    } else if constexpr (n == 1) {
+      raw = uint16_t(bf2(x[0], 0.f));
+    } else {
+#pragma unroll
+      for (int c = 0; c < n; c += 2) w[c / 2] = bf2(x[c], x[c + 1]);
+    }
   }
 };
 
-constexpr int kRopeUnroll = 4;
+// (a, b) turned by (co, si): spelt out, so that every width rounds alike.
+__device__ __forceinline__ void turn_pair(float a, float b, float co, float si, float& f,
+                                          float& g) {
+  f = __fmaf_rn(a, co, -__fmul_rn(b, si));
+  g = __fmaf_rn(a, si, __fmul_rn(b, co));
+}
 
-template <typename T, int kB>
-__global__ void __launch_bounds__(kThreads) rope_rows(const __grid_constant__ RopeArgs A) {
+constexpr int kRopeUnroll = 2;  // tensors in flight
+
+// kMixed: pairs of neighbours (GNN_ROPE_INTERLEAVED).
+template <typename T, int kB, bool kMixed>
+__global__ void __launch_bounds__(kThreads, 5) rope_rows(const __grid_constant__ RopeArgs A) {
   using Vec = RopeVec<T, kB>;
   using Raw = typename Access<kB>::type;
   constexpr int V = Vec::n;
-  __shared__ uint64_t turns[GNN_ROPE_MAX_DIM / 2];
-  for (int i = threadIdx.x; i < A.half; i += kThreads) turns[i] = A.turns[i];
-  const int64_t item = int64_t(blockIdx.x) * kThreads + threadIdx.x;
-  const bool on = item < A.items;
-  const int64_t node =
-      !on ? 0 : A.per == 1 ? item : int64_t(__umul64hi(uint64_t(item), A.div_per));
-  const uint32_t r = on ? uint32_t(item - node * A.per) : 0u;
-  const int lane = int(r / A.slots), slot = int(r - uint32_t(lane) * A.slots);
-  const int32_t p = __ldg(A.pos + node);
-  __syncthreads();
-  if (!on) return;
-  // the two accesses of a slot, as elements of the head vector: b < 0 where there is none
-  int a, b;
-  const bool turn = slot < A.turned;
-  if (turn) {
-    a = A.interleaved ? 2 * slot * V : slot * V;
-    b = A.interleaved ? a + V : a + A.half;
-  } else {
-    a = A.dim + 2 * (slot - A.turned) * V;
-    b = a + V < A.D ? a + V : -1;
-  }
-  float co[V], si[V];
-  if (turn) {
-#pragma unroll
-    for (int c = 0; c < V; ++c) {
-      const uint64_t left = uint64_t(int64_t(p)) * turns[slot * V + c];
-      const float x = float(int32_t(uint32_t(left >> 32))) * 4.656612873077393e-10f;  // 2^-31
-      sincospif(x, &si[c], &co[c]);
-      co[c] *= A.amplitude;
-      si[c] *= A.sine;
+  // cosines and sines of pairs i, i + 1 (one pair where a slot has one): [i / 2][node]
+  constexpr int P = V > 1 ? 2 : 1;
+  __shared__ __align__(16) float table[kThreads * V * 2];
+  const int64_t first = int64_t(blockIdx.x) << A.nodes_log2;
+  const int nodes = int(min(int64_t(1) << A.nodes_log2, A.n - first));
+  const int local = A.per > kThreads ? 0 : int(threadIdx.x * A.div_per >> 16);
+  const uint32_t r = threadIdx.x - uint32_t(local) * A.per;
+  const int lane = A.per > kThreads ? 0 : int(r * A.div_slots >> 16);
+  uint32_t slot = r - uint32_t(lane) * A.slots;
+  const int64_t node = first + local;
+  bool ready = false;  // the table
+  for (uint32_t round = 0; round < A.slots; round += kThreads, slot += kThreads) {
+    const bool on = local < nodes && slot < A.slots;
+    const bool turn = int(slot) < A.turned;
+    // the slot's accesses, as elements of the head vector: b < 0 where there is none
+    int a, b;
+    if (turn) {
+      a = kMixed ? 2 * int(slot) * V : int(slot) * V;
+      b = kMixed ? a + V : a + A.half;
+    } else {
+      a = A.dim + 2 * (int(slot) - A.turned) * V;
+      b = a + V < A.D ? a + V : -1;
     }
-  }
-  int k = 0, h = 0;  // the next tensor and its head for lane 0 (the same in every thread)
-  while (k < A.count) {
-    Vec va[kRopeUnroll], vb[kRopeUnroll];
-    T* to[kRopeUnroll];
+    for (int h = 0; h < A.heads; h += A.lanes)
+      for (int k = 0; k < A.count; k += kRopeUnroll) {
+        Vec va[kRopeUnroll], vb[kRopeUnroll];
+        bool go[kRopeUnroll];
 #pragma unroll
-    for (int u = 0; u < kRopeUnroll; ++u) {
-      to[u] = nullptr;
-      if (k < A.count) {
-        const gnn_rope_rows& t = A.t[k];
-        const int head = h + lane;
-        if (head < t.H && (turn || t.x != t.y)) {
-          const T* x = static_cast<const T*>(t.x) + node * t.x_node + head * t.x_head;
-          to[u] = static_cast<T*>(t.y) + node * t.y_node + head * t.y_head;
-          va[u].raw = *reinterpret_cast<const Raw*>(x + a);
-          if (b >= 0) vb[u].raw = *reinterpret_cast<const Raw*>(x + b);
-        }
-        h += A.lanes;
-        if (h >= t.H) {
-          h = 0;
-          ++k;
-        }
-      }
-    }
-#pragma unroll
-    for (int u = 0; u < kRopeUnroll; ++u) {
-      if (!to[u]) continue;
-      if (turn) {
-        float x[V], y[V], f[V], g[V];
-        va[u].get(x);
-        vb[u].get(y);
-        if (A.interleaved && V > 1) {
-          // pairs (0, 1), (2, 3) .. of the first access, then of the second
-#pragma unroll
-          for (int c = 0; c + 1 < V; c += 2) {
-            const int d = c / 2, e = (V + c) / 2;
-            f[c] = x[c] * co[d] - x[c + 1] * si[d];
-            f[c + 1] = x[c] * si[d] + x[c + 1] * co[d];
-            g[c] = y[c] * co[e] - y[c + 1] * si[e];
-            g[c + 1] = y[c] * si[e] + y[c + 1] * co[e];
-          }
-        } else {
-#pragma unroll
-          for (int c = 0; c < V; ++c) {
-            f[c] = x[c] * co[c] - y[c] * si[c];
-            g[c] = x[c] * si[c] + y[c] * co[c];
+        for (int u = 0; u < kRopeUnroll; ++u) {
+          go[u] = false;
+          if (k + u < A.count) {
+            const gnn_rope_rows& t = A.t[k + u];
+            go[u] = on && h + lane < t.H && (turn || t.x != t.y);
+            const T* x = static_cast<const T*>(t.x) + node * t.x_node + (h + lane) * t.x_head;
+            if (go[u]) va[u].raw = *reinterpret_cast<const Raw*>(x + a);
+            if (go[u] && b >= 0) vb[u].raw = *reinterpret_cast<const Raw*>(x + b);
           }
         }
-        va[u].set(f);
-        vb[u].set(g);
+        if (!ready) {
+          ready = true;
+          for (int e = threadIdx.x; e < A.half << A.nodes_log2; e += blockDim.x) {
+            const int i = e >> A.nodes_log2, at = e - (i << A.nodes_log2);
+            if (at >= nodes) continue;
+            const uint64_t left = uint64_t(int64_t(__ldg(A.pos + first + at))) * A.turns[i];
+            const float x =
+                float(int32_t(uint32_t(left >> 32))) * 4.656612873077393e-10f;  // 2^-31
+            float si, co;
+            sincospif(x, &si, &co);
+            float* to = table + 2 * P * (((i / P) << A.nodes_log2) + at) + i % P;
+            to[0] = co * A.amplitude;
+            to[P] = si * A.sine;
+          }
+          __syncthreads();
+        }
+        if (turn) {
+          const float* cs = table + 2 * P * ((int(slot) * (V / P) << A.nodes_log2) + local);
+          float co[V], si[V];
+#pragma unroll
+          for (int c = 0; c < V; c += P) {
+            const float* at = cs + 2 * P * ((c / P) << A.nodes_log2);
+            if constexpr (P == 2) {
+              const float4 q = *reinterpret_cast<const float4*>(at);
+              co[c] = q.x;
+              co[c + 1] = q.y;
+              si[c] = q.z;
+              si[c + 1] = q.w;
+            } else {
+              const float2 q = *reinterpret_cast<const float2*>(at);
+              co[c] = q.x;
+              si[c] = q.y;
+            }
+          }
+#pragma unroll
+          for (int u = 0; u < kRopeUnroll; ++u) {
+            if (!go[u]) continue;
+            float x[V], y[V], f[V], g[V];
+            va[u].get(x);
+            vb[u].get(y);
+            if constexpr (kMixed && V > 1) {
+              // pairs (0, 1), (2, 3) .. of the first access, then of the second
+#pragma unroll
+              for (int c = 0; c < V / 2; ++c) {
+                turn_pair(x[2 * c], x[2 * c + 1], co[c], si[c], f[2 * c], f[2 * c + 1]);
+                turn_pair(y[2 * c], y[2 * c + 1], co[V / 2 + c], si[V / 2 + c], g[2 * c],
+                          g[2 * c + 1]);
+              }
+            } else if constexpr (V > 1) {
+              // turn_pair, two at a time
+#pragma unroll
+              for (int c = 0; c < V; c += 2) {
+                float s0, s1;
+                mul2v(s0, s1, y[c], y[c + 1], si[c], si[c + 1]);
+                f[c] = -s0;
+                f[c + 1] = -s1;
+                fma2(f[c], f[c + 1], x[c], x[c + 1], co[c], co[c + 1]);
+                mul2v(g[c], g[c + 1], y[c], y[c + 1], co[c], co[c + 1]);
+                fma2(g[c], g[c + 1], x[c], x[c + 1], si[c], si[c + 1]);
+              }
+            } else {
+              turn_pair(x[0], y[0], co[0], si[0], f[0], g[0]);
+            }
+            va[u].set(f);
+            vb[u].set(g);
+          }
+        }
+#pragma unroll
+        for (int u = 0; u < kRopeUnroll; ++u) {
+          if (k + u >= A.count) continue;
+          const gnn_rope_rows& t = A.t[k + u];
+          T* y = static_cast<T*>(t.y) + node * t.y_node + (h + lane) * t.y_head;
+          if (go[u]) *reinterpret_cast<Raw*>(y + a) = va[u].raw;
+          if (go[u] && b >= 0) *reinterpret_cast<Raw*>(y + b) = vb[u].raw;
+        }
       }
-      *reinterpret_cast<Raw*>(to[u] + a) = va[u].raw;
-      if (b >= 0) *reinterpret_cast<Raw*>(to[u] + b) = vb[u].raw;
-    }
   }
 }
 
 template <typename T, int kB>
-cudaError_t launch(RopeArgs& A, int64_t n, int most_heads, int sm_count, cudaStream_t st) {
+cudaError_t launch(RopeArgs& A, bool mixed, cudaStream_t st) {
   constexpr int V = RopeVec<T, kB>::n;
   A.turned = A.half / V;
   A.slots = uint32_t(A.turned + (A.D - A.dim + 2 * V - 1) / (2 * V));
-  // Heads side by side: whole lines (eight threads take 256 bytes of a tensor), and
-  // enough threads for the GPU as long as there are heads.
-  const int64_t full = int64_t(sm_count) * 1024;
-  int lanes = 1;
-  while (lanes < most_heads && (A.slots * lanes < 8 || n * A.slots * lanes < full)) lanes *= 2;
-  A.lanes = lanes < most_heads ? lanes : most_heads;
+  // as many heads side by side as there are, and as a block has threads
+  const int most = A.slots < kThreads ? kThreads / int(A.slots) : 1;
+  A.lanes = most < A.heads ? most : A.heads;
   A.per = A.slots * uint32_t(A.lanes);
-  A.div_per = A.per == 1 ? 0 : ~uint64_t(0) / A.per + 1;
-  A.items = n * A.per;
-  const int64_t blocks = (A.items + kThreads - 1) / kThreads;
-  if (blocks > 0x7fffffff) return cudaErrorInvalidValue;
-  rope_rows<T, kB><<<unsigned(blocks), kThreads, 0, st>>>(A);
+  A.div_per = 65535 / A.per + 1;
+  A.div_slots = 65535 / A.slots + 1;
+  while ((A.per << (A.nodes_log2 + 1)) <= kThreads) ++A.nodes_log2;
+  const int64_t blocks = (A.n + (int64_t(1) << A.nodes_log2) - 1) >> A.nodes_log2;
+  const uint32_t threads = A.per > kThreads ? kThreads : ((A.per << A.nodes_log2) + 31) / 32 * 32;
+  auto kernel = mixed ? rope_rows<T, kB, true> : rope_rows<T, kB, false>;
+  kernel<<<unsigned(blocks), threads, 0, st>>>(A);
   return cudaGetLastError();
 }
 
 }  // namespace
 
 cudaError_t launch_rope(const gnn_rope& rope, int inverse, int64_t n, int D, const int32_t* pos,
-                        int count, const gnn_rope_rows* t, gnn_dtype dt, int width, int sm_count,
+                        int count, const gnn_rope_rows* t, gnn_dtype dt, int width,
                         cudaStream_t st) {
   RopeArgs A{};
+  A.n = n;
   A.half = rope.dim / 2;
   A.dim = rope.dim;
   A.D = D;
   A.count = count;
-  A.interleaved = rope.layout == GNN_ROPE_INTERLEAVED;
+  const bool mixed = rope.layout == GNN_ROPE_INTERLEAVED;
   A.amplitude = rope.amplitude;
   A.sine = inverse ? -rope.amplitude : rope.amplitude;
   A.pos = pos;
-  int most = 1;
   for (int k = 0; k < count; ++k) {
     A.t[k] = t[k];
-    most = t[k].H > most ? t[k].H : most;
+    A.heads = t[k].H > A.heads ? t[k].H : A.heads;
   }
   for (int i = 0; i < A.half; ++i) A.turns[i] = rope.turns[i];
   if (dt == GNN_F32)
-    return width == 16  ? launch<float, 16>(A, n, most, sm_count, st)
-           : width == 8 ? launch<float, 8>(A, n, most, sm_count, st)
-                        : launch<float, 4>(A, n, most, sm_count, st);
-  return width == 16  ? launch<__nv_bfloat16, 16>(A, n, most, sm_count, st)
-         : width == 8 ? launch<__nv_bfloat16, 8>(A, n, most, sm_count, st)
-         : width == 4 ? launch<__nv_bfloat16, 4>(A, n, most, sm_count, st)
-                      : launch<__nv_bfloat16, 2>(A, n, most, sm_count, st);
+    return width == 16  ? launch<float, 16>(A, mixed, st)
+           : width == 8 ? launch<float, 8>(A, mixed, st)
+                        : launch<float, 4>(A, mixed, st);
+  return width == 16  ? launch<__nv_bfloat16, 16>(A, mixed, st)
+         : width == 8 ? launch<__nv_bfloat16, 8>(A, mixed, st)
+         : width == 4 ? launch<__nv_bfloat16, 4>(A, mixed, st)
+                      : launch<__nv_bfloat16, 2>(A, mixed, st);
 }
 
 }  // namespace gnn
