@@ -42,6 +42,11 @@ the norms, gate and residual scale between two blocks of a layer:
     y, z = norm_residual_forward(x, o, gate, w_post, scale=scale, w_pre=w_pre)
     grads = norm_residual_backward(y, o, dy, dz, gate, w_post, scale=scale, w_pre=w_pre)
 
+the sum with the residual and its root-mean-square norm in 8 bits, for a projection's input:
+
+    y, z8 = add_norm8_forward(x, o, w, fmt="e4m3", group=128)   # z8: values and scales
+    dx, dw = add_norm8_backward(y, dy, dz, w)
+
 rotary positions of q and key (views of a fused projection [N, 3, H, D] as they are):
 
     rope = Rope(D, "half", scaling="yarn", factor=8, length=4096)     # once
@@ -81,7 +86,8 @@ __all__ = ["Graph", "gat_forward", "gat_backward", "GATAggregate", "GnnError", "
            "transformer_rel_backward", "TransformerRelAggregate", "norm_residual_forward",
            "norm_residual_backward", "NormResidual", "Packed8", "pack8", "unpack8",
            "transformer_backward8", "TransformerCheckpoint8", "transformer_layer", "Rope",
-           "rope_forward", "rope_backward", "RotaryPositions"]
+           "rope_forward", "rope_backward", "RotaryPositions", "add_norm8_forward",
+           "add_norm8_backward", "AddNorm8"]
 
 
 def _ptr(t):
@@ -717,8 +723,9 @@ class TransformerRelAggregate(torch.autograd.Function):
 
 
 class Packed8(NamedTuple):
-    """An activation [N, H, D] in 8 bits: int8 values of that shape and a
-    float32 scale [N, H], standing for values * scale[..., None]."""
+    """An activation [N, H, D] in 8 bits: int8 (from add_norm8_forward also
+    float8_e4m3fn) values of that shape and a float32 scale [N, H], standing for
+    values * scale[..., None]."""
 
     values: torch.Tensor
     scale: torch.Tensor
@@ -761,6 +768,10 @@ def pack8(*xs: torch.Tensor, out=None):
     return out
 
 
+_EIGHT_DTYPES = {torch.int8: 0, torch.float8_e4m3fn: 1}  # gnn_eight
+_EIGHTS = {"int8": torch.int8, "e4m3": torch.float8_e4m3fn}
+
+
 def _packed(p, name, shape, device) -> _native.Packed8:
     if not isinstance(p, Packed8):
         raise TypeError(f"{name} must be a Packed8, got {type(p).__name__}")
@@ -776,11 +787,21 @@ def unpack8(p: Packed8, dtype: torch.dtype = torch.float32, out=None):
             p.values.dim() != 3 or not p.values.is_cuda:
         raise ValueError("unpack8 takes a Packed8 of CUDA tensors")
     dt = _dtype_code(dtype)
-    shape, device = p.values.shape, p.values.device
-    c = _packed(p, "p", shape, device)
+    values, shape, device = p.values, p.values.shape, p.values.device
+    _plain_tensor(values, "p.values", shape,
+                  values.dtype if values.dtype in _EIGHT_DTYPES else torch.int8, device)
+    _plain_tensor(p.scale, "p.scale", shape[:2], torch.float32, device)
     out = _output(out, "out", shape, dtype, device)
-    _launch(_native.load().gnn_unpack8, "gnn_unpack8", device, *shape, dt, ctypes.byref(c),
-            _at(out))
+    N, H, D = shape
+    if values.dtype == torch.int8 and D <= 256 and D & (D - 1) == 0 and \
+            H * D <= (1024 if D >= 8 else 512):
+        # (rows that pack8 makes; a shape that it does not take is refused there)
+        c = _native.Packed8(values.data_ptr(), p.scale.data_ptr())
+        _launch(_native.load().gnn_unpack8, "gnn_unpack8", device, N, H, D, dt, ctypes.byref(c),
+                _at(out))
+    else:
+        _launch(_native.load().gnn_unpack8_groups, "gnn_unpack8_groups", device, N * H, D,
+                _EIGHT_DTYPES[values.dtype], dt, _at(values), _at(p.scale), _at(out))
     return out
 
 
@@ -982,6 +1003,124 @@ class NormResidual(torch.autograd.Function):
                   for k, t in zip(_NORM_PARAMS, params)), None, None)
 
 
+def _rows(x, name):
+    """The rows and the width of a contiguous CUDA tensor [N, ...]."""
+    if not isinstance(x, torch.Tensor) or x.dim() < 2:
+        raise ValueError(f"{name} must be a tensor [N, ...]")
+    if not x.is_cuda or not x.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous CUDA tensor")
+    n, *rest = x.shape
+    return n, rest[0] if len(rest) == 1 else math.prod(rest)
+
+
+def _weight(w, F, device):
+    """w [F] widened to float32 (None: 1)."""
+    if w is None:
+        return None
+    if not isinstance(w, torch.Tensor) or not w.is_floating_point():
+        raise TypeError("w must be a floating-point tensor")
+    if w.dtype is not torch.float32:
+        w = w.to(torch.float32)
+    return _plain_tensor(w, "w", (F,), torch.float32, device)
+
+
+@_on_stream
+def add_norm8_forward(x: torch.Tensor, o=None, w=None, fmt: str = "int8",
+                      group: int | None = None, eps: float = 1e-6, y=None, out=None):
+    """y = x + o and z = w y / sqrt(mean(y^2) + eps) in 8 bits, for x, o [N, ...] (a
+    node's F features flattened) and w [F].
+
+    Returns y (None where o is None: y is x) and z as a Packed8 of values [N, F/group,
+    group], int8 or float8_e4m3fn (fmt "int8", "e4m3"), with a float32 scale [N,
+    F/group].  group: features that share a scale (default: the row).  unpack8 reads z
+    back.  y, out: tensors to write."""
+    n, F = _rows(x, "x")
+    dtype, device = x.dtype, x.device
+    dt = _dtype_code(dtype)
+    if fmt not in _EIGHTS:
+        raise ValueError(f"fmt must be one of {sorted(_EIGHTS)}")
+    if o is not None:
+        _plain_tensor(o, "o", x.shape, dtype, device)
+        y = _like(y, "y", x)
+    elif y is not None:
+        raise ValueError("there is no y without o: y is x")
+    w = _weight(w, F, device)
+    group = F if group is None else group
+    if not isinstance(group, int) or group < 1 or F % group:
+        raise ValueError(f"group must divide the {F} features of a row")
+    shape = (n, F // group, group)
+    if out is None:
+        out = Packed8(torch.empty(shape, dtype=_EIGHTS[fmt], device=device),
+                      torch.empty(shape[:2], dtype=torch.float32, device=device))
+    else:
+        if not isinstance(out, Packed8):
+            raise TypeError(f"out must be a Packed8, got {type(out).__name__}")
+        _plain_tensor(out.values, "out.values", shape, _EIGHTS[fmt], device)
+        _plain_tensor(out.scale, "out.scale", shape[:2], torch.float32, device)
+    d = _native.AddNorm8(n, F, group, _native.EIGHTS[fmt], eps)
+    _launch(_native.load().gnn_add_norm8_forward, "gnn_add_norm8_forward", device,
+            ctypes.byref(d), dt, _at(x), _at(o), _at(w), _at(y), _at(out.values), _at(out.scale))
+    return y, out
+
+
+@_on_stream
+def add_norm8_backward(y: torch.Tensor, dy, dz: torch.Tensor, w=None, eps: float = 1e-6, dx=None,
+                       dw=None, ws=None):
+    """The gradients of add_norm8_forward with its rounding to 8 bits taken as the
+    identity: dx (y's dtype), of x and of o alike, and dw [F] float32 (None without w).
+    y is the forward's y (x where it had no o), dy the gradient that reaches y past the
+    norm (None: nothing) and dz that of the values that z stands for."""
+    n, F = _rows(y, "y")
+    dtype, device = y.dtype, y.device
+    dt = _dtype_code(dtype)
+    _plain_tensor(dz, "dz", y.shape, dtype, device)
+    if dy is not None:
+        _plain_tensor(dy, "dy", y.shape, dtype, device)
+    w = _weight(w, F, device)
+    dx = _like(dx, "dx", y)
+    if w is not None:
+        dw = _like(dw, "dw", w)
+    elif dw is not None:
+        raise ValueError("there is no dw without w")
+    d = _native.AddNorm8(n, F, F, 0, eps)
+    lib = _native.load()
+    if ws is None:
+        ws = torch.empty(lib.gnn_add_norm8_workspace_bytes(ctypes.byref(d), dt),
+                         dtype=torch.uint8, device=device) if w is not None else None
+    elif not isinstance(ws, torch.Tensor) or ws.dtype != torch.uint8 or ws.dim() != 1 or \
+            ws.device != device or not ws.is_contiguous():
+        raise ValueError(f"ws must be a one-dimensional uint8 tensor on {device}")
+    _launch(lib.gnn_add_norm8_backward, "gnn_add_norm8_backward", device, ctypes.byref(d), dt,
+            _at(y), _at(dy), _at(dz), _at(w), _at(dx), _at(dw), _at(ws),
+            0 if ws is None else ws.numel())
+    return dx, dw
+
+
+class AddNorm8(torch.autograd.Function):
+    """y, z = AddNorm8.apply(x, o, w, fmt, group, eps): z [N, ...] in x's dtype holds the
+    values that the 8 bits stand for, and its gradient passes their rounding unchanged
+    (training for 8-bit projections).  o None: z alone."""
+
+    @staticmethod
+    def forward(ctx, x, o, w, fmt, group, eps):
+        x, o, w = (None if t is None else t.contiguous() for t in (x, o, w))
+        y, z8 = add_norm8_forward(x, o, w, fmt, group, eps)
+        z = unpack8(z8, x.dtype).view(x.shape)
+        ctx.eps = eps
+        ctx.summed = o is not None
+        ctx.save_for_backward(x if o is None else y, w)
+        return z if o is None else (y, z)
+
+    @staticmethod
+    @once_differentiable
+    def backward(ctx, *grads):
+        y, w = ctx.saved_tensors
+        dy = grads[0].contiguous() if ctx.summed else None
+        dx, dw = add_norm8_backward(y, dy, grads[-1].contiguous(), w, ctx.eps)
+        return (dx, dx if ctx.summed else None, None if w is None else dw.to(w.dtype), None, None,
+                None)
+
+
 class Rope:
     """Frequencies of rotary positions: the first dim elements of a head vector are dim/2
     pairs, of elements i and i + dim/2 (layout "half") or 2 i and 2 i + 1
@@ -1117,7 +1256,12 @@ def transformer_layer(g: Graph, x: torch.Tensor, q: torch.Tensor, key: torch.Ten
     norm, gate, residual scale and sum with x, and the norm before the next
     layer.  Returns (y, z) as norm_residual_forward does.  checkpoint8: the
     attention keeps 8-bit checkpoints of q, key and val for its backward pass
-    instead of the tensors.  rope and pos [N] int32: rotary positions of q and key
+    instead of the tensors.  rope and pos [N] int32: the sum with the residual and its root-mean-square norm in 8 bits, for a projection's input:
+
+    y, z8 = add_norm8_forward(x, o, w, fmt="e4m3", group=128)   # z8: values and scales
+    dx, dw = add_norm8_backward(y, dy, dz, w)
+
+rotary positions of q and key
     before the attention.  To capture a training step into a CUDA graph, let no
     eager autograd graph of the same leaves be alive (torch would order the
     captured gradients behind the eager stream)."""

@@ -20,6 +20,7 @@ ERR_WORKSPACE_TOO_SMALL, ERR_CUDA, ERR_DEVICE_ASSERT, ERR_TIMEOUT = 4, 5, 6, 7
 F32, BF16 = 0, 1
 NORMS = {"sum": 0, "mean": 1, "sym": 2}  # gnn_norm
 REDUCE_OPS = {"max": 0, "min": 1}        # gnn_reduce_op
+EIGHTS = {"int8": 0, "e4m3": 1}          # gnn_eight
 ROPE_LAYOUTS = {"half": 0, "interleaved": 1}  # gnn_rope_layout
 ROPE_SCALINGS = {None: 0, "linear": 1, "ntk": 2, "yarn": 3}  # gnn_rope_scaling
 ROWNORMS = {"none": 0, "rms": 1, "layer": 2}  # gnn_rownorm
@@ -79,6 +80,10 @@ SIGNATURES = [
     ("gnn_norm_residual_forward", _I32, [_P, _I32, _P, _P, _P, _P, _P, _P]),
     ("gnn_norm_residual_workspace_bytes", _SZ, [_P, _I32]),
     ("gnn_norm_residual_backward", _I32, [_P, _I32, _P, _P, _P, _P, _P, _P, _P, _SZ, _P]),
+    ("gnn_add_norm8_forward", _I32, [_P, _I32, _P, _P, _P, _P, _P, _P, _P]),
+    ("gnn_add_norm8_workspace_bytes", _SZ, [_P, _I32]),
+    ("gnn_add_norm8_backward", _I32, [_P, _I32, _P, _P, _P, _P, _P, _P, _P, _SZ, _P]),
+    ("gnn_unpack8_groups", _I32, [_I64, _I32, _I32, _I32, _P, _P, _P, _P]),
     ("gnn_rope_frequencies", _I32, [_I32, _D, _I32, _D, _D, _D, _D, _P, _P]),
     ("gnn_rope_prepare", _I32, [_I32, _I32, _P, _F, _P]),
     ("gnn_rope_apply", _I32, [_P, _I32, _I64, _I32, _P, _I32, _P, _I32, _P]),
@@ -113,6 +118,10 @@ class NormResidual(ctypes.Structure):  # gnn_norm_residual, its parameters in li
 class NormGrads(ctypes.Structure):
     _fields_ = [(k, _P) for k in ("dx", "dout", "dgate", "dw_post", "db_post", "dscale", "dw_pre",
                                   "db_pre")]
+
+
+class AddNorm8(ctypes.Structure):  # gnn_add_norm8
+    _fields_ = [("n", _I64), ("F", _I32), ("group", _I32), ("fmt", _I32), ("eps", _F)]
 
 
 ROPE_MAX_DIM = 256  # GNN_ROPE_MAX_DIM

@@ -1,5 +1,5 @@
 // C-ABI entry points of the operators round a layer's projections (rotary
-// positions): argument checks, then the launchers.
+// positions, 8-bit norms): argument checks, then the launchers.
 #include <math.h>
 
 #include "api_util.h"
@@ -13,6 +13,21 @@ namespace {
 bool dtype_ok(gnn_dtype dt) { return dt == GNN_F32 || dt == GNN_BF16; }
 
 bool rope_dim_ok(int dim) { return dim >= 2 && dim <= GNN_ROPE_MAX_DIM && dim % 2 == 0; }
+
+bool eight_ok(gnn_eight f) { return f == GNN_INT8 || f == GNN_E4M3; }
+
+gnn_status add_norm8_check(const gnn_add_norm8* d, gnn_dtype dt) {
+  if (!d || !dtype_ok(dt) || !eight_ok(d->fmt) || d->n < 0 || d->n >= (int64_t(1) << 31) ||
+      d->F < 1 || d->group < 1 || d->group > d->F || d->F % d->group || !(d->eps >= 1e-30f) ||
+      d->eps > 3.0e38f)
+    return GNN_ERR_INVALID_ARG;
+  const int s = dt == GNN_F32 ? 4 : 2;
+  if (d->F > 32768 / s || d->F * s % 16) return GNN_ERR_UNSUPPORTED;
+  const int bytes = d->group * s;
+  if (d->group != d->F && (bytes < 16 || bytes > 512 || (bytes & (bytes - 1))))
+    return GNN_ERR_UNSUPPORTED;
+  return GNN_OK;
+}
 
 // Rows of D elements at these strides lie apart: heads inside nodes, or nodes
 // inside heads.  (A single node's or head's stride is of no account.)
@@ -136,6 +151,60 @@ gnn_status gnn_rope_apply(const gnn_rope* rope, int inverse, int64_t n, int D, c
   const int width = int(all & (~all + 1));  // the lowest bit set: at most 16
   return from_cuda(gnn::launch_rope(*rope, inverse, n, D, pos, count, t, dtype, width,
                                     static_cast<cudaStream_t>(stream)));
+}
+
+gnn_status gnn_add_norm8_forward(const gnn_add_norm8* d, gnn_dtype dtype, const void* x,
+                                 const void* o, const float* w, void* y, void* values,
+                                 float* scale, void* stream) {
+  const gnn_status r = add_norm8_check(d, dtype);
+  if (r != GNN_OK) return r;
+  if (d->n == 0) return GNN_OK;
+  if (!x || !values || !scale || (o != nullptr) != (y != nullptr)) return GNN_ERR_INVALID_ARG;
+  if (!aligned(x, 16) || !aligned(o, 16) || !aligned(w, 16) || !aligned(y, 16) ||
+      !aligned(values, 16) || !aligned(scale, 4))
+    return GNN_ERR_INVALID_ARG;
+  return from_cuda(gnn::launch_add_norm8_forward(*d, dtype, x, o, w, y, values, scale,
+                                                 static_cast<cudaStream_t>(stream)));
+}
+
+size_t gnn_add_norm8_workspace_bytes(const gnn_add_norm8* d, gnn_dtype dtype) {
+  return add_norm8_check(d, dtype) == GNN_OK ? gnn::add_norm8_ws_bytes(*d, dtype) : 0;
+}
+
+gnn_status gnn_add_norm8_backward(const gnn_add_norm8* d, gnn_dtype dtype, const void* y,
+                                  const void* dy, const void* dz, const float* w, void* dx,
+                                  float* dw, void* ws, size_t ws_bytes, void* stream) {
+  const gnn_status r = add_norm8_check(d, dtype);
+  if (r != GNN_OK) return r;
+  if (!aligned(w, 16) || !aligned(dw, 4)) return GNN_ERR_INVALID_ARG;
+  if (d->n == 0)
+    return dw ? from_cuda(cudaMemsetAsync(dw, 0, size_t(d->F) * sizeof(float),
+                                          static_cast<cudaStream_t>(stream)))
+              : GNN_OK;
+  if (!y || !dz || !dx || !aligned(y, 16) || !aligned(dy, 16) || !aligned(dz, 16) ||
+      !aligned(dx, 16))
+    return GNN_ERR_INVALID_ARG;
+  if (dw) {
+    if (ws_bytes < gnn::add_norm8_ws_bytes(*d, dtype)) return GNN_ERR_WORKSPACE_TOO_SMALL;
+    if (!ws || !aligned(ws, 256)) return GNN_ERR_INVALID_ARG;
+  }
+  return from_cuda(gnn::launch_add_norm8_backward(*d, dtype, y, dy, dz, w, dx, dw,
+                                                  static_cast<char*>(ws),
+                                                  static_cast<cudaStream_t>(stream)));
+}
+
+gnn_status gnn_unpack8_groups(int64_t groups, int group, gnn_eight fmt, gnn_dtype dtype,
+                              const void* values, const float* scale, void* x, void* stream) {
+  if (!eight_ok(fmt) || !dtype_ok(dtype) || groups < 0 || group < 1 || group > (1 << 24) ||
+      groups > (int64_t(1) << 42) / group)
+    return GNN_ERR_INVALID_ARG;
+  if (group % (dtype == GNN_F32 ? 4 : 8)) return GNN_ERR_UNSUPPORTED;
+  if (groups == 0) return GNN_OK;
+  if (!values || !scale || !x || !aligned(values, dtype == GNN_F32 ? 4 : 8) ||
+      !aligned(scale, 4) || !aligned(x, 16))
+    return GNN_ERR_INVALID_ARG;
+  return from_cuda(gnn::launch_unpack8_groups(groups, group, fmt, dtype, values, scale, x,
+                                              static_cast<cudaStream_t>(stream)));
 }
 
 }  // extern "C"

@@ -222,6 +222,18 @@ cudaError_t launch_norm_residual_backward(const gnn_norm_residual& d, gnn_dtype 
                                           const void* dz, const gnn_norm_grads& grads, char* ws,
                                           cudaStream_t st);
 
+// Sum with the residual and root-mean-square norm in 8 bits (norm8.cu).
+size_t add_norm8_ws_bytes(const gnn_add_norm8& d, gnn_dtype dt);
+cudaError_t launch_add_norm8_forward(const gnn_add_norm8& d, gnn_dtype dt, const void* x,
+                                     const void* o, const float* w, void* y, void* values,
+                                     float* scale, cudaStream_t st);
+cudaError_t launch_add_norm8_backward(const gnn_add_norm8& d, gnn_dtype dt, const void* y,
+                                      const void* dy, const void* dz, const float* w, void* dx,
+                                      float* dw, char* ws, cudaStream_t st);
+cudaError_t launch_unpack8_groups(int64_t groups, int group, gnn_eight fmt, gnn_dtype dt,
+                                  const void* values, const float* scale, void* x,
+                                  cudaStream_t st);
+
 // Rotary positions (rope.cu): count tensors, `width` bytes an access (16, 8, 4 or 2).
 constexpr int kRopeMax = 8;  // tensors of one call
 cudaError_t launch_rope(const gnn_rope& rope, int inverse, int64_t n, int D, const int32_t* pos,

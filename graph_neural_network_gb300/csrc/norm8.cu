@@ -1,0 +1,617 @@
+// The sum with the residual and its root-mean-square norm in 8 bits, in one pass:
+//   y = x + o,  t = y w,  z = t / sqrt(mean(y^2) + eps)
+// with z as 8-bit values and a float scale for each group of a row.  The norm's
+// factor is the same for a whole row, so the values are those of t alone:
+//   s = max(max |t| / top, 2^-126),  values = t / s rounded to nearest, ties to even,
+//   scale = s / sqrt(mean(y^2) + eps)
+// and the row's sum of squares and the maxima are reduced together, after one look at
+// the data.  t is float32 (a sum and a product, each rounded once), and the exact
+// quotient t / s decides the rounding.  The sum of squares is float32; a row whose sum
+// overflows takes it again with y 2^-80.
+//
+// Backward (straight through the rounding), g = dz w, y^ = y rstd:
+//   dx = dy + rstd (g - y^ mean(g y^)),  dw = sum of dz y^ over the rows
+// with mean(g y^) = rstd mean(g y): both sums of a row are again taken together.
+// dw: float32 per thread over its rows, float64 over threads and blocks, fixed order.
+//
+// Bound: HBM.  3 s + 1 bytes an element forward (4 a group), 4 s backward.
+//
+// A row of up to 128 16-byte vectors is one warp's (a sub-group's where it is
+// narrower than 32), up to four vectors a lane and no barrier; a wider one is a
+// block's, one barrier a row.  Forward, blocks do not loop: the loads of the next
+// rows in flight are those of the other blocks on the SM.  Backward, blocks stay and
+// keep their sums of dw, and load the next row before they work on the present one.
+#include "quant8.cuh"
+
+namespace gnn {
+namespace {
+
+constexpr float kInf = __builtin_huge_valf();
+constexpr float kDown = 8.271806125530277e-25f;  // 2^-80
+constexpr int kWideThreads = 512;                // most of a block that takes one row
+
+struct An8Args {
+  int64_t n;
+  int F, rv;          // elements and 16-byte vectors of a row
+  int tpr_log2;       // threads of a row that a warp takes
+  int gv_log2;        // vectors of a group; -1: the group is the row
+  float eps, inv_f;
+  const void *x, *o, *dz;  // backward: y, dy, dz
+  const float* w;
+  void *y, *dx;
+  uint8_t* values;
+  float* scale;
+  float* part;        // [blocks][F]
+};
+
+// The place of a thread: NV vectors of R rows (one of the two is 1).
+template <int NV, int R, bool kWide>
+struct Spot {
+  int vec, step;       // the first vector, and from one to the next
+  int64_t row, stride; // the first row, and from one to the next
+  __device__ __forceinline__ explicit Spot(const An8Args& A) {
+    if (kWide) {
+      vec = threadIdx.x;
+      step = blockDim.x;
+      row = blockIdx.x;
+      stride = 0;
+    } else {
+      const int slots = kThreads >> A.tpr_log2;
+      vec = threadIdx.x & ((1 << A.tpr_log2) - 1);
+      step = 1 << A.tpr_log2;
+      row = int64_t(blockIdx.x) * (slots * R) + (threadIdx.x >> A.tpr_log2);
+      stride = slots;
+    }
+  }
+};
+
+// Sums of v and maxima of m over the threads of a row, on each of them.
+template <bool kWide, int S, int M>
+__device__ __forceinline__ void over_row(float (&v)[S], uint32_t (&m)[M], bool with_m,
+                                         int tpr_log2, float* buf) {
+  const int lanes = kWide ? 32 : 1 << tpr_log2;
+  for (int o = 1; o < lanes; o <<= 1) {
+#pragma unroll
+    for (int k = 0; k < S; ++k) v[k] += __shfl_xor_sync(kFull, v[k], o);
+    if (with_m)
+#pragma unroll
+      for (int k = 0; k < M; ++k) m[k] = max(m[k], __shfl_xor_sync(kFull, m[k], o));
+  }
+  if constexpr (kWide) {
+    constexpr int kMost = kWideThreads / 32;
+    const int wid = threadIdx.x >> 5, warps = blockDim.x >> 5;
+    if ((threadIdx.x & 31) == 0) {
+#pragma unroll
+      for (int k = 0; k < S; ++k) buf[k * kMost + wid] = v[k];
+      if (with_m)
+#pragma unroll
+        for (int k = 0; k < M; ++k) buf[(S + k) * kMost + wid] = __uint_as_float(m[k]);
+    }
+    __syncthreads();
+#pragma unroll
+    for (int k = 0; k < S; ++k) {
+      v[k] = buf[k * kMost];
+      for (int w = 1; w < warps; ++w) v[k] += buf[k * kMost + w];
+    }
+    if (with_m)
+#pragma unroll
+      for (int k = 0; k < M; ++k)
+        for (int w = 0; w < warps; ++w)
+          m[k] = max(m[k], __float_as_uint(buf[(S + k) * kMost + w]));
+  }
+}
+
+template <typename T>
+__device__ __forceinline__ uint4 load_vec(const void* p, int64_t at, bool ok) {
+  return ok ? ld16(reinterpret_cast<const char*>(p) + 16 * at) : make_uint4(0, 0, 0, 0);
+}
+
+template <int V>
+__device__ __forceinline__ void load_w(const float* w, int vec, bool ok, float (&f)[V]) {
+#pragma unroll
+  for (int c = 0; c < V; c += 4) {
+    const float4 q = ok ? ld16f(w + vec * V + c) : make_float4(0.f, 0.f, 0.f, 0.f);
+    f[c] = q.x;
+    f[c + 1] = q.y;
+    f[c + 2] = q.z;
+    f[c + 3] = q.w;
+  }
+}
+
+template <int V>
+__device__ __forceinline__ uint32_t top_of(const float (&t)[V]) {
+  uint32_t m = 0;
+#pragma unroll
+  for (int c = 0; c < V; ++c) m = max(m, __float_as_uint(t[c]) & 0x7fffffffu);
+  return m;
+}
+
+// The thread's V values of t / s as bytes.
+template <bool kE4m3, int V>
+__device__ __forceinline__ void to_bytes(const float (&t)[V], float s, uint32_t (&w)[V / 4]) {
+  const float inv = reciprocal(s);
+  if constexpr (kE4m3) {
+    float r[V];
+    bool near = false;
+#pragma unroll
+    for (int c = 0; c < V; ++c) {
+      r[c] = t[c] * inv;
+      near |= near_border(r[c]);
+    }
+    if (near) {
+#pragma unroll
+      for (int c = 0; c < V; ++c)
+        if (near_border(r[c])) r[c] = off_border(r[c], t[c], s);
+    }
+#pragma unroll
+    for (int c = 0; c < V; c += 4)
+      w[c / 4] = e4m3x2(r[c], r[c + 1]) | e4m3x2(r[c + 2], r[c + 3]) << 16;
+  } else {
+    float k[V], r[V];
+    const float half = 0.5f * s;
+    if (candidates<V>(t, s, inv, k, r) >= half) settle<V>(half, k, r);
+#pragma unroll
+    for (int c = 0; c < V; c += 4) w[c / 4] = low_bytes(&k[c]);
+  }
+}
+
+template <typename T, bool kE4m3, int NV, int R, bool kWide>
+__global__ void __launch_bounds__(kWide ? kWideThreads : kThreads)
+    an8_fwd(const An8Args A) {
+  static_assert(NV == 1 || R == 1, "one index runs over both");
+  constexpr int V = VecOf<T>::n, I = NV * R;
+  __shared__ float buf[kWide ? 2 * (kWideThreads / 32) : 1];
+  __shared__ float again[kWide ? 2 * (kWideThreads / 32) : 1];
+  const Spot<NV, R, kWide> P(A);
+  const bool by_row = A.gv_log2 < 0;
+  uint4 rx[I], ro[I];
+  bool ok[I];
+  int64_t at[I];
+#pragma unroll
+  for (int i = 0; i < I; ++i) {
+    const int vec = P.vec + (R == 1 ? i * P.step : 0);
+    const int64_t row = P.row + (R == 1 ? 0 : i * P.stride);
+    ok[i] = vec < A.rv && row < A.n;
+    at[i] = row * A.rv + vec;
+    rx[i] = load_vec<T>(A.x, at[i], ok[i]);
+    ro[i] = load_vec<T>(A.o, at[i], ok[i] && A.o);
+  }
+  float t[I][V], ss[R];
+  uint32_t top[I];
+#pragma unroll
+  for (int r = 0; r < R; ++r) ss[r] = 0.f;
+#pragma unroll
+  for (int i = 0; i < I; ++i) {
+    float o[V];
+    unpack<T>(rx[i], t[i]);
+    if (A.o) {
+      unpack<T>(ro[i], o);
+#pragma unroll
+      for (int c = 0; c < V; c += 2)
+        add2(t[i][c], t[i][c + 1], t[i][c], t[i][c + 1], o[c], o[c + 1]);
+      if (ok[i]) st16(reinterpret_cast<char*>(A.y) + 16 * at[i], pack<T>(t[i]));
+    }
+    ss[R == 1 ? 0 : i] += dot<V>(t[i], t[i]);
+    if (A.w) {
+      float w[V];
+      load_w<V>(A.w, P.vec + (R == 1 ? i * P.step : 0), ok[i], w);
+#pragma unroll
+      for (int c = 0; c < V; c += 2)
+        mul2v(t[i][c], t[i][c + 1], t[i][c], t[i][c + 1], w[c], w[c + 1]);
+    }
+    top[i] = top_of<V>(t[i]);
+  }
+  uint32_t whole[R];
+#pragma unroll
+  for (int r = 0; r < R; ++r) {
+    whole[r] = top[r];
+    if (R == 1)
+#pragma unroll
+      for (int i = 1; i < NV; ++i) whole[0] = max(whole[0], top[i]);
+  }
+  over_row<kWide>(ss, whole, by_row, A.tpr_log2, buf);
+  if (by_row) {
+#pragma unroll
+    for (int i = 0; i < I; ++i) top[i] = whole[R == 1 ? 0 : i];
+  } else {
+    for (int o = 1; o < (1 << A.gv_log2); o <<= 1)
+#pragma unroll
+      for (int i = 0; i < I; ++i) top[i] = max(top[i], __shfl_xor_sync(kFull, top[i], o));
+  }
+  // sums that are not finite: of y 2^-80 (all rows of the warp, or the block's, take part)
+  float pre[R], rstd[R];
+  bool any = false;
+#pragma unroll
+  for (int r = 0; r < R; ++r) any |= !(ss[r] < kInf);
+  if (kWide ? any : __any_sync(kFull, any)) {
+    float low[R];
+#pragma unroll
+    for (int r = 0; r < R; ++r) low[r] = 0.f;
+#pragma unroll
+    for (int i = 0; i < I; ++i) {
+      float y[V], o[V];
+      unpack<T>(load_vec<T>(A.x, at[i], ok[i]), y);
+      unpack<T>(load_vec<T>(A.o, at[i], ok[i] && A.o), o);
+#pragma unroll
+      for (int c = 0; c < V; ++c) y[c] = (y[c] + o[c]) * kDown;
+      low[R == 1 ? 0 : i] += dot<V>(y, y);
+    }
+    uint32_t none[1] = {0u};
+    over_row<kWide>(low, none, false, A.tpr_log2, again);
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+      const bool big = !(ss[r] < kInf);
+      pre[r] = big ? kDown : 1.f;
+      rstd[r] = big ? rsqrtf(fmaf(low[r], A.inv_f, A.eps * kDown * kDown))
+                    : rsqrtf(fmaf(ss[r], A.inv_f, A.eps));
+      if (big && !(low[r] < kInf)) rstd[r] = __int_as_float(0x7fc00000);
+    }
+  } else {
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+      pre[r] = 1.f;
+      rstd[r] = rsqrtf(fmaf(ss[r], A.inv_f, A.eps));
+    }
+  }
+  const int lead = by_row ? 0 : (1 << A.gv_log2) - 1;
+#pragma unroll
+  for (int i = 0; i < I; ++i) {
+    const int r = R == 1 ? 0 : i;
+    const bool finite = top[i] < 0x7f800000u && rstd[r] < kInf;
+    const float s = scale_of<kE4m3 ? 448 : 127>(__uint_as_float(top[i]));
+    uint32_t w[V / 4];
+    to_bytes<kE4m3, V>(t[i], s, w);
+    if (!ok[i]) continue;
+#pragma unroll
+    for (int c = 0; c < V / 4; ++c) w[c] = finite ? w[c] : 0u;
+    if constexpr (V == 8)
+      reinterpret_cast<uint2*>(A.values)[at[i]] = make_uint2(w[0], w[1]);
+    else
+      reinterpret_cast<uint32_t*>(A.values)[at[i]] = w[0];
+    const int vec = P.vec + (R == 1 ? i * P.step : 0);
+    const float scale = finite ? s * pre[r] * rstd[r] : __int_as_float(0x7fc00000);
+    if (by_row) {
+      if (vec == 0) A.scale[P.row + (R == 1 ? 0 : i * P.stride)] = scale;
+    } else if ((vec & lead) == 0) {
+      A.scale[at[i] >> A.gv_log2] = scale;
+    }
+  }
+}
+
+// Resident blocks of the backward pass that its grid is made for, on 152 SMs (a
+// constant: the workspace query asks no device).
+constexpr int kBwdBlocks = 152 * 2;
+
+template <typename T, int NV, bool kWide>
+__global__ void __launch_bounds__(kWide ? kWideThreads : kThreads)
+    an8_bwd(const An8Args A) {
+  constexpr int V = VecOf<T>::n;
+  __shared__ float buf[2][kWide ? 2 * (kWideThreads / 32) : 1];
+  extern __shared__ __align__(16) float sums[];  // [row slots][F] (rows of a warp)
+  const Spot<NV, 1, kWide> P(A);
+  const int slots = kWide ? 1 : kThreads >> A.tpr_log2;
+  const int64_t stride = int64_t(gridDim.x) * slots;
+  float acc[NV][V];
+#pragma unroll
+  for (int i = 0; i < NV; ++i) zero<V>(acc[i]);
+  int64_t row = P.row;
+  uint4 ry[NV], rd[NV], rz[NV];
+  const auto load = [&] {
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      const int vec = P.vec + i * P.step;
+      const bool ok = vec < A.rv && row < A.n;
+      const int64_t at = row * A.rv + vec;
+      ry[i] = load_vec<T>(A.x, at, ok);
+      rz[i] = load_vec<T>(A.dz, at, ok);
+      rd[i] = load_vec<T>(A.o, at, ok && A.o);
+    }
+  };
+  load();
+  int turn = 0;
+  // every thread of the block makes the same number of turns (barriers, shuffles)
+  for (int64_t r0 = int64_t(blockIdx.x) * slots; r0 < A.n; r0 += stride) {
+    float y[NV][V], z[NV][V], d[NV][V];
+    float q[2] = {0.f, 0.f};
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      unpack<T>(ry[i], y[i]);
+      unpack<T>(rz[i], z[i]);
+      unpack<T>(rd[i], d[i]);
+    }
+    const int64_t now = row;
+    row += stride;
+    load();
+    const auto weigh = [&](int i, float (&g)[V]) {  // g = dz w
+      if (A.w) {
+        const int vec = P.vec + i * P.step;
+        load_w<V>(A.w, vec, vec < A.rv, g);
+#pragma unroll
+        for (int c = 0; c < V; c += 2)
+          mul2v(g[c], g[c + 1], z[i][c], z[i][c + 1], g[c], g[c + 1]);
+      } else {
+#pragma unroll
+        for (int c = 0; c < V; ++c) g[c] = z[i][c];
+      }
+    };
+    const auto row_dots = [&] {
+      q[0] = q[1] = 0.f;
+#pragma unroll
+      for (int i = 0; i < NV; ++i) {
+        float g[V];
+        weigh(i, g);
+        q[0] += dot<V>(y[i], y[i]);
+        q[1] += dot<V>(g, y[i]);
+      }
+      uint32_t none[1] = {0u};
+      over_row<kWide>(q, none, false, A.tpr_log2, buf[turn & 1]);
+      ++turn;
+    };
+    row_dots();
+    float up = 1.f;  // rows whose sum of squares overflows: of y 2^-80
+    const bool big = !(q[0] < kInf);
+    if (kWide ? big : __any_sync(kFull, big)) {
+      up = big ? kDown : 1.f;
+#pragma unroll
+      for (int i = 0; i < NV; ++i) scale<V>(y[i], up);
+      row_dots();
+    }
+    const float rstd = rsqrtf(fmaf(q[0], A.inv_f, A.eps * up * up));
+    const float mean = q[1] * A.inv_f * rstd;  // of g y^
+    const float back = rstd * up;
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      float g[V];
+      weigh(i, g);
+      scale<V>(y[i], rstd);  // y^
+#pragma unroll
+      for (int c = 0; c < V; c += 2) {
+        fma2(acc[i][c], acc[i][c + 1], z[i][c], z[i][c + 1], y[i][c], y[i][c + 1]);
+        fma2(g[c], g[c + 1], y[i][c], y[i][c + 1], -mean, -mean);
+        fma2(d[i][c], d[i][c + 1], g[c], g[c + 1], back, back);
+      }
+      const int vec = P.vec + i * P.step;
+      if (vec < A.rv && now < A.n)
+        st16(reinterpret_cast<char*>(A.dx) + 16 * (now * A.rv + vec), pack<T>(d[i]));
+    }
+  }
+  let_next_start();
+  if (!A.part) return;
+  float* part = A.part + int64_t(blockIdx.x) * A.F;
+  if constexpr (kWide) {
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      const int vec = P.vec + i * P.step;
+      if (vec < A.rv)
+#pragma unroll
+        for (int c = 0; c < V; c += 4)
+          *reinterpret_cast<float4*>(part + vec * V + c) =
+              make_float4(acc[i][c], acc[i][c + 1], acc[i][c + 2], acc[i][c + 3]);
+    }
+  } else {
+    const int slot = threadIdx.x >> A.tpr_log2;
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      const int vec = P.vec + i * P.step;
+      if (vec < A.rv)
+#pragma unroll
+        for (int c = 0; c < V; ++c) sums[slot * A.F + vec * V + c] = acc[i][c];
+    }
+    __syncthreads();
+    for (int f = threadIdx.x; f < A.F; f += kThreads) {
+      double s = 0.0;
+      for (int k = 0; k < slots; ++k) s += double(sums[k * A.F + f]);
+      part[f] = float(s);
+    }
+  }
+}
+
+// dw from the blocks' sums in a fixed order: a block takes 32 channels in 32 slices of
+// the blocks.
+constexpr int kDwSlices = 32;
+__global__ void __launch_bounds__(kDwSlices * 32)
+    an8_dw(const float* part, int blocks, int F, float* dw) {
+  __shared__ double t[kDwSlices][33];
+  const int lane = threadIdx.x & 31, slice = threadIdx.x >> 5;
+  const int f = blockIdx.x * 32 + lane;
+  double s = 0.0;
+  grid_wait();
+  if (f < F) {
+    constexpr int kLoads = (kBwdBlocks + kDwSlices - 1) / kDwSlices;
+    float v[kLoads];
+#pragma unroll
+    for (int u = 0; u < kLoads; ++u) {
+      const int b = slice + u * kDwSlices;
+      v[u] = b < blocks ? part[int64_t(b) * F + f] : 0.f;
+    }
+#pragma unroll
+    for (int u = 0; u < kLoads; ++u) s += double(v[u]);
+  }
+  t[slice][lane] = s;
+  __syncthreads();
+  if (slice != 0 || f >= F) return;
+  double all = 0.0;
+#pragma unroll
+  for (int k = 0; k < kDwSlices; ++k) all += t[k][lane];
+  dw[f] = float(all);
+}
+
+An8Args an8_args(const gnn_add_norm8& d, gnn_dtype dt) {
+  An8Args A{};
+  const int s = dt == GNN_F32 ? 4 : 2;
+  A.n = d.n;
+  A.F = d.F;
+  A.rv = d.F * s / 16;
+  while ((1 << A.tpr_log2) < A.rv && A.tpr_log2 < 5) ++A.tpr_log2;
+  A.gv_log2 = -1;
+  if (d.group != d.F) {
+    A.gv_log2 = 0;
+    while ((16 << A.gv_log2) < d.group * s) ++A.gv_log2;
+  }
+  A.eps = d.eps;
+  A.inv_f = 1.f / float(d.F);
+  return A;
+}
+
+// Vectors a thread holds: of a warp's row, or of a block's; the block's threads.
+int warp_vecs(int rv) { return rv <= 32 ? 1 : rv <= 64 ? 2 : 4; }
+constexpr int kWarpVecs = 128;  // rows of at most so many are a warp's
+int block_threads(int rv, int nv) { return ((rv + nv - 1) / nv + 31) / 32 * 32; }
+int fwd_vecs(int rv) { return rv <= 256 ? 1 : rv <= 512 ? 2 : 4; }
+int bwd_vecs(int rv) { return rv <= 256 ? 1 : rv <= 1024 ? 2 : 4; }
+
+template <typename T, bool kE4m3, int NV, int R, bool kWide>
+cudaError_t fwd(const An8Args& A, cudaStream_t st) {
+  const int64_t rows = kWide ? 1 : int64_t(kThreads >> A.tpr_log2) * R;
+  const int threads = kWide ? block_threads(A.rv, NV) : kThreads;
+  an8_fwd<T, kE4m3, NV, R, kWide>
+      <<<unsigned((A.n + rows - 1) / rows), threads, 0, st>>>(A);
+  return cudaGetLastError();
+}
+
+template <typename T, bool kE4m3>
+cudaError_t fwd_t(const An8Args& A, cudaStream_t st) {
+  if (A.rv > kWarpVecs) {
+    const int nv = fwd_vecs(A.rv);
+    return nv == 1   ? fwd<T, kE4m3, 1, 1, true>(A, st)
+           : nv == 2 ? fwd<T, kE4m3, 2, 1, true>(A, st)
+                     : fwd<T, kE4m3, 4, 1, true>(A, st);
+  }
+  const int nv = warp_vecs(A.rv);
+  return nv == 1   ? fwd<T, kE4m3, 1, 2, false>(A, st)
+         : nv == 2 ? fwd<T, kE4m3, 2, 1, false>(A, st)
+                   : fwd<T, kE4m3, 4, 1, false>(A, st);
+}
+
+// Blocks of the backward pass: at most kBwdBlocks, at least four rows a slot.
+int bwd_blocks(const An8Args& A) {
+  const int64_t slots = A.rv > kWarpVecs ? 1 : kThreads >> A.tpr_log2;
+  const int64_t want = (A.n + slots * 4 - 1) / (slots * 4);
+  return want < 1 ? 1 : want < kBwdBlocks ? int(want) : kBwdBlocks;
+}
+
+template <typename T, int NV, bool kWide>
+cudaError_t bwd(const An8Args& A, int blocks, cudaStream_t st) {
+  const int threads = kWide ? block_threads(A.rv, NV) : kThreads;
+  const size_t smem = kWide || !A.part ? 0 : size_t(kThreads >> A.tpr_log2) * A.F * 4;
+  an8_bwd<T, NV, kWide><<<unsigned(blocks), threads, smem, st>>>(A);
+  return cudaGetLastError();
+}
+
+template <typename T>
+cudaError_t bwd_t(const An8Args& A, int blocks, cudaStream_t st) {
+  if (A.rv > kWarpVecs) {
+    const int nv = bwd_vecs(A.rv);
+    return nv == 1   ? bwd<T, 1, true>(A, blocks, st)
+           : nv == 2 ? bwd<T, 2, true>(A, blocks, st)
+                     : bwd<T, 4, true>(A, blocks, st);
+  }
+  const int nv = warp_vecs(A.rv);
+  return nv == 1   ? bwd<T, 1, false>(A, blocks, st)
+         : nv == 2 ? bwd<T, 2, false>(A, blocks, st)
+                   : bwd<T, 4, false>(A, blocks, st);
+}
+
+// values * scale as T: 16 bytes of T a step, kSteps of them in flight.
+constexpr int kSteps = 4;
+
+template <typename T, bool kE4m3>
+__global__ void __launch_bounds__(kThreads)
+    unpack8_groups(const uint8_t* values, const float* scale, int64_t vecs, uint64_t div, void* x) {
+  constexpr int E = VecOf<T>::n;
+  const int64_t first = int64_t(blockIdx.x) * (kSteps * kThreads) + threadIdx.x;
+  uint32_t w[kSteps][E / 4];
+  float s[kSteps];
+#pragma unroll
+  for (int u = 0; u < kSteps; ++u) {
+    const int64_t v = first + u * kThreads;
+    if (v >= vecs) break;
+    if constexpr (E == 8) {
+      const uint2 t = __ldg(reinterpret_cast<const uint2*>(values) + v);
+      w[u][0] = t.x;
+      w[u][1] = t.y;
+    } else {
+      w[u][0] = __ldg(reinterpret_cast<const uint32_t*>(values) + v);
+    }
+    s[u] = __ldg(scale + (div ? int64_t(__umul64hi(uint64_t(v), div)) : v));
+  }
+#pragma unroll
+  for (int u = 0; u < kSteps; ++u) {
+    const int64_t v = first + u * kThreads;
+    if (v >= vecs) break;
+    float e[E];
+#pragma unroll
+    for (int c = 0; c < E; c += 4) {
+      if constexpr (kE4m3) {
+        widen_e4m3(w[u][c / 4] & 0xffffu, e[c], e[c + 1]);
+        widen_e4m3(w[u][c / 4] >> 16, e[c + 2], e[c + 3]);
+      } else {
+        widen8(w[u][c / 4], &e[c]);
+      }
+    }
+    gnn::scale<E>(e, s[u]);
+    st16(reinterpret_cast<char*>(x) + 16 * v, pack<T>(e));
+  }
+}
+
+}  // namespace
+
+size_t add_norm8_ws_bytes(const gnn_add_norm8& d, gnn_dtype dt) {
+  return align_up(size_t(bwd_blocks(an8_args(d, dt))) * d.F * 4, 256);
+}
+
+cudaError_t launch_add_norm8_forward(const gnn_add_norm8& d, gnn_dtype dt, const void* x,
+                                     const void* o, const float* w, void* y, void* values,
+                                     float* scale, cudaStream_t st) {
+  An8Args A = an8_args(d, dt);
+  A.x = x;
+  A.o = o;
+  A.w = w;
+  A.y = y;
+  A.values = static_cast<uint8_t*>(values);
+  A.scale = scale;
+  const bool e = d.fmt == GNN_E4M3;
+  if (dt == GNN_F32) return e ? fwd_t<float, true>(A, st) : fwd_t<float, false>(A, st);
+  return e ? fwd_t<__nv_bfloat16, true>(A, st) : fwd_t<__nv_bfloat16, false>(A, st);
+}
+
+cudaError_t launch_add_norm8_backward(const gnn_add_norm8& d, gnn_dtype dt, const void* y,
+                                      const void* dy, const void* dz, const float* w, void* dx,
+                                      float* dw, char* ws, cudaStream_t st) {
+  An8Args A = an8_args(d, dt);
+  A.x = y;
+  A.o = dy;
+  A.dz = dz;
+  A.w = w;
+  A.dx = dx;
+  A.part = dw ? reinterpret_cast<float*>(ws) : nullptr;
+  const int blocks = bwd_blocks(A);
+  const cudaError_t e =
+      dt == GNN_F32 ? bwd_t<float>(A, blocks, st) : bwd_t<__nv_bfloat16>(A, blocks, st);
+  if (e != cudaSuccess || !dw) return e;
+  return launch_after(an8_dw, dim3(unsigned((d.F + 31) / 32)), kDwSlices * 32, 0, st, A.part,
+                      blocks, d.F, dw);
+}
+
+cudaError_t launch_unpack8_groups(int64_t groups, int group, gnn_eight fmt, gnn_dtype dt,
+                                  const void* values, const float* scale, void* x,
+                                  cudaStream_t st) {
+  const int per = group / (dt == GNN_F32 ? 4 : 8);  // vectors of a group
+  const int64_t vecs = groups * per;
+  // v / per for v < 2^40 or so: the multiple of ceil(2^64 / per) is off by v per / 2^64
+  const uint64_t div = per == 1 ? 0 : ~uint64_t(0) / uint64_t(per) + 1;
+  const int64_t blocks = (vecs + kSteps * kThreads - 1) / (kSteps * kThreads);
+  if (blocks > 0x7fffffff) return cudaErrorInvalidValue;
+  const uint8_t* v = static_cast<const uint8_t*>(values);
+  const unsigned g = unsigned(blocks);
+  const bool e = fmt == GNN_E4M3;
+  if (dt == GNN_F32)
+    (e ? unpack8_groups<float, true> : unpack8_groups<float, false>)<<<g, kThreads, 0, st>>>(
+        v, scale, vecs, div, x);
+  else
+    (e ? unpack8_groups<__nv_bfloat16, true>
+       : unpack8_groups<__nv_bfloat16, false>)<<<g, kThreads, 0, st>>>(v, scale, vecs, div, x);
+  return cudaGetLastError();
+}
+
+}  // namespace gnn

@@ -19,7 +19,7 @@
 // group of lanes by shuffles; rows are contiguous, so the tensor is one stream.
 // 1M x 128 bfloat16, three tensors: 197 us, 6.3 TB/s (288 us with a division and a
 // rounding per element).
-#include "device.cuh"
+#include "quant8.cuh"
 
 namespace gnn {
 namespace {
@@ -31,8 +31,6 @@ struct Pack8Args {
   int8_t* x8[kPack8Max];
   float* s[kPack8Max];
 };
-
-constexpr float kWhole = 12582912.f;  // 1.5 * 2^23: adding it rounds to a whole number
 
 // Magnitude bits (infinities and NaN above all numbers) of the largest element.
 template <typename T>
@@ -51,36 +49,6 @@ __device__ __forceinline__ uint32_t top_bits<__nv_bfloat16>(const uint4& r) {
   };
   const uint32_t m = two(two(r.x, r.y), two(r.z, r.w));
   return max(m << 16, m & 0xffff0000u);
-}
-
-// max(top / 127, 2^-126).  The quotient is correctly rounded (Markstein 1990,
-// "Computation of elementary functions on the IBM RISC System/6000": with c the
-// rounded reciprocal and q within one step, q + (a - b q) c rounds to a / b);
-// quotients below 2^-126, where the residue is not exact, give way to the bound.
-__device__ __forceinline__ float scale_of(float top) {
-  const float c = 0.007874015748031496f;
-  const float q = __fmul_rn(top, c);
-  return fmaxf(__fmaf_rn(__fmaf_rn(-127.f, q, top), c, q), 1.17549435e-38f);
-}
-
-// Candidates t[k] (whole numbers plus kWhole) for the quotients x / s, and the
-// largest residue.
-template <int V>
-__device__ __forceinline__ float candidates(const float (&x)[V], float s, float inv,
-                                            float (&t)[V], float (&r)[V]) {
-  float most = 0.f;
-#pragma unroll
-  for (int c = 0; c < V; c += 2) {
-    t[c] = t[c + 1] = kWhole;
-    fma2(t[c], t[c + 1], x[c], x[c + 1], inv, inv);
-    float q0, q1;
-    add2(q0, q1, t[c], t[c + 1], -kWhole, -kWhole);
-    r[c] = x[c];
-    r[c + 1] = x[c + 1];
-    fma2(r[c], r[c + 1], q0, q1, -s, -s);
-    most = fmaxf(most, fmaxf(fabsf(r[c]), fabsf(r[c + 1])));
-  }
-  return most;
 }
 
 template <typename T>
@@ -110,28 +78,16 @@ __global__ void __launch_bounds__(kThreads) pack8_rows(const __grid_constant__ P
     for (int u = 0; u < U; ++u) {
       const int64_t v = v0 + u * kThreads + threadIdx.x;
       const bool finite = top[u] < 0x7f800000u;
-      const float s = scale_of(__uint_as_float(top[u]));
+      const float s = scale_of<127>(__uint_as_float(top[u]));
       float inv;
       asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(inv) : "f"(s));
       float e[V], t[V], r[V];
       unpack<T>(raw[u], e);
       const float half = 0.5f * s;
-      if (candidates<V>(e, s, inv, t, r) >= half) {
-#pragma unroll
-        for (int c = 0; c < V; ++c) {
-          const float a = fabsf(r[c]);
-          if (a > half || (a == half && (__float_as_uint(t[c]) & 1)))
-            t[c] += r[c] > 0.f ? 1.f : -1.f;
-        }
-      }
-      // the low byte of whole + kWhole is the whole number's
+      if (candidates<V>(e, s, inv, t, r) >= half) settle<V>(half, t, r);
       uint32_t w[V / 4];
 #pragma unroll
-      for (int c = 0; c < V / 4; ++c) {
-        const uint32_t a = __byte_perm(__float_as_uint(t[4 * c]), __float_as_uint(t[4 * c + 1]), 0x0040);
-        const uint32_t b = __byte_perm(__float_as_uint(t[4 * c + 2]), __float_as_uint(t[4 * c + 3]), 0x0040);
-        w[c] = finite ? __byte_perm(a, b, 0x5410) : 0u;
-      }
+      for (int c = 0; c < V / 4; ++c) w[c] = finite ? low_bytes(&t[4 * c]) : 0u;
       if (v >= A.vecs) continue;
       if constexpr (V == 8)
         reinterpret_cast<uint2*>(x8)[v] = make_uint2(w[0], w[1]);

@@ -514,6 +514,57 @@ gnn_status gnn_norm_residual_backward(const gnn_norm_residual* d, gnn_dtype dtyp
                                       const void* dz, const gnn_norm_grads* grads, void* ws,
                                       size_t ws_bytes, void* stream);
 
+/* ---- Sum with the residual and root-mean-square norm in 8 bits -----------------
+ *
+ * The input of a projection in 8 bits, in one pass over the rows: per row of F
+ * elements
+ *     y = x + o,  t = y * w,  z = t / sqrt(mean(y^2) + eps)
+ * with z in 8-bit values and a float scale for each group of `group` elements, which
+ * stand for values * scale:
+ *     s = max(max |t| / top, 2^-126) over the group (top 127 or 448),
+ *     values = t / s rounded to the nearest, ties to even (the exact quotient of the
+ *     float32 t and s decides), scale = s / sqrt(mean(y^2) + eps).
+ * GNN_INT8: as gnn_pack8 packs t.  GNN_E4M3: sign, four bits of exponent, three of
+ * mantissa, largest 448, no infinity.  A group is the row (group = F), or group *
+ * sizeof(dtype) is 16 bytes times a power of two up to 512 and group divides F.
+ * A row with an infinity or NaN in x + o, or a group with one in t, gets scale
+ * NaN and values 0: it reads back as NaN.
+ * F * sizeof(dtype) a multiple of 16, at most 32768 bytes.  x, o, y: dtype
+ * [n][F], 16-byte aligned; o null: y is x and is not written (y null).  w: float
+ * [F], 16-byte aligned, or null (1).  values: [n][F] bytes, 16-byte aligned; scale:
+ * [n][F / group].  Arithmetic in float32, y rounded once (z comes from the unrounded
+ * one).  No output may overlap an input.  Asynchronous on `stream`; bitwise
+ * reproducible. */
+typedef enum { GNN_INT8 = 0, GNN_E4M3 = 1 } gnn_eight;
+
+typedef struct {
+  int64_t n;
+  int32_t F, group;
+  gnn_eight fmt;
+  float eps; /* 1e-30 to 3e38 */
+} gnn_add_norm8;
+
+gnn_status gnn_add_norm8_forward(const gnn_add_norm8* d, gnn_dtype dtype, const void* x,
+                                 const void* o, const float* w, void* y, void* values,
+                                 float* scale, void* stream);
+
+/* Workspace of the backward pass (host only; 0 for an unsupported shape). */
+size_t gnn_add_norm8_workspace_bytes(const gnn_add_norm8* d, gnn_dtype dtype);
+
+/* Gradients with the rounding to 8 bits taken as the identity: dz [n][F] dtype, of
+ * the values that z stands for; dy [n][F] dtype, what reaches y past the norm (null:
+ * nothing); y as the forward stored it.  dx: the gradient of x and of o, every element
+ * written; dw [F]: of w, null where not wanted (ws may then be null). */
+gnn_status gnn_add_norm8_backward(const gnn_add_norm8* d, gnn_dtype dtype, const void* y,
+                                  const void* dy, const void* dz, const float* w, void* dx,
+                                  float* dw, void* ws, size_t ws_bytes, void* stream);
+
+/* x = values * scale, rounded to dtype: `groups` groups of `group` values with a scale
+ * each.  group * sizeof(dtype) a multiple of 16; values 8-byte (bfloat16) or 4-byte
+ * aligned, x 16. */
+gnn_status gnn_unpack8_groups(int64_t groups, int group, gnn_eight fmt, gnn_dtype dtype,
+                              const void* values, const float* scale, void* x, void* stream);
+
 /* ---- Rotary positions --------------------------------------------------------
  *
  * Nodes that lie along a sequence can carry their positions in q and key
