@@ -47,6 +47,14 @@ the sum with the residual and its root-mean-square norm in 8 bits, for a project
     y, z8 = add_norm8_forward(x, o, w, fmt="e4m3", group=128)   # z8: values and scales
     dx, dw = add_norm8_backward(y, dy, dz, w)
 
+tokens in the order of the experts that a router chose, and back:
+
+    plan = Experts(ids, num_experts, align=128)        # ids [N, K]; stays on the device
+    xs = expert_dispatch_forward(plan, x)              # expert e: rows offsets[e] ...
+    y = expert_combine_forward(plan, ys, weights, residual)
+    dys, dweights = expert_combine_backward(plan, dy, ys, weights)
+    dx = expert_dispatch_backward(plan, dxs)
+
 rotary positions of q and key (views of a fused projection [N, 3, H, D] as they are):
 
     rope = Rope(D, "half", scaling="yarn", factor=8, length=4096)     # once
@@ -87,7 +95,9 @@ __all__ = ["Graph", "gat_forward", "gat_backward", "GATAggregate", "GnnError", "
            "norm_residual_backward", "NormResidual", "Packed8", "pack8", "unpack8",
            "transformer_backward8", "TransformerCheckpoint8", "transformer_layer", "Rope",
            "rope_forward", "rope_backward", "RotaryPositions", "add_norm8_forward",
-           "add_norm8_backward", "AddNorm8"]
+           "add_norm8_backward", "AddNorm8", "Experts", "expert_dispatch_forward",
+           "expert_dispatch_backward", "expert_combine_forward", "expert_combine_backward",
+           "ExpertDispatch", "ExpertCombine", "expert_layer"]
 
 
 def _ptr(t):
@@ -1121,6 +1131,201 @@ class AddNorm8(torch.autograd.Function):
                 None)
 
 
+class Experts:
+    """The order of tokens by expert: a plan for the calls that take their rows there
+    and back, made on the device without waiting for it.
+
+    ids [N, K] or [N] int32 or int64: the experts that each token (node) chose; one
+    outside [0, num_experts) drops its choice.  Expert e has the rows offsets[e] to
+    offsets[e] + counts[e], its tokens in their order, and the next segment starts at a
+    multiple of align.  Tensors (int32, views of the plan's buffer): offsets
+    [num_experts + 1], counts [num_experts], order [rows] (the pair n K + k of a row, -1
+    for padding) and slots [N, K] (the row of a pair, -1 where dropped).  rows holds
+    every pair and the most padding there can be.  ids are not kept."""
+
+    @_on_stream
+    def __init__(self, ids: torch.Tensor, num_experts: int, align: int = 1):
+        lib = _native.load()
+        if not isinstance(ids, torch.Tensor) or ids.dim() not in (1, 2) or not ids.is_cuda:
+            raise ValueError("ids must be a CUDA tensor [N, K] or [N]")
+        if ids.dtype not in (torch.int32, torch.int64):
+            raise TypeError(f"ids must be int32 or int64, got {ids.dtype}")
+        if not ids.is_contiguous():
+            raise ValueError("ids must be contiguous")
+        n, K = ids.shape if ids.dim() == 2 else (ids.shape[0], 1)
+        size = (n, K, num_experts, align)
+        nb = lib.gnn_experts_buffer_bytes(*size)
+        if nb == 0:
+            raise ValueError(f"{num_experts} experts, {K} choices of {n} tokens and align {align} "
+                             "are out of range (1 to 1024, 1 to 64, rows below 2^31, 1 to 65536)")
+        self.device = ids.device
+        self.tokens, self.choices, self.num_experts, self.align = size
+        self.buffer = torch.empty(nb, dtype=torch.uint8, device=self.device)
+        self._c = _native.Experts()
+
+        def prepare(s):
+            return lib.gnn_experts_prepare(_at(ids), ids.element_size(), *size, _at(self.buffer),
+                                           nb, s, ctypes.byref(self._c))
+
+        _launch(prepare, "gnn_experts_prepare", self.device)
+        self._ref = ctypes.byref(self._c)
+        self._lib = lib
+        self.rows = self._c.rows
+
+    def _view(self, at, *shape):
+        off = at - self.buffer.data_ptr()
+        return self.buffer[off:off + 4 * math.prod(shape)].view(torch.int32).view(shape)
+
+    @property
+    def offsets(self):
+        return self._view(self._c.offsets, self.num_experts + 1)
+
+    @property
+    def counts(self):
+        return self._view(self._c.counts, self.num_experts)
+
+    @property
+    def order(self):
+        return self._view(self._c.order, self.rows)
+
+    @property
+    def slots(self):
+        return self._view(self._c.slots, self.tokens, self.choices)
+
+
+def _expert_rows(plan, x, name, kind):
+    """Raise unless x is contiguous on the plan's device, with a row for each of its
+    `kind` ("tokens" or "rows"); its rows' width."""
+    if not isinstance(plan, Experts):
+        raise TypeError(f"plan must be Experts, got {type(plan).__name__}")
+    n = getattr(plan, kind)
+    rows, F = _rows(x, name)
+    if rows != n:
+        raise ValueError(f"{name} must have {n} rows, got {rows}")
+    if x.device != plan.device:
+        raise ValueError(f"{name} must be on the plan's device {plan.device}, got {x.device}")
+    return F
+
+
+def _expert_weights(plan, weights):
+    if weights is None:
+        return None
+    if not isinstance(weights, torch.Tensor) or not weights.is_floating_point():
+        raise TypeError("weights must be a floating-point tensor")
+    if weights.dtype is not torch.float32:
+        weights = weights.to(torch.float32)
+    shape = weights.shape if weights.shape == (plan.tokens,) and plan.choices == 1 else \
+        (plan.tokens, plan.choices)
+    return _plain_tensor(weights, "weights", shape, torch.float32, plan.device)
+
+
+def _dispatch_rows(plan, x, name, out):
+    F = _expert_rows(plan, x, name, "tokens")
+    out = _output(out, "out", (plan.rows, *x.shape[1:]), x.dtype, plan.device)
+    _launch(plan._lib.gnn_expert_dispatch, "gnn_expert_dispatch", plan.device, plan._ref,
+            F * x.element_size(), _at(x), _at(out))
+    return out
+
+
+@_on_stream
+def expert_dispatch_forward(plan: Experts, x, out=None):
+    """The rows of x [N, ...] in the order of their experts: [plan.rows, ...], zeros in
+    padding rows.  x: a tensor of any type whose rows are a multiple of 4 bytes, or a
+    Packed8 (values and scales; out then a Packed8)."""
+    if not isinstance(x, Packed8):
+        return _dispatch_rows(plan, x, "x", out)
+    values, scale = (None, None) if out is None else out
+    return Packed8(_dispatch_rows(plan, x.values, "x.values", values),
+                   _dispatch_rows(plan, x.scale, "x.scale", scale))
+
+
+@_on_stream
+def expert_dispatch_backward(plan: Experts, dxs: torch.Tensor, dx=None):
+    """The gradient of expert_dispatch_forward's x [N, ...] from that of its rows dxs
+    [plan.rows, ...]: the sum over a token's choices."""
+    F = _expert_rows(plan, dxs, "dxs", "rows")
+    dt = _dtype_code(dxs.dtype)
+    dx = _output(dx, "dx", (plan.tokens, *dxs.shape[1:]), dxs.dtype, plan.device)
+    _launch(plan._lib.gnn_expert_combine, "gnn_expert_combine", plan.device, plan._ref, F, dt,
+            _at(dxs), None, None, _at(dx))
+    return dx
+
+
+@_on_stream
+def expert_combine_forward(plan: Experts, ys: torch.Tensor, weights=None, residual=None,
+                           out=None):
+    """residual [N, ...] plus the rows of ys [plan.rows, ...] of each token's choices times
+    weights [N, K] (None: 1), added in float32 and rounded once.  A dropped choice adds
+    nothing.  out may be residual itself."""
+    F = _expert_rows(plan, ys, "ys", "rows")
+    dt = _dtype_code(ys.dtype)
+    weights = _expert_weights(plan, weights)
+    shape = (plan.tokens, *ys.shape[1:])
+    if residual is not None:
+        _plain_tensor(residual, "residual", shape, ys.dtype, plan.device)
+    out = _output(out, "out", shape, ys.dtype, plan.device)
+    _launch(plan._lib.gnn_expert_combine, "gnn_expert_combine", plan.device, plan._ref, F, dt,
+            _at(ys), _at(weights), _at(residual), _at(out))
+    return out
+
+
+@_on_stream
+def expert_combine_backward(plan: Experts, dy: torch.Tensor, ys=None, weights=None, dys=None,
+                            dweights=None):
+    """The gradients of expert_combine_forward: dys [plan.rows, ...] (zeros in padding rows)
+    and dweights [N, K] float32 (0 where dropped; None without weights, and ys is then not
+    needed).  The residual's gradient is dy."""
+    F = _expert_rows(plan, dy, "dy", "tokens")
+    dt = _dtype_code(dy.dtype)
+    weights = _expert_weights(plan, weights)
+    shape = (plan.rows, *dy.shape[1:])
+    dys = _output(dys, "dys", shape, dy.dtype, plan.device)
+    if weights is not None:
+        _plain_tensor(ys, "ys", shape, dy.dtype, plan.device)
+        dweights = _like(dweights, "dweights", weights)
+    elif dweights is not None:
+        raise ValueError("there are no dweights without weights")
+    _launch(plan._lib.gnn_expert_combine_backward, "gnn_expert_combine_backward", plan.device,
+            plan._ref, F, dt, _at(dy), None if weights is None else _at(ys), _at(weights),
+            _at(dys), _at(dweights))
+    return dys, dweights
+
+
+class ExpertDispatch(torch.autograd.Function):
+    """xs = ExpertDispatch.apply(plan, x)."""
+
+    @staticmethod
+    def forward(ctx, plan, x):
+        ctx.plan = plan
+        return expert_dispatch_forward(plan, x.contiguous())
+
+    @staticmethod
+    @once_differentiable
+    def backward(ctx, dxs):
+        return None, expert_dispatch_backward(ctx.plan, dxs.contiguous())
+
+
+class ExpertCombine(torch.autograd.Function):
+    """y = ExpertCombine.apply(plan, ys, weights, residual); weights and residual or None."""
+
+    @staticmethod
+    def forward(ctx, plan, ys, weights, residual):
+        ys, weights, residual = (None if t is None else t.contiguous()
+                                 for t in (ys, weights, residual))
+        ctx.plan, ctx.added = plan, residual is not None
+        ctx.save_for_backward(None if weights is None else ys, weights)
+        return expert_combine_forward(plan, ys, weights, residual)
+
+    @staticmethod
+    @once_differentiable
+    def backward(ctx, dy):
+        ys, weights = ctx.saved_tensors
+        dy = dy.contiguous()
+        dys, dw = expert_combine_backward(ctx.plan, dy, ys, weights)
+        return (None, dys, None if weights is None else dw.to(weights.dtype),
+                dy if ctx.added else None)
+
+
 class Rope:
     """Frequencies of rotary positions: the first dim elements of a head vector are dim/2
     pairs, of elements i and i + dim/2 (layout "half") or 2 i and 2 i + 1
@@ -1279,6 +1484,16 @@ rotary positions of q and key
         out = TransformerAggregate.apply(g, q, key, val, scale)
     o = out.reshape(x.shape) if project is None else project(out)
     return NormResidual.apply(x, o, gate, w_post, b_post, res_scale, w_pre, b_pre, kind, eps)
+
+
+def expert_layer(plan: Experts, z: torch.Tensor, experts, weights=None, residual=None):
+    """The feed-forward half of a layer whose experts a router chose, with autograd: the
+    rows of z [N, ...] in the order of their experts, `experts` (a function of the rows
+    [plan.rows, F] and the plan, whose expert e has the rows from plan.offsets[e] on,
+    returning [plan.rows, F']), and back: residual plus the weighted sum over each token's
+    choices.  y and z of transformer_layer are its residual and its z."""
+    xs = ExpertDispatch.apply(plan, z)
+    return ExpertCombine.apply(plan, experts(xs, plan), weights, residual)
 
 
 def _reduce_ws(g, F, dt, ws, device):

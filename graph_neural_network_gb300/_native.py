@@ -80,6 +80,12 @@ SIGNATURES = [
     ("gnn_norm_residual_forward", _I32, [_P, _I32, _P, _P, _P, _P, _P, _P]),
     ("gnn_norm_residual_workspace_bytes", _SZ, [_P, _I32]),
     ("gnn_norm_residual_backward", _I32, [_P, _I32, _P, _P, _P, _P, _P, _P, _P, _SZ, _P]),
+    ("gnn_experts_rows", _I64, [_I64, _I32, _I32, _I32]),
+    ("gnn_experts_buffer_bytes", _SZ, [_I64, _I32, _I32, _I32]),
+    ("gnn_experts_prepare", _I32, [_P, _I32, _I64, _I32, _I32, _I32, _P, _SZ, _P, _P]),
+    ("gnn_expert_dispatch", _I32, [_P, _I64, _P, _P, _P]),
+    ("gnn_expert_combine", _I32, [_P, _I32, _I32, _P, _P, _P, _P, _P]),
+    ("gnn_expert_combine_backward", _I32, [_P, _I32, _I32, _P, _P, _P, _P, _P, _P]),
     ("gnn_add_norm8_forward", _I32, [_P, _I32, _P, _P, _P, _P, _P, _P, _P]),
     ("gnn_add_norm8_workspace_bytes", _SZ, [_P, _I32]),
     ("gnn_add_norm8_backward", _I32, [_P, _I32, _P, _P, _P, _P, _P, _P, _P, _SZ, _P]),
@@ -122,6 +128,11 @@ class NormGrads(ctypes.Structure):
 
 class AddNorm8(ctypes.Structure):  # gnn_add_norm8
     _fields_ = [("n", _I64), ("F", _I32), ("group", _I32), ("fmt", _I32), ("eps", _F)]
+
+
+class Experts(ctypes.Structure):  # gnn_experts
+    _fields_ = [("tokens", _I64), ("rows", _I64), ("choices", _I32), ("experts", _I32),
+                ("align", _I32)] + [(k, _P) for k in ("offsets", "counts", "order", "slots")]
 
 
 ROPE_MAX_DIM = 256  # GNN_ROPE_MAX_DIM

@@ -1,11 +1,12 @@
 // C-ABI entry points of the operators round a layer's projections (rotary
-// positions, 8-bit norms): argument checks, then the launchers.
+// positions, 8-bit norms, experts): argument checks, then the launchers.
 #include <math.h>
 
 #include "api_util.h"
 #include "internal.h"
 
 using gnn::aligned;
+using gnn::current_sms;
 using gnn::from_cuda;
 
 namespace {
@@ -27,6 +28,26 @@ gnn_status add_norm8_check(const gnn_add_norm8* d, gnn_dtype dt) {
   if (d->group != d->F && (bytes < 16 || bytes > 512 || (bytes & (bytes - 1))))
     return GNN_ERR_UNSUPPORTED;
   return GNN_OK;
+}
+
+bool experts_size_ok(int64_t tokens, int choices, int experts, int align) {
+  return tokens >= 0 && tokens < (int64_t(1) << 31) && choices >= 1 && choices <= 64 &&
+         experts >= 1 && experts <= 1024 && align >= 1 && align <= 65536 &&
+         gnn::expert_rows(tokens, choices, experts, align) < (int64_t(1) << 31) &&
+         tokens * choices < (int64_t(1) << 31);
+}
+
+bool plan_ok(const gnn_experts* p) {
+  return p && experts_size_ok(p->tokens, p->choices, p->experts, p->align) &&
+         p->rows == gnn::expert_rows(p->tokens, p->choices, p->experts, p->align) && p->offsets &&
+         p->counts && p->order && p->slots;
+}
+
+// Rows of a call: 16-byte vectors.
+gnn_status expert_shape(const gnn_experts* p, int F, gnn_dtype dt) {
+  if (!plan_ok(p) || !dtype_ok(dt) || F < 1) return GNN_ERR_INVALID_ARG;
+  const int64_t bytes = int64_t(F) * (dt == GNN_F32 ? 4 : 2);
+  return bytes % 16 || bytes > (1 << 20) ? GNN_ERR_UNSUPPORTED : GNN_OK;
 }
 
 // Rows of D elements at these strides lie apart: heads inside nodes, or nodes
@@ -205,6 +226,82 @@ gnn_status gnn_unpack8_groups(int64_t groups, int group, gnn_eight fmt, gnn_dtyp
     return GNN_ERR_INVALID_ARG;
   return from_cuda(gnn::launch_unpack8_groups(groups, group, fmt, dtype, values, scale, x,
                                               static_cast<cudaStream_t>(stream)));
+}
+
+int64_t gnn_experts_rows(int64_t tokens, int choices, int experts, int align) {
+  return experts_size_ok(tokens, choices, experts, align)
+             ? gnn::expert_rows(tokens, choices, experts, align)
+             : -1;
+}
+
+size_t gnn_experts_buffer_bytes(int64_t tokens, int choices, int experts, int align) {
+  return experts_size_ok(tokens, choices, experts, align)
+             ? gnn::experts_buffer_bytes(tokens, choices, experts, align)
+             : 0;
+}
+
+gnn_status gnn_experts_prepare(const void* ids, int id_bytes, int64_t tokens, int choices,
+                               int experts, int align, void* buffer, size_t buffer_bytes,
+                               void* stream, gnn_experts* out) {
+  if (!out) return GNN_ERR_INVALID_ARG;
+  *out = gnn_experts{};
+  if ((id_bytes != 4 && id_bytes != 8) || !experts_size_ok(tokens, choices, experts, align) ||
+      (tokens > 0 && !ids) || !aligned(ids, id_bytes) || !buffer || !aligned(buffer, 256))
+    return GNN_ERR_INVALID_ARG;
+  if (buffer_bytes < gnn::experts_buffer_bytes(tokens, choices, experts, align))
+    return GNN_ERR_WORKSPACE_TOO_SMALL;
+  gnn_experts p{};
+  p.tokens = tokens;
+  p.rows = gnn::expert_rows(tokens, choices, experts, align);
+  p.choices = choices;
+  p.experts = experts;
+  p.align = align;
+  const gnn_status r = from_cuda(gnn::launch_experts_prepare(
+      ids, id_bytes, static_cast<char*>(buffer), &p, static_cast<cudaStream_t>(stream)));
+  if (r == GNN_OK) *out = p;
+  return r;
+}
+
+gnn_status gnn_expert_dispatch(const gnn_experts* plan, int64_t row_bytes, const void* x,
+                               void* xs, void* stream) {
+  if (!plan_ok(plan) || row_bytes < 1) return GNN_ERR_INVALID_ARG;
+  if (row_bytes % 4 || row_bytes > (1 << 20)) return GNN_ERR_UNSUPPORTED;
+  if (plan->tokens == 0) return GNN_OK;
+  const int width = row_bytes % 16 == 0 ? 16 : row_bytes % 8 == 0 ? 8 : 4;
+  if (!x || !xs || !aligned(x, width) || !aligned(xs, width)) return GNN_ERR_INVALID_ARG;
+  int sms = 0;
+  if (!current_sms(&sms)) return GNN_ERR_CUDA;
+  return from_cuda(gnn::launch_expert_dispatch(*plan, row_bytes, width, x, xs, sms,
+                                               static_cast<cudaStream_t>(stream)));
+}
+
+gnn_status gnn_expert_combine(const gnn_experts* plan, int F, gnn_dtype dtype, const void* ys,
+                              const float* weights, const void* residual, void* y, void* stream) {
+  const gnn_status r = expert_shape(plan, F, dtype);
+  if (r != GNN_OK) return r;
+  if (plan->tokens == 0) return GNN_OK;
+  if (!ys || !y || !aligned(ys, 16) || !aligned(weights, 4) || !aligned(residual, 16) ||
+      !aligned(y, 16))
+    return GNN_ERR_INVALID_ARG;
+  return from_cuda(gnn::launch_expert_combine(*plan, F, dtype, ys, weights, residual, y,
+                                              static_cast<cudaStream_t>(stream)));
+}
+
+gnn_status gnn_expert_combine_backward(const gnn_experts* plan, int F, gnn_dtype dtype,
+                                       const void* dy, const void* ys, const float* weights,
+                                       void* dys, float* dweights, void* stream) {
+  const gnn_status r = expert_shape(plan, F, dtype);
+  if (r != GNN_OK) return r;
+  if (plan->tokens == 0) return GNN_OK;
+  if (!dy || !dys || (dweights && !ys) || !aligned(dy, 16) || !aligned(ys, 16) ||
+      !aligned(weights, 4) || !aligned(dys, 16) || !aligned(dweights, 4))
+    return GNN_ERR_INVALID_ARG;
+  int sms = 0;
+  if (!current_sms(&sms)) return GNN_ERR_CUDA;
+  return from_cuda(gnn::launch_expert_combine_backward(*plan, F, dtype, dy,
+                                                       dweights ? ys : nullptr, weights, dys,
+                                                       dweights, sms,
+                                                       static_cast<cudaStream_t>(stream)));
 }
 
 }  // extern "C"

@@ -1,0 +1,569 @@
+// Tokens in the order of the experts that they chose, and back.
+//
+// Plan.  A stable counting sort of the (token, choice) pairs by expert: rank of a pair =
+// pairs of its expert before it, row = the expert's first row + rank.  A warp takes a
+// run of pairs, 32 at a time; lanes of equal experts find one another by a match, and
+// the warp keeps its own counts in shared memory, so ranks depend on no scheduling.
+// One pass counts, the warps' counts (and the blocks' before this one) are added up
+// in order, and a second pass ranks and writes.  Up to kOneBlock pairs a single block
+// does it all; more take a kernel that counts for each block and one that reads all
+// blocks' counts, starts early and counts its own warps meanwhile.
+// Bound: latency.  A pair costs its id twice and two writes of 4 bytes.
+//
+// Dispatch: a token's row is read once and written to the rows of its choices; padding
+// rows are found in the order (-1) by blocks of their own and written zero.  Combine:
+// the rows of a token's choices, weighted, are added in the order of its choices in
+// float32 on top of the residual, and rounded once.  Its gradient: dys = w dy and dw = dy .
+// ys in one pass, a warp (sub-group, or a block where tokens are few) a token.
+// Bound: HBM; each row is read and written once.
+#include "device.cuh"
+
+namespace gnn {
+namespace {
+
+// ---- plan ---------------------------------------------------------------------
+
+constexpr int kOneBlock = 8192;   // pairs that a single block sorts
+constexpr int kLoadSteps = 8;     // steps of 32 pairs a warp loads at once
+constexpr int kSortBlocks = 304;
+
+struct SortArgs {
+  const void* ids;
+  int64_t pairs, rows;
+  int E, align;
+  int steps;           // of 32 pairs, of a warp
+  int blocks;
+  int32_t *offsets, *counts, *order, *slots;
+  int32_t* seen;       // [blocks][E] (more than one block)
+};
+
+// Warps of a block: their counts take at most 32 KB.
+int sort_warps(int E) { return E <= 256 ? 32 : 8; }
+int sort_blocks(int64_t pairs, int E) {
+  if (pairs <= kOneBlock) return 1;
+  const int64_t want = (pairs + kOneBlock / 2 - 1) / (kOneBlock / 2), cap = 32768 / E;
+  const int64_t most = cap < kSortBlocks ? cap : kSortBlocks;
+  return int(want < most ? want : most);
+}
+
+// The experts of this lane's pairs of steps s0 .. s0 + kLoadSteps, -1 where dropped.
+template <typename Id>
+__device__ __forceinline__ void load_experts(const SortArgs& A, int64_t first, int s0,
+                                             int (&e)[kLoadSteps]) {
+#pragma unroll
+  for (int u = 0; u < kLoadSteps; ++u) {
+    const int64_t p = first + int64_t(s0 + u) * 32 + (threadIdx.x & 31);
+    const Id id = s0 + u < A.steps && p < A.pairs ? __ldg(static_cast<const Id*>(A.ids) + p)
+                                                  : Id(-1);
+    e[u] = id >= 0 && id < Id(A.E) ? int(id) : -1;
+  }
+}
+
+// Adds the warp's pairs to its counts.
+template <typename Id>
+__device__ __forceinline__ void count_experts(const SortArgs& A, int64_t first, int32_t* mine) {
+  const int lane = threadIdx.x & 31;
+  for (int s0 = 0; s0 < A.steps; s0 += kLoadSteps) {
+    int e[kLoadSteps];
+    load_experts<Id>(A, first, s0, e);
+#pragma unroll
+    for (int u = 0; u < kLoadSteps; ++u) {
+      if (s0 + u >= A.steps) break;
+      const unsigned same = __match_any_sync(kFull, e[u]);
+      if (e[u] >= 0 && lane == __ffs(same) - 1) mine[e[u]] += __popc(same);
+      __syncwarp();
+    }
+  }
+}
+
+template <typename Id>
+__global__ void __launch_bounds__(1024) sort_count(const SortArgs A) {
+  extern __shared__ int32_t counts[];  // [warps][E]
+  const int warps = blockDim.x >> 5, wid = threadIdx.x >> 5;
+  for (int x = threadIdx.x; x < warps * A.E; x += blockDim.x) counts[x] = 0;
+  __syncthreads();
+  count_experts<Id>(A, (int64_t(blockIdx.x) * warps + wid) * A.steps * 32, counts + wid * A.E);
+  __syncthreads();
+  for (int e = threadIdx.x; e < A.E; e += blockDim.x) {
+    int s = 0;
+    for (int w = 0; w < warps; ++w) s += counts[w * A.E + e];
+    A.seen[int64_t(blockIdx.x) * A.E + e] = s;
+  }
+  let_next_start();
+}
+
+template <typename Id>
+__global__ void __launch_bounds__(1024) sort_place(const SortArgs A) {
+  extern __shared__ int32_t counts[];      // [warps][E]
+  const int threads = blockDim.x, warps = threads >> 5, wid = threadIdx.x >> 5,
+            lane = threadIdx.x & 31;
+  int32_t* total = counts + warps * A.E;   // [E] pairs of each expert
+  int32_t* before = total + A.E;           // [E] of them in the blocks before this one
+  int32_t* offset = before + A.E;          // [E + 1] first rows
+  for (int x = threadIdx.x; x < (warps + 2) * A.E; x += threads) counts[x] = 0;
+  __syncthreads();
+  const int64_t first = (int64_t(blockIdx.x) * warps + wid) * A.steps * 32;
+  count_experts<Id>(A, first, counts + wid * A.E);
+  __syncthreads();
+  if (A.blocks == 1) {
+    for (int e = threadIdx.x; e < A.E; e += threads)
+      for (int w = 0; w < warps; ++w) total[e] += counts[w * A.E + e];
+  } else {
+    grid_wait();
+    // slices of blocks side by side where there are fewer experts than threads
+    const int width = A.E < threads ? A.E : threads, slices = threads / width;
+    const int slice = threadIdx.x / width;
+    if (slice < slices)
+      for (int e = threadIdx.x - slice * width; e < A.E; e += width) {
+        int all = 0, past = 0;
+#pragma unroll 8
+        for (int b = slice; b < A.blocks; b += slices) {
+          const int c = A.seen[int64_t(b) * A.E + e];
+          all += c;
+          past += b < int(blockIdx.x) ? c : 0;
+        }
+        atomicAdd(total + e, all);
+        atomicAdd(before + e, past);
+      }
+  }
+  __syncthreads();
+  if (wid == 0) {
+    int run = 0;
+    for (int e0 = 0; e0 < A.E; e0 += 32) {
+      const int e = e0 + lane;
+      const int mine = e < A.E ? (total[e] + A.align - 1) / A.align * A.align : 0;
+      int sum = mine;
+      for (int o = 1; o < 32; o <<= 1) {
+        const int up = __shfl_up_sync(kFull, sum, o);
+        if (lane >= o) sum += up;
+      }
+      if (e < A.E) offset[e] = run + sum - mine;
+      run += __shfl_sync(kFull, sum, 31);
+    }
+    if (lane == 0) offset[A.E] = run;
+  }
+  __syncthreads();
+  for (int e = threadIdx.x; e < A.E; e += threads) {
+    int run = offset[e] + before[e];
+    for (int w = 0; w < warps; ++w) {
+      const int c = counts[w * A.E + e];
+      counts[w * A.E + e] = run;
+      run += c;
+    }
+  }
+  __syncthreads();
+  int32_t* next = counts + wid * A.E;
+  for (int s0 = 0; s0 < A.steps; s0 += kLoadSteps) {
+    int e[kLoadSteps];
+    load_experts<Id>(A, first, s0, e);
+#pragma unroll
+    for (int u = 0; u < kLoadSteps; ++u) {
+      if (s0 + u >= A.steps) break;
+      const unsigned same = __match_any_sync(kFull, e[u]);
+      const int base = e[u] >= 0 ? next[e[u]] : 0;
+      __syncwarp();
+      if (e[u] >= 0 && lane == __ffs(same) - 1) next[e[u]] = base + __popc(same);
+      __syncwarp();
+      const int64_t p = first + int64_t(s0 + u) * 32 + lane;
+      if (p < A.pairs) {
+        const int row = e[u] >= 0 ? base + __popc(same & ((1u << lane) - 1u)) : -1;
+        A.slots[p] = row;
+        if (row >= 0) A.order[row] = int32_t(p);
+      }
+    }
+  }
+  if (blockIdx.x == 0) {
+    for (int e = threadIdx.x; e <= A.E; e += threads) A.offsets[e] = offset[e];
+    for (int e = threadIdx.x; e < A.E; e += threads) A.counts[e] = total[e];
+  }
+  // rows without a pair: behind each expert's, and behind all of them
+  if (A.align > 1)
+    for (int e = blockIdx.x * warps + wid; e < A.E; e += A.blocks * warps)
+      for (int r = offset[e] + total[e] + lane; r < offset[e + 1]; r += 32) A.order[r] = -1;
+  for (int64_t r = offset[A.E] + int64_t(blockIdx.x) * threads + threadIdx.x; r < A.rows;
+       r += int64_t(A.blocks) * threads)
+    A.order[r] = -1;
+}
+
+// ---- rows ---------------------------------------------------------------------
+
+struct RowArgs {
+  int64_t tokens, rows;
+  int K;
+  int rv;             // accesses (vectors) of a row
+  int tpr_log2;       // lanes of a row
+  int chunks;         // of a row, a warp each (rows wider than a warp takes at once)
+  uint64_t div;       // ceil(2^64 / chunks), 0 for 1: warp * div / 2^64 is its token
+  int64_t work_blocks;  // blocks that take tokens; those behind them take padding rows
+  const int32_t *slots, *order;
+  const float* weights;
+  const void *x, *ys, *residual;
+  void *y;
+  float* dweights;
+};
+
+template <int kB>
+struct RawOf;
+template <>
+struct RawOf<16> { using type = uint4; };
+template <>
+struct RawOf<8> { using type = uint2; };
+template <>
+struct RawOf<4> { using type = uint32_t; };
+
+// Zeros in the rows of the order without a pair: 32 rows a warp and turn.
+template <typename Raw>
+__device__ __forceinline__ void zero_padding(const RowArgs& A) {
+  const int lane = threadIdx.x & 31;
+  const int64_t warps = (int64_t(gridDim.x) - A.work_blocks) * kWarps;
+  const int64_t w0 = (int64_t(blockIdx.x) - A.work_blocks) * kWarps + (threadIdx.x >> 5);
+  for (int64_t r0 = w0 * 32; r0 < A.rows; r0 += warps * 32) {
+    const bool pad = r0 + lane < A.rows && __ldg(A.order + r0 + lane) < 0;
+    for (unsigned left = __ballot_sync(kFull, pad); left; left &= left - 1) {
+      Raw* row = static_cast<Raw*>(A.y) + (r0 + __ffs(left) - 1) * A.rv;
+      for (int v = lane; v < A.rv; v += 32) row[v] = Raw{};
+    }
+  }
+}
+
+// The thread's accesses: kFlight of them, of as many tokens (rows of at most a
+// warp's lanes, kWide false) or of one token (kWide).
+constexpr int kFlight = 4;
+
+template <bool kWide>
+struct Where {
+  int64_t token, token_step;
+  int vec, vec_step;
+  __device__ __forceinline__ explicit Where(const RowArgs& A) {
+    const int64_t warp = int64_t(blockIdx.x) * kWarps + (threadIdx.x >> 5);
+    const int lane = threadIdx.x & 31;
+    if (kWide) {
+      token = A.div ? int64_t(__umul64hi(uint64_t(warp), A.div)) : warp;
+      vec = int(warp - token * A.chunks) * (32 * kFlight) + lane;
+      vec_step = 32;
+      token_step = 0;
+    } else {
+      const int per = 32 >> A.tpr_log2;
+      token = warp * (per * kFlight) + (lane >> A.tpr_log2);
+      token_step = per;
+      vec = lane & ((1 << A.tpr_log2) - 1);
+      vec_step = 0;
+    }
+  }
+  __device__ __forceinline__ int64_t token_of(int u) const { return token + u * token_step; }
+  __device__ __forceinline__ int vec_of(int u) const { return vec + u * vec_step; }
+  __device__ __forceinline__ bool in(const RowArgs& A, int u) const {
+    return token_of(u) < A.tokens && vec_of(u) < A.rv;
+  }
+};
+
+template <int kB, bool kWide>
+__global__ void __launch_bounds__(kThreads) expert_dispatch(const RowArgs A) {
+  using Raw = typename RawOf<kB>::type;
+  if (blockIdx.x >= A.work_blocks) {
+    zero_padding<Raw>(A);
+    return;
+  }
+  const Where<kWide> W(A);
+  const Raw* x = static_cast<const Raw*>(A.x);
+  Raw* xs = static_cast<Raw*>(A.y);
+  Raw r[kFlight];
+#pragma unroll
+  for (int u = 0; u < kFlight; ++u)
+    if (W.in(A, u)) r[u] = __ldg(x + W.token_of(u) * A.rv + W.vec_of(u));
+  for (int k = 0; k < A.K; ++k)
+#pragma unroll
+    for (int u = 0; u < kFlight; ++u)
+      if (W.in(A, u)) {
+        const int s = __ldg(A.slots + W.token_of(u) * A.K + k);
+        if (s >= 0) xs[int64_t(s) * A.rv + W.vec_of(u)] = r[u];
+      }
+}
+
+// y = residual + sum of w ys over a token's choices.
+template <typename T, bool kWide>
+__global__ void __launch_bounds__(kThreads) expert_combine(const RowArgs A) {
+  constexpr int V = VecOf<T>::n;
+  const Where<kWide> W(A);
+  float acc[kFlight][V];
+#pragma unroll
+  for (int u = 0; u < kFlight; ++u) {
+    uint4 r = make_uint4(0, 0, 0, 0);
+    if (A.residual && W.in(A, u))
+      r = static_cast<const uint4*>(A.residual)[W.token_of(u) * A.rv + W.vec_of(u)];
+    unpack<T>(r, acc[u]);
+  }
+  for (int k = 0; k < A.K; ++k) {
+    uint4 r[kFlight];
+    float w[kFlight];
+#pragma unroll
+    for (int u = 0; u < kFlight; ++u) {
+      w[u] = 0.f;
+      r[u] = make_uint4(0, 0, 0, 0);
+      if (!W.in(A, u)) continue;
+      const int64_t at = W.token_of(u) * A.K + k;
+      const int s = __ldg(A.slots + at);
+      if (s < 0) continue;
+      w[u] = A.weights ? __ldg(A.weights + at) : 1.f;
+      r[u] = ld16(static_cast<const uint4*>(A.ys) + int64_t(s) * A.rv + W.vec_of(u));
+    }
+#pragma unroll
+    for (int u = 0; u < kFlight; ++u) {
+      float x[V];
+      unpack<T>(r[u], x);
+      axpy<V>(acc[u], w[u], x);
+    }
+  }
+#pragma unroll
+  for (int u = 0; u < kFlight; ++u)
+    if (W.in(A, u))
+      st16(static_cast<uint4*>(A.y) + W.token_of(u) * A.rv + W.vec_of(u), pack<T>(acc[u]));
+}
+
+// dys = w dy into the rows of a token's choices, dw = dy . ys: kK choices at a time.
+// kBlock: a block takes a token; otherwise a warp or a part of one.
+constexpr int kK = 4;
+
+template <typename T, bool kBlock>
+__global__ void __launch_bounds__(kThreads) expert_combine_bwd(const RowArgs A) {
+  constexpr int V = VecOf<T>::n;
+  __shared__ float part[kBlock ? kWarps * kK : 1];
+  if (blockIdx.x >= A.work_blocks) {
+    zero_padding<uint4>(A);
+    return;
+  }
+  const int lane = threadIdx.x & 31, wid = threadIdx.x >> 5;
+  const int lanes = kBlock ? kThreads : 1 << A.tpr_log2;
+  const int64_t token = kBlock ? int64_t(blockIdx.x)
+                               : (int64_t(blockIdx.x) * kWarps + wid) * (32 >> A.tpr_log2) +
+                                     (lane >> A.tpr_log2);
+  const int v0 = kBlock ? threadIdx.x : lane & (lanes - 1);
+  const bool on = token < A.tokens;
+  const uint4* dy = static_cast<const uint4*>(A.x) + token * A.rv;
+  for (int k0 = 0; k0 < A.K; k0 += kK) {
+    int s[kK];
+    float w[kK], dot_[kK];
+#pragma unroll
+    for (int k = 0; k < kK; ++k) {
+      const bool has = on && k0 + k < A.K;
+      const int64_t at = token * A.K + k0 + k;
+      s[k] = has ? __ldg(A.slots + at) : -1;
+      w[k] = has && A.weights ? __ldg(A.weights + at) : 1.f;
+      dot_[k] = 0.f;
+    }
+    if (on)
+#pragma unroll 2
+      for (int v = v0; v < A.rv; v += lanes) {
+        const uint4 rd = ld16(dy + v);
+        uint4 ry[kK];
+#pragma unroll
+        for (int k = 0; k < kK; ++k)
+          ry[k] = s[k] >= 0 && A.ys
+                      ? ld16(static_cast<const uint4*>(A.ys) + int64_t(s[k]) * A.rv + v)
+                      : make_uint4(0, 0, 0, 0);
+        float d[V];
+        unpack<T>(rd, d);
+#pragma unroll
+        for (int k = 0; k < kK; ++k) {
+          float y[V];
+          unpack<T>(ry[k], y);
+          dot_[k] += dot<V>(d, y);
+          if (s[k] >= 0) {
+#pragma unroll
+            for (int c = 0; c < V; ++c) y[c] = d[c];
+            scale<V>(y, w[k]);
+            st16(static_cast<uint4*>(A.y) + int64_t(s[k]) * A.rv + v, pack<T>(y));
+          }
+        }
+      }
+    if (!A.dweights) continue;
+    for (int o = 1; o < (kBlock ? 32 : lanes); o <<= 1)
+#pragma unroll
+      for (int k = 0; k < kK; ++k) dot_[k] += __shfl_xor_sync(kFull, dot_[k], o);
+    if constexpr (kBlock) {
+      if (lane == 0)
+#pragma unroll
+        for (int k = 0; k < kK; ++k) part[wid * kK + k] = dot_[k];
+      __syncthreads();
+#pragma unroll
+      for (int k = 0; k < kK; ++k) {
+        dot_[k] = 0.f;
+        for (int x = 0; x < kWarps; ++x) dot_[k] += part[x * kK + k];
+      }
+      __syncthreads();  // before the next choices' sums
+    }
+    if (on && v0 == 0)
+#pragma unroll
+      for (int k = 0; k < kK; ++k)
+        if (k0 + k < A.K) A.dweights[token * A.K + k0 + k] = s[k] >= 0 ? dot_[k] : 0.f;
+  }
+}
+
+RowArgs row_args(const gnn_experts& p, int rv) {
+  RowArgs A{};
+  A.tokens = p.tokens;
+  A.rows = p.rows;
+  A.K = p.choices;
+  A.rv = rv;
+  while ((1 << A.tpr_log2) < rv && A.tpr_log2 < 5) ++A.tpr_log2;
+  A.chunks = (rv + 32 * kFlight - 1) / (32 * kFlight);
+  A.div = A.chunks > 1 ? ~uint64_t(0) / uint64_t(A.chunks) + 1 : 0;
+  A.slots = p.slots;
+  A.order = p.order;
+  return A;
+}
+
+// Blocks for the tokens: a warp takes a chunk of one, or kFlight of its lanes' rows.
+int64_t token_blocks(const RowArgs& A) {
+  const int64_t warps = A.rv > 32 ? A.tokens * A.chunks
+                                  : (A.tokens + (kFlight << (5 - A.tpr_log2)) - 1) /
+                                        (kFlight << (5 - A.tpr_log2));
+  return (warps + kWarps - 1) / kWarps;
+}
+
+// Blocks for the padding: a warp reads 32 rows of the order at once.
+int64_t padding_blocks(int64_t rows, int sm_count) {
+  const int64_t want = (rows + 32 * kWarps - 1) / (32 * kWarps), cap = int64_t(sm_count) * 4;
+  return want < cap ? want : cap;
+}
+
+template <int kB>
+cudaError_t dispatch(const RowArgs& A, unsigned blocks, cudaStream_t st) {
+  auto kernel = A.rv > 32 ? expert_dispatch<kB, true> : expert_dispatch<kB, false>;
+  kernel<<<blocks, kThreads, 0, st>>>(A);
+  return cudaGetLastError();
+}
+
+template <typename T>
+cudaError_t combine(const RowArgs& A, unsigned blocks, cudaStream_t st) {
+  auto kernel = A.rv > 32 ? expert_combine<T, true> : expert_combine<T, false>;
+  kernel<<<blocks, kThreads, 0, st>>>(A);
+  return cudaGetLastError();
+}
+
+template <typename Id>
+cudaError_t sort(SortArgs& A, cudaStream_t st) {
+  const int warps = sort_warps(A.E);
+  A.blocks = sort_blocks(A.pairs, A.E);
+  const int64_t runs = int64_t(A.blocks) * warps * 32;
+  A.steps = int((A.pairs + runs - 1) / runs);
+  const size_t counts = size_t(warps) * A.E * 4;
+  if (A.blocks == 1) {
+    sort_place<Id><<<1, warps * 32, counts + (3 * size_t(A.E) + 1) * 4, st>>>(A);
+    return cudaGetLastError();
+  }
+  sort_count<Id><<<unsigned(A.blocks), warps * 32, counts, st>>>(A);
+  const cudaError_t e = cudaGetLastError();
+  if (e != cudaSuccess) return e;
+  return launch_after(sort_place<Id>, dim3(unsigned(A.blocks)), warps * 32,
+                      counts + (3 * size_t(A.E) + 1) * 4, st, A);
+}
+
+// Byte offsets of the arrays in a plan's buffer, and its size.
+struct PlanLayout {
+  size_t offsets, counts, order, slots, seen, total;
+  PlanLayout(int64_t pairs, int64_t rows, int E) {
+    size_t at = 0;
+    const auto take = [&](size_t ints) {
+      const size_t r = at;
+      at += align_up(ints * 4, 16);
+      return r;
+    };
+    offsets = take(size_t(E) + 1);
+    counts = take(size_t(E));
+    order = take(size_t(rows));
+    slots = take(size_t(pairs));
+    const int blocks = sort_blocks(pairs, E);
+    seen = take(blocks > 1 ? size_t(blocks) * E : 0);
+    total = align_up(at, 256);
+  }
+};
+
+}  // namespace
+
+int64_t expert_rows(int64_t tokens, int choices, int experts, int align) {
+  const int64_t pairs = tokens * choices;
+  const int64_t padded = pairs < experts ? pairs : experts;  // experts with a pair, at most
+  return (pairs + padded * (align - 1)) / align * align;
+}
+
+size_t experts_buffer_bytes(int64_t tokens, int choices, int experts, int align) {
+  return PlanLayout(tokens * choices, expert_rows(tokens, choices, experts, align), experts).total;
+}
+
+cudaError_t launch_experts_prepare(const void* ids, int id_bytes, char* buffer, gnn_experts* p,
+                                   cudaStream_t st) {
+  const int64_t pairs = p->tokens * p->choices;
+  const PlanLayout L(pairs, p->rows, p->experts);
+  SortArgs A{};
+  A.ids = ids;
+  A.pairs = pairs;
+  A.rows = p->rows;
+  A.E = p->experts;
+  A.align = p->align;
+  A.offsets = reinterpret_cast<int32_t*>(buffer + L.offsets);
+  A.counts = reinterpret_cast<int32_t*>(buffer + L.counts);
+  A.order = reinterpret_cast<int32_t*>(buffer + L.order);
+  A.slots = reinterpret_cast<int32_t*>(buffer + L.slots);
+  A.seen = reinterpret_cast<int32_t*>(buffer + L.seen);
+  p->offsets = A.offsets;
+  p->counts = A.counts;
+  p->order = A.order;
+  p->slots = A.slots;
+  return id_bytes == 4 ? sort<int32_t>(A, st) : sort<int64_t>(A, st);
+}
+
+cudaError_t launch_expert_dispatch(const gnn_experts& p, int64_t row_bytes, int width,
+                                   const void* x, void* xs, int sm_count, cudaStream_t st) {
+  RowArgs A = row_args(p, int(row_bytes / width));
+  A.x = x;
+  A.y = xs;
+  A.work_blocks = token_blocks(A);
+  const int64_t blocks = A.work_blocks + padding_blocks(A.rows, sm_count);
+  if (blocks > 0x7fffffff) return cudaErrorInvalidValue;
+  return width == 16  ? dispatch<16>(A, unsigned(blocks), st)
+         : width == 8 ? dispatch<8>(A, unsigned(blocks), st)
+                      : dispatch<4>(A, unsigned(blocks), st);
+}
+
+cudaError_t launch_expert_combine(const gnn_experts& p, int F, gnn_dtype dt, const void* ys,
+                                  const float* weights, const void* residual, void* y,
+                                  cudaStream_t st) {
+  RowArgs A = row_args(p, F * (dt == GNN_F32 ? 4 : 2) / 16);
+  A.ys = ys;
+  A.weights = weights;
+  A.residual = residual;
+  A.y = y;
+  const int64_t blocks = token_blocks(A);
+  if (blocks > 0x7fffffff) return cudaErrorInvalidValue;
+  return dt == GNN_F32 ? combine<float>(A, unsigned(blocks), st)
+                       : combine<__nv_bfloat16>(A, unsigned(blocks), st);
+}
+
+cudaError_t launch_expert_combine_backward(const gnn_experts& p, int F, gnn_dtype dt,
+                                           const void* dy, const void* ys, const float* weights,
+                                           void* dys, float* dweights, int sm_count,
+                                           cudaStream_t st) {
+  RowArgs A = row_args(p, F * (dt == GNN_F32 ? 4 : 2) / 16);
+  A.x = dy;
+  A.ys = ys;
+  A.weights = weights;
+  A.y = dys;
+  A.dweights = dweights;
+  // a block a token where warps would leave the GPU idle and a row keeps a block busy
+  const bool block = A.rv >= 64 && A.tokens < int64_t(sm_count) * 16;
+  const int64_t per = block ? 1 : int64_t(kWarps) << (5 - A.tpr_log2);
+  A.work_blocks = (A.tokens + per - 1) / per;
+  const int64_t blocks = A.work_blocks + padding_blocks(A.rows, sm_count);
+  if (blocks > 0x7fffffff) return cudaErrorInvalidValue;
+  const unsigned g = unsigned(blocks);
+  if (dt == GNN_F32)
+    (block ? expert_combine_bwd<float, true>
+           : expert_combine_bwd<float, false>)<<<g, kThreads, 0, st>>>(A);
+  else
+    (block ? expert_combine_bwd<__nv_bfloat16, true>
+           : expert_combine_bwd<__nv_bfloat16, false>)<<<g, kThreads, 0, st>>>(A);
+  return cudaGetLastError();
+}
+
+}  // namespace gnn

@@ -240,6 +240,23 @@ cudaError_t launch_rope(const gnn_rope& rope, int inverse, int64_t n, int D, con
                         int count, const gnn_rope_rows* t, gnn_dtype dt, int width,
                         cudaStream_t st);
 
+// Tokens in the order of their experts (experts.cu).
+int64_t expert_rows(int64_t tokens, int choices, int experts, int align);
+size_t experts_buffer_bytes(int64_t tokens, int choices, int experts, int align);
+// p: sizes set, the pointers are set here.
+cudaError_t launch_experts_prepare(const void* ids, int id_bytes, char* buffer, gnn_experts* p,
+                                   cudaStream_t st);
+// width: bytes of an access (16, 8 or 4).
+cudaError_t launch_expert_dispatch(const gnn_experts& p, int64_t row_bytes, int width,
+                                   const void* x, void* xs, int sm_count, cudaStream_t st);
+cudaError_t launch_expert_combine(const gnn_experts& p, int F, gnn_dtype dt, const void* ys,
+                                  const float* weights, const void* residual, void* y,
+                                  cudaStream_t st);
+cudaError_t launch_expert_combine_backward(const gnn_experts& p, int F, gnn_dtype dt,
+                                           const void* dy, const void* ys, const float* weights,
+                                           void* dys, float* dweights, int sm_count,
+                                           cudaStream_t st);
+
 // Bounded-wait self-test (diag.cu).
 cudaError_t launch_wait_selftest(const gnn_graph* g, int polls, cudaStream_t st);
 

@@ -629,6 +629,63 @@ typedef struct {
 gnn_status gnn_rope_apply(const gnn_rope* rope, int inverse, int64_t n, int D, const int32_t* pos,
                           int count, const gnn_rope_rows* t, gnn_dtype dtype, void* stream);
 
+/* ---- Tokens in the order of their experts ----------------------------------------
+ *
+ * A router gives each of `tokens` tokens (nodes) `choices` experts: ids [tokens]
+ * [choices].  The plan orders these pairs by expert, pairs of one expert by their
+ * numbers t * choices + k, and lays them into rows: expert e has rows offsets[e] to
+ * offsets[e] + counts[e], its segment ends at offsets[e + 1], and segments start at
+ * multiples of `align`.  An id outside [0, experts) drops its pair.  Two choices of
+ * one token may be equal.  All of it stays on the device: nothing waits for it.
+ *   offsets [experts + 1], counts [experts];
+ *   order [rows]: the pair of a row, -1 for padding (behind a segment's pairs, and
+ *   from offsets[experts] on);
+ *   slots [tokens][choices]: the row of a pair, -1 where it is dropped.
+ * rows = gnn_experts_rows: all pairs and the most padding there can be. */
+typedef struct {
+  int64_t tokens, rows;
+  int32_t choices, experts, align;
+  const int32_t *offsets, *counts, *order, *slots; /* device, in the plan's buffer */
+} gnn_experts;
+
+/* Host only: -1 for a size that is not supported.  choices 1 to 64, experts 1 to
+ * 1024, align 1 to 65536, rows below 2^31. */
+int64_t gnn_experts_rows(int64_t tokens, int choices, int experts, int align);
+
+/* Bytes of caller-owned device memory of a plan; 0 where rows is -1. */
+size_t gnn_experts_buffer_bytes(int64_t tokens, int choices, int experts, int align);
+
+/* ids: device, 32 or 64 bits each (id_bytes 4 or 8), read during the call's kernels
+ * only.  buffer: device, 256-byte aligned, holds the plan's arrays for as long as *out
+ * is used (host memory; a plan needs no destroying).  Asynchronous on `stream`;
+ * reproducible. */
+gnn_status gnn_experts_prepare(const void* ids, int id_bytes, int64_t tokens, int choices,
+                               int experts, int align, void* buffer, size_t buffer_bytes,
+                               void* stream, gnn_experts* out);
+
+/* xs [rows][row_bytes]: the row of x [tokens][row_bytes] of each row's token, zeros in
+ * padding rows; every row is written.  row_bytes: a multiple of 4 (x and xs aligned to
+ * its largest power of two up to 16), at most 2^20. */
+gnn_status gnn_expert_dispatch(const gnn_experts* plan, int64_t row_bytes, const void* x,
+                               void* xs, void* stream);
+
+/* y [tokens][F] = residual + sum over a token's choices of weights[t][k] * ys[its row],
+ * in the order of the choices in float32, rounded once.  weights: float [tokens]
+ * [choices], null: 1; residual: dtype [tokens][F], null: 0.  Dropped pairs add nothing,
+ * whatever their weights.  Without weights and residual it is the gradient of
+ * gnn_expert_dispatch.  F * sizeof(dtype) a multiple of 16, at most 2^20; ys [rows][F].
+ * ys, residual, y: 16-byte aligned; y may be residual.  Bitwise reproducible. */
+gnn_status gnn_expert_combine(const gnn_experts* plan, int F, gnn_dtype dtype, const void* ys,
+                              const float* weights, const void* residual, void* y, void* stream);
+
+/* Gradients of gnn_expert_combine (that of the residual is dy itself):
+ *     dys[row of (t, k)] = weights[t][k] * dy[t], zeros in padding rows,
+ *     dweights[t][k] = dy[t] . ys[row of (t, k)], 0 where dropped.
+ * dweights null where not wanted (ys may then be null).  Every row is written. */
+gnn_status gnn_expert_combine_backward(const gnn_experts* plan, int F, gnn_dtype dtype,
+                                       const void* dy, const void* ys, const float* weights,
+                                       void* dys, float* dweights, void* stream);
+
 /* ---- Max / min neighbourhood reduction -----------------------------------
  *
  * out[i][f] = max (or min) over the in-neighbours j of i of x[j][f], and
