@@ -1160,7 +1160,7 @@ class Experts:
                              "are out of range (1 to 1024, 1 to 64, rows below 2^31, 1 to 65536)")
         self.device = ids.device
         self.tokens, self.choices, self.num_experts, self.align = size
-        self.buffer = torch.empty(nb, dtype=torch.uint8, device=self.device)
+        self.buffer = torch.empty(nb // 4, dtype=torch.int32, device=self.device)
         self._c = _native.Experts()
 
         def prepare(s):
@@ -1173,8 +1173,8 @@ class Experts:
         self.rows = self._c.rows
 
     def _view(self, at, *shape):
-        off = at - self.buffer.data_ptr()
-        return self.buffer[off:off + 4 * math.prod(shape)].view(torch.int32).view(shape)
+        strides = (1,) if len(shape) == 1 else (shape[1], 1)
+        return self.buffer.as_strided(shape, strides, (at - self.buffer.data_ptr()) // 4)
 
     @property
     def offsets(self):
@@ -1378,6 +1378,21 @@ class Rope:
         self._lib = lib
 
 
+def _head_rows(x, name, n, D, dtype, device):
+    """The node and head strides of x [n, H, D], whose rows of D are contiguous."""
+    if not isinstance(x, torch.Tensor) or x.dim() != 3:
+        raise ValueError(f"{name} must be a tensor [{n}, H, {D}]")
+    shape = x.shape
+    if shape[0] != n or shape[2] != D:
+        raise ValueError(f"{name} must have shape [{n}, H, {D}], got {tuple(shape)}")
+    if x.dtype != dtype or x.device != device:
+        raise TypeError(f"{name} must be {dtype} on {device}, got {x.dtype} on {x.device}")
+    node, head, one = x.stride()
+    if one != 1 and D > 1:
+        raise ValueError(f"{name} must have contiguous rows of D elements")
+    return node, head
+
+
 def _rope_call(rope, inverse, pos, xs, out, what):
     if not isinstance(rope, Rope):
         raise TypeError(f"rope must be a Rope, got {type(rope).__name__}")
@@ -1392,28 +1407,25 @@ def _rope_call(rope, inverse, pos, xs, out, what):
     if D < rope.dim:
         raise ValueError(f"heads of {D} elements are narrower than the rope's {rope.dim}")
     _plain_tensor(pos, "pos", (n,), torch.int32, device)
-    if out is None:
-        out = [None] * len(xs)
-    elif len(out) != len(xs):
+    if out is not None and len(out) != len(xs):
         raise ValueError("out must have a tensor for every tensor")
-    got, rows = [], []
-    for x, y in zip(xs, out):
-        y = torch.empty(x.shape, dtype=dtype, device=device) if y is None else y
-        for name, t in (("every tensor", x), ("out", y)):
-            if not isinstance(t, torch.Tensor) or t.dim() != 3 or t.shape[0] != n or \
-                    t.shape[2] != D or t.shape[1] != x.shape[1]:
-                raise ValueError(f"{name} must be [{n}, H, {D}]")
-            if t.dtype != dtype or t.device != device:
-                raise TypeError(f"{name} must be {dtype} on {device}")
-            if t.stride(2) != 1 and D > 1:
-                raise ValueError(f"{name} must have contiguous rows of D elements")
-        if x.shape[1] < 1:
+    got, rows = [], _native.ROPE_ROWS[len(xs)]()
+    for k, x in enumerate(xs):
+        xn, xh = _head_rows(x, "every tensor", n, D, dtype, device)
+        H = x.shape[1]
+        if H < 1:
             raise ValueError("every tensor must have a head")
+        if out is None:
+            y, yn, yh = torch.empty((n, H, D), dtype=dtype, device=device), H * D, D
+        else:
+            y = out[k]
+            yn, yh = _head_rows(y, "out", n, D, dtype, device)
+            if y.shape[1] != H:
+                raise ValueError(f"out must have shape {(n, H, D)}, got {tuple(y.shape)}")
         got.append(y)
-        rows.append(_native.RopeRows(x.data_ptr(), y.data_ptr(), x.stride(0), x.stride(1),
-                                     y.stride(0), y.stride(1), x.shape[1]))
+        rows[k] = (x.data_ptr(), y.data_ptr(), xn, xh, yn, yh, H)
     _launch(rope._lib.gnn_rope_apply, what, device, ctypes.byref(rope._c), inverse, n, D,
-            _at(pos), len(rows), _native.ROPE_ROWS[len(rows)](*rows), dt)
+            _at(pos), len(xs), rows, dt)
     return tuple(got)
 
 

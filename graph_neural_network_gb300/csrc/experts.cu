@@ -24,8 +24,10 @@ namespace {
 // ---- plan ---------------------------------------------------------------------
 
 constexpr int kOneBlock = 8192;   // pairs that a single block sorts
-constexpr int kLoadSteps = 8;     // steps of 32 pairs a warp loads at once
+constexpr int kBlockPairs = 2048; // pairs of a block where there are more
+constexpr int kLoadSteps = 4;     // steps of 32 pairs a warp loads at once
 constexpr int kSortBlocks = 304;
+constexpr int kSortThreads = 512;
 
 struct SortArgs {
   const void* ids;
@@ -38,10 +40,10 @@ struct SortArgs {
 };
 
 // Warps of a block: their counts take at most 32 KB.
-int sort_warps(int E) { return E <= 256 ? 32 : 8; }
+int sort_warps(int E) { return E <= 512 ? kSortThreads / 32 : 8; }
 int sort_blocks(int64_t pairs, int E) {
   if (pairs <= kOneBlock) return 1;
-  const int64_t want = (pairs + kOneBlock / 2 - 1) / (kOneBlock / 2), cap = 32768 / E;
+  const int64_t want = (pairs + kBlockPairs - 1) / kBlockPairs, cap = 32768 / E;
   const int64_t most = cap < kSortBlocks ? cap : kSortBlocks;
   return int(want < most ? want : most);
 }
@@ -59,12 +61,13 @@ __device__ __forceinline__ void load_experts(const SortArgs& A, int64_t first, i
   }
 }
 
-// Adds the warp's pairs to its counts.
+// Adds the warp's pairs to its counts.  e: the experts of its last steps (all of them
+// where it has kLoadSteps at most).
 template <typename Id>
-__device__ __forceinline__ void count_experts(const SortArgs& A, int64_t first, int32_t* mine) {
+__device__ __forceinline__ void count_experts(const SortArgs& A, int64_t first, int32_t* mine,
+                                              int (&e)[kLoadSteps]) {
   const int lane = threadIdx.x & 31;
   for (int s0 = 0; s0 < A.steps; s0 += kLoadSteps) {
-    int e[kLoadSteps];
     load_experts<Id>(A, first, s0, e);
 #pragma unroll
     for (int u = 0; u < kLoadSteps; ++u) {
@@ -77,12 +80,13 @@ __device__ __forceinline__ void count_experts(const SortArgs& A, int64_t first, 
 }
 
 template <typename Id>
-__global__ void __launch_bounds__(1024) sort_count(const SortArgs A) {
+__global__ void __launch_bounds__(kSortThreads) sort_count(const SortArgs A) {
   extern __shared__ int32_t counts[];  // [warps][E]
   const int warps = blockDim.x >> 5, wid = threadIdx.x >> 5;
   for (int x = threadIdx.x; x < warps * A.E; x += blockDim.x) counts[x] = 0;
   __syncthreads();
-  count_experts<Id>(A, (int64_t(blockIdx.x) * warps + wid) * A.steps * 32, counts + wid * A.E);
+  int e_[kLoadSteps];
+  count_experts<Id>(A, (int64_t(blockIdx.x) * warps + wid) * A.steps * 32, counts + wid * A.E, e_);
   __syncthreads();
   for (int e = threadIdx.x; e < A.E; e += blockDim.x) {
     int s = 0;
@@ -93,7 +97,7 @@ __global__ void __launch_bounds__(1024) sort_count(const SortArgs A) {
 }
 
 template <typename Id>
-__global__ void __launch_bounds__(1024) sort_place(const SortArgs A) {
+__global__ void __launch_bounds__(kSortThreads) sort_place(const SortArgs A) {
   extern __shared__ int32_t counts[];      // [warps][E]
   const int threads = blockDim.x, warps = threads >> 5, wid = threadIdx.x >> 5,
             lane = threadIdx.x & 31;
@@ -103,12 +107,21 @@ __global__ void __launch_bounds__(1024) sort_place(const SortArgs A) {
   for (int x = threadIdx.x; x < (warps + 2) * A.E; x += threads) counts[x] = 0;
   __syncthreads();
   const int64_t first = (int64_t(blockIdx.x) * warps + wid) * A.steps * 32;
-  count_experts<Id>(A, first, counts + wid * A.E);
+  int e[kLoadSteps];
+  count_experts<Id>(A, first, counts + wid * A.E, e);
   __syncthreads();
-  if (A.blocks == 1) {
-    for (int e = threadIdx.x; e < A.E; e += threads)
-      for (int w = 0; w < warps; ++w) total[e] += counts[w * A.E + e];
-  } else {
+  // the warps' counts become the pairs in the warps before; a warp an expert, a lane a warp
+  for (int e = wid; e < A.E; e += warps) {
+    const int c = lane < warps ? counts[lane * A.E + e] : 0;
+    int sum = c;
+    for (int o = 1; o < 32; o <<= 1) {
+      const int up = __shfl_up_sync(kFull, sum, o);
+      if (lane >= o) sum += up;
+    }
+    if (lane < warps) counts[lane * A.E + e] = sum - c;
+    if (A.blocks == 1 && lane == 31) total[e] = sum;
+  }
+  if (A.blocks > 1) {
     grid_wait();
     // slices of blocks side by side where there are fewer experts than threads
     const int width = A.E < threads ? A.E : threads, slices = threads / width;
@@ -143,19 +156,11 @@ __global__ void __launch_bounds__(1024) sort_place(const SortArgs A) {
     if (lane == 0) offset[A.E] = run;
   }
   __syncthreads();
-  for (int e = threadIdx.x; e < A.E; e += threads) {
-    int run = offset[e] + before[e];
-    for (int w = 0; w < warps; ++w) {
-      const int c = counts[w * A.E + e];
-      counts[w * A.E + e] = run;
-      run += c;
-    }
-  }
-  __syncthreads();
+  for (int e = lane; e < A.E; e += 32) counts[wid * A.E + e] += offset[e] + before[e];
+  __syncwarp();
   int32_t* next = counts + wid * A.E;
   for (int s0 = 0; s0 < A.steps; s0 += kLoadSteps) {
-    int e[kLoadSteps];
-    load_experts<Id>(A, first, s0, e);
+    if (A.steps > kLoadSteps) load_experts<Id>(A, first, s0, e);
 #pragma unroll
     for (int u = 0; u < kLoadSteps; ++u) {
       if (s0 + u >= A.steps) break;
@@ -271,13 +276,20 @@ __global__ void __launch_bounds__(kThreads) expert_dispatch(const RowArgs A) {
 #pragma unroll
   for (int u = 0; u < kFlight; ++u)
     if (W.in(A, u)) r[u] = __ldg(x + W.token_of(u) * A.rv + W.vec_of(u));
-  for (int k = 0; k < A.K; ++k)
+  for (int k = 0; k < A.K; k += 2) {
+    int s[kFlight][2];
 #pragma unroll
     for (int u = 0; u < kFlight; ++u)
-      if (W.in(A, u)) {
-        const int s = __ldg(A.slots + W.token_of(u) * A.K + k);
-        if (s >= 0) xs[int64_t(s) * A.rv + W.vec_of(u)] = r[u];
-      }
+#pragma unroll
+      for (int j = 0; j < 2; ++j)
+        s[u][j] = W.in(A, u) && k + j < A.K
+                      ? __ldg(A.slots + W.token_of(u) * A.K + k + j) : -1;
+#pragma unroll
+    for (int u = 0; u < kFlight; ++u)
+#pragma unroll
+      for (int j = 0; j < 2; ++j)
+        if (s[u][j] >= 0) xs[int64_t(s[u][j]) * A.rv + W.vec_of(u)] = r[u];
+  }
 }
 
 // y = residual + sum of w ys over a token's choices.
