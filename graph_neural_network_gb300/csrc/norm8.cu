@@ -12,15 +12,18 @@
 // Backward (straight through the rounding), g = dz w, y^ = y rstd:
 //   dx = dy + rstd (g - y^ mean(g y^)),  dw = sum of dz y^ over the rows
 // with mean(g y^) = rstd mean(g y): both sums of a row are again taken together.
-// dw: float32 per thread over its rows, float64 over threads and blocks, fixed order.
+// dw: float32 per thread over its rows, then float64 or compensated, in a fixed order.
 //
 // Bound: HBM.  3 s + 1 bytes an element forward (4 a group), 4 s backward.
 //
 // A row of up to 128 16-byte vectors is one warp's (a sub-group's where it is
 // narrower than 32), up to four vectors a lane and no barrier; a wider one is a
 // block's, one barrier a row.  Forward, blocks do not loop: the loads of the next
-// rows in flight are those of the other blocks on the SM.  Backward, blocks stay and
-// keep their sums of dw, and load the next row before they work on the present one.
+// rows in flight are those of the other blocks on the SM (65,536 x 4096 bfloat16, groups
+// of 128: 273 us, 6.9 TB/s; 100,003 x 128 float32: 27.7 us, 6.0 TB/s).  Backward, blocks
+// stay and keep their sums of dw in registers, and a thread copies the vectors of its next
+// rows to shared memory while it works on the present one's (30,001 x 4096 bfloat16:
+// 145 us, 6.8 TB/s).
 #include "quant8.cuh"
 
 namespace gnn {
@@ -278,82 +281,123 @@ __global__ void __launch_bounds__(kWide ? kWideThreads : kThreads)
   }
 }
 
-// Resident blocks of the backward pass that its grid is made for, on 152 SMs (a
-// constant: the workspace query asks no device).
-constexpr int kBwdBlocks = 152 * 2;
+// The backward pass is made for the blocks that are resident on 152 SMs (a constant: the
+// workspace query asks no device).
+constexpr int kSms = 152;
 
-template <typename T, int NV, bool kWide>
-__global__ void __launch_bounds__(kWide ? kWideThreads : kThreads)
-    an8_bwd(const An8Args A) {
+// 16 bytes from global to this thread's place in shared memory, zeros where !ok.
+__device__ __forceinline__ void copy_async(uint4* to, const void* from, int64_t at, bool ok) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_u32(to)),
+               "l"(static_cast<const uint4*>(from) + (ok ? at : 0)), "r"(ok ? 16 : 0)
+               : "memory");
+}
+__device__ __forceinline__ void copies_end() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int kLeft>
+__device__ __forceinline__ void copies_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(kLeft) : "memory");
+}
+
+// Rows of a thread in shared memory: one it works on, the others on their way.  Each
+// thread copies its own vectors and reads no other's, so nothing but the copies
+// themselves is waited for.
+constexpr size_t ring_bytes(int stages, int NV, int threads) {
+  return size_t(stages) * 3 * NV * threads * 16;
+}
+
+template <typename T, int NV, int S, bool kWide, int kMost, int kPerSm>
+__global__ void __launch_bounds__(kMost, kPerSm) an8_bwd(const An8Args A) {
   constexpr int V = VecOf<T>::n;
   __shared__ float buf[2][kWide ? 2 * (kWideThreads / 32) : 1];
-  extern __shared__ __align__(16) float sums[];  // [row slots][F] (rows of a warp)
+  // [S][3][NV][threads]; at the end [row slots][F] sums (rows of a warp)
+  extern __shared__ __align__(16) uint4 ring[];
   const Spot<NV, 1, kWide> P(A);
   const int slots = kWide ? 1 : kThreads >> A.tpr_log2;
   const int64_t stride = int64_t(gridDim.x) * slots;
+  const int threads = blockDim.x;
   float acc[NV][V];
 #pragma unroll
   for (int i = 0; i < NV; ++i) zero<V>(acc[i]);
-  int64_t row = P.row;
-  uint4 ry[NV], rd[NV], rz[NV];
-  const auto load = [&] {
+  // the thread's weights, where registers hold them beside its sums: read from L1 for
+  // every row they take half of its bandwidth (30,000 x 8192: 446 us instead of 301)
+  constexpr bool kHold = NV * V <= 16;
+  float held[kHold ? NV : 1][V];
+  if constexpr (kHold)
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      const int vec = P.vec + i * P.step;
+      load_w<V>(A.w, vec, A.w && vec < A.rv, held[i]);
+      if (!A.w)
+#pragma unroll
+        for (int c = 0; c < V; ++c) held[i][c] = 1.f;
+    }
+  const auto place = [&](int stage, int t, int i) {
+    return ring + ((stage * 3 + t) * NV + i) * threads + threadIdx.x;
+  };
+  const auto load = [&](int64_t row, int stage) {
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
       const int vec = P.vec + i * P.step;
       const bool ok = vec < A.rv && row < A.n;
       const int64_t at = row * A.rv + vec;
-      ry[i] = load_vec<T>(A.x, at, ok);
-      rz[i] = load_vec<T>(A.dz, at, ok);
-      rd[i] = load_vec<T>(A.o, at, ok && A.o);
+      copy_async(place(stage, 0, i), A.x, at, ok);
+      copy_async(place(stage, 1, i), A.dz, at, ok);
+      if (A.o) copy_async(place(stage, 2, i), A.o, at, ok);
     }
+    copies_end();
   };
-  load();
-  int turn = 0;
+#pragma unroll
+  for (int s = 0; s < S - 1; ++s) load(P.row + s * stride, s);
+  int turn = 0, stage = 0;
+  int64_t row = P.row;
   // every thread of the block makes the same number of turns (barriers, shuffles)
-  for (int64_t r0 = int64_t(blockIdx.x) * slots; r0 < A.n; r0 += stride) {
-    float y[NV][V], z[NV][V], d[NV][V];
-    float q[2] = {0.f, 0.f};
+  for (int64_t r0 = int64_t(blockIdx.x) * slots; r0 < A.n; r0 += stride, row += stride) {
+    copies_wait<S - 2>();
+    // into the place of the row before, which this thread has done with
+    load(row + (S - 1) * stride, stage == 0 ? S - 1 : stage - 1);
+    uint4 ry[NV], rz[NV];
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
-      unpack<T>(ry[i], y[i]);
-      unpack<T>(rz[i], z[i]);
-      unpack<T>(rd[i], d[i]);
+      ry[i] = *place(stage, 0, i);
+      rz[i] = *place(stage, 1, i);
     }
-    const int64_t now = row;
-    row += stride;
-    load();
-    const auto weigh = [&](int i, float (&g)[V]) {  // g = dz w
-      if (A.w) {
+    // g = dz w of vector i
+    const auto weigh = [&](int i, const float (&z)[V], float (&g)[V]) {
+      if constexpr (kHold) {
+#pragma unroll
+        for (int c = 0; c < V; c += 2)
+          mul2v(g[c], g[c + 1], z[c], z[c + 1], held[i][c], held[i][c + 1]);
+      } else if (A.w) {
         const int vec = P.vec + i * P.step;
         load_w<V>(A.w, vec, vec < A.rv, g);
 #pragma unroll
-        for (int c = 0; c < V; c += 2)
-          mul2v(g[c], g[c + 1], z[i][c], z[i][c + 1], g[c], g[c + 1]);
+        for (int c = 0; c < V; c += 2) mul2v(g[c], g[c + 1], z[c], z[c + 1], g[c], g[c + 1]);
       } else {
 #pragma unroll
-        for (int c = 0; c < V; ++c) g[c] = z[i][c];
+        for (int c = 0; c < V; ++c) g[c] = z[c];
       }
     };
+    float q[2], up = 1.f;
     const auto row_dots = [&] {
       q[0] = q[1] = 0.f;
 #pragma unroll
       for (int i = 0; i < NV; ++i) {
-        float g[V];
-        weigh(i, g);
-        q[0] += dot<V>(y[i], y[i]);
-        q[1] += dot<V>(g, y[i]);
+        float y[V], z[V], g[V];
+        unpack<T>(ry[i], y);
+        unpack<T>(rz[i], z);
+        scale<V>(y, up);
+        weigh(i, z, g);
+        q[0] += dot<V>(y, y);
+        q[1] += dot<V>(g, y);
       }
       uint32_t none[1] = {0u};
       over_row<kWide>(q, none, false, A.tpr_log2, buf[turn & 1]);
       ++turn;
     };
     row_dots();
-    float up = 1.f;  // rows whose sum of squares overflows: of y 2^-80
+    // rows whose sum of squares overflows: of y 2^-80
     const bool big = !(q[0] < kInf);
     if (kWide ? big : __any_sync(kFull, big)) {
       up = big ? kDown : 1.f;
-#pragma unroll
-      for (int i = 0; i < NV; ++i) scale<V>(y[i], up);
       row_dots();
     }
     const float rstd = rsqrtf(fmaf(q[0], A.inv_f, A.eps * up * up));
@@ -361,20 +405,26 @@ __global__ void __launch_bounds__(kWide ? kWideThreads : kThreads)
     const float back = rstd * up;
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
-      float g[V];
-      weigh(i, g);
-      scale<V>(y[i], rstd);  // y^
+      float y[V], z[V], g[V], d[V];
+      unpack<T>(ry[i], y);
+      unpack<T>(rz[i], z);
+      unpack<T>(A.o ? *place(stage, 2, i) : make_uint4(0, 0, 0, 0), d);
+      weigh(i, z, g);
+      scale<V>(y, up);
+      scale<V>(y, rstd);  // y^
 #pragma unroll
       for (int c = 0; c < V; c += 2) {
-        fma2(acc[i][c], acc[i][c + 1], z[i][c], z[i][c + 1], y[i][c], y[i][c + 1]);
-        fma2(g[c], g[c + 1], y[i][c], y[i][c + 1], -mean, -mean);
-        fma2(d[i][c], d[i][c + 1], g[c], g[c + 1], back, back);
+        fma2(acc[i][c], acc[i][c + 1], z[c], z[c + 1], y[c], y[c + 1]);
+        fma2(g[c], g[c + 1], y[c], y[c + 1], -mean, -mean);
+        fma2(d[c], d[c + 1], g[c], g[c + 1], back, back);
       }
       const int vec = P.vec + i * P.step;
-      if (vec < A.rv && now < A.n)
-        st16(reinterpret_cast<char*>(A.dx) + 16 * (now * A.rv + vec), pack<T>(d[i]));
+      if (vec < A.rv && row < A.n)
+        st16(reinterpret_cast<char*>(A.dx) + 16 * (row * A.rv + vec), pack<T>(d));
     }
+    stage = stage == S - 1 ? 0 : stage + 1;
   }
+  copies_wait<0>();
   let_next_start();
   if (!A.part) return;
   float* part = A.part + int64_t(blockIdx.x) * A.F;
@@ -389,7 +439,9 @@ __global__ void __launch_bounds__(kWide ? kWideThreads : kThreads)
               make_float4(acc[i][c], acc[i][c + 1], acc[i][c + 2], acc[i][c + 3]);
     }
   } else {
+    float* sums = reinterpret_cast<float*>(ring);
     const int slot = threadIdx.x >> A.tpr_log2;
+    __syncthreads();  // every thread has done with its rows
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
       const int vec = P.vec + i * P.step;
@@ -407,32 +459,36 @@ __global__ void __launch_bounds__(kWide ? kWideThreads : kThreads)
 }
 
 // dw from the blocks' sums in a fixed order: a block takes 32 channels in 32 slices of
-// the blocks.
+// the blocks.  Compensated float32 sums over a slice (a double precision addition
+// for each of them would bound the call: 17 us of 64 rows of 4096), float64 over the
+// slices.
 constexpr int kDwSlices = 32;
 __global__ void __launch_bounds__(kDwSlices * 32)
     an8_dw(const float* part, int blocks, int F, float* dw) {
-  __shared__ double t[kDwSlices][33];
+  __shared__ float t[kDwSlices][33];
   const int lane = threadIdx.x & 31, slice = threadIdx.x >> 5;
   const int f = blockIdx.x * 32 + lane;
-  double s = 0.0;
+  float s = 0.f, c = 0.f;
   grid_wait();
   if (f < F) {
-    constexpr int kLoads = (kBwdBlocks + kDwSlices - 1) / kDwSlices;
-    float v[kLoads];
+    constexpr int kLoads = 5;
+    for (int b0 = slice; b0 < blocks; b0 += kLoads * kDwSlices) {
+      float v[kLoads];
 #pragma unroll
-    for (int u = 0; u < kLoads; ++u) {
-      const int b = slice + u * kDwSlices;
-      v[u] = b < blocks ? part[int64_t(b) * F + f] : 0.f;
+      for (int u = 0; u < kLoads; ++u) {
+        const int b = b0 + u * kDwSlices;
+        v[u] = b < blocks ? part[int64_t(b) * F + f] : 0.f;
+      }
+#pragma unroll
+      for (int u = 0; u < kLoads; ++u) kahan_add(s, c, v[u]);
     }
-#pragma unroll
-    for (int u = 0; u < kLoads; ++u) s += double(v[u]);
   }
   t[slice][lane] = s;
   __syncthreads();
   if (slice != 0 || f >= F) return;
   double all = 0.0;
 #pragma unroll
-  for (int k = 0; k < kDwSlices; ++k) all += t[k][lane];
+  for (int k = 0; k < kDwSlices; ++k) all += double(t[k][lane]);
   dw[f] = float(all);
 }
 
@@ -458,7 +514,6 @@ int warp_vecs(int rv) { return rv <= 32 ? 1 : rv <= 64 ? 2 : 4; }
 constexpr int kWarpVecs = 128;  // rows of at most so many are a warp's
 int block_threads(int rv, int nv) { return ((rv + nv - 1) / nv + 31) / 32 * 32; }
 int fwd_vecs(int rv) { return rv <= 256 ? 1 : rv <= 512 ? 2 : 4; }
-int bwd_vecs(int rv) { return rv <= 256 ? 1 : rv <= 1024 ? 2 : 4; }
 
 template <typename T, bool kE4m3, int NV, int R, bool kWide>
 cudaError_t fwd(const An8Args& A, cudaStream_t st) {
@@ -483,33 +538,54 @@ cudaError_t fwd_t(const An8Args& A, cudaStream_t st) {
                    : fwd<T, kE4m3, 4, 1, false>(A, st);
 }
 
-// Blocks of the backward pass: at most kBwdBlocks, at least four rows a slot.
+// The backward pass by the width of a row (share of 6.68 TB/s at 30,000 rows and more of
+// bfloat16; in brackets another form's time against this one's, the sum of dw about 10 us
+// slower in both):
+// vectors   a row's    vectors a  threads   blocks
+// of a row  place      thread     (most)    an SM
+//   .. 32   warp       1          256       3       64 features 94 %, 256 103 %
+//   .. 64   warp       2          256       2
+//   .. 128  block      1          128       4       1024: 96 % [a warp's, 4 a thread: 321 to 263 us]
+//   .. 256  block      2          128       3       2048: 94 % [1 a thread of 256: 88 to 87]
+//   .. 512  block      2          256       2       4096: 101 % [1 a thread of 512: 178 to 153]
+//   .. 640  block      2          320       2       4104: 87 % [4 a thread of 160: 219 to 179]
+//   .. 1024 block      2          512       1       8192: 106 %
+//   .. 2048 block      4          512       1       16384: 62 %, float32 of 8192 107 %
+// Grids of more blocks than are resident end in a wave that is not full (4096: 175 to 153).
+constexpr int kBwdWarpVecs = 64;
+int bwd_per_sm(int rv) {
+  return rv <= 32 ? 3 : rv <= 64 ? 2 : rv <= 128 ? 4 : rv <= 256 ? 3 : rv <= 640 ? 2 : 1;
+}
+// Blocks: what is resident, at most; a row each where a row is a block's, otherwise at least
+// four rows a slot.
 int bwd_blocks(const An8Args& A) {
-  const int64_t slots = A.rv > kWarpVecs ? 1 : kThreads >> A.tpr_log2;
-  const int64_t want = (A.n + slots * 4 - 1) / (slots * 4);
-  return want < 1 ? 1 : want < kBwdBlocks ? int(want) : kBwdBlocks;
+  const int64_t rows = A.rv > kBwdWarpVecs ? 1 : int64_t(kThreads >> A.tpr_log2) * 4;
+  const int64_t want = (A.n + rows - 1) / rows, cap = kSms * bwd_per_sm(A.rv);
+  return want < 1 ? 1 : want < cap ? int(want) : int(cap);
 }
 
-template <typename T, int NV, bool kWide>
+template <typename T, int NV, int S, bool kWide, int kMost, int kPerSm>
 cudaError_t bwd(const An8Args& A, int blocks, cudaStream_t st) {
+  auto kernel = an8_bwd<T, NV, S, kWide, kMost, kPerSm>;
   const int threads = kWide ? block_threads(A.rv, NV) : kThreads;
-  const size_t smem = kWide || !A.part ? 0 : size_t(kThreads >> A.tpr_log2) * A.F * 4;
-  an8_bwd<T, NV, kWide><<<unsigned(blocks), threads, smem, st>>>(A);
+  // (a warp's rows' sums, 4 V NV bytes a thread, fit into the ring)
+  const size_t smem = ring_bytes(S, NV, threads);
+  const cudaError_t e = allow_smem(kernel, smem);
+  if (e != cudaSuccess) return e;
+  kernel<<<unsigned(blocks), threads, smem, st>>>(A);
   return cudaGetLastError();
 }
 
 template <typename T>
 cudaError_t bwd_t(const An8Args& A, int blocks, cudaStream_t st) {
-  if (A.rv > kWarpVecs) {
-    const int nv = bwd_vecs(A.rv);
-    return nv == 1   ? bwd<T, 1, true>(A, blocks, st)
-           : nv == 2 ? bwd<T, 2, true>(A, blocks, st)
-                     : bwd<T, 4, true>(A, blocks, st);
-  }
-  const int nv = warp_vecs(A.rv);
-  return nv == 1   ? bwd<T, 1, false>(A, blocks, st)
-         : nv == 2 ? bwd<T, 2, false>(A, blocks, st)
-                   : bwd<T, 4, false>(A, blocks, st);
+  return A.rv <= 32     ? bwd<T, 1, 3, false, 256, 3>(A, blocks, st)
+         : A.rv <= 64   ? bwd<T, 2, 3, false, 256, 2>(A, blocks, st)
+         : A.rv <= 128  ? bwd<T, 1, 3, true, 128, 4>(A, blocks, st)
+         : A.rv <= 256  ? bwd<T, 2, 3, true, 128, 3>(A, blocks, st)
+         : A.rv <= 512  ? bwd<T, 2, 3, true, 256, 2>(A, blocks, st)
+         : A.rv <= 640  ? bwd<T, 2, 3, true, 320, 2>(A, blocks, st)
+         : A.rv <= 1024 ? bwd<T, 2, 3, true, 512, 1>(A, blocks, st)
+                        : bwd<T, 4, 2, true, 512, 1>(A, blocks, st);
 }
 
 // values * scale as T: 16 bytes of T a step, kSteps of them in flight.
