@@ -283,7 +283,9 @@ gnn_status gnn_expert_combine(const gnn_experts* plan, int F, gnn_dtype dtype, c
   if (!ys || !y || !aligned(ys, 16) || !aligned(weights, 4) || !aligned(residual, 16) ||
       !aligned(y, 16))
     return GNN_ERR_INVALID_ARG;
-  return from_cuda(gnn::launch_expert_combine(*plan, F, dtype, ys, weights, residual, y,
+  int sms = 0;
+  if (!current_sms(&sms)) return GNN_ERR_CUDA;
+  return from_cuda(gnn::launch_expert_combine(*plan, F, dtype, ys, weights, residual, y, sms,
                                               static_cast<cudaStream_t>(stream)));
 }
 

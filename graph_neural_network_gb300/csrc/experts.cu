@@ -23,8 +23,8 @@ namespace {
 
 // ---- plan ---------------------------------------------------------------------
 
-constexpr int kOneBlock = 8192;   // pairs that a single block sorts
-constexpr int kBlockPairs = 2048; // pairs of a block where there are more
+constexpr int kOneBlock = 2048;   // pairs that a single block sorts, and of a block where there
+                                  // are more (8000 in one block: 16 us, in four 7 us)
 constexpr int kLoadSteps = 4;     // steps of 32 pairs a warp loads at once
 constexpr int kSortBlocks = 304;
 constexpr int kSortThreads = 512;
@@ -43,7 +43,7 @@ struct SortArgs {
 int sort_warps(int E) { return E <= 512 ? kSortThreads / 32 : 8; }
 int sort_blocks(int64_t pairs, int E) {
   if (pairs <= kOneBlock) return 1;
-  const int64_t want = (pairs + kBlockPairs - 1) / kBlockPairs, cap = 32768 / E;
+  const int64_t want = (pairs + kOneBlock - 1) / kOneBlock, cap = 32768 / E;
   const int64_t most = cap < kSortBlocks ? cap : kSortBlocks;
   return int(want < most ? want : most);
 }
@@ -233,9 +233,7 @@ __device__ __forceinline__ void zero_padding(const RowArgs& A) {
 
 // The thread's accesses: kFlight of them, of as many tokens (rows of at most a
 // warp's lanes, kWide false) or of one token (kWide).
-constexpr int kFlight = 4;
-
-template <bool kWide>
+template <bool kWide, int kFlight>
 struct Where {
   int64_t token, token_step;
   int vec, vec_step;
@@ -262,14 +260,17 @@ struct Where {
   }
 };
 
+constexpr int kDispatchFlight = 4;
+
 template <int kB, bool kWide>
 __global__ void __launch_bounds__(kThreads) expert_dispatch(const RowArgs A) {
   using Raw = typename RawOf<kB>::type;
+  constexpr int kFlight = kDispatchFlight;
   if (blockIdx.x >= A.work_blocks) {
     zero_padding<Raw>(A);
     return;
   }
-  const Where<kWide> W(A);
+  const Where<kWide, kFlight> W(A);
   const Raw* x = static_cast<const Raw*>(A.x);
   Raw* xs = static_cast<Raw*>(A.y);
   Raw r[kFlight];
@@ -292,11 +293,12 @@ __global__ void __launch_bounds__(kThreads) expert_dispatch(const RowArgs A) {
   }
 }
 
-// y = residual + sum of w ys over a token's choices.
-template <typename T, bool kWide>
-__global__ void __launch_bounds__(kThreads) expert_combine(const RowArgs A) {
+// y = residual + sum of w ys over a token's choices: kFlight accesses (Where), kC choices
+// of each at a time, kPerSm blocks on an SM.
+template <typename T, bool kWide, int kFlight, int kC, int kPerSm>
+__global__ void __launch_bounds__(kThreads, kPerSm) expert_combine(const RowArgs A) {
   constexpr int V = VecOf<T>::n;
-  const Where<kWide> W(A);
+  const Where<kWide, kFlight> W(A);
   float acc[kFlight][V];
 #pragma unroll
   for (int u = 0; u < kFlight; ++u) {
@@ -305,26 +307,30 @@ __global__ void __launch_bounds__(kThreads) expert_combine(const RowArgs A) {
       r = static_cast<const uint4*>(A.residual)[W.token_of(u) * A.rv + W.vec_of(u)];
     unpack<T>(r, acc[u]);
   }
-  for (int k = 0; k < A.K; ++k) {
-    uint4 r[kFlight];
-    float w[kFlight];
+  for (int k0 = 0; k0 < A.K; k0 += kC) {
+    uint4 r[kFlight][kC];
+    float w[kFlight][kC];
 #pragma unroll
-    for (int u = 0; u < kFlight; ++u) {
-      w[u] = 0.f;
-      r[u] = make_uint4(0, 0, 0, 0);
-      if (!W.in(A, u)) continue;
-      const int64_t at = W.token_of(u) * A.K + k;
-      const int s = __ldg(A.slots + at);
-      if (s < 0) continue;
-      w[u] = A.weights ? __ldg(A.weights + at) : 1.f;
-      r[u] = ld16(static_cast<const uint4*>(A.ys) + int64_t(s) * A.rv + W.vec_of(u));
-    }
+    for (int u = 0; u < kFlight; ++u)
 #pragma unroll
-    for (int u = 0; u < kFlight; ++u) {
-      float x[V];
-      unpack<T>(r[u], x);
-      axpy<V>(acc[u], w[u], x);
-    }
+      for (int j = 0; j < kC; ++j) {
+        w[u][j] = 0.f;
+        r[u][j] = make_uint4(0, 0, 0, 0);
+        if (!W.in(A, u) || k0 + j >= A.K) continue;
+        const int64_t at = W.token_of(u) * A.K + k0 + j;
+        const int s = __ldg(A.slots + at);
+        if (s < 0) continue;
+        w[u][j] = A.weights ? __ldg(A.weights + at) : 1.f;
+        r[u][j] = ld16(static_cast<const uint4*>(A.ys) + int64_t(s) * A.rv + W.vec_of(u));
+      }
+#pragma unroll
+    for (int u = 0; u < kFlight; ++u)
+#pragma unroll
+      for (int j = 0; j < kC; ++j) {
+        float x[V];
+        unpack<T>(r[u][j], x);
+        axpy<V>(acc[u], w[u][j], x);
+      }
   }
 #pragma unroll
   for (int u = 0; u < kFlight; ++u)
@@ -337,7 +343,7 @@ __global__ void __launch_bounds__(kThreads) expert_combine(const RowArgs A) {
 constexpr int kK = 4;
 
 template <typename T, bool kBlock>
-__global__ void __launch_bounds__(kThreads) expert_combine_bwd(const RowArgs A) {
+__global__ void __launch_bounds__(kThreads, 5) expert_combine_bwd(const RowArgs A) {
   constexpr int V = VecOf<T>::n;
   __shared__ float part[kBlock ? kWarps * kK : 1];
   if (blockIdx.x >= A.work_blocks) {
@@ -364,7 +370,7 @@ __global__ void __launch_bounds__(kThreads) expert_combine_bwd(const RowArgs A) 
       dot_[k] = 0.f;
     }
     if (on)
-#pragma unroll 2
+#pragma unroll 1
       for (int v = v0; v < A.rv; v += lanes) {
         const uint4 rd = ld16(dy + v);
         uint4 ry[kK];
@@ -418,18 +424,22 @@ RowArgs row_args(const gnn_experts& p, int rv) {
   A.K = p.choices;
   A.rv = rv;
   while ((1 << A.tpr_log2) < rv && A.tpr_log2 < 5) ++A.tpr_log2;
-  A.chunks = (rv + 32 * kFlight - 1) / (32 * kFlight);
-  A.div = A.chunks > 1 ? ~uint64_t(0) / uint64_t(A.chunks) + 1 : 0;
   A.slots = p.slots;
   A.order = p.order;
   return A;
 }
 
-// Blocks for the tokens: a warp takes a chunk of one, or kFlight of its lanes' rows.
-int64_t token_blocks(const RowArgs& A) {
+// The warps of a row for `flight` accesses of a lane.
+void fit_rows(RowArgs& A, int flight) {
+  A.chunks = (A.rv + 32 * flight - 1) / (32 * flight);
+  A.div = A.chunks > 1 ? ~uint64_t(0) / uint64_t(A.chunks) + 1 : 0;
+}
+
+// Blocks for the tokens: a warp takes a chunk of one, or `flight` rows for each sub-group.
+int64_t token_blocks(const RowArgs& A, int flight) {
   const int64_t warps = A.rv > 32 ? A.tokens * A.chunks
-                                  : (A.tokens + (kFlight << (5 - A.tpr_log2)) - 1) /
-                                        (kFlight << (5 - A.tpr_log2));
+                                  : (A.tokens + (flight << (5 - A.tpr_log2)) - 1) /
+                                        (flight << (5 - A.tpr_log2));
   return (warps + kWarps - 1) / kWarps;
 }
 
@@ -446,11 +456,27 @@ cudaError_t dispatch(const RowArgs& A, unsigned blocks, cudaStream_t st) {
   return cudaGetLastError();
 }
 
-template <typename T>
-cudaError_t combine(const RowArgs& A, unsigned blocks, cudaStream_t st) {
-  auto kernel = A.rv > 32 ? expert_combine<T, true> : expert_combine<T, false>;
-  kernel<<<blocks, kThreads, 0, st>>>(A);
+template <typename T, bool kWide, int kFlight, int kC, int kPerSm>
+cudaError_t combine(RowArgs& A, cudaStream_t st) {
+  fit_rows(A, kFlight);
+  const int64_t blocks = token_blocks(A, kFlight);
+  if (blocks > 0x7fffffff) return cudaErrorInvalidValue;
+  expert_combine<T, kWide, kFlight, kC, kPerSm><<<unsigned(blocks), kThreads, 0, st>>>(A);
   return cudaGetLastError();
+}
+
+// Rows that a warp's lanes take at once: with more than two choices a lane keeps four of
+// one token on their way (100,000 x 256 bfloat16, 8 choices: 77 us; two of two tokens 85),
+// otherwise two of two (300,000 x 64, 2 choices: 30 us; four of one 31, one of four 36).
+// Wider rows: two choices of four accesses where that makes enough warps (65,536 x 2048, 4
+// choices: 230 us; of two accesses 237), otherwise of two (1000 x 4096, 8: 10 us; of four 13).
+template <typename T>
+cudaError_t combine_t(RowArgs& A, int sm_count, cudaStream_t st) {
+  if (A.rv <= 32)
+    return A.K > 2 ? combine<T, false, 1, 4, 6>(A, st) : combine<T, false, 2, 2, 4>(A, st);
+  return A.tokens * ((A.rv + 127) / 128) >= int64_t(sm_count) * 64
+             ? combine<T, true, 4, 2, 3>(A, st)
+             : combine<T, true, 2, 2, 4>(A, st);
 }
 
 template <typename Id>
@@ -528,9 +554,10 @@ cudaError_t launch_experts_prepare(const void* ids, int id_bytes, char* buffer, 
 cudaError_t launch_expert_dispatch(const gnn_experts& p, int64_t row_bytes, int width,
                                    const void* x, void* xs, int sm_count, cudaStream_t st) {
   RowArgs A = row_args(p, int(row_bytes / width));
+  fit_rows(A, kDispatchFlight);
   A.x = x;
   A.y = xs;
-  A.work_blocks = token_blocks(A);
+  A.work_blocks = token_blocks(A, kDispatchFlight);
   const int64_t blocks = A.work_blocks + padding_blocks(A.rows, sm_count);
   if (blocks > 0x7fffffff) return cudaErrorInvalidValue;
   return width == 16  ? dispatch<16>(A, unsigned(blocks), st)
@@ -540,16 +567,14 @@ cudaError_t launch_expert_dispatch(const gnn_experts& p, int64_t row_bytes, int 
 
 cudaError_t launch_expert_combine(const gnn_experts& p, int F, gnn_dtype dt, const void* ys,
                                   const float* weights, const void* residual, void* y,
-                                  cudaStream_t st) {
+                                  int sm_count, cudaStream_t st) {
   RowArgs A = row_args(p, F * (dt == GNN_F32 ? 4 : 2) / 16);
   A.ys = ys;
   A.weights = weights;
   A.residual = residual;
   A.y = y;
-  const int64_t blocks = token_blocks(A);
-  if (blocks > 0x7fffffff) return cudaErrorInvalidValue;
-  return dt == GNN_F32 ? combine<float>(A, unsigned(blocks), st)
-                       : combine<__nv_bfloat16>(A, unsigned(blocks), st);
+  return dt == GNN_F32 ? combine_t<float>(A, sm_count, st)
+                       : combine_t<__nv_bfloat16>(A, sm_count, st);
 }
 
 cudaError_t launch_expert_combine_backward(const gnn_experts& p, int F, gnn_dtype dt,

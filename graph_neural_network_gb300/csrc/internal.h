@@ -251,7 +251,7 @@ cudaError_t launch_expert_dispatch(const gnn_experts& p, int64_t row_bytes, int 
                                    const void* x, void* xs, int sm_count, cudaStream_t st);
 cudaError_t launch_expert_combine(const gnn_experts& p, int F, gnn_dtype dt, const void* ys,
                                   const float* weights, const void* residual, void* y,
-                                  cudaStream_t st);
+                                  int sm_count, cudaStream_t st);
 cudaError_t launch_expert_combine_backward(const gnn_experts& p, int F, gnn_dtype dt,
                                            const void* dy, const void* ys, const float* weights,
                                            void* dys, float* dweights, int sm_count,

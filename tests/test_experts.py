@@ -76,7 +76,7 @@ def check_plan(ids, E, align):
 @pytest.mark.gpu
 @pytest.mark.parametrize("n, K, E", [
     (0, 2, 4), (1, 1, 1), (1, 8, 64), (31, 1, 3), (33, 3, 5), (512, 8, 64), (1024, 8, 256),
-    (4096, 2, 257), (1025, 8, 64), (2731, 3, 1024), (100, 64, 1000), (40_000, 2, 8),
+    (4096, 2, 257), (1025, 8, 64), (2731, 3, 1024), (2048, 1, 64), (683, 3, 700), (100, 64, 1000), (40_000, 2, 8),
     (300_007, 1, 1), (200_001, 4, 64), (150_000, 3, 300), (90_001, 8, 1024), (700_001, 5, 100)])
 @pytest.mark.parametrize("kind", ["even", "skewed", "dropped", "one", "none"])
 def test_plan(n, K, E, kind):
