@@ -8,14 +8,19 @@
 // in order, and a second pass ranks and writes.  Up to kOneBlock pairs a single block
 // does it all; more take a kernel that counts for each block and one that reads all
 // blocks' counts, starts early and counts its own warps meanwhile.
-// Bound: latency.  A pair costs its id twice and two writes of 4 bytes.
+// Bound: latency.  A pair costs its id twice and two writes of 4 bytes; 400,006 pairs, 16
+// experts: 9.8 us.
 //
 // Dispatch: a token's row is read once and written to the rows of its choices; padding
 // rows are found in the order (-1) by blocks of their own and written zero.  Combine:
 // the rows of a token's choices, weighted, are added in the order of its choices in
 // float32 on top of the residual, and rounded once.  Its gradient: dys = w dy and dw = dy .
 // ys in one pass, a warp (sub-group, or a block where tokens are few) a token.
-// Bound: HBM; each row is read and written once.
+// Bound: HBM; each row is read and written once.  65,536 tokens of 2048 bfloat16, 4
+// choices, of 6.68 TB/s: dispatch 228 us (90 %), combine 231 us (105 %, the residual
+// partly in L2), its gradient 371 us (99 %).  What hides the latency of the scattered
+// rows is warps more than loads of one: five blocks an SM instead of three took the
+// gradient from 437 us.
 #include "device.cuh"
 
 namespace gnn {
@@ -339,7 +344,7 @@ __global__ void __launch_bounds__(kThreads, kPerSm) expert_combine(const RowArgs
 }
 
 // dys = w dy into the rows of a token's choices, dw = dy . ys: kK choices at a time.
-// kBlock: a block takes a token; otherwise a warp or a part of one.
+// kBlock: a block takes a token, otherwise a warp.
 constexpr int kK = 4;
 
 template <typename T, bool kBlock>
@@ -351,11 +356,9 @@ __global__ void __launch_bounds__(kThreads, 5) expert_combine_bwd(const RowArgs 
     return;
   }
   const int lane = threadIdx.x & 31, wid = threadIdx.x >> 5;
-  const int lanes = kBlock ? kThreads : 1 << A.tpr_log2;
-  const int64_t token = kBlock ? int64_t(blockIdx.x)
-                               : (int64_t(blockIdx.x) * kWarps + wid) * (32 >> A.tpr_log2) +
-                                     (lane >> A.tpr_log2);
-  const int v0 = kBlock ? threadIdx.x : lane & (lanes - 1);
+  constexpr int lanes = kBlock ? kThreads : 32;
+  const int64_t token = kBlock ? int64_t(blockIdx.x) : int64_t(blockIdx.x) * kWarps + wid;
+  const int v0 = kBlock ? threadIdx.x : lane;
   const bool on = token < A.tokens;
   const uint4* dy = static_cast<const uint4*>(A.x) + token * A.rv;
   for (int k0 = 0; k0 < A.K; k0 += kK) {
@@ -395,7 +398,8 @@ __global__ void __launch_bounds__(kThreads, 5) expert_combine_bwd(const RowArgs 
         }
       }
     if (!A.dweights) continue;
-    for (int o = 1; o < (kBlock ? 32 : lanes); o <<= 1)
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1)
 #pragma unroll
       for (int k = 0; k < kK; ++k) dot_[k] += __shfl_xor_sync(kFull, dot_[k], o);
     if constexpr (kBlock) {
@@ -414,6 +418,75 @@ __global__ void __launch_bounds__(kThreads, 5) expert_combine_bwd(const RowArgs 
 #pragma unroll
       for (int k = 0; k < kK; ++k)
         if (k0 + k < A.K) A.dweights[token * A.K + k0 + k] = s[k] >= 0 ? dot_[k] : 0.f;
+  }
+}
+
+// The same for rows that the lanes of a warp, or of a part of it, take at once: kR tokens
+// and kC of their choices on their way.
+template <typename T, int kR, int kC, int kPerSm>
+__global__ void __launch_bounds__(kThreads, kPerSm) expert_combine_bwd_narrow(const RowArgs A) {
+  constexpr int V = VecOf<T>::n;
+  if (blockIdx.x >= A.work_blocks) {
+    zero_padding<uint4>(A);
+    return;
+  }
+  const Where<false, kR> W(A);
+  const int lanes = 1 << A.tpr_log2, vec = W.vec_of(0);
+  uint4 rd[kR];
+#pragma unroll
+  for (int u = 0; u < kR; ++u)
+    rd[u] = W.in(A, u) ? ld16(static_cast<const uint4*>(A.x) + W.token_of(u) * A.rv + vec)
+                       : make_uint4(0, 0, 0, 0);
+  for (int k0 = 0; k0 < A.K; k0 += kC) {
+    int s[kR][kC];
+    float w[kR][kC], sum[kR][kC];
+    uint4 ry[kR][kC];
+#pragma unroll
+    for (int u = 0; u < kR; ++u)
+#pragma unroll
+      for (int k = 0; k < kC; ++k) {
+        const bool has = W.token_of(u) < A.tokens && k0 + k < A.K;
+        const int64_t at = W.token_of(u) * A.K + k0 + k;
+        s[u][k] = has ? __ldg(A.slots + at) : -1;
+        w[u][k] = has && A.weights ? __ldg(A.weights + at) : 1.f;
+      }
+#pragma unroll
+    for (int u = 0; u < kR; ++u)
+#pragma unroll
+      for (int k = 0; k < kC; ++k)
+        ry[u][k] = s[u][k] >= 0 && A.ys && vec < A.rv
+                       ? ld16(static_cast<const uint4*>(A.ys) + int64_t(s[u][k]) * A.rv + vec)
+                       : make_uint4(0, 0, 0, 0);
+#pragma unroll
+    for (int u = 0; u < kR; ++u) {
+      float d[V];
+      unpack<T>(rd[u], d);
+#pragma unroll
+      for (int k = 0; k < kC; ++k) {
+        float y[V];
+        unpack<T>(ry[u][k], y);
+        sum[u][k] = dot<V>(d, y);
+        if (s[u][k] >= 0 && vec < A.rv) {
+#pragma unroll
+          for (int c = 0; c < V; ++c) y[c] = d[c];
+          scale<V>(y, w[u][k]);
+          st16(static_cast<uint4*>(A.y) + int64_t(s[u][k]) * A.rv + vec, pack<T>(y));
+        }
+      }
+    }
+    if (!A.dweights) continue;
+    for (int o = 1; o < lanes; o <<= 1)
+#pragma unroll
+      for (int u = 0; u < kR; ++u)
+#pragma unroll
+        for (int k = 0; k < kC; ++k) sum[u][k] += __shfl_xor_sync(kFull, sum[u][k], o);
+    if (vec == 0)
+#pragma unroll
+      for (int u = 0; u < kR; ++u)
+#pragma unroll
+        for (int k = 0; k < kC; ++k)
+          if (W.token_of(u) < A.tokens && k0 + k < A.K)
+            A.dweights[W.token_of(u) * A.K + k0 + k] = s[u][k] >= 0 ? sum[u][k] : 0.f;
   }
 }
 
@@ -477,6 +550,34 @@ cudaError_t combine_t(RowArgs& A, int sm_count, cudaStream_t st) {
   return A.tokens * ((A.rv + 127) / 128) >= int64_t(sm_count) * 64
              ? combine<T, true, 4, 2, 3>(A, st)
              : combine<T, true, 2, 2, 4>(A, st);
+}
+
+template <typename T, int kR, int kC, int kPerSm>
+cudaError_t combine_bwd_narrow(RowArgs& A, int sm_count, cudaStream_t st) {
+  A.work_blocks = token_blocks(A, kR);
+  const int64_t blocks = A.work_blocks + padding_blocks(A.rows, sm_count);
+  if (blocks > 0x7fffffff) return cudaErrorInvalidValue;
+  expert_combine_bwd_narrow<T, kR, kC, kPerSm><<<unsigned(blocks), kThreads, 0, st>>>(A);
+  return cudaGetLastError();
+}
+
+// More than two choices: four of one token on their way (100,000 x 256 bfloat16, 8
+// choices: 131 us; two of two tokens 134, four of two 142); otherwise two of two (200,003 x
+// 64 float32, 2 choices: 40 us; two of one token 44, of four 42).
+template <typename T>
+cudaError_t combine_bwd_narrow_t(RowArgs& A, int sm_count, cudaStream_t st) {
+  return A.K > 2 ? combine_bwd_narrow<T, 1, 4, 5>(A, sm_count, st)
+                 : combine_bwd_narrow<T, 2, 2, 5>(A, sm_count, st);
+}
+
+template <typename T>
+cudaError_t combine_bwd(RowArgs& A, bool block, int sm_count, cudaStream_t st) {
+  A.work_blocks = block ? A.tokens : (A.tokens + kWarps - 1) / kWarps;
+  const int64_t blocks = A.work_blocks + padding_blocks(A.rows, sm_count);
+  if (blocks > 0x7fffffff) return cudaErrorInvalidValue;
+  auto kernel = block ? expert_combine_bwd<T, true> : expert_combine_bwd<T, false>;
+  kernel<<<unsigned(blocks), kThreads, 0, st>>>(A);
+  return cudaGetLastError();
 }
 
 template <typename Id>
@@ -587,20 +688,13 @@ cudaError_t launch_expert_combine_backward(const gnn_experts& p, int F, gnn_dtyp
   A.weights = weights;
   A.y = dys;
   A.dweights = dweights;
+  if (A.rv <= 32)
+    return dt == GNN_F32 ? combine_bwd_narrow_t<float>(A, sm_count, st)
+                         : combine_bwd_narrow_t<__nv_bfloat16>(A, sm_count, st);
   // a block a token where warps would leave the GPU idle and a row keeps a block busy
   const bool block = A.rv >= 64 && A.tokens < int64_t(sm_count) * 16;
-  const int64_t per = block ? 1 : int64_t(kWarps) << (5 - A.tpr_log2);
-  A.work_blocks = (A.tokens + per - 1) / per;
-  const int64_t blocks = A.work_blocks + padding_blocks(A.rows, sm_count);
-  if (blocks > 0x7fffffff) return cudaErrorInvalidValue;
-  const unsigned g = unsigned(blocks);
-  if (dt == GNN_F32)
-    (block ? expert_combine_bwd<float, true>
-           : expert_combine_bwd<float, false>)<<<g, kThreads, 0, st>>>(A);
-  else
-    (block ? expert_combine_bwd<__nv_bfloat16, true>
-           : expert_combine_bwd<__nv_bfloat16, false>)<<<g, kThreads, 0, st>>>(A);
-  return cudaGetLastError();
+  return dt == GNN_F32 ? combine_bwd<float>(A, block, sm_count, st)
+                       : combine_bwd<__nv_bfloat16>(A, block, sm_count, st);
 }
 
 }  // namespace gnn
