@@ -1060,8 +1060,8 @@ def add_norm8_forward(x: torch.Tensor, o=None, w=None, fmt: str = "int8",
         raise ValueError(f"group must divide the {F} features of a row")
     shape = (n, F // group, group)
     if out is None:
-        out = Packed8(torch.empty(shape, dtype=_EIGHTS[fmt], device=device),
-                      torch.empty(shape[:2], dtype=torch.float32, device=device))
+        out = Packed8(x.new_empty(shape, dtype=_EIGHTS[fmt]),
+                      x.new_empty(shape[:2], dtype=torch.float32))
     else:
         if not isinstance(out, Packed8):
             raise TypeError(f"out must be a Packed8, got {type(out).__name__}")
@@ -1369,7 +1369,7 @@ class Rope:
                 0.0 if length is None else length, fast, slow, table, ctypes.byref(rule)),
                 "gnn_rope_frequencies")
         self.dim, self.layout = dim, layout
-        self.freqs = list(table)
+        self._table = table
         self.amplitude = rule.value if amplitude is None else float(amplitude)
         self._c = _native.Rope()
         _native.check(lib.gnn_rope_prepare(dim, _native.ROPE_LAYOUTS[layout], table,
@@ -1377,20 +1377,25 @@ class Rope:
                       "gnn_rope_prepare")
         self._lib = lib
 
+    @property
+    def freqs(self):
+        """Radians a position of each pair."""
+        return list(self._table)
+
 
 def _head_rows(x, name, n, D, dtype, device):
-    """The node and head strides of x [n, H, D], whose rows of D are contiguous."""
+    """H and the node and head strides of x [n, H, D], whose rows of D are contiguous."""
     if not isinstance(x, torch.Tensor) or x.dim() != 3:
         raise ValueError(f"{name} must be a tensor [{n}, H, {D}]")
-    shape = x.shape
-    if shape[0] != n or shape[2] != D:
-        raise ValueError(f"{name} must have shape [{n}, H, {D}], got {tuple(shape)}")
+    rows, H, width = x.shape
+    if rows != n or width != D:
+        raise ValueError(f"{name} must have shape [{n}, H, {D}], got {tuple(x.shape)}")
     if x.dtype != dtype or x.device != device:
         raise TypeError(f"{name} must be {dtype} on {device}, got {x.dtype} on {x.device}")
     node, head, one = x.stride()
     if one != 1 and D > 1:
         raise ValueError(f"{name} must have contiguous rows of D elements")
-    return node, head
+    return H, node, head
 
 
 def _rope_call(rope, inverse, pos, xs, out, what):
@@ -1409,23 +1414,22 @@ def _rope_call(rope, inverse, pos, xs, out, what):
     _plain_tensor(pos, "pos", (n,), torch.int32, device)
     if out is not None and len(out) != len(xs):
         raise ValueError("out must have a tensor for every tensor")
-    got, rows = [], _native.ROPE_ROWS[len(xs)]()
+    got, rows = [], []
     for k, x in enumerate(xs):
-        xn, xh = _head_rows(x, "every tensor", n, D, dtype, device)
-        H = x.shape[1]
+        H, xn, xh = _head_rows(x, "every tensor", n, D, dtype, device)
         if H < 1:
             raise ValueError("every tensor must have a head")
         if out is None:
-            y, yn, yh = torch.empty((n, H, D), dtype=dtype, device=device), H * D, D
+            y, yn, yh = x.new_empty((n, H, D)), H * D, D
         else:
             y = out[k]
-            yn, yh = _head_rows(y, "out", n, D, dtype, device)
-            if y.shape[1] != H:
+            yH, yn, yh = _head_rows(y, "out", n, D, dtype, device)
+            if yH != H:
                 raise ValueError(f"out must have shape {(n, H, D)}, got {tuple(y.shape)}")
         got.append(y)
-        rows[k] = (x.data_ptr(), y.data_ptr(), xn, xh, yn, yh, H)
+        rows += x.data_ptr(), y.data_ptr(), xn, xh, yn, yh, H
     _launch(rope._lib.gnn_rope_apply, what, device, ctypes.byref(rope._c), inverse, n, D,
-            _at(pos), len(xs), rows, dt)
+            _at(pos), len(xs), _native.ROPE_ROWS[len(xs)](*rows), dt)
     return tuple(got)
 
 
@@ -1503,7 +1507,8 @@ def expert_layer(plan: Experts, z: torch.Tensor, experts, weights=None, residual
     rows of z [N, ...] in the order of their experts, `experts` (a function of the rows
     [plan.rows, F] and the plan, whose expert e has the rows from plan.offsets[e] on,
     returning [plan.rows, F']), and back: residual plus the weighted sum over each token's
-    choices.  y and z of transformer_layer are its residual and its z."""
+    choices.  y and z of transformer_layer are its residual and its z.  (Capturing: as
+    for transformer_layer.)"""
     xs = ExpertDispatch.apply(plan, z)
     return ExpertCombine.apply(plan, experts(xs, plan), weights, residual)
 

@@ -148,7 +148,9 @@ class RopeRows(ctypes.Structure):  # gnn_rope_rows
                 ("y_head", _I64), ("H", _I32)]
 
 
-ROPE_ROWS = [RopeRows * n for n in range(9)]  # arrays of them, by length
+# Arrays of them, by length, as whole numbers of 64 bits: seven each, in the order of the
+# fields (H with its padding).
+ROPE_ROWS = [_I64 * (7 * n) for n in range(9)]
 
 
 class GnnError(RuntimeError):

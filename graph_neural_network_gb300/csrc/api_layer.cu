@@ -15,6 +15,20 @@ bool dtype_ok(gnn_dtype dt) { return dt == GNN_F32 || dt == GNN_BF16; }
 
 bool rope_dim_ok(int dim) { return dim >= 2 && dim <= GNN_ROPE_MAX_DIM && dim % 2 == 0; }
 
+// f / (2 pi) modulo 1 in 64 whole bits (|f| <= 2^30).  f is m 2^e with m of 53 bits, and
+// 1 / (2 pi) is taken to 128 bits: their product, less what lies below it, is shifted
+// right by -e >= 22.
+uint64_t turns_of(double f) {
+  constexpr uint64_t hi = 0x28be60db9391054aull, lo = 0x7f09d5f47d4d3770ull;
+  int e;
+  const uint64_t m = uint64_t(ldexp(frexp(fabs(f), &e), 53));
+  e -= 53;
+  using u128 = unsigned __int128;
+  const u128 product = u128(m) * hi + (u128(m) * lo >> 64);
+  const uint64_t t = -e < 128 ? uint64_t(product >> -e) : 0;
+  return f < 0 ? 0 - t : t;
+}
+
 bool eight_ok(gnn_eight f) { return f == GNN_INT8 || f == GNN_E4M3; }
 
 gnn_status add_norm8_check(const gnn_add_norm8* d, gnn_dtype dt) {
@@ -130,13 +144,7 @@ gnn_status gnn_rope_prepare(int dim, gnn_rope_layout layout, const double* freqs
   out->dim = dim;
   out->layout = layout;
   out->amplitude = amplitude;
-  for (int i = 0; i < dim / 2; ++i) {
-    // the fraction of a turn in [0, 1), then its first 64 bits
-    long double t = (long double)(freqs[i]) / (2.0L * 3.14159265358979323846264338327950288L);
-    t -= floorl(t);
-    const long double w = floorl(ldexpl(t, 64));
-    out->turns[i] = w >= 18446744073709551616.0L ? ~uint64_t(0) : uint64_t(w);
-  }
+  for (int i = 0; i < dim / 2; ++i) out->turns[i] = turns_of(freqs[i]);
   return GNN_OK;
 }
 
@@ -161,8 +169,8 @@ gnn_status gnn_rope_apply(const gnn_rope* rope, int inverse, int64_t n, int D, c
       return GNN_ERR_INVALID_ARG;
     if (r.x == r.y && ((n > 1 && r.x_node != r.y_node) || (r.H > 1 && r.x_head != r.y_head)))
       return GNN_ERR_INVALID_ARG;
-    for (int j = 0; j < k; ++j)
-      if (t[j].y == r.y) return GNN_ERR_INVALID_ARG;
+    for (int j = 0; j < count; ++j)  // another tensor's output or input written
+      if (j != k && (t[j].y == r.y || t[j].x == r.y)) return GNN_ERR_INVALID_ARG;
     all |= reinterpret_cast<uintptr_t>(r.x) | reinterpret_cast<uintptr_t>(r.y);
     if (n > 1) all |= uint64_t(r.x_node) * s | uint64_t(r.y_node) * s;
     if (r.H > 1) all |= uint64_t(r.x_head) * s | uint64_t(r.y_head) * s;

@@ -674,7 +674,8 @@ gnn_status gnn_expert_dispatch(const gnn_experts* plan, int64_t row_bytes, const
  * [choices], null: 1; residual: dtype [tokens][F], null: 0.  Dropped pairs add nothing,
  * whatever their weights.  Without weights and residual it is the gradient of
  * gnn_expert_dispatch.  F * sizeof(dtype) a multiple of 16, at most 2^20; ys [rows][F].
- * ys, residual, y: 16-byte aligned; y may be residual.  Bitwise reproducible. */
+ * ys, residual, y: 16-byte aligned; y may be residual, no output of these calls may
+ * overlap an input otherwise.  Bitwise reproducible. */
 gnn_status gnn_expert_combine(const gnn_experts* plan, int F, gnn_dtype dtype, const void* ys,
                               const float* weights, const void* residual, void* y, void* stream);
 

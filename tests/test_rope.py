@@ -119,11 +119,21 @@ def test_refusals_on_the_host():
     rope = gnn.Rope(8)
     P = 4096
 
+    assert ctypes.sizeof(_native.RopeRows) == 56
+
+    def packed(rows):    # as the binding lays them out
+        whole = _native.ROPE_ROWS[len(rows)]()
+        ctypes.memmove(whole, (_native.RopeRows * len(rows))(*rows), ctypes.sizeof(whole))
+        return whole
+
+    one = _native.RopeRows(1, 2, 3, 4, 5, 6, 7)
+    assert list(packed([one])) == [1, 2, 3, 4, 5, 6, 7]
+
     def call(rows=None, n=4, D=16, pos=P, count=None, dt=0, inverse=0, c=rope._c):
         rows = [_native.RopeRows(P, 2 * P, 32, 16, 32, 16, 2)] if rows is None else rows
         return lib.gnn_rope_apply(None if c is None else ctypes.byref(c), inverse, n, D, pos,
                                   len(rows) if count is None else count,
-                                  _native.ROPE_ROWS[len(rows)](*rows), dt, None)
+                                  packed(rows), dt, None)
 
     bad = _native.ERR_INVALID_ARG
     assert call(n=0) == _native.OK and call(n=0, pos=None) == _native.OK
@@ -141,6 +151,9 @@ def test_refusals_on_the_host():
         assert call([row]) == bad
     twice = R(P, 2 * P, 32, 16, 32, 16, 2)
     assert call([twice, twice]) == bad
+    # an output that is another tensor's input: both calls would read what the other writes
+    there, back = R(P, 2 * P, 32, 16, 32, 16, 2), R(2 * P, P, 32, 16, 32, 16, 2)
+    assert call([there, back]) == bad and call([R(P, P, 32, 16, 32, 16, 2), there]) == bad
     broken = _native.Rope.from_buffer_copy(rope._c)
     broken.dim = 7
     assert call(c=broken) == bad
