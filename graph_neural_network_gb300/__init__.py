@@ -1060,8 +1060,8 @@ def add_norm8_forward(x: torch.Tensor, o=None, w=None, fmt: str = "int8",
         raise ValueError(f"group must divide the {F} features of a row")
     shape = (n, F // group, group)
     if out is None:
-        out = Packed8(x.new_empty(shape, dtype=_EIGHTS[fmt]),
-                      x.new_empty(shape[:2], dtype=torch.float32))
+        out = Packed8(torch.empty(shape, dtype=_EIGHTS[fmt], device=device),
+                      torch.empty(shape[:2], dtype=torch.float32, device=device))
     else:
         if not isinstance(out, Packed8):
             raise TypeError(f"out must be a Packed8, got {type(out).__name__}")
@@ -1420,7 +1420,7 @@ def _rope_call(rope, inverse, pos, xs, out, what):
         if H < 1:
             raise ValueError("every tensor must have a head")
         if out is None:
-            y, yn, yh = x.new_empty((n, H, D)), H * D, D
+            y, yn, yh = torch.empty((n, H, D), dtype=dtype, device=device), H * D, D
         else:
             y = out[k]
             yH, yn, yh = _head_rows(y, "out", n, D, dtype, device)

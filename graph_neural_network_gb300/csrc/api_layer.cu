@@ -177,8 +177,10 @@ gnn_status gnn_rope_apply(const gnn_rope* rope, int inverse, int64_t n, int D, c
   }
   if (n == 0) return GNN_OK;
   if (!pos || !aligned(pos, 4)) return GNN_ERR_INVALID_ARG;
+  int sms = 0;
+  if (!current_sms(&sms)) return GNN_ERR_CUDA;
   const int width = int(all & (~all + 1));  // the lowest bit set: at most 16
-  return from_cuda(gnn::launch_rope(*rope, inverse, n, D, pos, count, t, dtype, width,
+  return from_cuda(gnn::launch_rope(*rope, inverse, n, D, pos, count, t, dtype, width, sms,
                                     static_cast<cudaStream_t>(stream)));
 }
 

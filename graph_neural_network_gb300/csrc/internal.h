@@ -237,7 +237,7 @@ cudaError_t launch_unpack8_groups(int64_t groups, int group, gnn_eight fmt, gnn_
 // Rotary positions (rope.cu): count tensors, `width` bytes an access (16, 8, 4 or 2).
 constexpr int kRopeMax = 8;  // tensors of one call
 cudaError_t launch_rope(const gnn_rope& rope, int inverse, int64_t n, int D, const int32_t* pos,
-                        int count, const gnn_rope_rows* t, gnn_dtype dt, int width,
+                        int count, const gnn_rope_rows* t, gnn_dtype dt, int width, int sm_count,
                         cudaStream_t st);
 
 // Tokens in the order of their experts (experts.cu).

@@ -14,7 +14,9 @@
 // turns.  A thread then turns a slot (two accesses of `width` bytes, the partners of
 // their pairs) of one head in each tensor, or of several heads, its loads issued
 // before the block computes.  Slots of a node, then its heads, stand side by side
-// over the threads, so that accesses are whole lines.
+// over the threads, so that accesses are whole lines.  300,000 nodes, 4 + 4 heads of 64
+// (32 turned) out of a fused projection, bfloat16: 103 us, 6.0 TB/s; 1,000,003 nodes, 8 + 8
+// heads of 16: 164 us, 6.3 TB/s.
 #include "device.cuh"
 
 namespace gnn {
@@ -89,11 +91,13 @@ __device__ __forceinline__ void turn_pair(float a, float b, float co, float si, 
   g = __fmaf_rn(a, si, __fmul_rn(b, co));
 }
 
-constexpr int kRopeUnroll = 2;  // tensors in flight
+constexpr int kRopeUnroll = 2;  // heads in flight
 
-// kMixed: pairs of neighbours (GNN_ROPE_INTERLEAVED).
-template <typename T, int kB, bool kMixed>
-__global__ void __launch_bounds__(kThreads, 5) rope_rows(const __grid_constant__ RopeArgs A) {
+// kMixed: pairs of neighbours (GNN_ROPE_INTERLEAVED).  kRounds: tensors of different
+// numbers of heads, taken one after the other in rounds of `lanes` heads; otherwise every
+// tensor has a head for (almost) every lane, and two tensors' heads are taken at once.
+template <typename T, int kB, bool kMixed, bool kRounds>
+__global__ void __launch_bounds__(kThreads, kRounds ? 4 : 5) rope_rows(const __grid_constant__ RopeArgs A) {
   using Vec = RopeVec<T, kB>;
   using Raw = typename Access<kB>::type;
   constexpr int V = Vec::n;
@@ -120,115 +124,169 @@ __global__ void __launch_bounds__(kThreads, 5) rope_rows(const __grid_constant__
       a = A.dim + 2 * (int(slot) - A.turned) * V;
       b = a + V < A.D ? a + V : -1;
     }
-    for (int h = 0; h < A.heads; h += A.lanes)
-      for (int k = 0; k < A.count; k += kRopeUnroll) {
-        Vec va[kRopeUnroll], vb[kRopeUnroll];
-        bool go[kRopeUnroll];
+    // heads h[u] + lane of the tensors k[u] (none from A.count on)
+    const auto take = [&](const int (&k)[kRopeUnroll], const int (&h)[kRopeUnroll]) {
+      Vec va[kRopeUnroll], vb[kRopeUnroll];
+      bool go[kRopeUnroll];
 #pragma unroll
-        for (int u = 0; u < kRopeUnroll; ++u) {
-          go[u] = false;
-          if (k + u < A.count) {
-            const gnn_rope_rows& t = A.t[k + u];
-            go[u] = on && h + lane < t.H && (turn || t.x != t.y);
-            const T* x = static_cast<const T*>(t.x) + node * t.x_node + (h + lane) * t.x_head;
-            if (go[u]) va[u].raw = *reinterpret_cast<const Raw*>(x + a);
-            if (go[u] && b >= 0) vb[u].raw = *reinterpret_cast<const Raw*>(x + b);
-          }
-        }
-        if (!ready) {
-          ready = true;
-          for (int e = threadIdx.x; e < A.half << A.nodes_log2; e += blockDim.x) {
-            const int i = e >> A.nodes_log2, at = e - (i << A.nodes_log2);
-            if (at >= nodes) continue;
-            const uint64_t left = uint64_t(int64_t(__ldg(A.pos + first + at))) * A.turns[i];
-            const float x =
-                float(int32_t(uint32_t(left >> 32))) * 4.656612873077393e-10f;  // 2^-31
-            float si, co;
-            sincospif(x, &si, &co);
-            float* to = table + 2 * P * (((i / P) << A.nodes_log2) + at) + i % P;
-            to[0] = co * A.amplitude;
-            to[P] = si * A.sine;
-          }
-          __syncthreads();
-        }
-        if (turn) {
-          const float* cs = table + 2 * P * ((int(slot) * (V / P) << A.nodes_log2) + local);
-          float co[V], si[V];
-#pragma unroll
-          for (int c = 0; c < V; c += P) {
-            const float* at = cs + 2 * P * ((c / P) << A.nodes_log2);
-            if constexpr (P == 2) {
-              const float4 q = *reinterpret_cast<const float4*>(at);
-              co[c] = q.x;
-              co[c + 1] = q.y;
-              si[c] = q.z;
-              si[c + 1] = q.w;
-            } else {
-              const float2 q = *reinterpret_cast<const float2*>(at);
-              co[c] = q.x;
-              si[c] = q.y;
-            }
-          }
-#pragma unroll
-          for (int u = 0; u < kRopeUnroll; ++u) {
-            if (!go[u]) continue;
-            float x[V], y[V], f[V], g[V];
-            va[u].get(x);
-            vb[u].get(y);
-            if constexpr (kMixed && V > 1) {
-              // pairs (0, 1), (2, 3) .. of the first access, then of the second
-#pragma unroll
-              for (int c = 0; c < V / 2; ++c) {
-                turn_pair(x[2 * c], x[2 * c + 1], co[c], si[c], f[2 * c], f[2 * c + 1]);
-                turn_pair(y[2 * c], y[2 * c + 1], co[V / 2 + c], si[V / 2 + c], g[2 * c],
-                          g[2 * c + 1]);
-              }
-            } else if constexpr (V > 1) {
-              // turn_pair, two at a time
-#pragma unroll
-              for (int c = 0; c < V; c += 2) {
-                float s0, s1;
-                mul2v(s0, s1, y[c], y[c + 1], si[c], si[c + 1]);
-                f[c] = -s0;
-                f[c + 1] = -s1;
-                fma2(f[c], f[c + 1], x[c], x[c + 1], co[c], co[c + 1]);
-                mul2v(g[c], g[c + 1], y[c], y[c + 1], co[c], co[c + 1]);
-                fma2(g[c], g[c + 1], x[c], x[c + 1], si[c], si[c + 1]);
-              }
-            } else {
-              turn_pair(x[0], y[0], co[0], si[0], f[0], g[0]);
-            }
-            va[u].set(f);
-            vb[u].set(g);
-          }
-        }
-#pragma unroll
-        for (int u = 0; u < kRopeUnroll; ++u) {
-          if (k + u >= A.count) continue;
-          const gnn_rope_rows& t = A.t[k + u];
-          T* y = static_cast<T*>(t.y) + node * t.y_node + (h + lane) * t.y_head;
-          if (go[u]) *reinterpret_cast<Raw*>(y + a) = va[u].raw;
-          if (go[u] && b >= 0) *reinterpret_cast<Raw*>(y + b) = vb[u].raw;
+      for (int u = 0; u < kRopeUnroll; ++u) {
+        go[u] = false;
+        if (k[u] < A.count) {
+          const gnn_rope_rows& t = A.t[k[u]];
+          go[u] = on && h[u] + lane < t.H && (turn || t.x != t.y);  // in place: nothing to copy
+          const T* x = static_cast<const T*>(t.x) + node * t.x_node + (h[u] + lane) * t.x_head;
+          if (go[u]) va[u].raw = *reinterpret_cast<const Raw*>(x + a);
+          if (go[u] && b >= 0) vb[u].raw = *reinterpret_cast<const Raw*>(x + b);
         }
       }
+      if (!ready) {
+        ready = true;
+        for (int e = threadIdx.x; e < A.half << A.nodes_log2; e += blockDim.x) {
+          const int i = e >> A.nodes_log2, at = e - (i << A.nodes_log2);
+          if (at >= nodes) continue;
+          const uint64_t left = uint64_t(int64_t(__ldg(A.pos + first + at))) * A.turns[i];
+          const float x =
+              float(int32_t(uint32_t(left >> 32))) * 4.656612873077393e-10f;  // 2^-31
+          float si, co;
+          sincospif(x, &si, &co);
+          float* to = table + 2 * P * (((i / P) << A.nodes_log2) + at) + i % P;
+          to[0] = co * A.amplitude;
+          to[P] = si * A.sine;
+        }
+        __syncthreads();
+      }
+      if (turn) {
+        // (a thread behind the last node reads inside the table too, for nothing)
+        const float* cs = table + 2 * P * ((int(slot) * (V / P) << A.nodes_log2) + local);
+        float co[V], si[V];
+#pragma unroll
+        for (int c = 0; c < V; c += P) {
+          const float* at = cs + 2 * P * ((c / P) << A.nodes_log2);
+          if constexpr (P == 2) {
+            const float4 q = *reinterpret_cast<const float4*>(at);
+            co[c] = q.x;
+            co[c + 1] = q.y;
+            si[c] = q.z;
+            si[c + 1] = q.w;
+          } else {
+            const float2 q = *reinterpret_cast<const float2*>(at);
+            co[c] = q.x;
+            si[c] = q.y;
+          }
+        }
+#pragma unroll
+        for (int u = 0; u < kRopeUnroll; ++u) {
+          if (!go[u]) continue;
+          float x[V], y[V], f[V], g[V];
+          va[u].get(x);
+          vb[u].get(y);
+          if constexpr (kMixed && V > 1) {
+            // pairs (0, 1), (2, 3) .. of the first access, then of the second
+#pragma unroll
+            for (int c = 0; c < V / 2; ++c) {
+              turn_pair(x[2 * c], x[2 * c + 1], co[c], si[c], f[2 * c], f[2 * c + 1]);
+              turn_pair(y[2 * c], y[2 * c + 1], co[V / 2 + c], si[V / 2 + c], g[2 * c],
+                        g[2 * c + 1]);
+            }
+          } else if constexpr (V > 1) {
+            // turn_pair, two at a time
+#pragma unroll
+            for (int c = 0; c < V; c += 2) {
+              float s0, s1;
+              mul2v(s0, s1, y[c], y[c + 1], si[c], si[c + 1]);
+              f[c] = -s0;
+              f[c + 1] = -s1;
+              fma2(f[c], f[c + 1], x[c], x[c + 1], co[c], co[c + 1]);
+              mul2v(g[c], g[c + 1], y[c], y[c + 1], co[c], co[c + 1]);
+              fma2(g[c], g[c + 1], x[c], x[c + 1], si[c], si[c + 1]);
+            }
+          } else {
+            turn_pair(x[0], y[0], co[0], si[0], f[0], g[0]);
+          }
+          va[u].set(f);
+          vb[u].set(g);
+        }
+      }
+#pragma unroll
+      for (int u = 0; u < kRopeUnroll; ++u) {
+        if (k[u] >= A.count) continue;
+        const gnn_rope_rows& t = A.t[k[u]];
+        T* y = static_cast<T*>(t.y) + node * t.y_node + (h[u] + lane) * t.y_head;
+        if (go[u]) *reinterpret_cast<Raw*>(y + a) = va[u].raw;
+        if (go[u] && b >= 0) *reinterpret_cast<Raw*>(y + b) = vb[u].raw;
+      }
+    };
+    // (the counts are the same in every thread: the first call ends in a barrier)
+    if constexpr (kRounds) {
+      int k = 0, h = 0;
+      while (k < A.count) {
+        int ks[kRopeUnroll], hs[kRopeUnroll];
+#pragma unroll
+        for (int u = 0; u < kRopeUnroll; ++u) {
+          ks[u] = k;
+          hs[u] = h;
+          h += A.lanes;
+          if (k < A.count && h >= A.t[k].H) {
+            h = 0;
+            ++k;
+          }
+        }
+        take(ks, hs);
+      }
+    } else {
+      for (int h = 0; h < A.heads; h += A.lanes)
+        for (int k = 0; k < A.count; k += kRopeUnroll) {
+          const int ks[kRopeUnroll] = {k, k + 1};
+          const int hs[kRopeUnroll] = {h, h};
+          take(ks, hs);
+        }
+    }
   }
 }
 
+// Heads side by side: as many as the widest tensor has (and a block room for), or, where
+// nodes make enough threads without and over a quarter of the lanes had no head then, the
+// number that leaves the fewest without; whole lines in any case (eight threads take 256
+// bytes).  100,000 nodes, 32 + 8 heads of 128 bfloat16: 353 us with 8, 421 with 32.
+int lanes_of(const RopeArgs& A, int widest, int sm_count) {
+  const auto taken = [&](int lanes) {
+    int64_t n = 0;
+    for (int k = 0; k < A.count; ++k) n += (A.t[k].H + lanes - 1) / lanes * lanes;
+    return n;
+  };
+  int64_t heads = 0;
+  for (int k = 0; k < A.count; ++k) heads += A.t[k].H;
+  int best = widest;
+  int64_t least = taken(widest);
+  if (4 * least <= 5 * heads) return widest;
+  for (int lanes = widest - 1; lanes >= 1; --lanes) {
+    const int64_t threads = int64_t(A.slots) * lanes;
+    if (threads < 8 || A.n * threads < int64_t(sm_count) * 1024) break;
+    if (taken(lanes) < least) {
+      least = taken(lanes);
+      best = lanes;
+    }
+  }
+  return best;
+}
+
 template <typename T, int kB>
-cudaError_t launch(RopeArgs& A, bool mixed, cudaStream_t st) {
+cudaError_t launch(RopeArgs& A, bool mixed, int sm_count, cudaStream_t st) {
   constexpr int V = RopeVec<T, kB>::n;
   A.turned = A.half / V;
   A.slots = uint32_t(A.turned + (A.D - A.dim + 2 * V - 1) / (2 * V));
-  // as many heads side by side as there are, and as a block has threads
-  const int most = A.slots < kThreads ? kThreads / int(A.slots) : 1;
-  A.lanes = most < A.heads ? most : A.heads;
+  const int all = A.slots < kThreads ? kThreads / int(A.slots) : 1;
+  const int widest = all < A.heads ? all : A.heads;
+  A.lanes = lanes_of(A, widest, sm_count);
+  const bool rounds = A.lanes < widest;
   A.per = A.slots * uint32_t(A.lanes);
   A.div_per = 65535 / A.per + 1;
   A.div_slots = 65535 / A.slots + 1;
   while ((A.per << (A.nodes_log2 + 1)) <= kThreads) ++A.nodes_log2;
   const int64_t blocks = (A.n + (int64_t(1) << A.nodes_log2) - 1) >> A.nodes_log2;
   const uint32_t threads = A.per > kThreads ? kThreads : ((A.per << A.nodes_log2) + 31) / 32 * 32;
-  auto kernel = mixed ? rope_rows<T, kB, true> : rope_rows<T, kB, false>;
+  auto kernel = mixed ? (rounds ? rope_rows<T, kB, true, true> : rope_rows<T, kB, true, false>)
+                      : (rounds ? rope_rows<T, kB, false, true> : rope_rows<T, kB, false, false>);
   kernel<<<unsigned(blocks), threads, 0, st>>>(A);
   return cudaGetLastError();
 }
@@ -236,7 +294,7 @@ cudaError_t launch(RopeArgs& A, bool mixed, cudaStream_t st) {
 }  // namespace
 
 cudaError_t launch_rope(const gnn_rope& rope, int inverse, int64_t n, int D, const int32_t* pos,
-                        int count, const gnn_rope_rows* t, gnn_dtype dt, int width,
+                        int count, const gnn_rope_rows* t, gnn_dtype dt, int width, int sm_count,
                         cudaStream_t st) {
   RopeArgs A{};
   A.n = n;
@@ -254,13 +312,13 @@ cudaError_t launch_rope(const gnn_rope& rope, int inverse, int64_t n, int D, con
   }
   for (int i = 0; i < A.half; ++i) A.turns[i] = rope.turns[i];
   if (dt == GNN_F32)
-    return width == 16  ? launch<float, 16>(A, mixed, st)
-           : width == 8 ? launch<float, 8>(A, mixed, st)
-                        : launch<float, 4>(A, mixed, st);
-  return width == 16  ? launch<__nv_bfloat16, 16>(A, mixed, st)
-         : width == 8 ? launch<__nv_bfloat16, 8>(A, mixed, st)
-         : width == 4 ? launch<__nv_bfloat16, 4>(A, mixed, st)
-                      : launch<__nv_bfloat16, 2>(A, mixed, st);
+    return width == 16  ? launch<float, 16>(A, mixed, sm_count, st)
+           : width == 8 ? launch<float, 8>(A, mixed, sm_count, st)
+                        : launch<float, 4>(A, mixed, sm_count, st);
+  return width == 16  ? launch<__nv_bfloat16, 16>(A, mixed, sm_count, st)
+         : width == 8 ? launch<__nv_bfloat16, 8>(A, mixed, sm_count, st)
+         : width == 4 ? launch<__nv_bfloat16, 4>(A, mixed, sm_count, st)
+                      : launch<__nv_bfloat16, 2>(A, mixed, sm_count, st);
 }
 
 }  // namespace gnn
