@@ -1477,12 +1477,7 @@ def transformer_layer(g: Graph, x: torch.Tensor, q: torch.Tensor, key: torch.Ten
     norm, gate, residual scale and sum with x, and the norm before the next
     layer.  Returns (y, z) as norm_residual_forward does.  checkpoint8: the
     attention keeps 8-bit checkpoints of q, key and val for its backward pass
-    instead of the tensors.  rope and pos [N] int32: the sum with the residual and its root-mean-square norm in 8 bits, for a projection's input:
-
-    y, z8 = add_norm8_forward(x, o, w, fmt="e4m3", group=128)   # z8: values and scales
-    dx, dw = add_norm8_backward(y, dy, dz, w)
-
-rotary positions of q and key
+    instead of the tensors.  rope and pos [N] int32: rotary positions of q and key
     before the attention.  To capture a training step into a CUDA graph, let no
     eager autograd graph of the same leaves be alive (torch would order the
     captured gradients behind the eager stream)."""

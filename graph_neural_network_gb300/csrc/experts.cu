@@ -204,6 +204,7 @@ struct RowArgs {
   int tpr_log2;       // lanes of a row
   int chunks;         // of a row, a warp each (rows wider than a warp takes at once)
   uint64_t div;       // ceil(2^64 / chunks), 0 for 1: warp * div / 2^64 is its token
+  int pad_rows;       // rows of the order that a warp looks at at once
   int64_t work_blocks;  // blocks that take tokens; those behind them take padding rows
   const int32_t *slots, *order;
   const float* weights;
@@ -221,18 +222,15 @@ struct RawOf<8> { using type = uint2; };
 template <>
 struct RawOf<4> { using type = uint32_t; };
 
-// Zeros in the rows of the order without a pair: kPadRows rows a warp and turn, whose
-// lanes look at the order for them (of few rows each, as padding lies together: 1351
-// tokens in 15,000 rows of 14 KB, 114 us with 32 rows a warp).
-constexpr int kPadRows = 4;
-
+// Zeros in the rows of the order without a pair: pad_rows of them a warp and turn, whose
+// lanes look at the order for them.
 template <typename Raw>
 __device__ __forceinline__ void zero_padding(const RowArgs& A) {
   const int lane = threadIdx.x & 31;
   const int64_t warps = (int64_t(gridDim.x) - A.work_blocks) * kWarps;
   const int64_t w0 = (int64_t(blockIdx.x) - A.work_blocks) * kWarps + (threadIdx.x >> 5);
-  for (int64_t r0 = w0 * kPadRows; r0 < A.rows; r0 += warps * kPadRows) {
-    const bool pad = lane < kPadRows && r0 + lane < A.rows && __ldg(A.order + r0 + lane) < 0;
+  for (int64_t r0 = w0 * A.pad_rows; r0 < A.rows; r0 += warps * A.pad_rows) {
+    const bool pad = lane < A.pad_rows && r0 + lane < A.rows && __ldg(A.order + r0 + lane) < 0;
     for (unsigned left = __ballot_sync(kFull, pad); left; left &= left - 1) {
       Raw* row = static_cast<Raw*>(A.y) + (r0 + __ffs(left) - 1) * A.rv;
       for (int v = lane; v < A.rv; v += 32) row[v] = Raw{};
@@ -501,6 +499,10 @@ RowArgs row_args(const gnn_experts& p, int rv) {
   A.K = p.choices;
   A.rv = rv;
   while ((1 << A.tpr_log2) < rv && A.tpr_log2 < 5) ++A.tpr_log2;
+  // padding lies together: a warp looks at few rows where a row is much to write (1351
+  // tokens in 15,000 rows of 14 KB: 81 us with 4, 114 with 32), at many where it is not
+  // (200,003 tokens in 402,000 rows of 256 bytes: 31 us with 32, 33 with 4)
+  A.pad_rows = rv >= 128 ? 4 : rv <= 16 ? 32 : 512 / rv;
   A.slots = p.slots;
   A.order = p.order;
   return A;
@@ -521,8 +523,8 @@ int64_t token_blocks(const RowArgs& A, int flight) {
 }
 
 // Blocks for the padding: up to two turns of what is resident.
-int64_t padding_blocks(int64_t rows, int sm_count) {
-  const int64_t want = (rows + kPadRows * kWarps - 1) / (kPadRows * kWarps);
+int64_t padding_blocks(const RowArgs& A, int sm_count) {
+  const int64_t want = (A.rows + A.pad_rows * kWarps - 1) / (A.pad_rows * kWarps);
   const int64_t cap = int64_t(sm_count) * 16;
   return want < cap ? want : cap;
 }
@@ -546,13 +548,14 @@ cudaError_t combine(RowArgs& A, cudaStream_t st) {
 // Rows that a warp's lanes take at once: with more than two choices a lane keeps four of
 // one token on their way (100,000 x 256 bfloat16, 8 choices: 77 us; two of two tokens 85),
 // otherwise two of two (300,000 x 64, 2 choices: 30 us; four of one 31, one of four 36).
-// Wider rows: two choices of four accesses where that makes enough warps (65,536 x 2048, 4
-// choices: 230 us; of two accesses 237), otherwise of two (1000 x 4096, 8: 10 us; of four 13).
+// Wider rows: two choices of four accesses where a row has them and that makes enough
+// warps (65,536 x 2048, 4 choices: 230 us; of two accesses 237), otherwise of two (1000 x
+// 4096, 8 choices: 10 us; of four 13).
 template <typename T>
 cudaError_t combine_t(RowArgs& A, int sm_count, cudaStream_t st) {
   if (A.rv <= 32)
     return A.K > 2 ? combine<T, false, 1, 4, 6>(A, st) : combine<T, false, 2, 2, 4>(A, st);
-  return A.tokens * ((A.rv + 127) / 128) >= int64_t(sm_count) * 64
+  return A.rv > 64 && A.tokens * ((A.rv + 127) / 128) >= int64_t(sm_count) * 64
              ? combine<T, true, 4, 2, 3>(A, st)
              : combine<T, true, 2, 2, 4>(A, st);
 }
@@ -560,7 +563,7 @@ cudaError_t combine_t(RowArgs& A, int sm_count, cudaStream_t st) {
 template <typename T, int kR, int kC, int kPerSm>
 cudaError_t combine_bwd_narrow(RowArgs& A, int sm_count, cudaStream_t st) {
   A.work_blocks = token_blocks(A, kR);
-  const int64_t blocks = A.work_blocks + padding_blocks(A.rows, sm_count);
+  const int64_t blocks = A.work_blocks + padding_blocks(A, sm_count);
   if (blocks > 0x7fffffff) return cudaErrorInvalidValue;
   expert_combine_bwd_narrow<T, kR, kC, kPerSm><<<unsigned(blocks), kThreads, 0, st>>>(A);
   return cudaGetLastError();
@@ -578,7 +581,7 @@ cudaError_t combine_bwd_narrow_t(RowArgs& A, int sm_count, cudaStream_t st) {
 template <typename T>
 cudaError_t combine_bwd(RowArgs& A, bool block, int sm_count, cudaStream_t st) {
   A.work_blocks = block ? A.tokens : (A.tokens + kWarps - 1) / kWarps;
-  const int64_t blocks = A.work_blocks + padding_blocks(A.rows, sm_count);
+  const int64_t blocks = A.work_blocks + padding_blocks(A, sm_count);
   if (blocks > 0x7fffffff) return cudaErrorInvalidValue;
   auto kernel = block ? expert_combine_bwd<T, true> : expert_combine_bwd<T, false>;
   kernel<<<unsigned(blocks), kThreads, 0, st>>>(A);
@@ -664,7 +667,7 @@ cudaError_t launch_expert_dispatch(const gnn_experts& p, int64_t row_bytes, int 
   A.x = x;
   A.y = xs;
   A.work_blocks = token_blocks(A, kDispatchFlight);
-  const int64_t blocks = A.work_blocks + padding_blocks(A.rows, sm_count);
+  const int64_t blocks = A.work_blocks + padding_blocks(A, sm_count);
   if (blocks > 0x7fffffff) return cudaErrorInvalidValue;
   return width == 16  ? dispatch<16>(A, unsigned(blocks), st)
          : width == 8 ? dispatch<8>(A, unsigned(blocks), st)
@@ -697,7 +700,9 @@ cudaError_t launch_expert_combine_backward(const gnn_experts& p, int F, gnn_dtyp
     return dt == GNN_F32 ? combine_bwd_narrow_t<float>(A, sm_count, st)
                          : combine_bwd_narrow_t<__nv_bfloat16>(A, sm_count, st);
   // a block a token where warps would leave the GPU idle and a row keeps a block busy
-  const bool block = A.rv >= 64 && A.tokens < int64_t(sm_count) * 16;
+  // (bfloat16: 1000 x 2048, 5 choices 10 us, 14 with a warp; 1000 x 512, 2 choices 5, 4 with a
+  // warp; 4000 x 2048 38, 41 with a warp)
+  const bool block = A.rv >= 256 && A.tokens < int64_t(sm_count) * 16;
   return dt == GNN_F32 ? combine_bwd<float>(A, block, sm_count, st)
                        : combine_bwd<__nv_bfloat16>(A, block, sm_count, st);
 }
