@@ -291,7 +291,9 @@ __device__ __forceinline__ void copy_async(uint4* to, const void* from, int64_t 
                "l"(static_cast<const uint4*>(from) + (ok ? at : 0)), "r"(ok ? 16 : 0)
                : "memory");
 }
-__device__ __forceinline__ void copies_end() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+__device__ __forceinline__ void copies_end() {
+  asm volatile("cp.async.commit_group;" ::: "memory");
+}
 template <int kLeft>
 __device__ __forceinline__ void copies_wait() {
   asm volatile("cp.async.wait_group %0;" ::"n"(kLeft) : "memory");
@@ -304,7 +306,9 @@ constexpr size_t ring_bytes(int stages, int NV, int threads) {
   return size_t(stages) * 3 * NV * threads * 16;
 }
 
-template <typename T, int NV, int S, bool kWide, int kMost, int kPerSm>
+// kReread: the rows are read from shared memory for each of the two looks at them (their
+// registers go to the sums and weights of rows of four vectors, or to a third block).
+template <typename T, int NV, int S, bool kWide, bool kReread, int kMost, int kPerSm>
 __global__ void __launch_bounds__(kMost, kPerSm) an8_bwd(const An8Args A) {
   constexpr int V = VecOf<T>::n;
   __shared__ float buf[2][kWide ? 2 * (kWideThreads / 32) : 1];
@@ -317,19 +321,17 @@ __global__ void __launch_bounds__(kMost, kPerSm) an8_bwd(const An8Args A) {
   float acc[NV][V];
 #pragma unroll
   for (int i = 0; i < NV; ++i) zero<V>(acc[i]);
-  // the thread's weights, where registers hold them beside its sums: read from L1 for
-  // every row they take half of its bandwidth (30,000 x 8192: 446 us instead of 301)
-  constexpr bool kHold = NV * V <= 16;
-  float held[kHold ? NV : 1][V];
-  if constexpr (kHold)
+  // the thread's weights: read from L1 for every row they would take half of its bandwidth
+  // (30,000 x 8192: 446 us instead of 301)
+  float held[NV][V];
 #pragma unroll
-    for (int i = 0; i < NV; ++i) {
-      const int vec = P.vec + i * P.step;
-      load_w<V>(A.w, vec, A.w && vec < A.rv, held[i]);
-      if (!A.w)
+  for (int i = 0; i < NV; ++i) {
+    const int vec = P.vec + i * P.step;
+    load_w<V>(A.w, vec, A.w && vec < A.rv, held[i]);
+    if (!A.w)
 #pragma unroll
-        for (int c = 0; c < V; ++c) held[i][c] = 1.f;
-    }
+      for (int c = 0; c < V; ++c) held[i][c] = 1.f;
+  }
   const auto place = [&](int stage, int t, int i) {
     return ring + ((stage * 3 + t) * NV + i) * threads + threadIdx.x;
   };
@@ -354,27 +356,29 @@ __global__ void __launch_bounds__(kMost, kPerSm) an8_bwd(const An8Args A) {
     copies_wait<S - 2>();
     // into the place of the row before, which this thread has done with
     load(row + (S - 1) * stride, stage == 0 ? S - 1 : stage - 1);
-    uint4 ry[NV], rz[NV];
+    uint4 ry[kReread ? 1 : NV], rz[kReread ? 1 : NV];
+    if constexpr (!kReread) {
 #pragma unroll
-    for (int i = 0; i < NV; ++i) {
-      ry[i] = *place(stage, 0, i);
-      rz[i] = *place(stage, 1, i);
+      for (int i = 0; i < NV; ++i) {
+        ry[i] = *place(stage, 0, i);
+        rz[i] = *place(stage, 1, i);
+      }
     }
+    // y and dz of vector i
+    const auto look = [&](int i, float (&y)[V], float (&z)[V]) {
+      if constexpr (kReread) {
+        unpack<T>(*place(stage, 0, i), y);
+        unpack<T>(*place(stage, 1, i), z);
+      } else {
+        unpack<T>(ry[i], y);
+        unpack<T>(rz[i], z);
+      }
+    };
     // g = dz w of vector i
     const auto weigh = [&](int i, const float (&z)[V], float (&g)[V]) {
-      if constexpr (kHold) {
 #pragma unroll
-        for (int c = 0; c < V; c += 2)
-          mul2v(g[c], g[c + 1], z[c], z[c + 1], held[i][c], held[i][c + 1]);
-      } else if (A.w) {
-        const int vec = P.vec + i * P.step;
-        load_w<V>(A.w, vec, vec < A.rv, g);
-#pragma unroll
-        for (int c = 0; c < V; c += 2) mul2v(g[c], g[c + 1], z[c], z[c + 1], g[c], g[c + 1]);
-      } else {
-#pragma unroll
-        for (int c = 0; c < V; ++c) g[c] = z[c];
-      }
+      for (int c = 0; c < V; c += 2)
+        mul2v(g[c], g[c + 1], z[c], z[c + 1], held[i][c], held[i][c + 1]);
     };
     float q[2], up = 1.f;
     const auto row_dots = [&] {
@@ -382,8 +386,7 @@ __global__ void __launch_bounds__(kMost, kPerSm) an8_bwd(const An8Args A) {
 #pragma unroll
       for (int i = 0; i < NV; ++i) {
         float y[V], z[V], g[V];
-        unpack<T>(ry[i], y);
-        unpack<T>(rz[i], z);
+        look(i, y, z);
         scale<V>(y, up);
         weigh(i, z, g);
         q[0] += dot<V>(y, y);
@@ -406,8 +409,8 @@ __global__ void __launch_bounds__(kMost, kPerSm) an8_bwd(const An8Args A) {
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
       float y[V], z[V], g[V], d[V];
-      unpack<T>(ry[i], y);
-      unpack<T>(rz[i], z);
+      if (kReread) asm volatile("" ::: "memory");  // anew, not out of registers
+      look(i, y, z);
       unpack<T>(A.o ? *place(stage, 2, i) : make_uint4(0, 0, 0, 0), d);
       weigh(i, z, g);
       scale<V>(y, up);
@@ -545,16 +548,17 @@ cudaError_t fwd_t(const An8Args& A, cudaStream_t st) {
 // of a row  place      thread     (most)    an SM
 //   .. 32   warp       1          256       3       64 features 94 %, 256 103 %
 //   .. 64   warp       2          256       2
-//   .. 128  block      1          128       4       1024: 96 % [a warp's, 4 a thread: 321 to 263 us]
+//   .. 128  block      1          128       4       1024: 96 % [a warp's: 321 to 263 us]
 //   .. 256  block      2          128       3       2048: 94 % [1 a thread of 256: 88 to 87]
 //   .. 512  block      2          256       2       4096: 101 % [1 a thread of 512: 178 to 153]
-//   .. 640  block      2          320       2       4104: 87 % [4 a thread of 160: 219 to 179]
+//   .. 640  block      2          320       3       4104: 89 % [2 blocks: 170 to 166]
 //   .. 1024 block      2          512       1       8192: 106 %
-//   .. 2048 block      4          512       1       16384: 62 %, float32 of 8192 107 %
+//   .. 2048 block      4          512       1       16384: 100 % [w from L1: 322 to 196]
 // Grids of more blocks than are resident end in a wave that is not full (4096: 175 to 153).
 constexpr int kBwdWarpVecs = 64;
 int bwd_per_sm(int rv) {
-  return rv <= 32 ? 3 : rv <= 64 ? 2 : rv <= 128 ? 4 : rv <= 256 ? 3 : rv <= 640 ? 2 : 1;
+  return rv <= 32 ? 3 : rv <= 64 ? 2 : rv <= 128 ? 4 : rv <= 256 ? 3 : rv <= 512 ? 2
+         : rv <= 640 ? 3 : 1;
 }
 // Blocks: what is resident, at most; a row each where a row is a block's, otherwise at least
 // four rows a slot.
@@ -564,9 +568,9 @@ int bwd_blocks(const An8Args& A) {
   return want < 1 ? 1 : want < cap ? int(want) : int(cap);
 }
 
-template <typename T, int NV, int S, bool kWide, int kMost, int kPerSm>
+template <typename T, int NV, int S, bool kWide, bool kReread, int kMost, int kPerSm>
 cudaError_t bwd(const An8Args& A, int blocks, cudaStream_t st) {
-  auto kernel = an8_bwd<T, NV, S, kWide, kMost, kPerSm>;
+  auto kernel = an8_bwd<T, NV, S, kWide, kReread, kMost, kPerSm>;
   const int threads = kWide ? block_threads(A.rv, NV) : kThreads;
   // (a warp's rows' sums, 4 V NV bytes a thread, fit into the ring)
   const size_t smem = ring_bytes(S, NV, threads);
@@ -578,14 +582,14 @@ cudaError_t bwd(const An8Args& A, int blocks, cudaStream_t st) {
 
 template <typename T>
 cudaError_t bwd_t(const An8Args& A, int blocks, cudaStream_t st) {
-  return A.rv <= 32     ? bwd<T, 1, 3, false, 256, 3>(A, blocks, st)
-         : A.rv <= 64   ? bwd<T, 2, 3, false, 256, 2>(A, blocks, st)
-         : A.rv <= 128  ? bwd<T, 1, 3, true, 128, 4>(A, blocks, st)
-         : A.rv <= 256  ? bwd<T, 2, 3, true, 128, 3>(A, blocks, st)
-         : A.rv <= 512  ? bwd<T, 2, 3, true, 256, 2>(A, blocks, st)
-         : A.rv <= 640  ? bwd<T, 2, 3, true, 320, 2>(A, blocks, st)
-         : A.rv <= 1024 ? bwd<T, 2, 3, true, 512, 1>(A, blocks, st)
-                        : bwd<T, 4, 2, true, 512, 1>(A, blocks, st);
+  return A.rv <= 32     ? bwd<T, 1, 3, false, false, 256, 3>(A, blocks, st)
+         : A.rv <= 64   ? bwd<T, 2, 3, false, false, 256, 2>(A, blocks, st)
+         : A.rv <= 128  ? bwd<T, 1, 3, true, false, 128, 4>(A, blocks, st)
+         : A.rv <= 256  ? bwd<T, 2, 3, true, false, 128, 3>(A, blocks, st)
+         : A.rv <= 512  ? bwd<T, 2, 3, true, false, 256, 2>(A, blocks, st)
+         : A.rv <= 640  ? bwd<T, 2, 2, true, true, 320, 3>(A, blocks, st)
+         : A.rv <= 1024 ? bwd<T, 2, 3, true, false, 512, 1>(A, blocks, st)
+                        : bwd<T, 4, 2, true, true, 512, 1>(A, blocks, st);
 }
 
 // values * scale as T: 16 bytes of T a step, kSteps of them in flight.

@@ -171,6 +171,23 @@ def test_values_are_those_of_pack8():
     assert torch.equal(z8.values, p.values)
 
 
+@pytest.mark.gpu
+def test_rows_of_several_dimensions_and_weights_in_another_type():
+    import graph_neural_network_gb300 as gnn
+    x, o, dz = (to_device(draw(s, 30, 4, 16), "f32") for s in (1, 2, 3))
+    w = torch.from_numpy(1 + draw(4, 64, std=0.1)).cuda().double()
+    y, z = gnn.add_norm8_forward(x, o, w, group=16)
+    y2, z2 = gnn.add_norm8_forward(x.view(30, 64), o.view(30, 64), w.float(), group=16)
+    assert y.shape == x.shape and torch.equal(y.view(30, 64), y2)
+    assert z.values.shape == (30, 4, 16) and torch.equal(z.values, z2.values)
+    dx, dw = gnn.add_norm8_backward(y, None, dz, w)
+    assert dx.shape == x.shape and dw.dtype == torch.float32
+    leaf = w.clone().requires_grad_(True)
+    out = gnn.AddNorm8.apply(x, o, leaf, "int8", 16, 1e-6)
+    (g,) = torch.autograd.grad(out[1], leaf, dz)
+    assert out[1].shape == x.shape and g.dtype == torch.float64 and torch.equal(g, dw.double())
+
+
 def check_backward(n, F, dtype, with_dy=True, with_w=True, std=2.0, what=""):
     import graph_neural_network_gb300 as gnn
     a = [draw(s, n, F, dtype=dtype, std=sd) for s, sd in ((1, std), (2, 1.0), (3, 1.0))]

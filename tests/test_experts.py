@@ -191,6 +191,40 @@ def test_rows_that_are_not_read():
 
 
 @pytest.mark.gpu
+def test_no_tokens():
+    import graph_neural_network_gb300 as gnn
+    plan = check_plan(np.zeros((0, 2), np.int64), 4, 8)
+    x, w = torch.zeros(0, 3, 16, device="cuda"), torch.zeros(0, 2, device="cuda")
+    assert gnn.expert_dispatch_forward(plan, x).shape == (0, 3, 16)
+    assert gnn.expert_combine_forward(plan, x, w, x).shape == (0, 3, 16)
+    assert gnn.expert_dispatch_backward(plan, x).shape == (0, 3, 16)
+    dys, dw = gnn.expert_combine_backward(plan, x, x, w)
+    assert dys.shape == (0, 3, 16) and dw.shape == (0, 2)
+
+
+@pytest.mark.gpu
+def test_one_choice_and_rows_of_several_dimensions():
+    """ids and weights [N], rows [N, H, D], weights in another type."""
+    import graph_neural_network_gb300 as gnn
+    ids = torch.from_numpy(choose(60, 1, 5, 3, "dropped")[:, 0].copy()).cuda()
+    x = to_device(draw(1, 60, 4, 8), "f32")
+    w = torch.from_numpy(draw(2, 60)).cuda().bfloat16()
+    one, two = gnn.Experts(ids, 5, align=4), gnn.Experts(ids[:, None].contiguous(), 5, align=4)
+    xs = gnn.expert_dispatch_forward(one, x)
+    assert xs.shape == (one.rows, 4, 8) and one.slots.shape == (60, 1)
+    assert torch.equal(xs.view(-1, 32), gnn.expert_dispatch_forward(two, x.view(60, 32)))
+    y = gnn.expert_combine_forward(one, xs, w, x)
+    want = gnn.expert_combine_forward(two, xs.view(-1, 32), w.float()[:, None].contiguous(),
+                                      x.view(60, 32))
+    assert y.shape == x.shape and torch.equal(y.view(60, 32), want)
+    dys, dw = gnn.expert_combine_backward(one, x, xs, w)
+    assert dys.shape == xs.shape and dw.shape == (60,) and dw.dtype == torch.float32
+    leaf = w.clone().requires_grad_(True)
+    (g,) = torch.autograd.grad(gnn.ExpertCombine.apply(one, xs, leaf, None), leaf, x)
+    assert g.dtype == torch.bfloat16 and torch.equal(g, dw.bfloat16())
+
+
+@pytest.mark.gpu
 def test_packed_rows():
     """Rows in 8 bits go with their scales."""
     import graph_neural_network_gb300 as gnn

@@ -175,7 +175,8 @@ def test_refusals_on_the_host():
     (33, (4, 4), 64, 32, "bf16"), (7, (2,), 10, 6, "bf16"), (9, (5,), 20, 20, "bf16"),
     (6, (3,), 80, 40, "bf16"), (6, (3,), 36, 4, "f32"), (3, (2, 7), 6, 2, "f32"),
     (17, (2,), 256, 256, "f32"), (4, (1,), 300, 256, "bf16"), (300, (1,) * 8, 16, 8, "f32"),
-    (70_001, (2, 1), 8, 8, "bf16")])
+    (3, (2,), 2048, 16, "f32"), (2, (1, 3), 4098, 6, "bf16"), (20_011, (12, 3), 64, 48, "bf16"),
+    (30_001, (5, 1, 2), 64, 64, "f32"), (70_001, (2, 1), 8, 8, "bf16")])
 def test_sizes(n, heads, D, dim, dtype, layout):
     import graph_neural_network_gb300 as gnn
     rope = gnn.Rope(dim, layout, amplitude=1.25)
@@ -229,6 +230,22 @@ def test_views_and_in_place(dtype, dim):
         assert torch.equal(place, want), name
         place.copy_(v)
         assert torch.equal(whole, flat), name
+
+
+@pytest.mark.gpu
+def test_two_views_of_one_tensor_in_place():
+    """q and key of a fused projection, rotated where they lie in one call."""
+    import graph_neural_network_gb300 as gnn
+    n, H, D = 45, 3, 32
+    rope = gnn.Rope(16, "interleaved")
+    pt = torch.from_numpy(positions(n)).cuda()
+    qkv = to_device(draw(4, n, 3, H, D, dtype="bf16"), "bf16")
+    want = gnn.rope_forward(rope, pt, qkv[:, 0], qkv[:, 1])
+    val = qkv[:, 2].clone()
+    got = gnn.rope_forward(rope, pt, qkv[:, 0], qkv[:, 1], out=[qkv[:, 0], qkv[:, 1]])
+    assert got[0].data_ptr() == qkv.data_ptr()
+    assert torch.equal(qkv[:, 0], want[0]) and torch.equal(qkv[:, 1], want[1])
+    assert torch.equal(qkv[:, 2], val)
 
 
 @pytest.mark.gpu
