@@ -12,13 +12,13 @@
 // experts: 9.8 us.
 //
 // Dispatch: a token's row is read once and written to the rows of its choices; padding
-// rows are found in the order (-1) by blocks of their own and written zero.  Combine:
+// rows are found in the order (-1) by blocks of their own, the first, and written zero.  Combine:
 // the rows of a token's choices, weighted, are added in the order of its choices in
 // float32 on top of the residual, and rounded once.  Its gradient: dys = w dy and dw = dy .
 // ys in one pass, a warp (sub-group, or a block where tokens are few) a token.
 // Bound: HBM; each row is read and written once.  65,536 tokens of 2048 bfloat16, 4
-// choices, of 6.68 TB/s: dispatch 228 us (90 %), combine 231 us (105 %, the residual
-// partly in L2), its gradient 371 us (99 %).  What hides the latency of the scattered
+// choices, of 6.68 TB/s: dispatch 205 us (100 %), combine 231 us (104 %, the residual
+// partly in L2), its gradient 365 us (100 %).  What hides the latency of the scattered
 // rows is warps more than loads of one: five blocks an SM instead of three took the
 // gradient from 437 us.
 #include "device.cuh"
@@ -205,7 +205,7 @@ struct RowArgs {
   int chunks;         // of a row, a warp each (rows wider than a warp takes at once)
   uint64_t div;       // ceil(2^64 / chunks), 0 for 1: warp * div / 2^64 is its token
   int pad_rows;       // rows of the order that a warp looks at at once
-  int64_t work_blocks;  // blocks that take tokens; those behind them take padding rows
+  int64_t pad_blocks; // blocks that take padding rows; those behind them take tokens
   const int32_t *slots, *order;
   const float* weights;
   const void *x, *ys, *residual;
@@ -227,8 +227,8 @@ struct RawOf<4> { using type = uint32_t; };
 template <typename Raw>
 __device__ __forceinline__ void zero_padding(const RowArgs& A) {
   const int lane = threadIdx.x & 31;
-  const int64_t warps = (int64_t(gridDim.x) - A.work_blocks) * kWarps;
-  const int64_t w0 = (int64_t(blockIdx.x) - A.work_blocks) * kWarps + (threadIdx.x >> 5);
+  const int64_t warps = A.pad_blocks * kWarps;
+  const int64_t w0 = int64_t(blockIdx.x) * kWarps + (threadIdx.x >> 5);
   for (int64_t r0 = w0 * A.pad_rows; r0 < A.rows; r0 += warps * A.pad_rows) {
     const bool pad = lane < A.pad_rows && r0 + lane < A.rows && __ldg(A.order + r0 + lane) < 0;
     for (unsigned left = __ballot_sync(kFull, pad); left; left &= left - 1) {
@@ -245,7 +245,7 @@ struct Where {
   int64_t token, token_step;
   int vec, vec_step;
   __device__ __forceinline__ explicit Where(const RowArgs& A) {
-    const int64_t warp = int64_t(blockIdx.x) * kWarps + (threadIdx.x >> 5);
+    const int64_t warp = (int64_t(blockIdx.x) - A.pad_blocks) * kWarps + (threadIdx.x >> 5);
     const int lane = threadIdx.x & 31;
     if (kWide) {
       token = A.div ? int64_t(__umul64hi(uint64_t(warp), A.div)) : warp;
@@ -267,13 +267,13 @@ struct Where {
   }
 };
 
-constexpr int kDispatchFlight = 4;
+constexpr int kDispatchFlight = 2;  // 100,000 x 256 bfloat16, 8 choices: 73 us; 4: 75, 8: 77
 
 template <int kB, bool kWide>
-__global__ void __launch_bounds__(kThreads) expert_dispatch(const RowArgs A) {
+__global__ void __launch_bounds__(kThreads, 8) expert_dispatch(const RowArgs A) {
   using Raw = typename RawOf<kB>::type;
   constexpr int kFlight = kDispatchFlight;
-  if (blockIdx.x >= A.work_blocks) {
+  if (blockIdx.x < A.pad_blocks) {
     zero_padding<Raw>(A);
     return;
   }
@@ -353,13 +353,14 @@ template <typename T, bool kBlock>
 __global__ void __launch_bounds__(kThreads, 5) expert_combine_bwd(const RowArgs A) {
   constexpr int V = VecOf<T>::n;
   __shared__ float part[kBlock ? kWarps * kK : 1];
-  if (blockIdx.x >= A.work_blocks) {
+  if (blockIdx.x < A.pad_blocks) {
     zero_padding<uint4>(A);
     return;
   }
   const int lane = threadIdx.x & 31, wid = threadIdx.x >> 5;
   constexpr int lanes = kBlock ? kThreads : 32;
-  const int64_t token = kBlock ? int64_t(blockIdx.x) : int64_t(blockIdx.x) * kWarps + wid;
+  const int64_t block = int64_t(blockIdx.x) - A.pad_blocks;
+  const int64_t token = kBlock ? block : block * kWarps + wid;
   const int v0 = kBlock ? threadIdx.x : lane;
   const bool on = token < A.tokens;
   const uint4* dy = static_cast<const uint4*>(A.x) + token * A.rv;
@@ -428,7 +429,7 @@ __global__ void __launch_bounds__(kThreads, 5) expert_combine_bwd(const RowArgs 
 template <typename T, int kR, int kC, int kPerSm>
 __global__ void __launch_bounds__(kThreads, kPerSm) expert_combine_bwd_narrow(const RowArgs A) {
   constexpr int V = VecOf<T>::n;
-  if (blockIdx.x >= A.work_blocks) {
+  if (blockIdx.x < A.pad_blocks) {
     zero_padding<uint4>(A);
     return;
   }
@@ -522,10 +523,11 @@ int64_t token_blocks(const RowArgs& A, int flight) {
   return (warps + kWarps - 1) / kWarps;
 }
 
-// Blocks for the padding: up to two turns of what is resident.
+// Blocks for the padding: up to what is resident, in front of the others (behind them their
+// zeros came last: 200,003 tokens, a tenth dropped, 31 us instead of 27).
 int64_t padding_blocks(const RowArgs& A, int sm_count) {
   const int64_t want = (A.rows + A.pad_rows * kWarps - 1) / (A.pad_rows * kWarps);
-  const int64_t cap = int64_t(sm_count) * 16;
+  const int64_t cap = int64_t(sm_count) * 8;
   return want < cap ? want : cap;
 }
 
@@ -562,8 +564,8 @@ cudaError_t combine_t(RowArgs& A, int sm_count, cudaStream_t st) {
 
 template <typename T, int kR, int kC, int kPerSm>
 cudaError_t combine_bwd_narrow(RowArgs& A, int sm_count, cudaStream_t st) {
-  A.work_blocks = token_blocks(A, kR);
-  const int64_t blocks = A.work_blocks + padding_blocks(A, sm_count);
+  A.pad_blocks = padding_blocks(A, sm_count);
+  const int64_t blocks = A.pad_blocks + token_blocks(A, kR);
   if (blocks > 0x7fffffff) return cudaErrorInvalidValue;
   expert_combine_bwd_narrow<T, kR, kC, kPerSm><<<unsigned(blocks), kThreads, 0, st>>>(A);
   return cudaGetLastError();
@@ -580,8 +582,8 @@ cudaError_t combine_bwd_narrow_t(RowArgs& A, int sm_count, cudaStream_t st) {
 
 template <typename T>
 cudaError_t combine_bwd(RowArgs& A, bool block, int sm_count, cudaStream_t st) {
-  A.work_blocks = block ? A.tokens : (A.tokens + kWarps - 1) / kWarps;
-  const int64_t blocks = A.work_blocks + padding_blocks(A, sm_count);
+  A.pad_blocks = padding_blocks(A, sm_count);
+  const int64_t blocks = A.pad_blocks + (block ? A.tokens : (A.tokens + kWarps - 1) / kWarps);
   if (blocks > 0x7fffffff) return cudaErrorInvalidValue;
   auto kernel = block ? expert_combine_bwd<T, true> : expert_combine_bwd<T, false>;
   kernel<<<unsigned(blocks), kThreads, 0, st>>>(A);
@@ -666,8 +668,8 @@ cudaError_t launch_expert_dispatch(const gnn_experts& p, int64_t row_bytes, int 
   fit_rows(A, kDispatchFlight);
   A.x = x;
   A.y = xs;
-  A.work_blocks = token_blocks(A, kDispatchFlight);
-  const int64_t blocks = A.work_blocks + padding_blocks(A, sm_count);
+  A.pad_blocks = padding_blocks(A, sm_count);
+  const int64_t blocks = A.pad_blocks + token_blocks(A, kDispatchFlight);
   if (blocks > 0x7fffffff) return cudaErrorInvalidValue;
   return width == 16  ? dispatch<16>(A, unsigned(blocks), st)
          : width == 8 ? dispatch<8>(A, unsigned(blocks), st)
