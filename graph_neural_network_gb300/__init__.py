@@ -1043,7 +1043,7 @@ def add_norm8_forward(x: torch.Tensor, o=None, w=None, fmt: str = "int8",
     Returns y (None where o is None: y is x) and z as a Packed8 of values [N, F/group,
     group], int8 or float8_e4m3fn (fmt "int8", "e4m3"), with a float32 scale [N,
     F/group].  group: features that share a scale (default: the row).  unpack8 reads z
-    back.  y, out: tensors to write."""
+    back.  y, out: tensors to write (y may be x or o: a residual stream updated in place)."""
     n, F = _rows(x, "x")
     dtype, device = x.dtype, x.device
     dt = _dtype_code(dtype)

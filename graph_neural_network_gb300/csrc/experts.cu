@@ -189,7 +189,8 @@ __global__ void __launch_bounds__(kSortThreads) sort_place(const SortArgs A) {
   // rows without a pair: behind each expert's, and behind all of them
   if (A.align > 1)
     for (int e = blockIdx.x * warps + wid; e < A.E; e += A.blocks * warps)
-      for (int r = offset[e] + total[e] + lane; r < offset[e + 1]; r += 32) A.order[r] = -1;
+      for (int64_t r = int64_t(offset[e]) + total[e] + lane; r < offset[e + 1]; r += 32)
+        A.order[r] = -1;
   for (int64_t r = offset[A.E] + int64_t(blockIdx.x) * threads + threadIdx.x; r < A.rows;
        r += int64_t(A.blocks) * threads)
     A.order[r] = -1;

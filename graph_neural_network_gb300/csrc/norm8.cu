@@ -6,8 +6,8 @@
 //   scale = s / sqrt(mean(y^2) + eps)
 // and the row's sum of squares and the maxima are reduced together, after one look at
 // the data.  t is float32 (a sum and a product, each rounded once), and the exact
-// quotient t / s decides the rounding.  The sum of squares is float32; a row whose sum
-// overflows takes it again with y 2^-80.
+// quotient t / s decides the rounding.  The sum of squares is float32; where it overflows
+// that of y 2^-80 takes its place.
 //
 // Backward (straight through the rounding), g = dz w, y^ = y rstd:
 //   dx = dy + rstd (g - y^ mean(g y^)),  dw = sum of dz y^ over the rows
@@ -109,6 +109,11 @@ __device__ __forceinline__ uint4 load_vec(const void* p, int64_t at, bool ok) {
   return ok ? ld16(reinterpret_cast<const char*>(p) + 16 * at) : make_uint4(0, 0, 0, 0);
 }
 
+// The same where the kernel may write what it read (not the read-only path).
+__device__ __forceinline__ uint4 load_own(const void* p, int64_t at, bool ok) {
+  return ok ? static_cast<const uint4*>(p)[at] : make_uint4(0, 0, 0, 0);
+}
+
 template <int V>
 __device__ __forceinline__ void load_w(const float* w, int vec, bool ok, float (&f)[V]) {
 #pragma unroll
@@ -176,13 +181,13 @@ __global__ void __launch_bounds__(kWide ? kWideThreads : kThreads)
     const int64_t row = P.row + (R == 1 ? 0 : i * P.stride);
     ok[i] = vec < A.rv && row < A.n;
     at[i] = row * A.rv + vec;
-    rx[i] = load_vec<T>(A.x, at[i], ok[i]);
-    ro[i] = load_vec<T>(A.o, at[i], ok[i] && A.o);
+    rx[i] = load_own(A.x, at[i], ok[i]);
+    ro[i] = load_own(A.o, at[i], ok[i] && A.o);
   }
-  float t[I][V], ss[R];
+  float t[I][V], ss[R], low[R];  // low: the sum of (y 2^-80)^2
   uint32_t top[I];
 #pragma unroll
-  for (int r = 0; r < R; ++r) ss[r] = 0.f;
+  for (int r = 0; r < R; ++r) ss[r] = low[r] = 0.f;
 #pragma unroll
   for (int i = 0; i < I; ++i) {
     float o[V];
@@ -194,7 +199,16 @@ __global__ void __launch_bounds__(kWide ? kWideThreads : kThreads)
         add2(t[i][c], t[i][c + 1], t[i][c], t[i][c + 1], o[c], o[c + 1]);
       if (ok[i]) st16(reinterpret_cast<char*>(A.y) + 16 * at[i], pack<T>(t[i]));
     }
-    ss[R == 1 ? 0 : i] += dot<V>(t[i], t[i]);
+    const float d = dot<V>(t[i], t[i]);
+    float less = d * kDown * kDown;
+    if (!(d < kInf)) {
+      float y[V];
+#pragma unroll
+      for (int c = 0; c < V; ++c) y[c] = t[i][c] * kDown;
+      less = dot<V>(y, y);
+    }
+    ss[R == 1 ? 0 : i] += d;
+    low[R == 1 ? 0 : i] += less;
     if (A.w) {
       float w[V];
       load_w<V>(A.w, P.vec + (R == 1 ? i * P.step : 0), ok[i], w);
@@ -221,24 +235,12 @@ __global__ void __launch_bounds__(kWide ? kWideThreads : kThreads)
 #pragma unroll
       for (int i = 0; i < I; ++i) top[i] = max(top[i], __shfl_xor_sync(kFull, top[i], o));
   }
-  // sums that are not finite: of y 2^-80 (all rows of the warp, or the block's, take part)
+  // sums that overflowed: those of y 2^-80 (all rows of the warp, or the block's, take part)
   float pre[R], rstd[R];
   bool any = false;
 #pragma unroll
   for (int r = 0; r < R; ++r) any |= !(ss[r] < kInf);
   if (kWide ? any : __any_sync(kFull, any)) {
-    float low[R];
-#pragma unroll
-    for (int r = 0; r < R; ++r) low[r] = 0.f;
-#pragma unroll
-    for (int i = 0; i < I; ++i) {
-      float y[V], o[V];
-      unpack<T>(load_vec<T>(A.x, at[i], ok[i]), y);
-      unpack<T>(load_vec<T>(A.o, at[i], ok[i] && A.o), o);
-#pragma unroll
-      for (int c = 0; c < V; ++c) y[c] = (y[c] + o[c]) * kDown;
-      low[R == 1 ? 0 : i] += dot<V>(y, y);
-    }
     uint32_t none[1] = {0u};
     over_row<kWide>(low, none, false, A.tpr_log2, again);
 #pragma unroll

@@ -533,8 +533,8 @@ gnn_status gnn_norm_residual_backward(const gnn_norm_residual* d, gnn_dtype dtyp
  * [n][F], 16-byte aligned; o null: y is x and is not written (y null).  w: float
  * [F], 16-byte aligned, or null (1).  values: [n][F] bytes, 16-byte aligned; scale:
  * [n][F / group].  Arithmetic in float32, y rounded once (z comes from the unrounded
- * one).  No output may overlap an input.  Asynchronous on `stream`; bitwise
- * reproducible. */
+ * one).  y may be x or o itself, no output may overlap an input otherwise.
+ * Asynchronous on `stream`; bitwise reproducible. */
 typedef enum { GNN_INT8 = 0, GNN_E4M3 = 1 } gnn_eight;
 
 typedef struct {

@@ -163,6 +163,22 @@ def test_zeros_extremes_and_numbers_that_are_none(F, group, fmt):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("F", [64, 520, 4096])
+def test_in_place(F):
+    """The sum written over x or o, rows whose squares overflow among them."""
+    import graph_neural_network_gb300 as gnn
+    x, o = (to_device(draw(s, 9, F, dtype="bf16"), "bf16") for s in (1, 2))
+    x[4] *= 1e25
+    want, z = gnn.add_norm8_forward(x, o, fmt="e4m3")
+    assert torch.isfinite(z.scale).all()
+    for k in (0, 1):
+        t = [x.clone(), o.clone()]
+        y, z8 = gnn.add_norm8_forward(*t, fmt="e4m3", y=t[k])
+        assert y is t[k] and torch.equal(y, want) and torch.equal(z8.scale, z.scale)
+        assert torch.equal(z8.values.view(torch.uint8), z.values.view(torch.uint8))
+
+
+@pytest.mark.gpu
 def test_values_are_those_of_pack8():
     import graph_neural_network_gb300 as gnn
     x, o = (to_device(draw(s, 500, 4 * 32, dtype="bf16"), "bf16") for s in (1, 2))
