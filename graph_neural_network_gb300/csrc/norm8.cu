@@ -12,7 +12,8 @@
 // Backward (straight through the rounding), g = dz w, y^ = y rstd:
 //   dx = dy + rstd (g - y^ mean(g y^)),  dw = sum of dz y^ over the rows
 // with mean(g y^) = rstd mean(g y): both sums of a row are again taken together.
-// dw: float32 per thread over its rows, then float64 or compensated, in a fixed order.
+// dw: float32 per thread over its rows (kKeepRows), then float64 or compensated, in a fixed
+// order.
 //
 // Bound: HBM.  3 s + 1 bytes an element forward (4 a group), 4 s backward.
 //
@@ -308,21 +309,42 @@ constexpr size_t ring_bytes(int stages, int NV, int threads) {
   return size_t(stages) * 3 * NV * threads * 16;
 }
 
+// float32 rows whose terms of dw a thread adds up in registers before it adds them to its
+// sums in shared memory: two levels of additions lose with the roots of 64 and of the
+// number of parts, not with that of all rows (400,000 rows of 512, 660 a thread).  Rows of
+// bfloat16 carry 2^-9 each, and their sums, twice as wide, would cost a block an SM: one
+// level.
+constexpr int kKeepRows = 64;
+template <typename T>
+constexpr bool kTwoLevels = sizeof(T) == 4;
+
 // kReread: the rows are read from shared memory for each of the two looks at them (their
 // registers go to the sums and weights of rows of four vectors, or to a third block).
 template <typename T, int NV, int S, bool kWide, bool kReread, int kMost, int kPerSm>
 __global__ void __launch_bounds__(kMost, kPerSm) an8_bwd(const An8Args A) {
   constexpr int V = VecOf<T>::n;
   __shared__ float buf[2][kWide ? 2 * (kWideThreads / 32) : 1];
-  // [S][3][NV][threads]; at the end [row slots][F] sums (rows of a warp)
+  // [S][3][NV][threads]; at the end [row slots][F] sums (rows of a warp).  Behind it, with
+  // two levels, the threads' sums [NV][threads].
   extern __shared__ __align__(16) uint4 ring[];
   const Spot<NV, 1, kWide> P(A);
   const int slots = kWide ? 1 : kThreads >> A.tpr_log2;
   const int64_t stride = int64_t(gridDim.x) * slots;
   const int threads = blockDim.x;
   float acc[NV][V];
+  float4* const kept = reinterpret_cast<float4*>(ring + S * 3 * NV * threads) + threadIdx.x;
+  // acc becomes the sum of both
+  const auto join = [&](int i) {
+    const float4 k = kept[i * threads];
+    add2(acc[i][0], acc[i][1], acc[i][0], acc[i][1], k.x, k.y);
+    add2(acc[i][2], acc[i][3], acc[i][2], acc[i][3], k.z, k.w);
+  };
+  int rows_left = kKeepRows;
 #pragma unroll
-  for (int i = 0; i < NV; ++i) zero<V>(acc[i]);
+  for (int i = 0; i < NV; ++i) {
+    zero<V>(acc[i]);
+    if (kTwoLevels<T>) kept[i * threads] = make_float4(0.f, 0.f, 0.f, 0.f);
+  }
   // the thread's weights: read from L1 for every row they would take half of its bandwidth
   // (30,000 x 8192: 446 us instead of 301)
   float held[NV][V];
@@ -428,7 +450,19 @@ __global__ void __launch_bounds__(kMost, kPerSm) an8_bwd(const An8Args A) {
         st16(reinterpret_cast<char*>(A.dx) + 16 * (row * A.rv + vec), pack<T>(d));
     }
     stage = stage == S - 1 ? 0 : stage + 1;
+    if (kTwoLevels<T> && --rows_left == 0) {
+      rows_left = kKeepRows;
+#pragma unroll
+      for (int i = 0; i < NV; ++i) {
+        join(i);
+        kept[i * threads] = make_float4(acc[i][0], acc[i][1], acc[i][2], acc[i][3]);
+        zero<V>(acc[i]);
+      }
+    }
   }
+  if (kTwoLevels<T>)
+#pragma unroll
+    for (int i = 0; i < NV; ++i) join(i);
   copies_wait<0>();
   let_next_start();
   if (!A.part) return;
@@ -575,7 +609,8 @@ cudaError_t bwd(const An8Args& A, int blocks, cudaStream_t st) {
   auto kernel = an8_bwd<T, NV, S, kWide, kReread, kMost, kPerSm>;
   const int threads = kWide ? block_threads(A.rv, NV) : kThreads;
   // (a warp's rows' sums, 4 V NV bytes a thread, fit into the ring)
-  const size_t smem = ring_bytes(S, NV, threads);
+  const size_t smem =
+      ring_bytes(S, NV, threads) + (kTwoLevels<T> ? size_t(NV) * threads * 16 : 0);
   const cudaError_t e = allow_smem(kernel, smem);
   if (e != cudaSuccess) return e;
   kernel<<<unsigned(blocks), threads, smem, st>>>(A);

@@ -266,6 +266,27 @@ def test_backward_of_large_rows():
 
 
 @pytest.mark.gpu
+def test_parameter_sums_over_many_rows():
+    """400,000 rows, some 660 of them a thread.  An addition into a partial sum of k random
+    terms is off by U / sqrt(3) of it at most on average, so m of them in a row by U sqrt(m / 6)
+    of their sum: 3.3 U for 64, 1.3 U for the 11 parts after them; the terms themselves, products
+    with y^, have errors of 1 U that are common to a row (rstd: they add up like the terms) and 1 U
+    that are not: 1 U of the sum each at most.  Together, as squares: 3.9 U (one chain of 660:
+    10.6 U)."""
+    import graph_neural_network_gb300 as gnn
+    n, F = 400_000, 512
+    gen = torch.Generator("cuda").manual_seed(3)
+    y, dz = (torch.randn(n, F, generator=gen, device="cuda") for _ in range(2))
+    _, dw = gnn.add_norm8_backward(y, None, dz, torch.ones(F, device="cuda"))
+    want = 0
+    for a, b in zip(y.split(50_000), dz.split(50_000)):
+        a = a.double()
+        want = want + (b.double() * a * (a.pow(2).mean(-1, keepdim=True) + 1e-6).rsqrt()).sum(0)
+    error = (dw.double() - want).norm() / want.norm()
+    assert error <= 4 * U, float(error)
+
+
+@pytest.mark.gpu
 def test_autograd_and_differences():
     """Straight through: the gradients are those of the norm itself, whose central
     differences in float64 agree to h^2 and the rounding of dx."""
