@@ -2,14 +2,14 @@
 //
 // Plan.  A stable counting sort of the (token, choice) pairs by expert: rank of a pair =
 // pairs of its expert before it, row = the expert's first row + rank.  A warp takes a
-// run of pairs, 32 at a time; lanes of equal experts find one another by a match, and
+// run of pairs, 32 at a time; lanes of equal experts find one another by votes, and
 // the warp keeps its own counts in shared memory, so ranks depend on no scheduling.
 // One pass counts, the warps' counts (and the blocks' before this one) are added up
 // in order, and a second pass ranks and writes.  Up to kOneBlock pairs a single block
 // does it all; more take a kernel that counts for each block and one that reads all
 // blocks' counts, starts early and counts its own warps meanwhile.
 // Bound: latency.  A pair costs its id twice and two writes of 4 bytes; 400,006 pairs, 16
-// experts: 9.8 us.
+// experts: 9.6 us; 512 pairs 3.5 us.
 //
 // Dispatch: a token's row is read once and written to the rows of its choices; padding
 // rows are found in the order (-1) by blocks of their own, the first, and written zero.  Combine:
@@ -21,6 +21,8 @@
 // partly in L2), its gradient 365 us (100 %).  What hides the latency of the scattered
 // rows is warps more than loads of one: five blocks an SM instead of three took the
 // gradient from 437 us.
+#include <math.h>
+
 #include "device.cuh"
 
 namespace gnn {
@@ -28,29 +30,35 @@ namespace {
 
 // ---- plan ---------------------------------------------------------------------
 
-constexpr int kOneBlock = 2048;   // pairs that a single block sorts, and of a block where there
-                                  // are more (8000 in one block: 16 us, in four 7 us)
+constexpr int kOneBlock = 2048;   // pairs that a single block sorts (5.2 us, in two 6.5; 8000
+                                  // in one 16 us, in eight 6.4)
 constexpr int kLoadSteps = 4;     // steps of 32 pairs a warp loads at once
 constexpr int kSortBlocks = 304;
-constexpr int kSortThreads = 512;
+constexpr int kSortThreads = 512, kSortWarps = kSortThreads / 32;
+constexpr int kMostExperts = 1024;
 
 struct SortArgs {
   const void* ids;
   int64_t pairs, rows;
   int E, align;
   int steps;           // of 32 pairs, of a warp
+  int bits;            // of E
   int blocks;
   int32_t *offsets, *counts, *order, *slots;
   int32_t* seen;       // [blocks][E] (more than one block)
 };
 
-// Warps of a block: their counts take at most 32 KB.
-int sort_warps(int E) { return E <= 512 ? kSortThreads / 32 : 8; }
+// Blocks.  A block takes pairs / blocks pairs and reads blocks * E counts of the others, so
+// the best number goes with the root of pairs / E; 2.5 of it fits what was measured (800,000
+// pairs of 256 experts: 22 us, with 3.2 of it 31; 131,072 of 64: 8.6 and 7.4; 524,288 of
+// 1000: 35 and 33).
 int sort_blocks(int64_t pairs, int E) {
   if (pairs <= kOneBlock) return 1;
-  const int64_t want = (pairs + kOneBlock - 1) / kOneBlock, cap = 32768 / E;
-  const int64_t most = cap < kSortBlocks ? cap : kSortBlocks;
-  return int(want < most ? want : most);
+  int64_t most = 1 + int64_t(2.5 * sqrt(double(pairs) / E));
+  if (most > kSortBlocks) most = kSortBlocks;
+  // a whole number of steps a warp
+  const int64_t steps = (pairs + kSortThreads * most - 1) / (kSortThreads * most);
+  return int((pairs + kSortThreads * steps - 1) / (kSortThreads * steps));
 }
 
 // The experts of this lane's pairs of steps s0 .. s0 + kLoadSteps, -1 where dropped.
@@ -66,6 +74,20 @@ __device__ __forceinline__ void load_experts(const SortArgs& A, int64_t first, i
   }
 }
 
+// The lanes whose expert is this lane's, by a vote on each of its bits (dropped pairs count
+// as expert E).  A match instruction takes its turns by the experts among the lanes:
+// 131,072 pairs of 64 experts 10.3 us with it, 8.5 so.
+__device__ __forceinline__ unsigned same_expert(int e, int bits, int E) {
+  const int key = e >= 0 ? e : E;
+  unsigned same = kFull;
+  for (int b = 0; b < bits; ++b) {
+    const bool one = key >> b & 1;
+    const unsigned set = __ballot_sync(kFull, one);
+    same &= one ? set : ~set;
+  }
+  return same;
+}
+
 // Adds the warp's pairs to its counts.  e: the experts of its last steps (all of them
 // where it has kLoadSteps at most).
 template <typename Id>
@@ -77,7 +99,7 @@ __device__ __forceinline__ void count_experts(const SortArgs& A, int64_t first, 
 #pragma unroll
     for (int u = 0; u < kLoadSteps; ++u) {
       if (s0 + u >= A.steps) break;
-      const unsigned same = __match_any_sync(kFull, e[u]);
+      const unsigned same = same_expert(e[u], A.bits, A.E);
       if (e[u] >= 0 && lane == __ffs(same) - 1) mine[e[u]] += __popc(same);
       __syncwarp();
     }
@@ -87,15 +109,17 @@ __device__ __forceinline__ void count_experts(const SortArgs& A, int64_t first, 
 template <typename Id>
 __global__ void __launch_bounds__(kSortThreads) sort_count(const SortArgs A) {
   extern __shared__ int32_t counts[];  // [warps][E]
-  const int warps = blockDim.x >> 5, wid = threadIdx.x >> 5;
-  for (int x = threadIdx.x; x < warps * A.E; x += blockDim.x) counts[x] = 0;
+  const int wid = threadIdx.x >> 5;
+  for (int x = threadIdx.x; x < kSortWarps * A.E; x += kSortThreads) counts[x] = 0;
   __syncthreads();
   int e_[kLoadSteps];
-  count_experts<Id>(A, (int64_t(blockIdx.x) * warps + wid) * A.steps * 32, counts + wid * A.E, e_);
+  count_experts<Id>(A, (int64_t(blockIdx.x) * kSortWarps + wid) * A.steps * 32, counts + wid * A.E,
+                    e_);
   __syncthreads();
-  for (int e = threadIdx.x; e < A.E; e += blockDim.x) {
+  for (int e = threadIdx.x; e < A.E; e += kSortThreads) {
     int s = 0;
-    for (int w = 0; w < warps; ++w) s += counts[w * A.E + e];
+#pragma unroll
+    for (int w = 0; w < kSortWarps; ++w) s += counts[w * A.E + e];
     A.seen[int64_t(blockIdx.x) * A.E + e] = s;
   }
   let_next_start();
@@ -104,27 +128,29 @@ __global__ void __launch_bounds__(kSortThreads) sort_count(const SortArgs A) {
 template <typename Id>
 __global__ void __launch_bounds__(kSortThreads) sort_place(const SortArgs A) {
   extern __shared__ int32_t counts[];      // [warps][E]
-  const int threads = blockDim.x, warps = threads >> 5, wid = threadIdx.x >> 5,
-            lane = threadIdx.x & 31;
+  constexpr int threads = kSortThreads, warps = kSortWarps;
+  const int wid = threadIdx.x >> 5, lane = threadIdx.x & 31;
   int32_t* total = counts + warps * A.E;   // [E] pairs of each expert
   int32_t* before = total + A.E;           // [E] of them in the blocks before this one
   int32_t* offset = before + A.E;          // [E + 1] first rows
+  __shared__ int32_t warp_rows[warps];
   for (int x = threadIdx.x; x < (warps + 2) * A.E; x += threads) counts[x] = 0;
   __syncthreads();
   const int64_t first = (int64_t(blockIdx.x) * warps + wid) * A.steps * 32;
   int e[kLoadSteps];
   count_experts<Id>(A, first, counts + wid * A.E, e);
   __syncthreads();
-  // the warps' counts become the pairs in the warps before; a warp an expert, a lane a warp
-  for (int e = wid; e < A.E; e += warps) {
-    const int c = lane < warps ? counts[lane * A.E + e] : 0;
-    int sum = c;
-    for (int o = 1; o < 32; o <<= 1) {
-      const int up = __shfl_up_sync(kFull, sum, o);
-      if (lane >= o) sum += up;
+  // the warps' counts become the pairs in the warps before
+  for (int e = threadIdx.x; e < A.E; e += threads) {
+    int c[warps], run = 0;
+#pragma unroll
+    for (int w = 0; w < warps; ++w) c[w] = counts[w * A.E + e];
+#pragma unroll
+    for (int w = 0; w < warps; ++w) {
+      counts[w * A.E + e] = run;
+      run += c[w];
     }
-    if (lane < warps) counts[lane * A.E + e] = sum - c;
-    if (A.blocks == 1 && lane == 31) total[e] = sum;
+    if (A.blocks == 1) total[e] = run;
   }
   if (A.blocks > 1) {
     grid_wait();
@@ -145,21 +171,30 @@ __global__ void __launch_bounds__(kSortThreads) sort_place(const SortArgs A) {
       }
   }
   __syncthreads();
-  if (wid == 0) {
-    int run = 0;
-    for (int e0 = 0; e0 < A.E; e0 += 32) {
-      const int e = e0 + lane;
-      const int mine = e < A.E ? (total[e] + A.align - 1) / A.align * A.align : 0;
-      int sum = mine;
-      for (int o = 1; o < 32; o <<= 1) {
-        const int up = __shfl_up_sync(kFull, sum, o);
-        if (lane >= o) sum += up;
-      }
-      if (e < A.E) offset[e] = run + sum - mine;
-      run += __shfl_sync(kFull, sum, 31);
-    }
-    if (lane == 0) offset[A.E] = run;
+  // first rows: a scan over the experts, kEach neighbours a thread
+  constexpr int kEach = kMostExperts / threads;
+  const int e0 = threadIdx.x * kEach;
+  int rows[kEach], sum = 0;
+#pragma unroll
+  for (int k = 0; k < kEach; ++k) {
+    rows[k] = sum;
+    if (e0 + k < A.E) sum += (total[e0 + k] + A.align - 1) / A.align * A.align;
   }
+  int upto = sum;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int up = __shfl_up_sync(kFull, upto, o);
+    if (lane >= o) upto += up;
+  }
+  if (lane == 31) warp_rows[wid] = upto;
+  __syncthreads();
+  int past = upto - sum;
+#pragma unroll
+  for (int w = 0; w < warps; ++w) past += w < wid ? warp_rows[w] : 0;
+#pragma unroll
+  for (int k = 0; k < kEach; ++k)
+    if (e0 + k < A.E) offset[e0 + k] = past + rows[k];
+  if (threadIdx.x == threads - 1) offset[A.E] = past + sum;
   __syncthreads();
   for (int e = lane; e < A.E; e += 32) counts[wid * A.E + e] += offset[e] + before[e];
   __syncwarp();
@@ -169,7 +204,7 @@ __global__ void __launch_bounds__(kSortThreads) sort_place(const SortArgs A) {
 #pragma unroll
     for (int u = 0; u < kLoadSteps; ++u) {
       if (s0 + u >= A.steps) break;
-      const unsigned same = __match_any_sync(kFull, e[u]);
+      const unsigned same = same_expert(e[u], A.bits, A.E);
       const int base = e[u] >= 0 ? next[e[u]] : 0;
       __syncwarp();
       if (e[u] >= 0 && lane == __ffs(same) - 1) next[e[u]] = base + __popc(same);
@@ -593,20 +628,25 @@ cudaError_t combine_bwd(RowArgs& A, bool block, int sm_count, cudaStream_t st) {
 
 template <typename Id>
 cudaError_t sort(SortArgs& A, cudaStream_t st) {
-  const int warps = sort_warps(A.E);
   A.blocks = sort_blocks(A.pairs, A.E);
-  const int64_t runs = int64_t(A.blocks) * warps * 32;
+  while ((A.E >> A.bits) != 0) ++A.bits;
+  const int64_t runs = int64_t(A.blocks) * kSortThreads;
   A.steps = int((A.pairs + runs - 1) / runs);
-  const size_t counts = size_t(warps) * A.E * 4;
+  const size_t counts = size_t(kSortWarps) * A.E * 4, all = counts + (3 * size_t(A.E) + 1) * 4;
+  // (what a kernel keeps in shared memory otherwise is not part of these)
+  constexpr size_t kAlways = 48 * 1024 - 256;
+  cudaError_t e = allow_smem(sort_place<Id>, all, kAlways);
+  if (e != cudaSuccess) return e;
   if (A.blocks == 1) {
-    sort_place<Id><<<1, warps * 32, counts + (3 * size_t(A.E) + 1) * 4, st>>>(A);
+    sort_place<Id><<<1, kSortThreads, all, st>>>(A);
     return cudaGetLastError();
   }
-  sort_count<Id><<<unsigned(A.blocks), warps * 32, counts, st>>>(A);
-  const cudaError_t e = cudaGetLastError();
+  e = allow_smem(sort_count<Id>, counts, kAlways);
   if (e != cudaSuccess) return e;
-  return launch_after(sort_place<Id>, dim3(unsigned(A.blocks)), warps * 32,
-                      counts + (3 * size_t(A.E) + 1) * 4, st, A);
+  sort_count<Id><<<unsigned(A.blocks), kSortThreads, counts, st>>>(A);
+  e = cudaGetLastError();
+  if (e != cudaSuccess) return e;
+  return launch_after(sort_place<Id>, dim3(unsigned(A.blocks)), kSortThreads, all, st, A);
 }
 
 // Byte offsets of the arrays in a plan's buffer, and its size.
